@@ -444,6 +444,125 @@ int llama_sample(llama_ctx* ctx, const float* logits, int32_t B, int32_t V,
                  const int32_t* history, const int32_t* history_len, int32_t history_stride,
                  const float* uniforms, int32_t* next_ids);
 
+/* ---- Attention beside the plain Llama2 path: models that normalise their
+ * query and key heads, rotate half-split or partial heads or stretch the
+ * positions (§1.4 gives the plain RoPE), cap or bias their scores, pack
+ * documents, or serve a batch over one shared prompt. llama_op_rope_norm_append
+ * writes the cache; llama_op_attention_docs attends over the prompt rows and
+ * llama_op_attention_decode_shared over the cache. All three are single
+ * operations on the context's stream, like the ones above; the context's
+ * device must be current (INVALID_ARG otherwise). ---- */
+
+/* Rotation angles of scaled positions: table[m][j] = magnitude * (cos, sin) of
+ * m * f_j for positions m = 0 .. n_pos-1 and pairs j = 0 .. rotary_dim/2 - 1,
+ * computed in fp64 and rounded once. f_j = theta^(-2j / rotary_dim), then
+ *   LLAMA_ROPE_PLAIN : f_j
+ *   LLAMA_ROPE_LINEAR: f_j / factor (positions compressed by factor)
+ *   LLAMA_ROPE_BANDS : pairs that turn often keep their angle, slow ones are
+ *       compressed: t = original_len * f_j / (2 pi) turns over the original
+ *       context, g = clamp((t - low_turns) / (high_turns - low_turns), 0, 1),
+ *       f_j * (g + (1 - g) / factor).
+ * (A larger base is theta itself.) magnitude 1 leaves lengths unchanged; some
+ * long-context models scale both q and k by it. */
+#define LLAMA_ROPE_PLAIN 0
+#define LLAMA_ROPE_LINEAR 1
+#define LLAMA_ROPE_BANDS 2
+typedef struct llama_rope_scaling {
+  int32_t kind;          /* LLAMA_ROPE_PLAIN, _LINEAR or _BANDS */
+  float theta;           /* > 0 */
+  float factor;          /* > 0 (LINEAR, BANDS) */
+  float low_turns;       /* BANDS: 0 <= low_turns < high_turns */
+  float high_turns;
+  int32_t original_len;  /* BANDS: >= 1 */
+  float magnitude;       /* > 0 */
+} llama_rope_scaling;
+/* Fill table, DEVICE fp32 [n_pos][rotary_dim/2][2], 16-byte aligned;
+ * rotary_dim a positive multiple of 8. stream is a cudaStream_t (NULL: the
+ * legacy default stream). Made once and kept by the caller. Asynchronous. */
+int llama_rope_table(const llama_rope_scaling* scaling, int32_t rotary_dim, int32_t n_pos,
+                     float* table, void* stream);
+
+/* How heads rotate: the first rotary_dim values of each head turn, the rest
+ * pass through. ADJACENT turns the pairs (2j, 2j+1) as llama_op_rope_append
+ * does, HALF the pairs (j, j + rotary_dim/2). */
+#define LLAMA_ROPE_ADJACENT 0
+#define LLAMA_ROPE_HALF 1
+typedef struct llama_rope {
+  int32_t layout;
+  int32_t rotary_dim;  /* a multiple of 8, 0 .. head_dim (0: no rotation) */
+  const float* table;  /* DEVICE [n_pos][rotary_dim/2][2] (llama_rope_table), 16-byte aligned,
+                          or NULL: the context's table (rotary_dim == head_dim, n_pos ignored) */
+  int32_t n_pos;
+} llama_rope;
+
+/* Head norms, rotation and KV append in one pass. qkv [n_rows, >= (n_q + 2 n_kv) d]
+ * (Q heads | K heads | V heads) as fp32 or in the context's dtype (qkv_dtype
+ * LLAMA_F32 or LLAMA_BF16), row r at qkv + r * qkv_ld elements; rows 16-byte
+ * aligned. Rows are packed as in llama_extend (cu_rows, start_pos; B
+ * sequences); cu_rows NULL is the single-token form: row b is sequence b's, at
+ * start_pos[b], and n_rows must be B. Per row:
+ *   1. with gains (T [d], 16-byte aligned; each may be NULL: that head kind
+ *      is not normalised), every Q / K head x becomes
+ *      x / sqrt(mean(x^2) + norm_eps) * gain;
+ *   2. Q and K heads rotate by the row's position (rope);
+ *   3. Q goes to q_out T [n_rows, n_q d]; K and V go to the cache slot of the
+ *      row's sequence and position in layer `layer` (E4M3 caches as in
+ *      llama_op_rope_append), and, if k_out / v_out are not NULL, to them as
+ *      T [n_rows, n_kv d] (plain T values whatever the cache's type).
+ * Rows before cu_rows[0] or from cu_rows[B] on are left as they were. A
+ * position outside the table flags LLAMA_FLAG_POS_RANGE: the row's outputs are
+ * zeros and nothing is cached; past the cache (or a page id outside the pool,
+ * LLAMA_FLAG_PAGE_RANGE) only the cache write is skipped. Two rows of the
+ * same slot in one call leave either's values there. Outputs must not overlap
+ * qkv. rope may be NULL (no rotation; positions may then be any of the cache's). */
+int llama_op_rope_norm_append(llama_ctx* ctx, const void* qkv, int32_t qkv_dtype, int64_t qkv_ld,
+                              int32_t n_rows, const int32_t* cu_rows, const int32_t* start_pos,
+                              int32_t B, const llama_rope* rope, const void* q_gain,
+                              const void* k_gain, float norm_eps, int32_t layer,
+                              const llama_kv* kv, void* q_out, void* k_out, void* v_out);
+
+/* Attention scores: with x = scale * q.k,
+ *   s = (cap > 0 ? cap * tanh(x / cap) : x) - slopes[h] * |i - j|
+ * for query position i and key position j of head h, then the mask. */
+typedef struct llama_scores {
+  float scale;          /* > 0, or 0: 1 / sqrt(head_dim) */
+  float cap;            /* > 0, or 0: no cap */
+  const float* slopes;  /* DEVICE fp32 [n_q], or NULL: no distance bias */
+} llama_scores;
+
+/* Prompt attention over packed documents: q T [n_rows, n_q, d], k and v T
+ * [n_rows, n_kv, d] (k rotated), 16-byte aligned; document b owns rows
+ * cu_rows[b] .. cu_rows[b+1] - 1 (DEVICE int32 [B+1], non-decreasing; a document
+ * may be empty). Row i of a document attends the document's rows 0 .. i and,
+ * with prefix_len (DEVICE int32 [B] or NULL), every row below prefix_len[b]
+ * (attended both ways; clamped to the document). Never across documents. out
+ * T [n_rows, n_q d]; rows of no document are left as they were. scores may be
+ * NULL (plain scores). A hidden key takes part with weight 0 where it shares
+ * a tile of 128 keys with a visible one, so V must be finite within a
+ * document; other documents' rows and rows of none may hold anything. cu_rows
+ * outside [0, n_rows] or decreasing flag LLAMA_FLAG_POS_RANGE (rows outside
+ * are skipped). Any number of rows (no context limit), n_rows * n_q < 2^30. */
+int llama_op_attention_docs(llama_ctx* ctx, const void* q, const void* k, const void* v,
+                            int32_t n_rows, const int32_t* cu_rows, int32_t B,
+                            const int32_t* prefix_len, const llama_scores* scores, void* out);
+
+/* Decode attention over a cache whose first shared_len positions are the same
+ * for the whole batch: q T [B, n_q, d] (rotated, 16-byte aligned), sequence b
+ * attends keys 0 .. positions[b] of layer `layer`; keys below shared_len are
+ * read once for the batch from sequence shared_seq (its page-table row, or its
+ * slot of a contiguous cache, which may be one past the batch), the others
+ * from b's own. shared_len may end inside a page: keys from shared_len on
+ * come from b's own page there. shared_len 0 is plain decode attention with
+ * these scores. positions as in llama_op_attention_decode (a negative one
+ * flags and gives zeros; one past the cache or max_seq flags, and the keys in
+ * range are attended). out T [B, n_q d]. B <= max_batch; shared_len <= the
+ * cache's positions and max_seq. The cache has the context's dtype (an E4M3
+ * cache is UNSUPPORTED). */
+int llama_op_attention_decode_shared(llama_ctx* ctx, const void* q, const int32_t* positions,
+                                     int32_t B, int32_t layer, const llama_kv* kv,
+                                     int32_t shared_len, int32_t shared_seq,
+                                     const llama_scores* scores, void* out);
+
 #ifdef __cplusplus
 }
 #endif

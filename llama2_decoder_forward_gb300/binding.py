@@ -58,6 +58,26 @@ class Sampling(ctypes.Structure):
                 ("repetition_penalty", ctypes.c_float)]
 
 
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDS = 0, 1, 2
+ROPE_ADJACENT, ROPE_HALF = 0, 1
+
+
+class RopeScaling(ctypes.Structure):
+    """llama_rope_scaling: kind ROPE_PLAIN, ROPE_LINEAR or ROPE_BANDS."""
+    _fields_ = [("kind", c_int32), ("theta", ctypes.c_float), ("factor", ctypes.c_float),
+                ("low_turns", ctypes.c_float), ("high_turns", ctypes.c_float),
+                ("original_len", c_int32), ("magnitude", ctypes.c_float)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("layout", c_int32), ("rotary_dim", c_int32), ("table", c_void_p),
+                ("n_pos", c_int32)]
+
+
+class _Scores(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("slopes", c_void_p)]
+
+
 KV_MODEL, KV_E4M3 = 0, 1
 
 
@@ -112,6 +132,17 @@ _SIGS = {
     "llama_op_attention_prefill": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
                                              c_void_p]),
     "llama_op_embed": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p]),
+    "llama_rope_table": (c_int32, [ctypes.POINTER(RopeScaling), c_int32, c_int32, c_void_p,
+                                   c_void_p]),
+    "llama_op_rope_norm_append": (c_int32, [c_void_p, c_void_p, c_int32, ctypes.c_int64, c_int32,
+                                            c_void_p, c_void_p, c_int32, ctypes.POINTER(_Rope),
+                                            c_void_p, c_void_p, ctypes.c_float, c_int32,
+                                            ctypes.POINTER(KV), c_void_p, c_void_p, c_void_p]),
+    "llama_op_attention_docs": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p,
+                                          c_int32, c_void_p, ctypes.POINTER(_Scores), c_void_p]),
+    "llama_op_attention_decode_shared": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                                   ctypes.POINTER(KV), c_int32, c_int32,
+                                                   ctypes.POINTER(_Scores), c_void_p]),
     "llama_op_argmax": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p]),
     "llama_sample": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, ctypes.POINTER(Sampling), c_void_p,
                                c_void_p, c_int32, c_void_p, c_void_p]),
@@ -198,6 +229,67 @@ def workspace_bytes(cfg: LlamaConfig) -> int:
     if rc:
         raise LlamaError(rc, "llama_workspace_bytes")
     return n.value
+
+
+def rope_table(n_pos, rotary_dim, *, theta=10000.0, kind=ROPE_PLAIN, factor=1.0, low_turns=1.0,
+               high_turns=32.0, original_len=4096, magnitude=1.0, stream=None):
+    """Rotation angles of scaled positions (llama_rope_table): a device tensor
+    [n_pos, rotary_dim / 2, 2] of fp32 (cos, sin), for Rope."""
+    import torch
+    if n_pos < 1 or rotary_dim < 8 or rotary_dim % 8:
+        raise ValueError("rope_table: n_pos %r, rotary_dim %r" % (n_pos, rotary_dim))
+    table = torch.empty(n_pos, rotary_dim // 2, 2, dtype=torch.float32, device="cuda")
+    sc = RopeScaling(kind, theta, factor, low_turns, high_turns, original_len, magnitude)
+    rc = lib().llama_rope_table(ctypes.byref(sc), rotary_dim, n_pos, _p(table),
+                                _stream_handle(stream))
+    if rc:
+        raise LlamaError(rc, "llama_rope_table")
+    return table
+
+
+class Rope:
+    """How heads rotate (llama_rope). table: [n_pos, rotary_dim / 2, 2] fp32 from
+    rope_table, or None for the context's own (whole heads). Keeps the table alive."""
+
+    def __init__(self, table=None, layout=ROPE_ADJACENT, rotary_dim=None):
+        import torch
+        if table is not None:
+            if table.dtype != torch.float32 or not table.is_contiguous() or table.dim() != 3 or \
+                    table.shape[2] != 2:
+                raise ValueError("Rope: the table is a contiguous fp32 [n_pos, rotary_dim / 2, 2]")
+            if rotary_dim not in (None, 0, 2 * table.shape[1]):
+                raise ValueError("Rope: rotary_dim %d, the table has %d pairs"
+                                 % (rotary_dim, table.shape[1]))
+            rotary_dim = 2 * table.shape[1] if rotary_dim is None else rotary_dim
+        elif rotary_dim is None:
+            raise ValueError("Rope: without a table give rotary_dim (the head size)")
+        self.table = table
+        self._c = _Rope(layout, rotary_dim, None if table is None else table.data_ptr(),
+                        0 if table is None else table.shape[0])
+        self._ref = ctypes.byref(self._c)
+
+
+class Scores:
+    """Score options (llama_scores): scale (0: 1/sqrt(d)), cap (0: none), slopes
+    fp32 [n_q] on the device or None. Keeps the slopes alive."""
+
+    def __init__(self, scale=0.0, cap=0.0, slopes=None):
+        import torch
+        if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_contiguous()):
+            raise ValueError("Scores: slopes are a contiguous fp32 tensor")
+        self.slopes = slopes
+        self._c = _Scores(scale, cap, None if slopes is None else slopes.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+
+def _need(what, t, dtype, shape):
+    """The tensor's address; ValueError unless it is a contiguous tensor of that
+    type and element count on the device."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != shape:
+        raise ValueError("%s: want a contiguous device tensor of %d %s, got %s %s%s" %
+                         (what, shape, dtype, tuple(t.shape), t.dtype,
+                          "" if t.is_contiguous() else " (strided)"))
+    return t.data_ptr()
 
 
 class KVCache:
@@ -402,6 +494,65 @@ class Model:
     def op_attention_prefill(self, q, k, v, B, T, out):
         self._chk(lib().llama_op_attention_prefill(self.ctx, _p(q), _p(k), _p(v), B, T, _p(out)),
                   "llama_op_attention_prefill")
+
+    def op_rope_norm_append(self, qkv, start_pos, layer, kv: KVCache, q_out, *, rope=None,
+                            cu_rows=None, q_gain=None, k_gain=None, eps=None, k_out=None,
+                            v_out=None):
+        """Head norms, rotation and KV append of packed rows (llama_op_rope_norm_append).
+        qkv [n_rows, (n_q + 2 n_kv) d], fp32 or the model's dtype, rows may be
+        strided; start_pos int32 [B]; cu_rows int32 [B + 1], or None for one row
+        per sequence; eps defaults to the model's rms_eps."""
+        import torch
+        s, dt = self.shape, self.shape.torch_dtype
+        n, B, d = qkv.shape[0], start_pos.numel(), s.head_dim
+        if qkv.dim() != 2 or qkv.shape[1] != s.qkv_rows or qkv.stride(1) != 1 or not qkv.is_cuda \
+                or (qkv.dtype != torch.float32 and qkv.dtype != dt):
+            raise ValueError("qkv: want device rows of %d %s or fp32, got %s %s"
+                             % (s.qkv_rows, dt, tuple(qkv.shape), qkv.dtype))
+        self._chk(lib().llama_op_rope_norm_append(
+            self.ctx, qkv.data_ptr(), F32 if qkv.dtype == torch.float32 else BF16, qkv.stride(0), n,
+            None if cu_rows is None else _need("cu_rows", cu_rows, torch.int32, B + 1),
+            _need("start_pos", start_pos, torch.int32, B), B, None if rope is None else rope._ref,
+            None if q_gain is None else _need("q_gain", q_gain, dt, d),
+            None if k_gain is None else _need("k_gain", k_gain, dt, d),
+            s.rms_eps if eps is None else eps, layer, ctypes.byref(kv.struct()),
+            _need("q_out", q_out, dt, n * s.n_q_heads * d),
+            None if k_out is None else _need("k_out", k_out, dt, n * s.n_kv_heads * d),
+            None if v_out is None else _need("v_out", v_out, dt, n * s.n_kv_heads * d)),
+            "llama_op_rope_norm_append")
+
+    def op_attention_docs(self, q, k, v, cu_rows, out, *, prefix=None, scores=None):
+        """Prompt attention over packed documents (llama_op_attention_docs): q
+        [n_rows, n_q, d], k and v [n_rows, n_kv, d], cu_rows int32 [B + 1]; prefix
+        int32 [B] rows attended both ways; scores a Scores."""
+        import torch
+        s, dt = self.shape, self.shape.torch_dtype
+        n, B = q.shape[0], cu_rows.numel() - 1
+        if scores is not None and scores.slopes is not None:
+            _need("slopes", scores.slopes, torch.float32, s.n_q_heads)
+        qn, kn = n * s.n_q_heads * s.head_dim, n * s.n_kv_heads * s.head_dim
+        self._chk(lib().llama_op_attention_docs(
+            self.ctx, _need("q", q, dt, qn), _need("k", k, dt, kn), _need("v", v, dt, kn), n,
+            _need("cu_rows", cu_rows, torch.int32, B + 1), B,
+            None if prefix is None else _need("prefix", prefix, torch.int32, B),
+            None if scores is None else scores._ref, _need("out", out, dt, qn)),
+            "llama_op_attention_docs")
+
+    def op_attention_decode_shared(self, q, positions, layer, kv: KVCache, out, *, shared_len=0,
+                                   shared_seq=0, scores=None):
+        """Decode attention over a cache whose first shared_len positions are
+        sequence shared_seq's for the whole batch (llama_op_attention_decode_shared)."""
+        import torch
+        s, dt = self.shape, self.shape.torch_dtype
+        B = positions.numel()
+        if scores is not None and scores.slopes is not None:
+            _need("slopes", scores.slopes, torch.float32, s.n_q_heads)
+        qn = B * s.n_q_heads * s.head_dim
+        self._chk(lib().llama_op_attention_decode_shared(
+            self.ctx, _need("q", q, dt, qn), _need("positions", positions, torch.int32, B), B, layer,
+            ctypes.byref(kv.struct()), shared_len, shared_seq,
+            None if scores is None else scores._ref, _need("out", out, dt, qn)),
+            "llama_op_attention_decode_shared")
 
     def op_embed(self, tokens, out):
         self._chk(lib().llama_op_embed(self.ctx, _p(tokens), tokens.numel(), _p(out)), "llama_op_embed")

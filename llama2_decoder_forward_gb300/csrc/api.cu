@@ -49,6 +49,7 @@ bool load_encode() {
     g_prep_err = gemm_prepare();
     if (g_prep_err == cudaSuccess) g_prep_err = attn_prepare();
     if (g_prep_err == cudaSuccess) g_prep_err = sample_prepare();
+    if (g_prep_err == cudaSuccess) g_prep_err = attn_simt_prepare();
   });
   return g_encode != nullptr && g_prep_err == cudaSuccess;
 }
@@ -1204,6 +1205,197 @@ int llama_sample(llama_ctx* c, const float* logits, int32_t B, int32_t V, const 
   Prof pf(c, LLAMA_KERNEL_SAMPLE);
   c->launches++;
   return cuda_rc(launch_sample(sc, c->stream));
+}
+
+// ---------------------------------------------------------------- beside the plain path
+namespace {
+// The new operations launch on the context's device only.
+int check_device(const llama_ctx* c) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return LLAMA_ERR_CUDA;
+  }
+  return dev == c->device ? LLAMA_OK : LLAMA_ERR_INVALID_ARG;
+}
+
+int score_args(const llama_ctx* c, const llama_scores* s, ScoreArgs* out) {
+  out->scale = 1.f / std::sqrt((float)c->cfg.head_dim);
+  out->cap = 0.f;
+  out->slopes = nullptr;
+  if (!s) return LLAMA_OK;
+  if (!(s->scale >= 0.f) || !std::isfinite(s->scale) || !(s->cap >= 0.f) || !std::isfinite(s->cap) ||
+      (reinterpret_cast<uintptr_t>(s->slopes) & 3u) != 0)
+    return LLAMA_ERR_INVALID_ARG;
+  if (s->scale > 0.f) out->scale = s->scale;
+  out->cap = s->cap;
+  out->slopes = s->slopes;
+  return LLAMA_OK;
+}
+}  // namespace
+
+int llama_rope_table(const llama_rope_scaling* s, int32_t rotary_dim, int32_t n_pos, float* table,
+                     void* stream) {
+  if (!s || !table || !aligned16(table) || rotary_dim < 8 || rotary_dim % 8 != 0 || n_pos < 1)
+    return LLAMA_ERR_INVALID_ARG;
+  if (s->kind != LLAMA_ROPE_PLAIN && s->kind != LLAMA_ROPE_LINEAR && s->kind != LLAMA_ROPE_BANDS)
+    return LLAMA_ERR_INVALID_ARG;
+  if (!(s->theta > 0.f) || !std::isfinite(s->theta) || !(s->magnitude > 0.f) ||
+      !std::isfinite(s->magnitude))
+    return LLAMA_ERR_INVALID_ARG;
+  if (s->kind != LLAMA_ROPE_PLAIN && (!(s->factor > 0.f) || !std::isfinite(s->factor)))
+    return LLAMA_ERR_INVALID_ARG;
+  if (s->kind == LLAMA_ROPE_BANDS &&
+      (!(s->low_turns >= 0.f) || !(s->high_turns > s->low_turns) || !std::isfinite(s->high_turns) ||
+       s->original_len < 1))
+    return LLAMA_ERR_INVALID_ARG;
+  return cuda_rc(launch_rope_scaled_table(*s, rotary_dim, n_pos, reinterpret_cast<float2*>(table),
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int llama_op_rope_norm_append(llama_ctx* c, const void* qkv, int32_t qkv_dtype, int64_t qkv_ld,
+                              int32_t n_rows, const int32_t* cu_rows, const int32_t* start_pos,
+                              int32_t B, const llama_rope* rope, const void* q_gain,
+                              const void* k_gain, float norm_eps, int32_t layer,
+                              const llama_kv* kv, void* q_out, void* k_out, void* v_out) {
+  TRY(check_ctx(c));
+  const llama_config& cf = c->cfg;
+  if (!qkv || !start_pos || !q_out || n_rows < 1 || B < 1 || layer < 0 || layer >= cf.n_layers)
+    return LLAMA_ERR_INVALID_ARG;
+  if (!cu_rows && n_rows != B) return LLAMA_ERR_INVALID_ARG;
+  if (qkv_dtype != LLAMA_F32 && qkv_dtype != cf.dtype) return LLAMA_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)(cf.n_q_heads + 2 * cf.n_kv_heads) * cf.head_dim;
+  if (qkv_ld < width || qkv_ld * elem_size(qkv_dtype) % 16 != 0) return LLAMA_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(q_gain) || !aligned16(k_gain) || !aligned16(q_out) ||
+      !aligned16(k_out) || !aligned16(v_out))
+    return LLAMA_ERR_INVALID_ARG;
+  if ((q_gain || k_gain) && !(norm_eps > 0.f && std::isfinite(norm_eps)))
+    return LLAMA_ERR_INVALID_ARG;
+  RopeNormArgs a{};
+  if (rope) {
+    if (rope->layout != LLAMA_ROPE_ADJACENT && rope->layout != LLAMA_ROPE_HALF)
+      return LLAMA_ERR_INVALID_ARG;
+    if (rope->rotary_dim < 0 || rope->rotary_dim > cf.head_dim) return LLAMA_ERR_INVALID_ARG;
+    if (rope->rotary_dim % 8 != 0) return LLAMA_ERR_UNSUPPORTED;
+    a.rotary = rope->rotary_dim;
+    a.half = rope->layout == LLAMA_ROPE_HALF;
+    if (a.rotary > 0 && rope->table) {
+      if (rope->n_pos < 1 || !aligned16(rope->table)) return LLAMA_ERR_INVALID_ARG;
+      a.table = reinterpret_cast<const float2*>(rope->table);
+      a.n_pos = rope->n_pos;
+    } else if (a.rotary > 0) {
+      if (a.rotary != cf.head_dim) return LLAMA_ERR_INVALID_ARG;
+      a.table = c->rope;
+      a.n_pos = cf.max_seq;
+    }
+  }
+  TRY(check_kv(c, kv, B));
+  TRY(check_device(c));
+  a.qkv = qkv;
+  a.ld = qkv_ld;
+  a.n_rows = n_rows;
+  a.n_seq = B;
+  a.cu_rows = cu_rows;
+  a.start_pos = start_pos;
+  a.q_gain = q_gain;
+  a.k_gain = k_gain;
+  a.eps = norm_eps;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.k_cache = kv->k;
+  a.v_cache = kv->v;
+  a.page_table = kv->page_table;
+  a.status = c->status;
+  a.n_q = cf.n_q_heads;
+  a.n_kv = cf.n_kv_heads;
+  a.head_dim = cf.head_dim;
+  a.layer = layer;
+  a.page_size = kv->page_size;
+  a.capacity = kv->capacity;
+  a.batch_cap = kv->batch_capacity;
+  a.n_pages = kv->n_pages;
+  a.max_pages = kv->max_pages_per_seq;
+  a.kv_fp8 = kv->kv_dtype == LLAMA_KV_E4M3;
+  a.k_scale = kv->k_scale;
+  a.v_scale = kv->v_scale;
+  Prof pf(c, LLAMA_KERNEL_ROPE_APPEND);
+  c->launches++;
+  return cuda_rc(launch_rope_norm_append(cf.dtype, qkv_dtype, a, c->stream));
+}
+
+int llama_op_attention_docs(llama_ctx* c, const void* q, const void* k, const void* v,
+                            int32_t n_rows, const int32_t* cu_rows, int32_t B,
+                            const int32_t* prefix_len, const llama_scores* scores, void* out) {
+  TRY(check_ctx(c));
+  const llama_config& cf = c->cfg;
+  if (!q || !k || !v || !out || !cu_rows || n_rows < 1 || B < 1) return LLAMA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+    return LLAMA_ERR_INVALID_ARG;
+  if ((int64_t)n_rows * cf.n_q_heads >= (1ll << 30)) return LLAMA_ERR_OUT_OF_RANGE;
+  DocsArgs a{};
+  TRY(score_args(c, scores, &a.sc));
+  TRY(check_device(c));
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.n_rows = n_rows;
+  a.n_docs = B;
+  a.n_q = cf.n_q_heads;
+  a.n_kv = cf.n_kv_heads;
+  a.head_dim = cf.head_dim;
+  a.cu_rows = cu_rows;
+  a.prefix_len = prefix_len;
+  a.status = c->status;
+  Prof pf(c, LLAMA_KERNEL_ATTN_PREFILL);
+  c->launches++;
+  return cuda_rc(launch_docs_simt(cf.dtype, a, c->stream));
+}
+
+int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t* positions,
+                                     int32_t B, int32_t layer, const llama_kv* kv,
+                                     int32_t shared_len, int32_t shared_seq,
+                                     const llama_scores* scores, void* out) {
+  TRY(check_ctx(c));
+  const llama_config& cf = c->cfg;
+  if (!q || !positions || !out || B < 1 || layer < 0 || layer >= cf.n_layers || shared_len < 0 ||
+      shared_seq < 0)
+    return LLAMA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return LLAMA_ERR_INVALID_ARG;
+  if (B > cf.max_batch) return LLAMA_ERR_OUT_OF_RANGE;
+  TRY(check_kv(c, kv, B));
+  if (kv->kv_dtype != LLAMA_KV_MODEL) return LLAMA_ERR_UNSUPPORTED;
+  if (shared_seq >= (kv->page_size ? B : kv->batch_capacity)) return LLAMA_ERR_INVALID_ARG;
+  const int64_t slots = kv->page_size ? (int64_t)kv->max_pages_per_seq * kv->page_size : kv->capacity;
+  const int limit = (int)std::min<int64_t>(slots, cf.max_seq);
+  if (shared_len > limit) return LLAMA_ERR_OUT_OF_RANGE;
+  SharedArgs a{};
+  TRY(score_args(c, scores, &a.sc));
+  TRY(check_device(c));
+  a.q = q;
+  a.out = out;
+  a.positions = positions;
+  a.k_cache = kv->k;
+  a.v_cache = kv->v;
+  a.page_table = kv->page_table;
+  a.B = B;
+  a.n_q = cf.n_q_heads;
+  a.n_kv = cf.n_kv_heads;
+  a.head_dim = cf.head_dim;
+  a.layer = layer;
+  a.page_size = kv->page_size;
+  a.capacity = kv->capacity;
+  a.batch_cap = kv->batch_capacity;
+  a.n_pages = kv->n_pages;
+  a.max_pages = kv->max_pages_per_seq;
+  a.key_limit = limit;
+  a.shared_len = shared_len;
+  a.shared_seq = shared_seq;
+  a.status = c->status;
+  Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
+  c->launches++;
+  return cuda_rc(launch_shared_simt(cf.dtype, a, c->stream));
 }
 
 int llama_op_argmax(llama_ctx* c, const float* logits, int32_t B, int32_t V, int32_t* ids) {

@@ -223,6 +223,63 @@ cudaError_t attn_prepare();
 cudaError_t launch_attn_prefill_tc(const AttnPrefillArgs& a, cudaStream_t st);
 cudaError_t attn_prefill_tc_prepare();
 
+// ---- head norms + rotation + append (k_rope_norm.cu)
+struct RopeNormArgs {
+  const void* qkv;           // [n_rows, ld] fp32 or T
+  int64_t ld;
+  int n_rows, n_seq;
+  const int32_t* cu_rows;    // [n_seq + 1], or null: row b is sequence b's
+  const int32_t* start_pos;  // [n_seq]
+  const float2* table;       // [n_pos][rotary / 2]
+  int n_pos, rotary, half;
+  const void* q_gain;        // T [d] or null
+  const void* k_gain;
+  float eps;
+  void *q_out, *k_out, *v_out, *k_cache, *v_cache;
+  const int32_t* page_table;
+  uint32_t* status;
+  int n_q, n_kv, head_dim, layer;
+  int page_size, capacity, batch_cap, n_pages, max_pages;
+  int kv_fp8;
+  float k_scale, v_scale;
+};
+cudaError_t launch_rope_norm_append(int dtype, int src_dtype, const RopeNormArgs& a,
+                                    cudaStream_t st);
+cudaError_t launch_rope_scaled_table(const llama_rope_scaling& s, int rotary_dim, int n_pos,
+                                     float2* table, cudaStream_t st);
+
+// ---- capped / biased attention over documents and over the cache
+struct ScoreArgs {
+  float scale, cap;     // cap 0: none
+  const float* slopes;  // [n_q] or null
+};
+struct DocsArgs {
+  const void *q, *k, *v;       // [n_rows, n_q, d], [n_rows, n_kv, d]
+  void* out;                   // [n_rows, n_q, d]
+  int n_rows, n_docs, n_q, n_kv, head_dim;
+  const int32_t* cu_rows;      // [n_docs + 1]
+  const int32_t* prefix_len;   // [n_docs] or null
+  ScoreArgs sc;
+  uint32_t* status;
+};
+struct SharedArgs {
+  const void* q;               // [B, n_q, d]
+  void* out;
+  const int32_t* positions;    // [B]
+  const void *k_cache, *v_cache;
+  const int32_t* page_table;
+  int B, n_q, n_kv, head_dim, layer;
+  int page_size, capacity, batch_cap, n_pages, max_pages;
+  int key_limit;               // min(cache positions, max_seq)
+  int shared_len, shared_seq;
+  ScoreArgs sc;
+  uint32_t* status;
+};
+// CUDA-core forms for any head_dim (k_attn_simt.cu)
+cudaError_t attn_simt_prepare();
+cudaError_t launch_docs_simt(int dtype, const DocsArgs& a, cudaStream_t st);
+cudaError_t launch_shared_simt(int dtype, const SharedArgs& a, cudaStream_t st);
+
 // ---- token sampling (k_sample.cu)
 struct SampleCall {
   const float* logits;  // [B, ldl] fp32, V used per row

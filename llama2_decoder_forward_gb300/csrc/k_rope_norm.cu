@@ -1,0 +1,218 @@
+// Head norms, rotation and KV-cache append of new rows in one pass, and the
+// table of scaled rotation angles ("Llama2架构与推理全解析" §1.2 RMSNorm, here
+// over each Q / K head; §1.4 RoPE; §2.4 append).
+//
+//   u = x / sqrt(mean(x^2) + eps) * gain           (Q and K heads, optional)
+//   (y0, y1) = (u0 c - u1 s, u0 s + u1 c)          for the rotating pairs
+//
+// Bound by the bytes of the rows: each source value is read once and each
+// output written once. A thread owns 8 values of one head as two groups of 4
+// at e0 and e1: for the half layout e0 = 4u and e1 = rotary/2 + 4u, so both
+// values of a pair sit in one thread and nothing is exchanged; else 8
+// consecutive values. The lanes of a head (16 at 128 values) add up its
+// squares with butterflies.
+#include "common.cuh"
+#include "internal.h"
+
+namespace llgb {
+
+namespace {
+
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+__device__ __forceinline__ void load4(const bf16* p, float* v) {
+  const uint2 x = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(x.x << 16);
+  v[1] = __uint_as_float(x.x & 0xffff0000u);
+  v[2] = __uint_as_float(x.y << 16);
+  v[3] = __uint_as_float(x.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(bf16* p, const float* v) {  // nearest even, the cache's type
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+}
+__device__ __forceinline__ uint32_t e4m3x4(const float* v, float scale) {
+  return (uint32_t)f32_to_e4m3(v[0] / scale) | (uint32_t)f32_to_e4m3(v[1] / scale) << 8 |
+         (uint32_t)f32_to_e4m3(v[2] / scale) << 16 | (uint32_t)f32_to_e4m3(v[3] / scale) << 24;
+}
+
+// The sequence of packed row r: the largest b with cu[b] <= r, or -1 when no
+// sequence owns the row. A whole warp searches 32 ways per step, one load
+// each, so 1024 sequences cost two dependent loads.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seq, int r, int lane) {
+  int lo = 0, n = n_seq;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const uint32_t m = __ballot_sync(0xffffffffu, i < n && cu[lo + i] <= r);
+    const int k = max(0, __popc(m) - 1);
+    lo += k * step;
+    n = max(1, min(step, n - k * step));
+  }
+  return cu[lo] <= r && r < cu[lo + 1] ? lo : -1;
+}
+
+constexpr int RN_THREADS = 256;
+
+// grid: (chunks of RN_THREADS / lanes heads) x rows, flattened.
+template <typename S, typename T>
+__global__ void __launch_bounds__(RN_THREADS) rope_norm_append_kernel(RopeNormArgs a, int lanes,
+                                                                      int chunks) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int d = a.head_dim, heads = a.n_q + 2 * a.n_kv;
+  const int r = blockIdx.x / chunks, chunk = blockIdx.x - r * chunks;
+  const int u = threadIdx.x & (lanes - 1);
+  const int head = chunk * (RN_THREADS / lanes) + threadIdx.x / lanes;
+  const bool on = head < heads && u < d / 8;
+  const bool is_v = head >= a.n_q + a.n_kv;
+  const bool turns = on && !is_v && u < a.rotary / 8;
+  int e0 = 8 * u, e1 = 8 * u + 4;
+  if (a.half && u < a.rotary / 8) {
+    e0 = 4 * u;
+    e1 = a.rotary / 2 + 4 * u;
+  }
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (on) {
+    const S* src = reinterpret_cast<const S*>(a.qkv) + (size_t)r * a.ld + (size_t)head * d;
+    load4(src + e0, v);
+    load4(src + e1, v + 4);
+  }
+  // the row's sequence and position
+  int b = r, pos;
+  if (a.cu_rows) {
+    b = sequence_of(a.cu_rows, a.n_seq, r, threadIdx.x & 31);
+    if (b < 0) return;  // a row of no sequence
+    pos = a.start_pos[b] + (r - a.cu_rows[b]);
+  } else {
+    pos = a.start_pos[b];
+  }
+  const bool pos_ok = pos >= 0 && (a.rotary == 0 || pos < a.n_pos);
+  if (!pos_ok && chunk == 0 && threadIdx.x == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
+
+  const T* gain = reinterpret_cast<const T*>(is_v ? nullptr : head < a.n_q ? a.q_gain : a.k_gain);
+  if (a.q_gain || a.k_gain) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+    for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (on && gain) {
+      const float inv = 1.0f / sqrtf(ss / (float)d + a.eps);
+      float g[8];
+      load4(gain + e0, g);
+      load4(gain + e1, g + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * g[i];
+    }
+  }
+  if (!on) return;
+  if (!pos_ok) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  } else if (turns) {
+    const float4* cs4 = reinterpret_cast<const float4*>(a.table + (size_t)pos * (a.rotary / 2) + 4 * u);
+    const float4 c01 = cs4[0], c23 = cs4[1];
+    const float c[4] = {c01.x, c01.z, c23.x, c23.z}, s[4] = {c01.y, c01.w, c23.y, c23.w};
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int i0 = a.half ? p : 2 * p, i1 = a.half ? 4 + p : 2 * p + 1;
+      const float x0 = v[i0], x1 = v[i1];
+      v[i0] = x0 * c[p] - x1 * s[p];
+      v[i1] = x0 * s[p] + x1 * c[p];
+    }
+  }
+  if (head < a.n_q) {
+    T* dst = reinterpret_cast<T*>(a.q_out) + ((size_t)r * a.n_q + head) * d;
+    store4(dst + e0, v);
+    store4(dst + e1, v + 4);
+    return;
+  }
+  const int g = is_v ? head - a.n_q - a.n_kv : head - a.n_q;
+  if (void* side = is_v ? a.v_out : a.k_out) {
+    T* dst = reinterpret_cast<T*>(side) + ((size_t)r * a.n_kv + g) * d;
+    store4(dst + e0, v);
+    store4(dst + e1, v + 4);
+  }
+  if (!pos_ok) return;
+  size_t slot;
+  if (a.page_size == 0) {
+    if (pos >= a.capacity || b >= a.batch_cap) {
+      if (u == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
+      return;
+    }
+    slot = (((size_t)a.layer * a.batch_cap + b) * a.n_kv + g) * a.capacity + pos;
+  } else {
+    const int pi = pos / a.page_size;
+    if (pi >= a.max_pages) {
+      if (u == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
+      return;
+    }
+    const int page = a.page_table[(size_t)b * a.max_pages + pi];
+    if (page < 0 || page >= a.n_pages) {
+      if (u == 0) flag(a.status, LLAMA_FLAG_PAGE_RANGE);
+      return;
+    }
+    slot = (((size_t)a.layer * a.n_pages + page) * a.n_kv + g) * a.page_size + (pos - pi * a.page_size);
+  }
+  void* cache = is_v ? a.v_cache : a.k_cache;
+  if (a.kv_fp8) {
+    uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + slot * d;
+    const float sc = is_v ? a.v_scale : a.k_scale;
+    *reinterpret_cast<uint32_t*>(dst + e0) = e4m3x4(v, sc);
+    *reinterpret_cast<uint32_t*>(dst + e1) = e4m3x4(v + 4, sc);
+  } else {
+    T* dst = reinterpret_cast<T*>(cache) + slot * d;
+    store4(dst + e0, v);
+    store4(dst + e1, v + 4);
+  }
+}
+
+// table[m * n + j] = magnitude * (cos, sin)(m * f_j), n = rotary_dim / 2; the
+// angles in fp64 (a far position's angle has no fp32 digits left), rounded once.
+__global__ void rope_scaled_table_kernel(llama_rope_scaling s, int n, int n_pos, float2* table) {
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (long long)n_pos * n) return;
+  const int m = (int)(i / n), j = (int)(i - (long long)m * n);
+  double f = pow((double)s.theta, -(double)j / (double)n);
+  if (s.kind == LLAMA_ROPE_LINEAR) {
+    f /= (double)s.factor;
+  } else if (s.kind == LLAMA_ROPE_BANDS) {
+    const double turns = (double)s.original_len * f / 6.283185307179586476925;
+    const double lo = (double)s.low_turns, hi = (double)s.high_turns;
+    const double g = fmin(1.0, fmax(0.0, (turns - lo) / (hi - lo)));
+    f *= g + (1.0 - g) / (double)s.factor;
+  }
+  double sn, cs;
+  sincos((double)m * f, &sn, &cs);
+  table[i] = make_float2((float)(cs * (double)s.magnitude), (float)(sn * (double)s.magnitude));
+}
+
+template <typename S, typename T>
+cudaError_t launch_rn(const RopeNormArgs& a, cudaStream_t st) {
+  int lanes = 1;
+  while (lanes * 8 < a.head_dim) lanes <<= 1;
+  const int per = RN_THREADS / lanes, chunks = (a.n_q + 2 * a.n_kv + per - 1) / per;
+  return launch_k(rope_norm_append_kernel<S, T>, dim3((unsigned)((long long)chunks * a.n_rows)),
+                  dim3(RN_THREADS), 0, st, 0, a, lanes, chunks);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_norm_append(int dtype, int src_dtype, const RopeNormArgs& a,
+                                    cudaStream_t st) {
+  if (dtype == LLAMA_F32) return launch_rn<float, float>(a, st);
+  return src_dtype == LLAMA_F32 ? launch_rn<float, bf16>(a, st) : launch_rn<bf16, bf16>(a, st);
+}
+
+cudaError_t launch_rope_scaled_table(const llama_rope_scaling& s, int rotary_dim, int n_pos,
+                                     float2* table, cudaStream_t st) {
+  const long long n = (long long)n_pos * (rotary_dim / 2);
+  rope_scaled_table_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(s, rotary_dim / 2, n_pos,
+                                                                        table);
+  return cudaGetLastError();
+}
+
+}  // namespace llgb

@@ -1,0 +1,661 @@
+"""The operators beside the plain Llama2 path against plain fp64 forms: head
+norms + rotation + append, attention over packed documents, decode attention
+over a shared prefix; and the three together, as a server runs them.
+
+Tolerances. A rounding is off by at most half a step, eps / 2 relative: 2^-8
+for bf16, 2^-24 for fp32, 2^-4 for E4M3 (2^-10 absolute below its normals).
+
+* Rows: bf16 outputs are one rounding of an fp32 value whose own error is
+  some 2^-24 of the head's largest value: 2^-8 |ref| + 2^-18 max|head|.
+* Attention, bf16: the output's rounding, 2^-8 |ref|; the weights are rounded
+  once for the tensor cores, 2^-8 of sum p|v|; scores carry fp32 sums of 128
+  products, below 2^-11 at these magnitudes, which moves every weight by that
+  and the normalising sum by as much: 2^-10 of sum p|v|.
+* Attention, fp32: a score is off by at most (d + 8) 2^-24 sum|q k| scale plus
+  2^-22 of its bias, cap or size (a few fp32 roundings); twice that, and n/8 + 64
+  roundings of the sums and exponentials, act on sum p|v|.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from _common import f64, need_gpu, to_dev
+from llama2_decoder_forward_gb300 import binding, synth
+from oracle import attention_forms as A
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _randn(shape, dtype, seed, std=1.0):
+    return (torch.randn(*shape, generator=_gen(seed)) * std).to(dtype)
+
+
+def _model(nq, nkv, d=128, dtype="bf16", max_batch=8, max_seq=4096, n_layers=1):
+    need_gpu()
+    shape = synth.Shape(n_layers, 256, nq, nkv, d, 256, 256, dtype=dtype)
+    w = {"layers": [synth.layer_weights(shape, 3, l) for l in range(n_layers)]}
+    return binding.Model(shape, to_dev(w), max_batch=max_batch, max_tokens=0, max_seq=max_seq,
+                         has_embed_head=False), shape
+
+
+def _within(got, ref, bound, what):
+    got = f64(got)
+    err = np.abs(got - ref)
+    bad = ~(err <= bound)
+    if bad.any():
+        i = np.unravel_index(np.argmax(np.where(np.isfinite(err), err - bound, np.inf)), err.shape)
+        raise AssertionError("%s: %d of %d out of tolerance; worst at %s: got %r ref %r bound %r"
+                             % (what, bad.sum(), bad.size, i, got[i], ref[i], np.broadcast_to(bound, err.shape)[i]))
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# --------------------------------------------------------------------------- table
+@pytest.mark.parametrize("kind,kw", [
+    ("plain", {}), ("plain", dict(theta=1e6)), ("linear", dict(factor=4.0)),
+    ("bands", dict(factor=8.0, low_turns=1.0, high_turns=4.0, original_len=8192)),
+    ("bands", dict(factor=16.0, low_turns=1.0, high_turns=32.0, original_len=4096, magnitude=1.25)),
+])
+@pytest.mark.parametrize("n_pos,r", [(1, 8), (1000, 128), (70001, 24)])
+def test_rope_table(kind, kw, n_pos, r):
+    need_gpu()
+    kinds = dict(plain=binding.ROPE_PLAIN, linear=binding.ROPE_LINEAR, bands=binding.ROPE_BANDS)
+    t = binding.rope_table(n_pos, r, kind=kinds[kind], **kw)
+    ref = A.rotation_table(n_pos, r, kind=kind, **kw)
+    # one fp32 rounding of an fp64 value; the fp64 angle (up to 7e4 rad) of either side is off by 2^-36
+    _within(t, ref, 2.0 ** -24 * np.abs(ref) + 2.0 ** -33, "table")
+
+
+# --------------------------------------------------------------------------- rows
+def _rows_case(nq, nkv, d, dtype, src, lens, starts, *, rotary=128, half=True, norm="qk", page=16,
+               e4m3=None, side=True, token=False, lead=0, tail=0, ld_pad=0, layers=2, layer=1, seed=5,
+               own_table=True, scaled=False):
+    """Runs the operator and checks q, side rows, every written slot and that nothing else changed."""
+    m, shape = _model(nq, nkv, d, dtype, max_batch=len(lens), n_layers=layers)
+    dt = shape.torch_dtype
+    n, width = lead + sum(lens) + tail, (nq + 2 * nkv) * d
+    x = _randn((n, width + ld_pad), torch.float32 if src == "f32" else dt, seed, 1.5)
+    gains = [(1 + 0.1 * torch.randn(d, generator=_gen(seed + i))).to(dt) for i in (1, 2)]
+    qg, kg = (gains[0] if "q" in norm else None), (gains[1] if "k" in norm else None)
+    top = max(s + l for s, l in zip(starts, lens)) or 1
+    kw = dict(kind="linear", factor=4.0) if scaled else {}
+    table = A.rotation_table(max(top, 1), rotary, **kw).astype(np.float32) if rotary else None
+    rope = None
+    if rotary and own_table:
+        rope = binding.Rope(torch.from_numpy(table).cuda(), binding.ROPE_HALF if half else binding.ROPE_ADJACENT)
+    elif rotary:
+        rope = binding.Rope(None, binding.ROPE_HALF if half else binding.ROPE_ADJACENT, rotary)
+    cu = [lead]
+    for l in lens:
+        cu.append(cu[-1] + l)
+    if page:
+        pages = [max(1, math.ceil((s + l) / page)) for s, l in zip(starts, lens)]
+        pt, total = synth.page_table(pages, max(pages), seed)
+        kv = binding.KVCache(shape, n_pages=total, page_size=page, page_table=pt.cuda(), e4m3=e4m3)
+    else:
+        kv = binding.KVCache(shape, batch=len(lens), capacity=top + 3, e4m3=e4m3)
+    mark = 0x35 if e4m3 else 7.0
+    kv.k.fill_(mark)
+    kv.v.fill_(mark)
+    q_out = torch.full((n, nq * d), 3.0, dtype=dt, device="cuda")
+    ko = torch.full((n, nkv * d), 3.0, dtype=dt, device="cuda") if side else None
+    vo = torch.full((n, nkv * d), 3.0, dtype=dt, device="cuda") if side else None
+    xd = x.cuda()
+    m.op_rope_norm_append(xd[:, :width], _i32(starts), layer, kv, q_out, rope=rope,
+                          cu_rows=None if token else _i32(cu), q_gain=None if qg is None else qg.cuda(),
+                          k_gain=None if kg is None else kg.cuda(), eps=1e-6, k_out=ko, v_out=vo)
+    m.sync()
+    xf = f64(x)[:, :width].reshape(n, nq + 2 * nkv, d)
+    K, V = kv.k, kv.v
+    if e4m3:
+        K, V = (t.view(torch.float8_e4m3fn).float() for t in (K, V))
+    K, V = f64(K)[layer].copy(), f64(V)[layer].copy()
+    if e4m3:  # codes stand for value / scale
+        mark = float(torch.tensor([0x35], dtype=torch.uint8).view(torch.float8_e4m3fn).float())
+
+    def close(got, ref, what, scale=None):
+        big = np.abs(ref).max(-1, keepdims=True)
+        if scale is not None:
+            ref = np.clip(ref / scale, -448, 448)
+            _within(got, ref, 2.0 ** -4 * np.abs(ref) + 2.0 ** -10 + 2.0 ** -18 * np.minimum(big / scale, 448), what)
+        elif dtype == "bf16":
+            _within(got, ref, 2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * big, what)
+        else:
+            _within(got, ref, 2.0 ** -24 * np.abs(ref) + 32 * 2.0 ** -24 * big, what)
+
+    for b, (l, p0) in enumerate(zip(lens, starts)):
+        for i in range(l):
+            r, p = cu[b] + i, p0 + i
+            q, k, v = xf[r, :nq], xf[r, nq:nq + nkv], xf[r, nq + nkv:]
+            q = q if qg is None else A.head_norm(q, f64(qg), 1e-6)
+            k = k if kg is None else A.head_norm(k, f64(kg), 1e-6)
+            if rotary:
+                q, k = A.rotate(q, table[p].astype(np.float64), half), A.rotate(k, table[p].astype(np.float64), half)
+            close(q_out[r].view(nq, d), q, "q row %d" % r)
+            if side:
+                close(ko[r].view(nkv, d), k, "k side row %d" % r)
+                close(vo[r].view(nkv, d), v, "v side row %d" % r)
+            at = (int(pt[b, p // page]), slice(None), p % page) if page else (b, slice(None), p)
+            close(K[at], k, "cached k %d" % r, e4m3 and e4m3[0])
+            close(V[at], v, "cached v %d" % r, e4m3 and e4m3[1])
+            K[at], V[at] = mark, mark
+    assert np.all(K == mark) and np.all(V == mark), "another slot of the layer was written"
+    for t in (kv.k, kv.v):
+        others = torch.cat((t[:layer].flatten(), t[layer + 1:].flatten()))
+        assert torch.all(others == (0x35 if e4m3 else 7.0)), "another layer was written"
+    outside = list(range(lead)) + list(range(cu[-1], n))
+    if outside:
+        assert torch.all(q_out[outside] == 3.0) and (not side or torch.all(ko[outside] == 3.0))
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("rotary", [0, 8, 24, 64, 128])
+@pytest.mark.parametrize("norm", ["", "qk", "k"])
+def test_rows_layouts(half, rotary, norm):
+    _rows_case(8, 2, 128, "bf16", "f32", [5, 0, 17, 1], [0, 9, 30, 1500], half=half, rotary=rotary, norm=norm)
+
+
+@pytest.mark.parametrize("src", ["f32", "bf16"])
+@pytest.mark.parametrize("page", [0, 16, 48])
+@pytest.mark.parametrize("e4m3", [None, (0.02, 0.004)])
+def test_rows_caches(src, page, e4m3):
+    _rows_case(16, 4, 128, "bf16", src, [1, 33, 2], [15, 40, 0], page=page, e4m3=e4m3, half=False)
+
+
+@pytest.mark.parametrize("nq,nkv,d", [(4, 2, 64), (5, 5, 40), (3, 1, 256), (1, 1, 8)])
+@pytest.mark.parametrize("half", [False, True])
+def test_rows_fp32(nq, nkv, d, half):
+    _rows_case(nq, nkv, d, "f32", "f32", [7, 1, 20], [0, 100, 3], rotary=d if d < 64 else d - 24, page=16,
+               half=half)
+
+
+def test_rows_single_tokens():
+    _rows_case(64, 8, 128, "bf16", "bf16", [1] * 33, [3 * i for i in range(33)], token=True, side=False)
+
+
+def test_rows_of_no_sequence_are_left():
+    _rows_case(8, 8, 128, "bf16", "f32", [3, 1], [4, 0], lead=2, tail=5)
+
+
+def test_rows_strided_source():
+    _rows_case(12, 4, 128, "bf16", "f32", [9], [4], ld_pad=64)
+    _rows_case(12, 4, 128, "bf16", "bf16", [9], [4], ld_pad=8)
+
+
+def test_rows_many_sequences():
+    g = _gen(9)
+    lens = torch.randint(0, 3, (1500,), generator=g).tolist()
+    _rows_case(1, 1, 128, "bf16", "f32", lens, [i % 5 for i in range(1500)], page=16, rotary=32)
+
+
+def test_rows_context_table_matches_plain_append():
+    # without a table the context's own angles; the same bits as the plain operator
+    m, shape = _model(8, 2)
+    x = _randn((6, shape.qkv_rows), torch.float32, 21).cuda()
+    pos = _i32([0, 1, 77, 4095, 12, 3])
+    outs = []
+    for fused in (False, True):
+        kv = binding.KVCache(shape, batch=6, capacity=4096)
+        q = torch.empty(6, 8 * 128, dtype=torch.bfloat16, device="cuda")
+        if fused:
+            m.op_rope_norm_append(x, pos, 0, kv, q, rope=binding.Rope(None, binding.ROPE_ADJACENT, 128))
+        else:
+            m.op_rope_append(x, 1, pos, 0, kv, q)
+        m.sync()
+        outs.append((q, kv.k, kv.v))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_rows_out_of_range_are_flagged_and_skipped():
+    m, shape = _model(4, 2, max_batch=4)
+    d = 128
+    x = _randn((4, shape.qkv_rows), torch.float32, 31).cuda()
+    pt = _i32([[0, 1], [2, 9], [3, 4], [5, -1]])  # page 9 is not in the pool
+    kv = binding.KVCache(shape, n_pages=6, page_size=16, page_table=pt)
+    table = binding.rope_table(40, 128)
+    q = torch.full((4, 4 * d), 3.0, dtype=torch.bfloat16, device="cuda")
+    # in range; bad page; past the table; past the cache's pages (but in the table)
+    m.op_rope_norm_append(x, _i32([5, 20, 40, 35]), 0, kv, q, rope=binding.Rope(table))
+    rc, flags = m.sync_status()
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE | binding.FLAG_PAGE_RANGE
+    assert torch.all(q[2] == 0) and torch.all(q[[0, 1, 3]].abs().sum(-1) > 0)
+    assert int((kv.k != 0).any(-1).sum()) == 2  # one position's two K/V heads
+    m.op_rope_norm_append(x, _i32([-1, 20, 0, 0]), 0, kv, q, rope=binding.Rope(table))
+    rc, flags = m.sync_status()
+    assert rc == 5 and flags & binding.FLAG_POS_RANGE and torch.all(q[0] == 0)
+
+
+# --------------------------------------------------------------------------- attention
+def _attn_bound(ref, mass, dtype, n, d, big, extra):
+    if dtype == "bf16":
+        return 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * mass
+    score = (d + 8) * 2.0 ** -24 * big + 2.0 ** -22 * extra
+    return 2.0 ** -24 * np.abs(ref) + (2 * score + (n / 8 + 64) * 2.0 ** -24) * mass
+
+
+def _slopes(nq):
+    return torch.exp2(-8.0 * torch.arange(1, nq + 1).float() / nq)
+
+
+def _docs_case(nq, nkv, d, dtype, lens, *, prefix=None, cap=0.0, bias=False, scale=0.0, lead=0, tail=0,
+               seed=7, std=1.5, rows=None, poison=False):
+    m, shape = _model(nq, nkv, d, dtype)
+    dt = shape.torch_dtype
+    n = lead + sum(lens) + tail
+    q, k, v = (_randn((n, h, d), dt, seed + i, s) for i, (h, s) in enumerate(((nq, std), (nkv, std), (nkv, 1.0))))
+    cu = [lead]
+    for l in lens:
+        cu.append(cu[-1] + l)
+    if poison:  # rows of no document may hold anything
+        for t in (q, k, v):
+            t[:lead] = float("nan")
+            t[cu[-1]:] = float("inf")
+    slopes = _slopes(nq) if bias else None
+    out = torch.full((n, nq * d), 3.0, dtype=dt, device="cuda")
+    m.op_attention_docs(q.cuda(), k.cuda(), v.cuda(), _i32(cu), out,
+                        prefix=None if prefix is None else _i32(prefix),
+                        scores=binding.Scores(scale, cap, None if slopes is None else slopes.cuda()))
+    m.sync()
+    sc = scale or 1 / math.sqrt(d)
+    ref, mass = A.attend_documents(f64(q), f64(k), f64(v), cu, prefix, sc, cap,
+                                   None if slopes is None else f64(slopes), rows)
+    big = float(np.nanmax(np.abs(f64(q)[lead:cu[-1]]))) ** 2 * d * sc if dtype == "f32" else 0
+    sel = sorted(rows) if rows is not None else list(range(lead, cu[-1]))
+    _within(out.view(n, nq, d)[sel], ref[sel],
+            _attn_bound(ref[sel], mass[sel], dtype, n, d, big, cap + (n if bias else 0)), "docs")
+    outside = list(range(lead)) + list(range(cu[-1], n))
+    if outside:
+        assert torch.all(out[outside] == 3.0)
+    return out
+
+
+OPTIONS = [dict(), dict(cap=5.0), dict(bias=True), dict(cap=30.0, bias=True, scale=0.2)]
+
+
+@pytest.mark.parametrize("nq,nkv", [(2, 2), (4, 1), (6, 2), (3, 1)])
+@pytest.mark.parametrize("opt", range(4))
+def test_docs_bf16(nq, nkv, opt):
+    _docs_case(nq, nkv, 128, "bf16", [1, 0, 37, 130, 2], **OPTIONS[opt])
+
+
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300])
+def test_docs_bf16_one_document(n):
+    _docs_case(2, 1, 128, "bf16", [n], cap=20.0, bias=True)
+    _docs_case(1, 1, 128, "bf16", [n])
+
+
+@pytest.mark.parametrize("nq,nkv", [(2, 2), (4, 2), (1, 1)])
+def test_docs_bf16_prefix(nq, nkv):
+    # no prefix, all of it, past the document, one past a tile, negative
+    _docs_case(nq, nkv, 128, "bf16", [20, 150, 90, 300, 5], prefix=[0, 150, 1000, 129, -3], bias=True)
+
+
+def test_docs_bf16_long():
+    rows = {0, 1, 127, 128, 700, 1023, 1024, 1999, 2300, 2301, 2399}
+    _docs_case(4, 2, 128, "bf16", [2000, 400], cap=50.0, rows=rows)
+    _docs_case(3, 3, 128, "bf16", [2000, 400], prefix=[900, 130], rows=rows)
+
+
+def test_docs_rows_of_no_document():
+    _docs_case(4, 2, 128, "bf16", [30, 140], lead=3, tail=40, poison=True)
+    _docs_case(2, 2, 64, "f32", [30, 70], lead=3, tail=40, poison=True)
+
+
+def test_docs_large_scores():
+    # scores of some hundreds: the running maximum moves from tile to tile
+    _docs_case(2, 1, 128, "bf16", [400], std=8.0)
+    _docs_case(2, 1, 128, "bf16", [400], std=8.0, cap=400.0)
+    _docs_case(2, 1, 64, "f32", [200], std=4.0)
+
+
+def test_docs_many_documents():
+    lens = torch.randint(0, 4, (200,), generator=_gen(3)).tolist()
+    _docs_case(2, 1, 128, "bf16", lens)
+
+
+@pytest.mark.parametrize("nq,nkv,d", [(4, 2, 64), (2, 2, 40), (2, 1, 128), (1, 1, 256), (3, 1, 8)])
+@pytest.mark.parametrize("opt", range(4))
+def test_docs_fp32(nq, nkv, d, opt):
+    _docs_case(nq, nkv, d, "f32", [1, 70, 0, 130], prefix=[0, 3, 0, 100] if opt & 1 else None, **OPTIONS[opt])
+
+
+def test_docs_matches_plain_prefill():
+    m, shape = _model(4, 2)
+    B, T = 2, 200
+    q, k, v = (_randn((B * T, h, 128), torch.bfloat16, 40 + i).cuda() for i, h in enumerate((4, 2, 2)))
+    a, b = (torch.empty(B * T, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    m.op_attention_prefill(q, k, v, B, T, a)
+    m.op_attention_docs(q, k, v, _i32([0, T, 2 * T]), b)
+    m.sync()
+    ref, mass = A.attend_documents(f64(q), f64(k), f64(v), [0, T, 2 * T], None, 1 / math.sqrt(128))
+    for t in (a, b):
+        _within(t.view(B * T, 4, 128), ref, _attn_bound(ref, mass, "bf16", T, 128, 0, 0), "prefill")
+
+
+def test_docs_bad_bounds_are_flagged():
+    m, shape = _model(2, 2)
+    q, k, v = (_randn((50, 2, 128), torch.bfloat16, 50 + i).cuda() for i in range(3))
+    out = torch.full((50, 256), 3.0, dtype=torch.bfloat16, device="cuda")
+    m.op_attention_docs(q, k, v, _i32([0, 20, 70]), out)  # the second document ends past the rows
+    rc, flags = m.sync_status()
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE
+    ref, mass = A.attend_documents(f64(q), f64(k), f64(v), [0, 20, 50], None, 1 / math.sqrt(128))
+    _within(out.view(50, 2, 128), ref, _attn_bound(ref, mass, "bf16", 50, 128, 0, 0), "cut document")
+
+
+# --------------------------------------------------------------------------- decode
+def _shared_case(nq, nkv, d, dtype, positions, shared, *, page=16, seq=0, cap=0.0, bias=False, scale=0.0,
+                 seed=11, std=1.5, layers=1, layer=0, max_seq=None, poison=True):
+    B = len(positions)
+    top = max(max(positions) + 1, shared, 1)
+    m, shape = _model(nq, nkv, d, dtype, max_batch=B, max_seq=max_seq or top, n_layers=layers)
+    dt = shape.torch_dtype
+    q = _randn((B, nq, d), dt, seed, std)
+    extra = 1 if seq >= B else 0
+    if page:
+        whole = shared // page
+        counts = [whole] + [max(math.ceil(max(p + 1, shared) / page) - whole, 0) for p in positions]
+        t, total = synth.page_table(counts, max(math.ceil(top / page), 1), seed)
+        pt = torch.full((B, t.shape[1]), -1, dtype=torch.int32)
+        for b in range(B):
+            pt[b, :whole] = t[0, :whole]
+            pt[b, whole:whole + counts[b + 1]] = t[b + 1, :counts[b + 1]]
+        size = (layers, max(total, 1), nkv, page, d)
+    else:
+        size = (layers, B + extra, nkv, top, d)
+    k, v = _randn(size, dt, seed + 1, std), _randn(size, dt, seed + 2)
+
+    def rows(t, b):  # (keys, values) as the definition reads them
+        n = positions[b] + 1
+        if page:
+            at = lambda s, j: (layer, int(pt[s, j // page]), slice(None), j % page)
+        else:
+            at = lambda s, j: (layer, s, slice(None), j)
+        return [at(seq if j < shared else b, j) for j in range(n)]
+    if poison:  # slots that no key of any sequence is read from
+        used = set()
+        for b in range(B):
+            used |= {(i[1], i[3]) for i in rows(None, b)}
+        for i in range(size[1]):
+            for j in range(size[3]):
+                if (i, j) not in used:
+                    k[layer, i, :, j] = float("nan")
+                    v[layer, i, :, j] = float("nan") if (i + j) % 2 else float("inf")
+    kv = binding.KVCache(shape, n_pages=size[1], page_size=page, page_table=pt.cuda(), k=k.cuda(), v=v.cuda()) \
+        if page else binding.KVCache(shape, batch=size[1], capacity=top, k=k.cuda(), v=v.cuda())
+    slopes = _slopes(nq) if bias else None
+    out = torch.full((B, nq * d), 3.0, dtype=dt, device="cuda")
+    m.op_attention_decode_shared(q.cuda(), _i32(positions), layer, kv, out, shared_len=shared, shared_seq=seq,
+                                 scores=binding.Scores(scale, cap, None if slopes is None else slopes.cuda()))
+    m.sync()
+    sc = scale or 1 / math.sqrt(d)
+    kf, vf, qf = f64(k), f64(v), f64(q)
+    for b in range(B):
+        where = rows(None, b)
+        n = len(where)
+        K = np.stack([kf[i] for i in where], 1)
+        V = np.stack([vf[i] for i in where], 1)
+        ref, mass = np.empty((nq, d)), np.empty((nq, d))
+        for h in range(nq):
+            g = h // (nq // nkv)
+            ref[h], mass[h] = A.attend_row(qf[b, h], K[g], V[g], positions[b], np.ones(n, bool), sc, cap,
+                                           0.0 if slopes is None else float(slopes[h]))
+        big = float(np.abs(qf).max()) ** 2 * d * sc if dtype == "f32" else 0
+        _within(out[b].view(nq, d), ref, _attn_bound(ref, mass, dtype, n, d, big, cap + (n if bias else 0)),
+                "decode b=%d n=%d" % (b, n))
+
+
+@pytest.mark.parametrize("nq,nkv", [(4, 4), (8, 1), (6, 2), (16, 1), (12, 1)])
+@pytest.mark.parametrize("opt", range(4))
+def test_shared_bf16(nq, nkv, opt):
+    _shared_case(nq, nkv, 128, "bf16", [200, 150, 128, 333, 129], 128, **OPTIONS[opt])
+
+
+@pytest.mark.parametrize("page", [0, 16, 64, 80])
+@pytest.mark.parametrize("shared", [0, 1, 15, 64, 100, 257])
+def test_shared_bf16_ends(page, shared):
+    # the shared part ends inside a page or a tile; single own keys and long ones
+    _shared_case(8, 2, 128, "bf16", [shared, shared + 1, shared + 63, shared + 64, shared + 300, shared + 7], shared,
+                 page=page)
+
+
+def test_shared_bf16_positions_inside_the_prefix():
+    _shared_case(8, 2, 128, "bf16", [0, 10, 63, 64, 199, 200, 400], 200)
+    _shared_case(2, 2, 128, "bf16", [0, 10, 63, 64, 199, 200, 400], 200, page=0, cap=10.0, bias=True)
+
+
+@pytest.mark.parametrize("page,seq", [(0, 2), (0, 4), (16, 3)])
+def test_shared_bf16_other_sequence(page, seq):
+    _shared_case(4, 2, 128, "bf16", [300, 280, 260, 256], 256, page=page, seq=seq)
+
+
+@pytest.mark.parametrize("B,nq,nkv", [(1, 32, 32), (1, 8, 1), (17, 16, 2), (40, 8, 1), (130, 2, 2), (9, 16, 1)])
+def test_shared_bf16_batches(B, nq, nkv):
+    # one row block, several, and the last one ragged
+    _shared_case(nq, nkv, 128, "bf16", [140 + (7 * b) % 50 for b in range(B)], 130)
+
+
+def test_shared_bf16_long_splits():
+    _shared_case(8, 2, 128, "bf16", [4000, 2500], 2048, page=64, cap=30.0)
+    _shared_case(4, 4, 128, "bf16", [5000], 0, page=0, bias=True)
+
+
+def test_shared_second_layer():
+    _shared_case(4, 2, 128, "bf16", [90, 70], 40, layers=3, layer=2)
+
+
+def test_shared_large_scores():
+    _shared_case(4, 2, 128, "bf16", [500, 300], 256, std=8.0)
+
+
+@pytest.mark.parametrize("nq,nkv,d", [(4, 2, 64), (2, 2, 40), (20, 1, 128), (1, 1, 256)])
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("opt", range(4))
+def test_shared_fp32(nq, nkv, d, page, opt):
+    _shared_case(nq, nkv, d, "f32", [0, 70, 99, 130], 50 if opt & 1 else 0, page=page, **OPTIONS[opt])
+
+
+def test_shared_bad_positions_and_pages():
+    m, shape = _model(4, 2, max_batch=4, max_seq=64)
+    q = _randn((4, 4, 128), torch.bfloat16, 60).cuda()
+    k, v = (_randn((1, 8, 2, 16, 128), torch.bfloat16, 61 + i) for i in range(2))
+    pt = _i32([[0, 1, 2, 3], [0, 4, -1, -1], [0, 5, 6, 7], [0, 7, 90, -1]])
+    kv = binding.KVCache(shape, n_pages=8, page_size=16, page_table=pt, k=k.cuda(), v=v.cuda())
+    out = torch.full((4, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    # sequence 1 has no keys, 2 asks past max_seq (all 64 keys attended), 3 has a page outside the pool
+    m.op_attention_decode_shared(q, _i32([40, -1, 64, 40]), 0, kv, out, shared_len=16)
+    rc, flags = m.sync_status()
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE | binding.FLAG_PAGE_RANGE
+    assert torch.all(out[1] == 0)
+    for b, n in ((0, 41), (2, 64)):
+        ids = pt[b].cpu().numpy()
+        K = np.concatenate([f64(k)[0, ids[i]] for i in range(4)], 1)[:, :n]
+        V = np.concatenate([f64(v)[0, ids[i]] for i in range(4)], 1)[:, :n]
+        for h in range(4):
+            ref, mass = A.attend_row(f64(q)[b, h], K[h // 2], V[h // 2], n - 1, np.ones(n, bool), 1 / math.sqrt(128))
+            _within(out[b].view(4, 128)[h], ref, _attn_bound(ref, mass, "bf16", n, 128, 0, 0), "beside bad ones")
+    m.op_attention_decode_shared(q, _i32([40, 20, 63, 30]), 0, kv, out, shared_len=16)
+    m.sync()  # the context is usable again
+
+
+# --------------------------------------------------------------------------- together
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_serving_run(dtype):
+    """A system prompt and three user prompts are prefilled, then all sequences
+    decode over the shared prompt: append -> documents -> append -> decode."""
+    nq, nkv, d, page, P = 4, 2, 128, 16, 70
+    m, shape = _model(nq, nkv, d, dtype, max_batch=4, max_seq=256)
+    dt = shape.torch_dtype
+    table = binding.rope_table(256, 96, kind=binding.ROPE_LINEAR, factor=2.0)
+    rope = binding.Rope(table, binding.ROPE_HALF)
+    qg, kg = ((1 + 0.1 * torch.randn(d, generator=_gen(i))).to(dt) for i in (1, 2))
+    slopes = _slopes(nq)
+    scores = binding.Scores(cap=20.0, slopes=slopes.cuda())
+    own = [5, 40, 17]  # tokens after the shared prompt
+    # table rows 0-2: users (own copy of the partly filled page); row 3: the prompt itself
+    pt = torch.full((4, 16), -1, dtype=torch.int32)
+    pt[3, :5] = torch.tensor([9, 2, 30, 7, 11])
+    for b in range(3):
+        pt[b, :4] = pt[3, :4]
+        pt[b, 4:9] = torch.tensor([12, 13, 14, 15, 16]) + 5 * b
+    kv = binding.KVCache(shape, n_pages=40, page_size=page, page_table=pt.cuda())
+    tf = f64(table)
+
+    def ref_rows(x, pos):
+        x = f64(x).reshape(len(pos), nq + 2 * nkv, d)
+        q, k = A.head_norm(x[:, :nq], f64(qg), 1e-5), A.head_norm(x[:, nq:nq + nkv], f64(kg), 1e-5)
+        q = np.stack([A.rotate(q[i], tf[p], True) for i, p in enumerate(pos)])
+        k = np.stack([A.rotate(k[i], tf[p], True) for i, p in enumerate(pos)])
+        return q, k, x[:, nq + nkv:]
+
+    # the prompt into sequence 3, attended as one document with a two-way part
+    x = _randn((P, shape.qkv_rows), torch.float32, 70)
+    q, o = (torch.empty(P, nq * d, dtype=dt, device="cuda") for _ in range(2))
+    k, v = (torch.empty(P, nkv * d, dtype=dt, device="cuda") for _ in range(2))
+    kw = dict(rope=rope, q_gain=qg.cuda(), k_gain=kg.cuda())
+    m.op_rope_norm_append(x.cuda(), _i32([0, 0, 0, 0]), 0, kv, q, cu_rows=_i32([0, 0, 0, 0, P]), k_out=k, v_out=v, **kw)
+    m.op_attention_docs(q, k, v, _i32([0, P]), o, prefix=_i32([20]), scores=scores)
+    m.sync()
+    ref, mass = A.attend_documents(f64(q).reshape(P, nq, d), f64(k).reshape(P, nkv, d), f64(v).reshape(P, nkv, d),
+                                   [0, P], [20], 1 / math.sqrt(d), 20.0, f64(slopes))
+    _within(o.view(P, nq, d), ref, _attn_bound(ref, mass, dtype, P, d, 400.0, 20 + P), "prompt")
+    rq, rk, rv = ref_rows(x, range(P))
+    tol = 2.0 ** -7 if dtype == "bf16" else 2.0 ** -20
+    for got, want in ((q, rq), (k, rk), (v, rv)):
+        _within(got.view(P, -1, d), want, tol * np.abs(want) + 2.0 ** -16 * 6, "prompt rows")
+    keys = [[k.view(P, nkv, d)[j] for j in range(P)] for _ in range(3)]
+    vals = [[v.view(P, nkv, d)[j] for j in range(P)] for _ in range(3)]
+    # the users' own tokens join one batch of packed rows, then two decode steps
+    for step, lens in enumerate((own, [1] * 3, [1] * 3)):
+        n = sum(lens)
+        x = _randn((n, shape.qkv_rows), torch.float32, 80 + step)
+        start = [len(keys[b]) for b in range(3)]
+        cu = np.concatenate(([0], np.cumsum(lens))).tolist()
+        q = torch.empty(n, nq * d, dtype=dt, device="cuda")
+        k, v = (torch.empty(n, nkv * d, dtype=dt, device="cuda") for _ in range(2))
+        m.op_rope_norm_append(x.cuda(), _i32(start), 0, kv, q, cu_rows=_i32(cu) if step == 0 else None, k_out=k,
+                              v_out=v, **kw)
+        m.sync()
+        for b in range(3):
+            for r in range(cu[b], cu[b + 1]):
+                keys[b].append(k.view(n, nkv, d)[r])
+                vals[b].append(v.view(n, nkv, d)[r])
+        last = [c - 1 for c in cu[1:]]
+        qd = torch.cat((q[last], q[:1] * 0)).contiguous()  # sequence 3 is only a prefix: no query
+        pos = [len(keys[b]) - 1 for b in range(3)] + [-1]
+        o = torch.full((4, nq * d), 3.0, dtype=dt, device="cuda")
+        m.op_attention_decode_shared(qd, _i32(pos), 0, kv, o, shared_len=P, shared_seq=3, scores=scores)
+        rc, flags = m.sync_status()
+        assert rc == 5 and flags == binding.FLAG_POS_RANGE  # the row without keys
+        assert torch.all(o[3] == 0)
+        for b in range(3):
+            K, V = f64(torch.stack(keys[b])), f64(torch.stack(vals[b]))
+            for h in range(nq):
+                ref, mass = A.attend_row(f64(qd)[b].reshape(nq, d)[h], K[:, h // 2], V[:, h // 2], pos[b],
+                                         np.ones(len(K), bool), 1 / math.sqrt(d), 20.0, float(slopes[h]))
+                _within(o[b].view(nq, d)[h], ref, _attn_bound(ref, mass, dtype, len(K), d, 400.0, 20 + len(K)),
+                        "step %d user %d" % (step, b))
+
+
+def test_captured_replays_follow_their_buffers():
+    # append and decode captured on a stream, replayed with new inputs and positions
+    m, shape = _model(8, 2, max_batch=3, max_seq=512)
+    s = torch.cuda.Stream()
+    pos = _i32([300, 310, 305])
+    x = torch.empty(3, shape.qkv_rows, device="cuda")
+    k, v = (_randn((1, 3, 2, 512, 128), torch.bfloat16, 90 + i).cuda() for i in range(2))
+    kv = binding.KVCache(shape, batch=3, capacity=512, k=k, v=v)
+    q, o = (torch.empty(3, 1024, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rope = binding.Rope(None, binding.ROPE_HALF, 128)
+    sc = binding.Scores(cap=30.0)
+
+    def step():
+        m.op_rope_norm_append(x, pos, 0, kv, q, rope=rope)
+        m.op_attention_decode_shared(q, pos, 0, kv, o, shared_len=200, scores=sc)
+    torch.cuda.synchronize()
+    m.set_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for i in range(3):
+        x.copy_(_randn((3, shape.qkv_rows), torch.float32, 95 + i))
+        before = (k.clone(), v.clone())
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        captured = o.clone()
+        k.copy_(before[0])
+        v.copy_(before[1])
+        o.fill_(3.0)
+        torch.cuda.synchronize()
+        step()
+        m.sync()
+        assert torch.equal(o, captured)
+        pos += 1
+    m.set_stream(torch.cuda.default_stream())
+
+
+# --------------------------------------------------------------------------- refusals
+def test_refusals():
+    m, shape = _model(4, 2, max_batch=2, max_seq=64)
+    m32, s32 = _model(2, 1, 64, "f32", max_batch=2, max_seq=64)
+    d, dt = 128, torch.bfloat16
+    x = torch.zeros(2, shape.qkv_rows, device="cuda")
+    pos = _i32([0, 1])
+    kv = binding.KVCache(shape, batch=2, capacity=64)
+    q = torch.zeros(2, 4 * d, dtype=dt, device="cuda")
+    k = torch.zeros(2, 2 * d, dtype=dt, device="cuda")
+    table = binding.rope_table(64, 64)
+
+    def refused(code, fn, *a, **kw):
+        with pytest.raises(binding.LlamaError) as e:
+            fn(*a, **kw)
+        assert e.value.rc == code
+    ap = m.op_rope_norm_append
+    refused(1, ap, x, pos, 1, kv, q)                                          # layer
+    refused(1, ap, x, pos, 0, kv, q, q_gain=q[0, :d].contiguous(), eps=0.0)   # eps
+    refused(2, ap, x, pos, 0, kv, q, rope=binding.Rope(None, 0, 60))          # not a multiple of 8
+    refused(1, ap, x, pos, 0, kv, q, rope=binding.Rope(None, 0, 64))          # the context turns whole heads
+    refused(1, ap, x, pos, 0, kv, q, rope=binding.Rope(table, 2))             # layout
+    refused(1, ap, x, pos, 0, kv, q, rope=binding.Rope(binding.rope_table(8, 136)))
+    refused(1, ap, x[:1], pos, 0, kv, q[:1])                                  # one row per sequence
+    with pytest.raises(ValueError):
+        ap(x.half(), pos, 0, kv, q)
+    with pytest.raises(ValueError):
+        ap(x, pos.long(), 0, kv, q)
+    with pytest.raises(ValueError):
+        ap(x, pos, 0, kv, q[:1])
+    bad = torch.zeros(2, shape.qkv_rows + 2, device="cuda")[:, :shape.qkv_rows]
+    refused(1, ap, bad, pos, 0, kv, q)                                        # rows not 16-byte aligned
+    docs = m.op_attention_docs
+    cu = _i32([0, 2])
+    for sc in (binding.Scores(cap=-1.0), binding.Scores(scale=float("nan")), binding.Scores(cap=float("inf"))):
+        refused(1, docs, q, k, k, cu, q.clone(), scores=sc)
+    with pytest.raises(ValueError):
+        docs(q, q, k, cu, q.clone())
+    with pytest.raises(ValueError):
+        docs(q, k, k, cu, q.clone(), scores=binding.Scores(slopes=torch.ones(3, device="cuda")))
+    with pytest.raises(ValueError):
+        docs(q, k, k, cu, q.t().contiguous().t())
+    dec = m.op_attention_decode_shared
+    refused(3, dec, q, pos, 0, kv, q.clone(), shared_len=65)                  # past the cache
+    refused(1, dec, q, pos, 0, kv, q.clone(), shared_len=8, shared_seq=2)
+    refused(1, dec, q, pos, 0, kv, q.clone(), shared_len=-1)
+    refused(2, dec, q, pos, 0, binding.KVCache(shape, batch=2, capacity=64, e4m3=(1.0, 1.0)), q.clone())
+    three = torch.zeros(3, 4 * d, dtype=dt, device="cuda")
+    refused(3, dec, three, _i32([0, 0, 0]), 0, binding.KVCache(shape, batch=3, capacity=64), three.clone())
+    x32 = torch.zeros(2, s32.qkv_rows, device="cuda")
+    with pytest.raises(ValueError):
+        m32.op_rope_norm_append(x32.bfloat16(), pos, 0, binding.KVCache(s32, batch=2, capacity=64),
+                                torch.zeros(2, 128, device="cuda"))
+    m.sync()
+    m32.sync()
