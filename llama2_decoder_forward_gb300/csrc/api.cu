@@ -50,6 +50,7 @@ bool load_encode() {
     if (g_prep_err == cudaSuccess) g_prep_err = attn_prepare();
     if (g_prep_err == cudaSuccess) g_prep_err = sample_prepare();
     if (g_prep_err == cudaSuccess) g_prep_err = attn_simt_prepare();
+    if (g_prep_err == cudaSuccess) g_prep_err = attn_forms_prepare();
   });
   return g_encode != nullptr && g_prep_err == cudaSuccess;
 }
@@ -1348,9 +1349,18 @@ int llama_op_attention_docs(llama_ctx* c, const void* q, const void* k, const vo
   a.cu_rows = cu_rows;
   a.prefix_len = prefix_len;
   a.status = c->status;
+  if (cf.dtype == LLAMA_BF16) {
+    trim_maps(c);
+    const uint64_t d = cf.head_dim, rows = n_rows;
+    a.map_q = map3d(c, q, d, cf.n_q_heads, rows, 1, 128);
+    a.map_k = map3d(c, k, d, cf.n_kv_heads, rows, 1, 128);
+    a.map_v = map3d(c, v, d, cf.n_kv_heads, rows, 1, 128);
+    if (!a.map_q || !a.map_k || !a.map_v) return LLAMA_ERR_CUDA;
+  }
   Prof pf(c, LLAMA_KERNEL_ATTN_PREFILL);
   c->launches++;
-  return cuda_rc(launch_docs_simt(cf.dtype, a, c->stream));
+  return cuda_rc(cf.dtype == LLAMA_BF16 ? launch_docs_tc(a, c->stream)
+                                        : launch_docs_simt(cf.dtype, a, c->stream));
 }
 
 int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t* positions,

@@ -261,6 +261,8 @@ struct DocsArgs {
   const int32_t* prefix_len;   // [n_docs] or null
   ScoreArgs sc;
   uint32_t* status;
+  // tensor-core form: 3D {d, heads, rows}, box {64, 1, 128}, SW128
+  const CUtensorMap *map_q = nullptr, *map_k = nullptr, *map_v = nullptr;
 };
 struct SharedArgs {
   const void* q;               // [B, n_q, d]
@@ -275,6 +277,9 @@ struct SharedArgs {
   ScoreArgs sc;
   uint32_t* status;
 };
+// bf16, head_dim 128 on tcgen05 (k_attn_forms_tc.cu)
+cudaError_t attn_forms_prepare();
+cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st);
 // CUDA-core forms for any head_dim (k_attn_simt.cu)
 cudaError_t attn_simt_prepare();
 cudaError_t launch_docs_simt(int dtype, const DocsArgs& a, cudaStream_t st);

@@ -1,0 +1,604 @@
+// Attention with capped or biased scores on the 5th-generation tensor cores
+// (tcgen05), head_dim 128, bf16: packed documents (causal, with a two-way
+// prefix), and the shared prefix of a decode batch.
+//
+//   x = scale q.k;  s = (cap tanh(x / cap) or x) - slope |i - j|;  p = softmax(s);  o = sum p v
+//
+// One pass over the keys with the running maximum and sum of each row
+// (FlashAttention): the scores never leave the SM. One CTA per SM works on two
+// tiles of 128 query rows (MMA M, one tensor-memory lane per row) against key
+// tiles of 128:
+//   warps 0-3, 4-7  softmax of row tile 0 and 1, one thread per row;
+//   warp 8, 9       TMA producers of Q + K and of V (rings of 32 KB tiles);
+//   warp 10, 11     MMA issuers of row tile 0 and 1.
+// While one tile's softmax runs on the CUDA cores, the tensor cores work for
+// the other tile. An issuer's order is O += P_j V_j, then S_{j+1} = Q K^T_{j+1}:
+// tcgen05 operations of one thread execute in order, so P_j (bf16, written
+// over the scores it came from) is read before S_{j+1} replaces it, and the
+// arrival of S_{j+1} also says that O += P_j V_j is done. Tensor memory: per row
+// tile 128 columns of S / P and 128 of O, all 512.
+// The two row tiles are
+//   documents, n_q / n_kv even : two query heads of one K/V head, same rows;
+//   documents, else            : rows q0 .. q0+127 and q0+128 .. q0+255;
+//   prefix, over 128 rows      : two blocks of (sequence, head of the group) rows;
+//   prefix, up to 128 rows     : the same rows; tile t takes every second key tile
+//                                (two key splits; each K/V tile has one reader).
+// so K and V are loaded once for both. Every mask here is "keys below a row's
+// limit": max(position + 1, prefix) for documents, the sequence's keys for the
+// prefix. O is rescaled lazily, when a row's maximum grows by more than 2^8.
+// P is rounded once to bf16 (V's type, which the MMA shares); the sum that
+// normalises it is taken in fp32 before that.
+#include <algorithm>
+
+#include "attn_score.cuh"
+#include "internal.h"
+
+namespace llgb {
+
+namespace {
+
+constexpr int TM = 128;                     // rows of a tile
+constexpr int TN = 128;                     // keys of a tile
+constexpr uint32_t HALF = 128 * 128;        // 128 rows x 64 dims bf16, 128-byte swizzled: 16 KB
+constexpr uint32_t TILE = 2 * HALF;         // 128 rows x 128 dims
+constexpr int SLOTS = 7;                    // Q 0, (Q 1), then the K ring and the V ring
+constexpr uint32_t OFF_BAR = SLOTS * TILE;
+constexpr size_t FORMS_SMEM = OFF_BAR + 256;
+constexpr int FORMS_THREADS = 384;
+constexpr int MAXK = 4, MAXV = 2;           // ring sizes at most
+constexpr uint32_t O_COL = 256;             // S tiles at columns 0 and 128, O tiles at 256 and 384
+constexpr float kLazy = 8.f;
+static_assert(FORMS_SMEM <= 232448, "227 KB of shared memory per CTA");
+
+struct FormsParams {
+  int n_q, n_kv, G;
+  float scale, cap;
+  const float* slopes;
+  uint32_t* status;
+  // documents
+  bf16* out;
+  const int32_t *cu_rows, *prefix_len;
+  int n_rows, n_docs, head_pairs;
+  // prefix of a decode batch
+  const int32_t *positions, *page_table;
+  int B, rows_seq;                          // sequences of a row tile (128 / G)
+  int alternate;                            // both row tiles hold the same rows
+  int layer, page_size, capacity, batch_cap, n_pages, max_pages, box_rows;
+  int key_limit, shared_len, shared_seq, tiles_per_split;
+  float *part_o, *part_ml;                  // [B n_q][splits][128], [B n_q][splits][2] (max log2, sum)
+  int splits;                               // partials of a row written here start at 0
+};
+
+// Bounded wait without a call, for code whose registers setmaxnreg resizes:
+// at most 2^20 tries of up to 2 us.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < (1 << 20); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
+        : "memory");
+    if (ok) return true;
+  }
+  flag(status, LLAMA_FLAG_WAIT_TIMEOUT);
+  return false;
+}
+
+// Ring position: slot and phase parity of the n-th use.
+struct Ring {
+  int n, slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int size) : n(size) {}
+  __device__ __forceinline__ void step(int k = 1) {
+    slot += k;
+    if (slot >= n) {
+      slot -= n;
+      phase ^= 1;
+    }
+  }
+};
+
+// Cache row of the keys starting at k0 of sequence b, K/V head g; a page
+// outside the pool is flagged and mapped to rows that TMA fills with zeros.
+__device__ __forceinline__ int forms_kv_row(const FormsParams& p, int b, int g, int k0) {
+  if (p.page_size == 0) return (b * p.n_kv + g) * p.capacity + k0;
+  const int pi = k0 / p.page_size;
+  const int page = pi < p.max_pages ? p.page_table[(size_t)b * p.max_pages + pi] : -1;
+  if (page < 0 || page >= p.n_pages) {
+    flag(p.status, LLAMA_FLAG_PAGE_RANGE);
+    return -64;
+  }
+  return (page * p.n_kv + g) * p.page_size + (k0 - pi * p.page_size);
+}
+
+template <bool DOCS>
+__device__ __forceinline__ void load_tile(const FormsParams& p, const CUtensorMap* big,
+                                          const CUtensorMap* m16, uint8_t* dst, uint64_t* bar, int g,
+                                          int rowbase, int k0, int nvalid) {
+  if (DOCS) {
+    mbar_arrive_expect_tx(bar, TILE);
+    tma_load_3d(dst, big, bar, 0, g, rowbase + k0);
+    tma_load_3d(dst + HALF, big, bar, 64, g, rowbase + k0);
+    return;
+  }
+  uint32_t bytes = 0;
+  for (int rb = 0; rb < 2; ++rb) {
+    const int nv = min(64, nvalid - rb * 64);
+    if (nv > 0) bytes += (p.box_rows == 64 && nv == 64) ? 2 * 64 * 128 : 2 * ((nv + 15) / 16) * 16 * 128;
+  }
+  mbar_arrive_expect_tx(bar, bytes);
+  for (int rb = 0; rb < 2; ++rb) {
+    const int nv = min(64, nvalid - rb * 64);
+    if (nv <= 0) break;
+    uint8_t* d = dst + rb * 64 * 128;
+    if (p.box_rows == 64 && nv == 64) {
+      const int row = forms_kv_row(p, p.shared_seq, g, k0 + rb * 64);
+      tma_load_3d(d, big, bar, 0, row, p.layer);
+      tma_load_3d(d + HALF, big, bar, 64, row, p.layer);
+    } else {
+      for (int j = 0; j < (nv + 15) / 16; ++j) {
+        const int row = forms_kv_row(p, p.shared_seq, g, k0 + rb * 64 + 16 * j);
+        tma_load_3d(d + j * 16 * 128, m16, bar, 0, row, p.layer);
+        tma_load_3d(d + HALF + j * 16 * 128, m16, bar, 64, row, p.layer);
+      }
+    }
+  }
+}
+
+// 1 / (1 + 2^z): one exponential and one reciprocal on the special-function unit
+__device__ __forceinline__ float inv_1p_ex2(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(z)));
+  return r;
+}
+
+template <bool DOCS, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(FORMS_THREADS, 1)
+    attn_forms_kernel(const __grid_constant__ CUtensorMap mapQ,
+                      const __grid_constant__ CUtensorMap mapK,
+                      const __grid_constant__ CUtensorMap mapV,
+                      const __grid_constant__ CUtensorMap mapK16,
+                      const __grid_constant__ CUtensorMap mapV16, FormsParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* kfull = qfull + 1;
+  uint64_t* kempty = kfull + MAXK;
+  uint64_t* vfull = kempty + MAXK;
+  uint64_t* vempty = vfull + MAXV;
+  uint64_t* vtail = vempty + MAXV;  // the ragged last V tile has its absent rows zeroed
+  uint64_t* sfull = vtail + 1;      // [2] S_j of row tile t is in tensor memory
+  uint64_t* pready = sfull + 2;     // [2] P_j is, and O is rescaled
+  uint64_t* fin = pready + 2;       // [2] every MMA of the tile's issuer is done
+  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(fin + 2);  // tensor memory, abort
+  static_assert((1 + 2 * MAXK + 2 * MAXV + 1 + 6) * 8 + 8 <= 256, "barrier block");
+  grid_dep_wait();
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((smem_u32(smem) & 1023u) != 0 ||  // the swizzled tiles need 1024-byte alignment
+      !bc_smem(smem, FORMS_SMEM, 1024, threadIdx.x == 0 ? p.status : nullptr)) {
+    if (threadIdx.x == 0) flag(p.status, LLAMA_FLAG_INDEX);
+    return;
+  }
+  // ---- what this CTA computes
+  int g, b = 0, lo = 0, n = 0, q0 = 0, pre = 0;   // documents: document b, its rows [lo, lo + n)
+  int t0 = 0, n_tiles;                            // first key tile and how many
+  int kmax;                                       // keys below this exist for some row
+  int nt0, nt1;                                   // key tiles that row tile 0 / 1 visits
+  int split = 0, seq0 = 0;
+  if (DOCS) {
+    const int per = p.head_pairs ? p.n_q / 2 : p.n_q;
+    const int hx = blockIdx.x % per;
+    int tile;
+    if (!find_tile(p.cu_rows, p.n_docs, p.n_rows, p.head_pairs ? TM : 2 * TM, blockIdx.x / per,
+                   p.status, b, tile, lo, n))
+      return;
+    q0 = tile * (p.head_pairs ? TM : 2 * TM);
+    g = hx;  // query head (pair) until the K/V head is known
+    pre = p.prefix_len ? min(max(p.prefix_len[b], 0), n) : 0;
+    const int last0 = max(min(q0 + TM, n), pre);
+    const int last1 = p.head_pairs ? last0 : q0 + TM < n ? max(min(q0 + 2 * TM, n), pre) : 0;
+    nt0 = (last0 + TN - 1) / TN;
+    nt1 = (last1 + TN - 1) / TN;
+    kmax = max(last0, last1);
+    n_tiles = max(nt0, nt1);
+  } else {
+    split = blockIdx.x;
+    g = blockIdx.z;
+    seq0 = blockIdx.y * p.rows_seq * (p.alternate ? 1 : 2);
+    t0 = split * p.tiles_per_split;
+    const int all = (p.shared_len + TN - 1) / TN;
+    n_tiles = min(p.tiles_per_split, all - t0);
+    if (n_tiles <= 0) return;
+    kmax = p.shared_len;
+    if (p.alternate) {
+      nt0 = (n_tiles + 1) / 2;
+      nt1 = n_tiles / 2;
+    } else {
+      nt0 = n_tiles;
+      nt1 = seq0 + p.rows_seq < p.B ? n_tiles : 0;
+    }
+  }
+  const bool alt = !DOCS && p.alternate;
+  const int KR = alt ? 4 : 3, VR = 2;  // even rings when each slot has one reader
+  const int q_tiles = alt || nt1 == 0 ? 1 : 2;
+  uint8_t* kslots = smem + (alt ? 1 : 2) * TILE;
+  uint8_t* vslots = kslots + KR * TILE;
+  const int h0 = DOCS ? (p.head_pairs ? 2 * g : g) : 0;  // documents: head of row tile 0
+  if (DOCS) g = h0 / p.G;
+
+  if (threadIdx.x == 0) {
+    const uint32_t readers = alt ? 1 : 2;
+    mbar_init(qfull, 1);
+    for (int s = 0; s < MAXK; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], readers);
+    }
+    for (int s = 0; s < MAXV; ++s) {
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], readers);
+    }
+    mbar_init(vtail, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sfull[t], 1);
+      mbar_init(&pready[t], 4);
+      mbar_init(&fin[t], 1);
+    }
+    ctl[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 10) tmem_alloc(const_cast<uint32_t*>(ctl), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl[0];
+  const int last_rows = kmax - (t0 + n_tiles - 1) * TN;  // keys of the last tile; over 128: all
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 8) {  // ------------------------------------------- Q and K producer
+      if (lane == 0) {
+        tma_prefetch_desc(&mapQ);
+        tma_prefetch_desc(&mapK);
+        const uint32_t qbytes = DOCS ? TILE : (uint32_t)(p.rows_seq * p.G) * 256;
+        mbar_arrive_expect_tx(qfull, q_tiles * qbytes);
+        for (int t = 0; t < q_tiles; ++t)
+          for (int half = 0; half < 2; ++half) {
+            uint8_t* d = smem + t * TILE + half * HALF;
+            if (DOCS)
+              tma_load_3d(d, &mapQ, qfull, 64 * half, p.head_pairs ? h0 + t : h0,
+                          lo + q0 + (p.head_pairs ? 0 : t * TM));
+            else
+              tma_load_3d(d, &mapQ, qfull, 64 * half, g * p.G, seq0 + t * p.rows_seq);
+          }
+        Ring r(KR);
+        int issued = 0;
+        for (int j = 0; j < n_tiles; ++j, r.step()) {
+          if (ctl[1] || !wait_bar(&kempty[r.slot], r.phase ^ 1, p.status)) {
+            ctl[1] = 1;
+            break;
+          }
+          load_tile<DOCS>(p, &mapK, &mapK16, kslots + r.slot * TILE, &kfull[r.slot], g, lo,
+                          (t0 + j) * TN, min(TN, kmax - (t0 + j) * TN));
+          ++issued;
+        }
+        wait_bar(qfull, 0, p.status);  // no copy in flight when the CTA exits
+        for (int j = max(0, issued - KR); j < issued; ++j)
+          wait_bar(&kfull[j % KR], (j / KR) & 1, p.status);
+      }
+    } else if (warp == 9) {  // ------------------------------------ V producer
+      int issued = 0;
+      if (lane == 0) {
+        tma_prefetch_desc(&mapV);
+        Ring r(VR);
+        for (int j = 0; j < n_tiles; ++j, r.step()) {
+          if (ctl[1] || !wait_bar(&vempty[r.slot], r.phase ^ 1, p.status)) {
+            ctl[1] = 1;
+            break;
+          }
+          load_tile<DOCS>(p, &mapV, &mapV16, vslots + r.slot * TILE, &vfull[r.slot], g, lo,
+                          (t0 + j) * TN, min(TN, kmax - (t0 + j) * TN));
+          ++issued;
+        }
+        for (int j = max(0, issued - VR); j < issued; ++j)
+          wait_bar(&vfull[j % VR], (j / VR) & 1, p.status);
+      }
+      issued = __shfl_sync(0xffffffffu, issued, 0);
+      if (issued == n_tiles && last_rows < TN) {
+        // V rows past the last key may hold anything, and 0 * NaN is not 0
+        uint8_t* vt = vslots + ((n_tiles - 1) % VR) * TILE;
+        const int nz = (TN - last_rows) * 16;
+        for (int i = lane; i < nz; i += 32) {
+          const int row = last_rows + (i >> 4), half = (i >> 3) & 1, chunk = i & 7;
+          *reinterpret_cast<uint4*>(vt + half * HALF + row * 128 + chunk * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();  // the MMA reads V through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vtail);
+      }
+    } else {  // ------------------------------------------------------ MMA issuers
+      const int t = warp - 10, mine = t ? nt1 : nt0;
+      if (lane == 0) {
+        const uint32_t id_s = idesc_bf16_f32(TM, TN);
+        const uint32_t id_o = idesc_bf16_f32(TM, 128) | (1u << 16);  // B (V) MN-major
+        const uint64_t qd = smem_desc_sw128(smem_u32(smem + (q_tiles == 2 ? t : 0) * TILE));
+        const uint64_t kd0 = smem_desc_sw128(smem_u32(kslots));
+        const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(vslots), HALF);
+        const uint32_t sc = tmem + (uint32_t)t * TN, oc = tmem + O_COL + (uint32_t)t * 128;
+        Ring kr(KR), vr(VR);
+        if (alt) {
+          kr.step(t);
+          vr.step(t);
+        }
+        const int stride = alt ? 2 : 1;
+        const int loops = alt ? mine : n_tiles;  // else: every slot is released here too
+        bool ok = wait_bar(qfull, 0, p.status);
+        // S_j, or just the release of K_j
+        auto score = [&](int j) {
+          if (ctl[1] || !wait_bar(&kfull[kr.slot], kr.phase, p.status)) return false;
+          if (j < mine) {
+            tc_fence_after();
+            const uint64_t kd = kd0 + (uint64_t)(kr.slot * (TILE >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)  // 16 dims per MMA: 32 bytes of Q and K rows
+              tc_mma_f16(sc, qd + ((kk >> 2) * HALF + (kk & 3) * 32) / 16,
+                         kd + ((kk >> 2) * HALF + (kk & 3) * 32) / 16, id_s, kk > 0 ? 1u : 0u);
+            tc_commit(&sfull[t]);
+            tc_commit(&kempty[kr.slot]);
+          } else {
+            mbar_arrive(&kempty[kr.slot]);
+          }
+          kr.step(stride);
+          return true;
+        };
+        ok = ok && (loops == 0 || score(0));
+        for (int j = 0; ok && j < loops; ++j) {
+          if (ctl[1] || (j < mine && !wait_bar(&pready[t], j & 1, p.status)) ||
+              !wait_bar(&vfull[vr.slot], vr.phase, p.status)) {
+            ok = false;
+            break;
+          }
+          if (j < mine) {
+            const int tile = alt ? 2 * j + t : j;
+            if (tile == n_tiles - 1 && last_rows < TN && !wait_bar(vtail, 0, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t vd = vd0 + (uint64_t)(vr.slot * (TILE >> 4));
+#pragma unroll
+            for (int kk = 0; kk < TN / 16; ++kk)  // 16 keys per MMA: 8 P columns, two 8-key V groups
+              tc_mma_f16_ts(oc, sc + 8u * kk, vd + kk * (2048 / 16), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(&vempty[vr.slot]);
+          } else {
+            mbar_arrive(&vempty[vr.slot]);
+          }
+          vr.step(stride);
+          if (j + 1 < loops && !score(j + 1)) {
+            ok = false;
+            break;
+          }
+        }
+        if (!ok) ctl[1] = 1;
+        tc_commit(&fin[t]);
+        wait_bar(&fin[t], 0, p.status);  // retired before the tensor memory is freed
+      }
+    }
+  } else {  // ----------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int t = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t sc = tl + (uint32_t)t * TN, oc = tl + O_COL + (uint32_t)t * 128;
+    // this row: its position, its visible keys, where it goes
+    bool row_ok;
+    int pos, lim, head;
+    size_t row;  // documents: packed row; prefix: sequence
+    if (DOCS) {
+      const int i = q0 + (p.head_pairs ? 0 : t * TM) + r;
+      row_ok = i < n;
+      pos = i;
+      lim = min(max(i + 1, pre), n);
+      head = p.head_pairs ? h0 + t : h0;
+      row = (size_t)lo + i;
+    } else {
+      const int s = seq0 + (p.alternate ? 0 : t * p.rows_seq) + r / p.G;
+      row_ok = r < p.rows_seq * p.G && s < p.B;
+      pos = row_ok ? p.positions[s] : 0;
+      lim = row_ok ? min(min(max(pos + 1, 0), p.key_limit), p.shared_len) : 0;
+      head = g * p.G + r % p.G;
+      row = s;
+    }
+    constexpr float kLog2e = 1.4426950408889634f;
+    // BIAS or CAP: sv in log2 units; else raw scores (the factor c is positive)
+    const float c = p.scale * kLog2e;
+    const float zc = CAP ? 2.f * c / p.cap : 0.f, cl = p.cap * kLog2e;
+    const float sl = BIAS && row_ok ? p.slopes[head] * kLog2e : 0.f;
+    const float ce = (CAP || BIAS) ? 1.f : c;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    const int count = t ? nt1 : nt0;
+    for (int j = 0; j < count; ++j) {
+      if (!__all_sync(0xffffffffu, !ctl[1] && wait_bar(&sfull[t], j & 1, p.status))) {
+        ok = false;
+        ctl[1] = 1;
+        break;
+      }
+      tc_fence_after();
+      const int k0 = (t0 + (alt ? 2 * j + t : j)) * TN;
+      float sv[TN];
+#pragma unroll
+      for (int q = 0; q < TN; q += 32) tmem_ld32(sc + q, reinterpret_cast<uint32_t*>(sv + q));
+      tmem_ld_wait();
+      if (CAP) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i) sv[i] = fmaf(-2.f * cl, inv_1p_ex2(sv[i] * zc), cl);
+      }
+      if (BIAS) {
+        const float base = sl * (float)(k0 - pos);  // -slope (pos - key) at the tile's first key
+        // keys ahead of the row are visible only through a prefix
+        const bool ahead = DOCS && __any_sync(0xffffffffu, pre > pos && k0 + TN - 1 > pos);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          float bias = fmaf(sl, (float)i, base);
+          if (ahead && k0 + i > pos) bias = -bias;
+          sv[i] = CAP ? sv[i] + bias : fmaf(sv[i], c, bias);
+        }
+      }
+      if (!__all_sync(0xffffffffu, lim >= k0 + TN)) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+          if (k0 + i >= lim) sv[i] = -INFINITY;
+      }
+      float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+      for (int i = 4; i < TN; ++i) mx[i & 3] = fmaxf(mx[i & 3], sv[i]);
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ce;
+      const float m_new = fmaxf(m, mt);
+      const bool need = m_new > m + kLazy;  // also the first finite maximum
+      if (__any_sync(0xffffffffu, need && j > 0)) {
+        const float f = !need ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
+#pragma unroll 1
+        for (int q = 0; q < 128; q += 32) {
+          uint32_t u[32];
+          tmem_ld32(oc + q, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
+          tmem_st32(oc + q, u);
+        }
+        l *= f;
+      }
+      if (need) m = m_new;
+      const float mu = m == -INFINITY ? 0.f : m;
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < TN; q += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float e0 = ex2((CAP || BIAS) ? sv[q + i] - mu : fmaf(sv[q + i], c, -mu));
+          const float e1 = ex2((CAP || BIAS) ? sv[q + i + 1] - mu : fmaf(sv[q + i + 1], c, -mu));
+          ls[i & 2] += e0;
+          ls[(i & 2) + 1] += e1;
+          w[i / 2] = pack_bf16(e0, e1);
+        }
+        tmem_st16(sc + q / 2, w);
+      }
+      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pready[t]);
+    }
+    // ---- epilogue
+    const bool done = __all_sync(0xffffffffu, ok && (count == 0 || wait_bar(&fin[t], 0, p.status)));
+    if (done && !ctl[1]) {
+      tc_fence_after();
+      if (DOCS) {
+        if (count > 0) {
+          const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+          bf16* dst = p.out + (row * p.n_q + head) * 128;
+#pragma unroll 1
+          for (int q = 0; q < 128; q += 32) {
+            float u[32];
+            tmem_ld32(oc + q, reinterpret_cast<uint32_t*>(u));
+            tmem_ld_wait();
+            if (row_ok) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(dst + q + i) =
+                    make_uint4(pack_bf16(u[i] * inv, u[i + 1] * inv), pack_bf16(u[i + 2] * inv, u[i + 3] * inv),
+                               pack_bf16(u[i + 4] * inv, u[i + 5] * inv), pack_bf16(u[i + 6] * inv, u[i + 7] * inv));
+            }
+          }
+        }
+      } else {
+        const int mine = p.alternate ? 2 * split + t : split;
+        const size_t at = (row * p.n_q + head) * p.splits + mine;
+        if (count > 0) {
+#pragma unroll 1
+          for (int q = 0; q < 128; q += 32) {
+            float u[32];
+            tmem_ld32(oc + q, reinterpret_cast<uint32_t*>(u));
+            tmem_ld_wait();
+            if (row_ok) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(p.part_o + at * 128 + q + i) =
+                    make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+            }
+          }
+        }
+        if (row_ok && (p.alternate || count > 0)) {  // a tile without keys: no mass
+          p.part_ml[2 * at] = count > 0 ? m : -INFINITY;
+          p.part_ml[2 * at + 1] = count > 0 ? l : 0.f;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 10) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool DOCS>
+using FormsKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                             const CUtensorMap, const CUtensorMap, FormsParams);
+
+template <bool DOCS>
+FormsKernel<DOCS> forms_kernel(const ScoreArgs& s) {
+  if (s.cap > 0.f)
+    return s.slopes ? attn_forms_kernel<DOCS, true, true> : attn_forms_kernel<DOCS, true, false>;
+  return s.slopes ? attn_forms_kernel<DOCS, false, true> : attn_forms_kernel<DOCS, false, false>;
+}
+
+template <bool DOCS>
+cudaError_t prep() {
+  for (int i = 0; i < 4; ++i) {
+    ScoreArgs s{1.f, i & 1 ? 1.f : 0.f, i & 2 ? reinterpret_cast<const float*>(16) : nullptr};
+    const cudaError_t e = cudaFuncSetAttribute(
+        forms_kernel<DOCS>(s), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FORMS_SMEM);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t attn_forms_prepare() {
+  const cudaError_t e = prep<true>();
+  return e == cudaSuccess ? prep<false>() : e;
+}
+
+cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st) {
+  if (a.head_dim != 128) return cudaErrorInvalidValue;
+  FormsParams p{};
+  p.n_q = a.n_q;
+  p.n_kv = a.n_kv;
+  p.G = a.n_q / a.n_kv;
+  p.scale = a.sc.scale;
+  p.cap = a.sc.cap;
+  p.slopes = a.sc.slopes;
+  p.status = a.status;
+  p.out = (bf16*)a.out;
+  p.cu_rows = a.cu_rows;
+  p.prefix_len = a.prefix_len;
+  p.n_rows = a.n_rows;
+  p.n_docs = a.n_docs;
+  p.head_pairs = p.G % 2 == 0;
+  const int rows = p.head_pairs ? TM : 2 * TM, per = p.head_pairs ? a.n_q / 2 : a.n_q;
+  const long long tiles = a.n_rows / rows + (long long)std::min(a.n_docs, a.n_rows);  // an upper bound
+  return launch_k(forms_kernel<true>(a.sc), dim3((unsigned)(tiles * per)), dim3(FORMS_THREADS),
+                  FORMS_SMEM, st, 0, *a.map_q, *a.map_k, *a.map_v, *a.map_k, *a.map_v, p);
+}
+
+}  // namespace llgb
