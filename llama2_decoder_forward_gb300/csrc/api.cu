@@ -51,6 +51,7 @@ bool load_encode() {
     if (g_prep_err == cudaSuccess) g_prep_err = sample_prepare();
     if (g_prep_err == cudaSuccess) g_prep_err = attn_simt_prepare();
     if (g_prep_err == cudaSuccess) g_prep_err = attn_forms_prepare();
+    if (g_prep_err == cudaSuccess) g_prep_err = attn_own_prepare();
   });
   return g_encode != nullptr && g_prep_err == cudaSuccess;
 }
@@ -69,7 +70,7 @@ int sm_count_or_default() {
 // Workspace layout (byte offsets from the workspace base).
 struct Layout {
   size_t status, rope, x, u, qkv, q, kside, vside, o, a, u_last, logits, ids, tok, pos, apart,
-      ssq, total;
+      ssq, spart, total;
   size_t apart_bytes;
   int R;
 };
@@ -141,6 +142,10 @@ Layout make_layout(const llama_config* c, int sm_count) {
   L.apart = take(std::max<size_t>(L.apart_bytes, 16));
   // fused RMSNorm: per-(128-feature tile, row) sums of squares of the residual stream
   L.ssq = take((H + 127) / 128 * (size_t)R * 4);
+  // partial results of decode attention over a shared prefix (bf16)
+  L.spart = take(c->dtype == LLAMA_BF16 ? shared_partial_bytes(c->max_batch, (int)nq, (int)nkv,
+                                                               c->max_seq, sm_count)
+                                        : 16);
   L.total = off;
   return L;
 }
@@ -1400,12 +1405,37 @@ int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t*
   a.n_pages = kv->n_pages;
   a.max_pages = kv->max_pages_per_seq;
   a.key_limit = limit;
-  a.shared_len = shared_len;
+  // a batch of one that is its own prefix has nothing to share
+  a.shared_len = B == 1 && shared_seq == 0 ? 0 : shared_len;
   a.shared_seq = shared_seq;
   a.status = c->status;
+  if (cf.dtype != LLAMA_BF16) {
+    Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
+    c->launches++;
+    return cuda_rc(launch_shared_simt(cf.dtype, a, c->stream));
+  }
+  const SharedPlan plan =
+      shared_plan(B, cf.n_q_heads, cf.n_kv_heads, limit, a.shared_len, c->sm_count);
+  if (plan.partials * (128 + 2) * sizeof(float) >
+      shared_partial_bytes(cf.max_batch, cf.n_q_heads, cf.n_kv_heads, cf.max_seq, c->sm_count))
+    return LLAMA_ERR_WORKSPACE;
+  trim_maps(c);
+  const uint64_t d = cf.head_dim, nkv = cf.n_kv_heads;
+  const uint64_t rows = kv->page_size ? (uint64_t)kv->n_pages * nkv * kv->page_size
+                                      : (uint64_t)kv->batch_capacity * nkv * kv->capacity;
+  const uint32_t G = cf.n_q_heads / cf.n_kv_heads;
+  a.box_rows = attn_decode_box_rows(kv->page_size);
+  a.map_q = map3d(c, q, d, cf.n_q_heads, B, G, plan.rows_seq);
+  a.map_k = map3d(c, kv->k, d, rows, cf.n_layers, a.box_rows, 1);
+  a.map_v = map3d(c, kv->v, d, rows, cf.n_layers, a.box_rows, 1);
+  a.map_k16 = map3d(c, kv->k, d, rows, cf.n_layers, 16, 1);
+  a.map_v16 = map3d(c, kv->v, d, rows, cf.n_layers, 16, 1);
+  if (!a.map_q || !a.map_k || !a.map_v || !a.map_k16 || !a.map_v16) return LLAMA_ERR_CUDA;
+  a.partial = c->at<float>(c->L.spart);
   Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
-  c->launches++;
-  return cuda_rc(launch_shared_simt(cf.dtype, a, c->stream));
+  c->launches += (plan.prefix_parts ? 1 : 0) + (plan.own_splits > 1 ? 2 : 1);
+  if (plan.prefix_parts) TRY(cuda_rc(launch_shared_prefix(a, plan, c->stream)));
+  return cuda_rc(launch_shared_own(a, plan, c->stream));
 }
 
 int llama_op_argmax(llama_ctx* c, const float* logits, int32_t B, int32_t V, int32_t* ids) {

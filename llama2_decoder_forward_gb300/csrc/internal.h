@@ -276,10 +276,32 @@ struct SharedArgs {
   int shared_len, shared_seq;
   ScoreArgs sc;
   uint32_t* status;
+  // tensor-core form: q as 3D {d, n_q, B}, box {64, G, 128 / G}; the cache's
+  // views as in AttnDecodeArgs
+  const CUtensorMap *map_q = nullptr, *map_k = nullptr, *map_v = nullptr, *map_k16 = nullptr,
+                    *map_v16 = nullptr;
+  int box_rows = 16;
+  float* partial = nullptr;    // workspace, SharedPlan::partials x (128 + 2) floats
 };
+// How a decode batch over a shared prefix is cut: the prefix kernel's grid
+// (prefix_splits, row_blocks, n_kv) and the own keys' splits.
+struct SharedPlan {
+  int rows_seq;         // sequences of a 128-row tile
+  int alternate;        // one row tile: the two halves of a CTA share its keys
+  int row_blocks, tiles_per_split, prefix_splits;
+  int prefix_parts;     // partials per row of the prefix kernel (0: no prefix)
+  int base, own_splits, keys_per_split;
+  size_t partials;      // partial rows in all
+};
+SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, int sm_count);
+size_t shared_partial_bytes(int max_batch, int n_q, int n_kv, int max_seq, int sm_count);
 // bf16, head_dim 128 on tcgen05 (k_attn_forms_tc.cu)
 cudaError_t attn_forms_prepare();
 cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st);
+cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaStream_t st);
+// own keys of a decode batch and the merge with its prefix (k_attn_own.cu)
+cudaError_t attn_own_prepare();
+cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStream_t st);
 // CUDA-core forms for any head_dim (k_attn_simt.cu)
 cudaError_t attn_simt_prepare();
 cudaError_t launch_docs_simt(int dtype, const DocsArgs& a, cudaStream_t st);

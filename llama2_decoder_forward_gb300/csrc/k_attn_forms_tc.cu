@@ -601,4 +601,38 @@ cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st) {
                   FORMS_SMEM, st, 0, *a.map_q, *a.map_k, *a.map_v, *a.map_k, *a.map_v, p);
 }
 
+cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaStream_t st) {
+  if (a.head_dim != 128) return cudaErrorInvalidValue;
+  FormsParams p{};
+  p.n_q = a.n_q;
+  p.n_kv = a.n_kv;
+  p.G = a.n_q / a.n_kv;
+  p.scale = a.sc.scale;
+  p.cap = a.sc.cap;
+  p.slopes = a.sc.slopes;
+  p.status = a.status;
+  p.positions = a.positions;
+  p.page_table = a.page_table;
+  p.B = a.B;
+  p.rows_seq = s.rows_seq;
+  p.alternate = s.alternate;
+  p.layer = a.layer;
+  p.page_size = a.page_size;
+  p.capacity = a.capacity;
+  p.batch_cap = a.batch_cap;
+  p.n_pages = a.n_pages;
+  p.max_pages = a.max_pages;
+  p.box_rows = a.box_rows;
+  p.key_limit = a.key_limit;
+  p.shared_len = a.shared_len;
+  p.shared_seq = a.shared_seq;
+  p.tiles_per_split = s.tiles_per_split;
+  p.part_o = a.partial;
+  p.part_ml = a.partial + s.partials * 128;
+  p.splits = s.prefix_parts;
+  return launch_k(forms_kernel<false>(a.sc), dim3(s.prefix_splits, s.row_blocks, a.n_kv),
+                  dim3(FORMS_THREADS), FORMS_SMEM, st, 0, *a.map_q, *a.map_k, *a.map_v, *a.map_k16,
+                  *a.map_v16, p);
+}
+
 }  // namespace llgb

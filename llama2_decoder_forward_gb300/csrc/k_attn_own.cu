@@ -1,0 +1,660 @@
+// Decode attention with capped or biased scores: the keys a sequence owns
+// (from the shared prefix's end to its position), bf16, head_dim 128, and the
+// merge with the prefix's partial results (k_attn_forms_tc.cu).
+//
+//   x = scale q.k;  s = (cap tanh(x / cap) or x) - slope (i - j);  softmax;  sum p v
+//
+// Bound by the K/V bytes: each key is read once, for all query heads of its
+// group. One CTA per (key split, K/V head, sequence): a producer warp streams
+// 64-key tiles (128-byte swizzled TMA boxes, L2 evict-first) into a 3-stage
+// ring; four consumer warps take 16 keys each and run S and P V on mma.sync,
+// with an fp32 online softmax; the warps' (max, sum, O) merge in shared memory.
+// Groups of up to 8 heads put the keys on the MMA's rows (S^T = K Q^T,
+// O^T = V^T P^T), larger ones the heads. P is a bf16 pair (high part and
+// remainder), free while memory bounds the kernel.
+// The launch follows the prefix kernel's and may start while it drains: that
+// kernel lets it start only after its own wait, so whatever ran before the
+// prefix kernel is complete; what is read before this kernel's wait comes
+// from L2 (TMA, .cg), and only the merge, after the wait, reads partials.
+// With one split the merge happens here; else a small kernel joins all parts.
+#include <algorithm>
+
+#include "attn_score.cuh"
+#include "internal.h"
+
+namespace llgb {
+
+namespace {
+
+constexpr int HD = 128;
+constexpr int SUB = 16;                         // keys of a warp's step
+constexpr int TILE_K = 64;                      // keys of a stage
+constexpr int STAGES = 3;
+constexpr int OWN_THREADS = 160;                // 4 consumer warps + the producer
+constexpr uint32_t SUB_HALF = SUB * 128;        // 16 keys x 64 dims
+constexpr uint32_t HALF = TILE_K * 128;         // 64 keys x 64 dims: 8 KB
+constexpr uint32_t STAGE = 4 * HALF;            // K and V, two dim halves each
+constexpr size_t OWN_SMEM = STAGES * STAGE + 1024 + 256;
+static_assert((4 * 16 * HD + 128) * 4 <= STAGES * STAGE, "the merge area aliases the ring");
+
+struct OwnParams {
+  const bf16* q;
+  bf16* out;
+  const int32_t *positions, *page_table;
+  uint32_t* status;
+  int n_q, n_kv, G, layer;
+  int page_size, capacity, n_pages, max_pages, box_rows;
+  int key_limit, first;        // keys from `first` on; position limit
+  int base;                    // first rounded down to a tile
+  int splits, keys_per_split;
+  int prefix_parts;            // partials per row that the prefix kernel wrote
+  float *part_o, *part_ml;     // [B n_q][prefix_parts][...]
+  float *own_o, *own_ml;       // [B n_q][splits][...] (splits > 1)
+  float scale, cap;
+  const float* slopes;
+};
+
+__device__ __forceinline__ void consumers_bar() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+
+__device__ __forceinline__ int own_kv_row(const OwnParams& p, int b, int g, int k0) {
+  if (p.page_size == 0) return (b * p.n_kv + g) * p.capacity + k0;
+  const int pi = k0 / p.page_size;
+  const int page = pi < p.max_pages ? __ldcg(p.page_table + (size_t)b * p.max_pages + pi) : -1;
+  if (page < 0 || page >= p.n_pages) {
+    flag(p.status, LLAMA_FLAG_PAGE_RANGE);
+    return -64;
+  }
+  return (page * p.n_kv + g) * p.page_size + (k0 - pi * p.page_size);
+}
+
+// Scores in log2 units: x log2e after the cap, minus the distance bias. zc =
+// 2 log2e scale / cap, cl = cap log2e; cap tanh(y) = cap (1 - 2 / (1 + e^2y)).
+struct ScoreConst {
+  float c, zc, cl;
+  bool cap;
+};
+__device__ __forceinline__ float score(const ScoreConst& k, float x) {
+  if (!k.cap) return x * k.c;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * k.zc)));
+  return fmaf(-2.f * k.cl, r, k.cl);
+}
+
+// Rows of a 16-key step outside [lead, valid) may hold anything: zero their V.
+__device__ __forceinline__ void clean_v(uint8_t* v, int lead, int valid, int lane) {
+  if (lead == 0 && valid == SUB) return;
+  for (int i = lane; i < SUB * 16; i += 32) {
+    const int row = i >> 4, half = (i >> 3) & 1, chunk = i & 7;
+    if (row < lead || row >= valid)
+      *reinterpret_cast<uint4*>(v + half * HALF + row * 128 + chunk * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Groups of up to 8 heads: keys on the MMA rows. Lane l tracks heads 2(l%4)
+// and 2(l%4) + 1. Leaves (max, sum, O) of this warp in shared memory.
+__device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, uint64_t* full,
+                                             uint64_t* empty, volatile uint32_t* stop, int b, int g,
+                                             int kbeg, int kend, int pos, int warp, int lane) {
+  const int G = p.G, hq = lane >> 2, hc = 2 * (lane & 3);
+  uint32_t qf[8][2];  // Q^T fragments: head lane/4
+  const bf16* qb = p.q + ((size_t)b * p.n_q + (size_t)g * G + hq) * HD;
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const int col = kk * 16 + 2 * (lane & 3);
+    qf[kk][0] = hq < G ? __ldcg(reinterpret_cast<const unsigned*>(qb + col)) : 0u;
+    qf[kk][1] = hq < G ? __ldcg(reinterpret_cast<const unsigned*>(qb + col + 8)) : 0u;
+  }
+  constexpr float kLog2e = 1.4426950408889634f;
+  const ScoreConst sc{p.scale * kLog2e, p.cap > 0.f ? 2.f * p.scale * kLog2e / p.cap : 0.f,
+                      p.cap * kLog2e, p.cap > 0.f};
+  float sl[2] = {0.f, 0.f};
+  if (p.slopes) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sl[j] = hc + j < G ? __ldcg(p.slopes + g * G + hc + j) * kLog2e : 0.f;
+  }
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  const int mi = lane >> 3, rr = lane & 7;
+  const int n_tiles = (kend - kbeg + TILE_K - 1) / TILE_K;
+  int s = 0;
+  uint32_t ph = 0;
+  for (int t = 0; t < n_tiles; ++t) {
+    if (*stop) break;
+    if (!mbar_wait(&full[s], ph, p.status)) {
+      *stop = 1;
+      break;
+    }
+    const int k0 = kbeg + t * TILE_K + warp * SUB;
+    const int lead = max(0, p.first - k0), valid = min(SUB, kend - k0);
+    if (lead < valid) {
+      uint8_t* st = smem + s * STAGE;
+      const uint32_t kbase = smem_u32(st + warp * SUB_HALF);
+      uint8_t* vptr = st + 2 * HALF + warp * SUB_HALF;
+      clean_v(vptr, lead, valid, lane);
+      const uint32_t vbase = smem_u32(vptr);
+      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {  // even and odd steps in separate chains
+        const int row = ((mi & 1) << 3) + rr, chunk = (kk & 3) * 2 + (mi >> 1);
+        uint32_t a[4];
+        ldsm_x4(kbase + (kk >> 2) * HALF + swz128(row, chunk), a[0], a[1], a[2], a[3]);
+        mma_bf16_16816((kk & 1) ? s1 : s0, a, qf[kk][0], qf[kk][1]);
+      }
+      float sv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = (lane >> 2) + (i >= 2 ? 8 : 0);
+        float x = score(sc, s0[i] + s1[i]);
+        if (p.slopes) x = fmaf(-sl[i & 1], (float)(pos - k0 - key), x);
+        sv[i] = key >= lead && key < valid ? x : -INFINITY;
+      }
+      float corr[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float mx = fmaxf(sv[j], sv[j + 2]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float mn = fmaxf(m[j], mx);
+        corr[j] = mn == m[j] ? 1.f : ex2(m[j] - mn);
+        m[j] = mn;
+      }
+      float pv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pv[i] = m[i & 1] == -INFINITY ? 0.f : ex2(sv[i] - m[i & 1]);
+      l[0] = l[0] * corr[0] + pv[0] + pv[2];
+      l[1] = l[1] * corr[1] + pv[1] + pv[3];
+      if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          o[d][0] *= corr[0];
+          o[d][1] *= corr[1];
+          o[d][2] *= corr[0];
+          o[d][3] *= corr[1];
+        }
+      }
+      uint32_t p0h, p0l, p1h, p1l;
+      split_pack(pv[0], pv[1], p0h, p0l);
+      split_pack(pv[2], pv[3], p1h, p1l);
+      const uint32_t bh0 = movmatrix_t(p0h), bh1 = movmatrix_t(p1h);
+      const uint32_t bl0 = movmatrix_t(p0l), bl1 = movmatrix_t(p1l);
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        const int c16 = d * 2 + (mi & 1), row = ((mi >> 1) << 3) + rr;
+        uint32_t a[4];
+        ldsm_x4_t(vbase + (c16 >> 3) * HALF + swz128(row, c16 & 7), a[0], a[1], a[2], a[3]);
+        mma_bf16_16816(o[d], a, bh0, bh1);
+        mma_bf16_16816(o[d], a, bl0, bl1);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    if (++s == STAGES) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 4);
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
+  }
+  float* so = reinterpret_cast<float*>(smem);  // [4][16][128], then max [4][16], sum [4][16]
+  float* sm = so + 4 * 16 * HD;
+  consumers_bar();  // every consumer is done with the ring
+#pragma unroll
+  for (int d = 0; d < 8; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (hc + (i & 1) < G)
+        so[(warp * 16 + hc + (i & 1)) * HD + d * 16 + (lane >> 2) + (i >= 2 ? 8 : 0)] = o[d][i];
+  if (lane < 4) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (hc + j < G) {
+        sm[warp * 16 + hc + j] = m[j];
+        sm[64 + warp * 16 + hc + j] = l[j];
+      }
+  }
+}
+
+// Groups of 9 to 16 heads: heads on the MMA rows (zero-padded to 16).
+__device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem, uint64_t* full,
+                                              uint64_t* empty, volatile uint32_t* stop, int b, int g,
+                                              int kbeg, int kend, int pos, int warp, int lane) {
+  const int G = p.G, r0 = lane >> 2;
+  uint32_t qa[8][4];
+  const bf16* qb = p.q + ((size_t)b * p.n_q + (size_t)g * G) * HD;
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = r0 + 8 * (i & 1), col = kk * 16 + 2 * (lane & 3) + 8 * (i >> 1);
+      qa[kk][i] = row < G ? __ldcg(reinterpret_cast<const unsigned*>(qb + row * HD + col)) : 0u;
+    }
+  constexpr float kLog2e = 1.4426950408889634f;
+  const ScoreConst sc{p.scale * kLog2e, p.cap > 0.f ? 2.f * p.scale * kLog2e / p.cap : 0.f,
+                      p.cap * kLog2e, p.cap > 0.f};
+  float sl[2] = {0.f, 0.f};
+  if (p.slopes) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sl[j] = r0 + 8 * j < G ? __ldcg(p.slopes + g * G + r0 + 8 * j) * kLog2e : 0.f;
+  }
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[16][4];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  const int mi = lane >> 3, rr = lane & 7;
+  const int n_tiles = (kend - kbeg + TILE_K - 1) / TILE_K;
+  int s = 0;
+  uint32_t ph = 0;
+  for (int t = 0; t < n_tiles; ++t) {
+    if (*stop) break;
+    if (!mbar_wait(&full[s], ph, p.status)) {
+      *stop = 1;
+      break;
+    }
+    const int k0 = kbeg + t * TILE_K + warp * SUB;
+    const int lead = max(0, p.first - k0), valid = min(SUB, kend - k0);
+    if (lead < valid) {
+      uint8_t* st = smem + s * STAGE;
+      const uint32_t kbase = smem_u32(st + warp * SUB_HALF);
+      uint8_t* vptr = st + 2 * HALF + warp * SUB_HALF;
+      clean_v(vptr, lead, valid, lane);
+      const uint32_t vbase = smem_u32(vptr);
+      float sv[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sv[0][i] = sv[1][i] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const int chunk = (kk & 3) * 2 + (mi & 1), row = ((mi >> 1) << 3) + rr;
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(kbase + (kk >> 2) * HALF + swz128(row, chunk), b0, b1, b2, b3);
+        mma_bf16_16816(sv[0], qa[kk], b0, b1);
+        mma_bf16_16816(sv[1], qa[kk], b2, b3);
+      }
+      float mx[2] = {-INFINITY, -INFINITY}, corr[2], ps[2] = {0.f, 0.f};
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = nb * 8 + 2 * (lane & 3) + (i & 1);
+          float x = score(sc, sv[nb][i]);
+          if (p.slopes) x = fmaf(-sl[i >> 1], (float)(pos - k0 - key), x);
+          sv[nb][i] = key >= lead && key < valid ? x : -INFINITY;
+          mx[i >> 1] = fmaxf(mx[i >> 1], sv[nb][i]);
+        }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        const float mn = fmaxf(m[h], mx[h]);
+        corr[h] = mn == m[h] ? 1.f : ex2(m[h] - mn);
+        m[h] = mn;
+      }
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = m[i >> 1] == -INFINITY ? 0.f : ex2(sv[nb][i] - m[i >> 1]);
+          sv[nb][i] = e;
+          ps[i >> 1] += e;
+        }
+      l[0] = l[0] * corr[0] + ps[0];
+      l[1] = l[1] * corr[1] + ps[1];
+#pragma unroll
+      for (int d = 0; d < 16; ++d) {
+        o[d][0] *= corr[0];
+        o[d][1] *= corr[0];
+        o[d][2] *= corr[1];
+        o[d][3] *= corr[1];
+      }
+      uint32_t pa[4], pl[4];
+      split_pack(sv[0][0], sv[0][1], pa[0], pl[0]);
+      split_pack(sv[0][2], sv[0][3], pa[1], pl[1]);
+      split_pack(sv[1][0], sv[1][1], pa[2], pl[2]);
+      split_pack(sv[1][2], sv[1][3], pa[3], pl[3]);
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        const int c16 = d * 2 + (mi >> 1), row = ((mi & 1) << 3) + rr;
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_t(vbase + (c16 >> 3) * HALF + swz128(row, c16 & 7), b0, b1, b2, b3);
+        mma_bf16_16816(o[2 * d], pa, b0, b1);
+        mma_bf16_16816(o[2 * d + 1], pa, b2, b3);
+        mma_bf16_16816(o[2 * d], pl, b0, b1);
+        mma_bf16_16816(o[2 * d + 1], pl, b2, b3);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    if (++s == STAGES) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+  }
+  float* so = reinterpret_cast<float*>(smem);
+  float* sm = so + 4 * 16 * HD;
+  consumers_bar();
+#pragma unroll
+  for (int d = 0; d < 16; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      so[(warp * 16 + r0 + (i >= 2 ? 8 : 0)) * HD + d * 8 + 2 * (lane & 3) + (i & 1)] = o[d][i];
+  if ((lane & 3) == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sm[warp * 16 + r0 + 8 * h] = m[h];
+      sm[64 + warp * 16 + r0 + 8 * h] = l[h];
+    }
+  }
+}
+
+// A row's running merge in one warp: maximum and sum (the same in every lane)
+// and the output's dims 4 lane .. 4 lane + 3, unnormalised.
+struct RowSum {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float f, const float4& v) {
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
+  }
+  __device__ __forceinline__ void scale_to(float mx) {
+    const float f = m == -INFINITY ? 0.f : exp2f(m - mx);
+    l *= f;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+    m = mx;
+  }
+};
+
+// Adds `parts` partials (at..) of the row: lane s reads part s's maximum and
+// sum, so they take one load for 32 parts; the order of the sums is fixed.
+__device__ __forceinline__ void fold(const float* o, const float* ml, size_t at, int parts, int lane,
+                                     RowSum& r) {
+  for (int s0 = 0; s0 < parts; s0 += 32) {
+    const int k = min(32, parts - s0);
+    float2 x = make_float2(-INFINITY, 0.f);
+    if (lane < k) x = __ldcg(reinterpret_cast<const float2*>(ml) + at + s0 + lane);
+    float mx = x.x;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+    mx = fmaxf(mx, r.m);
+    if (mx == -INFINITY) continue;
+    r.scale_to(mx);
+    const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - mx);
+    float ls = f == 0.f ? 0.f : x.y * f;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, w);
+    r.l += ls;
+    const float4* src = reinterpret_cast<const float4*>(o + (at + s0) * HD) + lane;
+#pragma unroll 8
+    for (int s = 0; s < k; ++s) {
+      const float fs = __shfl_sync(0xffffffffu, f, s);
+      // a part without keys may hold anything: its O was not written
+      if (fs != 0.f) r.add(fs, __ldcg(src + s * (HD / 4)));
+    }
+  }
+}
+
+__device__ __forceinline__ void store_row(bf16* dst, int lane, const RowSum& r) {
+  const float i = r.l > 0.f || r.l != r.l ? 1.f / r.l : 0.f;
+  reinterpret_cast<uint2*>(dst)[lane] =
+      make_uint2(pack_bf16(r.o.x * i, r.o.y * i), pack_bf16(r.o.z * i, r.o.w * i));
+}
+
+template <bool KEYS>
+__global__ void __launch_bounds__(OWN_THREADS, 2)
+    attn_own_kernel(const __grid_constant__ CUtensorMap mapK,
+                    const __grid_constant__ CUtensorMap mapV,
+                    const __grid_constant__ CUtensorMap mapK16,
+                    const __grid_constant__ CUtensorMap mapV16, OwnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
+  uint64_t* empty = full + STAGES;
+  volatile uint32_t* stop = reinterpret_cast<volatile uint32_t*>(empty + STAGES);
+  const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (!bc_smem(smem, STAGES * STAGE + 256, 1024, threadIdx.x == 0 ? p.status : nullptr)) {
+    grid_dep_wait();
+    return;
+  }
+  if (p.prefix_parts == 0) {  // else the prefix kernel has waited for what came before it
+    grid_dep_wait();
+    grid_dep_launch();
+  }
+  const int pos = __ldcg(p.positions + b);
+  int n = pos + 1;
+  if (pos < 0 || pos >= p.key_limit) {
+    if (split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
+    n = pos < 0 ? 0 : p.key_limit;
+  }
+  const int kbeg = p.base + split * p.keys_per_split;
+  const int kend = min(n, kbeg + p.keys_per_split);
+  const bool any = kend > max(kbeg, p.first);
+  if (any) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < STAGES; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], 4);
+      }
+      *stop = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+    const int n_tiles = (kend - kbeg + TILE_K - 1) / TILE_K;
+    if (warp == 4) {  // ------------------------------------------------ producer
+      if (lane == 0) {
+        tma_prefetch_desc(&mapK);
+        tma_prefetch_desc(&mapV);
+        const uint64_t pol = l2_policy_evict_first();  // own keys are streamed once
+        int s = 0, issued = 0;
+        uint32_t ph = 1;
+        for (int t = 0; t < n_tiles; ++t) {
+          if (*stop || !mbar_wait(&empty[s], ph, p.status)) {
+            *stop = 1;
+            break;
+          }
+          const int k0 = kbeg + t * TILE_K;
+          const int j0 = max(0, p.first - k0) / SUB;                     // 16-key steps that
+          const int j1 = min(TILE_K / SUB, (kend - k0 + SUB - 1) / SUB);  // hold own keys
+          uint8_t* st = smem + s * STAGE;
+          if (p.box_rows == TILE_K && j0 == 0 && j1 == TILE_K / SUB) {
+            const int row = own_kv_row(p, b, g, k0);
+            mbar_arrive_expect_tx(&full[s], STAGE);
+            tma_load_3d_hint(st, &mapK, &full[s], 0, row, p.layer, pol);
+            tma_load_3d_hint(st + HALF, &mapK, &full[s], 64, row, p.layer, pol);
+            tma_load_3d_hint(st + 2 * HALF, &mapV, &full[s], 0, row, p.layer, pol);
+            tma_load_3d_hint(st + 3 * HALF, &mapV, &full[s], 64, row, p.layer, pol);
+          } else {
+            mbar_arrive_expect_tx(&full[s], (uint32_t)(j1 - j0) * 4 * SUB_HALF);
+            for (int j = j0; j < j1; ++j) {
+              const int row = own_kv_row(p, b, g, k0 + j * SUB);
+              uint8_t* d = st + j * SUB_HALF;
+              tma_load_3d_hint(d, &mapK16, &full[s], 0, row, p.layer, pol);
+              tma_load_3d_hint(d + HALF, &mapK16, &full[s], 64, row, p.layer, pol);
+              tma_load_3d_hint(d + 2 * HALF, &mapV16, &full[s], 0, row, p.layer, pol);
+              tma_load_3d_hint(d + 3 * HALF, &mapV16, &full[s], 64, row, p.layer, pol);
+            }
+          }
+          ++issued;
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        // no copy in flight when the CTA exits, whoever gave up
+        for (int t = max(0, issued - STAGES); t < issued; ++t)
+          mbar_wait(&full[t % STAGES], (t / STAGES) & 1, p.status);
+      }
+      if (p.prefix_parts) grid_dep_wait();
+      return;
+    }
+    if (KEYS)
+      consume_keys(p, smem, full, empty, stop, b, g, kbeg, kend, pos, warp, lane);
+    else
+      consume_heads(p, smem, full, empty, stop, b, g, kbeg, kend, pos, warp, lane);
+    consumers_bar();
+    if (*stop) {
+      if (p.prefix_parts) grid_dep_wait();
+      return;
+    }
+  } else if (warp == 4) {
+    if (p.prefix_parts) grid_dep_wait();
+    return;
+  }
+  if (p.prefix_parts) {  // the partials of the prefix, and the output's last reader
+    grid_dep_wait();
+    grid_dep_launch();
+  }
+  if (!any && p.splits > 1) return;  // the joining kernel skips this split
+  const float* so = reinterpret_cast<const float*>(smem);
+  const float* sm = so + 4 * 16 * HD;
+  for (int r = warp; r < p.G; r += 4) {  // a warp per row
+    RowSum x;
+    if (any) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, sm[w * 16 + r]);
+      if (mx != -INFINITY) {
+        x.m = mx;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float mw = sm[w * 16 + r];
+          const float f = mw == -INFINITY ? 0.f : exp2f(mw - mx);
+          x.l = fmaf(sm[64 + w * 16 + r], f, x.l);
+          x.add(f, reinterpret_cast<const float4*>(so + (w * 16 + r) * HD)[lane]);
+        }
+      }
+    }
+    const size_t bh = (size_t)b * p.n_q + (size_t)g * p.G + r;
+    if (p.splits == 1) {
+      fold(p.part_o, p.part_ml, bh * p.prefix_parts, p.prefix_parts, lane, x);
+      store_row(p.out + bh * HD, lane, x);
+    } else {
+      const size_t at = bh * p.splits + split;
+      reinterpret_cast<float4*>(p.own_o + at * HD)[lane] = x.o;
+      if (lane == 0) *reinterpret_cast<float2*>(p.own_ml + 2 * at) = make_float2(x.m, x.l);
+    }
+  }
+}
+
+// Joins a row's prefix partials and own splits, one warp per (sequence, head).
+__global__ void __launch_bounds__(128) attn_own_join_kernel(OwnParams p, int rows) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, bh = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (bh >= rows) return;
+  const int pos = p.positions[bh / p.n_q];
+  const int n = pos < 0 ? 0 : min(pos + 1, p.key_limit);
+  const int used = n > p.first ? min(p.splits, (n - p.base + p.keys_per_split - 1) / p.keys_per_split) : 0;
+  RowSum x;
+  fold(p.part_o, p.part_ml, (size_t)bh * p.prefix_parts, p.prefix_parts, lane, x);
+  fold(p.own_o, p.own_ml, (size_t)bh * p.splits, used, lane, x);
+  store_row(p.out + (size_t)bh * HD, lane, x);
+}
+
+}  // namespace
+
+cudaError_t attn_own_prepare() {
+  cudaError_t e = cudaFuncSetAttribute(attn_own_kernel<true>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)OWN_SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attn_own_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)OWN_SMEM);
+  return e;
+}
+
+SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, int sm_count) {
+  SharedPlan s{};
+  const int G = n_q / n_kv;
+  // prefix: one CTA per SM, each with its share of the key tiles
+  s.rows_seq = 128 / G;
+  s.alternate = B <= s.rows_seq;
+  s.row_blocks = s.alternate ? 1 : (B + 2 * s.rows_seq - 1) / (2 * s.rows_seq);
+  const int tiles = (shared_len + 127) / 128;
+  if (tiles > 0) {
+    const int want = std::max(1, sm_count / (n_kv * s.row_blocks));
+    s.tiles_per_split = (tiles + want - 1) / want;
+    s.prefix_splits = (tiles + s.tiles_per_split - 1) / s.tiles_per_split;
+    s.prefix_parts = s.prefix_splits * (s.alternate ? 2 : 1);
+  }
+  // own keys: split while two CTAs per SM are not reached twice over and a
+  // split keeps 256 keys
+  s.base = shared_len / 64 * 64;
+  const int keys = std::max(1, key_limit - s.base), pairs = B * n_kv;
+  int k = 1;
+  while (pairs * k < 4 * sm_count && k < 16 && keys / (2 * k) >= 256) k *= 2;
+  s.keys_per_split = ((keys + k - 1) / k + 63) / 64 * 64;
+  s.own_splits = (keys + s.keys_per_split - 1) / s.keys_per_split;
+  const size_t rows = (size_t)B * n_q;
+  s.partials = rows * s.prefix_parts + (s.own_splits > 1 ? rows * s.own_splits : 0);
+  return s;
+}
+
+size_t shared_partial_bytes(int max_batch, int n_q, int n_kv, int max_seq, int sm_count) {
+  // shared_plan's partials over every batch up to max_batch and every prefix:
+  // prefix parts are at most 256 rows a CTA at one CTA per SM, or two per row;
+  // own splits double only below 4 CTAs per SM
+  const size_t rows = (size_t)max_batch * n_q, G = n_q / n_kv;
+  const size_t tiles = (size_t)(max_seq + 127) / 128;
+  const size_t prefix = std::max(2 * rows, std::min<size_t>(256 * (size_t)sm_count, rows * 2 * tiles));
+  const size_t own = std::min<size_t>(8 * (size_t)sm_count * G, rows * 16);
+  return (prefix + own) * (HD + 2) * sizeof(float);
+}
+
+cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStream_t st) {
+  OwnParams p{};
+  p.q = (const bf16*)a.q;
+  p.out = (bf16*)a.out;
+  p.positions = a.positions;
+  p.page_table = a.page_table;
+  p.status = a.status;
+  p.n_q = a.n_q;
+  p.n_kv = a.n_kv;
+  p.G = a.n_q / a.n_kv;
+  p.layer = a.layer;
+  p.page_size = a.page_size;
+  p.capacity = a.capacity;
+  p.n_pages = a.n_pages;
+  p.max_pages = a.max_pages;
+  p.box_rows = a.box_rows;
+  p.key_limit = a.key_limit;
+  p.first = a.shared_len;
+  p.base = s.base;
+  p.splits = s.own_splits;
+  p.keys_per_split = s.keys_per_split;
+  p.prefix_parts = s.prefix_parts;
+  const size_t rows = (size_t)a.B * a.n_q;
+  p.part_o = a.partial;
+  p.part_ml = p.part_o + s.partials * HD;
+  p.own_o = p.part_o + rows * s.prefix_parts * HD;
+  p.own_ml = p.part_ml + rows * s.prefix_parts * 2;
+  p.scale = a.sc.scale;
+  p.cap = a.sc.cap;
+  p.slopes = a.sc.slopes;
+  const dim3 grid(s.own_splits, a.n_kv, a.B), block(OWN_THREADS);
+  const cudaError_t e =
+      p.G <= 8 ? launch_k(attn_own_kernel<true>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
+                          *a.map_k16, *a.map_v16, p)
+               : launch_k(attn_own_kernel<false>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
+                          *a.map_k16, *a.map_v16, p);
+  if (e != cudaSuccess || s.own_splits == 1) return e;
+  return launch_k(attn_own_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 0, p,
+                  (int)rows);
+}
+
+}  // namespace llgb
