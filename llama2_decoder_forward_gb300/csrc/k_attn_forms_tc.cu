@@ -8,14 +8,17 @@
 // (FlashAttention): the scores never leave the SM. One CTA per SM works on two
 // tiles of 128 query rows (MMA M, one tensor-memory lane per row) against key
 // tiles of 128:
-//   warps 0-3, 4-7  softmax of row tile 0 and 1, one thread per row;
-//   warp 8, 9       TMA producers of Q + K and of V (rings of 32 KB tiles);
-//   warp 10, 11     MMA issuers of row tile 0 and 1.
-// While one tile's softmax runs on the CUDA cores, the tensor cores work for
-// the other tile. An issuer's order is O += P_j V_j, then S_{j+1} = Q K^T_{j+1}:
-// tcgen05 operations of one thread execute in order, so P_j (bf16, written
-// over the scores it came from) is read before S_{j+1} replaces it, and the
-// arrival of S_{j+1} also says that O += P_j V_j is done. Tensor memory: per row
+//   warps 0-7, 8-15  softmax of row tile 0 and 1: two threads per row, one for
+//                    keys 0-63 of a tile and output dims 0-63, one for the rest;
+//   warp 16, 17      TMA producers of Q + K and of V (rings of 32 KB tiles);
+//   warp 18          one thread issues the MMAs.
+// It alternates between the row tiles, O += P_j V_j and S_{j+1} = Q K^T_{j+1} of
+// one and then of the other, so while one tile's softmax runs on the CUDA cores
+// the tensor cores work for the other (with an issuer per row tile the tensor
+// pipe interleaved the two, both softmaxes ran at the same time and the pipe
+// idled meanwhile). tcgen05 operations of one thread execute in order: P_j (bf16,
+// written over the scores it came from) is read before S_{j+1} replaces it, and
+// the arrival of S_{j+1} also says that O += P_j V_j is done. Tensor memory: per row
 // tile 128 columns of S / P and 128 of O, all 512.
 // The two row tiles are
 //   documents, n_q / n_kv even : two query heads of one K/V head, same rows;
@@ -43,8 +46,12 @@ constexpr uint32_t HALF = 128 * 128;        // 128 rows x 64 dims bf16, 128-byte
 constexpr uint32_t TILE = 2 * HALF;         // 128 rows x 128 dims
 constexpr int SLOTS = 7;                    // Q 0, (Q 1), then the K ring and the V ring
 constexpr uint32_t OFF_BAR = SLOTS * TILE;
-constexpr size_t FORMS_SMEM = OFF_BAR + 256;
-constexpr int FORMS_THREADS = 384;
+// what the two threads of a row exchange: fp32 [2 row tiles][2 halves][128], the
+// tile's maxima, at the end the sums. One buffer is enough: a tile's maxima are
+// read before its P is announced, and the next tile's scores come after that.
+constexpr uint32_t OFF_X = OFF_BAR + 256;
+constexpr size_t FORMS_SMEM = OFF_X + 2 * 2 * 128 * 4;
+constexpr int FORMS_THREADS = 640;
 constexpr int MAXK = 4, MAXV = 2;           // ring sizes at most
 constexpr uint32_t O_COL = 256;             // S tiles at columns 0 and 128, O tiles at 256 and 384
 constexpr float kLazy = 8.f;
@@ -67,7 +74,15 @@ struct FormsParams {
   int key_limit, shared_len, shared_seq, tiles_per_split;
   float *part_o, *part_ml;                  // [B n_q][splits][128], [B n_q][splits][2] (max log2, sum)
   int splits;                               // partials of a row written here start at 0
+  float poly[6];                            // KCap: kTanh; KCapFixed: times powers of scale / cap
 };
+
+// What the scores need. A cap bounds them, so up to kFixedCap (log2 units) the
+// weights are 2^s with no maximum subtracted: 2^+-72 times any sum stays inside
+// fp32 (and bf16's exponent), and the row maxima, their exchange and every
+// rescale fall away.
+enum { KPlain, KBias, KCapFixed, KCap };
+constexpr float kFixedCap = 72.5f;  // caps up to 50
 
 // Bounded wait without a call, for code whose registers setmaxnreg resizes:
 // at most 2^20 tries of up to 2 us.
@@ -150,14 +165,26 @@ __device__ __forceinline__ void load_tile(const FormsParams& p, const CUtensorMa
   }
 }
 
-// 1 / (1 + 2^z): one exponential and one reciprocal on the special-function unit
-__device__ __forceinline__ float inv_1p_ex2(float z) {
+// tanh(y) = y R(y^2) for |y| <= 1, R of degree 5: a weighted least-squares fit of
+// smallest relative error (5.9e-7 in fp64, 7e-7 evaluated in fp32). Six
+// multiply-adds on pairs replace an exponential and a reciprocal per score on
+// the special-function unit, which would bound the kernel (three
+// special-function results per score against one).
+constexpr float kTanh[6] = {0.9999994039535522f,   -0.3332904279232025f,  0.13281433284282684f,
+                            -0.051605671644210815f, 0.016743114218115807f, -0.0030670599080622196f};
+
+// cap tanh(x / cap) in log2 units for any x (in units of 1 / zc): cl (1 - 2 / (1 + e^2y))
+__device__ __forceinline__ float cap_any(float x, float zc, float cl) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(z)));
-  return r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * zc)));
+  return fmaf(-2.f * cl, r, cl);
 }
 
-template <bool DOCS, bool CAP, bool BIAS>
+__device__ __forceinline__ void half_bar(int id) {  // the two warps that share 32 rows
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+
+template <bool DOCS, int KIND>
 __global__ void __launch_bounds__(FORMS_THREADS, 1)
     attn_forms_kernel(const __grid_constant__ CUtensorMap mapQ,
                       const __grid_constant__ CUtensorMap mapK,
@@ -173,12 +200,13 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   uint64_t* vtail = vempty + MAXV;  // the ragged last V tile has its absent rows zeroed
   uint64_t* sfull = vtail + 1;      // [2] S_j of row tile t is in tensor memory
   uint64_t* pready = sfull + 2;     // [2] P_j is, and O is rescaled
-  uint64_t* fin = pready + 2;       // [2] every MMA of the tile's issuer is done
-  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(fin + 2);  // tensor memory, abort
-  static_assert((1 + 2 * MAXK + 2 * MAXV + 1 + 6) * 8 + 8 <= 256, "barrier block");
+  uint64_t* fin = pready + 2;       // [2] the row tile's last O += P V is done
+  uint64_t* drained = fin + 2;      // every MMA is
+  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(drained + 1);  // tensor memory, abort
+  static_assert((1 + 2 * MAXK + 2 * MAXV + 1 + 7) * 8 + 8 <= 256, "barrier block");
   grid_dep_wait();
   grid_dep_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023u) != 0 ||  // the swizzled tiles need 1024-byte alignment
       !bc_smem(smem, FORMS_SMEM, 1024, threadIdx.x == 0 ? p.status : nullptr)) {
     if (threadIdx.x == 0) flag(p.status, LLAMA_FLAG_INDEX);
@@ -232,35 +260,36 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   if (DOCS) g = h0 / p.G;
 
   if (threadIdx.x == 0) {
-    const uint32_t readers = alt ? 1 : 2;
     mbar_init(qfull, 1);
     for (int s = 0; s < MAXK; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], readers);
+      mbar_init(&kempty[s], 1);
     }
     for (int s = 0; s < MAXV; ++s) {
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], readers);
+      mbar_init(&vempty[s], 1);
     }
     mbar_init(vtail, 1);
+    mbar_init(drained, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
-      mbar_init(&pready[t], 4);
+      mbar_init(&pready[t], 8);
       mbar_init(&fin[t], 1);
     }
     ctl[1] = 0;
     fence_mbar_init();
   }
-  if (warp == 10) tmem_alloc(const_cast<uint32_t*>(ctl), 512);
+  if (warp == 18) tmem_alloc(const_cast<uint32_t*>(ctl), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl[0];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl[0], 0);
   const int last_rows = kmax - (t0 + n_tiles - 1) * TN;  // keys of the last tile; over 128: all
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 8) {  // ------------------------------------------- Q and K producer
+  // launched with 640 x 96 registers: 512 x 104 + 128 x 64
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 16) {  // ------------------------------------------- Q and K producer
       if (lane == 0) {
         tma_prefetch_desc(&mapQ);
         tma_prefetch_desc(&mapK);
@@ -290,7 +319,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         for (int j = max(0, issued - KR); j < issued; ++j)
           wait_bar(&kfull[j % KR], (j / KR) & 1, p.status);
       }
-    } else if (warp == 9) {  // ------------------------------------ V producer
+    } else if (warp == 17) {  // ------------------------------------ V producer
       int issued = 0;
       if (lane == 0) {
         tma_prefetch_desc(&mapV);
@@ -320,80 +349,90 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(vtail);
       }
-    } else {  // ------------------------------------------------------ MMA issuers
-      const int t = warp - 10, mine = t ? nt1 : nt0;
-      if (lane == 0) {
-        const uint32_t id_s = idesc_bf16_f32(TM, TN);
-        const uint32_t id_o = idesc_bf16_f32(TM, 128) | (1u << 16);  // B (V) MN-major
-        const uint64_t qd = smem_desc_sw128(smem_u32(smem + (q_tiles == 2 ? t : 0) * TILE));
-        const uint64_t kd0 = smem_desc_sw128(smem_u32(kslots));
-        const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(vslots), HALF);
-        const uint32_t sc = tmem + (uint32_t)t * TN, oc = tmem + O_COL + (uint32_t)t * 128;
-        Ring kr(KR), vr(VR);
-        if (alt) {
-          kr.step(t);
-          vr.step(t);
-        }
-        const int stride = alt ? 2 : 1;
-        const int loops = alt ? mine : n_tiles;  // else: every slot is released here too
-        bool ok = wait_bar(qfull, 0, p.status);
-        // S_j, or just the release of K_j
-        auto score = [&](int j) {
-          if (ctl[1] || !wait_bar(&kfull[kr.slot], kr.phase, p.status)) return false;
-          if (j < mine) {
-            tc_fence_after();
-            const uint64_t kd = kd0 + (uint64_t)(kr.slot * (TILE >> 4));
+    } else if (warp == 18) {  // -------------------------------------- MMA issuer
+      // The whole warp walks the tiles and one elected lane issues, so slots,
+      // descriptors and addresses stay in uniform registers: from a branch that
+      // one lane takes alone, moving them there made an MMA's issue take some
+      // 100 cycles against the 64 of its work.
+      const uint32_t id_s = idesc_bf16_f32(TM, TN);
+      const uint32_t id_o = idesc_bf16_f32(TM, 128) | (1u << 16);  // B (V) MN-major
+      const uint64_t qd = smem_desc_sw128(smem_u32(smem));
+      const uint64_t kd0 = smem_desc_sw128(smem_u32(kslots));
+      const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(vslots), HALF);
+      const int stride = alt ? 2 : 1;
+      Ring kr[2] = {Ring(KR), Ring(KR)}, vr[2] = {Ring(VR), Ring(VR)};
+      if (alt) {
+        kr[1].step();
+        vr[1].step();
+      }
+      bool ok = __all_sync(0xffffffffu, wait_bar(qfull, 0, p.status));
+      // the reader that frees a slot: row tile 1, which sees every key tile, if
+      // it has any; an arrival covers the thread's earlier operations too
+      auto frees = [&](int t) { return alt || t == 1 || nt1 == 0; };
+      auto score = [&](int t) {  // S_t of the next key tile
+        const int slot = __shfl_sync(0xffffffffu, kr[t].slot, 0);
+        if (!__all_sync(0xffffffffu, wait_bar(&kfull[slot], kr[t].phase, p.status))) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t kd = kd0 + (uint64_t)(slot * (TILE >> 4));
+          const uint64_t q = qd + (uint64_t)(q_tiles == 2 ? t * (TILE >> 4) : 0);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 16 dims per MMA: 32 bytes of Q and K rows
-              tc_mma_f16(sc, qd + ((kk >> 2) * HALF + (kk & 3) * 32) / 16,
-                         kd + ((kk >> 2) * HALF + (kk & 3) * 32) / 16, id_s, kk > 0 ? 1u : 0u);
-            tc_commit(&sfull[t]);
-            tc_commit(&kempty[kr.slot]);
-          } else {
-            mbar_arrive(&kempty[kr.slot]);
-          }
-          kr.step(stride);
-          return true;
-        };
-        ok = ok && (loops == 0 || score(0));
-        for (int j = 0; ok && j < loops; ++j) {
-          if (ctl[1] || (j < mine && !wait_bar(&pready[t], j & 1, p.status)) ||
-              !wait_bar(&vfull[vr.slot], vr.phase, p.status)) {
-            ok = false;
-            break;
-          }
-          if (j < mine) {
-            const int tile = alt ? 2 * j + t : j;
-            if (tile == n_tiles - 1 && last_rows < TN && !wait_bar(vtail, 0, p.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t vd = vd0 + (uint64_t)(vr.slot * (TILE >> 4));
+          for (int kk = 0; kk < 8; ++kk)  // 16 dims per MMA: 32 bytes of Q and K rows
+            tc_mma_f16(tmem + (uint32_t)t * TN, q + ((kk >> 2) * HALF + (kk & 3) * 32) / 16,
+                       kd + ((kk >> 2) * HALF + (kk & 3) * 32) / 16, id_s, kk > 0 ? 1u : 0u);
+          tc_commit(&sfull[t]);
+          if (frees(t)) tc_commit(&kempty[slot]);
+        }
+        __syncwarp();
+        kr[t].step(stride);
+        return true;
+      };
+#pragma unroll
+      for (int t = 0; t < 2; ++t) ok = ok && ((t ? nt1 : nt0) == 0 || score(t));
+      const int loops = max(nt0, nt1);
+      for (int j = 0; ok && j < loops; ++j) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int count = t ? nt1 : nt0;
+          if (j >= count || !ok) continue;
+          const int slot = __shfl_sync(0xffffffffu, vr[t].slot, 0);
+          const bool go =
+              !ctl[1] && wait_bar(&vfull[slot], vr[t].phase, p.status) &&
+              !((alt ? 2 * j + t : j) == n_tiles - 1 && last_rows < TN && !wait_bar(vtail, 0, p.status)) &&
+              wait_bar(&pready[t], j & 1, p.status);
+          ok = __all_sync(0xffffffffu, go);  // the warp stays together
+          if (!ok) continue;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t vd = vd0 + (uint64_t)(slot * (TILE >> 4));
 #pragma unroll
             for (int kk = 0; kk < TN / 16; ++kk)  // 16 keys per MMA: 8 P columns, two 8-key V groups
-              tc_mma_f16_ts(oc, sc + 8u * kk, vd + kk * (2048 / 16), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-            tc_commit(&vempty[vr.slot]);
-          } else {
-            mbar_arrive(&vempty[vr.slot]);
+              tc_mma_f16_ts(tmem + O_COL + (uint32_t)t * 128,
+                            tmem + (uint32_t)t * TN + 64u * (kk >> 2) + 8u * (kk & 3),
+                            vd + kk * (2048 / 16), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+            if (frees(t)) tc_commit(&vempty[slot]);
+            if (j + 1 == count) tc_commit(&fin[t]);
           }
-          vr.step(stride);
-          if (j + 1 < loops && !score(j + 1)) {
-            ok = false;
-            break;
-          }
+          __syncwarp();
+          vr[t].step(stride);
+          if (j + 1 < count && !score(t)) ok = false;
         }
-        if (!ok) ctl[1] = 1;
-        tc_commit(&fin[t]);
-        wait_bar(&fin[t], 0, p.status);  // retired before the tensor memory is freed
       }
+      if (!ok) ctl[1] = 1;
+      if (elect_one()) tc_commit(drained);
+      __syncwarp();
+      wait_bar(drained, 0, p.status);  // retired before the tensor memory is freed
     }
   } else {  // ----------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int t = warp >> 2, quad = warp & 3;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    constexpr bool CAP = KIND == KCapFixed || KIND == KCap, BIAS = KIND == KBias || KIND == KCap;
+    const int t = warp >> 3, grp = (warp >> 2) & 1, quad = warp & 3;
     const int r = quad * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t sc = tl + (uint32_t)t * TN, oc = tl + O_COL + (uint32_t)t * 128;
+    // this thread's scores (then P: keys 64 grp .. at the same columns) and O dims
+    const uint32_t sc = tl + (uint32_t)(t * TN + 64 * grp), oc = tl + O_COL + (uint32_t)(t * 128 + 64 * grp);
+    float* xch = reinterpret_cast<float*>(smem + OFF_X) + t * 256 + r;
+    const int bar_id = 1 + t * 4 + quad;
     // this row: its position, its visible keys, where it goes
     bool row_ok;
     int pos, lim, head;
@@ -414,97 +453,186 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       row = s;
     }
     constexpr float kLog2e = 1.4426950408889634f;
-    // BIAS or CAP: sv in log2 units; else raw scores (the factor c is positive)
     const float c = p.scale * kLog2e;
-    const float zc = CAP ? 2.f * c / p.cap : 0.f, cl = p.cap * kLog2e;
-    const float sl = BIAS && row_ok ? p.slopes[head] * kLog2e : 0.f;
-    const float ce = (CAP || BIAS) ? 1.f : c;
-    float m = -INFINITY, l = 0.f;
+    const float cl = p.cap * kLog2e, yk = CAP ? p.scale / p.cap : 0.f;
+    const float sl = BIAS && p.slopes && row_ok ? p.slopes[head] * kLog2e : 0.f;
+    const f32x2 c2 = pair2(KIND == KCap ? cl : c, KIND == KCap ? cl : c), sl8[4] = {
+        pair2(0.f, sl), pair2(2.f * sl, 3.f * sl), pair2(4.f * sl, 5.f * sl), pair2(6.f * sl, 7.f * sl)};
+    float m = KIND == KCapFixed ? 0.f : -INFINITY, l = 0.f;
     bool ok = true;
     const int count = t ? nt1 : nt0;
     for (int j = 0; j < count; ++j) {
-      if (!__all_sync(0xffffffffu, !ctl[1] && wait_bar(&sfull[t], j & 1, p.status))) {
-        ok = false;
-        ctl[1] = 1;
-        break;
+      ok = ok && __all_sync(0xffffffffu, wait_bar(&sfull[t], j & 1, p.status));
+      if (!ok) {  // no more work, but the partner's barriers are kept
+        if (KIND != KCapFixed) half_bar(bar_id);
+        continue;
       }
       tc_fence_after();
-      const int k0 = (t0 + (alt ? 2 * j + t : j)) * TN;
-      float sv[TN];
+      const int k0 = (t0 + (alt ? 2 * j + t : j)) * TN + 64 * grp;  // this thread's first key
+      f32x2 x[32];
+      {
+        uint32_t u[64];
+        tmem_ld32(sc, u);
+        tmem_ld32(sc + 32, u + 32);
+        tmem_ld_wait();
 #pragma unroll
-      for (int q = 0; q < TN; q += 32) tmem_ld32(sc + q, reinterpret_cast<uint32_t*>(sv + q));
-      tmem_ld_wait();
+        for (int i = 0; i < 32; ++i) x[i] = pair2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+      }
+      const bool part = !__all_sync(0xffffffffu, lim >= k0 + 64);
+      // ---- scores: KPlain raw (x c later), else in log2 units
       if (CAP) {
+        // hidden keys and rows must not choose the path: they may hold anything,
+        // and the two paths differ in the last bits
+        if (part) {
 #pragma unroll
-        for (int i = 0; i < TN; ++i) sv[i] = fmaf(-2.f * cl, inv_1p_ex2(sv[i] * zc), cl);
+          for (int i = 0; i < 32; ++i) {
+            float a, b2;
+            unpair2(x[i], a, b2);
+            x[i] = pair2(k0 + 2 * i < lim ? a : 0.f, k0 + 2 * i + 1 < lim ? b2 : 0.f);
+          }
+        }
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float a, b2;
+          unpair2(x[i], a, b2);
+          big = max3(big, fabsf(a), fabsf(b2));
+        }
+        if (__all_sync(0xffffffffu, big * yk <= 1.f || !row_ok)) {
+          if (KIND == KCapFixed) {  // the coefficients hold scale, cap and log2e
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const f32x2 w = mul2(x[i], x[i]);
+              f32x2 q = pair2(p.poly[5], p.poly[5]);
+#pragma unroll
+              for (int d = 4; d >= 0; --d) q = fma2(q, w, pair2(p.poly[d], p.poly[d]));
+              x[i] = mul2(x[i], q);
+            }
+          } else {
+            const f32x2 yk2 = pair2(yk, yk);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const f32x2 y = mul2(x[i], yk2), w = mul2(y, y);
+              f32x2 q = pair2(p.poly[5], p.poly[5]);
+#pragma unroll
+              for (int d = 4; d >= 0; --d) q = fma2(q, w, pair2(p.poly[d], p.poly[d]));
+              x[i] = mul2(y, q);  // tanh; times cl with the bias below
+            }
+          }
+        } else {
+          const float zc = 2.f * c / p.cap, out = KIND == KCap ? 1.f : cl;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float a, b2;
+            unpair2(x[i], a, b2);
+            x[i] = pair2(cap_any(a, zc, out), cap_any(b2, zc, out));
+          }
+        }
       }
       if (BIAS) {
-        const float base = sl * (float)(k0 - pos);  // -slope (pos - key) at the tile's first key
+        // -slope (pos - key) log2e, exact to a rounding per group of 8 keys
+        const float base = sl * (float)(k0 - pos);
         // keys ahead of the row are visible only through a prefix
-        const bool ahead = DOCS && __any_sync(0xffffffffu, pre > pos && k0 + TN - 1 > pos);
+        if (DOCS && __any_sync(0xffffffffu, pre > pos && k0 + 63 > pos)) {
+          const float c1 = KIND == KCap ? cl : c;
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
-          float bias = fmaf(sl, (float)i, base);
-          if (ahead && k0 + i > pos) bias = -bias;
-          sv[i] = CAP ? sv[i] + bias : fmaf(sv[i], c, bias);
+          for (int i = 0; i < 32; ++i) {
+            float a, b2;
+            unpair2(x[i], a, b2);
+            const float d0 = (float)(k0 - pos + 2 * i), d1 = (float)(k0 - pos + 2 * i + 1);
+            x[i] = pair2(fmaf(-sl, fabsf(d0), a * c1), fmaf(-sl, fabsf(d1), b2 * c1));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float b8 = fmaf(sl, (float)(2 * i), base);
+            const f32x2 bb = pair2(b8, b8);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i + e] = fma2(x[i + e], c2, add2(bb, sl8[e]));
+          }
         }
       }
-      if (!__all_sync(0xffffffffu, lim >= k0 + TN)) {
+      if (part) {
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-          if (k0 + i >= lim) sv[i] = -INFINITY;
+        for (int i = 0; i < 32; ++i) {
+          float a, b2;
+          unpair2(x[i], a, b2);
+          x[i] = pair2(k0 + 2 * i < lim ? a : -INFINITY, k0 + 2 * i + 1 < lim ? b2 : -INFINITY);
+        }
       }
-      float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+      // ---- the row's maximum, and O rescaled when it grew
+      if (KIND != KCapFixed) {
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 4; i < TN; ++i) mx[i & 3] = fmaxf(mx[i & 3], sv[i]);
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ce;
-      const float m_new = fmaxf(m, mt);
-      const bool need = m_new > m + kLazy;  // also the first finite maximum
-      if (__any_sync(0xffffffffu, need && j > 0)) {
-        const float f = !need ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
+        for (int i = 0; i < 32; ++i) {
+          float a, b2;
+          unpair2(x[i], a, b2);
+          mx[i & 3] = max3(mx[i & 3], a, b2);
+        }
+        const float mh = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        xch[128 * grp] = mh;
+        half_bar(bar_id);
+        const float mt = fmaxf(mh, xch[128 * (grp ^ 1)]) * (KIND == KPlain ? c : 1.f);
+        const float m_new = fmaxf(m, mt);
+        const bool need = m_new > m + kLazy;  // also the first finite maximum
+        if (__any_sync(0xffffffffu, need && j > 0)) {
+          const float f = !need ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
 #pragma unroll 1
-        for (int q = 0; q < 128; q += 32) {
-          uint32_t u[32];
-          tmem_ld32(oc + q, u);
-          tmem_ld_wait();
+          for (int q = 0; q < 64; q += 16) {
+            uint32_t u[16];
+            tmem_ld16(oc + q, u);
+            tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
-          tmem_st32(oc + q, u);
+            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
+            tmem_st16(oc + q, u);
+          }
+          l *= f;
         }
-        l *= f;
+        if (need) m = m_new;
       }
-      if (need) m = m_new;
-      const float mu = m == -INFINITY ? 0.f : m;
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      // ---- weights, their sum, P over the scores
+      const float mu = m == -INFINITY ? 0.f : -m;
+      const f32x2 mu2 = pair2(mu, mu);
+      f32x2 ls[2] = {0ull, 0ull};
 #pragma unroll
-      for (int q = 0; q < TN; q += 32) {
+      for (int q = 0; q < 32; q += 16) {
         uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float e0 = ex2((CAP || BIAS) ? sv[q + i] - mu : fmaf(sv[q + i], c, -mu));
-          const float e1 = ex2((CAP || BIAS) ? sv[q + i + 1] - mu : fmaf(sv[q + i + 1], c, -mu));
-          ls[i & 2] += e0;
-          ls[(i & 2) + 1] += e1;
-          w[i / 2] = pack_bf16(e0, e1);
+        for (int i = 0; i < 16; ++i) {
+          f32x2 e = x[q + i];
+          if (KIND == KPlain) e = fma2(e, c2, mu2);
+          if (BIAS) e = add2(e, mu2);
+          float e0, e1;
+          unpair2(e, e0, e1);
+          e0 = ex2(e0);  // hidden keys: -inf -> 0
+          e1 = ex2(e1);
+          ls[i & 1] = add2(ls[i & 1], pair2(e0, e1));
+          w[i] = pack_bf16(e0, e1);
         }
-        tmem_st16(sc + q / 2, w);
+        tmem_st16(sc + q, w);
       }
-      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      float s0, s1;
+      unpair2(add2(ls[0], ls[1]), s0, s1);
+      l += s0 + s1;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&pready[t]);
     }
-    // ---- epilogue
+    // ---- epilogue: this thread's 64 dims; l of both halves
+    if (!ok) ctl[1] = 1;
     const bool done = __all_sync(0xffffffffu, ok && (count == 0 || wait_bar(&fin[t], 0, p.status)));
+    xch[128 * grp] = l;
+    half_bar(bar_id);
+    l = xch[0] + xch[128];
     if (done && !ctl[1]) {
       tc_fence_after();
       if (DOCS) {
         if (count > 0) {
           const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-          bf16* dst = p.out + (row * p.n_q + head) * 128;
+          bf16* dst = p.out + (row * p.n_q + head) * 128 + 64 * grp;
 #pragma unroll 1
-          for (int q = 0; q < 128; q += 32) {
+          for (int q = 0; q < 64; q += 32) {
             float u[32];
             tmem_ld32(oc + q, reinterpret_cast<uint32_t*>(u));
             tmem_ld_wait();
@@ -522,51 +650,68 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         const size_t at = (row * p.n_q + head) * p.splits + mine;
         if (count > 0) {
 #pragma unroll 1
-          for (int q = 0; q < 128; q += 32) {
+          for (int q = 0; q < 64; q += 32) {
             float u[32];
             tmem_ld32(oc + q, reinterpret_cast<uint32_t*>(u));
             tmem_ld_wait();
             if (row_ok) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(p.part_o + at * 128 + q + i) =
+                *reinterpret_cast<float4*>(p.part_o + at * 128 + 64 * grp + q + i) =
                     make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
             }
           }
         }
-        if (row_ok && (p.alternate || count > 0)) {  // a tile without keys: no mass
-          p.part_ml[2 * at] = count > 0 ? m : -INFINITY;
-          p.part_ml[2 * at + 1] = count > 0 ? l : 0.f;
+        if (row_ok && grp == 0 && (p.alternate || count > 0)) {  // no visible key: no mass
+          p.part_ml[2 * at] = l == 0.f ? -INFINITY : m;
+          p.part_ml[2 * at + 1] = l;
         }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 10) {
+  if (warp == 18) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <bool DOCS>
 using FormsKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
                              const CUtensorMap, const CUtensorMap, FormsParams);
 
 template <bool DOCS>
-FormsKernel<DOCS> forms_kernel(const ScoreArgs& s) {
-  if (s.cap > 0.f)
-    return s.slopes ? attn_forms_kernel<DOCS, true, true> : attn_forms_kernel<DOCS, true, false>;
-  return s.slopes ? attn_forms_kernel<DOCS, false, true> : attn_forms_kernel<DOCS, false, false>;
+FormsKernel forms_kernel(int kind) {
+  switch (kind) {
+    case KPlain: return attn_forms_kernel<DOCS, KPlain>;
+    case KBias: return attn_forms_kernel<DOCS, KBias>;
+    case KCapFixed: return attn_forms_kernel<DOCS, KCapFixed>;
+    default: return attn_forms_kernel<DOCS, KCap>;
+  }
+}
+
+// The kernel for these scores, and what it needs of them. KCapFixed scales the
+// polynomial's coefficients by powers of scale / cap up to the 11th, which
+// have to stay normal fp32 numbers, as have the powers of x up to cap / scale.
+int score_kind(const ScoreArgs& s, FormsParams* p) {
+  p->scale = s.scale;
+  p->cap = s.cap;
+  p->slopes = s.slopes;
+  if (!(s.cap > 0.f)) return s.slopes ? KBias : KPlain;
+  const double cl = (double)s.cap * 1.4426950408889634, k = (double)s.scale / s.cap;
+  for (int i = 0; i < 6; ++i) p->poly[i] = kTanh[i];
+  if (s.slopes || cl > kFixedCap || k < 1.0 / 512 || k > 8.0) return KCap;
+  double f = cl * k;
+  for (int i = 0; i < 6; ++i, f *= k * k) p->poly[i] = (float)(f * kTanh[i]);
+  return KCapFixed;
 }
 
 template <bool DOCS>
 cudaError_t prep() {
   for (int i = 0; i < 4; ++i) {
-    ScoreArgs s{1.f, i & 1 ? 1.f : 0.f, i & 2 ? reinterpret_cast<const float*>(16) : nullptr};
     const cudaError_t e = cudaFuncSetAttribute(
-        forms_kernel<DOCS>(s), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FORMS_SMEM);
+        forms_kernel<DOCS>(i), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FORMS_SMEM);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -585,9 +730,7 @@ cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st) {
   p.n_q = a.n_q;
   p.n_kv = a.n_kv;
   p.G = a.n_q / a.n_kv;
-  p.scale = a.sc.scale;
-  p.cap = a.sc.cap;
-  p.slopes = a.sc.slopes;
+  const int kind = score_kind(a.sc, &p);
   p.status = a.status;
   p.out = (bf16*)a.out;
   p.cu_rows = a.cu_rows;
@@ -597,7 +740,7 @@ cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st) {
   p.head_pairs = p.G % 2 == 0;
   const int rows = p.head_pairs ? TM : 2 * TM, per = p.head_pairs ? a.n_q / 2 : a.n_q;
   const long long tiles = a.n_rows / rows + (long long)std::min(a.n_docs, a.n_rows);  // an upper bound
-  return launch_k(forms_kernel<true>(a.sc), dim3((unsigned)(tiles * per)), dim3(FORMS_THREADS),
+  return launch_k(forms_kernel<true>(kind), dim3((unsigned)(tiles * per)), dim3(FORMS_THREADS),
                   FORMS_SMEM, st, 0, *a.map_q, *a.map_k, *a.map_v, *a.map_k, *a.map_v, p);
 }
 
@@ -607,9 +750,7 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
   p.n_q = a.n_q;
   p.n_kv = a.n_kv;
   p.G = a.n_q / a.n_kv;
-  p.scale = a.sc.scale;
-  p.cap = a.sc.cap;
-  p.slopes = a.sc.slopes;
+  const int kind = score_kind(a.sc, &p);
   p.status = a.status;
   p.positions = a.positions;
   p.page_table = a.page_table;
@@ -630,7 +771,7 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
   p.part_o = a.partial;
   p.part_ml = a.partial + s.partials * 128;
   p.splits = s.prefix_parts;
-  return launch_k(forms_kernel<false>(a.sc), dim3(s.prefix_splits, s.row_blocks, a.n_kv),
+  return launch_k(forms_kernel<false>(kind), dim3(s.prefix_splits, s.row_blocks, a.n_kv),
                   dim3(FORMS_THREADS), FORMS_SMEM, st, 0, *a.map_q, *a.map_k, *a.map_v, *a.map_k16,
                   *a.map_v16, p);
 }
