@@ -11,14 +11,16 @@
 //   warps 0-7, 8-15  softmax of row tile 0 and 1: two threads per row, one for
 //                    keys 0-63 of a tile and output dims 0-63, one for the rest;
 //   warp 16, 17      TMA producers of Q + K and of V (rings of 32 KB tiles);
-//   warp 18          one thread issues the MMAs.
-// It alternates between the row tiles, O += P_j V_j and S_{j+1} = Q K^T_{j+1} of
-// one and then of the other, so while one tile's softmax runs on the CUDA cores
-// the tensor cores work for the other (with an issuer per row tile the tensor
-// pipe interleaved the two, both softmaxes ran at the same time and the pipe
-// idled meanwhile). tcgen05 operations of one thread execute in order: P_j (bf16,
-// written over the scores it came from) is read before S_{j+1} replaces it, and
-// the arrival of S_{j+1} also says that O += P_j V_j is done. Tensor memory: per row
+//   warp 18, 19      issue the MMAs of row tile 0 and 1.
+// A turn of an issuer is O += P_j V_j, then S_{j+1} = Q K^T_{j+1}; the turns
+// alternate between the row tiles by tokens, so while one tile's softmax runs on
+// the CUDA cores the tensor cores work for the other. (Without the order the
+// tensor pipe interleaves the two tiles' MMAs, both softmaxes then run at the
+// same time, and the pipe idles meanwhile; with one issuer for both, its waits
+// between turns leave the pipe idle.) tcgen05 operations of one thread execute
+// in order: P_j (bf16, written over the scores it came from) is read before
+// S_{j+1} replaces it, and the arrival of S_{j+1} also says that O += P_j V_j is
+// done. Tensor memory: per row
 // tile 128 columns of S / P and 128 of O, all 512.
 // The two row tiles are
 //   documents, n_q / n_kv even : two query heads of one K/V head, same rows;
@@ -74,7 +76,7 @@ struct FormsParams {
   int key_limit, shared_len, shared_seq, tiles_per_split;
   float *part_o, *part_ml;                  // [B n_q][splits][128], [B n_q][splits][2] (max log2, sum)
   int splits;                               // partials of a row written here start at 0
-  float poly[6];                            // KCap: kTanh; KCapFixed: times powers of scale / cap
+  float poly[13];                           // KCapFixed: kTanh times powers of scale / cap
 };
 
 // What the scores need. A cap bounds them, so up to kFixedCap (log2 units) the
@@ -84,21 +86,18 @@ struct FormsParams {
 enum { KPlain, KBias, KCapFixed, KCap };
 constexpr float kFixedCap = 72.5f;  // caps up to 50
 
-// Bounded wait without a call, for code whose registers setmaxnreg resizes:
-// at most 2^20 tries of up to 2 us.
+// Bounded wait without a call (setmaxnreg leaves no registers for one); the
+// clock is read once every 64 tries.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t since = 0;
 #pragma unroll 1
-  for (int i = 0; i < (1 << 20); ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
-        : "memory");
-    if (ok) return true;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (since == 0) since = now;
+      if (now - since > kWaitLimitNs) break;
+    }
   }
   flag(status, LLAMA_FLAG_WAIT_TIMEOUT);
   return false;
@@ -165,13 +164,37 @@ __device__ __forceinline__ void load_tile(const FormsParams& p, const CUtensorMa
   }
 }
 
-// tanh(y) = y R(y^2) for |y| <= 1, R of degree 5: a weighted least-squares fit of
-// smallest relative error (5.9e-7 in fp64, 7e-7 evaluated in fp32). Six
-// multiply-adds on pairs replace an exponential and a reciprocal per score on
-// the special-function unit, which would bound the kernel (three
-// special-function results per score against one).
-constexpr float kTanh[6] = {0.9999994039535522f,   -0.3332904279232025f,  0.13281433284282684f,
-                            -0.051605671644210815f, 0.016743114218115807f, -0.0030670599080622196f};
+// tanh(y) = y R(y^2): weighted least-squares fits of smallest relative error
+// with 3 coefficients for |y| <= 1/4, 4 for 1/2 and 6 for 1 (below 7e-7 each,
+// evaluated in fp32). A warp takes the shortest that covers its scores: caps
+// are seldom approached. On the special-function unit a cap would cost an
+// exponential and a reciprocal per score beside the softmax's own exponential.
+constexpr float kTanh[13] = {
+    0.9999995827674866f, -0.33321908116340637f, 0.12841613590717316f,
+    0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f,
+    0.9999994039535522f, -0.3332904279232025f, 0.13281433284282684f, -0.051605671644210815f,
+    0.016743114218115807f, -0.0030670599080622196f};
+
+// x times the polynomial with N coefficients c[0..] in w. (Scalar: a pair
+// instruction, fma.rn.f32x2, occupies the FMA pipe for 4.4 cycles a warp,
+// measured, a scalar one for 1.2.)
+template <int N>
+__device__ __forceinline__ float odd_poly(float x, float w, const float* c) {
+  float q = c[N - 1];
+#pragma unroll
+  for (int d = N - 2; d >= 0; --d) q = fmaf(q, w, c[d]);
+  return x * q;
+}
+
+// Which fit covers a warp's scores x (in units of 1 / yk): 0, 1, 2, or 3 for none.
+template <int N>
+__device__ __forceinline__ int cap_level(const float* x, float yk) {
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) big = max3(big, fabsf(x[i]), fabsf(x[i + 1]));
+  big *= yk;
+  return __reduce_max_sync(0xffffffffu, (big > 0.25f) + (big > 0.5f) + (big > 1.f));
+}
 
 // cap tanh(x / cap) in log2 units for any x (in units of 1 / zc): cl (1 - 2 / (1 + e^2y))
 __device__ __forceinline__ float cap_any(float x, float zc, float cl) {
@@ -199,11 +222,12 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   uint64_t* vempty = vfull + MAXV;
   uint64_t* vtail = vempty + MAXV;  // the ragged last V tile has its absent rows zeroed
   uint64_t* sfull = vtail + 1;      // [2] S_j of row tile t is in tensor memory
-  uint64_t* pready = sfull + 2;     // [2] P_j is, and O is rescaled
-  uint64_t* fin = pready + 2;       // [2] the row tile's last O += P V is done
-  uint64_t* drained = fin + 2;      // every MMA is
-  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(drained + 1);  // tensor memory, abort
-  static_assert((1 + 2 * MAXK + 2 * MAXV + 1 + 7) * 8 + 8 <= 256, "barrier block");
+  uint64_t* pready = sfull + 2;     // [2][2] each part of P_j is, and O is rescaled
+  uint64_t* fin = pready + 4;       // [2] the row tile's last O += P V is done
+  uint64_t* token = fin + 2;        // [2] the row tile's next turn at the tensor pipe
+  uint64_t* drained = token + 2;    // [2] every MMA of the issuer is done
+  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(drained + 2);  // tensor memory, abort
+  static_assert((1 + 2 * MAXK + 2 * MAXV + 1 + 12) * 8 + 8 <= 256, "barrier block");
   grid_dep_wait();
   grid_dep_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -260,21 +284,24 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   if (DOCS) g = h0 / p.G;
 
   if (threadIdx.x == 0) {
+    const uint32_t readers = alt || nt1 == 0 ? 1 : 2;
     mbar_init(qfull, 1);
     for (int s = 0; s < MAXK; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+      mbar_init(&kempty[s], readers);
     }
     for (int s = 0; s < MAXV; ++s) {
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 1);
+      mbar_init(&vempty[s], readers);
     }
     mbar_init(vtail, 1);
-    mbar_init(drained, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
-      mbar_init(&pready[t], 8);
+      mbar_init(&pready[2 * t], 8);
+      mbar_init(&pready[2 * t + 1], 8);
       mbar_init(&fin[t], 1);
+      mbar_init(&token[t], 1);
+      mbar_init(&drained[t], 1);
     }
     ctl[1] = 0;
     fence_mbar_init();
@@ -349,88 +376,109 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(vtail);
       }
-    } else if (warp == 18) {  // -------------------------------------- MMA issuer
+    } else if ((warp == 18 ? nt0 : nt1) > 0) {  // -------------------- MMA issuers
       // The whole warp walks the tiles and one elected lane issues, so slots,
       // descriptors and addresses stay in uniform registers: from a branch that
       // one lane takes alone, moving them there made an MMA's issue take some
       // 100 cycles against the 64 of its work.
+      const int t = warp - 18;
+      const int count = t ? nt1 : nt0, others = t ? nt0 : nt1;
       const uint32_t id_s = idesc_bf16_f32(TM, TN);
       const uint32_t id_o = idesc_bf16_f32(TM, 128) | (1u << 16);  // B (V) MN-major
-      const uint64_t qd = smem_desc_sw128(smem_u32(smem));
+      const uint64_t qd = smem_desc_sw128(smem_u32(smem)) + (uint64_t)(q_tiles == 2 ? t * (TILE >> 4) : 0);
       const uint64_t kd0 = smem_desc_sw128(smem_u32(kslots));
       const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(vslots), HALF);
+      const uint32_t sc = tmem + (uint32_t)t * TN, oc = tmem + O_COL + (uint32_t)t * 128;
       const int stride = alt ? 2 : 1;
-      Ring kr[2] = {Ring(KR), Ring(KR)}, vr[2] = {Ring(VR), Ring(VR)};
+      Ring kr(KR), vr(VR);
       if (alt) {
-        kr[1].step();
-        vr[1].step();
+        kr.step(t);
+        vr.step(t);
       }
       bool ok = __all_sync(0xffffffffu, wait_bar(qfull, 0, p.status));
-      // the reader that frees a slot: row tile 1, which sees every key tile, if
-      // it has any; an arrival covers the thread's earlier operations too
-      auto frees = [&](int t) { return alt || t == 1 || nt1 == 0; };
-      auto score = [&](int t) {  // S_t of the next key tile
-        const int slot = __shfl_sync(0xffffffffu, kr[t].slot, 0);
-        if (!__all_sync(0xffffffffu, wait_bar(&kfull[slot], kr[t].phase, p.status))) return false;
+      auto score = [&]() {  // S of the next key tile
+        const int slot = __shfl_sync(0xffffffffu, kr.slot, 0);
+        if (!__all_sync(0xffffffffu, wait_bar(&kfull[slot], kr.phase, p.status))) return false;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t kd = kd0 + (uint64_t)(slot * (TILE >> 4));
-          const uint64_t q = qd + (uint64_t)(q_tiles == 2 ? t * (TILE >> 4) : 0);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // 16 dims per MMA: 32 bytes of Q and K rows
-            tc_mma_f16(tmem + (uint32_t)t * TN, q + ((kk >> 2) * HALF + (kk & 3) * 32) / 16,
+            tc_mma_f16(sc, qd + ((kk >> 2) * HALF + (kk & 3) * 32) / 16,
                        kd + ((kk >> 2) * HALF + (kk & 3) * 32) / 16, id_s, kk > 0 ? 1u : 0u);
           tc_commit(&sfull[t]);
-          if (frees(t)) tc_commit(&kempty[slot]);
+          tc_commit(&kempty[slot]);
         }
         __syncwarp();
-        kr[t].step(stride);
+        kr.step(stride);
         return true;
       };
+      ok = ok && score();
+      for (int j = 0; ok && j < count; ++j) {
+        const int slot = __shfl_sync(0xffffffffu, vr.slot, 0);
+        const bool tail = (alt ? 2 * j + t : j) == n_tiles - 1 && last_rows < TN;
+        const uint64_t vd = vd0 + (uint64_t)(slot * (TILE >> 4));
+        // 16 keys per MMA: 8 P columns, two 8-key V groups. P: keys 64 h .. at
+        // columns 64 h ..; the first part is keys 0-31 of both halves
+        auto add_pv = [&](int part, uint32_t acc) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) ok = ok && ((t ? nt1 : nt0) == 0 || score(t));
-      const int loops = max(nt0, nt1);
-      for (int j = 0; ok && j < loops; ++j) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int count = t ? nt1 : nt0;
-          if (j >= count || !ok) continue;
-          const int slot = __shfl_sync(0xffffffffu, vr[t].slot, 0);
-          const bool go =
-              !ctl[1] && wait_bar(&vfull[slot], vr[t].phase, p.status) &&
-              !((alt ? 2 * j + t : j) == n_tiles - 1 && last_rows < TN && !wait_bar(vtail, 0, p.status)) &&
-              wait_bar(&pready[t], j & 1, p.status);
-          ok = __all_sync(0xffffffffu, go);  // the warp stays together
-          if (!ok) continue;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t vd = vd0 + (uint64_t)(slot * (TILE >> 4));
-#pragma unroll
-            for (int kk = 0; kk < TN / 16; ++kk)  // 16 keys per MMA: 8 P columns, two 8-key V groups
-              tc_mma_f16_ts(tmem + O_COL + (uint32_t)t * 128,
-                            tmem + (uint32_t)t * TN + 64u * (kk >> 2) + 8u * (kk & 3),
-                            vd + kk * (2048 / 16), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-            if (frees(t)) tc_commit(&vempty[slot]);
-            if (j + 1 == count) tc_commit(&fin[t]);
+          for (int i = 0; i < 4; ++i) {
+            const int kk = 4 * (i >> 1) + 2 * part + (i & 1);
+            tc_mma_f16_ts(oc, sc + 64u * (kk >> 2) + 8u * (kk & 3), vd + kk * (2048 / 16), id_o,
+                          acc | (uint32_t)(i > 0));
           }
-          __syncwarp();
-          vr[t].step(stride);
-          if (j + 1 < count && !score(t)) ok = false;
+        };
+        ok = wait_bar(&vfull[slot], vr.phase, p.status) && (!tail || wait_bar(vtail, 0, p.status)) &&
+             wait_bar(&pready[2 * t], j & 1, p.status);
+        // the turn: after the other row tile's j-th, or (j - 1)-th for tile 0
+        const int before = t ? j : j - 1;
+        if (before >= 0 && before < others) ok = ok && wait_bar(&token[t], before & 1, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        // the first part of P while the softmax works on the second
+        if (elect_one()) add_pv(0, j > 0);
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, wait_bar(&pready[2 * t + 1], j & 1, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          add_pv(1, 1u);
+          tc_commit(&vempty[slot]);
+          if (j + 1 == count) tc_commit(&fin[t]);
         }
+        __syncwarp();
+        vr.step(stride);
+        if (j + 1 < count) ok = score();
+        if (lane == 0 && (t ? j + 1 : j) < others) mbar_arrive(&token[t ^ 1]);
       }
+      if (!alt && nt1 > 0)  // slots that only the other row tile reads
+        for (int j = count; ok && j < n_tiles; ++j) {
+          ok = __all_sync(0xffffffffu, wait_bar(&kfull[kr.slot], kr.phase, p.status) &&
+                                           wait_bar(&vfull[vr.slot], vr.phase, p.status));
+          if (ok && lane == 0) {
+            mbar_arrive(&kempty[kr.slot]);
+            mbar_arrive(&vempty[vr.slot]);
+          }
+          kr.step();
+          vr.step();
+        }
       if (!ok) ctl[1] = 1;
-      if (elect_one()) tc_commit(drained);
+      if (elect_one()) tc_commit(&drained[t]);
       __syncwarp();
-      wait_bar(drained, 0, p.status);  // retired before the tensor memory is freed
+      wait_bar(&drained[t], 0, p.status);  // retired before the tensor memory is freed
     }
   } else {  // ----------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const float kTanh3[3] = {kTanh[0], kTanh[1], kTanh[2]},
+                kTanh6[6] = {kTanh[7], kTanh[8], kTanh[9], kTanh[10], kTanh[11], kTanh[12]};
     constexpr bool CAP = KIND == KCapFixed || KIND == KCap, BIAS = KIND == KBias || KIND == KCap;
+    constexpr int NK = TN / 2;  // keys of a thread
     const int t = warp >> 3, grp = (warp >> 2) & 1, quad = warp & 3;
     const int r = quad * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-    // this thread's scores (then P: keys 64 grp .. at the same columns) and O dims
-    const uint32_t sc = tl + (uint32_t)(t * TN + 64 * grp), oc = tl + O_COL + (uint32_t)(t * 128 + 64 * grp);
+    // this thread's scores (then P at the same columns) and O dims
+    const uint32_t sc = tl + (uint32_t)(t * TN + NK * grp), oc = tl + O_COL + (uint32_t)(t * 128 + 64 * grp);
     float* xch = reinterpret_cast<float*>(smem + OFF_X) + t * 256 + r;
     const int bar_id = 1 + t * 4 + quad;
     // this row: its position, its visible keys, where it goes
@@ -456,8 +504,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     const float c = p.scale * kLog2e;
     const float cl = p.cap * kLog2e, yk = CAP ? p.scale / p.cap : 0.f;
     const float sl = BIAS && p.slopes && row_ok ? p.slopes[head] * kLog2e : 0.f;
-    const f32x2 c2 = pair2(KIND == KCap ? cl : c, KIND == KCap ? cl : c), sl8[4] = {
-        pair2(0.f, sl), pair2(2.f * sl, 3.f * sl), pair2(4.f * sl, 5.f * sl), pair2(6.f * sl, 7.f * sl)};
+    const float ct = KIND == KCap ? cl : c;  // log2 units of a raw score (of tanh)
     float m = KIND == KCapFixed ? 0.f : -INFINITY, l = 0.f;
     bool ok = true;
     const int count = t ? nt1 : nt0;
@@ -468,107 +515,63 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         continue;
       }
       tc_fence_after();
-      const int k0 = (t0 + (alt ? 2 * j + t : j)) * TN + 64 * grp;  // this thread's first key
-      f32x2 x[32];
-      {
-        uint32_t u[64];
-        tmem_ld32(sc, u);
-        tmem_ld32(sc + 32, u + 32);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = pair2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-      }
-      const bool part = !__all_sync(0xffffffffu, lim >= k0 + 64);
-      // ---- scores: KPlain raw (x c later), else in log2 units
+      const int k0 = (t0 + (alt ? 2 * j + t : j)) * TN + NK * grp;  // this thread's first key
+      const int left = lim - k0;                                    // visible keys (over NK: all)
+      float x[NK];
+      tmem_ld32(sc, reinterpret_cast<uint32_t*>(x));
+      tmem_ld32(sc + 32, reinterpret_cast<uint32_t*>(x + 32));
+      tmem_ld_wait();
+      const bool part = !__all_sync(0xffffffffu, left >= NK);
+      int level = 0;
       if (CAP) {
         // hidden keys and rows must not choose the path: they may hold anything,
-        // and the two paths differ in the last bits
+        // and the paths differ in the last bits
         if (part) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float a, b2;
-            unpair2(x[i], a, b2);
-            x[i] = pair2(k0 + 2 * i < lim ? a : 0.f, k0 + 2 * i + 1 < lim ? b2 : 0.f);
+          for (int i = 0; i < NK; ++i) x[i] = i < left ? x[i] : 0.f;
+        }
+        level = cap_level<NK>(x, row_ok ? yk : 0.f);
+      }
+      if (KIND == KCap) {  // tanh; times cl with the bias below
+        if (level == 0) {
+#pragma unroll
+          for (int i = 0; i < NK; ++i) {
+            const float y = x[i] * yk;
+            x[i] = odd_poly<3>(y, y * y, kTanh3);
           }
-        }
-        float big = 0.f;
+        } else if (level <= 2) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float a, b2;
-          unpair2(x[i], a, b2);
-          big = max3(big, fabsf(a), fabsf(b2));
-        }
-        if (__all_sync(0xffffffffu, big * yk <= 1.f || !row_ok)) {
-          if (KIND == KCapFixed) {  // the coefficients hold scale, cap and log2e
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const f32x2 w = mul2(x[i], x[i]);
-              f32x2 q = pair2(p.poly[5], p.poly[5]);
-#pragma unroll
-              for (int d = 4; d >= 0; --d) q = fma2(q, w, pair2(p.poly[d], p.poly[d]));
-              x[i] = mul2(x[i], q);
-            }
-          } else {
-            const f32x2 yk2 = pair2(yk, yk);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const f32x2 y = mul2(x[i], yk2), w = mul2(y, y);
-              f32x2 q = pair2(p.poly[5], p.poly[5]);
-#pragma unroll
-              for (int d = 4; d >= 0; --d) q = fma2(q, w, pair2(p.poly[d], p.poly[d]));
-              x[i] = mul2(y, q);  // tanh; times cl with the bias below
-            }
+          for (int i = 0; i < NK; ++i) {
+            const float y = x[i] * yk;
+            x[i] = odd_poly<6>(y, y * y, kTanh6);
           }
         } else {
-          const float zc = 2.f * c / p.cap, out = KIND == KCap ? 1.f : cl;
+          const float zc = 2.f * c / p.cap;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float a, b2;
-            unpair2(x[i], a, b2);
-            x[i] = pair2(cap_any(a, zc, out), cap_any(b2, zc, out));
-          }
+          for (int i = 0; i < NK; ++i) x[i] = cap_any(x[i], zc, 1.f);
         }
       }
-      if (BIAS) {
-        // -slope (pos - key) log2e, exact to a rounding per group of 8 keys
-        const float base = sl * (float)(k0 - pos);
-        // keys ahead of the row are visible only through a prefix
-        if (DOCS && __any_sync(0xffffffffu, pre > pos && k0 + 63 > pos)) {
-          const float c1 = KIND == KCap ? cl : c;
+      if (BIAS) {  // -slope |pos - key| log2e; keys ahead are visible only through a prefix
+        const int d0 = k0 - pos;
+        if (DOCS && __any_sync(0xffffffffu, pre > pos && d0 + NK - 1 > 0)) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float a, b2;
-            unpair2(x[i], a, b2);
-            const float d0 = (float)(k0 - pos + 2 * i), d1 = (float)(k0 - pos + 2 * i + 1);
-            x[i] = pair2(fmaf(-sl, fabsf(d0), a * c1), fmaf(-sl, fabsf(d1), b2 * c1));
-          }
+          for (int i = 0; i < NK; ++i) x[i] = fmaf(-sl, fabsf((float)(d0 + i)), x[i] * ct);
         } else {
+          const float base = sl * (float)d0;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float b8 = fmaf(sl, (float)(2 * i), base);
-            const f32x2 bb = pair2(b8, b8);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[i + e] = fma2(x[i + e], c2, add2(bb, sl8[e]));
-          }
+          for (int i = 0; i < NK; ++i) x[i] = fmaf(x[i], ct, fmaf(sl, (float)i, base));
         }
       }
-      if (part) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float a, b2;
-          unpair2(x[i], a, b2);
-          x[i] = pair2(k0 + 2 * i < lim ? a : -INFINITY, k0 + 2 * i + 1 < lim ? b2 : -INFINITY);
-        }
-      }
-      // ---- the row's maximum, and O rescaled when it grew
+      float mu = 0.f;
       if (KIND != KCapFixed) {
+        if (part) {
+#pragma unroll
+          for (int i = 0; i < NK; ++i) x[i] = i < left ? x[i] : -INFINITY;
+        }
+        // ---- the row's maximum, and O rescaled when it grew
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float a, b2;
-          unpair2(x[i], a, b2);
-          mx[i & 3] = max3(mx[i & 3], a, b2);
-        }
+        for (int i = 0; i < NK; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[i], x[i + 1]);
         const float mh = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         xch[128 * grp] = mh;
         half_bar(bar_id);
@@ -589,35 +592,47 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           l *= f;
         }
         if (need) m = m_new;
+        mu = m == -INFINITY ? 0.f : -m;
       }
       // ---- weights, their sum, P over the scores
-      const float mu = m == -INFINITY ? 0.f : -m;
-      const f32x2 mu2 = pair2(mu, mu);
-      f32x2 ls[2] = {0ull, 0ull};
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < 32; q += 16) {
+      for (int q = 0; q < NK; q += 32) {
+        if (KIND == KCapFixed) {  // the coefficients hold scale, cap and log2e
+          if (level == 0) {
+#pragma unroll
+            for (int i = q; i < q + 32; ++i) x[i] = odd_poly<3>(x[i], x[i] * x[i], p.poly);
+          } else if (level == 1) {
+#pragma unroll
+            for (int i = q; i < q + 32; ++i) x[i] = odd_poly<4>(x[i], x[i] * x[i], p.poly + 3);
+          } else if (level == 2) {
+#pragma unroll
+            for (int i = q; i < q + 32; ++i) x[i] = odd_poly<6>(x[i], x[i] * x[i], p.poly + 7);
+          } else {
+            const float zc = 2.f * c / p.cap;
+#pragma unroll
+            for (int i = q; i < q + 32; ++i) x[i] = cap_any(x[i], zc, cl);
+          }
+          if (part) {
+#pragma unroll
+            for (int i = q; i < q + 32; ++i) x[i] = i < left ? x[i] : -INFINITY;
+          }
+        }
         uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          f32x2 e = x[q + i];
-          if (KIND == KPlain) e = fma2(e, c2, mu2);
-          if (BIAS) e = add2(e, mu2);
-          float e0, e1;
-          unpair2(e, e0, e1);
-          e0 = ex2(e0);  // hidden keys: -inf -> 0
-          e1 = ex2(e1);
-          ls[i & 1] = add2(ls[i & 1], pair2(e0, e1));
-          w[i] = pack_bf16(e0, e1);
+        for (int i = 0; i < 32; ++i) {
+          const float e = x[q + i];
+          x[q + i] = ex2(KIND == KPlain ? fmaf(e, c, mu) : BIAS ? e + mu : e);  // -inf -> 0
+          ls[i & 3] += x[q + i];
+          if (i & 1) w[i / 2] = pack_bf16(x[q + i - 1], x[q + i]);
         }
-        tmem_st16(sc + q, w);
+        tmem_st16(sc + q / 2, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pready[2 * t + q / 32]);
       }
-      float s0, s1;
-      unpair2(add2(ls[0], ls[1]), s0, s1);
-      l += s0 + s1;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pready[t]);
+      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
     }
     // ---- epilogue: this thread's 64 dims; l of both halves
     if (!ok) ctl[1] = 1;
@@ -656,7 +671,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
             tmem_ld_wait();
             if (row_ok) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
+              for (int i = 0; i < TN / 2; i += 4)
                 *reinterpret_cast<float4*>(p.part_o + at * 128 + 64 * grp + q + i) =
                     make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
             }
@@ -700,10 +715,11 @@ int score_kind(const ScoreArgs& s, FormsParams* p) {
   p->slopes = s.slopes;
   if (!(s.cap > 0.f)) return s.slopes ? KBias : KPlain;
   const double cl = (double)s.cap * 1.4426950408889634, k = (double)s.scale / s.cap;
-  for (int i = 0; i < 6; ++i) p->poly[i] = kTanh[i];
   if (s.slopes || cl > kFixedCap || k < 1.0 / 512 || k > 8.0) return KCap;
-  double f = cl * k;
-  for (int i = 0; i < 6; ++i, f *= k * k) p->poly[i] = (float)(f * kTanh[i]);
+  for (int at = 0, n = 3; at < 13; at += n, n = n == 3 ? 4 : 6) {
+    double f = cl * k;
+    for (int i = 0; i < n; ++i, f *= k * k) p->poly[at + i] = (float)(f * kTanh[at + i]);
+  }
   return KCapFixed;
 }
 
