@@ -457,49 +457,49 @@ __global__ void __launch_bounds__(OWN_THREADS, 2)
     __syncthreads();
     const int n_tiles = (kend - kbeg + TILE_K - 1) / TILE_K;
     if (warp == 4) {  // ------------------------------------------------ producer
+      // The whole warp: lane i looks up the cache row of 16-key step i of the
+      // next 32 (one load for their page ids), and lanes 0-15 issue a tile's
+      // sixteen small boxes together.
       if (lane == 0) {
         tma_prefetch_desc(&mapK);
         tma_prefetch_desc(&mapV);
-        const uint64_t pol = l2_policy_evict_first();  // own keys are streamed once
-        int s = 0, issued = 0;
-        uint32_t ph = 1;
-        for (int t = 0; t < n_tiles; ++t) {
-          if (*stop || !mbar_wait(&empty[s], ph, p.status)) {
-            *stop = 1;
-            break;
-          }
-          const int k0 = kbeg + t * TILE_K;
-          const int j0 = max(0, p.first - k0) / SUB;                     // 16-key steps that
-          const int j1 = min(TILE_K / SUB, (kend - k0 + SUB - 1) / SUB);  // hold own keys
-          uint8_t* st = smem + s * STAGE;
-          if (p.box_rows == TILE_K && j0 == 0 && j1 == TILE_K / SUB) {
-            const int row = own_kv_row(p, b, g, k0);
-            mbar_arrive_expect_tx(&full[s], STAGE);
-            tma_load_3d_hint(st, &mapK, &full[s], 0, row, p.layer, pol);
-            tma_load_3d_hint(st + HALF, &mapK, &full[s], 64, row, p.layer, pol);
-            tma_load_3d_hint(st + 2 * HALF, &mapV, &full[s], 0, row, p.layer, pol);
-            tma_load_3d_hint(st + 3 * HALF, &mapV, &full[s], 64, row, p.layer, pol);
-          } else {
-            mbar_arrive_expect_tx(&full[s], (uint32_t)(j1 - j0) * 4 * SUB_HALF);
-            for (int j = j0; j < j1; ++j) {
-              const int row = own_kv_row(p, b, g, k0 + j * SUB);
-              uint8_t* d = st + j * SUB_HALF;
-              tma_load_3d_hint(d, &mapK16, &full[s], 0, row, p.layer, pol);
-              tma_load_3d_hint(d + HALF, &mapK16, &full[s], 64, row, p.layer, pol);
-              tma_load_3d_hint(d + 2 * HALF, &mapV16, &full[s], 0, row, p.layer, pol);
-              tma_load_3d_hint(d + 3 * HALF, &mapV16, &full[s], 64, row, p.layer, pol);
-            }
-          }
-          ++issued;
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1;
-          }
-        }
-        // no copy in flight when the CTA exits, whoever gave up
-        for (int t = max(0, issued - STAGES); t < issued; ++t)
-          mbar_wait(&full[t % STAGES], (t / STAGES) & 1, p.status);
       }
+      const uint64_t pol = l2_policy_evict_first();  // own keys are streamed once
+      const int n_steps = (kend - kbeg + SUB - 1) / SUB, first_step = max(0, p.first - kbeg) / SUB;
+      int s = 0, issued = 0, rows = 0;
+      uint32_t ph = 1;
+      for (int t = 0; t < n_tiles; ++t) {
+        if ((t & 7) == 0) {
+          const int step = 4 * t + lane;
+          rows = step >= first_step && step < n_steps ? own_kv_row(p, b, g, kbeg + step * SUB) : 0;
+        }
+        const bool go = !*stop && mbar_wait(&empty[s], ph, p.status);
+        if (!__all_sync(0xffffffffu, go)) {
+          *stop = 1;
+          break;
+        }
+        const int j0 = max(0, first_step - 4 * t), j1 = min(TILE_K / SUB, n_steps - 4 * t);
+        uint8_t* st = smem + s * STAGE;
+        const bool whole = p.box_rows == TILE_K && j0 == 0 && j1 == TILE_K / SUB;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[s], whole ? STAGE : (uint32_t)(j1 - j0) * 4 * SUB_HALF);
+        // lane = 4 * step + (K low dims, K high, V low, V high)
+        const int j = lane >> 2, part = lane & 3;
+        const int row = __shfl_sync(0xffffffffu, rows, (4 * (t & 7) + j) & 31);
+        uint8_t* d = st + part * HALF + j * SUB_HALF;
+        if (whole ? j == 0 : j >= j0 && j < j1) {
+          const CUtensorMap* m = whole ? (part < 2 ? &mapK : &mapV) : (part < 2 ? &mapK16 : &mapV16);
+          tma_load_3d_hint(d, m, &full[s], 64 * (part & 1), row, p.layer, pol);
+        }
+        ++issued;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      // no copy in flight when the CTA exits, whoever gave up
+      for (int t = max(0, issued - STAGES); t < issued; ++t)
+        mbar_wait(&full[t % STAGES], (t / STAGES) & 1, p.status);
       if (p.prefix_parts) grid_dep_wait();
       return;
     }
