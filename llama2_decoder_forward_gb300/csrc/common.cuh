@@ -257,6 +257,11 @@ __device__ __forceinline__ float4 dsmem_ld4(uint32_t addr) {
                : "r"(addr));
   return v;
 }
+__device__ __forceinline__ float2 dsmem_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
 
 // ------------------------------------------------------------------ programmatic dependent launch
 // Let the next kernel on the stream start launching (its CTAs run the part

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "../../include/llama_gb300.h"
 
 namespace llgb {
@@ -20,8 +22,8 @@ void set_pdl(bool on);
 bool pdl_enabled();
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                     cudaStream_t st, int cluster_z, Args&&... args) {
+cudaError_t launch_kc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                      cudaStream_t st, dim3 cluster, Args&&... args) {  // cluster.x 0: none
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -34,16 +36,23 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
     attr[n].val.programmaticStreamSerializationAllowed = 1;
     ++n;
   }
-  if (cluster_z > 0) {
+  if (cluster.x > 0) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = 1;
-    attr[n].val.clusterDim.y = 1;
-    attr[n].val.clusterDim.z = cluster_z;
+    attr[n].val.clusterDim.x = cluster.x;
+    attr[n].val.clusterDim.y = cluster.y;
+    attr[n].val.clusterDim.z = cluster.z;
     ++n;
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                     cudaStream_t st, int cluster_z, Args&&... args) {
+  return launch_kc(kernel, grid, block, smem, st,
+                   cluster_z > 0 ? dim3(1, 1, cluster_z) : dim3(0, 0, 0),
+                   std::forward<Args>(args)...);
 }
 
 // ------------------------------------------------------------------ RoPE + append
@@ -291,6 +300,7 @@ struct SharedPlan {
   int row_blocks, tiles_per_split, prefix_splits;
   int prefix_parts;     // partials per row of the prefix kernel (0: no prefix)
   int base, own_splits, keys_per_split;
+  int cluster;          // the own splits of a row form a thread-block cluster
   size_t partials;      // partial rows in all
 };
 SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, int sm_count);
