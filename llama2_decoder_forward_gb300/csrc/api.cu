@@ -1354,6 +1354,7 @@ int llama_op_attention_docs(llama_ctx* c, const void* q, const void* k, const vo
   a.cu_rows = cu_rows;
   a.prefix_len = prefix_len;
   a.status = c->status;
+  a.sm_count = c->sm_count;
   if (cf.dtype == LLAMA_BF16) {
     trim_maps(c);
     const uint64_t d = cf.head_dim, rows = n_rows;

@@ -272,6 +272,7 @@ struct DocsArgs {
   uint32_t* status;
   // tensor-core form: 3D {d, heads, rows}, box {64, 1, 128}, SW128
   const CUtensorMap *map_q = nullptr, *map_k = nullptr, *map_v = nullptr;
+  int sm_count = 152;
 };
 struct SharedArgs {
   const void* q;               // [B, n_q, d]

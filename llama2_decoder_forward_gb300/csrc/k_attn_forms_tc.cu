@@ -13,7 +13,7 @@
 //   warp 16, 17      TMA producers of Q + K and of V (rings of 32 KB tiles);
 //   warp 18, 19      issue the MMAs of row tile 0 and 1.
 // A turn of an issuer is O += P_j V_j, then S_{j+1} = Q K^T_{j+1}; the turns
-// alternate between the row tiles by tokens, so while one tile's softmax runs on
+// alternate between the row tiles by counts of them, so while one tile's softmax runs on
 // the CUDA cores the tensor cores work for the other. (Without the order the
 // tensor pipe interleaves the two tiles' MMAs, both softmaxes then run at the
 // same time, and the pipe idles meanwhile; with one issuer for both, its waits
@@ -28,7 +28,12 @@
 //   prefix, over 128 rows      : two blocks of (sequence, head of the group) rows;
 //   prefix, up to 128 rows     : the same rows; tile t takes every second key tile
 //                                (two key splits; each K/V tile has one reader).
-// so K and V are loaded once for both. Every mask here is "keys below a row's
+// so K and V are loaded once for both. Documents run as one CTA per SM that takes
+// gridDim-th part of the work items (tiles of a document from its end, heads of a tile
+// next to each other): its producers load the next item's Q, K and V while the
+// softmax and the store of the last one go on, and barriers and tensor memory
+// are set up once (17 packed documents of 8192 rows, 64 heads: 246 us with a CTA
+// per item, 216 us so). Every mask here is "keys below a row's
 // limit": max(position + 1, prefix) for documents, the sequence's keys for the
 // prefix. O is rescaled lazily, when a row's maximum grows by more than 2^8.
 // P is rounded once to bf16 (V's type, which the MMA shares); the sum that
@@ -87,20 +92,46 @@ enum { KPlain, KBias, KCapFixed, KCap };
 constexpr float kFixedCap = 72.5f;  // caps up to 50
 
 // Bounded wait without a call (setmaxnreg leaves no registers for one); the
-// clock is read once every 64 tries.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, uint32_t* status) {
+// clock and the abort flag are read once every 64 tries. False, and the flag
+// set for everyone, when the time is up.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile uint32_t* stop,
+                                         uint32_t* status) {
   uint64_t since = 0;
 #pragma unroll 1
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
     if ((i & 63) == 0) {
       const uint64_t now = globaltimer_ns();
       if (since == 0) since = now;
-      if (now - since > kWaitLimitNs) break;
+      if (*stop) return false;
+      if (now - since > kWaitLimitNs) {
+        *stop = 1;
+        flag(status, LLAMA_FLAG_WAIT_TIMEOUT);
+        return false;
+      }
     }
   }
-  flag(status, LLAMA_FLAG_WAIT_TIMEOUT);
-  return false;
+  return true;
+}
+// The same for the other issuer's turns to reach n. (An order for speed's sake:
+// what the MMAs read and write is guarded by the barriers.)
+__device__ __forceinline__ bool wait_turn(volatile uint32_t* turns, uint32_t n, volatile uint32_t* stop,
+                                          uint32_t* status) {
+  uint64_t since = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; (int32_t)(*turns - n) < 0; ++i) {
+    __nanosleep(20);  // polling steals issue slots from the softmax
+    if ((i & 63) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (since == 0) since = now;
+      if (*stop) return false;
+      if (now - since > kWaitLimitNs) {
+        *stop = 1;
+        flag(status, LLAMA_FLAG_WAIT_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
 }
 
 // Ring position: slot and phase parity of the n-th use.
@@ -130,38 +161,37 @@ __device__ __forceinline__ int forms_kv_row(const FormsParams& p, int b, int g, 
   return (page * p.n_kv + g) * p.page_size + (k0 - pi * p.page_size);
 }
 
+// Cache rows of a prefix's next four key tiles, one 16-key step per lane (tile
+// j + lane / 8, step lane % 8): looked up once per four tiles and ahead of the
+// wait for a free slot (a lookup per box in front of its copy held every tile
+// back by some 2000 cycles).
+__device__ __forceinline__ int tile_rows(const FormsParams& p, int g, int tile, int kmax, int lane) {
+  const int k0 = (tile + (lane >> 3)) * TN + (lane & 7) * 16;
+  return k0 < kmax ? forms_kv_row(p, p.shared_seq, g, k0) : 0;
+}
+
+// K or V tile of keys k0 .. k0 + nvalid - 1 by a whole warp, completing on bar.
+// Prefix: per 64 keys one box per dim half where the view has 64-row boxes and
+// the keys are all there, else 16-key boxes; rows as from tile_rows, j the tile.
 template <bool DOCS>
 __device__ __forceinline__ void load_tile(const FormsParams& p, const CUtensorMap* big,
                                           const CUtensorMap* m16, uint8_t* dst, uint64_t* bar, int g,
-                                          int rowbase, int k0, int nvalid) {
+                                          int rowbase, int k0, int nvalid, int rows, int j, int lane) {
   if (DOCS) {
-    mbar_arrive_expect_tx(bar, TILE);
-    tma_load_3d(dst, big, bar, 0, g, rowbase + k0);
-    tma_load_3d(dst + HALF, big, bar, 64, g, rowbase + k0);
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, TILE);
+      tma_load_3d(dst, big, bar, 0, g, rowbase + k0);
+      tma_load_3d(dst + HALF, big, bar, 64, g, rowbase + k0);
+    }
     return;
   }
-  uint32_t bytes = 0;
-  for (int rb = 0; rb < 2; ++rb) {
-    const int nv = min(64, nvalid - rb * 64);
-    if (nv > 0) bytes += (p.box_rows == 64 && nv == 64) ? 2 * 64 * 128 : 2 * ((nv + 15) / 16) * 16 * 128;
-  }
-  mbar_arrive_expect_tx(bar, bytes);
-  for (int rb = 0; rb < 2; ++rb) {
-    const int nv = min(64, nvalid - rb * 64);
-    if (nv <= 0) break;
-    uint8_t* d = dst + rb * 64 * 128;
-    if (p.box_rows == 64 && nv == 64) {
-      const int row = forms_kv_row(p, p.shared_seq, g, k0 + rb * 64);
-      tma_load_3d(d, big, bar, 0, row, p.layer);
-      tma_load_3d(d + HALF, big, bar, 64, row, p.layer);
-    } else {
-      for (int j = 0; j < (nv + 15) / 16; ++j) {
-        const int row = forms_kv_row(p, p.shared_seq, g, k0 + rb * 64 + 16 * j);
-        tma_load_3d(d + j * 16 * 128, m16, bar, 0, row, p.layer);
-        tma_load_3d(d + HALF + j * 16 * 128, m16, bar, 64, row, p.layer);
-      }
-    }
-  }
+  if (lane == 0) mbar_arrive_expect_tx(bar, 2 * ((nvalid + 15) / 16) * 16 * 128);
+  __syncwarp();
+  const int step = lane >> 1, half = lane & 1;  // lanes 0-15
+  const int row = __shfl_sync(0xffffffffu, rows, 8 * (j & 3) + (step & 7));
+  const bool whole = p.box_rows == 64 && nvalid - (step >> 2) * 64 >= 64;
+  if (step < 8 && step * 16 < nvalid && (!whole || (step & 3) == 0))
+    tma_load_3d(dst + half * HALF + step * 16 * 128, whole ? big : m16, bar, 64 * half, row, p.layer);
 }
 
 // tanh(y) = y R(y^2): weighted least-squares fits of smallest relative error
@@ -221,6 +251,57 @@ __device__ __forceinline__ void half_bar(int id) {  // the two warps that share 
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
 
+// One work item: its two row tiles and the key tiles that they visit.
+struct FormsWork {
+  int lo, n, q0, pre;   // documents: the document's rows [lo, lo + n), first query row, prefix
+  int g, h0;            // K/V head, query head of row tile 0
+  int t0, n_tiles;      // first key tile and how many
+  int kmax;             // keys below this exist for some row
+  int nt0, nt1;         // key tiles that row tile 0 / 1 visits
+  int split, seq0;      // prefix: key split, first sequence
+  int last_rows;        // keys of the last tile; over TN: all
+};
+// The CTA's it-th item; false: no more.
+template <bool DOCS>
+__device__ __forceinline__ bool forms_work(const FormsParams& p, int it, DocCursor& cursor, FormsWork& w) {
+  if (DOCS) {
+    const int per = p.head_pairs ? p.n_q / 2 : p.n_q, rows = p.head_pairs ? TM : 2 * TM;
+    // every other round backwards: items shrink along a document, and whoever
+    // had the longest of one round gets the shortest of the next
+    const long long item = (long long)it * gridDim.x + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    const int hx = (int)(item % per);
+    int b, tile;
+    if (!find_tile(p.cu_rows, p.n_docs, p.n_rows, rows, (int)(item / per), p.status, cursor, b, tile,
+                   w.lo, w.n))
+      return false;
+    w.q0 = tile * rows;
+    w.h0 = p.head_pairs ? 2 * hx : hx;
+    w.g = w.h0 / p.G;
+    w.pre = p.prefix_len ? min(max(p.prefix_len[b], 0), w.n) : 0;
+    const int last0 = max(min(w.q0 + TM, w.n), w.pre);
+    const int last1 = p.head_pairs ? last0 : w.q0 + TM < w.n ? max(min(w.q0 + 2 * TM, w.n), w.pre) : 0;
+    w.nt0 = (last0 + TN - 1) / TN;
+    w.nt1 = (last1 + TN - 1) / TN;
+    w.kmax = max(last0, last1);
+    w.n_tiles = max(w.nt0, w.nt1);
+    w.t0 = w.split = w.seq0 = 0;
+  } else {
+    if (it > 0) return false;
+    w.lo = w.n = w.q0 = w.pre = w.h0 = 0;
+    w.split = blockIdx.x;
+    w.g = blockIdx.z;
+    w.seq0 = blockIdx.y * p.rows_seq * (p.alternate ? 1 : 2);
+    w.t0 = w.split * p.tiles_per_split;
+    w.n_tiles = min(p.tiles_per_split, (p.shared_len + TN - 1) / TN - w.t0);
+    if (w.n_tiles <= 0) return false;
+    w.kmax = p.shared_len;
+    w.nt0 = p.alternate ? (w.n_tiles + 1) / 2 : w.n_tiles;
+    w.nt1 = p.alternate ? w.n_tiles / 2 : w.seq0 + p.rows_seq < p.B ? w.n_tiles : 0;
+  }
+  w.last_rows = w.kmax - (w.t0 + w.n_tiles - 1) * TN;
+  return true;
+}
+
 template <bool DOCS, int KIND>
 __global__ void __launch_bounds__(FORMS_THREADS, 1)
     attn_forms_kernel(const __grid_constant__ CUtensorMap mapQ,
@@ -230,18 +311,21 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
                       const __grid_constant__ CUtensorMap mapV16, FormsParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-  uint64_t* kfull = qfull + 1;
+  uint64_t* qempty = qfull + 1;
+  uint64_t* kfull = qempty + 1;
   uint64_t* kempty = kfull + MAXK;
   uint64_t* vfull = kempty + MAXK;
   uint64_t* vempty = vfull + MAXV;
-  uint64_t* vtail = vempty + MAXV;  // the ragged last V tile has its absent rows zeroed
-  uint64_t* sfull = vtail + 1;      // [2] S_j of row tile t is in tensor memory
+  uint64_t* vland = vempty + MAXV;  // a ragged last V tile is there; vfull follows when it is cleaned
+  uint64_t* sfull = vland + 1;      // [2] S_j of row tile t is in tensor memory
   uint64_t* pready = sfull + 2;     // [2][2] each part of P_j is, and O is rescaled
   uint64_t* fin = pready + 4;       // [2] the row tile's last O += P V is done
-  uint64_t* token = fin + 2;        // [2] the row tile's next turn at the tensor pipe
-  uint64_t* drained = token + 2;    // [2] every MMA of the issuer is done
-  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(drained + 2);  // tensor memory, abort
-  static_assert((1 + 2 * MAXK + 2 * MAXV + 1 + 12) * 8 + 8 <= 256, "barrier block");
+  uint64_t* drained = fin + 2;      // [2] every MMA of the issuer is done
+  // tensor memory, abort, and the turns at the tensor pipe that each issuer has
+  // had: counts, because a phase bit could be lapped
+  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(drained + 2);
+  volatile uint32_t* stop = ctl + 1;
+  static_assert((2 + 2 * MAXK + 2 * MAXV + 1 + 10) * 8 + 16 <= 256, "barrier block");
   grid_dep_wait();
   grid_dep_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -250,56 +334,15 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     if (threadIdx.x == 0) flag(p.status, LLAMA_FLAG_INDEX);
     return;
   }
-  // ---- what this CTA computes
-  int g, b = 0, lo = 0, n = 0, q0 = 0, pre = 0;   // documents: document b, its rows [lo, lo + n)
-  int t0 = 0, n_tiles;                            // first key tile and how many
-  int kmax;                                       // keys below this exist for some row
-  int nt0, nt1;                                   // key tiles that row tile 0 / 1 visits
-  int split = 0, seq0 = 0;
-  if (DOCS) {
-    const int per = p.head_pairs ? p.n_q / 2 : p.n_q;
-    const int hx = blockIdx.x % per;
-    int tile;
-    if (!find_tile(p.cu_rows, p.n_docs, p.n_rows, p.head_pairs ? TM : 2 * TM, blockIdx.x / per,
-                   p.status, b, tile, lo, n))
-      return;
-    q0 = tile * (p.head_pairs ? TM : 2 * TM);
-    g = hx;  // query head (pair) until the K/V head is known
-    pre = p.prefix_len ? min(max(p.prefix_len[b], 0), n) : 0;
-    const int last0 = max(min(q0 + TM, n), pre);
-    const int last1 = p.head_pairs ? last0 : q0 + TM < n ? max(min(q0 + 2 * TM, n), pre) : 0;
-    nt0 = (last0 + TN - 1) / TN;
-    nt1 = (last1 + TN - 1) / TN;
-    kmax = max(last0, last1);
-    n_tiles = max(nt0, nt1);
-  } else {
-    split = blockIdx.x;
-    g = blockIdx.z;
-    seq0 = blockIdx.y * p.rows_seq * (p.alternate ? 1 : 2);
-    t0 = split * p.tiles_per_split;
-    const int all = (p.shared_len + TN - 1) / TN;
-    n_tiles = min(p.tiles_per_split, all - t0);
-    if (n_tiles <= 0) return;
-    kmax = p.shared_len;
-    if (p.alternate) {
-      nt0 = (n_tiles + 1) / 2;
-      nt1 = n_tiles / 2;
-    } else {
-      nt0 = n_tiles;
-      nt1 = seq0 + p.rows_seq < p.B ? n_tiles : 0;
-    }
-  }
   const bool alt = !DOCS && p.alternate;
   const int KR = alt ? 4 : 3, VR = 2;  // even rings when each slot has one reader
-  const int q_tiles = alt || nt1 == 0 ? 1 : 2;
   uint8_t* kslots = smem + (alt ? 1 : 2) * TILE;
   uint8_t* vslots = kslots + KR * TILE;
-  const int h0 = DOCS ? (p.head_pairs ? 2 * g : g) : 0;  // documents: head of row tile 0
-  if (DOCS) g = h0 / p.G;
 
   if (threadIdx.x == 0) {
-    const uint32_t readers = alt || nt1 == 0 ? 1 : 2;
+    const uint32_t readers = alt ? 1 : 2;
     mbar_init(qfull, 1);
+    mbar_init(qempty, 2);
     for (int s = 0; s < MAXK; ++s) {
       mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], readers);
@@ -308,16 +351,15 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       mbar_init(&vfull[s], 1);
       mbar_init(&vempty[s], readers);
     }
-    mbar_init(vtail, 1);
+    mbar_init(vland, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
       mbar_init(&pready[2 * t], 8);
       mbar_init(&pready[2 * t + 1], 8);
       mbar_init(&fin[t], 1);
-      mbar_init(&token[t], 1);
       mbar_init(&drained[t], 1);
     }
-    ctl[1] = 0;
+    ctl[1] = ctl[2] = ctl[3] = 0;
     fence_mbar_init();
   }
   if (warp == 18) tmem_alloc(const_cast<uint32_t*>(ctl), 512);
@@ -325,96 +367,125 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl[0], 0);
-  const int last_rows = kmax - (t0 + n_tiles - 1) * TN;  // keys of the last tile; over 128: all
 
   // launched with 640 x 96 registers: 512 x 104 + 128 x 64
   if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    DocCursor cursor;
+    FormsWork w;
     if (warp == 16) {  // ------------------------------------------- Q and K producer
       if (lane == 0) {
         tma_prefetch_desc(&mapQ);
         tma_prefetch_desc(&mapK);
-        const uint32_t qbytes = DOCS ? TILE : (uint32_t)(p.rows_seq * p.G) * 256;
-        mbar_arrive_expect_tx(qfull, q_tiles * qbytes);
-        for (int t = 0; t < q_tiles; ++t)
-          for (int half = 0; half < 2; ++half) {
-            uint8_t* d = smem + t * TILE + half * HALF;
-            if (DOCS)
-              tma_load_3d(d, &mapQ, qfull, 64 * half, p.head_pairs ? h0 + t : h0,
-                          lo + q0 + (p.head_pairs ? 0 : t * TM));
-            else
-              tma_load_3d(d, &mapQ, qfull, 64 * half, g * p.G, seq0 + t * p.rows_seq);
-          }
-        Ring r(KR);
-        int issued = 0;
-        for (int j = 0; j < n_tiles; ++j, r.step()) {
-          if (ctl[1] || !wait_bar(&kempty[r.slot], r.phase ^ 1, p.status)) {
-            ctl[1] = 1;
-            break;
-          }
-          load_tile<DOCS>(p, &mapK, &mapK16, kslots + r.slot * TILE, &kfull[r.slot], g, lo,
-                          (t0 + j) * TN, min(TN, kmax - (t0 + j) * TN));
-          ++issued;
-        }
-        wait_bar(qfull, 0, p.status);  // no copy in flight when the CTA exits
-        for (int j = max(0, issued - KR); j < issued; ++j)
-          wait_bar(&kfull[j % KR], (j / KR) & 1, p.status);
       }
+      Ring r(KR);
+      int issued = 0, loaded_q = 0, rows = 0;
+      bool ok = true;
+      for (int it = 0; ok && forms_work<DOCS>(p, it, cursor, w); ++it) {
+        if (!DOCS) rows = tile_rows(p, w.g, w.t0, w.kmax, lane);
+        ok = __all_sync(0xffffffffu, wait_bar(qempty, (it & 1) ^ 1, stop, p.status));
+        if (!ok) break;
+        ++loaded_q;
+        if (lane == 0) {
+          const int q_tiles = alt || w.nt1 == 0 ? 1 : 2;
+          const uint32_t qbytes = DOCS ? TILE : (uint32_t)(p.rows_seq * p.G) * 256;
+          mbar_arrive_expect_tx(qfull, q_tiles * qbytes);
+          for (int t = 0; t < q_tiles; ++t)
+            for (int half = 0; half < 2; ++half) {
+              uint8_t* d = smem + t * TILE + half * HALF;
+              if (DOCS)
+                tma_load_3d(d, &mapQ, qfull, 64 * half, p.head_pairs ? w.h0 + t : w.h0,
+                            w.lo + w.q0 + (p.head_pairs ? 0 : t * TM));
+              else
+                tma_load_3d(d, &mapQ, qfull, 64 * half, w.g * p.G, w.seq0 + t * p.rows_seq);
+            }
+        }
+        for (int j = 0; j < w.n_tiles; ++j) {
+          if (!DOCS && j > 0 && (j & 3) == 0) rows = tile_rows(p, w.g, w.t0 + j, w.kmax, lane);
+          ok = __all_sync(0xffffffffu, wait_bar(&kempty[r.slot], r.phase ^ 1, stop, p.status));
+          if (!ok) break;
+          load_tile<DOCS>(p, &mapK, &mapK16, kslots + r.slot * TILE, &kfull[r.slot], w.g, w.lo,
+                          (w.t0 + j) * TN, min(TN, w.kmax - (w.t0 + j) * TN), rows, j, lane);
+          ++issued;
+          r.step();
+        }
+      }
+      // no copy in flight when the CTA exits
+      if (loaded_q) mbar_wait(qfull, (loaded_q - 1) & 1, p.status);
+      for (int j = max(0, issued - KR); j < issued; ++j)
+        mbar_wait(&kfull[j % KR], (j / KR) & 1, p.status);
     } else if (warp == 17) {  // ------------------------------------ V producer
+      if (lane == 0) tma_prefetch_desc(&mapV);
+      Ring r(VR);
       int issued = 0;
-      if (lane == 0) {
-        tma_prefetch_desc(&mapV);
-        Ring r(VR);
-        for (int j = 0; j < n_tiles; ++j, r.step()) {
-          if (ctl[1] || !wait_bar(&vempty[r.slot], r.phase ^ 1, p.status)) {
-            ctl[1] = 1;
-            break;
+      uint32_t ph_land = 0;
+      int rows = 0;
+      bool ok = true;
+      for (int it = 0; ok && forms_work<DOCS>(p, it, cursor, w); ++it) {
+        for (int j = 0; ok && j < w.n_tiles; ++j) {
+          if (!DOCS && (j & 3) == 0) rows = tile_rows(p, w.g, w.t0 + j, w.kmax, lane);
+          ok = __all_sync(0xffffffffu, wait_bar(&vempty[r.slot], r.phase ^ 1, stop, p.status));
+          if (!ok) break;
+          const bool ragged = j + 1 == w.n_tiles && w.last_rows < TN;
+          load_tile<DOCS>(p, &mapV, &mapV16, vslots + r.slot * TILE, ragged ? vland : &vfull[r.slot],
+                          w.g, w.lo, (w.t0 + j) * TN, min(TN, w.kmax - (w.t0 + j) * TN), rows, j, lane);
+          if (ragged) {
+            // V rows past the last key may hold anything, and 0 * NaN is not 0
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, wait_bar(vland, ph_land, stop, p.status));
+            ph_land ^= 1;
+            uint8_t* vt = vslots + r.slot * TILE;
+            const int nz = (TN - w.last_rows) * 16;
+            for (int i = lane; ok && i < nz; i += 32) {
+              const int row = w.last_rows + (i >> 4), half = (i >> 3) & 1, chunk = i & 7;
+              *reinterpret_cast<uint4*>(vt + half * HALF + row * 128 + chunk * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();  // the MMA reads V through the async proxy
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&vfull[r.slot]);
           }
-          load_tile<DOCS>(p, &mapV, &mapV16, vslots + r.slot * TILE, &vfull[r.slot], g, lo,
-                          (t0 + j) * TN, min(TN, kmax - (t0 + j) * TN));
-          ++issued;
+          if (ok) ++issued;
+          r.step();
         }
-        for (int j = max(0, issued - VR); j < issued; ++j)
-          wait_bar(&vfull[j % VR], (j / VR) & 1, p.status);
       }
-      issued = __shfl_sync(0xffffffffu, issued, 0);
-      if (issued == n_tiles && last_rows < TN) {
-        // V rows past the last key may hold anything, and 0 * NaN is not 0
-        uint8_t* vt = vslots + ((n_tiles - 1) % VR) * TILE;
-        const int nz = (TN - last_rows) * 16;
-        for (int i = lane; i < nz; i += 32) {
-          const int row = last_rows + (i >> 4), half = (i >> 3) & 1, chunk = i & 7;
-          *reinterpret_cast<uint4*>(vt + half * HALF + row * 128 + chunk * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();  // the MMA reads V through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vtail);
-      }
-    } else if ((warp == 18 ? nt0 : nt1) > 0) {  // -------------------- MMA issuers
+      for (int j = max(0, issued - VR); j < issued; ++j)
+        mbar_wait(&vfull[j % VR], (j / VR) & 1, p.status);
+    } else {  // ---------------------------------------------------- MMA issuers
       // The whole warp walks the tiles and one elected lane issues, so slots,
       // descriptors and addresses stay in uniform registers: from a branch that
       // one lane takes alone, moving them there made an MMA's issue take some
       // 100 cycles against the 64 of its work.
       const int t = warp - 18;
-      const int count = t ? nt1 : nt0, others = t ? nt0 : nt1;
       const uint32_t id_s = idesc_bf16_f32(TM, TN);
       const uint32_t id_o = idesc_bf16_f32(TM, 128) | (1u << 16);  // B (V) MN-major
-      const uint64_t qd = smem_desc_sw128(smem_u32(smem)) + (uint64_t)(q_tiles == 2 ? t * (TILE >> 4) : 0);
+      const uint64_t qd = smem_desc_sw128(smem_u32(smem)) + (uint64_t)(alt ? 0 : t * (TILE >> 4));
       const uint64_t kd0 = smem_desc_sw128(smem_u32(kslots));
       const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(vslots), HALF);
       const uint32_t sc = tmem + (uint32_t)t * TN, oc = tmem + O_COL + (uint32_t)t * 128;
+      // When a turn ends: plain scores, with its last MMA issued (the tensor pipe
+      // bounds them, and the hand-over passes while it executes); biased and
+      // capped ones, with S complete: their softmax is the longer part, and the
+      // further the row tiles are out of step the less the two share the CUDA
+      // cores. Measured, turn at issue and at completion: 2500 plain rows 47.6 and
+      // 52.7 us, 128 sequences over a prefix 180 and 184 us; packed biased
+      // documents 220 and 215 us, a capped prompt of 8192 rows 945 and 926 us.
+      constexpr bool LATE_TURN = KIND != KPlain;
       const int stride = alt ? 2 : 1;
       Ring kr(KR), vr(VR);
       if (alt) {
         kr.step(t);
         vr.step(t);
       }
-      bool ok = __all_sync(0xffffffffu, wait_bar(qfull, 0, p.status));
-      auto score = [&]() {  // S of the next key tile
-        const int slot = __shfl_sync(0xffffffffu, kr.slot, 0);
-        if (!__all_sync(0xffffffffu, wait_bar(&kfull[slot], kr.phase, p.status))) return false;
-        tc_fence_after();
-        if (elect_one()) {
+      uint32_t ph_p = 0, ph_s = 0;  // phases of pready, sfull
+      uint32_t mine = 0, theirs = 0;  // turns taken, and the other row tile's before this item
+      // No wait's outcome is looked at here (nor by the softmax): after an abort
+      // every wait returns at once, the rest runs on whatever is there, and
+      // nothing is stored. Checks and votes between the waits and the MMAs
+      // measured 5-15 % on all cases.
+      for (int it = 0; forms_work<DOCS>(p, it, cursor, w); ++it) {
+        const int count = t ? w.nt1 : w.nt0, others = t ? w.nt0 : w.nt1;
+        auto score = [&](int slot, bool last) {  // S of a key tile
           const uint64_t kd = kd0 + (uint64_t)(slot * (TILE >> 4));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // 16 dims per MMA: 32 bytes of Q and K rows
@@ -422,65 +493,86 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
                        kd + ((kk >> 2) * HALF + (kk & 3) * 32) / 16, id_s, kk > 0 ? 1u : 0u);
           tc_commit(&sfull[t]);
           tc_commit(&kempty[slot]);
-        }
-        __syncwarp();
-        kr.step(stride);
-        return true;
-      };
-      ok = ok && score();
-      for (int j = 0; ok && j < count; ++j) {
-        const int slot = __shfl_sync(0xffffffffu, vr.slot, 0);
-        const bool tail = (alt ? 2 * j + t : j) == n_tiles - 1 && last_rows < TN;
-        const uint64_t vd = vd0 + (uint64_t)(slot * (TILE >> 4));
-        // 16 keys per MMA: 8 P columns, two 8-key V groups. P: keys 64 h .. at
-        // columns 64 h ..; the first part is keys 0-31 of both halves
-        auto add_pv = [&](int part, uint32_t acc) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int kk = 4 * (i >> 1) + 2 * part + (i & 1);
-            tc_mma_f16_ts(oc, sc + 64u * (kk >> 2) + 8u * (kk & 3), vd + kk * (2048 / 16), id_o,
-                          acc | (uint32_t)(i > 0));
-          }
+          if (last) tc_commit(qempty);
         };
-        ok = wait_bar(&vfull[slot], vr.phase, p.status) && (!tail || wait_bar(vtail, 0, p.status)) &&
-             wait_bar(&pready[2 * t], j & 1, p.status);
-        // the turn: after the other row tile's j-th, or (j - 1)-th for tile 0
-        const int before = t ? j : j - 1;
-        if (before >= 0 && before < others) ok = ok && wait_bar(&token[t], before & 1, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        // the first part of P while the softmax works on the second
-        if (elect_one()) add_pv(0, j > 0);
-        __syncwarp();
-        ok = __all_sync(0xffffffffu, wait_bar(&pready[2 * t + 1], j & 1, p.status));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          add_pv(1, 1u);
-          tc_commit(&vempty[slot]);
-          if (j + 1 == count) tc_commit(&fin[t]);
+        wait_bar(qfull, it & 1, stop, p.status);
+        if (count > 0) {
+          const int slot = __shfl_sync(0xffffffffu, kr.slot, 0);
+          wait_bar(&kfull[slot], kr.phase, stop, p.status);
+          tc_fence_after();
+          if (elect_one()) score(slot, count == 1);
+          ph_s ^= 1;
+          kr.step(stride);
+        } else if (lane == 0) {
+          mbar_arrive(qempty);
         }
-        __syncwarp();
-        vr.step(stride);
-        if (j + 1 < count) ok = score();
-        if (lane == 0 && (t ? j + 1 : j) < others) mbar_arrive(&token[t ^ 1]);
-      }
-      if (!alt && nt1 > 0)  // slots that only the other row tile reads
-        for (int j = count; ok && j < n_tiles; ++j) {
-          ok = __all_sync(0xffffffffu, wait_bar(&kfull[kr.slot], kr.phase, p.status) &&
-                                           wait_bar(&vfull[vr.slot], vr.phase, p.status));
-          if (ok && lane == 0) {
-            mbar_arrive(&kempty[kr.slot]);
-            mbar_arrive(&vempty[vr.slot]);
+        for (int j = 0; j < count; ++j) {
+          // The issuer shares its scheduler with four softmax warps, so what it
+          // executes between a P and the MMAs is kept short: all other waits
+          // (V, the next K) come before P's.
+          const int slot = __shfl_sync(0xffffffffu, vr.slot, 0), next = __shfl_sync(0xffffffffu, kr.slot, 0);
+          const bool more = j + 1 < count;
+          const uint64_t vd = vd0 + (uint64_t)(slot * (TILE >> 4));
+          ++mine;
+          // 16 keys per MMA: 8 P columns, two 8-key V groups. P: keys 64 h .. at
+          // columns 64 h ..; the first part is keys 0-31 of both halves
+          auto add_pv = [&](int part, uint32_t acc) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int kk = 4 * (i >> 1) + 2 * part + (i & 1);
+              tc_mma_f16_ts(oc, sc + 64u * (kk >> 2) + 8u * (kk & 3), vd + kk * (2048 / 16), id_o,
+                            acc | (uint32_t)(i > 0));
+            }
+          };
+          wait_bar(&vfull[slot], vr.phase, stop, p.status);
+          if (more) wait_bar(&kfull[next], kr.phase, stop, p.status);
+          wait_bar(&pready[2 * t], ph_p, stop, p.status);
+          // the turn: after the other row tile's j-th, or (j - 1)-th for tile 0
+          // (last, when it has mostly come: this wait polls)
+          wait_turn(ctl + 2 + (t ^ 1), theirs + min(t ? j + 1 : j, others), stop, p.status);
+          tc_fence_after();
+          // the first part of P while the softmax works on the second
+          if (elect_one()) add_pv(0, j > 0);
+          wait_bar(&pready[2 * t + 1], ph_p, stop, p.status);
+          tc_fence_after();
+          if (elect_one()) {
+            add_pv(1, 1u);
+            tc_commit(&vempty[slot]);
+            if (more)
+              score(next, j + 2 == count);
+            else
+              tc_commit(&fin[t]);
+            if (!LATE_TURN || !more) ctl[2 + t] = mine;
           }
-          kr.step();
-          vr.step();
+          __syncwarp();
+          if (more) {
+            if (LATE_TURN) {
+              wait_bar(&sfull[t], ph_s, stop, p.status);
+              if (lane == 0) ctl[2 + t] = mine;
+            }
+            ph_s ^= 1;
+          }
+          ph_p ^= 1;
+          vr.step(stride);
+          if (more) kr.step(stride);
         }
-      if (!ok) ctl[1] = 1;
+        if (!alt)  // slots that only the other row tile reads
+          for (int j = count; j < w.n_tiles; ++j) {
+            wait_bar(&kfull[kr.slot], kr.phase, stop, p.status);
+            wait_bar(&vfull[vr.slot], vr.phase, stop, p.status);
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&kempty[kr.slot]);
+              mbar_arrive(&vempty[vr.slot]);
+            }
+            kr.step();
+            vr.step();
+          }
+        theirs += others;
+      }
       if (elect_one()) tc_commit(&drained[t]);
       __syncwarp();
-      wait_bar(&drained[t], 0, p.status);  // retired before the tensor memory is freed
+      mbar_wait(&drained[t], 0, p.status);  // retired before the tensor memory is freed
     }
   } else {  // ----------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
@@ -495,41 +587,44 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     const uint32_t sc = tl + (uint32_t)(t * TN + NK * grp), oc = tl + O_COL + (uint32_t)(t * 128 + 64 * grp);
     float* xch = reinterpret_cast<float*>(smem + OFF_X) + t * 256 + r;
     const int bar_id = 1 + t * 4 + quad;
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float c = p.scale * kLog2e;
+    const float cl = p.cap * kLog2e, yk = CAP ? p.scale / p.cap : 0.f;
+    const float ct = KIND == KCap ? cl : c;  // log2 units of a raw score (of tanh)
+    DocCursor cursor;
+    FormsWork w;
+    uint32_t ph_s = 0, ph_fin = 0;  // phases of sfull, fin
+#pragma unroll 1
+    for (int it = 0; forms_work<DOCS>(p, it, cursor, w); ++it) {
+    const int count = t ? w.nt1 : w.nt0;
+    if (DOCS && count == 0) continue;
     // this row: its position, its visible keys, where it goes
     bool row_ok;
     int pos, lim, head;
     size_t row;  // documents: packed row; prefix: sequence
+    const int pre = w.pre;
     if (DOCS) {
-      const int i = q0 + (p.head_pairs ? 0 : t * TM) + r;
-      row_ok = i < n;
+      const int i = w.q0 + (p.head_pairs ? 0 : t * TM) + r;
+      row_ok = i < w.n;
       pos = i;
-      lim = min(max(i + 1, pre), n);
-      head = p.head_pairs ? h0 + t : h0;
-      row = (size_t)lo + i;
+      lim = min(max(i + 1, pre), w.n);
+      head = p.head_pairs ? w.h0 + t : w.h0;
+      row = (size_t)w.lo + i;
     } else {
-      const int s = seq0 + (p.alternate ? 0 : t * p.rows_seq) + r / p.G;
+      const int s = w.seq0 + (p.alternate ? 0 : t * p.rows_seq) + r / p.G;
       row_ok = r < p.rows_seq * p.G && s < p.B;
       pos = row_ok ? p.positions[s] : 0;
       lim = row_ok ? min(min(max(pos + 1, 0), p.key_limit), p.shared_len) : 0;
-      head = g * p.G + r % p.G;
+      head = w.g * p.G + r % p.G;
       row = s;
     }
-    constexpr float kLog2e = 1.4426950408889634f;
-    const float c = p.scale * kLog2e;
-    const float cl = p.cap * kLog2e, yk = CAP ? p.scale / p.cap : 0.f;
     const float sl = BIAS && p.slopes && row_ok ? p.slopes[head] * kLog2e : 0.f;
-    const float ct = KIND == KCap ? cl : c;  // log2 units of a raw score (of tanh)
     float m = KIND == KCapFixed ? 0.f : -INFINITY, l = 0.f;
-    bool ok = true;
-    const int count = t ? nt1 : nt0;
     for (int j = 0; j < count; ++j) {
-      ok = ok && __all_sync(0xffffffffu, wait_bar(&sfull[t], j & 1, p.status));
-      if (!ok) {  // no more work, but the partner's barriers are kept
-        if (KIND != KCapFixed) half_bar(bar_id);
-        continue;
-      }
+      wait_bar(&sfull[t], ph_s, stop, p.status);
+      ph_s ^= 1;
       tc_fence_after();
-      const int k0 = (t0 + (alt ? 2 * j + t : j)) * TN + NK * grp;  // this thread's first key
+      const int k0 = (w.t0 + (alt ? 2 * j + t : j)) * TN + NK * grp;  // this thread's first key
       const int left = lim - k0;                                    // visible keys (over NK: all)
       const bool part = !__all_sync(0xffffffffu, left >= NK);
       float x[KIND == KCapFixed ? 1 : NK];
@@ -658,12 +753,15 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
     }
     // ---- epilogue: this thread's 64 dims; l of both halves
-    if (!ok) ctl[1] = 1;
-    const bool done = __all_sync(0xffffffffu, ok && (count == 0 || wait_bar(&fin[t], 0, p.status)));
+    if (count > 0) {
+      wait_bar(&fin[t], ph_fin, stop, p.status);
+      ph_fin ^= 1;
+    }
     xch[128 * grp] = l;
     half_bar(bar_id);
     l = xch[0] + xch[128];
-    if (done && !ctl[1]) {
+    half_bar(bar_id);  // both have read: the next item may write
+    if (!__any_sync(0xffffffffu, *stop)) {
       tc_fence_after();
       if (DOCS) {
         if (count > 0) {
@@ -684,7 +782,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           }
         }
       } else {
-        const int mine = p.alternate ? 2 * split + t : split;
+        const int mine = p.alternate ? 2 * w.split + t : w.split;
         const size_t at = (row * p.n_q + head) * p.splits + mine;
         if (count > 0) {
 #pragma unroll 1
@@ -706,6 +804,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         }
       }
     }
+    }  // items
   }
   tc_fence_before();
   __syncthreads();
@@ -779,8 +878,9 @@ cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st) {
   p.head_pairs = p.G % 2 == 0;
   const int rows = p.head_pairs ? TM : 2 * TM, per = p.head_pairs ? a.n_q / 2 : a.n_q;
   const long long tiles = a.n_rows / rows + (long long)std::min(a.n_docs, a.n_rows);  // an upper bound
-  return launch_k(forms_kernel<true>(kind), dim3((unsigned)(tiles * per)), dim3(FORMS_THREADS),
-                  FORMS_SMEM, st, 0, *a.map_q, *a.map_k, *a.map_v, *a.map_k, *a.map_v, p);
+  const unsigned grid = (unsigned)std::min<long long>(tiles * per, a.sm_count);
+  return launch_k(forms_kernel<true>(kind), dim3(grid), dim3(FORMS_THREADS), FORMS_SMEM, st, 0,
+                  *a.map_q, *a.map_k, *a.map_v, *a.map_k, *a.map_v, p);
 }
 
 cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaStream_t st) {
