@@ -1325,6 +1325,7 @@ int llama_op_rope_norm_append(llama_ctx* c, const void* qkv, int32_t qkv_dtype, 
   a.kv_fp8 = kv->kv_dtype == LLAMA_KV_E4M3;
   a.k_scale = kv->k_scale;
   a.v_scale = kv->v_scale;
+  a.sm_count = c->sm_count;
   Prof pf(c, LLAMA_KERNEL_ROPE_APPEND);
   c->launches++;
   return cuda_rc(launch_rope_norm_append(cf.dtype, qkv_dtype, a, c->stream));

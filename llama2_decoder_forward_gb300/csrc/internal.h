@@ -251,6 +251,7 @@ struct RopeNormArgs {
   int page_size, capacity, batch_cap, n_pages, max_pages;
   int kv_fp8;
   float k_scale, v_scale;
+  int sm_count;
 };
 cudaError_t launch_rope_norm_append(int dtype, int src_dtype, const RopeNormArgs& a,
                                     cudaStream_t st);

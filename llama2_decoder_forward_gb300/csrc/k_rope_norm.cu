@@ -57,29 +57,34 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seq, int r, 
 
 constexpr int RN_THREADS = 256;
 
-// grid: (chunks of RN_THREADS / lanes heads) x rows, flattened.
+// One block: `per_block` chunks of RN_THREADS / lanes heads of one row; grid:
+// blocks of a row, rows, flattened. What depends on the row alone (its sequence,
+// position, page) is a chain of dependent loads, so it is looked up once per
+// block, beside the first chunk's values, and the next chunk's values are
+// loaded before the current ones are used.
 template <typename S, typename T>
 __global__ void __launch_bounds__(RN_THREADS) rope_norm_append_kernel(RopeNormArgs a, int lanes,
-                                                                      int chunks) {
+                                                                      int chunks, int per_block) {
   grid_dep_wait();
   grid_dep_launch();
   const int d = a.head_dim, heads = a.n_q + 2 * a.n_kv;
-  const int r = blockIdx.x / chunks, chunk = blockIdx.x - r * chunks;
+  const int blocks = (chunks + per_block - 1) / per_block;
+  const int r = blockIdx.x / blocks, chunk0 = (blockIdx.x - r * blocks) * per_block;
+  const int step = RN_THREADS / lanes;  // heads of a chunk
   const int u = threadIdx.x & (lanes - 1);
-  const int head = chunk * (RN_THREADS / lanes) + threadIdx.x / lanes;
-  const bool on = head < heads && u < d / 8;
-  const bool is_v = head >= a.n_q + a.n_kv;
-  const bool turns = on && !is_v && u < a.rotary / 8;
+  const int head0 = chunk0 * step + threadIdx.x / lanes;
+  const int head_end = min(heads, (chunk0 + per_block) * step);
+  const bool unit = u < d / 8;
   int e0 = 8 * u, e1 = 8 * u + 4;
   if (a.half && u < a.rotary / 8) {
     e0 = 4 * u;
     e1 = a.rotary / 2 + 4 * u;
   }
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (on) {
-    const S* src = reinterpret_cast<const S*>(a.qkv) + (size_t)r * a.ld + (size_t)head * d;
-    load4(src + e0, v);
-    load4(src + e1, v + 4);
+  const S* src = reinterpret_cast<const S*>(a.qkv) + (size_t)r * a.ld;
+  float nx[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (unit && head0 < head_end) {
+    load4(src + (size_t)head0 * d + e0, nx);
+    load4(src + (size_t)head0 * d + e1, nx + 4);
   }
   // the row's sequence and position
   int b = r, pos;
@@ -91,82 +96,106 @@ __global__ void __launch_bounds__(RN_THREADS) rope_norm_append_kernel(RopeNormAr
     pos = a.start_pos[b];
   }
   const bool pos_ok = pos >= 0 && (a.rotary == 0 || pos < a.n_pos);
-  if (!pos_ok && chunk == 0 && threadIdx.x == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
-
-  const T* gain = reinterpret_cast<const T*>(is_v ? nullptr : head < a.n_q ? a.q_gain : a.k_gain);
-  if (a.q_gain || a.k_gain) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-    for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (on && gain) {
-      const float inv = 1.0f / sqrtf(ss / (float)d + a.eps);
-      float g[8];
-      load4(gain + e0, g);
-      load4(gain + e1, g + 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * g[i];
+  if (!pos_ok && chunk0 == 0 && threadIdx.x == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
+  // its cache slot, of K/V head 0 (the heads lie slot_step slots apart); -1: not cached
+  long long slot0 = -1;
+  const long long slot_step = a.page_size == 0 ? a.capacity : a.page_size;
+  if (pos_ok && head_end > a.n_q) {
+    uint32_t bad = 0;
+    if (a.page_size == 0) {
+      if (pos < a.capacity && b < a.batch_cap)
+        slot0 = ((long long)a.layer * a.batch_cap + b) * a.n_kv * a.capacity + pos;
+      else
+        bad = LLAMA_FLAG_POS_RANGE;
+    } else {
+      const int pi = pos / a.page_size;
+      if (pi < a.max_pages) {
+        const int page = a.page_table[(size_t)b * a.max_pages + pi];
+        if (page >= 0 && page < a.n_pages)
+          slot0 = ((long long)a.layer * a.n_pages + page) * a.n_kv * a.page_size + (pos - pi * a.page_size);
+        else
+          bad = LLAMA_FLAG_PAGE_RANGE;
+      } else {
+        bad = LLAMA_FLAG_POS_RANGE;
+      }
     }
+    if (bad && threadIdx.x == 0) flag(a.status, bad);
   }
-  if (!on) return;
-  if (!pos_ok) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  } else if (turns) {
+  // this thread's four angles: the same ones for every head
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+  const bool turns = u < a.rotary / 8;
+  if (turns && pos_ok) {
     const float4* cs4 = reinterpret_cast<const float4*>(a.table + (size_t)pos * (a.rotary / 2) + 4 * u);
     const float4 c01 = cs4[0], c23 = cs4[1];
-    const float c[4] = {c01.x, c01.z, c23.x, c23.z}, s[4] = {c01.y, c01.w, c23.y, c23.w};
+    c[0] = c01.x; c[1] = c01.z; c[2] = c23.x; c[3] = c23.z;
+    sn[0] = c01.y; sn[1] = c01.w; sn[2] = c23.y; sn[3] = c23.w;
+  }
+  const bool norms = a.q_gain || a.k_gain;
+#pragma unroll 1
+  for (int head = head0; head - head0 + chunk0 * step < head_end; head += step) {  // a block's trips are equal
+    float v[8];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int i0 = a.half ? p : 2 * p, i1 = a.half ? 4 + p : 2 * p + 1;
-      const float x0 = v[i0], x1 = v[i1];
-      v[i0] = x0 * c[p] - x1 * s[p];
-      v[i1] = x0 * s[p] + x1 * c[p];
+    for (int i = 0; i < 8; ++i) v[i] = nx[i];
+    const bool on = unit && head < head_end;
+    if (unit && head + step < head_end) {
+      load4(src + (size_t)(head + step) * d + e0, nx);
+      load4(src + (size_t)(head + step) * d + e1, nx + 4);
     }
-  }
-  if (head < a.n_q) {
-    T* dst = reinterpret_cast<T*>(a.q_out) + ((size_t)r * a.n_q + head) * d;
-    store4(dst + e0, v);
-    store4(dst + e1, v + 4);
-    return;
-  }
-  const int g = is_v ? head - a.n_q - a.n_kv : head - a.n_q;
-  if (void* side = is_v ? a.v_out : a.k_out) {
-    T* dst = reinterpret_cast<T*>(side) + ((size_t)r * a.n_kv + g) * d;
-    store4(dst + e0, v);
-    store4(dst + e1, v + 4);
-  }
-  if (!pos_ok) return;
-  size_t slot;
-  if (a.page_size == 0) {
-    if (pos >= a.capacity || b >= a.batch_cap) {
-      if (u == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
-      return;
+    const bool is_v = head >= a.n_q + a.n_kv;
+    if (norms) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+      if (!unit) ss = 0.f;
+      for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const T* gain = reinterpret_cast<const T*>(is_v ? nullptr : head < a.n_q ? a.q_gain : a.k_gain);
+      if (on && gain) {
+        const float inv = 1.0f / sqrtf(ss / (float)d + a.eps);
+        float g[8];
+        load4(gain + e0, g);
+        load4(gain + e1, g + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * g[i];
+      }
     }
-    slot = (((size_t)a.layer * a.batch_cap + b) * a.n_kv + g) * a.capacity + pos;
-  } else {
-    const int pi = pos / a.page_size;
-    if (pi >= a.max_pages) {
-      if (u == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
-      return;
+    if (!on) continue;
+    if (!pos_ok) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    } else if (turns && !is_v) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int i0 = a.half ? p : 2 * p, i1 = a.half ? 4 + p : 2 * p + 1;
+        const float x0 = v[i0], x1 = v[i1];
+        v[i0] = x0 * c[p] - x1 * sn[p];
+        v[i1] = x0 * sn[p] + x1 * c[p];
+      }
     }
-    const int page = a.page_table[(size_t)b * a.max_pages + pi];
-    if (page < 0 || page >= a.n_pages) {
-      if (u == 0) flag(a.status, LLAMA_FLAG_PAGE_RANGE);
-      return;
+    if (head < a.n_q) {
+      T* dst = reinterpret_cast<T*>(a.q_out) + ((size_t)r * a.n_q + head) * d;
+      store4(dst + e0, v);
+      store4(dst + e1, v + 4);
+      continue;
     }
-    slot = (((size_t)a.layer * a.n_pages + page) * a.n_kv + g) * a.page_size + (pos - pi * a.page_size);
-  }
-  void* cache = is_v ? a.v_cache : a.k_cache;
-  if (a.kv_fp8) {
-    uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + slot * d;
-    const float sc = is_v ? a.v_scale : a.k_scale;
-    *reinterpret_cast<uint32_t*>(dst + e0) = e4m3x4(v, sc);
-    *reinterpret_cast<uint32_t*>(dst + e1) = e4m3x4(v + 4, sc);
-  } else {
-    T* dst = reinterpret_cast<T*>(cache) + slot * d;
-    store4(dst + e0, v);
-    store4(dst + e1, v + 4);
+    const int g = is_v ? head - a.n_q - a.n_kv : head - a.n_q;
+    if (void* side = is_v ? a.v_out : a.k_out) {
+      T* dst = reinterpret_cast<T*>(side) + ((size_t)r * a.n_kv + g) * d;
+      store4(dst + e0, v);
+      store4(dst + e1, v + 4);
+    }
+    if (slot0 < 0) continue;
+    const size_t slot = (size_t)(slot0 + g * slot_step);
+    void* cache = is_v ? a.v_cache : a.k_cache;
+    if (a.kv_fp8) {
+      uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + slot * d;
+      const float sc = is_v ? a.v_scale : a.k_scale;
+      *reinterpret_cast<uint32_t*>(dst + e0) = e4m3x4(v, sc);
+      *reinterpret_cast<uint32_t*>(dst + e1) = e4m3x4(v + 4, sc);
+    } else {
+      T* dst = reinterpret_cast<T*>(cache) + slot * d;
+      store4(dst + e0, v);
+      store4(dst + e1, v + 4);
+    }
   }
 }
 
@@ -195,8 +224,12 @@ cudaError_t launch_rn(const RopeNormArgs& a, cudaStream_t st) {
   int lanes = 1;
   while (lanes * 8 < a.head_dim) lanes <<= 1;
   const int per = RN_THREADS / lanes, chunks = (a.n_q + 2 * a.n_kv + per - 1) / per;
-  return launch_k(rope_norm_append_kernel<S, T>, dim3((unsigned)((long long)chunks * a.n_rows)),
-                  dim3(RN_THREADS), 0, st, 0, a, lanes, chunks);
+  // few rows: a block per chunk (latency); many (a wave of 8 blocks per SM and
+  // more): a block per row
+  const int per_block = (long long)chunks * a.n_rows <= 8 * a.sm_count ? 1 : chunks;
+  const long long blocks = (long long)(chunks + per_block - 1) / per_block * a.n_rows;
+  return launch_k(rope_norm_append_kernel<S, T>, dim3((unsigned)blocks), dim3(RN_THREADS), 0, st, 0,
+                  a, lanes, chunks, per_block);
 }
 
 }  // namespace
