@@ -1367,7 +1367,7 @@ int llama_op_attention_docs(llama_ctx* c, const void* q, const void* k, const vo
   Prof pf(c, LLAMA_KERNEL_ATTN_PREFILL);
   c->launches++;
   return cuda_rc(cf.dtype == LLAMA_BF16 ? launch_docs_tc(a, c->stream)
-                                        : launch_docs_simt(cf.dtype, a, c->stream));
+                                        : launch_docs_simt(a, c->stream));
 }
 
 int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t* positions,
@@ -1414,7 +1414,7 @@ int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t*
   if (cf.dtype != LLAMA_BF16) {
     Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
     c->launches++;
-    return cuda_rc(launch_shared_simt(cf.dtype, a, c->stream));
+    return cuda_rc(launch_shared_simt(a, c->stream));
   }
   const SharedPlan plan =
       shared_plan(B, cf.n_q_heads, cf.n_kv_heads, limit, a.shared_len, c->sm_count);

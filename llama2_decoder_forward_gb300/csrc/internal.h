@@ -314,10 +314,10 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
 // own keys of a decode batch and the merge with its prefix (k_attn_own.cu)
 cudaError_t attn_own_prepare();
 cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStream_t st);
-// CUDA-core forms for any head_dim (k_attn_simt.cu)
+// fp32 on the CUDA cores, any head_dim (k_attn_simt.cu)
 cudaError_t attn_simt_prepare();
-cudaError_t launch_docs_simt(int dtype, const DocsArgs& a, cudaStream_t st);
-cudaError_t launch_shared_simt(int dtype, const SharedArgs& a, cudaStream_t st);
+cudaError_t launch_docs_simt(const DocsArgs& a, cudaStream_t st);
+cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st);
 
 // ---- token sampling (k_sample.cu)
 struct SampleCall {

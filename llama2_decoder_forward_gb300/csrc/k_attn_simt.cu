@@ -1,18 +1,20 @@
 // Attention with capped or biased scores on the CUDA cores, for fp32 models
-// and any head_dim up to 256: packed documents (two-way prefix, causal rest)
+// with any head_dim up to 256: packed documents (two-way prefix, causal rest)
 // and decode over a cache with a shared prefix.
 //
 //   x = scale q.k;  s = (cap tanh(x / cap) or x) - slope |i - j|;  softmax;  sum p v
 //
-// One CTA of 256 threads per (RT query rows, K/V source): documents take RT
-// rows of one head, decode the query heads of one K/V head and sequence.
-// Tiles of 64 keys pass through shared memory once; thread (ty, tx) computes
-// the scores of rows ty + 16 i and keys tx + 16 j, the row maxima and sums
-// are folded over the 16 threads of a row with butterflies (the running
-// maximum and sum of an online softmax, in fp32), P goes through shared
-// memory, and the same thread accumulates its rows' dims tx*4 + 64 m. Exact
-// fp32 arithmetic throughout (exp and tanh of the CUDA math library).
-// Bound by the fp32 FMA pipe and the shared-memory reads that feed it.
+// One CTA of 256 threads per (16 RI query rows, K/V source): documents take rows
+// of one head, decode the query heads of one K/V head and sequence. K and V
+// tiles of 64 keys come through shared memory with asynchronous copies, the
+// next tile's while the current one is used (two stages up to 128 dims).
+// Thread (ty, tx) computes the scores of rows ty + 16 i and keys tx + 16 j; the 16
+// threads of a row sit in one half-warp and fold its maximum and sum with
+// butterflies (the running maximum and sum of an online softmax, in fp32);
+// P goes through shared memory within the warp, and the same thread
+// accumulates its rows' dims 4 tx + 64 m. fp32 arithmetic throughout (exp and
+// tanh of the CUDA math library). Bound by the fp32 FMA pipe and, with 32-row
+// tiles, the shared-memory reads that feed it; with few tiles by their number.
 #include <algorithm>
 
 #include "attn_score.cuh"
@@ -25,10 +27,9 @@ namespace {
 constexpr int SK = 64;        // keys per tile
 constexpr int S_THREADS = 256;
 
-template <typename T>
 struct SimtParams {
-  const T *q, *k, *v;
-  T* out;
+  const float *q, *k, *v;
+  float* out;
   int n_q, n_kv, G, d;
   ScoreArgs sc;
   uint32_t* status;
@@ -38,13 +39,12 @@ struct SimtParams {
   // decode
   const int32_t *positions, *page_table;
   int layer, page_size, capacity, batch_cap, n_pages, max_pages, key_limit, shared_len, shared_seq;
-  int row_chunks;  // chunks of RT heads per K/V head
+  int row_chunks;  // chunks of 16 RI heads per K/V head
 };
 
 // Element offset of key j of sequence b, K/V head g in the cache; -1 (flagged)
 // for a page outside the pool.
-template <typename T>
-__device__ __forceinline__ long long key_offset(const SimtParams<T>& p, int b, int g, int j) {
+__device__ __forceinline__ long long key_offset(const SimtParams& p, int b, int g, int j) {
   if (j < p.shared_len) b = p.shared_seq;
   if (p.page_size == 0)
     return ((((long long)p.layer * p.batch_cap + b) * p.n_kv + g) * p.capacity + j) * p.d;
@@ -58,19 +58,36 @@ __device__ __forceinline__ long long key_offset(const SimtParams<T>& p, int b, i
          p.d;
 }
 
-// RT: query rows of a CTA (16 RI); DM: head_dim rounded up to 64, 128 or 256.
-template <typename T, int RI, int DM, bool DOCS>
-__global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams<T> p) {
+// 16 bytes global -> shared, or zeros
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int RI, int DM>
+struct SimtTile {  // DM: head_dim rounded up to 64, 128 or 256
+  static constexpr int RT = 16 * RI, LD = DM + 4, STAGES = DM <= 128 ? 2 : 1;
+  static constexpr size_t bytes =
+      (size_t)(RT * LD + STAGES * 2 * SK * LD + RT * (SK + 4)) * sizeof(float);
+};
+
+template <int RI, int DM, bool DOCS>
+__global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int RT = 16 * RI, LD = DM + 4;
+  using Tile = SimtTile<RI, DM>;
+  constexpr int RT = Tile::RT, LD = Tile::LD, ST = Tile::STAGES;
   extern __shared__ __align__(16) float sm[];
-  float* sq = sm;                // [RT][LD]
-  float* sk = sq + RT * LD;      // [SK][LD], K then V of a tile
-  float* sp = sk + SK * LD;      // [RT][SK + 4]
-  if (!bc_smem(sm, (uint32_t)((RT + SK) * LD + RT * (SK + 4)) * 4, 16,
-               threadIdx.x == 0 ? p.status : nullptr))
-    return;
+  float* sq = sm;                     // [RT][LD]
+  float* skv = sq + RT * LD;          // [ST][K, V][SK][LD]
+  float* sp = skv + ST * 2 * SK * LD; // [RT][SK + 4]
+  if (!bc_smem(sm, (uint32_t)Tile::bytes, 16, threadIdx.x == 0 ? p.status : nullptr)) return;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int d = p.d;
   // which rows
@@ -105,9 +122,25 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams<T> p) {
   auto row_off = [&](int r) -> size_t {
     return DOCS ? ((size_t)(lo + q0 + r) * p.n_q + h0) * d : ((size_t)b * p.n_q + h0 + r) * d;
   };
-  for (int i = threadIdx.x; i < RT * DM; i += S_THREADS) {
-    const int r = i / DM, x = i % DM;
-    sq[r * LD + x] = r < rows && x < d ? to_f32(p.q[row_off(r) + x]) : 0.f;
+  // K and V of the tile at k0; keys past n_keys and dims past d are zeros
+  auto load_tile = [&](int k0, int stage) {
+    float* dk = skv + stage * 2 * SK * LD;
+    for (int i = threadIdx.x; i < SK * (DM / 4); i += S_THREADS) {
+      const int j = i / (DM / 4), x = 4 * (i % (DM / 4));
+      long long off = -1;
+      if (k0 + j < n_keys && x < d)
+        off = DOCS ? ((long long)(lo + k0 + j) * p.n_kv + g) * d : key_offset(p, b, g, k0 + j);
+      copy16(dk + j * LD + x, off < 0 ? p.k : p.k + off + x, off >= 0);
+      copy16(dk + (SK + j) * LD + x, off < 0 ? p.v : p.v + off + x, off >= 0);
+    }
+    copies_commit();
+  };
+  if (n_keys > 0) load_tile(0, 0);
+  for (int i = threadIdx.x; i < RT * (DM / 4); i += S_THREADS) {
+    const int r = i / (DM / 4), x = 4 * (i % (DM / 4));
+    *reinterpret_cast<float4*>(sq + r * LD + x) =
+        r < rows && x < d ? *reinterpret_cast<const float4*>(p.q + row_off(r) + x)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   float slope[RI];
 #pragma unroll
@@ -123,25 +156,17 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams<T> p) {
 #pragma unroll
     for (int x = 0; x < DM / 16; ++x) o[i][x] = 0.f;
   }
-  auto load_tile = [&](const T* src, int k0) {  // keys past n_keys are zeros
-    for (int i = threadIdx.x; i < SK * (DM / 4); i += S_THREADS) {
-      const int j = i / (DM / 4), x = 4 * (i % (DM / 4));
-      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k0 + j < n_keys && x < d) {
-        const long long off = DOCS ? ((long long)(lo + k0 + j) * p.n_kv + g) * d
-                                   : key_offset(p, b, g, k0 + j);
-        if (off >= 0) {
-          const T* s = src + off + x;
-          w = make_float4(to_f32(s[0]), to_f32(s[1]), to_f32(s[2]), to_f32(s[3]));
-        }
-      }
-      *reinterpret_cast<float4*>(sk + j * LD + x) = w;
-    }
-  };
+  int stage = 0;
   for (int k0 = 0; k0 < n_keys; k0 += SK) {
+    if (ST == 2 && k0 + SK < n_keys) {
+      load_tile(k0 + SK, stage ^ 1);
+      copies_wait<1>();
+    } else {
+      copies_wait<0>();
+    }
     __syncthreads();
-    load_tile(p.k, k0);
-    __syncthreads();
+    const float* sk = skv + stage * 2 * SK * LD;
+    const float* sv = sk + SK * LD;
     float s[RI][4];
 #pragma unroll
     for (int i = 0; i < RI; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
@@ -188,26 +213,33 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams<T> p) {
 #pragma unroll
       for (int x = 0; x < DM / 16; ++x) o[i][x] *= f;
     }
-    __syncthreads();
-    load_tile(p.v, k0);
-    __syncthreads();
+    __syncwarp();  // a row's P is written and read by one half-warp
     const int nk = min(SK, n_keys - k0);
-    for (int j = 0; j < nk; ++j) {
-      float pr[RI];
+    // V rows past the last key are zeros, and so are their weights: whole fours
+    for (int j = 0; j < nk; j += 4) {
+      float4 pr[RI];
 #pragma unroll
-      for (int i = 0; i < RI; ++i) pr[i] = sp[(ty + 16 * i) * (SK + 4) + j];
+      for (int i = 0; i < RI; ++i) pr[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * (SK + 4) + j);
 #pragma unroll
-      for (int x = 0; x < DM / 64; ++x) {
-        const float4 vv = *reinterpret_cast<const float4*>(sk + j * LD + 4 * tx + 64 * x);
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int i = 0; i < RI; ++i) {
-          o[i][4 * x] = fmaf(pr[i], vv.x, o[i][4 * x]);
-          o[i][4 * x + 1] = fmaf(pr[i], vv.y, o[i][4 * x + 1]);
-          o[i][4 * x + 2] = fmaf(pr[i], vv.z, o[i][4 * x + 2]);
-          o[i][4 * x + 3] = fmaf(pr[i], vv.w, o[i][4 * x + 3]);
+        for (int x = 0; x < DM / 64; ++x) {
+          const float4 vv = *reinterpret_cast<const float4*>(sv + (j + q) * LD + 4 * tx + 64 * x);
+#pragma unroll
+          for (int i = 0; i < RI; ++i) {
+            const float w = q == 0 ? pr[i].x : q == 1 ? pr[i].y : q == 2 ? pr[i].z : pr[i].w;
+            o[i][4 * x] = fmaf(w, vv.x, o[i][4 * x]);
+            o[i][4 * x + 1] = fmaf(w, vv.y, o[i][4 * x + 1]);
+            o[i][4 * x + 2] = fmaf(w, vv.z, o[i][4 * x + 2]);
+            o[i][4 * x + 3] = fmaf(w, vv.w, o[i][4 * x + 3]);
+          }
         }
-      }
     }
+    __syncthreads();  // the stage may be overwritten
+    if (ST == 2)
+      stage ^= 1;
+    else if (k0 + SK < n_keys)
+      load_tile(k0 + SK, 0);
   }
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
@@ -216,55 +248,56 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams<T> p) {
     for (int w = 8; w > 0; w >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
     const int r = ty + 16 * i;
     if (r >= rows) continue;
-    T* dst = p.out + row_off(r);
+    float* dst = p.out + row_off(r);
 #pragma unroll
-    for (int x = 0; x < DM / 64; ++x)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int dim = 64 * x + 4 * tx + c;
-        if (dim < d) dst[dim] = from_f32<T>(n_keys > 0 ? o[i][4 * x + c] / lt : 0.f);
-      }
+    for (int x = 0; x < DM / 64; ++x) {
+      const int dim = 64 * x + 4 * tx;
+      if (dim >= d) continue;
+      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (n_keys > 0)
+        w = make_float4(o[i][4 * x] / lt, o[i][4 * x + 1] / lt, o[i][4 * x + 2] / lt, o[i][4 * x + 3] / lt);
+      *reinterpret_cast<float4*>(dst + dim) = w;
+    }
   }
 }
 
-template <int RI, int DM>
-constexpr size_t simt_smem() {
-  return (size_t)((16 * RI + SK) * (DM + 4) + 16 * RI * (SK + 4)) * sizeof(float);
-}
-
-template <typename T, int RI, bool DOCS>
+template <int RI, int DM, bool DOCS>
 cudaError_t prep() {
-  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, RI, 64, DOCS>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)simt_smem<RI, 64>());
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_simt_kernel<T, RI, 128, DOCS>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)simt_smem<RI, 128>());
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_simt_kernel<T, RI, 256, DOCS>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)simt_smem<RI, 256>());
-  return e;
+  return cudaFuncSetAttribute(attn_simt_kernel<RI, DM, DOCS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)SimtTile<RI, DM>::bytes);
 }
 
-template <typename T, int RI, bool DOCS>
-cudaError_t run(const SimtParams<T>& p, unsigned grid, cudaStream_t st) {
+template <int RI, bool DOCS>
+cudaError_t run(const SimtParams& p, unsigned grid, cudaStream_t st) {
   if (p.d <= 64)
-    return launch_k(attn_simt_kernel<T, RI, 64, DOCS>, dim3(grid), dim3(S_THREADS),
-                    simt_smem<RI, 64>(), st, 0, p);
+    return launch_k(attn_simt_kernel<RI, 64, DOCS>, dim3(grid), dim3(S_THREADS),
+                    SimtTile<RI, 64>::bytes, st, 0, p);
   if (p.d <= 128)
-    return launch_k(attn_simt_kernel<T, RI, 128, DOCS>, dim3(grid), dim3(S_THREADS),
-                    simt_smem<RI, 128>(), st, 0, p);
-  return launch_k(attn_simt_kernel<T, RI, 256, DOCS>, dim3(grid), dim3(S_THREADS),
-                  simt_smem<RI, 256>(), st, 0, p);
+    return launch_k(attn_simt_kernel<RI, 128, DOCS>, dim3(grid), dim3(S_THREADS),
+                    SimtTile<RI, 128>::bytes, st, 0, p);
+  return launch_k(attn_simt_kernel<RI, 256, DOCS>, dim3(grid), dim3(S_THREADS),
+                  SimtTile<RI, 256>::bytes, st, 0, p);
 }
 
-template <typename T>
-cudaError_t docs_simt(const DocsArgs& a, cudaStream_t st) {
-  SimtParams<T> p{};
-  p.q = (const T*)a.q;
-  p.k = (const T*)a.k;
-  p.v = (const T*)a.v;
-  p.out = (T*)a.out;
+}  // namespace
+
+cudaError_t attn_simt_prepare() {
+  cudaError_t (*const all[])() = {prep<4, 64, true>,  prep<4, 128, true>,  prep<4, 256, true>,
+                                  prep<2, 64, true>,  prep<2, 128, true>,  prep<2, 256, true>,
+                                  prep<1, 64, false>, prep<1, 128, false>, prep<1, 256, false>};
+  for (auto f : all) {
+    const cudaError_t e = f();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_docs_simt(const DocsArgs& a, cudaStream_t st) {
+  SimtParams p{};
+  p.q = (const float*)a.q;
+  p.k = (const float*)a.k;
+  p.v = (const float*)a.v;
+  p.out = (float*)a.out;
   p.n_q = a.n_q;
   p.n_kv = a.n_kv;
   p.G = a.n_q / a.n_kv;
@@ -275,17 +308,21 @@ cudaError_t docs_simt(const DocsArgs& a, cudaStream_t st) {
   p.prefix_len = a.prefix_len;
   p.n_rows = a.n_rows;
   p.n_docs = a.n_docs;
-  const long long tiles = a.n_rows / 64 + (long long)std::min(a.n_docs, a.n_rows);  // an upper bound
-  return run<T, 4, true>(p, (unsigned)(tiles * a.n_q), st);
+  // 64-row tiles feed the FMA pipe best; where they would leave SMs without work
+  // (fewer than two per SM), 32 rows (700 rows, 8 heads: 98 us with 64, 68 with
+  // 32, 71 with 16)
+  const long long docs = std::min(a.n_docs, a.n_rows);
+  auto tiles = [&](int rows) { return (a.n_rows / rows + docs) * a.n_q; };  // an upper bound
+  if (tiles(64) >= 2 * a.sm_count) return run<4, true>(p, (unsigned)tiles(64), st);
+  return run<2, true>(p, (unsigned)tiles(32), st);
 }
 
-template <typename T>
-cudaError_t shared_simt(const SharedArgs& a, cudaStream_t st) {
-  SimtParams<T> p{};
-  p.q = (const T*)a.q;
-  p.k = (const T*)a.k_cache;
-  p.v = (const T*)a.v_cache;
-  p.out = (T*)a.out;
+cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st) {
+  SimtParams p{};
+  p.q = (const float*)a.q;
+  p.k = (const float*)a.k_cache;
+  p.v = (const float*)a.v_cache;
+  p.out = (float*)a.out;
   p.n_q = a.n_q;
   p.n_kv = a.n_kv;
   p.G = a.n_q / a.n_kv;
@@ -304,24 +341,7 @@ cudaError_t shared_simt(const SharedArgs& a, cudaStream_t st) {
   p.shared_len = a.shared_len;
   p.shared_seq = a.shared_seq;
   p.row_chunks = (p.G + 15) / 16;
-  return run<T, 1, false>(p, (unsigned)((long long)a.B * a.n_kv * p.row_chunks), st);
-}
-
-}  // namespace
-
-cudaError_t attn_simt_prepare() {
-  cudaError_t e = prep<float, 4, true>();
-  if (e == cudaSuccess) e = prep<float, 1, false>();
-  if (e == cudaSuccess) e = prep<bf16, 4, true>();
-  if (e == cudaSuccess) e = prep<bf16, 1, false>();
-  return e;
-}
-
-cudaError_t launch_docs_simt(int dtype, const DocsArgs& a, cudaStream_t st) {
-  return dtype == LLAMA_F32 ? docs_simt<float>(a, st) : docs_simt<bf16>(a, st);
-}
-cudaError_t launch_shared_simt(int dtype, const SharedArgs& a, cudaStream_t st) {
-  return dtype == LLAMA_F32 ? shared_simt<float>(a, st) : shared_simt<bf16>(a, st);
+  return run<1, false>(p, (unsigned)((long long)a.B * a.n_kv * p.row_chunks), st);
 }
 
 }  // namespace llgb
