@@ -17,38 +17,33 @@ __device__ __forceinline__ void doc_rows(const int32_t* cu, int b, int n_rows, u
   if (lo != a || hi != e) flag(status, LLAMA_FLAG_POS_RANGE);
 }
 
-// Work items -> (document, tile of `rows` query rows, first row, row count), for a
-// whole warp that asks for items in ascending order: 32 documents per step,
-// their tile counts summed by a warp scan; the cursor keeps the step that the
-// last item was found in. Tiles of a document come last first (the longest
-// rows of a causal mask). False when the item is past the last document.
-struct DocCursor {
-  int b0 = 0, before = 0;  // first document of the step, tiles of the documents before it
-};
+// Work item -> (document, tile of `rows` query rows, first row, row count), for a
+// whole warp: 32 documents per step, their tile counts summed by a warp scan.
+// Tiles of a document come last first (the longest rows of a causal mask).
+// False when the item is past the last document's tiles.
 __device__ __forceinline__ bool find_tile(const int32_t* cu, int n_docs, int n_rows, int rows,
-                                          int item, uint32_t* status, DocCursor& c, int& b,
-                                          int& tile, int& lo, int& n) {
+                                          int item, uint32_t* status, int& b, int& tile, int& lo,
+                                          int& n) {
   const int lane = threadIdx.x & 31;
-  while (c.b0 < n_docs) {
+  for (int b0 = 0; b0 < n_docs; b0 += 32) {
     int my_lo = 0, my_n = 0;
-    if (c.b0 + lane < n_docs) doc_rows(cu, c.b0 + lane, n_rows, status, my_lo, my_n);
+    if (b0 + lane < n_docs) doc_rows(cu, b0 + lane, n_rows, status, my_lo, my_n);
     int upto = (my_n + rows - 1) / rows;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
-    const uint32_t m = __ballot_sync(0xffffffffu, item - c.before < upto);
+    const uint32_t m = __ballot_sync(0xffffffffu, item < upto);
     if (m) {
       const int w = __ffs(m) - 1;
-      b = c.b0 + w;
-      tile = __shfl_sync(0xffffffffu, upto, w) - 1 - (item - c.before);
+      b = b0 + w;
+      tile = __shfl_sync(0xffffffffu, upto, w) - 1 - item;
       lo = __shfl_sync(0xffffffffu, my_lo, w);
       n = __shfl_sync(0xffffffffu, my_n, w);
       return true;
     }
-    c.before += __shfl_sync(0xffffffffu, upto, 31);
-    c.b0 += 32;
+    item -= __shfl_sync(0xffffffffu, upto, 31);
   }
   return false;
 }

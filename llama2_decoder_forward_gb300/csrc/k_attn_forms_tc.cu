@@ -29,8 +29,7 @@
 //   prefix, up to 128 rows     : the same rows; tile t takes every second key tile
 //                                (two key splits; each K/V tile has one reader).
 // so K and V are loaded once for both. Documents run as one CTA per SM that takes
-// gridDim-th part of the work items (tiles of a document from its end, heads of a tile
-// next to each other): its producers load the next item's Q, K and V while the
+// gridDim-th part of the work items: its producers load the next item's Q, K and V while the
 // softmax and the store of the last one go on, and barriers and tensor memory
 // are set up once (17 packed documents of 8192 rows, 64 heads: 246 us with a CTA
 // per item, 216 us so). Every mask here is "keys below a row's
@@ -251,6 +250,76 @@ __device__ __forceinline__ void half_bar(int id) {  // the two warps that share 
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
 
+// The documents' work items in descending order of their key tiles, asked for in
+// ascending order by a whole warp. With C the key tiles of a causal item and P
+// those of the document's prefix, an item has max(C, P). Per count k and 32
+// documents, a lane knows how many items of its document have exactly k: with
+// tiles of 128 rows C = 1, 2, ..; with 256 rows C = 2, 4, .. and last the
+// document's own tile count. Longest first, dealt out in alternating order:
+// 17 packed documents end 1 % above the mean load (in the documents' order 13 %),
+// three with prefixes 13 % (61 %).
+struct DocCursor {
+  int k = -1, b0 = 0, before = 0;  // key tiles and first document of the step, items before it
+  int lo = 0, n = 0, P = 0;        // the lane's document of the step
+};
+__device__ __forceinline__ void cursor_load(const FormsParams& p, DocCursor& c, int lane) {
+  c.lo = c.n = c.P = 0;
+  if (c.b0 + lane < p.n_docs) {
+    doc_rows(p.cu_rows, c.b0 + lane, p.n_rows, p.status, c.lo, c.n);
+    const int pre = p.prefix_len ? min(max(p.prefix_len[c.b0 + lane], 0), c.n) : 0;
+    c.P = (pre + TN - 1) / TN;
+  }
+}
+__device__ __forceinline__ bool find_item(const FormsParams& p, int item, int per, DocCursor& c, int& b,
+                                          int& tile, int& lo, int& n, int& head) {
+  const int lane = threadIdx.x & 31;
+  if (c.k < 0) {
+    int most = 0;
+    for (c.b0 = 0; c.b0 < p.n_docs; c.b0 += 32) {
+      cursor_load(p, c, lane);
+      most = max(most, (c.n + TN - 1) / TN);
+    }
+    c.k = __reduce_max_sync(0xffffffffu, most);
+    c.b0 = 0;
+    cursor_load(p, c, lane);
+  }
+  while (c.k > 0) {
+    const int N = (c.n + TN - 1) / TN;  // key tiles of the whole document
+    int have = 0, first = 0;            // items with k key tiles, the first of them
+    if (c.k == c.P) {
+      have = p.head_pairs ? c.P : c.P >= N ? (N + 1) / 2 : c.P / 2;  // C up to P
+    } else if (c.k > c.P && c.k <= N) {
+      have = p.head_pairs || (c.k & 1) == 0 || c.k == N;
+      first = p.head_pairs ? c.k - 1 : (c.k + 1) / 2 - 1;
+    }
+    int upto = have;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, upto, 31);
+    if (item - c.before < total * per) {
+      const int i = (item - c.before) / per;
+      head = item - c.before - i * per;
+      const int w = __ffs(__ballot_sync(0xffffffffu, i < upto)) - 1;
+      b = c.b0 + w;
+      tile = __shfl_sync(0xffffffffu, first + i - (upto - have), w);
+      lo = __shfl_sync(0xffffffffu, c.lo, w);
+      n = __shfl_sync(0xffffffffu, c.n, w);
+      return true;
+    }
+    c.before += total * per;
+    c.b0 += 32;
+    if (c.b0 >= p.n_docs) {
+      c.b0 = 0;
+      --c.k;
+    }
+    if (p.n_docs > 32) cursor_load(p, c, lane);
+  }
+  return false;
+}
+
 // One work item: its two row tiles and the key tiles that they visit.
 struct FormsWork {
   int lo, n, q0, pre;   // documents: the document's rows [lo, lo + n), first query row, prefix
@@ -266,14 +335,12 @@ template <bool DOCS>
 __device__ __forceinline__ bool forms_work(const FormsParams& p, int it, DocCursor& cursor, FormsWork& w) {
   if (DOCS) {
     const int per = p.head_pairs ? p.n_q / 2 : p.n_q, rows = p.head_pairs ? TM : 2 * TM;
-    // every other round backwards: items shrink along a document, and whoever
-    // had the longest of one round gets the shortest of the next
+    // every other round backwards: whoever had the longest item of one round
+    // gets the shortest of the next
     const long long item = (long long)it * gridDim.x + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    const int hx = (int)(item % per);
-    int b, tile;
-    if (!find_tile(p.cu_rows, p.n_docs, p.n_rows, rows, (int)(item / per), p.status, cursor, b, tile,
-                   w.lo, w.n))
-      return false;
+    if (item >= 0x7fffffffll) return false;
+    int b, tile, hx;
+    if (!find_item(p, (int)item, per, cursor, b, tile, w.lo, w.n, hx)) return false;
     w.q0 = tile * rows;
     w.h0 = p.head_pairs ? 2 * hx : hx;
     w.g = w.h0 / p.G;

@@ -95,9 +95,7 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
   if (DOCS) {
     const int h = blockIdx.x % p.n_q;
     int tile;
-    DocCursor cursor;
-    if (!find_tile(p.cu_rows, p.n_docs, p.n_rows, RT, blockIdx.x / p.n_q, p.status, cursor, b, tile,
-                   lo, n))
+    if (!find_tile(p.cu_rows, p.n_docs, p.n_rows, RT, blockIdx.x / p.n_q, p.status, b, tile, lo, n))
       return;
     h0 = h;
     g = h / p.G;
