@@ -246,6 +246,24 @@ __device__ __forceinline__ float cap_any(float x, float zc, float cl) {
   return fmaf(-2.f * cl, r, cl);
 }
 
+// Scores of keys from `left` on replaced.
+template <int N>
+__device__ __forceinline__ void hide(float* x, int left, float with) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = i < left ? x[i] : with;
+}
+
+// a = a c + m, b likewise, as one pair instruction: half the issue slots, which
+// bound plain scores more than the FMA pipe (per 64 scores and four warps per
+// scheduler 1335 cycles with two scalar ones, 1112 with the pair)
+__device__ __forceinline__ void fma_pair(float& a, float& b, float c, float m) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(m));
+}
+
 __device__ __forceinline__ void half_bar(int id) {  // the two warps that share 32 rows
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
@@ -694,19 +712,18 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       const int k0 = (w.t0 + (alt ? 2 * j + t : j)) * TN + NK * grp;  // this thread's first key
       const int left = lim - k0;                                    // visible keys (over NK: all)
       const bool part = !__all_sync(0xffffffffu, left >= NK);
+      // a warp that sees none of the tile's keys (above the diagonal): its weights are 0
+      const bool none = !__any_sync(0xffffffffu, left > 0);
       float x[KIND == KCapFixed ? 1 : NK];
       if (KIND != KCapFixed) {
         tmem_ld32(sc, reinterpret_cast<uint32_t*>(x));
         tmem_ld32(sc + 32, reinterpret_cast<uint32_t*>(x + 32));
         tmem_ld_wait();
       }
-      if (KIND == KCap) {
+      if (KIND == KCap && !none) {
         // hidden keys and rows must not choose the path: they may hold anything,
         // and the paths differ in the last bits
-        if (part) {
-#pragma unroll
-          for (int i = 0; i < NK; ++i) x[i] = i < left ? x[i] : 0.f;
-        }
+        if (part) hide<NK>(x, left, 0.f);
         const int level = cap_level<NK>(x, row_ok ? yk : 0.f);  // tanh; times cl with the bias below
         if (level == 0) {
 #pragma unroll
@@ -720,27 +737,44 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           for (int i = 0; i < NK; ++i) x[i] = cap_any(x[i], zc, 1.f);
         }
       }
-      if (BIAS) {  // -slope |pos - key| log2e; keys ahead are visible only through a prefix
+      // The bias, -slope (pos - key) log2e = base + sb i, joins a score in the exponent.
+      // The reference of the weights need not be the row's maximum, only near and
+      // not below it: each 8 keys count with their largest score and their
+      // largest bias. Not so where 8 keys' biases are far apart (steep slopes) or
+      // keys ahead of a row are visible (a prefix, |pos - key|): there the scores
+      // are biased here, and factor 1, base 0, step 0 remain.
+      float cb = ct, sb = sl, base = BIAS ? sl * (float)(k0 - pos) : 0.f;
+      if (BIAS && !none) {
         const int d0 = k0 - pos;
-        if (DOCS && __any_sync(0xffffffffu, pre > pos && d0 + NK - 1 > 0)) {
+        const bool ahead = DOCS && __any_sync(0xffffffffu, pre > pos && d0 + NK - 1 > 0);
+        if (ahead || __any_sync(0xffffffffu, fabsf(sl) > 2.f)) {
 #pragma unroll
-          for (int i = 0; i < NK; ++i) x[i] = fmaf(-sl, fabsf((float)(d0 + i)), x[i] * ct);
-        } else {
-          const float base = sl * (float)d0;
-#pragma unroll
-          for (int i = 0; i < NK; ++i) x[i] = fmaf(x[i], ct, fmaf(sl, (float)i, base));
+          for (int i = 0; i < NK; ++i) {
+            const float dist = (float)(d0 + i);
+            x[i] = fmaf(sl, ahead ? -fabsf(dist) : dist, x[i] * ct);
+          }
+          cb = 1.f;
+          sb = base = 0.f;
         }
       }
       float mu = 0.f;
       if (KIND != KCapFixed) {
-        if (part) {
-#pragma unroll
-          for (int i = 0; i < NK; ++i) x[i] = i < left ? x[i] : -INFINITY;
-        }
+        if (part && !none) hide<NK>(x, left, -INFINITY);
         // ---- the row's maximum, and O rescaled when it grew
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (none) {
+        } else if (BIAS) {
+          const float top = base + fmaxf(0.f, 7.f * sb);
 #pragma unroll
-        for (int i = 0; i < NK; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[i], x[i + 1]);
+          for (int i = 0; i < NK; i += 8) {
+            const float a = max3(max3(x[i], x[i + 1], x[i + 2]), x[i + 3], x[i + 4]);
+            const float m8 = max3(a, fmaxf(x[i + 5], x[i + 6]), x[i + 7]);
+            mx[(i >> 3) & 3] = fmaxf(mx[(i >> 3) & 3], fmaf(m8, cb, fmaf(sb, (float)i, top)));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NK; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[i], x[i + 1]);
+        }
         const float mh = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         xch[128 * grp] = mh;
         half_bar(bar_id);
@@ -767,11 +801,21 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       float ls[4] = {0.f, 0.f, 0.f, 0.f};
       auto weigh = [&](float* y, int q) {  // y: the scores of keys q .. q + 31
         uint32_t w[16];
+        const float bmu = base + mu;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          y[i] = ex2(KIND == KPlain ? fmaf(y[i], c, mu) : BIAS ? y[i] + mu : y[i]);  // -inf -> 0
-          ls[i & 3] += y[i];
-          if (i & 1) w[i / 2] = pack_bf16(y[i - 1], y[i]);
+        for (int i = 0; i < 32; i += 2) {
+          float e0 = y[i], e1 = y[i + 1];
+          if (KIND == KPlain) {
+            fma_pair(e0, e1, c, mu);
+          } else if (BIAS) {
+            e0 = fmaf(e0, cb, fmaf(sb, (float)(q + i), bmu));
+            e1 = fmaf(e1, cb, fmaf(sb, (float)(q + i + 1), bmu));
+          }
+          e0 = ex2(e0);  // hidden: -inf -> 0
+          e1 = ex2(e1);
+          ls[i & 2] += e0;
+          ls[(i & 2) + 1] += e1;
+          w[i / 2] = pack_bf16(e0, e1);
         }
         tmem_st16(sc + q / 2, w);
         tmem_st_wait();
@@ -779,7 +823,18 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[2 * t + q / 32]);
       };
-      if (KIND == KCapFixed) {
+      if (none) {
+        const uint32_t zero[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        tmem_st16(sc, zero);
+        tmem_st16(sc + 16, zero);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&pready[2 * t]);
+          mbar_arrive(&pready[2 * t + 1]);
+        }
+      } else if (KIND == KCapFixed) {
         // scores straight from tensor memory, 32 at a time in a rolled loop
 #pragma unroll 1
         for (int q = 0; q < NK; q += 32) {
@@ -788,10 +843,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           tmem_ld_wait();
           // hidden keys and rows must not choose the path: they may hold
           // anything, and the paths differ in the last bits
-          if (part) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = q + i < left ? y[i] : 0.f;
-          }
+          if (part) hide<32>(y, left - q, 0.f);
           const int level = cap_level<32>(y, row_ok ? yk : 0.f);
           if (level == 0) {  // the coefficients hold scale, cap and log2e
 #pragma unroll
@@ -807,10 +859,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = cap_any(y[i], zc, cl);
           }
-          if (part) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = q + i < left ? y[i] : -INFINITY;
-          }
+          if (part) hide<32>(y, left - q, -INFINITY);
           weigh(y, q);
         }
       } else {
