@@ -282,14 +282,14 @@ class Scores:
         self._ref = ctypes.byref(self._c)
 
 
-def _need(what, t, dtype, shape):
+def _need(what, t, dtype, n):
     """The tensor's address; ValueError unless it is a contiguous tensor of that
     type and element count on the device."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != shape:
-        raise ValueError("%s: want a contiguous device tensor of %d %s, got %s %s%s" %
-                         (what, shape, dtype, tuple(t.shape), t.dtype,
-                          "" if t.is_contiguous() else " (strided)"))
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("%s: want a contiguous device tensor of %d %s, got %s %s%s%s" %
+                     (what, n, dtype, tuple(t.shape), t.dtype, "" if t.is_cuda else " on the CPU",
+                      "" if t.is_contiguous() else " (strided)"))
 
 
 class KVCache:
@@ -320,6 +320,19 @@ class KVCache:
         self.k = k if k is not None else torch.zeros(full, dtype=dt, device=device)
         self.v = v if v is not None else torch.zeros(full, dtype=dt, device=device)
         assert tuple(self.k.shape) == full and tuple(self.v.shape) == full
+        self._c = self.struct()
+        self._ref = ctypes.byref(self._c)
+
+    def _now(self):
+        """The kept C struct (the layout is fixed at construction) with the tensors'
+        present addresses and the scales."""
+        c = self._c
+        c.k = self.k.data_ptr()
+        c.v = self.v.data_ptr()
+        c.k_scale, c.v_scale = self.k_scale, self.v_scale
+        if self.page_table is not None:
+            c.page_table = self.page_table.data_ptr()
+        return self._ref
 
     def struct(self) -> KV:
         return KV(self.k.data_ptr(), self.v.data_ptr(), self.page_size, self.capacity, self.batch,
@@ -342,6 +355,7 @@ class Model:
         import torch
         self.shape = shape
         self.weights = weights  # keep the tensors alive
+        self._bind(shape)
         layers = weights["layers"]
         if len(layers) != shape.n_layers:
             raise ValueError("shape has %d layers, weights have %d" % (shape.n_layers, len(layers)))
@@ -364,6 +378,15 @@ class Model:
         if rc:
             raise LlamaError(rc, "llama_init")
         self.ctx = ctx
+
+    def _bind(self, shape):
+        """What the attention-form calls look up every time."""
+        import torch
+        l = lib()
+        self._append, self._docs = l.llama_op_rope_norm_append, l.llama_op_attention_docs
+        self._shared = l.llama_op_attention_decode_shared
+        self._dt, self._qkv_rows = shape.torch_dtype, shape.qkv_rows
+        self._i32, self._f32 = torch.int32, torch.float32
 
     def __del__(self):
         ctx = getattr(self, "ctx", None)
@@ -502,57 +525,59 @@ class Model:
         qkv [n_rows, (n_q + 2 n_kv) d], fp32 or the model's dtype, rows may be
         strided; start_pos int32 [B]; cu_rows int32 [B + 1], or None for one row
         per sequence; eps defaults to the model's rms_eps."""
-        import torch
-        s, dt = self.shape, self.shape.torch_dtype
-        n, B, d = qkv.shape[0], start_pos.numel(), s.head_dim
-        if qkv.dim() != 2 or qkv.shape[1] != s.qkv_rows or qkv.stride(1) != 1 or not qkv.is_cuda \
-                or (qkv.dtype != torch.float32 and qkv.dtype != dt):
+        s, dt = self.shape, self._dt
+        i32, f32 = self._i32, self._f32
+        n, width = qkv.shape
+        B, d, qdt, ld = start_pos.numel(), s.head_dim, qkv.dtype, qkv.stride()
+        if (qdt is not f32 and qdt is not dt) or width != self._qkv_rows or ld[1] != 1 or \
+                not qkv.is_cuda:
             raise ValueError("qkv: want device rows of %d %s or fp32, got %s %s"
-                             % (s.qkv_rows, dt, tuple(qkv.shape), qkv.dtype))
-        self._chk(lib().llama_op_rope_norm_append(
-            self.ctx, qkv.data_ptr(), F32 if qkv.dtype == torch.float32 else BF16, qkv.stride(0), n,
-            None if cu_rows is None else _need("cu_rows", cu_rows, torch.int32, B + 1),
-            _need("start_pos", start_pos, torch.int32, B), B, None if rope is None else rope._ref,
+                             % (s.qkv_rows, dt, tuple(qkv.shape), qdt))
+        rc = self._append(
+            self.ctx, qkv.data_ptr(), F32 if qdt is f32 else BF16, ld[0], n,
+            None if cu_rows is None else _need("cu_rows", cu_rows, i32, B + 1),
+            _need("start_pos", start_pos, i32, B), B, None if rope is None else rope._ref,
             None if q_gain is None else _need("q_gain", q_gain, dt, d),
             None if k_gain is None else _need("k_gain", k_gain, dt, d),
-            s.rms_eps if eps is None else eps, layer, ctypes.byref(kv.struct()),
+            s.rms_eps if eps is None else eps, layer, kv._now(),
             _need("q_out", q_out, dt, n * s.n_q_heads * d),
             None if k_out is None else _need("k_out", k_out, dt, n * s.n_kv_heads * d),
-            None if v_out is None else _need("v_out", v_out, dt, n * s.n_kv_heads * d)),
-            "llama_op_rope_norm_append")
+            None if v_out is None else _need("v_out", v_out, dt, n * s.n_kv_heads * d))
+        if rc:
+            raise LlamaError(rc, "llama_op_rope_norm_append")
 
     def op_attention_docs(self, q, k, v, cu_rows, out, *, prefix=None, scores=None):
         """Prompt attention over packed documents (llama_op_attention_docs): q
         [n_rows, n_q, d], k and v [n_rows, n_kv, d], cu_rows int32 [B + 1]; prefix
         int32 [B] rows attended both ways; scores a Scores."""
-        import torch
-        s, dt = self.shape, self.shape.torch_dtype
+        s, dt, i32 = self.shape, self._dt, self._i32
         n, B = q.shape[0], cu_rows.numel() - 1
         if scores is not None and scores.slopes is not None:
-            _need("slopes", scores.slopes, torch.float32, s.n_q_heads)
+            _need("slopes", scores.slopes, self._f32, s.n_q_heads)
         qn, kn = n * s.n_q_heads * s.head_dim, n * s.n_kv_heads * s.head_dim
-        self._chk(lib().llama_op_attention_docs(
+        rc = self._docs(
             self.ctx, _need("q", q, dt, qn), _need("k", k, dt, kn), _need("v", v, dt, kn), n,
-            _need("cu_rows", cu_rows, torch.int32, B + 1), B,
-            None if prefix is None else _need("prefix", prefix, torch.int32, B),
-            None if scores is None else scores._ref, _need("out", out, dt, qn)),
-            "llama_op_attention_docs")
+            _need("cu_rows", cu_rows, i32, B + 1), B,
+            None if prefix is None else _need("prefix", prefix, i32, B),
+            None if scores is None else scores._ref, _need("out", out, dt, qn))
+        if rc:
+            raise LlamaError(rc, "llama_op_attention_docs")
 
     def op_attention_decode_shared(self, q, positions, layer, kv: KVCache, out, *, shared_len=0,
                                    shared_seq=0, scores=None):
         """Decode attention over a cache whose first shared_len positions are
         sequence shared_seq's for the whole batch (llama_op_attention_decode_shared)."""
-        import torch
-        s, dt = self.shape, self.shape.torch_dtype
+        s, dt = self.shape, self._dt
         B = positions.numel()
         if scores is not None and scores.slopes is not None:
-            _need("slopes", scores.slopes, torch.float32, s.n_q_heads)
+            _need("slopes", scores.slopes, self._f32, s.n_q_heads)
         qn = B * s.n_q_heads * s.head_dim
-        self._chk(lib().llama_op_attention_decode_shared(
-            self.ctx, _need("q", q, dt, qn), _need("positions", positions, torch.int32, B), B, layer,
-            ctypes.byref(kv.struct()), shared_len, shared_seq,
-            None if scores is None else scores._ref, _need("out", out, dt, qn)),
-            "llama_op_attention_decode_shared")
+        rc = self._shared(
+            self.ctx, _need("q", q, dt, qn), _need("positions", positions, self._i32, B), B, layer,
+            kv._now(), shared_len, shared_seq, None if scores is None else scores._ref,
+            _need("out", out, dt, qn))
+        if rc:
+            raise LlamaError(rc, "llama_op_attention_decode_shared")
 
     def op_embed(self, tokens, out):
         self._chk(lib().llama_op_embed(self.ctx, _p(tokens), tokens.numel(), _p(out)), "llama_op_embed")

@@ -102,7 +102,7 @@ def test_null_context(lib):
     assert lib.llama_op_attention_decode_shared(None, None, None, 1, 0, ctypes.byref(kv), 0, 0, None, None) == 1
 
 
-def test_binding_refuses_wrong_tensors():
+def test_binding_refuses_wrong_tensors(lib):
     with pytest.raises(ValueError):
         binding.Rope()
     with pytest.raises(ValueError):
@@ -117,6 +117,7 @@ def test_binding_refuses_wrong_tensors():
         binding.rope_table(4, 12)
     m = binding.Model.__new__(binding.Model)
     m.shape, m.ctx = synth.Shape(1, 256, 4, 2, 128, 256, 256), None
+    m._bind(m.shape)
     q, k = torch.zeros(3, 512, dtype=torch.bfloat16), torch.zeros(3, 256, dtype=torch.bfloat16)
     with pytest.raises(ValueError):  # not on the device
         m.op_attention_docs(q, k, k, torch.zeros(2, dtype=torch.int32), q)

@@ -247,7 +247,7 @@ def _slopes(nq):
 
 
 def _docs_case(nq, nkv, d, dtype, lens, *, prefix=None, cap=0.0, bias=False, scale=0.0, lead=0, tail=0,
-               seed=7, std=1.5, rows=None, poison=False):
+               seed=7, std=1.5, rows=None, poison=False, slopes=None):
     m, shape = _model(nq, nkv, d, dtype)
     dt = shape.torch_dtype
     n = lead + sum(lens) + tail
@@ -259,7 +259,8 @@ def _docs_case(nq, nkv, d, dtype, lens, *, prefix=None, cap=0.0, bias=False, sca
         for t in (q, k, v):
             t[:lead] = float("nan")
             t[cu[-1]:] = float("inf")
-    slopes = _slopes(nq) if bias else None
+    slopes = torch.tensor(slopes) if slopes is not None else _slopes(nq) if bias else None
+    bias = slopes is not None
     out = torch.full((n, nq * d), 3.0, dtype=dt, device="cuda")
     m.op_attention_docs(q.cuda(), k.cuda(), v.cuda(), _i32(cu), out,
                         prefix=None if prefix is None else _i32(prefix),
@@ -317,6 +318,31 @@ def test_docs_large_scores():
     _docs_case(2, 1, 64, "f32", [200], std=4.0)
 
 
+SLOPES = [[5.0, -0.5, 0.0, 1.3], [1.3, 1.5, 0.1, 40.0], [-3.0, 0.0, -0.01, 2.0]]
+
+
+@pytest.mark.parametrize("slopes", SLOPES)
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_docs_steep_and_negative_slopes(slopes, cap):
+    # biases of some 100 between neighbouring tiles, rising and falling, per head
+    _docs_case(4, 2, 128, "bf16", [330, 70], slopes=slopes, cap=cap)
+    _docs_case(4, 4, 128, "bf16", [330, 70], slopes=slopes, cap=cap, prefix=[200, 70])
+
+
+@pytest.mark.parametrize("slopes", SLOPES)
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_shared_steep_and_negative_slopes(slopes, cap):
+    _shared_case(4, 1, 128, "bf16", [400, 260, 300], 256, slopes=slopes, cap=cap)
+    _shared_case(4, 4, 128, "bf16", [400, 260, 300], 0, slopes=slopes, cap=cap)
+
+
+@pytest.mark.parametrize("cap,scale", [(50.0, 0.0), (50.3, 0.0), (2.0, 0.5), (0.05, 1.0), (2000.0, 0.0), (300.0, 4.0)])
+def test_docs_caps(cap, scale):
+    # barely capped, far past the cap, and scale / cap outside the fitted range
+    _docs_case(4, 2, 128, "bf16", [300, 40], cap=cap, scale=scale)
+    _docs_case(3, 3, 128, "bf16", [300, 40], cap=cap, scale=scale, bias=True)
+
+
 def test_docs_many_documents():
     lens = torch.randint(0, 4, (200,), generator=_gen(3)).tolist()
     _docs_case(2, 1, 128, "bf16", lens)
@@ -354,7 +380,7 @@ def test_docs_bad_bounds_are_flagged():
 
 # --------------------------------------------------------------------------- decode
 def _shared_case(nq, nkv, d, dtype, positions, shared, *, page=16, seq=0, cap=0.0, bias=False, scale=0.0,
-                 seed=11, std=1.5, layers=1, layer=0, max_seq=None, poison=True):
+                 seed=11, std=1.5, layers=1, layer=0, max_seq=None, poison=True, slopes=None):
     B = len(positions)
     top = max(max(positions) + 1, shared, 1)
     m, shape = _model(nq, nkv, d, dtype, max_batch=B, max_seq=max_seq or top, n_layers=layers)
@@ -392,7 +418,8 @@ def _shared_case(nq, nkv, d, dtype, positions, shared, *, page=16, seq=0, cap=0.
                     v[layer, i, :, j] = float("nan") if (i + j) % 2 else float("inf")
     kv = binding.KVCache(shape, n_pages=size[1], page_size=page, page_table=pt.cuda(), k=k.cuda(), v=v.cuda()) \
         if page else binding.KVCache(shape, batch=size[1], capacity=top, k=k.cuda(), v=v.cuda())
-    slopes = _slopes(nq) if bias else None
+    slopes = torch.tensor(slopes) if slopes is not None else _slopes(nq) if bias else None
+    bias = slopes is not None
     out = torch.full((B, nq * d), 3.0, dtype=dt, device="cuda")
     m.op_attention_decode_shared(q.cuda(), _i32(positions), layer, kv, out, shared_len=shared, shared_seq=seq,
                                  scores=binding.Scores(scale, cap, None if slopes is None else slopes.cuda()))
