@@ -1411,6 +1411,7 @@ int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t*
   a.shared_len = B == 1 && shared_seq == 0 ? 0 : shared_len;
   a.shared_seq = shared_seq;
   a.status = c->status;
+  a.sm_count = c->sm_count;
   if (cf.dtype != LLAMA_BF16) {
     Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
     c->launches++;

@@ -291,7 +291,7 @@ struct SharedArgs {
   // views as in AttnDecodeArgs
   const CUtensorMap *map_q = nullptr, *map_k = nullptr, *map_v = nullptr, *map_k16 = nullptr,
                     *map_v16 = nullptr;
-  int box_rows = 16;
+  int box_rows = 16, sm_count = 152;
   float* partial = nullptr;    // workspace, SharedPlan::partials x (128 + 2) floats
 };
 // How a decode batch over a shared prefix is cut: the prefix kernel's grid

@@ -13,8 +13,11 @@
 // butterflies (the running maximum and sum of an online softmax, in fp32);
 // P goes through shared memory within the warp, and the same thread
 // accumulates its rows' dims 4 tx + 64 m. fp32 arithmetic throughout (exp and
-// tanh of the CUDA math library). Bound by the fp32 FMA pipe and, with 32-row
-// tiles, the shared-memory reads that feed it; with few tiles by their number.
+// tanh of the CUDA math library). Where there are few items, up to 8 CTAs (a
+// cluster) take an item's key tiles in turn and merge through distributed shared
+// memory. Bound by the fp32 FMA pipe and, with 32-row tiles, the shared-memory
+// reads that feed it (documents of 700 rows in all, 8 heads, 64 dims: 68 us
+// unsplit, 50 us with splits).
 #include <algorithm>
 
 #include "attn_score.cuh"
@@ -40,6 +43,7 @@ struct SimtParams {
   const int32_t *positions, *page_table;
   int layer, page_size, capacity, batch_cap, n_pages, max_pages, key_limit, shared_len, shared_seq;
   int row_chunks;  // chunks of 16 RI heads per K/V head
+  int splits;      // CTAs (a cluster) that share an item's key tiles
 };
 
 // Element offset of key j of sequence b, K/V head g in the cache; -1 (flagged)
@@ -90,12 +94,13 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
   if (!bc_smem(sm, (uint32_t)Tile::bytes, 16, threadIdx.x == 0 ? p.status : nullptr)) return;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int d = p.d;
+  const int item = blockIdx.x / p.splits, part = blockIdx.x - item * p.splits;
   // which rows
   int b, g, h0, lo = 0, n = 0, q0 = 0, rows, n_keys, pre = 0, pos = 0;
   if (DOCS) {
-    const int h = blockIdx.x % p.n_q;
+    const int h = item % p.n_q;
     int tile;
-    if (!find_tile(p.cu_rows, p.n_docs, p.n_rows, RT, blockIdx.x / p.n_q, p.status, b, tile, lo, n))
+    if (!find_tile(p.cu_rows, p.n_docs, p.n_rows, RT, item / p.n_q, p.status, b, tile, lo, n))
       return;
     h0 = h;
     g = h / p.G;
@@ -104,15 +109,15 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     pre = p.prefix_len ? min(max(p.prefix_len[b], 0), n) : 0;
     n_keys = max(q0 + rows, pre);
   } else {
-    const int c = blockIdx.x % p.row_chunks;
-    g = (blockIdx.x / p.row_chunks) % p.n_kv;
-    b = blockIdx.x / (p.row_chunks * p.n_kv);
+    const int c = item % p.row_chunks;
+    g = (item / p.row_chunks) % p.n_kv;
+    b = item / (p.row_chunks * p.n_kv);
     h0 = g * p.G + c * RT;
     rows = min(RT, p.G - c * RT);
     pos = p.positions[b];
     n_keys = pos + 1;
     if (pos < 0 || pos >= p.key_limit) {
-      if (threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
+      if (part == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
       n_keys = pos < 0 ? 0 : p.key_limit;
     }
   }
@@ -133,7 +138,8 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     }
     copies_commit();
   };
-  if (n_keys > 0) load_tile(0, 0);
+  const int first = part * SK, step = p.splits * SK;  // this CTA's key tiles
+  if (first < n_keys) load_tile(first, 0);
   for (int i = threadIdx.x; i < RT * (DM / 4); i += S_THREADS) {
     const int r = i / (DM / 4), x = 4 * (i % (DM / 4));
     *reinterpret_cast<float4*>(sq + r * LD + x) =
@@ -155,9 +161,9 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     for (int x = 0; x < DM / 16; ++x) o[i][x] = 0.f;
   }
   int stage = 0;
-  for (int k0 = 0; k0 < n_keys; k0 += SK) {
-    if (ST == 2 && k0 + SK < n_keys) {
-      load_tile(k0 + SK, stage ^ 1);
+  for (int k0 = first; k0 < n_keys; k0 += step) {
+    if (ST == 2 && k0 + step < n_keys) {
+      load_tile(k0 + step, stage ^ 1);
       copies_wait<1>();
     } else {
       copies_wait<0>();
@@ -236,14 +242,60 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     __syncthreads();  // the stage may be overwritten
     if (ST == 2)
       stage ^= 1;
-    else if (k0 + SK < n_keys)
-      load_tile(k0 + SK, 0);
+    else if (k0 + step < n_keys)
+      load_tile(k0 + step, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+  if (p.splits > 1) {
+    // The cluster's CTAs leave (O, maximum, sum) in their shared memory; row r is
+    // merged by CTA r % splits, in the order of the parts.
+    float* so = skv;            // [RT][DM], over the tiles
+    float* sml = so + RT * DM;  // [RT][2]
+    static_assert(RT * (DM + 2) <= ST * 2 * SK * LD, "the rows fit over the tiles");
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      const int r = ty + 16 * i;
+#pragma unroll
+      for (int x = 0; x < DM / 64; ++x)
+        *reinterpret_cast<float4*>(so + r * DM + 64 * x + 4 * tx) =
+            make_float4(o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]);
+      if (tx == 0) *reinterpret_cast<float2*>(sml + 2 * r) = make_float2(m[i], l[i]);
+    }
+    cluster_sync_all();
+    if (ty % p.splits == part) {  // 16 is a multiple of the cluster's size
+#pragma unroll
+      for (int i = 0; i < RI; ++i) {
+        const int r = ty + 16 * i;
+        const uint32_t am = smem_u32(sml + 2 * r), ao = smem_u32(so + r * DM + 4 * tx);
+        float M = -INFINITY, L = 0.f;
+        for (int c = 0; c < p.splits; ++c) M = fmaxf(M, dsmem_ld2(dsmem_addr(am, c)).x);
+#pragma unroll
+        for (int x = 0; x < DM / 16; ++x) o[i][x] = 0.f;
+        for (int c = 0; c < p.splits; ++c) {
+          const float2 ml = dsmem_ld2(dsmem_addr(am, c));
+          const float f = ml.x == -INFINITY ? 0.f : expf(ml.x - M);
+          L = fmaf(ml.y, f, L);
+#pragma unroll
+          for (int x = 0; x < DM / 64; ++x) {
+            const float4 v = dsmem_ld4(dsmem_addr(ao + 256 * x, c));
+            o[i][4 * x] = fmaf(v.x, f, o[i][4 * x]);
+            o[i][4 * x + 1] = fmaf(v.y, f, o[i][4 * x + 1]);
+            o[i][4 * x + 2] = fmaf(v.z, f, o[i][4 * x + 2]);
+            o[i][4 * x + 3] = fmaf(v.w, f, o[i][4 * x + 3]);
+          }
+        }
+        l[i] = L;
+      }
+    }
+    cluster_sync_all();  // nobody leaves while its rows are read
+    if (ty % p.splits != part) return;
   }
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
-    float lt = l[i];
-#pragma unroll
-    for (int w = 8; w > 0; w >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
     const int r = ty + 16 * i;
     if (r >= rows) continue;
     float* dst = p.out + row_off(r);
@@ -253,7 +305,8 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
       if (dim >= d) continue;
       float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
       if (n_keys > 0)
-        w = make_float4(o[i][4 * x] / lt, o[i][4 * x + 1] / lt, o[i][4 * x + 2] / lt, o[i][4 * x + 3] / lt);
+        w = make_float4(o[i][4 * x] / l[i], o[i][4 * x + 1] / l[i], o[i][4 * x + 2] / l[i],
+                        o[i][4 * x + 3] / l[i]);
       *reinterpret_cast<float4*>(dst + dim) = w;
     }
   }
@@ -266,15 +319,25 @@ cudaError_t prep() {
 }
 
 template <int RI, bool DOCS>
-cudaError_t run(const SimtParams& p, unsigned grid, cudaStream_t st) {
+cudaError_t run(const SimtParams& p, long long items, cudaStream_t st) {
+  const dim3 grid((unsigned)(items * p.splits)), cluster(p.splits > 1 ? p.splits : 0, 1, 1);
   if (p.d <= 64)
-    return launch_k(attn_simt_kernel<RI, 64, DOCS>, dim3(grid), dim3(S_THREADS),
-                    SimtTile<RI, 64>::bytes, st, 0, p);
+    return launch_kc(attn_simt_kernel<RI, 64, DOCS>, grid, dim3(S_THREADS), SimtTile<RI, 64>::bytes,
+                     st, cluster, p);
   if (p.d <= 128)
-    return launch_k(attn_simt_kernel<RI, 128, DOCS>, dim3(grid), dim3(S_THREADS),
-                    SimtTile<RI, 128>::bytes, st, 0, p);
-  return launch_k(attn_simt_kernel<RI, 256, DOCS>, dim3(grid), dim3(S_THREADS),
-                  SimtTile<RI, 256>::bytes, st, 0, p);
+    return launch_kc(attn_simt_kernel<RI, 128, DOCS>, grid, dim3(S_THREADS), SimtTile<RI, 128>::bytes,
+                     st, cluster, p);
+  return launch_kc(attn_simt_kernel<RI, 256, DOCS>, grid, dim3(S_THREADS), SimtTile<RI, 256>::bytes,
+                   st, cluster, p);
+}
+
+// CTAs that share an item's keys: doubled up to a cluster's 8 while there are
+// fewer than three CTAs per SM and each keeps a tile of the longest (three per SM
+// 50 us, two 61, six 68).
+int simt_splits(long long items, int keys, int sm_count) {
+  int s = 1;
+  while (s < 8 && items * s < 3 * sm_count && keys >= 2 * s * SK) s *= 2;
+  return s;
 }
 
 }  // namespace
@@ -306,13 +369,14 @@ cudaError_t launch_docs_simt(const DocsArgs& a, cudaStream_t st) {
   p.prefix_len = a.prefix_len;
   p.n_rows = a.n_rows;
   p.n_docs = a.n_docs;
-  // 64-row tiles feed the FMA pipe best; where they would leave SMs without work
-  // (fewer than two per SM), 32 rows (700 rows, 8 heads: 98 us with 64, 68 with
-  // 32, 71 with 16)
+  // 64-row tiles feed the FMA pipe best; where they leave SMs without work (fewer
+  // than two per SM), 32 rows (700 rows, 8 heads, keys split: 57 us with 64, 50
+  // with 32)
   const long long docs = std::min(a.n_docs, a.n_rows);
   auto tiles = [&](int rows) { return (a.n_rows / rows + docs) * a.n_q; };  // an upper bound
-  if (tiles(64) >= 2 * a.sm_count) return run<4, true>(p, (unsigned)tiles(64), st);
-  return run<2, true>(p, (unsigned)tiles(32), st);
+  const bool big = tiles(64) >= 2 * a.sm_count;
+  p.splits = simt_splits(tiles(big ? 64 : 32), a.n_rows, a.sm_count);
+  return big ? run<4, true>(p, tiles(64), st) : run<2, true>(p, tiles(32), st);
 }
 
 cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st) {
@@ -339,7 +403,9 @@ cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st) {
   p.shared_len = a.shared_len;
   p.shared_seq = a.shared_seq;
   p.row_chunks = (p.G + 15) / 16;
-  return run<1, false>(p, (unsigned)((long long)a.B * a.n_kv * p.row_chunks), st);
+  const long long items = (long long)a.B * a.n_kv * p.row_chunks;
+  p.splits = simt_splits(items, a.key_limit, a.sm_count);
+  return run<1, false>(p, items, st);
 }
 
 }  // namespace llgb
