@@ -1,5 +1,5 @@
-// Pieces shared by the attention kernels with capped or biased scores: the
-// score transform and the map from work items to packed documents.
+// Pieces shared by the attention kernels with capped or biased scores: the map
+// from work items to packed documents, and how partial results are merged.
 #pragma once
 
 #include "common.cuh"
@@ -16,6 +16,11 @@ __device__ __forceinline__ void doc_rows(const int32_t* cu, int b, int n_rows, u
   n = hi - lo;
   if (lo != a || hi != e) flag(status, LLAMA_FLAG_POS_RANGE);
 }
+
+// The maximum that a partial result of sum l is merged with: a maximum passes over
+// NaN scores, and without a finite one beside them the part would count as
+// empty, so a NaN sum takes part as +inf, which the merge turns into NaN.
+__device__ __forceinline__ float merge_max(float m, float l) { return l != l ? INFINITY : m; }
 
 // Work item -> (document, tile of `rows` query rows, first row, row count), for a
 // whole warp: 32 documents per step, their tile counts summed by a warp scan.

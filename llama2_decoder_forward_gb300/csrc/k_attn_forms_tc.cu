@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           }
         }
         if (row_ok && grp == 0 && (p.alternate || count > 0)) {  // no visible key: no mass
-          p.part_ml[2 * at] = l == 0.f ? -INFINITY : m;
+          p.part_ml[2 * at] = l == 0.f ? -INFINITY : merge_max(m, l);
           p.part_ml[2 * at + 1] = l;
         }
       }

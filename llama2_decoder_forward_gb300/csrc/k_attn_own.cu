@@ -169,7 +169,7 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
       }
       float pv[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pv[i] = m[i & 1] == -INFINITY ? 0.f : ex2(sv[i] - m[i & 1]);
+      for (int i = 0; i < 4; ++i) pv[i] = ex2(sv[i] - (m[i & 1] == -INFINITY ? 0.f : m[i & 1]));
       l[0] = l[0] * corr[0] + pv[0] + pv[2];
       l[1] = l[1] * corr[1] + pv[1] + pv[3];
       if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
@@ -221,7 +221,7 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       if (hc + j < G) {
-        sm[warp * 16 + hc + j] = m[j];
+        sm[warp * 16 + hc + j] = merge_max(m[j], l[j]);
         sm[64 + warp * 16 + hc + j] = l[j];
       }
   }
@@ -304,7 +304,7 @@ __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem,
       for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float e = m[i >> 1] == -INFINITY ? 0.f : ex2(sv[nb][i] - m[i >> 1]);
+          const float e = ex2(sv[nb][i] - (m[i >> 1] == -INFINITY ? 0.f : m[i >> 1]));
           sv[nb][i] = e;
           ps[i >> 1] += e;
         }
@@ -356,7 +356,7 @@ __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem,
   if ((lane & 3) == 0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      sm[warp * 16 + r0 + 8 * h] = m[h];
+      sm[warp * 16 + r0 + 8 * h] = merge_max(m[h], l[h]);
       sm[64 + warp * 16 + r0 + 8 * h] = l[h];
     }
   }

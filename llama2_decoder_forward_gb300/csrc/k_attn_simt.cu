@@ -204,12 +204,13 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
       const float mn = fmaxf(m[i], mx);
-      const float f = mn == -INFINITY ? 1.f : expf(m[i] - mn);
+      const float mu = mn == -INFINITY ? 0.f : mn;  // no finite score yet: weights 0 (of NaN: NaN)
+      const float f = expf(m[i] - mu);
       m[i] = mn;
       float ls = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float e = mn == -INFINITY ? 0.f : expf(s[i][j] - mn);
+        const float e = expf(s[i][j] - mu);
         ls += e;
         sp[(ty + 16 * i) * (SK + 4) + tx + 16 * j] = e;
       }

@@ -318,6 +318,62 @@ def test_docs_large_scores():
     _docs_case(2, 1, 64, "f32", [200], std=4.0)
 
 
+def _nan_pattern(out, want):
+    got = torch.isnan(out.float())
+    assert torch.equal(got.all(-1), got.any(-1)) and torch.equal(got.all(-1).cpu(), want)
+    assert torch.isfinite(out.float()[~got.any(-1)]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("opt", range(4))
+def test_docs_nan_reaches_the_rows_that_see_it(dtype, opt):
+    # a query, and the first 130 keys of the second document's K/V head 1: whole tiles of NaN scores
+    nq, nkv, d, n = 4, 2, 128, 300
+    m, shape = _model(nq, nkv, d, dtype)
+    dt = shape.torch_dtype
+    q, k, v = (_randn((n, h, d), dt, 120 + i) for i, h in enumerate((nq, nkv, nkv)))
+    q[33, 2, 5] = float("nan")
+    k[60:190, 1, 9] = float("nan")
+    o = OPTIONS[opt]
+    out = torch.empty(n, nq * d, dtype=dt, device="cuda")
+    m.op_attention_docs(q.cuda(), k.cuda(), v.cuda(), _i32([0, 60, n]), out, scores=binding.Scores(
+        o.get("scale", 0.0), o.get("cap", 0.0), _slopes(nq).cuda() if o.get("bias") else None))
+    m.sync()
+    want = torch.zeros(n, nq, dtype=torch.bool)
+    want[33, 2] = True
+    want[60:, 2:] = True
+    _nan_pattern(out.view(n, nq, d), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("opt", range(4))
+@pytest.mark.parametrize("nq,nkv", [(4, 2), (24, 2)])
+@pytest.mark.parametrize("shared", [0, 150])
+def test_shared_nan_reaches_the_rows_that_see_it(dtype, opt, nq, nkv, shared):
+    # a query, the first 130 keys of every (or the shared) sequence, and one own key past a shorter position
+    d, B, cap = 128, 3, 400
+    m, shape = _model(nq, nkv, d, dtype, max_batch=B, max_seq=cap)
+    dt = shape.torch_dtype
+    q = _randn((B, nq, d), dt, 130)
+    k, v = (_randn((1, B, nkv, cap, d), dt, 131 + i) for i in range(2))
+    q[1, 1, 5] = float("nan")
+    k[0, 0, 1, :130, 9] = float("nan")
+    k[0, 2, 0, 320] = float("nan")
+    o = OPTIONS[opt]
+    half = nq // nkv
+    kv = binding.KVCache(shape, batch=B, capacity=cap, k=k.cuda(), v=v.cuda())
+    out = torch.empty(B, nq * d, dtype=dt, device="cuda")
+    for pos in ([399, 399, 399], [200, 250, 319], [140, 100, 160]):
+        m.op_attention_decode_shared(q.cuda(), _i32(pos), 0, kv, out, shared_len=shared, scores=binding.Scores(
+            o.get("scale", 0.0), o.get("cap", 0.0), _slopes(nq).cuda() if o.get("bias") else None))
+        m.sync()
+        want = torch.zeros(B, nq, dtype=torch.bool)
+        want[1, 1] = True
+        want[slice(0, B) if shared else 0, half:] = True
+        want[2, :half] = pos[2] >= 320
+        _nan_pattern(out.view(B, nq, d), want)
+
+
 SLOPES = [[5.0, -0.5, 0.0, 1.3], [1.3, 1.5, 0.1, 40.0], [-3.0, 0.0, -0.01, 2.0]]
 
 
@@ -346,6 +402,15 @@ def test_docs_caps(cap, scale):
 def test_docs_many_documents():
     lens = torch.randint(0, 4, (200,), generator=_gen(3)).tolist()
     _docs_case(2, 1, 128, "bf16", lens)
+
+
+@pytest.mark.parametrize("nq,nkv", [(2, 1), (1, 1)])
+def test_docs_many_ragged_documents(nq, nkv):
+    # more documents than a warp's lanes, empty ones and prefixes of any length among them
+    lens = [0] * 40 + [300, 1, 0, 129, 128, 257] + [0] * 30 + [64] * 5 + [0, 200]
+    pre = torch.randint(0, 260, (len(lens),), generator=_gen(5)).tolist()
+    _docs_case(nq, nkv, 128, "bf16", lens)
+    _docs_case(nq, nkv, 128, "bf16", lens, prefix=pre, bias=True)
 
 
 @pytest.mark.parametrize("nq,nkv,d", [(4, 2, 64), (2, 2, 40), (2, 1, 128), (1, 1, 256), (3, 1, 8)])
@@ -629,6 +694,45 @@ def test_captured_replays_follow_their_buffers():
         assert torch.equal(o, captured)
         pos += 1
     m.set_stream(torch.cuda.default_stream())
+
+
+def test_two_contexts_on_two_streams_at_once():
+    # each with its own workspace: the same results as alone, and the same bits every time
+    runs = []
+    for i, (nq, nkv, B) in enumerate(((8, 2, 6), (16, 16, 2))):
+        m, shape = _model(nq, nkv, max_batch=B, max_seq=1024)
+        s = torch.cuda.Stream()
+        q = _randn((B, nq, 128), torch.bfloat16, 140 + i).cuda()
+        k, v = (_randn((1, B, nkv, 1024, 128), torch.bfloat16, 150 + 2 * i + j).cuda() for j in range(2))
+        kv = binding.KVCache(shape, batch=B, capacity=1024, k=k, v=v)
+        pos = _i32([1023 - 7 * b for b in range(B)])
+        dq = _randn((600, nq, 128), torch.bfloat16, 160 + i).cuda()
+        dk, dv = (_randn((600, nkv, 128), torch.bfloat16, 170 + 2 * i + j).cuda() for j in range(2))
+        cu = _i32([0, 350, 600])
+        torch.cuda.synchronize()
+        m.set_stream(s)
+        runs.append((m, s, q, kv, pos, dq, dk, dv, cu))
+
+    def once(r):
+        m, s, q, kv, pos, dq, dk, dv, cu = r
+        with torch.cuda.stream(s):
+            o = torch.empty(q.shape[0], q.shape[1] * 128, dtype=q.dtype, device="cuda")
+            do = torch.empty(600, q.shape[1] * 128, dtype=q.dtype, device="cuda")
+        m.op_attention_decode_shared(q, pos, 0, kv, o, shared_len=700, scores=binding.Scores(cap=20.0))
+        m.op_attention_docs(dq, dk, dv, cu, do)
+        return o, do
+    alone = []
+    for r in runs:
+        alone.append(once(r))
+        r[0].sync()
+    together = [[once(r) for r in runs] for _ in range(20)]
+    for r in runs:
+        r[0].sync()
+    for pair in together:
+        for got, want in zip(pair, alone):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for r in runs:
+        r[0].set_stream(torch.cuda.default_stream())
 
 
 # --------------------------------------------------------------------------- refusals
