@@ -276,64 +276,53 @@ __device__ __forceinline__ void half_bar(int id) {  // the two warps that share 
 // document's own tile count. Longest first, dealt out in alternating order:
 // 17 packed documents end 1 % above the mean load (in the documents' order 13 %),
 // three with prefixes 13 % (61 %).
+// (Beyond 32 documents, 32 at a time: every count over all documents would be
+// documents / 32 loads per count.)
 struct DocCursor {
-  int k = -1, b0 = 0, before = 0;  // key tiles and first document of the step, items before it
+  int k = -1, b0 = 0, before = 0;  // key tiles (-1: a new step) and first document of the step, items before
   int lo = 0, n = 0, P = 0;        // the lane's document of the step
 };
-__device__ __forceinline__ void cursor_load(const FormsParams& p, DocCursor& c, int lane) {
-  c.lo = c.n = c.P = 0;
-  if (c.b0 + lane < p.n_docs) {
-    doc_rows(p.cu_rows, c.b0 + lane, p.n_rows, p.status, c.lo, c.n);
-    const int pre = p.prefix_len ? min(max(p.prefix_len[c.b0 + lane], 0), c.n) : 0;
-    c.P = (pre + TN - 1) / TN;
-  }
-}
 __device__ __forceinline__ bool find_item(const FormsParams& p, int item, int per, DocCursor& c, int& b,
                                           int& tile, int& lo, int& n, int& head) {
   const int lane = threadIdx.x & 31;
-  if (c.k < 0) {
-    int most = 0;
-    for (c.b0 = 0; c.b0 < p.n_docs; c.b0 += 32) {
-      cursor_load(p, c, lane);
-      most = max(most, (c.n + TN - 1) / TN);
+  for (; c.b0 < p.n_docs; c.b0 += 32, c.k = -1) {
+    if (c.k < 0) {
+      c.lo = c.n = c.P = 0;
+      if (c.b0 + lane < p.n_docs) {
+        doc_rows(p.cu_rows, c.b0 + lane, p.n_rows, p.status, c.lo, c.n);
+        const int pre = p.prefix_len ? min(max(p.prefix_len[c.b0 + lane], 0), c.n) : 0;
+        c.P = (pre + TN - 1) / TN;
+      }
+      c.k = __reduce_max_sync(0xffffffffu, (c.n + TN - 1) / TN);
     }
-    c.k = __reduce_max_sync(0xffffffffu, most);
-    c.b0 = 0;
-    cursor_load(p, c, lane);
-  }
-  while (c.k > 0) {
-    const int N = (c.n + TN - 1) / TN;  // key tiles of the whole document
-    int have = 0, first = 0;            // items with k key tiles, the first of them
-    if (c.k == c.P) {
-      have = p.head_pairs ? c.P : c.P >= N ? (N + 1) / 2 : c.P / 2;  // C up to P
-    } else if (c.k > c.P && c.k <= N) {
-      have = p.head_pairs || (c.k & 1) == 0 || c.k == N;
-      first = p.head_pairs ? c.k - 1 : (c.k + 1) / 2 - 1;
-    }
-    int upto = have;
+    for (; c.k > 0; --c.k) {
+      const int N = (c.n + TN - 1) / TN;  // key tiles of the whole document
+      int have = 0, first = 0;            // items with k key tiles, the first of them
+      if (c.k == c.P) {
+        have = p.head_pairs ? c.P : c.P >= N ? (N + 1) / 2 : c.P / 2;  // C up to P
+      } else if (c.k > c.P && c.k <= N) {
+        have = p.head_pairs || (c.k & 1) == 0 || c.k == N;
+        first = p.head_pairs ? c.k - 1 : (c.k + 1) / 2 - 1;
+      }
+      int upto = have;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int total = __shfl_sync(0xffffffffu, upto, 31);
+      if (item - c.before < total * per) {
+        const int i = (item - c.before) / per;
+        head = item - c.before - i * per;
+        const int w = __ffs(__ballot_sync(0xffffffffu, i < upto)) - 1;
+        b = c.b0 + w;
+        tile = __shfl_sync(0xffffffffu, first + i - (upto - have), w);
+        lo = __shfl_sync(0xffffffffu, c.lo, w);
+        n = __shfl_sync(0xffffffffu, c.n, w);
+        return true;
+      }
+      c.before += total * per;
     }
-    const int total = __shfl_sync(0xffffffffu, upto, 31);
-    if (item - c.before < total * per) {
-      const int i = (item - c.before) / per;
-      head = item - c.before - i * per;
-      const int w = __ffs(__ballot_sync(0xffffffffu, i < upto)) - 1;
-      b = c.b0 + w;
-      tile = __shfl_sync(0xffffffffu, first + i - (upto - have), w);
-      lo = __shfl_sync(0xffffffffu, c.lo, w);
-      n = __shfl_sync(0xffffffffu, c.n, w);
-      return true;
-    }
-    c.before += total * per;
-    c.b0 += 32;
-    if (c.b0 >= p.n_docs) {
-      c.b0 = 0;
-      --c.k;
-    }
-    if (p.n_docs > 32) cursor_load(p, c, lane);
   }
   return false;
 }
