@@ -451,7 +451,11 @@ int llama_sample(llama_ctx* ctx, const float* logits, int32_t B, int32_t V,
  * writes the cache; llama_op_attention_docs attends over the prompt rows and
  * llama_op_attention_decode_shared over the cache. All three are single
  * operations on the context's stream, like the ones above; the context's
- * device must be current (INVALID_ARG otherwise). ---- */
+ * device must be current (INVALID_ARG otherwise). Outputs must not overlap
+ * inputs or each other. They may be captured into a caller's CUDA graph; a
+ * captured decode step keeps its partial results in the context's workspace, so
+ * graphs of one context are replayed one after the other, like its calls (one
+ * context per stream), and not while the context runs on another stream. ---- */
 
 /* Rotation angles of scaled positions: table[m][j] = magnitude * (cos, sin) of
  * m * f_j for positions m = 0 .. n_pos-1 and pairs j = 0 .. rotary_dim/2 - 1,
@@ -513,8 +517,8 @@ typedef struct llama_rope {
  * position outside the table flags LLAMA_FLAG_POS_RANGE: the row's outputs are
  * zeros and nothing is cached; past the cache (or a page id outside the pool,
  * LLAMA_FLAG_PAGE_RANGE) only the cache write is skipped. Two rows of the
- * same slot in one call leave either's values there. Outputs must not overlap
- * qkv. rope may be NULL (no rotation; positions may then be any of the cache's). */
+ * same slot in one call leave either's values there. rope may be NULL (no
+ * rotation; positions may then be any of the cache's). */
 int llama_op_rope_norm_append(llama_ctx* ctx, const void* qkv, int32_t qkv_dtype, int64_t qkv_ld,
                               int32_t n_rows, const int32_t* cu_rows, const int32_t* start_pos,
                               int32_t B, const llama_rope* rope, const void* q_gain,
@@ -553,9 +557,11 @@ int llama_op_attention_docs(llama_ctx* ctx, const void* q, const void* k, const 
  * slot of a contiguous cache, which may be one past the batch), the others
  * from b's own. shared_len may end inside a page: keys from shared_len on
  * come from b's own page there. shared_len 0 is plain decode attention with
- * these scores. positions as in llama_op_attention_decode (a negative one
+ * these scores. Where a position lies below shared_len, V of the keys from it up
+ * to shared_len must be finite (they take part with weight 0); K may hold
+ * anything there. positions as in llama_op_attention_decode (a negative one
  * flags and gives zeros; one past the cache or max_seq flags, and the keys in
- * range are attended). out T [B, n_q d]. B <= max_batch; shared_len <= the
+ * range are attended). out T [B, n_q d]. B <= max_batch and 65535; shared_len <= the
  * cache's positions and max_seq. The cache has the context's dtype (an E4M3
  * cache is UNSUPPORTED). */
 int llama_op_attention_decode_shared(llama_ctx* ctx, const void* q, const int32_t* positions,

@@ -1255,6 +1255,7 @@ int llama_rope_table(const llama_rope_scaling* s, int32_t rotary_dim, int32_t n_
       (!(s->low_turns >= 0.f) || !(s->high_turns > s->low_turns) || !std::isfinite(s->high_turns) ||
        s->original_len < 1))
     return LLAMA_ERR_INVALID_ARG;
+  if ((int64_t)n_pos * (rotary_dim / 2) >= (1ll << 38)) return LLAMA_ERR_OUT_OF_RANGE;  // the launch's grid
   return cuda_rc(launch_rope_scaled_table(*s, rotary_dim, n_pos, reinterpret_cast<float2*>(table),
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -1380,7 +1381,7 @@ int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t*
       shared_seq < 0)
     return LLAMA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return LLAMA_ERR_INVALID_ARG;
-  if (B > cf.max_batch) return LLAMA_ERR_OUT_OF_RANGE;
+  if (B > cf.max_batch || B > 65535) return LLAMA_ERR_OUT_OF_RANGE;
   TRY(check_kv(c, kv, B));
   if (kv->kv_dtype != LLAMA_KV_MODEL) return LLAMA_ERR_UNSUPPORTED;
   if (shared_seq >= (kv->page_size ? B : kv->batch_capacity)) return LLAMA_ERR_INVALID_ARG;

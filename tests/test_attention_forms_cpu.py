@@ -92,6 +92,7 @@ def test_table_arguments(lib):
                dict(low_turns=4.0), dict(low_turns=-1.0), dict(high_turns=float("inf")), dict(original_len=0),
                dict(magnitude=0.0), dict(magnitude=float("nan"))):
         assert call(**kw) == 1, kw
+    assert call(rotary=1 << 20, n_pos=1 << 20) == 3  # more angles than a launch's grid
 
 
 def test_null_context(lib):
