@@ -1420,7 +1420,7 @@ int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t*
   }
   const SharedPlan plan =
       shared_plan(B, cf.n_q_heads, cf.n_kv_heads, limit, a.shared_len, c->sm_count);
-  if (plan.partials * (128 + 2) * sizeof(float) >
+  if (plan.partials * (128 + 2) * sizeof(float) + 16 >
       shared_partial_bytes(cf.max_batch, cf.n_q_heads, cf.n_kv_heads, cf.max_seq, c->sm_count))
     return LLAMA_ERR_WORKSPACE;
   trim_maps(c);
@@ -1437,7 +1437,7 @@ int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t*
   if (!a.map_q || !a.map_k || !a.map_v || !a.map_k16 || !a.map_v16) return LLAMA_ERR_CUDA;
   a.partial = c->at<float>(c->L.spart);
   Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
-  c->launches += (plan.prefix_parts ? 1 : 0) + (plan.own_splits > 1 && !plan.cluster ? 2 : 1);
+  c->launches += (plan.prefix_parts ? 1 : 0) + (plan.join ? 2 : 1);
   if (plan.prefix_parts) TRY(cuda_rc(launch_shared_prefix(a, plan, c->stream)));
   return cuda_rc(launch_shared_own(a, plan, c->stream));
 }

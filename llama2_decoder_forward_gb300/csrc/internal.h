@@ -303,6 +303,7 @@ struct SharedPlan {
   int prefix_parts;     // partials per row of the prefix kernel (0: no prefix)
   int base, own_splits, keys_per_split;
   int cluster;          // the own splits of a row form a thread-block cluster
+  int join;             // own splits leave partials, which a joining kernel merges
   size_t partials;      // partial rows in all
 };
 SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, int sm_count);

@@ -38,6 +38,7 @@
 // P is rounded once to bf16 (V's type, which the MMA shares); the sum that
 // normalises it is taken in fp32 before that.
 #include <algorithm>
+#include <climits>
 
 #include "attn_score.cuh"
 #include "internal.h"
@@ -77,9 +78,13 @@ struct FormsParams {
   int B, rows_seq;                          // sequences of a row tile (128 / G)
   int alternate;                            // both row tiles hold the same rows
   int layer, page_size, capacity, batch_cap, n_pages, max_pages, box_rows;
-  int key_limit, shared_len, shared_seq, tiles_per_split;
+  int key_limit, shared_len, shared_seq;
   float *part_o, *part_ml;                  // [B n_q][splits][128], [B n_q][splits][2] (max log2, sum)
-  int splits;                               // partials of a row written here start at 0
+  int splits;                               // partials a row has room for
+  int *used;                                // how many of them are written
+  int sm_count;
+  int waiting;                              // the own keys' CTAs wait for this kernel
+  float own_items;                          // how many of them there are
   float poly[13];                           // KCapFixed: kTanh times powers of scale / cap
 };
 
@@ -337,9 +342,10 @@ struct FormsWork {
   int split, seq0;      // prefix: key split, first sequence
   int last_rows;        // keys of the last tile; over TN: all
 };
-// The CTA's it-th item; false: no more.
+// The CTA's it-th item; false: no more. share: key tiles of a prefix split.
 template <bool DOCS>
-__device__ __forceinline__ bool forms_work(const FormsParams& p, int it, DocCursor& cursor, FormsWork& w) {
+__device__ __forceinline__ bool forms_work(const FormsParams& p, int it, int share, DocCursor& cursor,
+                                           FormsWork& w) {
   if (DOCS) {
     const int per = p.head_pairs ? p.n_q / 2 : p.n_q, rows = p.head_pairs ? TM : 2 * TM;
     // every other round backwards: whoever had the longest item of one round
@@ -365,8 +371,8 @@ __device__ __forceinline__ bool forms_work(const FormsParams& p, int it, DocCurs
     w.split = blockIdx.x;
     w.g = blockIdx.z;
     w.seq0 = blockIdx.y * p.rows_seq * (p.alternate ? 1 : 2);
-    w.t0 = w.split * p.tiles_per_split;
-    w.n_tiles = min(p.tiles_per_split, (p.shared_len + TN - 1) / TN - w.t0);
+    w.t0 = w.split * share;
+    w.n_tiles = min(share, (p.shared_len + TN - 1) / TN - w.t0);
     if (w.n_tiles <= 0) return false;
     w.kmax = p.shared_len;
     w.nt0 = p.alternate ? (w.n_tiles + 1) / 2 : w.n_tiles;
@@ -374,6 +380,42 @@ __device__ __forceinline__ bool forms_work(const FormsParams& p, int it, DocCurs
   }
   w.last_rows = w.kmax - (w.t0 + w.n_tiles - 1) * TN;
   return true;
+}
+
+// Key tiles per prefix split, for a whole warp; the same in every CTA. A smaller
+// prefix grid leaves SMs to the own keys' kernel, which starts beside it and is
+// bound by bytes; a larger one ends sooner. Of all grids, the one with the
+// smallest estimate of both: 6 us and 1.3 - 2.1 us per turn here; an own CTA
+// 3.5 us and its bytes at 29 GB/s, three per free SM, 6.3 TB/s together at most,
+// and 6 us more for what is left when the prefix ends.
+template <int KIND>
+__device__ __forceinline__ int prefix_share(const FormsParams& p, int lane) {
+  float own = 0.f;
+  for (int i = lane; i < p.B; i += 32)
+    own += (float)max(0, min(p.positions[i], p.key_limit - 1) + 1 - p.shared_len);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+  own *= 512.f * gridDim.z;  // K and V
+  const float item = own / p.own_items;
+  const float sm_rate = 3.f * item / (3.5f + item / 0.029e6f);
+  constexpr float turn = KIND == KPlain ? 1.3f : KIND == KBias ? 1.6f : KIND == KCapFixed ? 1.95f : 2.1f;
+  const int tiles = (p.shared_len + TN - 1) / TN, unit = gridDim.y * gridDim.z;
+  float best = INFINITY;
+  int share = tiles;
+  for (int s = lane + 1; s <= gridDim.x; s += 32) {
+    const int n = (tiles + s - 1) / s, turns = p.alternate ? (n + 1) / 2 : n;
+    const float t = 6.f + turn * turns;
+    const float sms = (float)max(0, p.sm_count - (tiles + n - 1) / n * unit);
+    float done = fminf(6.3e6f, sm_rate * sms) * t;
+    if (p.waiting) done = fminf(done, 3.f * sms * item);  // one item per resident CTA
+    const float total = t + (own > done ? 6.f + (own - done) / 6.3e6f : 0.f);
+    if (total < best) {
+      best = total;
+      share = n;
+    }
+  }
+  const uint32_t top = __reduce_min_sync(0xffffffffu, __float_as_uint(best));
+  return __reduce_min_sync(0xffffffffu, __float_as_uint(best) == top ? share : INT_MAX);
 }
 
 template <bool DOCS, int KIND>
@@ -396,10 +438,10 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   uint64_t* fin = pready + 4;       // [2] the row tile's last O += P V is done
   uint64_t* drained = fin + 2;      // [2] every MMA of the issuer is done
   // tensor memory, abort, and the turns at the tensor pipe that each issuer has
-  // had: counts, because a phase bit could be lapped
+  // had (counts, because a phase bit could be lapped); a prefix split's key tiles
   volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(drained + 2);
   volatile uint32_t* stop = ctl + 1;
-  static_assert((2 + 2 * MAXK + 2 * MAXV + 1 + 10) * 8 + 16 <= 256, "barrier block");
+  static_assert((2 + 2 * MAXK + 2 * MAXV + 1 + 10) * 8 + 20 <= 256, "barrier block");
   grid_dep_wait();
   grid_dep_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -437,10 +479,19 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     fence_mbar_init();
   }
   if (warp == 18) tmem_alloc(const_cast<uint32_t*>(ctl), 512);
+  if (!DOCS && warp == 17) {
+    const int n = prefix_share<KIND>(p, lane);
+    if (lane == 0) {
+      ctl[4] = n;
+      if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+        *p.used = ((p.shared_len + TN - 1) / TN + n - 1) / n * (p.alternate ? 2 : 1);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl[0], 0);
+  const int share = DOCS ? 0 : __shfl_sync(0xffffffffu, ctl[4], 0);
 
   // launched with 640 x 96 registers: 512 x 104 + 128 x 64
   if (warp >= 16) {
@@ -455,7 +506,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       Ring r(KR);
       int issued = 0, loaded_q = 0, rows = 0;
       bool ok = true;
-      for (int it = 0; ok && forms_work<DOCS>(p, it, cursor, w); ++it) {
+      for (int it = 0; ok && forms_work<DOCS>(p, it, share, cursor, w); ++it) {
         if (!DOCS) rows = tile_rows(p, w.g, w.t0, w.kmax, lane);
         ok = __all_sync(0xffffffffu, wait_bar(qempty, (it & 1) ^ 1, stop, p.status));
         if (!ok) break;
@@ -495,7 +546,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       uint32_t ph_land = 0;
       int rows = 0;
       bool ok = true;
-      for (int it = 0; ok && forms_work<DOCS>(p, it, cursor, w); ++it) {
+      for (int it = 0; ok && forms_work<DOCS>(p, it, share, cursor, w); ++it) {
         for (int j = 0; ok && j < w.n_tiles; ++j) {
           if (!DOCS && (j & 3) == 0) rows = tile_rows(p, w.g, w.t0 + j, w.kmax, lane);
           ok = __all_sync(0xffffffffu, wait_bar(&vempty[r.slot], r.phase ^ 1, stop, p.status));
@@ -557,7 +608,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       // every wait returns at once, the rest runs on whatever is there, and
       // nothing is stored. Checks and votes between the waits and the MMAs
       // measured 5-15 % on all cases.
-      for (int it = 0; forms_work<DOCS>(p, it, cursor, w); ++it) {
+      for (int it = 0; forms_work<DOCS>(p, it, share, cursor, w); ++it) {
         const int count = t ? w.nt1 : w.nt0, others = t ? w.nt0 : w.nt1;
         auto score = [&](int slot, bool last) {  // S of a key tile
           const uint64_t kd = kd0 + (uint64_t)(slot * (TILE >> 4));
@@ -669,7 +720,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     FormsWork w;
     uint32_t ph_s = 0, ph_fin = 0;  // phases of sfull, fin
 #pragma unroll 1
-    for (int it = 0; forms_work<DOCS>(p, it, cursor, w); ++it) {
+    for (int it = 0; forms_work<DOCS>(p, it, share, cursor, w); ++it) {
     const int count = t ? w.nt1 : w.nt0;
     if (DOCS && count == 0) continue;
     // this row: its position, its visible keys, where it goes
@@ -897,7 +948,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
             tmem_ld_wait();
             if (row_ok) {
 #pragma unroll
-              for (int i = 0; i < TN / 2; i += 4)
+              for (int i = 0; i < 32; i += 4)
                 *reinterpret_cast<float4*>(p.part_o + at * 128 + 64 * grp + q + i) =
                     make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
             }
@@ -1011,10 +1062,13 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
   p.key_limit = a.key_limit;
   p.shared_len = a.shared_len;
   p.shared_seq = a.shared_seq;
-  p.tiles_per_split = s.tiles_per_split;
   p.part_o = a.partial;
   p.part_ml = a.partial + s.partials * 128;
   p.splits = s.prefix_parts;
+  p.used = reinterpret_cast<int*>(a.partial + s.partials * 130);
+  p.sm_count = a.sm_count;
+  p.waiting = !s.join;
+  p.own_items = (float)((double)a.B * a.n_kv * s.own_splits);
   return launch_k(forms_kernel<false>(kind), dim3(s.prefix_splits, s.row_blocks, a.n_kv),
                   dim3(FORMS_THREADS), FORMS_SMEM, st, 0, *a.map_q, *a.map_k, *a.map_v, *a.map_k16,
                   *a.map_v16, p);

@@ -23,6 +23,7 @@
 // contexts) go through partials and a small joining kernel. One sequence, 466
 // keys, 32 K/V heads: 8.7 us unsplit, 5.8 us as clusters of 8.
 #include <algorithm>
+#include <climits>
 
 #include "attn_score.cuh"
 #include "internal.h"
@@ -39,7 +40,9 @@ constexpr int OWN_THREADS = 160;                // 4 consumer warps + the produc
 constexpr uint32_t SUB_HALF = SUB * 128;        // 16 keys x 64 dims
 constexpr uint32_t HALF = TILE_K * 128;         // 64 keys x 64 dims: 8 KB
 constexpr uint32_t STAGE = 4 * HALF;            // K and V, two dim halves each
-constexpr size_t OWN_SMEM = STAGES * STAGE + 1024 + 256;
+constexpr int SORT_MAX = 256;                   // sequences that a CTA sorts
+constexpr uint32_t OFF_SORT = STAGES * STAGE + 256;
+constexpr size_t OWN_SMEM = OFF_SORT + (SORT_MAX + 4) * 4 + 1024;
 static_assert((4 * 16 * HD + 128) * 4 <= STAGES * STAGE, "the merge area aliases the ring");
 
 struct OwnParams {
@@ -52,19 +55,26 @@ struct OwnParams {
   int key_limit, first;        // keys from `first` on; position limit
   int base;                    // first rounded down to a tile
   int splits, keys_per_split, cluster;
-  int prefix_parts;            // partials per row that the prefix kernel wrote
+  int sorted;                  // sequences (B) to take longest first; 0: in order
+  int prefix_parts;            // partials per row of the prefix kernel, at most
+  const int* used;             // how many it wrote
+  int join;                    // leave partials for the joining kernel
   float *part_o, *part_ml;     // [B n_q][prefix_parts][...]
-  float *own_o, *own_ml;       // [B n_q][splits][...] (splits > 1, no cluster)
+  float *own_o, *own_ml;       // [B n_q][splits][...] (with a prefix, or splits > 1 without cluster)
   float scale, cap;
   const float* slopes;
 };
 
 __device__ __forceinline__ void consumers_bar() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
-__device__ __forceinline__ int own_kv_row(const OwnParams& p, int b, int g, int k0) {
+// Page id of key k0 of sequence b (-1: past its table), and the cache row there.
+__device__ __forceinline__ int own_page(const OwnParams& p, int b, int k0) {
+  const int pi = p.page_size == 0 ? 0 : k0 / p.page_size;
+  return p.page_size != 0 && pi < p.max_pages ? __ldcg(p.page_table + (size_t)b * p.max_pages + pi) : -1;
+}
+__device__ __forceinline__ int own_kv_row(const OwnParams& p, int b, int g, int k0, int page) {
   if (p.page_size == 0) return (b * p.n_kv + g) * p.capacity + k0;
   const int pi = k0 / p.page_size;
-  const int page = pi < p.max_pages ? __ldcg(p.page_table + (size_t)b * p.max_pages + pi) : -1;
   if (page < 0 || page >= p.n_pages) {
     flag(p.status, LLAMA_FLAG_PAGE_RANGE);
     return -64;
@@ -384,34 +394,61 @@ struct RowSum {
   }
 };
 
-// Adds `parts` partials (at..) of the row: lane s reads part s's maximum and
-// sum, so they take one load for 32 parts; the order of the sums is fixed.
-__device__ __forceinline__ void fold(const float* o, const float* ml, size_t at, int parts, int lane,
-                                     RowSum& r) {
-  for (int s0 = 0; s0 < parts; s0 += 32) {
-    const int k = min(32, parts - s0);
-    float2 x = make_float2(-INFINITY, 0.f);
-    if (lane < k) x = __ldcg(reinterpret_cast<const float2*>(ml) + at + s0 + lane);
-    float mx = x.x;
+// The partials of a row: lane s holds part s's maximum and sum, so they take
+// one load for 32 parts, and the first outputs are loaded beside them, before it
+// is known how many of the `cap` parts there is room for are there.
+template <int AHEAD>
+struct Parts {
+  const float4* o;
+  const float2* ml;
+  int cap;
+  float2 x;
+  float4 v[AHEAD];
+  __device__ __forceinline__ void outputs(int s, int n, int lane) {
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    mx = fmaxf(mx, r.m);
-    if (mx == -INFINITY) continue;
-    r.scale_to(mx);
-    const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - mx);
-    float ls = f == 0.f ? 0.f : x.y * f;
+    for (int i = 0; i < AHEAD; ++i)
+      if (s + i < n) v[i] = __ldcg(o + (size_t)(s + i) * (HD / 4) + lane);
+  }
+  __device__ __forceinline__ void load(const float* po, const float* pml, size_t at, int room, int lane) {
+    o = reinterpret_cast<const float4*>(po + at * HD);
+    ml = reinterpret_cast<const float2*>(pml) + at;
+    cap = room;
+    x = make_float2(-INFINITY, 0.f);
+    if (lane < cap) x = __ldcg(ml + lane);
+    outputs(0, cap, lane);
+  }
+  // adds the first `parts` of them to r, in their order
+  __device__ __forceinline__ void fold(int parts, int lane, RowSum& r) {
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+      const int k = min(32, parts - s0);
+      if (s0 > 0) {
+        if (lane < k) x = __ldcg(ml + s0 + lane);
+        outputs(s0, s0 + k, lane);
+      }
+      if (lane >= k) x = make_float2(-INFINITY, 0.f);
+      float mx = x.x;
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, w);
-    r.l += ls;
-    const float4* src = reinterpret_cast<const float4*>(o + (at + s0) * HD) + lane;
-#pragma unroll 8
-    for (int s = 0; s < k; ++s) {
-      const float fs = __shfl_sync(0xffffffffu, f, s);
-      // a part without keys may hold anything: its O was not written
-      if (fs != 0.f) r.add(fs, __ldcg(src + s * (HD / 4)));
+      for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      mx = fmaxf(mx, r.m);
+      if (mx == -INFINITY) continue;
+      r.scale_to(mx);
+      const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - mx);
+      float ls = f == 0.f ? 0.f : x.y * f;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, w);
+      r.l += ls;
+      for (int s = 0; s < k; s += AHEAD) {
+        if (s > 0) outputs(s0 + s, s0 + k, lane);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          const float fs = __shfl_sync(0xffffffffu, f, (s + i) & 31);
+          // a part without keys may hold anything: its O was not written
+          if (s + i < k && fs != 0.f) r.add(fs, v[i]);
+        }
+      }
     }
   }
-}
+};
 
 __device__ __forceinline__ void store_row(bf16* dst, int lane, const RowSum& r) {
   const float i = r.l > 0.f || r.l != r.l ? 1.f / r.l : 0.f;
@@ -431,44 +468,73 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
   uint64_t* empty = full + STAGES;
   volatile uint32_t* stop = reinterpret_cast<volatile uint32_t*>(empty + STAGES);
-  const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x, g = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (!bc_smem(smem, STAGES * STAGE + 256, 1024, threadIdx.x == 0 ? p.status : nullptr)) {
-    grid_dep_wait();
+  // With a prefix kernel before this one, what this one reads is complete: that
+  // kernel waited for it. One CTA's producer waits for the prefix kernel itself,
+  // so that whoever waits for this kernel has waited for both.
+  const bool prefix = p.prefix_parts != 0;
+  const bool waits = prefix && split == p.splits - 1 && g == p.n_kv - 1 && blockIdx.z == gridDim.z - 1;
+  if (!prefix) grid_dep_wait();
+  grid_dep_launch();
+  if (!bc_smem(smem, (uint32_t)(OWN_SMEM - 1024), 1024, threadIdx.x == 0 ? p.status : nullptr)) {
+    if (waits) grid_dep_wait();
     return;
   }
-  if (p.prefix_parts == 0) {  // else the prefix kernel has waited for what came before it
-    grid_dep_wait();
-    grid_dep_launch();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);
+    }
+    *stop = 0;
+    fence_mbar_init();
   }
-  const int pos = __ldcg(p.positions + b);
+  if (warp == 4 && lane == 0) {
+    tma_prefetch_desc(&mapK);
+    tma_prefetch_desc(&mapV);
+    tma_prefetch_desc(&mapK16);
+    tma_prefetch_desc(&mapV16);
+  }
+  int b = blockIdx.z, pos;
+  if (p.sorted) {
+    // the blockIdx.z-th longest sequence, so that the longest start first
+    int* at = reinterpret_cast<int*>(smem + OFF_SORT);
+    for (int i = threadIdx.x; i < SORT_MAX; i += OWN_THREADS)
+      at[i] = i < p.sorted ? __ldcg(p.positions + i) : INT_MIN;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.sorted; i += OWN_THREADS) {
+      const int mine = at[i];
+      int rank = 0;
+      for (int j = 0; j < p.sorted; j += 4) {
+        const int4 x = *reinterpret_cast<const int4*>(at + j);
+        rank += (x.x > mine || (x.x == mine && j < i)) + (x.y > mine || (x.y == mine && j + 1 < i)) +
+                (x.z > mine || (x.z == mine && j + 2 < i)) + (x.w > mine || (x.w == mine && j + 3 < i));
+      }
+      if (rank == b) at[SORT_MAX] = i;
+    }
+    __syncthreads();
+    b = at[SORT_MAX];
+    pos = at[b];
+  } else {
+    pos = __ldcg(p.positions + b);
+  }
+  const int kbeg = p.base + split * p.keys_per_split;
+  // the producer's first page ids, loaded beside the position
+  int page = warp == 4 ? own_page(p, b, kbeg + lane * SUB) : 0;
+  if (!p.sorted) __syncthreads();
   int n = pos + 1;
   if (pos < 0 || pos >= p.key_limit) {
     if (split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
     n = pos < 0 ? 0 : p.key_limit;
   }
-  const int kbeg = p.base + split * p.keys_per_split;
   const int kend = min(n, kbeg + p.keys_per_split);
   const bool any = kend > max(kbeg, p.first);
   if (any) {
-    if (threadIdx.x == 0) {
-      for (int s = 0; s < STAGES; ++s) {
-        mbar_init(&full[s], 1);
-        mbar_init(&empty[s], 4);
-      }
-      *stop = 0;
-      fence_mbar_init();
-    }
-    __syncthreads();
     const int n_tiles = (kend - kbeg + TILE_K - 1) / TILE_K;
     if (warp == 4) {  // ------------------------------------------------ producer
       // The whole warp: lane i looks up the cache row of 16-key step i of the
       // next 32 (one load for their page ids), and lanes 0-15 issue a tile's
       // sixteen small boxes together.
-      if (lane == 0) {
-        tma_prefetch_desc(&mapK);
-        tma_prefetch_desc(&mapV);
-      }
       const uint64_t pol = l2_policy_evict_first();  // own keys are streamed once
       const int n_steps = (kend - kbeg + SUB - 1) / SUB, first_step = max(0, p.first - kbeg) / SUB;
       int s = 0, issued = 0, rows = 0;
@@ -476,7 +542,8 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
       for (int t = 0; t < n_tiles; ++t) {
         if ((t & 7) == 0) {
           const int step = 4 * t + lane;
-          rows = step >= first_step && step < n_steps ? own_kv_row(p, b, g, kbeg + step * SUB) : 0;
+          if (t > 0 && step < n_steps) page = own_page(p, b, kbeg + step * SUB);
+          rows = step >= first_step && step < n_steps ? own_kv_row(p, b, g, kbeg + step * SUB, page) : 0;
         }
         const bool go = !*stop && mbar_wait(&empty[s], ph, p.status);
         if (!__all_sync(0xffffffffu, go)) {
@@ -505,7 +572,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
       // no copy in flight when the CTA exits, whoever gave up
       for (int t = max(0, issued - STAGES); t < issued; ++t)
         mbar_wait(&full[t % STAGES], (t / STAGES) & 1, p.status);
-      if (p.prefix_parts) grid_dep_wait();
+      if (waits) grid_dep_wait();
       return;
     }
     if (KEYS)
@@ -513,19 +580,17 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     else
       consume_heads(p, smem, full, empty, stop, b, g, kbeg, kend, pos, warp, lane);
     consumers_bar();
-    if (*stop && !p.cluster) {
-      if (p.prefix_parts) grid_dep_wait();
-      return;
-    }
+    if (*stop && !p.cluster) return;
   } else if (warp == 4) {  // (a cluster's barriers do not count threads that left)
-    if (p.prefix_parts) grid_dep_wait();
+    if (waits) grid_dep_wait();
     return;
   }
-  if (p.prefix_parts) {  // the partials of the prefix, and the output's last reader
+  if (!any && p.join) return;  // the joining kernel skips this split
+  int parts = 0;
+  if (prefix && !p.join) {
     grid_dep_wait();
-    grid_dep_launch();
+    parts = __ldcg(p.used);
   }
-  if (!any && p.splits > 1 && !p.cluster) return;  // the joining kernel skips this split
   const float* so = reinterpret_cast<const float*>(smem);
   const float* sm = so + 4 * 16 * HD;
   // a cluster's rows: [16][128] outputs, then maximum and sum [16][2]
@@ -552,8 +617,10 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     if (p.cluster) {
       reinterpret_cast<float4*>(mine + r * HD)[lane] = x.o;
       if (lane == 0) *reinterpret_cast<float2*>(mine + 16 * HD + 2 * r) = make_float2(x.m, x.l);
-    } else if (p.splits == 1) {
-      fold(p.part_o, p.part_ml, bh * p.prefix_parts, p.prefix_parts, lane, x);
+    } else if (!p.join) {
+      Parts<8> pre;
+      pre.load(p.part_o, p.part_ml, bh * p.prefix_parts, parts, lane);
+      pre.fold(parts, lane, x);
       store_row(p.out + bh * HD, lane, x);
     } else {
       const size_t at = bh * p.splits + split;
@@ -585,24 +652,31 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
       }
     }
     const size_t bh = (size_t)b * p.n_q + (size_t)g * p.G + r;
-    fold(p.part_o, p.part_ml, bh * p.prefix_parts, p.prefix_parts, lane, x);
+    Parts<8> pre;
+    pre.load(p.part_o, p.part_ml, bh * p.prefix_parts, parts, lane);
+    pre.fold(parts, lane, x);
     store_row(p.out + bh * HD, lane, x);
   }
   cluster_sync_all();  // nobody leaves while its rows are read
 }
 
 // Joins a row's prefix partials and own splits, one warp per (sequence, head).
-__global__ void __launch_bounds__(128) attn_own_join_kernel(OwnParams p, int rows) {
+__global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int rows) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, bh = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (bh >= rows) return;
-  const int pos = p.positions[bh / p.n_q];
+  Parts<8> pre;
+  Parts<2> own;
+  pre.load(p.part_o, p.part_ml, (size_t)bh * p.prefix_parts, p.prefix_parts, lane);
+  own.load(p.own_o, p.own_ml, (size_t)bh * p.splits, p.splits, lane);
+  const int parts = p.prefix_parts ? __ldcg(p.used) : 0;
+  const int pos = __ldcg(p.positions + bh / p.n_q);
   const int n = pos < 0 ? 0 : min(pos + 1, p.key_limit);
   const int used = n > p.first ? min(p.splits, (n - p.base + p.keys_per_split - 1) / p.keys_per_split) : 0;
   RowSum x;
-  fold(p.part_o, p.part_ml, (size_t)bh * p.prefix_parts, p.prefix_parts, lane, x);
-  fold(p.own_o, p.own_ml, (size_t)bh * p.splits, used, lane, x);
+  pre.fold(parts, lane, x);
+  own.fold(used, lane, x);
   store_row(p.out + (size_t)bh * HD, lane, x);
 }
 
@@ -639,9 +713,14 @@ SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, 
   while (pairs * k < 2 * sm_count && k < 128 && keys / (2 * k) >= (k < 8 ? 64 : 256)) k *= 2;
   s.own_splits = k;
   s.keys_per_split = ((keys + k - 1) / k + 63) / 64 * 64;
-  s.cluster = k > 1 && k <= 8;
+  // A long prefix: own CTAs that started beside it leave partials for a joining
+  // kernel, so that others can follow on their SMs. A short one (4 turns): they
+  // wait for it and merge.
+  const int turns = s.alternate ? (s.tiles_per_split + 1) / 2 : s.tiles_per_split;
+  s.join = k > 8 || turns > 4;
+  s.cluster = k > 1 && !s.join;
   const size_t rows = (size_t)B * n_q;
-  s.partials = rows * s.prefix_parts + (s.own_splits > 8 ? rows * s.own_splits : 0);
+  s.partials = rows * s.prefix_parts + (s.join ? rows * s.own_splits : 0);
   return s;
 }
 
@@ -652,8 +731,8 @@ size_t shared_partial_bytes(int max_batch, int n_q, int n_kv, int max_seq, int s
   const size_t rows = (size_t)max_batch * n_q, G = n_q / n_kv;
   const size_t tiles = (size_t)(max_seq + 127) / 128;
   const size_t prefix = std::max(2 * rows, std::min<size_t>(256 * (size_t)sm_count, rows * 2 * tiles));
-  const size_t own = std::min<size_t>(4 * (size_t)sm_count * G, rows * 128);
-  return (prefix + own) * (HD + 2) * sizeof(float);
+  const size_t own = std::max(rows, std::min<size_t>(4 * (size_t)sm_count * G, rows * 128));
+  return (prefix + own) * (HD + 2) * sizeof(float) + 16;
 }
 
 cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStream_t st) {
@@ -679,6 +758,11 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
   p.keys_per_split = s.keys_per_split;
   p.prefix_parts = s.prefix_parts;
   p.cluster = s.cluster;
+  p.join = s.join;
+  p.used = reinterpret_cast<const int*>(a.partial + s.partials * (HD + 2));
+  p.sorted = a.B > 1 && a.B <= SORT_MAX && s.own_splits * a.n_kv * a.B > 3 * a.sm_count
+                 ? a.B
+                 : 0;
   const size_t rows = (size_t)a.B * a.n_q;
   p.part_o = a.partial;
   p.part_ml = p.part_o + s.partials * HD;
@@ -694,7 +778,7 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
                            *a.map_v, *a.map_k16, *a.map_v16, p)
                : launch_kc(attn_own_kernel<false>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
                            *a.map_v, *a.map_k16, *a.map_v16, p);
-  if (e != cudaSuccess || s.own_splits == 1 || s.cluster) return e;
+  if (e != cudaSuccess || !s.join) return e;
   return launch_k(attn_own_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 0, p,
                   (int)rows);
 }
