@@ -73,6 +73,7 @@ struct FormsParams {
   bf16* out;
   const int32_t *cu_rows, *prefix_len;
   int n_rows, n_docs, head_pairs;
+  int out32;                                // out is 32-byte aligned
   // prefix of a decode batch
   const int32_t *positions, *page_table;
   int B, rows_seq;                          // sequences of a row tile (128 / G)
@@ -267,6 +268,13 @@ __device__ __forceinline__ void fma_pair(float& a, float& b, float c, float m) {
       "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(a), "+f"(b)
       : "f"(c), "f"(m));
+}
+
+// 32 aligned bytes: a thread owns a row, so a smaller store would write half a sector
+__device__ __forceinline__ void store_sector(void* dst, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]),
+               "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
 }
 
 __device__ __forceinline__ void half_bar(int id) {  // the two warps that share 32 rows
@@ -930,10 +938,17 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
             tmem_ld_wait();
             if (row_ok) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4*>(dst + q + i) =
-                    make_uint4(pack_bf16(u[i] * inv, u[i + 1] * inv), pack_bf16(u[i + 2] * inv, u[i + 3] * inv),
-                               pack_bf16(u[i + 4] * inv, u[i + 5] * inv), pack_bf16(u[i + 6] * inv, u[i + 7] * inv));
+              for (int i = 0; i < 32; i += 16) {
+                uint32_t x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = pack_bf16(u[i + 2 * k] * inv, u[i + 2 * k + 1] * inv);
+                if (p.out32) {
+                  store_sector(dst + q + i, x);
+                } else {
+                  *reinterpret_cast<uint4*>(dst + q + i) = make_uint4(x[0], x[1], x[2], x[3]);
+                  *reinterpret_cast<uint4*>(dst + q + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                }
+              }
             }
           }
         }
@@ -948,9 +963,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
             tmem_ld_wait();
             if (row_ok) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(p.part_o + at * 128 + 64 * grp + q + i) =
-                    make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+              for (int i = 0; i < 32; i += 8)
+                store_sector(p.part_o + at * 128 + 64 * grp + q + i, reinterpret_cast<const uint32_t*>(u + i));
             }
           }
         }
@@ -1027,6 +1041,7 @@ cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st) {
   const int kind = score_kind(a.sc, &p);
   p.status = a.status;
   p.out = (bf16*)a.out;
+  p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   p.cu_rows = a.cu_rows;
   p.prefix_len = a.prefix_len;
   p.n_rows = a.n_rows;
