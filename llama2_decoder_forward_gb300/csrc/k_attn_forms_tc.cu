@@ -56,7 +56,8 @@ constexpr uint32_t OFF_BAR = SLOTS * TILE;
 // what the two threads of a row exchange: fp32 [2 row tiles][2 halves][128], the
 // tile's maxima, at the end the sums. One buffer is enough: a tile's maxima are
 // read before its P is announced, and the next tile's scores come after that.
-constexpr uint32_t OFF_X = OFF_BAR + 256;
+constexpr uint32_t OFF_WORK = OFF_BAR + 256;  // documents: two published work items, 32 bytes each
+constexpr uint32_t OFF_X = OFF_WORK + 64;
 constexpr size_t FORMS_SMEM = OFF_X + 2 * 2 * 128 * 4;
 constexpr int FORMS_THREADS = 640;
 constexpr int MAXK = 4, MAXV = 2;           // ring sizes at most
@@ -350,42 +351,49 @@ struct FormsWork {
   int split, seq0;      // prefix: key split, first sequence
   int last_rows;        // keys of the last tile; over TN: all
 };
-// The CTA's it-th item; false: no more. share: key tiles of a prefix split.
-template <bool DOCS>
-__device__ __forceinline__ bool forms_work(const FormsParams& p, int it, int share, DocCursor& cursor,
-                                           FormsWork& w) {
-  if (DOCS) {
-    const int per = p.head_pairs ? p.n_q / 2 : p.n_q, rows = p.head_pairs ? TM : 2 * TM;
-    // every other round backwards: whoever had the longest item of one round
-    // gets the shortest of the next
-    const long long item = (long long)it * gridDim.x + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    if (item >= 0x7fffffffll) return false;
-    int b, tile, hx;
-    if (!find_item(p, (int)item, per, cursor, b, tile, w.lo, w.n, hx)) return false;
-    w.q0 = tile * rows;
-    w.h0 = p.head_pairs ? 2 * hx : hx;
-    w.g = w.h0 / p.G;
-    w.pre = p.prefix_len ? min(max(p.prefix_len[b], 0), w.n) : 0;
-    const int last0 = max(min(w.q0 + TM, w.n), w.pre);
-    const int last1 = p.head_pairs ? last0 : w.q0 + TM < w.n ? max(min(w.q0 + 2 * TM, w.n), w.pre) : 0;
-    w.nt0 = (last0 + TN - 1) / TN;
-    w.nt1 = (last1 + TN - 1) / TN;
-    w.kmax = max(last0, last1);
-    w.n_tiles = max(w.nt0, w.nt1);
-    w.t0 = w.split = w.seq0 = 0;
-  } else {
-    if (it > 0) return false;
-    w.lo = w.n = w.q0 = w.pre = w.h0 = 0;
-    w.split = blockIdx.x;
-    w.g = blockIdx.z;
-    w.seq0 = blockIdx.y * p.rows_seq * (p.alternate ? 1 : 2);
-    w.t0 = w.split * share;
-    w.n_tiles = min(share, (p.shared_len + TN - 1) / TN - w.t0);
-    if (w.n_tiles <= 0) return false;
-    w.kmax = p.shared_len;
-    w.nt0 = p.alternate ? (w.n_tiles + 1) / 2 : w.n_tiles;
-    w.nt1 = p.alternate ? w.n_tiles / 2 : w.seq0 + p.rows_seq < p.B ? w.n_tiles : 0;
-  }
+// Documents: what follows from an item's document, first row and head.
+__device__ __forceinline__ void doc_work(const FormsParams& p, int lo, int n, int q0, int pre, int h0, int g,
+                                         FormsWork& w) {
+  w.lo = lo;
+  w.n = n;
+  w.q0 = q0;
+  w.pre = pre;
+  w.h0 = h0;
+  w.g = g;
+  const int last0 = max(min(q0 + TM, n), pre);
+  const int last1 = p.head_pairs ? last0 : q0 + TM < n ? max(min(q0 + 2 * TM, n), pre) : 0;
+  w.nt0 = (last0 + TN - 1) / TN;
+  w.nt1 = (last1 + TN - 1) / TN;
+  w.kmax = max(last0, last1);
+  w.n_tiles = max(w.nt0, w.nt1);
+  w.t0 = w.split = w.seq0 = 0;
+  w.last_rows = w.kmax - (w.n_tiles - 1) * TN;
+}
+// The CTA's it-th document item; false: no more.
+__device__ __forceinline__ bool next_doc(const FormsParams& p, int it, DocCursor& cursor, FormsWork& w) {
+  const int per = p.head_pairs ? p.n_q / 2 : p.n_q, rows = p.head_pairs ? TM : 2 * TM;
+  // every other round backwards: whoever had the longest item of one round
+  // gets the shortest of the next
+  const long long item = (long long)it * gridDim.x + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  if (item >= 0x7fffffffll) return false;
+  int b, tile, hx, lo, n;
+  if (!find_item(p, (int)item, per, cursor, b, tile, lo, n, hx)) return false;
+  const int h0 = p.head_pairs ? 2 * hx : hx;
+  doc_work(p, lo, n, tile * rows, p.prefix_len ? min(max(p.prefix_len[b], 0), n) : 0, h0, h0 / p.G, w);
+  return true;
+}
+// The CTA's prefix item; false: the splits end before this one. share: key tiles of a split.
+__device__ __forceinline__ bool prefix_work(const FormsParams& p, int share, FormsWork& w) {
+  w.lo = w.n = w.q0 = w.pre = w.h0 = 0;
+  w.split = blockIdx.x;
+  w.g = blockIdx.z;
+  w.seq0 = blockIdx.y * p.rows_seq * (p.alternate ? 1 : 2);
+  w.t0 = w.split * share;
+  w.n_tiles = min(share, (p.shared_len + TN - 1) / TN - w.t0);
+  if (w.n_tiles <= 0) return false;
+  w.kmax = p.shared_len;
+  w.nt0 = p.alternate ? (w.n_tiles + 1) / 2 : w.n_tiles;
+  w.nt1 = p.alternate ? w.n_tiles / 2 : w.seq0 + p.rows_seq < p.B ? w.n_tiles : 0;
   w.last_rows = w.kmax - (w.t0 + w.n_tiles - 1) * TN;
   return true;
 }
@@ -445,11 +453,14 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   uint64_t* pready = sfull + 2;     // [2][2] each part of P_j is, and O is rescaled
   uint64_t* fin = pready + 4;       // [2] the row tile's last O += P V is done
   uint64_t* drained = fin + 2;      // [2] every MMA of the issuer is done
+  uint64_t* wfull = drained + 2;    // [2] a work item is published, [2] every other warp has read it
+  uint64_t* wempty = wfull + 2;
   // tensor memory, abort, and the turns at the tensor pipe that each issuer has
   // had (counts, because a phase bit could be lapped); a prefix split's key tiles
-  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(drained + 2);
+  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(wempty + 2);
   volatile uint32_t* stop = ctl + 1;
-  static_assert((2 + 2 * MAXK + 2 * MAXV + 1 + 10) * 8 + 20 <= 256, "barrier block");
+  static_assert((2 + 2 * MAXK + 2 * MAXV + 1 + 10 + 4) * 8 + 20 <= 256, "barrier block");
+  volatile int4* box = reinterpret_cast<volatile int4*>(smem + OFF_WORK);
   grid_dep_wait();
   grid_dep_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -482,6 +493,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       mbar_init(&pready[2 * t + 1], 8);
       mbar_init(&fin[t], 1);
       mbar_init(&drained[t], 1);
+      mbar_init(&wfull[t], 1);
+      mbar_init(&wempty[t], FORMS_THREADS / 32 - 1);
     }
     ctl[1] = ctl[2] = ctl[3] = 0;
     fence_mbar_init();
@@ -502,10 +515,23 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   const int share = DOCS ? 0 : __shfl_sync(0xffffffffu, ctl[4], 0);
 
   // launched with 640 x 96 registers: 512 x 104 + 128 x 64
+  // The it-th work item, as the Q and K producer published it: the walk to it
+  // costs some 3000 cycles, which in every warp delayed each item's start.
+  auto work = [&](int it, FormsWork& w) -> bool {
+    if (!DOCS) return it == 0 && prefix_work(p, share, w);
+    const int s = it & 1;
+    const bool ok = __all_sync(0xffffffffu, wait_bar(&wfull[s], (it >> 1) & 1, stop, p.status));
+    const int lo = box[2 * s].x, n = box[2 * s].y, q0 = box[2 * s].z, pre = box[2 * s].w;
+    const int h0 = box[2 * s + 1].x, g = box[2 * s + 1].y;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&wempty[s]);
+    if (!ok || n == 0) return false;
+    doc_work(p, lo, n, q0, pre, h0, g, w);
+    return true;
+  };
   if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    DocCursor cursor;
-    FormsWork w;
+    FormsWork w{};
     if (warp == 16) {  // ------------------------------------------- Q and K producer
       if (lane == 0) {
         tma_prefetch_desc(&mapQ);
@@ -514,8 +540,28 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       Ring r(KR);
       int issued = 0, loaded_q = 0, rows = 0;
       bool ok = true;
-      for (int it = 0; ok && forms_work<DOCS>(p, it, share, cursor, w); ++it) {
-        if (!DOCS) rows = tile_rows(p, w.g, w.t0, w.kmax, lane);
+      DocCursor cursor;
+      for (int it = 0; ok; ++it) {
+        if (DOCS) {
+          const bool more = next_doc(p, it, cursor, w);
+          ok = __all_sync(0xffffffffu, wait_bar(&wempty[it & 1], ((it >> 1) & 1) ^ 1, stop, p.status));
+          if (!ok) break;
+          if (lane == 0) {
+            volatile int4* to = box + 2 * (it & 1);
+            to->x = w.lo;
+            to->y = more ? w.n : 0;  // an item's document is never empty
+            to->z = w.q0;
+            to->w = w.pre;
+            to[1].x = w.h0;
+            to[1].y = w.g;
+            mbar_arrive(&wfull[it & 1]);
+          }
+          __syncwarp();
+          if (!more) break;
+        } else {
+          if (it > 0 || !prefix_work(p, share, w)) break;
+          rows = tile_rows(p, w.g, w.t0, w.kmax, lane);
+        }
         ok = __all_sync(0xffffffffu, wait_bar(qempty, (it & 1) ^ 1, stop, p.status));
         if (!ok) break;
         ++loaded_q;
@@ -554,7 +600,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       uint32_t ph_land = 0;
       int rows = 0;
       bool ok = true;
-      for (int it = 0; ok && forms_work<DOCS>(p, it, share, cursor, w); ++it) {
+      for (int it = 0; ok && work(it, w); ++it) {
         for (int j = 0; ok && j < w.n_tiles; ++j) {
           if (!DOCS && (j & 3) == 0) rows = tile_rows(p, w.g, w.t0 + j, w.kmax, lane);
           ok = __all_sync(0xffffffffu, wait_bar(&vempty[r.slot], r.phase ^ 1, stop, p.status));
@@ -616,7 +662,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       // every wait returns at once, the rest runs on whatever is there, and
       // nothing is stored. Checks and votes between the waits and the MMAs
       // measured 5-15 % on all cases.
-      for (int it = 0; forms_work<DOCS>(p, it, share, cursor, w); ++it) {
+      for (int it = 0; work(it, w); ++it) {
         const int count = t ? w.nt1 : w.nt0, others = t ? w.nt0 : w.nt1;
         auto score = [&](int slot, bool last) {  // S of a key tile
           const uint64_t kd = kd0 + (uint64_t)(slot * (TILE >> 4));
@@ -724,11 +770,10 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     const float c = p.scale * kLog2e;
     const float cl = p.cap * kLog2e, yk = CAP ? p.scale / p.cap : 0.f;
     const float ct = KIND == KCap ? cl : c;  // log2 units of a raw score (of tanh)
-    DocCursor cursor;
-    FormsWork w;
+    FormsWork w{};
     uint32_t ph_s = 0, ph_fin = 0;  // phases of sfull, fin
 #pragma unroll 1
-    for (int it = 0; forms_work<DOCS>(p, it, share, cursor, w); ++it) {
+    for (int it = 0; work(it, w); ++it) {
     const int count = t ? w.nt1 : w.nt0;
     if (DOCS && count == 0) continue;
     // this row: its position, its visible keys, where it goes
