@@ -4,39 +4,49 @@
 //
 //   x = scale q.k;  s = (cap tanh(x / cap) or x) - slope |i - j|;  p = softmax(s);  o = sum p v
 //
-// One pass over the keys with the running maximum and sum of each row
-// (FlashAttention): the scores never leave the SM. One CTA per SM works on two
-// tiles of 128 query rows (MMA M, one tensor-memory lane per row) against key
-// tiles of 128:
+// One pass over the keys with the running maximum and sum of each row: the
+// scores never leave the SM. One CTA per SM works on two tiles of 128 query rows
+// (MMA M, one tensor-memory lane per row) against key tiles of 128:
 //   warps 0-7, 8-15  softmax of row tile 0 and 1: two threads per row, one for
 //                    keys 0-63 of a tile and output dims 0-63, one for the rest;
 //   warp 16, 17      TMA producers of Q + K and of V (rings of 32 KB tiles);
 //   warp 18, 19      issue the MMAs of row tile 0 and 1.
 // A turn of an issuer is O += P_j V_j, then S_{j+1} = Q K^T_{j+1}; the turns
-// alternate between the row tiles by counts of them, so while one tile's softmax runs on
-// the CUDA cores the tensor cores work for the other. (Without the order the
-// tensor pipe interleaves the two tiles' MMAs, both softmaxes then run at the
-// same time, and the pipe idles meanwhile; with one issuer for both, its waits
-// between turns leave the pipe idle.) tcgen05 operations of one thread execute
-// in order: P_j (bf16, written over the scores it came from) is read before
-// S_{j+1} replaces it, and the arrival of S_{j+1} also says that O += P_j V_j is
-// done. Tensor memory: per row
-// tile 128 columns of S / P and 128 of O, all 512.
+// alternate between the row tiles, so while one tile's softmax runs on the CUDA
+// cores the tensor cores work for the other. (Without that order the tensor pipe
+// interleaves the two tiles' MMAs, both softmaxes then run at the same time, and
+// the pipe idles meanwhile; with one issuer for both, its waits between turns
+// leave the pipe idle.) tcgen05 operations of one thread execute in order: P_j
+// (bf16, written over the scores it came from) is read before S_{j+1} replaces
+// it, and the arrival of S_{j+1} also says that O += P_j V_j is done. Tensor
+// memory: per row tile 128 columns of S / P and 128 of O, all 512.
 // The two row tiles are
 //   documents, n_q / n_kv even : two query heads of one K/V head, same rows;
 //   documents, else            : rows q0 .. q0+127 and q0+128 .. q0+255;
 //   prefix, over 128 rows      : two blocks of (sequence, head of the group) rows;
 //   prefix, up to 128 rows     : the same rows; tile t takes every second key tile
 //                                (two key splits; each K/V tile has one reader).
-// so K and V are loaded once for both. Documents run as one CTA per SM that takes
-// gridDim-th part of the work items: its producers load the next item's Q, K and V while the
-// softmax and the store of the last one go on, and barriers and tensor memory
-// are set up once (17 packed documents of 8192 rows, 64 heads: 246 us with a CTA
-// per item, 216 us so). Every mask here is "keys below a row's
+// so K and V are loaded once for both. Every mask here is "keys below a row's
 // limit": max(position + 1, prefix) for documents, the sequence's keys for the
 // prefix. O is rescaled lazily, when a row's maximum grows by more than 2^8.
-// P is rounded once to bf16 (V's type, which the MMA shares); the sum that
-// normalises it is taken in fp32 before that.
+//
+// Documents run as one CTA per SM that takes its share of the work items: the
+// producers load the next item's Q, K and V while the softmax and the store of
+// the last one go on, and barriers and tensor memory are set up once (17 packed
+// documents of 8192 rows, 64 heads: 246 us with a CTA per item, 216 us so, and
+// 160 us with the items dealt out longest first and published by one warp, and
+// whole sectors stored).
+//
+// P is rounded once to bf16 (V's type, which the MMA shares), and the sum that
+// normalises it is that of the rounded weights, in fp32: what the dominant keys
+// of a row lose by rounding cancels (error against 64 bits, relative to the
+// outputs' root mean square: 0.0018 instead of 0.0022; rounding the output alone
+// is 0.0016). The add takes a bf16 operand, so it costs nothing beside the sum of
+// the unrounded weights but its latency (1 %; unpacked first, 6 %).
+//
+// What bounds it: plain scores, the tensor pipe and the hand-overs between it
+// and the softmax (2640 cycles per pair of turns, 2048 of them MMAs); capped and
+// biased ones the issue slots of the softmax (3200 and more).
 #include <algorithm>
 #include <climits>
 
@@ -269,6 +279,14 @@ __device__ __forceinline__ void fma_pair(float& a, float& b, float c, float m) {
       "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(a), "+f"(b)
       : "f"(c), "f"(m));
+}
+
+// a += low half of the bf16 pair x, b += its high half
+__device__ __forceinline__ void add_pair(float& a, float& b, uint32_t x) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(x));
 }
 
 // 32 aligned bytes: a thread owns a row, so a smaller store would write half a sector
@@ -906,9 +924,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           }
           e0 = ex2(e0);  // hidden: -inf -> 0
           e1 = ex2(e1);
-          ls[i & 2] += e0;
-          ls[(i & 2) + 1] += e1;
           w[i / 2] = pack_bf16(e0, e1);
+          add_pair(ls[i & 2], ls[(i & 2) + 1], w[i / 2]);
         }
         tmem_st16(sc + q / 2, w);
         tmem_st_wait();

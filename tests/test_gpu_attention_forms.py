@@ -8,7 +8,9 @@ for bf16, 2^-24 for fp32, 2^-4 for E4M3 (2^-10 absolute below its normals).
 * Rows: bf16 outputs are one rounding of an fp32 value whose own error is
   some 2^-24 of the head's largest value: 2^-8 |ref| + 2^-18 max|head|.
 * Attention, bf16: the output's rounding, 2^-8 |ref|; the weights are rounded
-  once for the tensor cores, 2^-8 of sum p|v|; scores carry fp32 sums of 128
+  once for the tensor cores, 2^-8 of sum p|v| (where the rounded weights are
+  also the ones that are summed, the mean o moves by sum p e (v - o), |e| <= 2^-8,
+  so sum p|v - o| stands there: the same for values of both signs); scores carry fp32 sums of 128
   products, below 2^-11 at these magnitudes, which moves every weight by that
   and the normalising sum by as much: 2^-10 of sum p|v|.
 * Attention, fp32: a score is off by at most (d + 8) 2^-24 sum|q k| scale plus
