@@ -89,14 +89,14 @@ struct FormsParams {
   const int32_t *positions, *page_table;
   int B, rows_seq;                          // sequences of a row tile (128 / G)
   int alternate;                            // both row tiles hold the same rows
-  int layer, page_size, capacity, batch_cap, n_pages, max_pages, box_rows;
+  int layer, page_size, capacity, n_pages, max_pages, box_rows;
   int key_limit, shared_len, shared_seq;
   float *part_o, *part_ml;                  // [B n_q][splits][128], [B n_q][splits][2] (max log2, sum)
   int splits;                               // partials a row has room for
   int *used;                                // how many of them are written
   int sm_count;
   int waiting;                              // the own keys' CTAs wait for this kernel
-  float own_items;                          // how many of them there are
+  float own_items;                          // how many those are
   float poly[13];                           // KCapFixed: kTanh times powers of scale / cap
 };
 
@@ -1132,7 +1132,6 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
   p.layer = a.layer;
   p.page_size = a.page_size;
   p.capacity = a.capacity;
-  p.batch_cap = a.batch_cap;
   p.n_pages = a.n_pages;
   p.max_pages = a.max_pages;
   p.box_rows = a.box_rows;

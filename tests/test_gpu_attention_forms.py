@@ -543,6 +543,43 @@ def test_shared_bf16_long_splits():
     _shared_case(4, 4, 128, "bf16", [5000], 0, page=0, bias=True)
 
 
+def test_shared_join_after_a_long_prefix():
+    # the own keys' blocks leave partials: both row tiles with the same rows, and two blocks of rows;
+    # own keys none, few and many, a position inside the prefix
+    _shared_case(40, 40, 128, "bf16", [3299, 3163, 90], 3160, page=64, cap=20.0)
+    _shared_case(40, 40, 128, "bf16", [3159, 3400], 3160, page=0, seq=2)
+    _shared_case(640, 40, 128, "bf16", [1700 + 11 * b for b in range(8)] + [1500], 1700, page=64, bias=True)
+
+
+def test_shared_longest_first():
+    # more blocks than are resident: taken by length, with ties and the shortest of all
+    g = _gen(9)
+    pos = torch.randint(0, 200, (62,), generator=g).tolist()
+    pos[3] = pos[40] = pos[41] = 199
+    pos[7] = 0
+    _shared_case(8, 8, 128, "bf16", pos, 0, page=16)
+    _shared_case(16, 8, 128, "bf16", [p + 70 for p in pos], 70, page=0, cap=30.0, bias=True)
+
+
+def test_shared_longest_first_beside_bad_positions():
+    m, shape = _model(8, 8, max_batch=64, max_seq=128)
+    q = _randn((64, 8, 128), torch.bfloat16, 190).cuda()
+    k, v = (_randn((1, 64, 8, 128, 128), torch.bfloat16, 191 + i).cuda() for i in range(2))
+    kv = binding.KVCache(shape, batch=64, capacity=128, k=k, v=v)
+    out, want = (torch.full((64, 1024), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pos = [(37 * b) % 128 for b in range(64)]
+    m.op_attention_decode_shared(q, _i32(pos), 0, kv, want)
+    m.sync()
+    bad = list(pos)
+    bad[5], bad[6], bad[50] = -1, -2 ** 31, 2 ** 31 - 1
+    m.op_attention_decode_shared(q, _i32(bad), 0, kv, out)
+    rc, flags = m.sync_status()
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE
+    assert torch.all(out[[5, 6]] == 0)
+    keep = [b for b in range(64) if b not in (5, 6, 50)]
+    assert torch.equal(out[keep], want[keep])
+
+
 def test_shared_second_layer():
     _shared_case(4, 2, 128, "bf16", [90, 70], 40, layers=3, layer=2)
 
