@@ -52,7 +52,7 @@ constexpr uint32_t HALF = TILE_K * 128;         // 64 keys x 64 dims: 8 KB
 constexpr uint32_t STAGE = 4 * HALF;            // K and V, two dim halves each
 constexpr int SORT_MAX = 256;                   // sequences that a CTA sorts
 constexpr uint32_t OFF_SORT = STAGES * STAGE + 256;
-constexpr size_t OWN_SMEM = OFF_SORT + (SORT_MAX + 4) * 4 + 1024;
+constexpr size_t OWN_SMEM = OFF_SORT + (2 * SORT_MAX + 4) * 4 + 1024;
 static_assert((4 * 16 * HD + 128) * 4 <= STAGES * STAGE, "the merge area aliases the ring");
 
 struct OwnParams {
@@ -507,18 +507,23 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   }
   int b = blockIdx.z, pos;
   if (p.sorted) {
-    // the blockIdx.z-th longest sequence, so that the longest start first
-    int* at = reinterpret_cast<int*>(smem + OFF_SORT);
-    for (int i = threadIdx.x; i < SORT_MAX; i += OWN_THREADS)
-      at[i] = i < p.sorted ? __ldcg(p.positions + i) : INT_MIN;
+    // the blockIdx.z-th longest sequence, so that the longest start first: one key
+    // of 32 bits per sequence, its length and (ties) its number
+    int* key = reinterpret_cast<int*>(smem + OFF_SORT);
+    int* at = key + SORT_MAX;
+    for (int i = threadIdx.x; i < SORT_MAX; i += OWN_THREADS) {
+      const int x = i < p.sorted ? __ldcg(p.positions + i) : -1;
+      at[i] = x;
+      key[i] = i < p.sorted ? (max(min(x, p.key_limit - 1), -1) + 1) * SORT_MAX + SORT_MAX - 1 - i : -1;
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < p.sorted; i += OWN_THREADS) {
-      const int mine = at[i];
+      const int mine = key[i];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < p.sorted; j += 4) {
-        const int4 x = *reinterpret_cast<const int4*>(at + j);
-        rank += (x.x > mine || (x.x == mine && j < i)) + (x.y > mine || (x.y == mine && j + 1 < i)) +
-                (x.z > mine || (x.z == mine && j + 2 < i)) + (x.w > mine || (x.w == mine && j + 3 < i));
+        const int4 x = *reinterpret_cast<const int4*>(key + j);
+        rank += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
       }
       if (rank == b) at[SORT_MAX] = i;
     }
@@ -770,7 +775,13 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
   p.cluster = s.cluster;
   p.join = s.join;
   p.used = reinterpret_cast<const int*>(a.partial + s.partials * (HD + 2));
-  p.sorted = a.B > 1 && a.B <= SORT_MAX && s.own_splits * a.n_kv * a.B > 3 * a.sm_count
+  // Longest first where there are more CTAs than resident ones, unless they are too
+  // short for it: each CTA looks at all positions. Sorted and in order, 8 K/V heads:
+  // 128 sequences of up to 512 keys 21.5 and 19.5 us, 256 of up to 1024 73 and 54 us,
+  // 200 of up to 2000 78 and 82 us; 128 of up to 3500 (and a prefix) 168 and 180 us.
+  const bool waves = s.own_splits * a.n_kv * a.B > 3 * a.sm_count;
+  p.sorted = waves && a.B > 1 && a.B <= SORT_MAX && s.keys_per_split >= 8 * a.B &&
+                     a.key_limit < INT_MAX / SORT_MAX
                  ? a.B
                  : 0;
   const size_t rows = (size_t)a.B * a.n_q;
