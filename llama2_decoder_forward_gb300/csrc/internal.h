@@ -301,7 +301,8 @@ struct SharedPlan {
   int alternate;        // one row tile: the two halves of a CTA share its keys
   int row_blocks, tiles_per_split, prefix_splits;
   int prefix_parts;     // partials per row of the prefix kernel (0: no prefix)
-  int base, own_splits, keys_per_split;
+  int base, keys;       // own keys start in the tile at base, and are `keys` at most
+  int own_splits, min_share;  // key splits, and the keys that a split has at least
   int cluster;          // the own splits of a row form a thread-block cluster
   int join;             // own splits leave partials, which a joining kernel merges
   size_t partials;      // partial rows in all

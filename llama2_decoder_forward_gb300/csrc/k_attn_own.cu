@@ -19,8 +19,10 @@
 // 1 to 3500 keys over 16384 shared ones: 180 -> 168 us). Up to 8 key splits of a
 // (K/V head, sequence) form a thread-block cluster and merge through distributed
 // shared memory; more (few sequences with very long contexts) leave partials for
-// a joining kernel. One sequence, 466 keys, 32 K/V heads: 8.7 us unsplit, 5.8 us
-// as clusters of 8.
+// a joining kernel. The splits share the keys that a sequence has, not those that
+// the cache has room for (8 sequences of up to 4000 keys, 8 K/V heads: 18.7 ->
+// 16.1 us). One sequence, 466 keys, 32 K/V heads: 8.7 us unsplit, 5.8 us as
+// clusters of 8.
 //
 // Beside a prefix: the launch follows the prefix kernel's and starts on the SMs
 // that it leaves free. That kernel lets it start only after its own wait, so
@@ -64,7 +66,7 @@ struct OwnParams {
   int page_size, capacity, n_pages, max_pages, box_rows;
   int key_limit, first;        // keys from `first` on; position limit
   int base;                    // first rounded down to a tile
-  int splits, keys_per_split, cluster;
+  int splits, min_share, cluster;  // a split has at least min_share keys
   int sorted;                  // sequences (B) to take longest first; 0: in order
   int prefix_parts;            // partials per row of the prefix kernel, at most
   const int* used;             // how many it wrote
@@ -77,6 +79,12 @@ struct OwnParams {
 
 __device__ __forceinline__ void consumers_bar() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
+// Keys of a split, a multiple of 64: the n - base that there are, shared evenly.
+__device__ __forceinline__ int own_share(const OwnParams& p, int n) {
+  if (p.splits == 1) return INT_MAX - p.base;
+  const int keys = max(n - p.base, 1);
+  return max(p.min_share, ((keys + p.splits - 1) / p.splits + 63) & ~63);
+}
 // Page id of key k0 of sequence b (-1: past its table), and the cache row there.
 __device__ __forceinline__ int own_page(const OwnParams& p, int b, int k0) {
   const int pi = p.page_size == 0 ? 0 : k0 / p.page_size;
@@ -533,16 +541,16 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   } else {
     pos = __ldcg(p.positions + b);
   }
-  const int kbeg = p.base + split * p.keys_per_split;
-  // the producer's first page ids, loaded beside the position
-  int page = warp == 4 ? own_page(p, b, kbeg + lane * SUB) : 0;
+  // the producer's first page ids, without splits loaded beside the position
+  int page = warp == 4 && p.splits == 1 ? own_page(p, b, p.base + lane * SUB) : 0;
   if (!p.sorted) __syncthreads();
   int n = pos + 1;
   if (pos < 0 || pos >= p.key_limit) {
     if (split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
     n = pos < 0 ? 0 : p.key_limit;
   }
-  const int kend = min(n, kbeg + p.keys_per_split);
+  const int share = own_share(p, n), kbeg = p.base + split * share;
+  const int kend = min(n, kbeg + share);
   const bool any = kend > max(kbeg, p.first);
   if (any) {
     const int n_tiles = (kend - kbeg + TILE_K - 1) / TILE_K;
@@ -557,7 +565,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
       for (int t = 0; t < n_tiles; ++t) {
         if ((t & 7) == 0) {
           const int step = 4 * t + lane;
-          if (t > 0 && step < n_steps) page = own_page(p, b, kbeg + step * SUB);
+          if ((t > 0 || p.splits > 1) && step < n_steps) page = own_page(p, b, kbeg + step * SUB);
           rows = step >= first_step && step < n_steps ? own_kv_row(p, b, g, kbeg + step * SUB, page) : 0;
         }
         const bool go = !*stop && mbar_wait(&empty[s], ph, p.status);
@@ -688,7 +696,11 @@ __global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int 
   const int parts = p.prefix_parts ? __ldcg(p.used) : 0;
   const int pos = __ldcg(p.positions + bh / p.n_q);
   const int n = pos < 0 ? 0 : min(pos + 1, p.key_limit);
-  const int used = n > p.first ? min(p.splits, (n - p.base + p.keys_per_split - 1) / p.keys_per_split) : 0;
+  int used = n > p.first;  // own splits that have keys
+  if (used && p.splits > 1) {
+    const int share = own_share(p, n);
+    used = (n - p.base + share - 1) / share;
+  }
   RowSum x;
   pre.fold(parts, lane, x);
   own.fold(used, lane, x);
@@ -721,13 +733,16 @@ SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, 
     s.prefix_parts = s.prefix_splits * (s.alternate ? 2 : 1);
   }
   // own keys: split while two CTAs per SM are not reached and a split keeps 64
-  // keys (one tile), beyond a cluster's 8 CTAs 256 (its partials are read again)
+  // keys (one tile); where a cluster's 8 CTAs do not reach them, as many as are
+  // resident, with 256 keys (their partials are read again)
   s.base = shared_len / 64 * 64;
   const int keys = std::max(1, key_limit - s.base), pairs = B * n_kv;
   int k = 1;
-  while (pairs * k < 2 * sm_count && k < 128 && keys / (2 * k) >= (k < 8 ? 64 : 256)) k *= 2;
+  while (pairs * k < 2 * sm_count && k < 8 && keys / (2 * k) >= 64) k *= 2;
+  if (k == 8 && pairs * k < 2 * sm_count) k = std::max(k, std::min({128, 3 * sm_count / pairs, keys / 256}));
+  s.keys = keys;
   s.own_splits = k;
-  s.keys_per_split = ((keys + k - 1) / k + 63) / 64 * 64;
+  s.min_share = k > 8 ? 256 : 64;
   // A long prefix: own CTAs that started beside it leave partials for a joining
   // kernel, so that others can follow on their SMs. A short one (4 turns): they
   // wait for it and merge.
@@ -742,7 +757,7 @@ SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, 
 size_t shared_partial_bytes(int max_batch, int n_q, int n_kv, int max_seq, int sm_count) {
   // shared_plan's partials over every batch up to max_batch and every prefix:
   // prefix parts are at most 256 rows a CTA at one CTA per SM, or two per row;
-  // own splits double only below 2 CTAs per SM
+  // own splits stay below 4 CTAs per SM
   const size_t rows = (size_t)max_batch * n_q, G = n_q / n_kv;
   const size_t tiles = (size_t)(max_seq + 127) / 128;
   const size_t prefix = std::max(2 * rows, std::min<size_t>(256 * (size_t)sm_count, rows * 2 * tiles));
@@ -770,7 +785,7 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
   p.first = a.shared_len;
   p.base = s.base;
   p.splits = s.own_splits;
-  p.keys_per_split = s.keys_per_split;
+  p.min_share = s.min_share;
   p.prefix_parts = s.prefix_parts;
   p.cluster = s.cluster;
   p.join = s.join;
@@ -780,7 +795,7 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
   // 128 sequences of up to 512 keys 21.5 and 19.5 us, 256 of up to 1024 73 and 54 us,
   // 200 of up to 2000 78 and 82 us; 128 of up to 3500 (and a prefix) 168 and 180 us.
   const bool waves = s.own_splits * a.n_kv * a.B > 3 * a.sm_count;
-  p.sorted = waves && a.B > 1 && a.B <= SORT_MAX && s.keys_per_split >= 8 * a.B &&
+  p.sorted = waves && a.B > 1 && a.B <= SORT_MAX && s.keys / s.own_splits > 7 * a.B &&
                      a.key_limit < INT_MAX / SORT_MAX
                  ? a.B
                  : 0;

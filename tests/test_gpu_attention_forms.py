@@ -554,20 +554,20 @@ def test_shared_join_after_a_long_prefix():
 def test_shared_longest_first():
     # more blocks than are resident: taken by length, with ties and the shortest of all
     g = _gen(9)
-    pos = torch.randint(0, 200, (62,), generator=g).tolist()
-    pos[3] = pos[40] = pos[41] = 199
+    pos = torch.randint(0, 200, (58,), generator=g).tolist()
+    pos[3] = pos[40] = pos[41] = 479
     pos[7] = 0
     _shared_case(8, 8, 128, "bf16", pos, 0, page=16)
     _shared_case(16, 8, 128, "bf16", [p + 70 for p in pos], 70, page=0, cap=30.0, bias=True)
 
 
 def test_shared_longest_first_beside_bad_positions():
-    m, shape = _model(8, 8, max_batch=64, max_seq=128)
-    q = _randn((64, 8, 128), torch.bfloat16, 190).cuda()
-    k, v = (_randn((1, 64, 8, 128, 128), torch.bfloat16, 191 + i).cuda() for i in range(2))
-    kv = binding.KVCache(shape, batch=64, capacity=128, k=k, v=v)
-    out, want = (torch.full((64, 1024), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
-    pos = [(37 * b) % 128 for b in range(64)]
+    m, shape = _model(8, 8, max_batch=58, max_seq=480)
+    q = _randn((58, 8, 128), torch.bfloat16, 190).cuda()
+    k, v = (_randn((1, 58, 8, 480, 128), torch.bfloat16, 191 + i).cuda() for i in range(2))
+    kv = binding.KVCache(shape, batch=58, capacity=480, k=k, v=v)
+    out, want = (torch.full((58, 1024), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pos = [(37 * b) % 480 for b in range(58)]
     m.op_attention_decode_shared(q, _i32(pos), 0, kv, want)
     m.sync()
     bad = list(pos)
@@ -576,7 +576,7 @@ def test_shared_longest_first_beside_bad_positions():
     rc, flags = m.sync_status()
     assert rc == 5 and flags == binding.FLAG_POS_RANGE
     assert torch.all(out[[5, 6]] == 0)
-    keep = [b for b in range(64) if b not in (5, 6, 50)]
+    keep = [b for b in range(58) if b not in (5, 6, 50)]
     assert torch.equal(out[keep], want[keep])
 
 
