@@ -18,6 +18,9 @@ for bf16, 2^-24 for fp32, 2^-4 for E4M3 (2^-10 absolute below its normals).
   roundings of the sums and exponentials, act on sum p|v|.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -829,3 +832,18 @@ def test_refusals():
                                 torch.zeros(2, 128, device="cuda"))
     m.sync()
     m32.sync()
+
+
+# --------------------------------------------------------------------------- checked build
+def test_suite_passes_on_the_bounds_check_build():
+    # every kernel checks its shared-memory layout and index invariants there
+    need_gpu()
+    if os.environ.get("LLAMA_GB300_BOUNDS_CHECK") == "1":
+        pytest.skip("this is that run")
+    from llama2_decoder_forward_gb300 import build
+    build.build_library(checked=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", os.path.abspath(__file__)],
+                       cwd=root, env=dict(os.environ, LLAMA_GB300_BOUNDS_CHECK="1"), capture_output=True, text=True,
+                       timeout=1200)
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
