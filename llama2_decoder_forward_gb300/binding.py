@@ -264,6 +264,7 @@ class Rope:
         elif rotary_dim is None:
             raise ValueError("Rope: without a table give rotary_dim (the head size)")
         self.table = table
+        self._dev = None if table is None else table.get_device()
         self._c = _Rope(layout, rotary_dim, None if table is None else table.data_ptr(),
                         0 if table is None else table.shape[0])
         self._ref = ctypes.byref(self._c)
@@ -282,13 +283,13 @@ class Scores:
         self._ref = ctypes.byref(self._c)
 
 
-def _need(what, t, dtype, n):
+def _need(what, t, dtype, n, dev):
     """The tensor's address; ValueError unless it is a contiguous tensor of that
-    type and element count on the device."""
-    if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+    type and element count on device number dev."""
+    if t.dtype is dtype and t.get_device() == dev and t.numel() == n and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError("%s: want a contiguous device tensor of %d %s, got %s %s%s%s" %
-                     (what, n, dtype, tuple(t.shape), t.dtype, "" if t.is_cuda else " on the CPU",
+    raise ValueError("%s: want a contiguous tensor of %d %s on cuda:%d, got %s %s on %s%s" %
+                     (what, n, dtype, dev, tuple(t.shape), t.dtype, t.device,
                       "" if t.is_contiguous() else " (strided)"))
 
 
@@ -323,15 +324,18 @@ class KVCache:
         self._c = self.struct()
         self._ref = ctypes.byref(self._c)
 
-    def _now(self):
+    def _now(self, dev):
         """The kept C struct (the layout is fixed at construction) with the tensors'
-        present addresses and the scales."""
-        c = self._c
+        present addresses and the scales; ValueError unless they are on device dev."""
+        c, pt = self._c, self.page_table
+        if self.k.get_device() != dev or self.v.get_device() != dev or \
+                (pt is not None and pt.get_device() != dev):
+            raise ValueError("cache: not on cuda:%d" % dev)
         c.k = self.k.data_ptr()
         c.v = self.v.data_ptr()
         c.k_scale, c.v_scale = self.k_scale, self.v_scale
-        if self.page_table is not None:
-            c.page_table = self.page_table.data_ptr()
+        if pt is not None:
+            c.page_table = pt.data_ptr()
         return self._ref
 
     def struct(self) -> KV:
@@ -387,6 +391,7 @@ class Model:
         self._shared = l.llama_op_attention_decode_shared
         self._dt, self._qkv_rows = shape.torch_dtype, shape.qkv_rows
         self._i32, self._f32 = torch.int32, torch.float32
+        self._dev = torch.cuda.current_device() if torch.cuda.is_available() else 0
 
     def __del__(self):
         ctx = getattr(self, "ctx", None)
@@ -526,23 +531,25 @@ class Model:
         strided; start_pos int32 [B]; cu_rows int32 [B + 1], or None for one row
         per sequence; eps defaults to the model's rms_eps."""
         s, dt = self.shape, self._dt
-        i32, f32 = self._i32, self._f32
+        i32, f32, dev = self._i32, self._f32, self._dev
         n, width = qkv.shape
         B, d, qdt, ld = start_pos.numel(), s.head_dim, qkv.dtype, qkv.stride()
         if (qdt is not f32 and qdt is not dt) or width != self._qkv_rows or ld[1] != 1 or \
-                not qkv.is_cuda:
-            raise ValueError("qkv: want device rows of %d %s or fp32, got %s %s"
-                             % (s.qkv_rows, dt, tuple(qkv.shape), qdt))
+                qkv.get_device() != dev:
+            raise ValueError("qkv: want rows of %d %s or fp32 on cuda:%d, got %s %s on %s"
+                             % (s.qkv_rows, dt, dev, tuple(qkv.shape), qdt, qkv.device))
+        if rope is not None and rope.table is not None and rope._dev != dev:
+            raise ValueError("rope: the table is not on cuda:%d" % dev)
         rc = self._append(
             self.ctx, qkv.data_ptr(), F32 if qdt is f32 else BF16, ld[0], n,
-            None if cu_rows is None else _need("cu_rows", cu_rows, i32, B + 1),
-            _need("start_pos", start_pos, i32, B), B, None if rope is None else rope._ref,
-            None if q_gain is None else _need("q_gain", q_gain, dt, d),
-            None if k_gain is None else _need("k_gain", k_gain, dt, d),
-            s.rms_eps if eps is None else eps, layer, kv._now(),
-            _need("q_out", q_out, dt, n * s.n_q_heads * d),
-            None if k_out is None else _need("k_out", k_out, dt, n * s.n_kv_heads * d),
-            None if v_out is None else _need("v_out", v_out, dt, n * s.n_kv_heads * d))
+            None if cu_rows is None else _need("cu_rows", cu_rows, i32, B + 1, dev),
+            _need("start_pos", start_pos, i32, B, dev), B, None if rope is None else rope._ref,
+            None if q_gain is None else _need("q_gain", q_gain, dt, d, dev),
+            None if k_gain is None else _need("k_gain", k_gain, dt, d, dev),
+            s.rms_eps if eps is None else eps, layer, kv._now(dev),
+            _need("q_out", q_out, dt, n * s.n_q_heads * d, dev),
+            None if k_out is None else _need("k_out", k_out, dt, n * s.n_kv_heads * d, dev),
+            None if v_out is None else _need("v_out", v_out, dt, n * s.n_kv_heads * d, dev))
         if rc:
             raise LlamaError(rc, "llama_op_rope_norm_append")
 
@@ -550,16 +557,16 @@ class Model:
         """Prompt attention over packed documents (llama_op_attention_docs): q
         [n_rows, n_q, d], k and v [n_rows, n_kv, d], cu_rows int32 [B + 1]; prefix
         int32 [B] rows attended both ways; scores a Scores."""
-        s, dt, i32 = self.shape, self._dt, self._i32
+        s, dt, i32, dev = self.shape, self._dt, self._i32, self._dev
         n, B = q.shape[0], cu_rows.numel() - 1
         if scores is not None and scores.slopes is not None:
-            _need("slopes", scores.slopes, self._f32, s.n_q_heads)
+            _need("slopes", scores.slopes, self._f32, s.n_q_heads, dev)
         qn, kn = n * s.n_q_heads * s.head_dim, n * s.n_kv_heads * s.head_dim
         rc = self._docs(
-            self.ctx, _need("q", q, dt, qn), _need("k", k, dt, kn), _need("v", v, dt, kn), n,
-            _need("cu_rows", cu_rows, i32, B + 1), B,
-            None if prefix is None else _need("prefix", prefix, i32, B),
-            None if scores is None else scores._ref, _need("out", out, dt, qn))
+            self.ctx, _need("q", q, dt, qn, dev), _need("k", k, dt, kn, dev), _need("v", v, dt, kn, dev), n,
+            _need("cu_rows", cu_rows, i32, B + 1, dev), B,
+            None if prefix is None else _need("prefix", prefix, i32, B, dev),
+            None if scores is None else scores._ref, _need("out", out, dt, qn, dev))
         if rc:
             raise LlamaError(rc, "llama_op_attention_docs")
 
@@ -567,15 +574,15 @@ class Model:
                                    shared_seq=0, scores=None):
         """Decode attention over a cache whose first shared_len positions are
         sequence shared_seq's for the whole batch (llama_op_attention_decode_shared)."""
-        s, dt = self.shape, self._dt
+        s, dt, dev = self.shape, self._dt, self._dev
         B = positions.numel()
         if scores is not None and scores.slopes is not None:
-            _need("slopes", scores.slopes, self._f32, s.n_q_heads)
+            _need("slopes", scores.slopes, self._f32, s.n_q_heads, dev)
         qn = B * s.n_q_heads * s.head_dim
         rc = self._shared(
-            self.ctx, _need("q", q, dt, qn), _need("positions", positions, self._i32, B), B, layer,
-            kv._now(), shared_len, shared_seq, None if scores is None else scores._ref,
-            _need("out", out, dt, qn))
+            self.ctx, _need("q", q, dt, qn, dev), _need("positions", positions, self._i32, B, dev), B, layer,
+            kv._now(dev), shared_len, shared_seq, None if scores is None else scores._ref,
+            _need("out", out, dt, qn, dev))
         if rc:
             raise LlamaError(rc, "llama_op_attention_decode_shared")
 

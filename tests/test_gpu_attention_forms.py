@@ -826,6 +826,25 @@ def test_refusals():
     refused(2, dec, q, pos, 0, binding.KVCache(shape, batch=2, capacity=64, e4m3=(1.0, 1.0)), q.clone())
     three = torch.zeros(3, 4 * d, dtype=dt, device="cuda")
     refused(3, dec, three, _i32([0, 0, 0]), 0, binding.KVCache(shape, batch=3, capacity=64), three.clone())
+    # tensors that are not on the context's device: each one by itself on the CPU, all of them elsewhere
+    for bad in range(3):
+        a = [t.cpu() if i == bad else t for i, t in enumerate((q, pos, q.clone()))]
+        with pytest.raises(ValueError):
+            dec(a[0], a[1], 0, kv, a[2])
+        with pytest.raises(ValueError):
+            docs(a[0], k, k, cu if bad != 1 else cu.cpu(), a[2])
+    with pytest.raises(ValueError):
+        ap(x, pos, 0, kv, q, rope=binding.Rope(table.cpu()))
+    host = binding.KVCache(shape, batch=2, capacity=64, device="cpu")
+    m._dev += 1
+    try:
+        for call in (lambda: ap(x, pos, 0, kv, q), lambda: docs(q, k, k, cu, q.clone()), lambda: dec(q, pos, 0, kv, q.clone())):
+            with pytest.raises(ValueError):
+                call()
+    finally:
+        m._dev -= 1
+    with pytest.raises(ValueError):
+        dec(q, pos, 0, host, q.clone())
     x32 = torch.zeros(2, s32.qkv_rows, device="cuda")
     with pytest.raises(ValueError):
         m32.op_rope_norm_append(x32.bfloat16(), pos, 0, binding.KVCache(s32, batch=2, capacity=64),
