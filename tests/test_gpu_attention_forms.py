@@ -424,6 +424,20 @@ def test_docs_fp32(nq, nkv, d, opt):
     _docs_case(nq, nkv, d, "f32", [1, 70, 0, 130], prefix=[0, 3, 0, 100] if opt & 1 else None, **OPTIONS[opt])
 
 
+def test_docs_output_aligned_to_16_bytes_only():
+    m, _ = _model(4, 2)
+    n = 200
+    q, k, v = (_randn((n, h, 128), torch.bfloat16, 210 + i).cuda() for i, h in enumerate((4, 2, 2)))
+    want = torch.empty(n, 512, dtype=torch.bfloat16, device="cuda")
+    buf = torch.full((n * 512 + 16,), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[8:8 + n * 512].view(n, 512)
+    assert out.data_ptr() % 32 == 16
+    for o in (want, out):
+        m.op_attention_docs(q, k, v, _i32([0, 70, n]), o)
+    m.sync()
+    assert torch.equal(out, want) and torch.all(buf[:8] == 3.0) and torch.all(buf[8 + n * 512:] == 3.0)
+
+
 def test_docs_matches_plain_prefill():
     m, shape = _model(4, 2)
     B, T = 2, 200
@@ -698,6 +712,63 @@ def test_serving_run(dtype):
                                          np.ones(len(K), bool), 1 / math.sqrt(d), 20.0, float(slopes[h]))
                 _within(o[b].view(nq, d)[h], ref, _attn_bound(ref, mass, dtype, len(K), d, 400.0, 20 + len(K)),
                         "step %d user %d" % (step, b))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [0, 64])
+def test_cache_offsets_past_32_bits(dtype, page):
+    # the last slots of a cache of more than 2^31 values: appended, then read as own and as shared keys
+    nq, nkv, d, cap, B, n = 4, 2, 128, 1 << 17, 66, 150
+    m, shape = _model(nq, nkv, d, dtype, max_batch=2, max_seq=256)
+    dt = shape.torch_dtype
+    if page:
+        total = B * cap // page
+        pt = torch.full((2, 4), -1, dtype=torch.int32)
+        pt[0, :3] = torch.tensor([total - 3, total - 1, total - 2])
+        pt[1] = torch.tensor([total - 3, total - 4, 0, 1])  # shares the first page only
+        kv = binding.KVCache(shape, n_pages=total, page_size=page, page_table=pt.cuda())
+        last = 0
+    else:
+        kv = binding.KVCache(shape, batch=B, capacity=cap)
+        last = B - 1
+    assert kv.k.numel() > 1 << 31
+    x = _randn((n, shape.qkv_rows), torch.float32, 200)
+    q = torch.empty(n, nq * d, dtype=dt, device="cuda")
+    k, v = (torch.empty(n, nkv * d, dtype=dt, device="cuda") for _ in range(2))
+    seqs = last + 1
+    cu = _i32([0] * seqs + [n])
+    m2 = m
+    if not page:  # row counts by sequence need a context of that batch
+        m2, _ = _model(nq, nkv, d, dtype, max_batch=B, max_seq=256)
+    m2.op_rope_norm_append(x.cuda(), _i32([0] * seqs), 0, kv, q, cu_rows=cu, k_out=k, v_out=v)
+    m2.sync()
+    assert torch.equal(q, x[:, :nq * d].to(dt).cuda()) and torch.equal(v, x[:, -nkv * d:].to(dt).cuda())
+    kf, vf = f64(k).reshape(n, nkv, d), f64(v).reshape(n, nkv, d)
+    qd = q[:2].contiguous()
+    # both sequences read the first 64 keys from the far slots
+    pos = [63, 63]
+    if page:
+        pos[last] = n - 1
+    o = torch.empty(2, nq * d, dtype=dt, device="cuda")
+    m.op_attention_decode_shared(qd, _i32(pos), 0, kv, o, shared_len=64, shared_seq=last)
+    m.sync()
+    for b in range(2):
+        for h in range(nq):
+            ref, mass = A.attend_row(f64(qd)[b].reshape(nq, d)[h], kf[:pos[b] + 1, h // 2], vf[:pos[b] + 1, h // 2], pos[b],
+                                     np.ones(pos[b] + 1, bool), 1 / math.sqrt(d))
+            _within(o[b].view(nq, d)[h], ref, _attn_bound(ref, mass, dtype, n, d, 400.0, 0), "row %d" % b)
+    if not page:  # as its own keys
+        positions = _i32([-1] * last + [n - 1])
+        qb = torch.zeros(B, nq * d, dtype=dt, device="cuda")
+        qb[last] = q[0]
+        ob = torch.empty_like(qb)
+        m2.op_attention_decode_shared(qb, positions, 0, kv, ob)
+        rc, flags = m2.sync_status()
+        assert rc == 5 and flags == binding.FLAG_POS_RANGE
+        for h in range(nq):
+            ref, mass = A.attend_row(f64(q)[0].reshape(nq, d)[h], kf[:, h // 2], vf[:, h // 2], n - 1,
+                                     np.ones(n, bool), 1 / math.sqrt(d))
+            _within(ob[last].view(nq, d)[h], ref, _attn_bound(ref, mass, dtype, n, d, 400.0, 0), "own")
 
 
 def test_captured_replays_follow_their_buffers():
