@@ -252,22 +252,31 @@ class Rope:
     rope_table, or None for the context's own (whole heads). Keeps the table alive."""
 
     def __init__(self, table=None, layout=ROPE_ADJACENT, rotary_dim=None):
-        import torch
-        if table is not None:
-            if table.dtype != torch.float32 or not table.is_contiguous() or table.dim() != 3 or \
-                    table.shape[2] != 2:
-                raise ValueError("Rope: the table is a contiguous fp32 [n_pos, rotary_dim / 2, 2]")
-            if rotary_dim not in (None, 0, 2 * table.shape[1]):
-                raise ValueError("Rope: rotary_dim %d, the table has %d pairs"
-                                 % (rotary_dim, table.shape[1]))
-            rotary_dim = 2 * table.shape[1] if rotary_dim is None else rotary_dim
-        elif rotary_dim is None:
+        if table is None and rotary_dim is None:
             raise ValueError("Rope: without a table give rotary_dim (the head size)")
-        self.table = table
-        self._dev = None if table is None else table.get_device()
-        self._c = _Rope(layout, rotary_dim, None if table is None else table.data_ptr(),
-                        0 if table is None else table.shape[0])
-        self._ref = ctypes.byref(self._c)
+        self.table, self.layout = table, layout
+        self.rotary_dim = 2 * table.shape[1] if rotary_dim is None and table.dim() == 3 else rotary_dim
+        self._check()
+
+    def _check(self):
+        import torch
+        t = self.table
+        if t is None:
+            return
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != 3 or t.shape[2] != 2:
+            raise ValueError("Rope: the table is a contiguous fp32 [n_pos, rotary_dim / 2, 2]")
+        if self.rotary_dim not in (0, 2 * t.shape[1]):
+            raise ValueError("Rope: rotary_dim %d, the table has %d pairs" % (self.rotary_dim, t.shape[1]))
+
+    def _now(self, dev):
+        """The C struct of the present attributes; ValueError unless the table is on device dev."""
+        t = self.table
+        if t is None:
+            return ctypes.byref(_Rope(self.layout, self.rotary_dim, None, 0))
+        self._check()
+        if t.get_device() != dev:
+            raise ValueError("rope: the table is not on cuda:%d" % dev)
+        return ctypes.byref(_Rope(self.layout, self.rotary_dim, t.data_ptr(), t.shape[0]))
 
 
 class Scores:
@@ -278,9 +287,14 @@ class Scores:
         import torch
         if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_contiguous()):
             raise ValueError("Scores: slopes are a contiguous fp32 tensor")
-        self.slopes = slopes
-        self._c = _Scores(scale, cap, None if slopes is None else slopes.data_ptr())
-        self._ref = ctypes.byref(self._c)
+        self.scale, self.cap, self.slopes = scale, cap, slopes
+
+    def _now(self, dtype, n_q, dev):
+        """The C struct of the present attributes; ValueError unless the slopes are
+        n_q values of dtype on device dev."""
+        t = self.slopes
+        return ctypes.byref(_Scores(self.scale, self.cap,
+                                    None if t is None else _need("slopes", t, dtype, n_q, dev)))
 
 
 def _need(what, t, dtype, n, dev):
@@ -538,12 +552,10 @@ class Model:
                 qkv.get_device() != dev:
             raise ValueError("qkv: want rows of %d %s or fp32 on cuda:%d, got %s %s on %s"
                              % (s.qkv_rows, dt, dev, tuple(qkv.shape), qdt, qkv.device))
-        if rope is not None and rope.table is not None and rope._dev != dev:
-            raise ValueError("rope: the table is not on cuda:%d" % dev)
         rc = self._append(
             self.ctx, qkv.data_ptr(), F32 if qdt is f32 else BF16, ld[0], n,
             None if cu_rows is None else _need("cu_rows", cu_rows, i32, B + 1, dev),
-            _need("start_pos", start_pos, i32, B, dev), B, None if rope is None else rope._ref,
+            _need("start_pos", start_pos, i32, B, dev), B, None if rope is None else rope._now(dev),
             None if q_gain is None else _need("q_gain", q_gain, dt, d, dev),
             None if k_gain is None else _need("k_gain", k_gain, dt, d, dev),
             s.rms_eps if eps is None else eps, layer, kv._now(dev),
@@ -559,14 +571,12 @@ class Model:
         int32 [B] rows attended both ways; scores a Scores."""
         s, dt, i32, dev = self.shape, self._dt, self._i32, self._dev
         n, B = q.shape[0], cu_rows.numel() - 1
-        if scores is not None and scores.slopes is not None:
-            _need("slopes", scores.slopes, self._f32, s.n_q_heads, dev)
         qn, kn = n * s.n_q_heads * s.head_dim, n * s.n_kv_heads * s.head_dim
         rc = self._docs(
             self.ctx, _need("q", q, dt, qn, dev), _need("k", k, dt, kn, dev), _need("v", v, dt, kn, dev), n,
             _need("cu_rows", cu_rows, i32, B + 1, dev), B,
             None if prefix is None else _need("prefix", prefix, i32, B, dev),
-            None if scores is None else scores._ref, _need("out", out, dt, qn, dev))
+            None if scores is None else scores._now(self._f32, s.n_q_heads, dev), _need("out", out, dt, qn, dev))
         if rc:
             raise LlamaError(rc, "llama_op_attention_docs")
 
@@ -576,12 +586,10 @@ class Model:
         sequence shared_seq's for the whole batch (llama_op_attention_decode_shared)."""
         s, dt, dev = self.shape, self._dt, self._dev
         B = positions.numel()
-        if scores is not None and scores.slopes is not None:
-            _need("slopes", scores.slopes, self._f32, s.n_q_heads, dev)
         qn = B * s.n_q_heads * s.head_dim
         rc = self._shared(
             self.ctx, _need("q", q, dt, qn, dev), _need("positions", positions, self._i32, B, dev), B, layer,
-            kv._now(dev), shared_len, shared_seq, None if scores is None else scores._ref,
+            kv._now(dev), shared_len, shared_seq, None if scores is None else scores._now(self._f32, s.n_q_heads, dev),
             _need("out", out, dt, qn, dev))
         if rc:
             raise LlamaError(rc, "llama_op_attention_decode_shared")

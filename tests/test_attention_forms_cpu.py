@@ -122,3 +122,80 @@ def test_binding_refuses_wrong_tensors(lib):
     q, k = torch.zeros(3, 512, dtype=torch.bfloat16), torch.zeros(3, 256, dtype=torch.bfloat16)
     with pytest.raises(ValueError):  # not on the device
         m.op_attention_docs(q, k, k, torch.zeros(2, dtype=torch.int32), q)
+
+
+# --------------------------------------------------------------------------- what reaches the C calls
+class _Recorded:
+    """A Model over CPU tensors whose three calls record the C structs they are given."""
+
+    def __init__(self, nq=4, nkv=2, n_layers=1):
+        self.shape = synth.Shape(n_layers, 256, nq, nkv, 128, 256, 256)
+        self.m = m = binding.Model.__new__(binding.Model)
+        m.shape, m.ctx = self.shape, None
+        m._bind(m.shape)
+        m._dev = -1  # what a CPU tensor's get_device() says
+        m._append = lambda *a: self._take(rope=a[8], kv=a[13])
+        m._docs = lambda *a: self._take(scores=a[8])
+        m._shared = lambda *a: self._take(kv=a[5], scores=a[8])
+        self.q = torch.zeros(2, nq * 128, dtype=torch.bfloat16)
+        self.kv_rows = torch.zeros(2, nkv * 128, dtype=torch.bfloat16)
+        self.qkv = torch.zeros(2, self.shape.qkv_rows)
+        self.pos = torch.zeros(2, dtype=torch.int32)
+
+    def _take(self, **structs):
+        for name, ref in structs.items():
+            s = None if ref is None else getattr(ref, "_obj", ref)
+            setattr(self, name, None if s is None else {f: getattr(s, f) for f, _ in s._fields_})
+        return 0
+
+    def cache(self, **kw):
+        kw = kw or dict(batch=2, capacity=64)
+        return binding.KVCache(self.shape, device="cpu", **kw)
+
+    def append(self, kv=None, rope=None):
+        self.m.op_rope_norm_append(self.qkv, self.pos, 0, kv or self.cache(), self.q, rope=rope)
+
+    def docs(self, scores):
+        self.m.op_attention_docs(self.q, self.kv_rows, self.kv_rows, torch.tensor([0, 2], dtype=torch.int32),
+                                 self.q.clone(), scores=scores)
+
+    def decode(self, kv=None, scores=None):
+        self.m.op_attention_decode_shared(self.q, self.pos, 0, kv or self.cache(), self.q.clone(), scores=scores)
+
+
+def test_scores_follow_their_attributes(lib):
+    r = _Recorded()
+    sc = binding.Scores(cap=5.0, slopes=torch.zeros(4))
+    for call in (r.docs, lambda s: r.decode(scores=s)):
+        sc.slopes = torch.ones(4)
+        call(sc)
+        assert r.scores == dict(scale=0.0, cap=5.0, slopes=sc.slopes.data_ptr())
+        sc.slopes = None
+        call(sc)
+        assert r.scores["slopes"] is None
+        for bad in (torch.ones(3), torch.ones(4).double(), torch.ones(4, 2)[:, 0]):
+            sc.slopes = bad
+            with pytest.raises(ValueError):
+                call(sc)
+
+
+def test_rope_follows_its_table(lib):
+    r = _Recorded()
+    rope = binding.Rope(torch.zeros(9, 32, 2), binding.ROPE_HALF)
+    r.append(rope=rope)
+    assert r.rope == dict(layout=binding.ROPE_HALF, rotary_dim=64, table=rope.table.data_ptr(), n_pos=9)
+    rope.table = torch.zeros(30, 32, 2)  # of more positions
+    r.append(rope=rope)
+    assert r.rope["table"] == rope.table.data_ptr() and r.rope["n_pos"] == 30
+    for bad in (torch.zeros(9, 16, 2), torch.zeros(9, 32, 2).double(), torch.zeros(9, 2, 32).transpose(1, 2),
+                torch.zeros(9, 64)):
+        rope.table = bad
+        with pytest.raises(ValueError):
+            r.append(rope=rope)
+    rope.table = torch.zeros(9, 32, 2)
+    rope.table.get_device = lambda: 0  # (a device that the context is not on)
+    with pytest.raises(ValueError):
+        r.append(rope=rope)
+    rope.table = None  # the context's own angles
+    r.append(rope=rope)
+    assert r.rope["table"] is None and r.rope["rotary_dim"] == 64
