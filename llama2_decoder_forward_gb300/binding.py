@@ -335,22 +335,14 @@ class KVCache:
         self.k = k if k is not None else torch.zeros(full, dtype=dt, device=device)
         self.v = v if v is not None else torch.zeros(full, dtype=dt, device=device)
         assert tuple(self.k.shape) == full and tuple(self.v.shape) == full
-        self._c = self.struct()
-        self._ref = ctypes.byref(self._c)
 
     def _now(self, dev):
-        """The kept C struct (the layout is fixed at construction) with the tensors'
-        present addresses and the scales; ValueError unless they are on device dev."""
-        c, pt = self._c, self.page_table
+        """The C struct of the present attributes; ValueError unless the tensors are on device dev."""
+        pt = self.page_table
         if self.k.get_device() != dev or self.v.get_device() != dev or \
                 (pt is not None and pt.get_device() != dev):
             raise ValueError("cache: not on cuda:%d" % dev)
-        c.k = self.k.data_ptr()
-        c.v = self.v.data_ptr()
-        c.k_scale, c.v_scale = self.k_scale, self.v_scale
-        if pt is not None:
-            c.page_table = pt.data_ptr()
-        return self._ref
+        return ctypes.byref(self.struct())
 
     def struct(self) -> KV:
         return KV(self.k.data_ptr(), self.v.data_ptr(), self.page_size, self.capacity, self.batch,

@@ -199,3 +199,31 @@ def test_rope_follows_its_table(lib):
     rope.table = None  # the context's own angles
     r.append(rope=rope)
     assert r.rope["table"] is None and r.rope["rotary_dim"] == 64
+
+
+def _fields(kv):
+    s = kv.struct()
+    return {f: getattr(s, f) for f, _ in s._fields_}
+
+
+def test_cache_layout_follows_its_attributes(lib):
+    r = _Recorded()
+    table = torch.zeros(2, 4, dtype=torch.int32)
+    paged = r.cache(n_pages=8, page_size=16, page_table=table)
+    flat = r.cache()
+    for kv in (paged, flat):
+        r.append(kv)
+        assert r.kv == _fields(kv)
+    # a server that widens its table, grows its pool, changes the page size
+    paged.page_table, paged.max_pages = torch.zeros(2, 9, dtype=torch.int32), 9
+    paged.k, paged.v = (torch.zeros(1, 24, 2, 16, 128, dtype=torch.bfloat16) for _ in range(2))
+    paged.n_pages = 24
+    flat.k, flat.v = (torch.zeros(1, 3, 2, 128, 128, dtype=torch.bfloat16) for _ in range(2))
+    flat.batch, flat.capacity = 3, 128
+    for call in (r.append, r.decode):
+        for kv in (paged, flat):
+            call(kv)
+            assert r.kv == _fields(kv)
+    paged.n_pages, paged.page_size = 48, 8
+    r.decode(paged)
+    assert r.kv == _fields(paged) and r.kv["page_size"] == 8
