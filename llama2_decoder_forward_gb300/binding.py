@@ -247,7 +247,22 @@ def rope_table(n_pos, rotary_dim, *, theta=10000.0, kind=ROPE_PLAIN, factor=1.0,
     return table
 
 
-class Rope:
+class _Kept:
+    """Keeps the C struct of its attributes until one of them is assigned; tensors'
+    addresses are read at every call."""
+
+    def __setattr__(self, name, value):
+        d = self.__dict__
+        d[name] = value
+        d["_c"] = None
+
+    def _keep(self, c):
+        d = self.__dict__
+        d["_c"], d["_ref"] = c, ctypes.byref(c)
+        return c
+
+
+class Rope(_Kept):
     """How heads rotate (llama_rope). table: [n_pos, rotary_dim / 2, 2] fp32 from
     rope_table, or None for the context's own (whole heads). Keeps the table alive."""
 
@@ -256,30 +271,30 @@ class Rope:
             raise ValueError("Rope: without a table give rotary_dim (the head size)")
         self.table, self.layout = table, layout
         self.rotary_dim = 2 * table.shape[1] if rotary_dim is None and table.dim() == 3 else rotary_dim
-        self._check()
+        self._struct()
 
-    def _check(self):
+    def _struct(self):
         import torch
         t = self.table
         if t is None:
-            return
+            return self._keep(_Rope(self.layout, self.rotary_dim, None, 0))
         if t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != 3 or t.shape[2] != 2:
             raise ValueError("Rope: the table is a contiguous fp32 [n_pos, rotary_dim / 2, 2]")
         if self.rotary_dim not in (0, 2 * t.shape[1]):
             raise ValueError("Rope: rotary_dim %d, the table has %d pairs" % (self.rotary_dim, t.shape[1]))
+        return self._keep(_Rope(self.layout, self.rotary_dim, t.data_ptr(), t.shape[0]))
 
     def _now(self, dev):
         """The C struct of the present attributes; ValueError unless the table is on device dev."""
-        t = self.table
-        if t is None:
-            return ctypes.byref(_Rope(self.layout, self.rotary_dim, None, 0))
-        self._check()
-        if t.get_device() != dev:
-            raise ValueError("rope: the table is not on cuda:%d" % dev)
-        return ctypes.byref(_Rope(self.layout, self.rotary_dim, t.data_ptr(), t.shape[0]))
+        c, t = self._c or self._struct(), self.table
+        if t is not None:
+            if t.get_device() != dev:
+                raise ValueError("rope: the table is not on cuda:%d" % dev)
+            c.table = t.data_ptr()
+        return self._ref
 
 
-class Scores:
+class Scores(_Kept):
     """Score options (llama_scores): scale (0: 1/sqrt(d)), cap (0: none), slopes
     fp32 [n_q] on the device or None. Keeps the slopes alive."""
 
@@ -292,9 +307,10 @@ class Scores:
     def _now(self, dtype, n_q, dev):
         """The C struct of the present attributes; ValueError unless the slopes are
         n_q values of dtype on device dev."""
-        t = self.slopes
-        return ctypes.byref(_Scores(self.scale, self.cap,
-                                    None if t is None else _need("slopes", t, dtype, n_q, dev)))
+        c, t = self._c or self._keep(_Scores(self.scale, self.cap, None)), self.slopes
+        if t is not None:
+            c.slopes = _need("slopes", t, dtype, n_q, dev)
+        return self._ref
 
 
 def _need(what, t, dtype, n, dev):
@@ -307,7 +323,7 @@ def _need(what, t, dtype, n, dev):
                       "" if t.is_contiguous() else " (strided)"))
 
 
-class KVCache:
+class KVCache(_Kept):
     """Caller-owned KV cache in the library's layout (torch device memory).
 
     contiguous: k, v [n_layers, batch, n_kv, capacity, d]
@@ -336,13 +352,41 @@ class KVCache:
         self.v = v if v is not None else torch.zeros(full, dtype=dt, device=device)
         assert tuple(self.k.shape) == full and tuple(self.v.shape) == full
 
-    def _now(self, dev):
-        """The C struct of the present attributes; ValueError unless the tensors are on device dev."""
-        pt = self.page_table
-        if self.k.get_device() != dev or self.v.get_device() != dev or \
+    def _struct(self, shape, dtype):
+        """The struct of the present attributes; ValueError unless the tensors are of the
+        layout's type and cover it, and the page table is as wide as it says."""
+        import torch
+        rows = self.n_pages * self.page_size if self.page_size else self.batch * self.capacity
+        need, pt = shape.n_layers * shape.n_kv_heads * shape.head_dim * rows, self.page_table
+        for t in (self.k, self.v):
+            if t.numel() < need or not t.is_contiguous() or \
+                    (t.dtype is not dtype if self.kv_dtype == KV_MODEL else t.element_size() != 1):
+                raise ValueError("cache: want contiguous k and v of %d %s, got %s %s%s" %
+                                 (need, dtype if self.kv_dtype == KV_MODEL else "E4M3 bytes", tuple(t.shape),
+                                  t.dtype, "" if t.is_contiguous() else " (strided)"))
+        if self.page_size and (pt is None or pt.dtype != torch.int32 or pt.dim() != 2 or
+                               pt.shape[1] != self.max_pages or not pt.is_contiguous()):
+            raise ValueError("cache: want a contiguous int32 page table of max_pages = %d columns, got %s" %
+                             (self.max_pages, None if pt is None else "%s %s" % (tuple(pt.shape), pt.dtype)))
+        d = self.__dict__
+        d["_shape"], d["_rows"] = shape, pt.shape[0] if self.page_size else 1 << 31
+        return self._keep(self.struct())
+
+    def _now(self, shape, dtype, B, dev):
+        """The C struct of the present attributes for a call on B sequences of a model of
+        this shape and type; ValueError unless they fit and are on device dev."""
+        c, k, v, pt = self._c, self.k, self.v, self.page_table
+        if c is None or self._shape is not shape:
+            c = self._struct(shape, dtype)
+        if k.get_device() != dev or v.get_device() != dev or \
                 (pt is not None and pt.get_device() != dev):
             raise ValueError("cache: not on cuda:%d" % dev)
-        return ctypes.byref(self.struct())
+        if B > self._rows:
+            raise ValueError("cache: %d sequences, the page table has %d rows" % (B, self._rows))
+        c.k, c.v = k.data_ptr(), v.data_ptr()
+        if pt is not None:
+            c.page_table = pt.data_ptr()
+        return self._ref
 
     def struct(self) -> KV:
         return KV(self.k.data_ptr(), self.v.data_ptr(), self.page_size, self.capacity, self.batch,
@@ -550,7 +594,7 @@ class Model:
             _need("start_pos", start_pos, i32, B, dev), B, None if rope is None else rope._now(dev),
             None if q_gain is None else _need("q_gain", q_gain, dt, d, dev),
             None if k_gain is None else _need("k_gain", k_gain, dt, d, dev),
-            s.rms_eps if eps is None else eps, layer, kv._now(dev),
+            s.rms_eps if eps is None else eps, layer, kv._now(s, dt, B, dev),
             _need("q_out", q_out, dt, n * s.n_q_heads * d, dev),
             None if k_out is None else _need("k_out", k_out, dt, n * s.n_kv_heads * d, dev),
             None if v_out is None else _need("v_out", v_out, dt, n * s.n_kv_heads * d, dev))
@@ -581,7 +625,7 @@ class Model:
         qn = B * s.n_q_heads * s.head_dim
         rc = self._shared(
             self.ctx, _need("q", q, dt, qn, dev), _need("positions", positions, self._i32, B, dev), B, layer,
-            kv._now(dev), shared_len, shared_seq, None if scores is None else scores._now(self._f32, s.n_q_heads, dev),
+            kv._now(s, dt, B, dev), shared_len, shared_seq, None if scores is None else scores._now(self._f32, s.n_q_heads, dev),
             _need("out", out, dt, qn, dev))
         if rc:
             raise LlamaError(rc, "llama_op_attention_decode_shared")

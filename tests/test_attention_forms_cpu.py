@@ -227,3 +227,48 @@ def test_cache_layout_follows_its_attributes(lib):
     paged.n_pages, paged.page_size = 48, 8
     r.decode(paged)
     assert r.kv == _fields(paged) and r.kv["page_size"] == 8
+
+
+def test_page_table_is_checked(lib):
+    # read past its end, as other integers or with another stride it would send writes anywhere
+    r = _Recorded()
+    good = torch.zeros(2, 4, dtype=torch.int32)
+    kv = r.cache(n_pages=8, page_size=16, page_table=good)
+    for bad in (torch.zeros(1, 4, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int64),
+                torch.zeros(4, 2, dtype=torch.int32).t(), torch.zeros(2, 8, dtype=torch.int32)[:, :4],
+                torch.zeros(2, 3, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), None):
+        kv.page_table = bad
+        for call in (r.append, r.decode):
+            with pytest.raises(ValueError):
+                call(kv)
+    kv.page_table = torch.zeros(5, 4, dtype=torch.int32)  # more sequences than the batch
+    r.append(kv)
+    r.decode(kv)
+
+
+def test_cache_tensors_cover_the_layout(lib):
+    r = _Recorded(n_layers=2)
+    for kw in (dict(batch=2, capacity=64), dict(n_pages=8, page_size=16, page_table=torch.zeros(2, 4, dtype=torch.int32))):
+        kv = r.cache(**kw)
+        k = kv.k
+        for name in ("k", "v"):
+            for bad in (k[:1], k.float(), k.transpose(3, 4), k[:, :-1].contiguous()):
+                setattr(kv, name, bad)
+                for call in (r.append, r.decode):
+                    with pytest.raises(ValueError):
+                        call(kv)
+            setattr(kv, name, k)
+        r.append(kv)
+        kv.n_pages, kv.batch = kv.n_pages and 9, kv.batch and 3
+        with pytest.raises(ValueError):
+            r.append(kv)
+        kv = r.cache(e4m3=(1.0, 1.0), **kw)
+        r.append(kv)
+        kv.k = k
+        with pytest.raises(ValueError):
+            r.append(kv)
+    r.append(r.cache(**kw))  # of two layers
+    one, kv = _Recorded(), _Recorded().cache(**kw)
+    one.append(kv)
+    with pytest.raises(ValueError):  # the same cache with a model of two
+        r.append(kv)
