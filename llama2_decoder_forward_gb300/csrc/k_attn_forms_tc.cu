@@ -210,17 +210,9 @@ __device__ __forceinline__ void load_tile(const FormsParams& p, const CUtensorMa
     tma_load_3d(dst + half * HALF + step * 16 * 128, whole ? big : m16, bar, 64 * half, row, p.layer);
 }
 
-// tanh(y) = y R(y^2): weighted least-squares fits of smallest relative error
-// with 3 coefficients for |y| <= 1/4, 4 for 1/2 and 6 for 1 (below 7e-7 each,
-// evaluated in fp32). A warp takes the shortest that covers its scores: caps
+// Of the fits of tanh (kTanh) a warp takes the shortest that covers its scores: caps
 // are seldom approached. On the special-function unit a cap would cost an
 // exponential and a reciprocal per score beside the softmax's own exponential.
-constexpr float kTanh[13] = {
-    0.9999995827674866f, -0.33321908116340637f, 0.12841613590717316f,
-    0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f,
-    0.9999994039535522f, -0.3332904279232025f, 0.13281433284282684f, -0.051605671644210815f,
-    0.016743114218115807f, -0.0030670599080622196f};
-
 // Eight x times the polynomial with N coefficients c[0..] in w = x^2 (UNIT: of y =
 // x yk), step by step over all eight: written element by element the compiler
 // keeps that order, and the chain of dependent multiply-adds took 1287 cycles

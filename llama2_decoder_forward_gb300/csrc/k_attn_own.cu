@@ -100,17 +100,28 @@ __device__ __forceinline__ int own_kv_row(const OwnParams& p, int b, int g, int 
   return (page * p.n_kv + g) * p.page_size + (k0 - pi * p.page_size);
 }
 
-// Scores in log2 units: x log2e after the cap, minus the distance bias. zc =
-// 2 log2e scale / cap, cl = cap log2e; cap tanh(y) = cap (1 - 2 / (1 + e^2y)).
+// Scores in log2 units: cl tanh(y), cl = cap log2e, y = x yk with yk = scale / cap,
+// or x c without a cap; the distance bias is subtracted later. Up to |y| = 1 tanh
+// is the polynomial that the prefix kernel takes, beyond it 1 - 2 / (1 + e^2y):
+// that difference has an error relative to the cap, which for caps far above the
+// scores would swallow them (weights off by 4 % at a cap of 1e6).
 struct ScoreConst {
-  float c, zc, cl;
+  float c, cl, yk;
   bool cap;
+  __device__ __forceinline__ ScoreConst(float scale, float cap_)
+      : c(scale * 1.4426950408889634f), cl(cap_ * 1.4426950408889634f),
+        yk(cap_ > 0.f ? scale / cap_ : 0.f), cap(cap_ > 0.f) {}
 };
 __device__ __forceinline__ float score(const ScoreConst& k, float x) {
   if (!k.cap) return x * k.c;
+  constexpr float kTanh6[6] = {kTanh[7], kTanh[8], kTanh[9], kTanh[10], kTanh[11], kTanh[12]};
+  const float y = x * k.yk, w = y * y;
+  float q = kTanh6[5];
+#pragma unroll
+  for (int i = 4; i >= 0; --i) q = fmaf(q, w, kTanh6[i]);
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * k.zc)));
-  return fmaf(-2.f * k.cl, r, k.cl);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(y * 2.885390081777927f)));
+  return k.cl * (fabsf(y) <= 1.f ? y * q : fmaf(-2.f, r, 1.f));
 }
 
 // Rows of a 16-key step outside [lead, valid) may hold anything: zero their V.
@@ -140,8 +151,7 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
     qf[kk][1] = hq < G ? __ldcg(reinterpret_cast<const unsigned*>(qb + col + 8)) : 0u;
   }
   constexpr float kLog2e = 1.4426950408889634f;
-  const ScoreConst sc{p.scale * kLog2e, p.cap > 0.f ? 2.f * p.scale * kLog2e / p.cap : 0.f,
-                      p.cap * kLog2e, p.cap > 0.f};
+  const ScoreConst sc(p.scale, p.cap);
   float sl[2] = {0.f, 0.f};
   if (p.slopes) {
 #pragma unroll
@@ -270,8 +280,7 @@ __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem,
       qa[kk][i] = row < G ? __ldcg(reinterpret_cast<const unsigned*>(qb + row * HD + col)) : 0u;
     }
   constexpr float kLog2e = 1.4426950408889634f;
-  const ScoreConst sc{p.scale * kLog2e, p.cap > 0.f ? 2.f * p.scale * kLog2e / p.cap : 0.f,
-                      p.cap * kLog2e, p.cap > 0.f};
+  const ScoreConst sc(p.scale, p.cap);
   float sl[2] = {0.f, 0.f};
   if (p.slopes) {
 #pragma unroll

@@ -560,6 +560,17 @@ def test_shared_bf16_long_splits():
     _shared_case(4, 4, 128, "bf16", [5000], 0, page=0, bias=True)
 
 
+@pytest.mark.parametrize("cap,scale", [(50.0, 0.0), (50.3, 0.0), (2.0, 0.5), (0.05, 1.0), (2000.0, 0.0), (300.0, 4.0),
+                                       (3e4, 0.0), (1e6, 0.0), (1e8, 0.0)])
+@pytest.mark.parametrize("nq,nkv", [(4, 2), (12, 1)])
+@pytest.mark.parametrize("shared", [0, 128])
+def test_shared_caps(cap, scale, nq, nkv, shared):
+    # barely capped, far past the cap, and caps beside which the scores are small: own and shared keys
+    # are capped alike, to an error relative to the score
+    _shared_case(nq, nkv, 128, "bf16", [200, 150, 333], shared, cap=cap, scale=scale)
+    _shared_case(nq, nkv, 128, "bf16", [200, 150, 333], shared, cap=cap, scale=scale, bias=True)
+
+
 def test_shared_join_after_a_long_prefix():
     # the own keys' blocks leave partials: both row tiles with the same rows, and two blocks of rows;
     # own keys none, few and many, a position inside the prefix
