@@ -17,6 +17,13 @@ __device__ __forceinline__ void doc_rows(const int32_t* cu, int b, int n_rows, u
   if (lo != a || hi != e) flag(status, LLAMA_FLAG_POS_RANGE);
 }
 
+// The position that a decode row attends up to: one past the limit (flagged by the
+// caller) attends the keys in range, as the last one does; the distance bias then
+// counts from there, which shifts all scores of the row alike. -1: no keys.
+__device__ __forceinline__ int key_position(int pos, int key_limit) {
+  return max(min(pos, key_limit - 1), -1);
+}
+
 // The maximum that a partial result of sum l is merged with: a maximum passes over
 // NaN scores, and without a finite one beside them the part would count as
 // empty, so a NaN sum takes part as +inf, which the merge turns into NaN.

@@ -418,7 +418,7 @@ template <int KIND>
 __device__ __forceinline__ int prefix_share(const FormsParams& p, int lane) {
   float own = 0.f;
   for (int i = lane; i < p.B; i += 32)
-    own += (float)max(0, min(p.positions[i], p.key_limit - 1) + 1 - p.shared_len);
+    own += (float)max(0, key_position(p.positions[i], p.key_limit) + 1 - p.shared_len);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
   own *= 512.f * gridDim.z;  // K and V
@@ -801,8 +801,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     } else {
       const int s = w.seq0 + (p.alternate ? 0 : t * p.rows_seq) + r / p.G;
       row_ok = r < p.rows_seq * p.G && s < p.B;
-      pos = row_ok ? p.positions[s] : 0;
-      lim = row_ok ? min(min(max(pos + 1, 0), p.key_limit), p.shared_len) : 0;
+      pos = row_ok ? key_position(p.positions[s], p.key_limit) : -1;
+      lim = min(pos + 1, p.shared_len);
       head = w.g * p.G + r % p.G;
       row = s;
     }

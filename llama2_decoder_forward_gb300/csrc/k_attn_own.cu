@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     for (int i = threadIdx.x; i < SORT_MAX; i += OWN_THREADS) {
       const int x = i < p.sorted ? __ldcg(p.positions + i) : -1;
       at[i] = x;
-      key[i] = i < p.sorted ? (max(min(x, p.key_limit - 1), -1) + 1) * SORT_MAX + SORT_MAX - 1 - i : -1;
+      key[i] = i < p.sorted ? (key_position(x, p.key_limit) + 1) * SORT_MAX + SORT_MAX - 1 - i : -1;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < p.sorted; i += OWN_THREADS) {
@@ -553,11 +553,9 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   // the producer's first page ids, without splits loaded beside the position
   int page = warp == 4 && p.splits == 1 ? own_page(p, b, p.base + lane * SUB) : 0;
   if (!p.sorted) __syncthreads();
-  int n = pos + 1;
-  if (pos < 0 || pos >= p.key_limit) {
-    if (split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
-    n = pos < 0 ? 0 : p.key_limit;
-  }
+  if ((pos < 0 || pos >= p.key_limit) && split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
+  pos = key_position(pos, p.key_limit);
+  const int n = pos + 1;
   const int share = own_share(p, n), kbeg = p.base + split * share;
   const int kend = min(n, kbeg + share);
   const bool any = kend > max(kbeg, p.first);
@@ -703,8 +701,7 @@ __global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int 
   pre.load(p.part_o, p.part_ml, (size_t)bh * p.prefix_parts, p.prefix_parts, lane);
   own.load(p.own_o, p.own_ml, (size_t)bh * p.splits, p.splits, lane);
   const int parts = p.prefix_parts ? __ldcg(p.used) : 0;
-  const int pos = __ldcg(p.positions + bh / p.n_q);
-  const int n = pos < 0 ? 0 : min(pos + 1, p.key_limit);
+  const int n = key_position(__ldcg(p.positions + bh / p.n_q), p.key_limit) + 1;
   int used = n > p.first;  // own splits that have keys
   if (used && p.splits > 1) {
     const int share = own_share(p, n);

@@ -147,11 +147,10 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     h0 = g * p.G + c * RT;
     rows = min(RT, p.G - c * RT);
     pos = p.positions[b];
+    if ((pos < 0 || pos >= p.key_limit) && part == 0 && threadIdx.x == 0)
+      flag(p.status, LLAMA_FLAG_POS_RANGE);
+    pos = key_position(pos, p.key_limit);
     n_keys = pos + 1;
-    if (pos < 0 || pos >= p.key_limit) {
-      if (part == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
-      n_keys = pos < 0 ? 0 : p.key_limit;
-    }
   }
   // element offset of row r (documents: packed row, one head; decode: one row, head h0 + r)
   auto row_off = [&](int r) -> size_t {

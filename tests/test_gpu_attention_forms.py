@@ -608,6 +608,30 @@ def test_shared_longest_first_beside_bad_positions():
     assert torch.equal(out[keep], want[keep])
 
 
+@pytest.mark.parametrize("dtype,nq,nkv,room,shared", [
+    ("bf16", 4, 2, 400, 0), ("bf16", 4, 2, 400, 100), ("bf16", 40, 40, 3400, 3160), ("bf16", 16, 1, 3400, 0),
+    ("f32", 4, 2, 400, 100)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_shared_positions_past_the_cache(dtype, nq, nkv, room, shared, bias):
+    # without a prefix, beside a short one, joined after a long one: the largest and the smallest
+    # position are flagged, and the keys in range are attended as from the last one
+    m, shape = _model(nq, nkv, 128, dtype, max_batch=4, max_seq=room)
+    dt = shape.torch_dtype
+    q = _randn((4, nq, 128), dt, 220).cuda()
+    k, v = (_randn((1, 4, nkv, room, 128), dt, 221 + i).cuda() for i in range(2))
+    kv = binding.KVCache(shape, batch=4, capacity=room, k=k, v=v)
+    sc = binding.Scores(slopes=_slopes(nq).cuda()) if bias else None
+    outs = []
+    for pos in ([room - 1, room - 30, room - 1, -1], [2 ** 31 - 1, room - 30, room, -2 ** 31]):
+        out = torch.full((4, nq * 128), 3.0, dtype=dt, device="cuda")
+        m.op_attention_decode_shared(q, _i32(pos), 0, kv, out, shared_len=shared, scores=sc)
+        rc, flags = m.sync_status()
+        assert rc == 5 and flags == binding.FLAG_POS_RANGE
+        outs.append(out)
+    assert torch.all(outs[0][3] == 0) and torch.isfinite(outs[0]).all() and torch.all(outs[0][:3].abs().sum(-1) > 0)
+    assert torch.equal(outs[0], outs[1])
+
+
 def test_shared_second_layer():
     _shared_case(4, 2, 128, "bf16", [90, 70], 40, layers=3, layer=2)
 
