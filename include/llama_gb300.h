@@ -529,8 +529,8 @@ int llama_op_rope_norm_append(llama_ctx* ctx, const void* qkv, int32_t qkv_dtype
  *   s = (cap > 0 ? cap * tanh(x / cap) : x) - slopes[h] * |i - j|
  * for query position i and key position j of head h, then the mask. */
 typedef struct llama_scores {
-  float scale;          /* > 0, or 0: 1 / sqrt(head_dim) */
-  float cap;            /* > 0, or 0: no cap */
+  float scale;          /* 2^-100 .. 2^100, or 0: 1 / sqrt(head_dim) */
+  float cap;            /* 2^-100 .. 2^100 with scale / cap in 2^-120 .. 2^120, or 0: no cap */
   const float* slopes;  /* DEVICE fp32 [n_q], or NULL: no distance bias */
 } llama_scores;
 

@@ -1230,10 +1230,13 @@ int score_args(const llama_ctx* c, const llama_scores* s, ScoreArgs* out) {
   out->cap = 0.f;
   out->slopes = nullptr;
   if (!s) return LLAMA_OK;
-  if (!(s->scale >= 0.f) || !std::isfinite(s->scale) || !(s->cap >= 0.f) || !std::isfinite(s->cap) ||
+  // the kernels' constants (scale log2e, cap log2e, scale / cap) stay normal fp32 numbers
+  const auto in_range = [](float x, float most = 0x1p100f) { return x >= 1.f / most && x <= most; };
+  if (!(s->scale == 0.f || in_range(s->scale)) || !(s->cap == 0.f || in_range(s->cap)) ||
       (reinterpret_cast<uintptr_t>(s->slopes) & 3u) != 0)
     return LLAMA_ERR_INVALID_ARG;
   if (s->scale > 0.f) out->scale = s->scale;
+  if (s->cap > 0.f && !in_range(out->scale / s->cap, 0x1p120f)) return LLAMA_ERR_INVALID_ARG;
   out->cap = s->cap;
   out->slopes = s->slopes;
   return LLAMA_OK;

@@ -883,6 +883,30 @@ def test_two_contexts_on_two_streams_at_once():
         r[0].set_stream(torch.cuda.default_stream())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scores_ranges(dtype):
+    # caps and scales at the ends of their range; beyond it the constants that the kernels form
+    # of them leave fp32
+    lo, hi = 2.0 ** -100, 2.0 ** 100
+    for cap, scale in ((hi, 0.0), (1e-29, 0.0), (lo, lo), (0.0, lo)):
+        _docs_case(4, 2, 128, dtype, [150, 40], cap=cap, scale=scale)
+        _docs_case(3, 3, 128, dtype, [150, 40], cap=cap, scale=scale, bias=True)
+        _shared_case(4, 2, 128, dtype, [200, 140], 128, cap=cap, scale=scale, bias=True)
+    m, shape = _model(4, 2, dtype=dtype, max_batch=2, max_seq=64)
+    dt = shape.torch_dtype
+    q, k = (torch.zeros(2, h * 128, dtype=dt, device="cuda") for h in (4, 2))
+    kv = binding.KVCache(shape, batch=2, capacity=64)
+    for cap, scale in ((3e38, 0.0), (2 * hi, 0.0), (lo / 2, 0.0), (1e-45, 0.0), (0.0, 2 * hi), (0.0, lo / 2),
+                       (1e-20, 1e20), (1e20, 1e-20)):
+        sc = binding.Scores(scale, cap)
+        for call in (lambda: m.op_attention_docs(q, k, k, _i32([0, 2]), q.clone(), scores=sc),
+                     lambda: m.op_attention_decode_shared(q, _i32([0, 1]), 0, kv, q.clone(), scores=sc)):
+            with pytest.raises(binding.LlamaError) as e:
+                call()
+            assert e.value.rc == 1
+    m.sync()
+
+
 # --------------------------------------------------------------------------- refusals
 def test_refusals():
     m, shape = _model(4, 2, max_batch=2, max_seq=64)
