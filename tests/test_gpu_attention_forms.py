@@ -907,6 +907,91 @@ def test_scores_ranges(dtype):
     m.sync()
 
 
+# --------------------------------------------------------------------------- several items per block
+def _docs_reference(q, k, v, lens, prefix, scale, cap, slopes):
+    """(out, mass) [n, n_q, d] in fp64 on the GPU, document by document."""
+    q, k, v = (t.cuda().double() for t in (q, k, v))
+    G = q.shape[1] // k.shape[1]
+    out, mass, lo = torch.empty_like(q), torch.empty_like(q), 0
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        K, V = (t[lo:lo + n].repeat_interleave(G, 1) for t in (k, v))
+        s = torch.einsum("ihd,jhd->hij", q[lo:lo + n], K) * scale
+        if cap > 0:
+            s = cap * torch.tanh(s / cap)
+        at = torch.arange(n, device="cuda")
+        if slopes is not None:
+            s = s - slopes.cuda().double()[:, None, None] * (at[:, None] - at).abs()
+        keep = at[:, None] >= at if prefix is None else (at[:, None] >= at) | (at < prefix[b])
+        p = torch.softmax(s.masked_fill(~keep, -math.inf), -1)
+        out[lo:lo + n] = torch.einsum("hij,jhd->ihd", p, V)
+        mass[lo:lo + n] = torch.einsum("hij,jhd->ihd", p, V.abs())
+        lo += n
+    return f64(out), f64(mass)
+
+
+def _one_key_per_dim(n, heads, dtype):
+    """Values with a one in dim (key % 128): with weights near each other, a key too
+    many or too few changes its dim by far more than a rounding. The values have one
+    sign, so a weight's error moves the mean o by up to 2^-8 sum p|v - o| <= 2^-8
+    (sum p|v| + |o|): 2^-8 |ref| more than values of both signs. And a dim may hold
+    none but tiny weights: those below fp32's normals are lost, 2^-126 of a reference
+    that lies up to 7 slopes of 2 octaves above the row's largest score, 2^-112 each
+    for the 6 keys of a dim: below 2^-109."""
+    v = torch.zeros(n, heads, 128)
+    v[torch.arange(n), :, torch.arange(n) % 128] = 1.0
+    return v.to(dtype)
+
+
+ITEM_LENS = [1, 300, 128, 129, 0, 700, 64, 257, 5, 40, 1, 512, 90, 33, 0, 17, 256, 2, 127, 385] + [1, 3] * 10
+
+
+@pytest.mark.parametrize("nq,nkv", [(32, 32), (40, 40), (64, 8)])
+@pytest.mark.parametrize("cap,bias,two_way", [(0.0, False, False), (0.0, False, True), (0.0, True, False), (0.0, True, True),
+                                              (20.0, False, False), (20.0, False, True), (60.0, True, True)])
+def test_docs_many_items_per_block(nq, nkv, cap, bias, two_way):
+    # each persistent block takes several work items, among them ones whose second row tile is
+    # empty and ones beyond the first 32 documents
+    pairs = nq // nkv % 2 == 0
+    items = sum(-(-n // (128 if pairs else 256)) for n in ITEM_LENS) * (nq // 2 if pairs else nq)
+    m, _ = _model(nq, nkv)
+    assert items > 4 * torch.cuda.get_device_properties(0).multi_processor_count and len(ITEM_LENS) > 32
+    n = sum(ITEM_LENS)
+    cu = [0]
+    for x in ITEM_LENS:
+        cu.append(cu[-1] + x)
+    pre = torch.randint(0, 280, (len(ITEM_LENS),), generator=_gen(8)).tolist() if two_way else None
+    slopes = _slopes(nq) if bias else None
+    sc = binding.Scores(cap=cap, slopes=None if slopes is None else slopes.cuda())
+    q, k = (_randn((n, h, 128), torch.bfloat16, 230 + h) for h in (nq, nkv))
+    for q, v, more in ((q, _randn((n, nkv, 128), torch.bfloat16, 232), 0.0),
+                       ((q.float() * 0.3).bfloat16(), _one_key_per_dim(n, nkv, torch.bfloat16), 2.0 ** -8)):
+        outs = []
+        qd, kd, vd = q.cuda(), k.cuda(), v.cuda()
+        for _ in range(3):
+            out = torch.full((n, nq * 128), 3.0, dtype=torch.bfloat16, device="cuda")
+            m.op_attention_docs(qd, kd, vd, _i32(cu), out, prefix=None if pre is None else _i32(pre), scores=sc)
+            outs.append(out)
+        m.sync()
+        ref, mass = _docs_reference(q, k, v, ITEM_LENS, pre, 128 ** -0.5, cap, slopes)
+        _within(outs[0].view(n, nq, 128), ref, _attn_bound(ref, mass, "bf16", n, 128, 0, 0) +
+                more * np.abs(ref) + 2.0 ** -109, "items")
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_docs_reference_is_the_definition():
+    need_gpu()
+    q, k, v = (_randn((45, h, 128), torch.bfloat16, 240 + h) for h in (4, 2, 2))
+    lens, pre, sl = [30, 0, 15], [7, 3, 0], _slopes(4)
+    cu = [0, 30, 30, 45]
+    for cap in (0.0, 9.0):
+        got = _docs_reference(q, k, v, lens, pre, 0.1, cap, sl)
+        want = A.attend_documents(f64(q), f64(k), f64(v), cu, pre, 0.1, cap, f64(sl))
+        for a, b in zip(got, want):
+            np.testing.assert_allclose(a, b, atol=1e-12)
+
+
 # --------------------------------------------------------------------------- refusals
 def test_refusals():
     m, shape = _model(4, 2, max_batch=2, max_seq=64)
