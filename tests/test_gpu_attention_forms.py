@@ -992,6 +992,92 @@ def test_docs_reference_is_the_definition():
             np.testing.assert_allclose(a, b, atol=1e-12)
 
 
+# --------------------------------------------------------------------------- many rows
+@pytest.mark.parametrize("nq,nkv,d,dtype,src,rotary,half,norm,e4m3,page,side", [
+    (32, 32, 128, "bf16", "f32", 128, True, "qk", None, 16, True),
+    (32, 32, 128, "bf16", "bf16", 128, False, "", None, 0, False),
+    (32, 32, 128, "bf16", "f32", 64, True, "k", (0.02, 0.004), 64, True),
+    (32, 32, 128, "bf16", "bf16", 0, False, "q", None, 48, False),
+    (40, 8, 128, "bf16", "f32", 96, False, "qk", (0.02, 0.004), 0, False),
+    (40, 8, 128, "bf16", "bf16", 96, True, "qk", None, 16, True),
+    (64, 8, 128, "bf16", "f32", 128, False, "qk", None, 64, True),
+    (12, 4, 256, "f32", "f32", 256, True, "qk", None, 16, True),
+    (12, 4, 256, "f32", "f32", 136, False, "", None, 0, True),
+    (30, 5, 128, "f32", "f32", 128, False, "k", None, 0, False)])
+def test_rows_one_block_walks_a_rows_heads(nq, nkv, d, dtype, src, rotary, half, norm, e4m3, page, side):
+    # rows enough for one block per row, which walks several chunks of its heads (the last one
+    # ragged in most of these) with the next one's values loaded ahead
+    lens, starts, lead, tail = [1, 500, 0, 131, 2, 30, 64], [9, 0, 4, 1000, 300, 63, 16], 3, 5
+    m, shape = _model(nq, nkv, d, dtype, max_batch=len(lens))
+    dt, heads, n = shape.torch_dtype, nq + 2 * nkv, lead + sum(lens) + tail
+    chunk = 256 // (1 << (d // 8 - 1).bit_length())  # heads that a block takes at a time
+    chunks = -(-heads // chunk)
+    assert chunks > 1 and chunks * n > 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    x = _randn((n, heads * d), torch.float32 if src == "f32" else dt, 250, 1.5)
+    gains = [(1 + 0.1 * torch.randn(d, generator=_gen(251 + i))).to(dt) for i in range(2)]
+    top = max(s + l for s, l in zip(starts, lens))
+    table = A.rotation_table(top, rotary, kind="linear", factor=4.0).astype(np.float32) if rotary else None
+    cu = [lead]
+    for l in lens:
+        cu.append(cu[-1] + l)
+    if page:
+        pages = [max(1, math.ceil((s + l) / page)) for s, l in zip(starts, lens)]
+        pt, total = synth.page_table(pages, max(pages), 7)
+        kv = binding.KVCache(shape, n_pages=total, page_size=page, page_table=pt.cuda(), e4m3=e4m3)
+    else:
+        kv = binding.KVCache(shape, batch=len(lens), capacity=top, e4m3=e4m3)
+    mark = 0x35 if e4m3 else 7.0
+    kv.k.fill_(mark)
+    kv.v.fill_(mark)
+    q_out = torch.full((n, nq * d), 3.0, dtype=dt, device="cuda")
+    ko, vo = (torch.full((n, nkv * d), 3.0, dtype=dt, device="cuda") if side else None for _ in range(2))
+    rope = binding.Rope(torch.from_numpy(table).cuda(), binding.ROPE_HALF if half else binding.ROPE_ADJACENT) \
+        if rotary else None
+    m.op_rope_norm_append(x.cuda(), _i32(starts), 0, kv, q_out, rope=rope, cu_rows=_i32(cu),
+                          q_gain=gains[0].cuda() if "q" in norm else None,
+                          k_gain=gains[1].cuda() if "k" in norm else None, eps=1e-6, k_out=ko, v_out=vo)
+    m.sync()
+    # all rows at once in fp64
+    r = np.arange(cu[0], cu[-1])
+    seq = np.searchsorted(np.array(cu[1:]), r, side="right")
+    pos = np.array(starts)[seq] + r - np.array(cu)[seq]
+    y = f64(x)[r].reshape(len(r), heads, d)
+    q, k, v = y[:, :nq], y[:, nq:nq + nkv], y[:, nq + nkv:]
+    q = A.head_norm(q, f64(gains[0]), 1e-6) if "q" in norm else q
+    k = A.head_norm(k, f64(gains[1]), 1e-6) if "k" in norm else k
+    if rotary:
+        c, s = table.astype(np.float64)[pos][:, None, :, 0], table.astype(np.float64)[pos][:, None, :, 1]
+        i0 = np.arange(rotary // 2) if half else 2 * np.arange(rotary // 2)
+        i1 = i0 + rotary // 2 if half else i0 + 1
+        q, k = q.copy(), k.copy()
+        for t in (q, k):
+            a, b = t[..., i0], t[..., i1]
+            t[..., i0], t[..., i1] = a * c - b * s, a * s + b * c
+    for got, ref, what in ((q_out, q, "q"),) + (((ko, k, "k rows"), (vo, v, "v rows")) if side else ()):
+        big = np.abs(ref).max(-1, keepdims=True)
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * big if dtype == "bf16" else 2.0 ** -24 * np.abs(ref) + 32 * 2.0 ** -24 * big
+        _within(got[cu[0]:cu[-1]].view(len(r), -1, d), ref, tol, what)
+        assert torch.all(got[:lead] == 3.0) and torch.all(got[cu[-1]:] == 3.0)
+    for cache, ref, scale in ((kv.k, k, e4m3 and e4m3[0]), (kv.v, v, e4m3 and e4m3[1])):
+        big = np.abs(ref).max(-1, keepdims=True)
+        c = cache.view(torch.float8_e4m3fn).float() if e4m3 else cache
+        c = f64(c)[0]
+        at = (pt.numpy()[seq, pos // page], slice(None), pos % page) if page else (seq, slice(None), pos)
+        got = torch.from_numpy(c[at])
+        if e4m3:
+            ref = np.clip(ref / scale, -448, 448)
+            tol = 2.0 ** -4 * np.abs(ref) + 2.0 ** -10 + 2.0 ** -18 * np.minimum(big / scale, 448)
+        elif dtype == "bf16":
+            tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * big
+        else:
+            tol = 2.0 ** -24 * np.abs(ref) + 32 * 2.0 ** -24 * big
+        _within(got, ref, tol, "cache")
+        rest = np.ones(c.shape[:1] + c.shape[2:3], bool)
+        rest[(at[0], at[2])] = False
+        left = cache[0].permute(0, 2, 1, 3)[torch.from_numpy(rest).cuda()]
+        assert left.numel() and torch.all(left == mark), "another slot was written"
+
+
 # --------------------------------------------------------------------------- refusals
 def test_refusals():
     m, shape = _model(4, 2, max_batch=2, max_seq=64)
