@@ -1078,6 +1078,60 @@ def test_rows_one_block_walks_a_rows_heads(nq, nkv, d, dtype, src, rotary, half,
         assert left.numel() and torch.all(left == mark), "another slot was written"
 
 
+# --------------------------------------------------------------------------- caches with room to grow
+@pytest.mark.parametrize("room", [1024, 4096, 32768])
+@pytest.mark.parametrize("dtype,nq,nkv,positions,shared", [
+    ("bf16", 8, 8, [465], 0), ("bf16", 32, 32, [465], 0), ("bf16", 16, 1, [465, 0], 0),
+    ("bf16", 8, 8, [499, 250, 3, 120], 0), ("bf16", 8, 2, [499, 250, 130, 640, 60], 130),
+    ("bf16", 8, 8, [249 - b % 7 for b in range(64)], 0), ("bf16", 40, 8, [959, 900, 999], 900),
+    ("f32", 8, 2, [465, 3, 64], 0), ("f32", 8, 8, [300, 200], 130)])
+@pytest.mark.parametrize("page", [0, 16])
+def test_shared_cache_with_room(room, dtype, nq, nkv, positions, shared, page):
+    # the cache has room for many more keys than there are, which chooses other splits of them
+    B, d, G = len(positions), 128, nq // nkv
+    if page == 0 and B * nkv * room > 1 << 20:
+        pytest.skip("the same plan as the paged cache's")
+    m, shape = _model(nq, nkv, d, dtype, max_batch=B, max_seq=room)
+    dt, top = shape.torch_dtype, max(positions) + 1
+    q = _randn((B, nq, d), dt, 260, 0.4)
+    k = _randn((B, nkv, top, d), dt, 261, 1.0)
+    k[:, :, :shared] = k[:1, :, :shared]
+    if page:
+        width = -(-top // page)
+        n_pages = B * width
+        table = torch.full((B, room // page), -1, dtype=torch.int32)
+        table[:, :width] = torch.randperm(n_pages, generator=_gen(262)).view(B, width).int()
+        slots = (1, n_pages, nkv, page, d)
+    else:
+        slots = (1, B, nkv, room, d)
+    one = _one_key_per_dim(top, B * nkv, dt).view(top, B, nkv, d).permute(1, 2, 0, 3).clone()
+    for v, more in ((_randn((B, nkv, top, d), dt, 263), 0.0), (one, 2.0 ** -8)):
+        v[:, :, :shared] = v[:1, :, :shared]
+        caches = []
+        for t in (k, v):
+            c = torch.full(slots, float("nan"), dtype=dt, device="cuda")
+            for b, p in enumerate(positions):
+                n = max(p + 1, shared)
+                if page:
+                    at = torch.arange(n)
+                    c[0][table[b].long()[at // page].cuda(), :, (at % page).cuda()] = t[b, :, :n].transpose(0, 1).cuda()
+                else:
+                    c[0, b, :, :n] = t[b, :, :n].cuda()
+            caches.append(c)
+        kw = dict(n_pages=n_pages, page_size=page, page_table=table.cuda()) if page else dict(batch=B, capacity=room)
+        kv = binding.KVCache(shape, k=caches[0], v=caches[1], **kw)
+        out = torch.full((B, nq * d), 3.0, dtype=dt, device="cuda")
+        m.op_attention_decode_shared(q.cuda(), _i32(positions), 0, kv, out, shared_len=shared)
+        m.sync()
+        for b, p in enumerate(positions):
+            K, V = (t[b, :, :p + 1].cuda().double().repeat_interleave(G, 0) for t in (k, v))
+            w = torch.softmax(torch.einsum("hd,hjd->hj", q[b].cuda().double(), K) / math.sqrt(d), -1)
+            ref, mass = f64(torch.einsum("hj,hjd->hd", w, V)), f64(torch.einsum("hj,hjd->hd", w, V.abs()))
+            big = float(q.float().abs().max() * k.float().abs().max()) * math.sqrt(d) if dtype == "f32" else 0
+            _within(out[b].view(nq, d), ref, _attn_bound(ref, mass, dtype, p + 1, d, big, 0) + more * np.abs(ref),
+                    "b=%d" % b)
+
+
 # --------------------------------------------------------------------------- refusals
 def test_refusals():
     m, shape = _model(4, 2, max_batch=2, max_seq=64)
