@@ -93,6 +93,7 @@ struct FormsParams {
   int key_limit, shared_len, shared_seq;
   float *part_o, *part_ml;                  // [B n_q][splits][128], [B n_q][splits][2] (max log2, sum)
   int splits;                               // partials a row has room for
+  size_t partials;                          // partials in all
   int *used;                                // how many of them are written
   int sm_count;
   int waiting;                              // the own keys' CTAs wait for this kernel
@@ -514,8 +515,9 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     const int n = prefix_share<KIND>(p, lane);
     if (lane == 0) {
       ctl[4] = n;
-      if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-        *p.used = ((p.shared_len + TN - 1) / TN + n - 1) / n * (p.alternate ? 2 : 1);
+      const int used = ((p.shared_len + TN - 1) / TN + n - 1) / n * (p.alternate ? 2 : 1);
+      if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && bc_ok(used <= p.splits, p.status))
+        *p.used = used;
     }
   }
   tc_fence_before();
@@ -990,7 +992,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
             float u[32];
             tmem_ld32(oc + q, reinterpret_cast<uint32_t*>(u));
             tmem_ld_wait();
-            if (row_ok) {
+            if (row_ok && bc_ok(row < (size_t)p.n_rows, p.status)) {
 #pragma unroll
               for (int i = 0; i < 32; i += 16) {
                 uint32_t x[8];
@@ -1009,20 +1011,21 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       } else {
         const int mine = p.alternate ? 2 * w.split + t : w.split;
         const size_t at = (row * p.n_q + head) * p.splits + mine;
+        const bool store = row_ok && bc_ok(mine < p.splits && at < p.partials, p.status);
         if (count > 0) {
 #pragma unroll 1
           for (int q = 0; q < 64; q += 32) {
             float u[32];
             tmem_ld32(oc + q, reinterpret_cast<uint32_t*>(u));
             tmem_ld_wait();
-            if (row_ok) {
+            if (store) {
 #pragma unroll
               for (int i = 0; i < 32; i += 8)
                 store_sector(p.part_o + at * 128 + 64 * grp + q + i, reinterpret_cast<const uint32_t*>(u + i));
             }
           }
         }
-        if (row_ok && grp == 0 && (p.alternate || count > 0)) {  // no visible key: no mass
+        if (store && grp == 0 && (p.alternate || count > 0)) {  // no visible key: no mass
           p.part_ml[2 * at] = l == 0.f ? -INFINITY : merge_max(m, l);
           p.part_ml[2 * at + 1] = l;
         }
@@ -1133,6 +1136,7 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
   p.part_o = a.partial;
   p.part_ml = a.partial + s.partials * 128;
   p.splits = s.prefix_parts;
+  p.partials = s.partials;
   p.used = reinterpret_cast<int*>(a.partial + s.partials * 130);
   p.sm_count = a.sm_count;
   p.waiting = !s.join;

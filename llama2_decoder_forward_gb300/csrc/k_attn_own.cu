@@ -73,6 +73,7 @@ struct OwnParams {
   int join;                    // leave partials for the joining kernel
   float *part_o, *part_ml;     // [B n_q][prefix_parts][...]
   float *own_o, *own_ml;       // [B n_q][splits][...] (with a prefix, or splits > 1 without cluster)
+  size_t rows, own_room;       // B n_q; partials behind the prefix's
   float scale, cap;
   const float* slopes;
 };
@@ -620,6 +621,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   if (prefix && !p.join) {
     grid_dep_wait();
     parts = __ldcg(p.used);
+    if (!bc_ok(parts <= p.prefix_parts, p.status)) parts = 0;
   }
   const float* so = reinterpret_cast<const float*>(smem);
   const float* sm = so + 4 * 16 * HD;
@@ -644,6 +646,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
       }
     }
     const size_t bh = (size_t)b * p.n_q + (size_t)g * p.G + r;
+    if (!bc_ok(bh < p.rows && (!p.join || bh * p.splits + split < p.own_room), p.status)) continue;
     if (p.cluster) {
       reinterpret_cast<float4*>(mine + r * HD)[lane] = x.o;
       if (lane == 0) *reinterpret_cast<float2*>(mine + 16 * HD + 2 * r) = make_float2(x.m, x.l);
@@ -700,12 +703,14 @@ __global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int 
   Parts<2> own;
   pre.load(p.part_o, p.part_ml, (size_t)bh * p.prefix_parts, p.prefix_parts, lane);
   own.load(p.own_o, p.own_ml, (size_t)bh * p.splits, p.splits, lane);
-  const int parts = p.prefix_parts ? __ldcg(p.used) : 0;
+  int parts = p.prefix_parts ? __ldcg(p.used) : 0;
+  if (!bc_ok(parts <= p.prefix_parts && (size_t)rows * p.splits <= p.own_room, p.status)) return;
   const int n = key_position(__ldcg(p.positions + bh / p.n_q), p.key_limit) + 1;
   int used = n > p.first;  // own splits that have keys
   if (used && p.splits > 1) {
     const int share = own_share(p, n);
     used = (n - p.base + share - 1) / share;
+    if (!bc_ok(used <= p.splits, p.status)) return;
   }
   RowSum x;
   pre.fold(parts, lane, x);
@@ -808,6 +813,8 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
   const size_t rows = (size_t)a.B * a.n_q;
   p.part_o = a.partial;
   p.part_ml = p.part_o + s.partials * HD;
+  p.rows = rows;
+  p.own_room = s.partials - rows * s.prefix_parts;
   p.own_o = p.part_o + rows * s.prefix_parts * HD;
   p.own_ml = p.part_ml + rows * s.prefix_parts * 2;
   p.scale = a.sc.scale;

@@ -48,6 +48,7 @@ struct SimtParams {
   // decode
   const int32_t *positions, *page_table;
   int layer, page_size, capacity, batch_cap, n_pages, max_pages, key_limit, shared_len, shared_seq;
+  int n_seq;
   int row_chunks;  // chunks of 16 heads per K/V head
   int splits;      // CTAs (a cluster) that share an item's key tiles
 };
@@ -56,6 +57,8 @@ struct SimtParams {
 // for a page outside the pool.
 __device__ __forceinline__ long long key_offset(const SimtParams& p, int b, int g, int j) {
   if (j < p.shared_len) b = p.shared_seq;
+  if (!bc_ok(p.page_size == 0 ? b < p.batch_cap && j < p.capacity : j / p.page_size < p.max_pages, p.status))
+    return -1;
   if (p.page_size == 0)
     return ((((long long)p.layer * p.batch_cap + b) * p.n_kv + g) * p.capacity + j) * p.d;
   const int pi = j / p.page_size;
@@ -138,6 +141,7 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     g = h / p.G;
     q0 = tile * RT;
     rows = min(RT, n - q0);
+    if (!bc_ok(lo + q0 + rows <= p.n_rows && h0 < p.n_q, p.status)) return;
     pre = p.prefix_len ? min(max(p.prefix_len[b], 0), n) : 0;
     n_keys = max(q0 + rows, pre);
   } else {
@@ -146,6 +150,7 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     b = item / (p.row_chunks * p.n_kv);
     h0 = g * p.G + c * RT;
     rows = min(RT, p.G - c * RT);
+    if (!bc_ok(b < p.n_seq && h0 + rows <= p.n_q, p.status)) return;
     pos = p.positions[b];
     if ((pos < 0 || pos >= p.key_limit) && part == 0 && threadIdx.x == 0)
       flag(p.status, LLAMA_FLAG_POS_RANGE);
@@ -395,6 +400,7 @@ cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st) {
   p.key_limit = a.key_limit;
   p.shared_len = a.shared_len;
   p.shared_seq = a.shared_seq;
+  p.n_seq = a.B;
   p.row_chunks = (p.G + 15) / 16;
   const long long items = (long long)a.B * a.n_kv * p.row_chunks;
   p.splits = simt_splits(items, a.key_limit, a.sm_count);

@@ -123,6 +123,10 @@ __global__ void __launch_bounds__(RN_THREADS) rope_norm_append_kernel(RopeNormAr
     }
     if (bad && threadIdx.x == 0) flag(a.status, bad);
   }
+  // (the checked build: the layer's slots end there)
+  const long long slots = (long long)(a.layer + 1) * (a.page_size == 0 ? a.batch_cap : a.n_pages) * a.n_kv * slot_step;
+  if (slot0 >= 0 && !bc_ok(slot0 + (a.n_kv - 1) * slot_step < slots, a.status)) slot0 = -1;
+  if (!bc_ok(r < a.n_rows && (!a.cu_rows || (r >= a.cu_rows[b] && r < a.cu_rows[b + 1])), a.status)) return;
   // this thread's four angles: the same ones for every head
   float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
   const bool turns = u < a.rotary / 8;
