@@ -543,7 +543,9 @@ typedef struct llama_scores {
  * T [n_rows, n_q d]; rows of no document are left as they were. scores may be
  * NULL (plain scores). A hidden key takes part with weight 0 where it shares
  * a tile of 128 keys with a visible one, so V must be finite within a
- * document; other documents' rows and rows of none may hold anything. cu_rows
+ * document; other documents' rows and rows of none may hold anything. In bf16
+ * with a cap of up to 50 and no slopes no maximum is subtracted, so |V| must stay
+ * below 2^55 / (a document's keys) for the sums to stay in fp32. cu_rows
  * outside [0, n_rows] or decreasing flag LLAMA_FLAG_POS_RANGE (rows outside
  * are skipped). Any number of rows (no context limit), n_rows * n_q < 2^30. */
 int llama_op_attention_docs(llama_ctx* ctx, const void* q, const void* k, const void* v,
@@ -559,7 +561,7 @@ int llama_op_attention_docs(llama_ctx* ctx, const void* q, const void* k, const 
  * come from b's own page there. shared_len 0 is plain decode attention with
  * these scores. Where a position lies below shared_len, V of the keys from it up
  * to shared_len must be finite (they take part with weight 0); K may hold
- * anything there. positions as in llama_op_attention_decode (a negative one
+ * anything there. |V| of the shared keys as in llama_op_attention_docs. positions as in llama_op_attention_decode (a negative one
  * flags and gives zeros; one past the cache or max_seq flags, and the keys in
  * range are attended). out T [B, n_q d]. B <= max_batch and 65535; shared_len <= the
  * cache's positions and max_seq. The cache has the context's dtype (an E4M3

@@ -1,5 +1,5 @@
-// Pieces shared by the attention kernels with capped or biased scores: the map
-// from work items to packed documents, and how partial results are merged.
+// Pieces shared by the attention kernels with capped or biased scores: a
+// document's rows, a decode row's last key, the cap, how partial results are merged.
 #pragma once
 
 #include "common.cuh"
@@ -37,36 +37,5 @@ constexpr float kTanh[13] = {
     0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f,
     0.9999994039535522f, -0.3332904279232025f, 0.13281433284282684f, -0.051605671644210815f,
     0.016743114218115807f, -0.0030670599080622196f};
-
-// Work item -> (document, tile of `rows` query rows, first row, row count), for a
-// whole warp: 32 documents per step, their tile counts summed by a warp scan.
-// Tiles of a document come last first (the longest rows of a causal mask).
-// False when the item is past the last document's tiles.
-__device__ __forceinline__ bool find_tile(const int32_t* cu, int n_docs, int n_rows, int rows,
-                                          int item, uint32_t* status, int& b, int& tile, int& lo,
-                                          int& n) {
-  const int lane = threadIdx.x & 31;
-  for (int b0 = 0; b0 < n_docs; b0 += 32) {
-    int my_lo = 0, my_n = 0;
-    if (b0 + lane < n_docs) doc_rows(cu, b0 + lane, n_rows, status, my_lo, my_n);
-    int upto = (my_n + rows - 1) / rows;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, item < upto);
-    if (m) {
-      const int w = __ffs(m) - 1;
-      b = b0 + w;
-      tile = __shfl_sync(0xffffffffu, upto, w) - 1 - item;
-      lo = __shfl_sync(0xffffffffu, my_lo, w);
-      n = __shfl_sync(0xffffffffu, my_n, w);
-      return true;
-    }
-    item -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return false;
-}
 
 }  // namespace llgb

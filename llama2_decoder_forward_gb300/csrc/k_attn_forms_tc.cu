@@ -102,9 +102,9 @@ struct FormsParams {
 };
 
 // What the scores need. A cap bounds them, so up to kFixedCap (log2 units) the
-// weights are 2^s with no maximum subtracted: 2^+-72 times any sum stays inside
-// fp32 (and bf16's exponent), and the row maxima, their exchange and every
-// rescale fall away.
+// weights are 2^s with no maximum subtracted: 2^+-72 times a sum stays inside fp32
+// (and bf16's exponent) for |V| below 2^55 / keys, and the row maxima, their
+// exchange and every rescale fall away.
 enum { KPlain, KBias, KCapFixed, KCap };
 constexpr float kFixedCap = 72.5f;  // caps up to 50
 

@@ -1132,6 +1132,24 @@ def test_shared_cache_with_room(room, dtype, nq, nkv, positions, shared, page):
                     "b=%d" % b)
 
 
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (50.0, False), (50.0, True)])
+def test_docs_values_scale(cap, bias):
+    # the outputs of values times a power of two are the outputs times it, to the bit, with every
+    # score at the cap or far below it
+    m, _ = _model(4, 2)
+    n = 400
+    q, k, v = (_randn((n, h, 128), torch.bfloat16, 270 + h, s).cuda() for h, s in ((4, 8.0), (2, 8.0), (2, 1.0)))
+    sc = binding.Scores(cap=cap, slopes=_slopes(4).cuda() if bias else None)
+    outs = []
+    for e in (0, 40, -30):
+        out = torch.empty(n, 512, dtype=torch.bfloat16, device="cuda")
+        m.op_attention_docs(q, k, v * 2.0 ** e, _i32([0, 250, n]), out, scores=sc)
+        outs.append(out.float() * 2.0 ** -e)
+    m.sync()
+    assert torch.isfinite(outs[0]).all() and torch.equal(outs[0], outs[1])
+    assert torch.equal(outs[0], outs[2])
+
+
 # --------------------------------------------------------------------------- refusals
 def test_refusals():
     m, shape = _model(4, 2, max_batch=2, max_seq=64)
