@@ -1150,6 +1150,55 @@ def test_docs_values_scale(cap, bias):
     assert torch.equal(outs[0], outs[2])
 
 
+def test_docs_all_empty_and_single_rows():
+    for dtype in ("bf16", "f32"):
+        m, shape = _model(4, 2, 128, dtype)
+        q, k = (torch.ones(3, h, 128, dtype=shape.torch_dtype, device="cuda") for h in (4, 2))
+        out = torch.full((3, 512), 3.0, dtype=shape.torch_dtype, device="cuda")
+        m.op_attention_docs(q, k, k, _i32([3, 3, 3]), out, prefix=_i32([1, 2]))
+        m.sync()
+        assert torch.all(out == 3.0)
+        _docs_case(4, 2, 128, dtype, [0] * 70 + [1] + [0] * 70, prefix=[5] * 141)
+        _docs_case(1, 1, 128, dtype, [1])
+
+
+@pytest.mark.parametrize("page", [1, 5, 12])
+def test_fp32_pages_of_any_size(page):
+    _shared_case(4, 2, 64, "f32", [0, 70, 99, 130], 52, page=page, cap=20.0)
+    _rows_case(4, 2, 64, "f32", "f32", [7, 1, 20], [0, 100, 3], rotary=64, page=page)
+
+
+@pytest.mark.parametrize("nq,nkv,shared,room", [(64, 8, 1100, 1600), (40, 40, 3200, 3400), (16, 16, 0, 700)])
+def test_append_and_decode_without_a_wait_between(nq, nkv, shared, room):
+    # the own keys' blocks start while the prefix kernel runs: they see what was appended just before it,
+    # and what is enqueued behind them waits for both
+    B, steps = 24, 12
+    m, shape = _model(nq, nkv, max_batch=B, max_seq=room)
+    k, v = (_randn((1, B, nkv, room, 128), torch.bfloat16, 280 + i).cuda() for i in range(2))
+    first = [shared + (29 * b) % (room - shared - steps) for b in range(B)]
+    xs = [_randn((B, shape.qkv_rows), torch.float32, 290 + i).cuda() for i in range(steps)]
+    pos = [_i32([p + i for p in first]) for i in range(steps)]
+    rope = binding.Rope(None, binding.ROPE_HALF, 128)
+    runs = []
+    for wait in (True, False):
+        ck, cv = k.clone(), v.clone()
+        cache = binding.KVCache(shape, batch=B, capacity=room, k=ck, v=cv)
+        q = torch.empty(B, nq * 128, dtype=torch.bfloat16, device="cuda")
+        outs = [torch.empty_like(q) for _ in range(steps)]
+        torch.cuda.synchronize()
+        for i in range(steps):
+            m.op_rope_norm_append(xs[i], pos[i], 0, cache, q, rope=rope)
+            if wait:
+                torch.cuda.synchronize()
+            m.op_attention_decode_shared(q, pos[i], 0, cache, outs[i], shared_len=shared, scores=binding.Scores(cap=30.0))
+            if wait:
+                torch.cuda.synchronize()
+        m.sync()
+        runs.append((outs, ck, cv))
+    assert all(torch.equal(a, b) for a, b in zip(runs[0][0], runs[1][0]))
+    assert torch.equal(runs[0][1], runs[1][1]) and torch.equal(runs[0][2], runs[1][2])
+
+
 # --------------------------------------------------------------------------- refusals
 def test_refusals():
     m, shape = _model(4, 2, max_batch=2, max_seq=64)
