@@ -34,14 +34,15 @@
 // producers load the next item's Q, K and V while the softmax and the store of
 // the last one go on, and barriers and tensor memory are set up once (17 packed
 // documents of 8192 rows, 64 heads: 246 us with a CTA per item, 216 us so, and
-// 160 us with the items dealt out longest first and published by one warp, and
-// whole sectors stored).
+// 162 us with the items dealt out longest first and published by one warp, and
+// whole sectors stored; back to back, 169 us among other work).
 //
 // P is rounded once to bf16 (V's type, which the MMA shares), and the sum that
 // normalises it is that of the rounded weights, in fp32: what the dominant keys
 // of a row lose by rounding cancels (error against 64 bits, relative to the
-// outputs' root mean square: 0.0018 instead of 0.0022; rounding the output alone
-// is 0.0016). The add takes a bf16 operand, so it costs nothing beside the sum of
+// outputs' root mean square, packed biased documents: 0.0019 instead of 0.0022;
+// prefixes 0.0020, capped scores 0.0021-0.0022; rounding the output alone is
+// 0.0016-0.0017). The add takes a bf16 operand, so it costs nothing beside the sum of
 // the unrounded weights but its latency (1 %; unpacked first, 6 %).
 //
 // What bounds it: plain scores, the tensor pipe and the hand-overs between it

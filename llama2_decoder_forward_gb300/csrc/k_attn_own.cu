@@ -21,8 +21,11 @@
 // shared memory; more (few sequences with very long contexts) leave partials for
 // a joining kernel. The splits share the keys that a sequence has, not those that
 // the cache has room for (8 sequences of up to 4000 keys, 8 K/V heads: 18.7 ->
-// 16.1 us). One sequence, 466 keys, 32 K/V heads: 8.7 us unsplit, 5.8 us as
-// clusters of 8.
+// 16.1 us). How many there are, and whether the longest start first, is chosen on
+// the host, which knows the room and not the keys. One sequence, 466 keys, 32 K/V
+// heads: 8.7 us unsplit, 5.9 us as clusters of 8, which it gets with room for up to
+// 1024 keys; with room for 4096 and 32768 it is 7.6 and 7.7 us (8 K/V heads: 4.8,
+// 6.7 and 7.0), and 256 sequences of 250 keys take 43.5, 62.5 and 62.9 us.
 //
 // Beside a prefix: the launch follows the prefix kernel's and starts on the SMs
 // that it leaves free. That kernel lets it start only after its own wait, so
@@ -32,7 +35,7 @@
 // SM idle); one CTA's producer waits for the prefix kernel, so that the joining
 // kernel, which waits for this one, finds both kinds of partials. A short prefix
 // is over before most CTAs are: they wait and merge, which saves the third launch
-// (32 sequences over 500 shared keys: 31 us, with the joining kernel 36). 128
+// (32 sequences over 500 shared keys: 32 us, with the joining kernel 36). 128
 // sequences over 16384 shared keys: 154 us, 6.1 TB/s of keys and values.
 #include <algorithm>
 #include <climits>

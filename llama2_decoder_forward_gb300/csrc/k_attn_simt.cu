@@ -16,8 +16,12 @@
 // math library). Where there are few items, up to 8 CTAs (a cluster) take an
 // item's key tiles in turn and merge through distributed shared memory.
 //
-// Bound by latency: with 4 warps per scheduler (two CTAs per SM) half of the
-// cycles issue nothing, for waits on shared memory and on barriers between tiles;
+// Bound by shared memory before arithmetic: per four dims a warp reads two K vectors
+// (4 wavefronts each) and a broadcast per row, 12 wavefronts for documents against
+// the 8 cycles that its 32 multiply-adds take of the SM, and P V the same; in
+// decode the row slots beyond a K/V head's query heads compute rows that are not
+// stored. On top comes latency: with 4 warps per scheduler (two CTAs per SM) half of
+// the cycles issue nothing, for waits on shared memory and on barriers between tiles;
 // hence the small single stage (four CTAs at 64 dims). Measured, against 16
 // lanes per row with two rows each: documents of 700 rows in all, 8 heads, 64
 // dims 49 -> 44 us; one document of 4000 rows 558 -> 549 us, with 128 dims 980 ->
