@@ -214,7 +214,7 @@ def work(c):
         m = min(n, c["keep"])
         rest = n - c["first"] - c["recent"]
         stay = c["first"] + rest / max(1, n - c["keep"]) if n > c["keep"] else m
-        b += heads * (8 * n + 4 * m + 4 * d * es * max(0.0, m - stay))
+        b += heads * (4 * n + 4 * max(lens) + 4 * m + 4 * d * es * max(0.0, m - stay))
     return {"bytes": int(b), "flops": 0}
 
 
@@ -466,11 +466,9 @@ def _plain_evict(s):
     there = kept < top
     _move(s, torch.where(there, kept, -1), torch.arange(keep, device="cuda").expand(kept.shape))
     s["kept"].copy_(torch.where(there, kept, -1))
-    s["weights_out"].copy_(s["weights"])
-    s["weights_out"].masked_fill_(slot < n, 0.0)
     m = min(keep, top)
-    s["weights_out"][..., :m] = torch.where(there[..., :m], s["weights"].gather(-1, kept[..., :m].clamp(max=top - 1)),
-                                            s["weights_out"][..., :m])
+    s["weights_out"].zero_()
+    s["weights_out"][..., :m] = s["weights"].gather(-1, kept[..., :m].clamp(max=top - 1)).where(there[..., :m], 0.0)
 
 
 # ---------------------------------------------------------------- the definition in fp64
@@ -536,15 +534,15 @@ def exact(c, seed):
         return None
     # of an eviction only the weights are numbers that could be rounded
     want = s["weights"].double().cpu()
-    new = want.clone()
+    new = torch.zeros_like(want)
     for layer in range(c["layers"]):
         for b, n in enumerate(lens):
             if n <= c["keep"]:
+                new[layer, b, :, :n] = want[layer, b, :, :n]
                 continue
             for g in range(nkv):
                 w = want[layer, b, g, :n].numpy()
                 middle = c["first"] + np.argsort(-w[c["first"]:n - c["recent"]], kind="stable")
                 kept = sorted([*range(c["first"]), *middle[:c["keep"] - c["first"] - c["recent"]], *range(n - c["recent"], n)])
-                new[layer, b, g, :n] = 0.0
                 new[layer, b, g, :c["keep"]] = torch.from_numpy(w[kept])
     return {"kept": None, "weights": new, "k": None, "v": None}
