@@ -309,7 +309,7 @@ int llama_free(llama_ctx* ctx);
  * and the launch count since the last reset, synchronising the stream. */
 #define LLAMA_KERNEL_RMSNORM 0
 #define LLAMA_KERNEL_GEMM 1
-#define LLAMA_KERNEL_ROPE_APPEND 2
+#define LLAMA_KERNEL_ROPE_APPEND 2 /* and the cache's other writers: commit, evict */
 #define LLAMA_KERNEL_ATTN_DECODE 3
 #define LLAMA_KERNEL_ATTN_PREFILL 4
 #define LLAMA_KERNEL_EMBED 5
@@ -570,6 +570,64 @@ int llama_op_attention_decode_shared(llama_ctx* ctx, const void* q, const int32_
                                      int32_t B, int32_t layer, const llama_kv* kv,
                                      int32_t shared_len, int32_t shared_seq,
                                      const llama_scores* scores, void* out);
+
+/* ---- Caches whose slots are not simply one token after the other: drafted trees
+ * and dropped keys. A step that verifies drafted tokens appends them behind the
+ * cached ones (llama_op_rope_norm_append_at: row i of a tree in slot start + i, at
+ * position start + its depth), attends (llama_op_attention_tree) and keeps the rows
+ * that were accepted (llama_op_cache_commit). A cache held to a number of keys adds up
+ * what each key weighs (llama_op_attention_decode_weights), drops the lightest
+ * (llama_op_cache_evict), and appends at slots behind the kept ones with the tokens'
+ * own positions. Streams, devices, graphs and overlaps as above. ---- */
+
+/* llama_op_rope_norm_append with positions of their own: row r goes to the slot that
+ * cu_rows and start_pos say, and rotates by positions[r] (DEVICE int32 [n_rows]; NULL: by
+ * its slot). A position outside the table (0 .. n_pos-1) flags
+ * LLAMA_FLAG_POS_RANGE: the row's outputs are zeros and nothing is cached; so does a
+ * negative slot. Without rotation positions are not read. */
+int llama_op_rope_norm_append_at(llama_ctx* ctx, const void* qkv, int32_t qkv_dtype, int64_t qkv_ld,
+                                 int32_t n_rows, const int32_t* cu_rows, const int32_t* start_pos,
+                                 int32_t B, const int32_t* positions, const llama_rope* rope,
+                                 const void* q_gain, const void* k_gain, float norm_eps, int32_t layer,
+                                 const llama_kv* kv, void* q_out, void* k_out, void* v_out);
+
+/* Of a cache's layers, all. */
+#define LLAMA_ALL_LAYERS (-1)
+
+/* Moves the accepted rows of a drafted tree together: in layer `layer` (or
+ * LLAMA_ALL_LAYERS) slot start_pos[b] + path[b][i] of sequence b goes to slot
+ * start_pos[b] + i for i = 0 .. path_len[b] - 1, K and V of every head, in place.
+ * path: DEVICE int32 [B][path_ld], the accepted rows of the tree in strictly ascending order
+ * (an ancestor comes before its descendants); start_pos, path_len: DEVICE int32 [B].
+ * Any cache type. An entry that does not ascend or whose slot is past the cache, a
+ * negative start and a path_len outside [0, path_ld] set LLAMA_FLAG_POS_RANGE (the
+ * entry, the sequence, what is outside is skipped); a page id outside the pool sets
+ * LLAMA_FLAG_PAGE_RANGE and its rows are skipped. The other slots stay as they
+ * are; a page that sequences share must not hold a slot that moves. Asynchronous;
+ * one launch. */
+int llama_op_cache_commit(llama_ctx* ctx, const llama_kv* kv, int32_t layer, const int32_t* start_pos,
+                          int32_t B, const int32_t* path, int32_t path_ld, const int32_t* path_len);
+
+/* Evicts from every sequence with more than `keep` filled slots: of its slots 0 ..
+ * lens[b]-1 (DEVICE int32 [B]) the `first` first, the `recent` last and, of those
+ * between, the keep - first - recent of largest weight stay (equal weights: the lower slot; NaN
+ * counts below every number), for each layer and K/V head on its own. What stays
+ * is moved to slots 0 .. keep-1 in place, in its order, so that sequence b then
+ * has min(lens[b], keep) slots; a sequence with fewer is not changed. Slots behind
+ * hold anything.
+ *   weights     : DEVICE fp32 [layers][B][n_kv][weights_ld], the weight of each slot
+ *                 (layers: all of the cache's with LLAMA_ALL_LAYERS, else 1)
+ *   weights_out : the same shape: the kept slots' weights, in their new places, and
+ *                 zeros behind them; may be `weights` itself (no other overlap)
+ *   kept        : DEVICE int32 [layers][B][n_kv][keep], the old slots in ascending
+ *                 order, then -1
+ * first + recent <= keep. A length outside [0, limit], limit the cache's slots and
+ * weights_ld, sets LLAMA_FLAG_POS_RANGE and is cut; a page id outside the pool sets
+ * LLAMA_FLAG_PAGE_RANGE and its rows are not moved. A sequence's pages must be its
+ * own. Any cache type. Asynchronous; two launches. */
+int llama_op_cache_evict(llama_ctx* ctx, const llama_kv* kv, int32_t layer, const int32_t* lens, int32_t B,
+                         int32_t keep, int32_t first, int32_t recent, const float* weights,
+                         int64_t weights_ld, float* weights_out, int32_t* kept);
 
 #ifdef __cplusplus
 }

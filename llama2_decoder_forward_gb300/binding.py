@@ -58,6 +58,7 @@ class Sampling(ctypes.Structure):
                 ("repetition_penalty", ctypes.c_float)]
 
 
+ALL_LAYERS = -1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDS = 0, 1, 2
 ROPE_ADJACENT, ROPE_HALF = 0, 1
 
@@ -143,6 +144,15 @@ _SIGS = {
     "llama_op_attention_decode_shared": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32,
                                                    ctypes.POINTER(KV), c_int32, c_int32,
                                                    ctypes.POINTER(_Scores), c_void_p]),
+    "llama_op_rope_norm_append_at": (c_int32, [c_void_p, c_void_p, c_int32, ctypes.c_int64, c_int32,
+                                               c_void_p, c_void_p, c_int32, c_void_p,
+                                               ctypes.POINTER(_Rope), c_void_p, c_void_p,
+                                               ctypes.c_float, c_int32, ctypes.POINTER(KV), c_void_p,
+                                               c_void_p, c_void_p]),
+    "llama_op_cache_commit": (c_int32, [c_void_p, ctypes.POINTER(KV), c_int32, c_void_p, c_int32,
+                                        c_void_p, c_int32, c_void_p]),
+    "llama_op_cache_evict": (c_int32, [c_void_p, ctypes.POINTER(KV), c_int32, c_void_p, c_int32, c_int32,
+                                       c_int32, c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p]),
     "llama_op_argmax": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p]),
     "llama_sample": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, ctypes.POINTER(Sampling), c_void_p,
                                c_void_p, c_int32, c_void_p, c_void_p]),
@@ -438,6 +448,7 @@ class Model:
         import torch
         l = lib()
         self._append, self._docs = l.llama_op_rope_norm_append, l.llama_op_attention_docs
+        self._append_at = l.llama_op_rope_norm_append_at
         self._shared = l.llama_op_attention_decode_shared
         self._dt, self._qkv_rows = shape.torch_dtype, shape.qkv_rows
         self._i32, self._f32 = torch.int32, torch.float32
@@ -575,11 +586,12 @@ class Model:
 
     def op_rope_norm_append(self, qkv, start_pos, layer, kv: KVCache, q_out, *, rope=None,
                             cu_rows=None, q_gain=None, k_gain=None, eps=None, k_out=None,
-                            v_out=None):
+                            v_out=None, positions=None):
         """Head norms, rotation and KV append of packed rows (llama_op_rope_norm_append).
         qkv [n_rows, (n_q + 2 n_kv) d], fp32 or the model's dtype, rows may be
         strided; start_pos int32 [B]; cu_rows int32 [B + 1], or None for one row
-        per sequence; eps defaults to the model's rms_eps."""
+        per sequence; eps defaults to the model's rms_eps; positions int32 [n_rows]
+        that the rows rotate by (llama_op_rope_norm_append_at), or None: their slots."""
         s, dt = self.shape, self._dt
         i32, f32, dev = self._i32, self._f32, self._dev
         n, width = qkv.shape
@@ -588,16 +600,21 @@ class Model:
                 qkv.get_device() != dev:
             raise ValueError("qkv: want rows of %d %s or fp32 on cuda:%d, got %s %s on %s"
                              % (s.qkv_rows, dt, dev, tuple(qkv.shape), qdt, qkv.device))
-        rc = self._append(
-            self.ctx, qkv.data_ptr(), F32 if qdt is f32 else BF16, ld[0], n,
-            None if cu_rows is None else _need("cu_rows", cu_rows, i32, B + 1, dev),
-            _need("start_pos", start_pos, i32, B, dev), B, None if rope is None else rope._now(dev),
-            None if q_gain is None else _need("q_gain", q_gain, dt, d, dev),
-            None if k_gain is None else _need("k_gain", k_gain, dt, d, dev),
-            s.rms_eps if eps is None else eps, layer, kv._now(s, dt, B, dev),
-            _need("q_out", q_out, dt, n * s.n_q_heads * d, dev),
-            None if k_out is None else _need("k_out", k_out, dt, n * s.n_kv_heads * d, dev),
-            None if v_out is None else _need("v_out", v_out, dt, n * s.n_kv_heads * d, dev))
+        # what the two entry points share: up to the sequences, and behind them
+        head = (self.ctx, qkv.data_ptr(), F32 if qdt is f32 else BF16, ld[0], n,
+                None if cu_rows is None else _need("cu_rows", cu_rows, i32, B + 1, dev),
+                _need("start_pos", start_pos, i32, B, dev), B)
+        rest = (None if rope is None else rope._now(dev),
+                None if q_gain is None else _need("q_gain", q_gain, dt, d, dev),
+                None if k_gain is None else _need("k_gain", k_gain, dt, d, dev),
+                s.rms_eps if eps is None else eps, layer, kv._now(s, dt, B, dev),
+                _need("q_out", q_out, dt, n * s.n_q_heads * d, dev),
+                None if k_out is None else _need("k_out", k_out, dt, n * s.n_kv_heads * d, dev),
+                None if v_out is None else _need("v_out", v_out, dt, n * s.n_kv_heads * d, dev))
+        if positions is None:
+            rc = self._append(*head, *rest)
+        else:
+            rc = self._append_at(*head, _need("positions", positions, i32, n, dev), *rest)
         if rc:
             raise LlamaError(rc, "llama_op_rope_norm_append")
 
@@ -629,6 +646,37 @@ class Model:
             _need("out", out, dt, qn, dev))
         if rc:
             raise LlamaError(rc, "llama_op_attention_decode_shared")
+
+    def op_cache_commit(self, kv: KVCache, start_pos, path, path_len, *, layer=None):
+        """Moves the accepted rows of a drafted tree together (llama_op_cache_commit): path
+        int32 [B, W] ascending rows of each sequence's tree, path_len int32 [B] how many,
+        start_pos int32 [B] the slot of row 0; layer None: every layer."""
+        i32, dev = self._i32, self._dev
+        B, W = path.shape
+        rc = lib().llama_op_cache_commit(
+            self.ctx, kv._now(self.shape, self._dt, B, dev), ALL_LAYERS if layer is None else layer,
+            _need("start_pos", start_pos, i32, B, dev), B, _need("path", path, i32, B * W, dev), W,
+            _need("path_len", path_len, i32, B, dev))
+        if rc:
+            raise LlamaError(rc, "llama_op_cache_commit")
+
+    def op_cache_evict(self, kv: KVCache, lens, keep, weights, kept, *, layer=None, first=0, recent=0,
+                       weights_out=None):
+        """Keeps `keep` slots of every sequence that has more (llama_op_cache_evict): the
+        first, the recent and the heaviest between. lens int32 [B] filled slots; weights
+        fp32 [layers, B, n_kv, ld] (one layer: [B, n_kv, ld] will do) and weights_out, which
+        may be the same (None); kept int32 [layers, B, n_kv, keep]; layer None: every layer."""
+        s, i32, dev = self.shape, self._i32, self._dev
+        B, ld = lens.numel(), weights.shape[-1]
+        heads = (s.n_layers if layer is None else 1) * B * s.n_kv_heads
+        w = _need("weights", weights, self._f32, heads * ld, dev)
+        rc = lib().llama_op_cache_evict(
+            self.ctx, kv._now(s, self._dt, B, dev), ALL_LAYERS if layer is None else layer,
+            _need("lens", lens, i32, B, dev), B, keep, first, recent, w, ld,
+            w if weights_out is None else _need("weights_out", weights_out, self._f32, heads * ld, dev),
+            _need("kept", kept, i32, heads * keep, dev))
+        if rc:
+            raise LlamaError(rc, "llama_op_cache_evict")
 
     def op_embed(self, tokens, out):
         self._chk(lib().llama_op_embed(self.ctx, _p(tokens), tokens.numel(), _p(out)), "llama_op_embed")

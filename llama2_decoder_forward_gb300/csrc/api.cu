@@ -1268,6 +1268,15 @@ int llama_op_rope_norm_append(llama_ctx* c, const void* qkv, int32_t qkv_dtype, 
                               int32_t B, const llama_rope* rope, const void* q_gain,
                               const void* k_gain, float norm_eps, int32_t layer,
                               const llama_kv* kv, void* q_out, void* k_out, void* v_out) {
+  return llama_op_rope_norm_append_at(c, qkv, qkv_dtype, qkv_ld, n_rows, cu_rows, start_pos, B, nullptr, rope,
+                                      q_gain, k_gain, norm_eps, layer, kv, q_out, k_out, v_out);
+}
+
+int llama_op_rope_norm_append_at(llama_ctx* c, const void* qkv, int32_t qkv_dtype, int64_t qkv_ld,
+                                 int32_t n_rows, const int32_t* cu_rows, const int32_t* start_pos,
+                                 int32_t B, const int32_t* positions, const llama_rope* rope,
+                                 const void* q_gain, const void* k_gain, float norm_eps, int32_t layer,
+                                 const llama_kv* kv, void* q_out, void* k_out, void* v_out) {
   TRY(check_ctx(c));
   const llama_config& cf = c->cfg;
   if (!qkv || !start_pos || !q_out || n_rows < 1 || B < 1 || layer < 0 || layer >= cf.n_layers)
@@ -1307,6 +1316,7 @@ int llama_op_rope_norm_append(llama_ctx* c, const void* qkv, int32_t qkv_dtype, 
   a.n_seq = B;
   a.cu_rows = cu_rows;
   a.start_pos = start_pos;
+  a.positions = positions;
   a.q_gain = q_gain;
   a.k_gain = k_gain;
   a.eps = norm_eps;
@@ -1443,6 +1453,91 @@ int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t*
   c->launches += (plan.prefix_parts ? 1 : 0) + (plan.join ? 2 : 1);
   if (plan.prefix_parts) TRY(cuda_rc(launch_shared_prefix(a, plan, c->stream)));
   return cuda_rc(launch_shared_own(a, plan, c->stream));
+}
+
+namespace {
+// The cache of a move: rows of `layers` layers from `layer` on.
+void move_args(const llama_ctx* c, const llama_kv* kv, int32_t layer, int32_t B, CacheMoveArgs* a) {
+  const llama_config& cf = c->cfg;
+  a->k = kv->k;
+  a->v = kv->v;
+  a->row_bytes = cf.head_dim * (kv->kv_dtype == LLAMA_KV_E4M3 ? 1 : elem_size(cf.dtype));
+  a->layer_rows = kv->page_size ? (size_t)kv->n_pages * cf.n_kv_heads * kv->page_size
+                                : (size_t)kv->batch_capacity * cf.n_kv_heads * kv->capacity;
+  a->layer = std::max(layer, 0);
+  a->layers = layer < 0 ? cf.n_layers : 1;
+  a->B = B;
+  a->n_kv = cf.n_kv_heads;
+  a->page_size = kv->page_size;
+  a->capacity = kv->capacity;
+  a->n_pages = kv->n_pages;
+  a->max_pages = kv->max_pages_per_seq;
+  a->page_table = kv->page_table;
+  a->limit = (int)std::min<int64_t>(
+      kv->page_size ? (int64_t)kv->max_pages_per_seq * kv->page_size : kv->capacity, 0x7fffffff);
+  a->status = c->status;
+  a->sm_count = c->sm_count;
+}
+// CTAs of a move at most: 32-byte slices of K and V rows
+bool move_fits(const CacheMoveArgs& a) {
+  return (int64_t)a.layers * a.B * a.n_kv < (1ll << 30) / (a.row_bytes / 32);
+}
+}  // namespace
+
+int llama_op_cache_commit(llama_ctx* c, const llama_kv* kv, int32_t layer, const int32_t* start_pos, int32_t B,
+                          const int32_t* path, int32_t path_ld, const int32_t* path_len) {
+  TRY(check_ctx(c));
+  if (!start_pos || !path || !path_len || B < 1 || path_ld < 1 || layer < LLAMA_ALL_LAYERS ||
+      layer >= c->cfg.n_layers)
+    return LLAMA_ERR_INVALID_ARG;
+  TRY(check_kv(c, kv, B));
+  TRY(check_device(c));
+  CacheMoveArgs a{};
+  move_args(c, kv, layer, B, &a);
+  a.list_ld = path_ld;
+  a.path = path;
+  a.start = start_pos;
+  a.count = path_len;
+  if (!move_fits(a)) return LLAMA_ERR_OUT_OF_RANGE;
+  Prof pf(c, LLAMA_KERNEL_ROPE_APPEND);
+  c->launches++;
+  return cuda_rc(launch_cache_move(a, c->stream));
+}
+
+int llama_op_cache_evict(llama_ctx* c, const llama_kv* kv, int32_t layer, const int32_t* lens, int32_t B,
+                         int32_t keep, int32_t first, int32_t recent, const float* weights, int64_t weights_ld,
+                         float* weights_out, int32_t* kept) {
+  TRY(check_ctx(c));
+  if (!lens || !weights || !weights_out || !kept || B < 1 || keep < 1 || first < 0 || recent < 0 ||
+      (int64_t)first + recent > keep || weights_ld < 1 || layer < LLAMA_ALL_LAYERS || layer >= c->cfg.n_layers)
+    return LLAMA_ERR_INVALID_ARG;
+  TRY(check_kv(c, kv, B));
+  TRY(check_device(c));
+  CacheMoveArgs a{};
+  move_args(c, kv, layer, B, &a);
+  a.limit = (int)std::min<int64_t>(a.limit, weights_ld);
+  a.list_ld = keep;
+  a.kept = kept;
+  a.lens = lens;
+  if (!move_fits(a)) return LLAMA_ERR_OUT_OF_RANGE;
+  EvictArgs e{};
+  e.weights = weights;
+  e.weights_out = weights_out;
+  e.kept = kept;
+  e.lens = lens;
+  e.ld = weights_ld;
+  e.layers = a.layers;
+  e.B = B;
+  e.n_kv = a.n_kv;
+  e.keep = keep;
+  e.first = first;
+  e.recent = recent;
+  e.limit = a.limit;
+  e.status = c->status;
+  Prof pf(c, LLAMA_KERNEL_ROPE_APPEND);
+  c->launches += 2;
+  TRY(cuda_rc(launch_evict_select(e, c->stream)));
+  return cuda_rc(launch_cache_move(a, c->stream));
 }
 
 int llama_op_argmax(llama_ctx* c, const float* logits, int32_t B, int32_t V, int32_t* ids) {

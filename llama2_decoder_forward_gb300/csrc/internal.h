@@ -239,6 +239,7 @@ struct RopeNormArgs {
   int n_rows, n_seq;
   const int32_t* cu_rows;    // [n_seq + 1], or null: row b is sequence b's
   const int32_t* start_pos;  // [n_seq]
+  const int32_t* positions;  // [n_rows] what rows rotate by, or null: their slot
   const float2* table;       // [n_pos][rotary / 2]
   int n_pos, rotary, half;
   const void* q_gain;        // T [d] or null
@@ -320,6 +321,34 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
 cudaError_t attn_simt_prepare();
 cudaError_t launch_docs_simt(const DocsArgs& a, cudaStream_t st);
 cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st);
+
+// ---- rows moved together in the cache (k_cache_move.cu)
+struct CacheMoveArgs {
+  void *k, *v;                 // whole caches
+  int row_bytes;               // of one slot's head (a multiple of 32)
+  size_t layer_rows;           // slots x heads of a layer
+  int layer, layers;           // first layer, how many
+  int B, n_kv, page_size, capacity, n_pages, max_pages, limit;
+  const int32_t* page_table;
+  uint32_t* status;
+  int sm_count;
+  int list_ld;
+  // commit: slot start[b] + path[b][i] to start[b] + i, i < count[b]
+  const int32_t *path = nullptr, *start = nullptr, *count = nullptr;
+  // evict: slot kept[layer][b][g][i] to i, where lens[b] is above list_ld
+  const int32_t *kept = nullptr, *lens = nullptr;
+};
+cudaError_t launch_cache_move(const CacheMoveArgs& a, cudaStream_t st);
+struct EvictArgs {
+  const float* weights;        // [layers][B][n_kv][ld]
+  float* weights_out;
+  int32_t* kept;               // [layers][B][n_kv][keep]
+  const int32_t* lens;         // [B]
+  int64_t ld;
+  int layers, B, n_kv, keep, first, recent, limit;
+  uint32_t* status;
+};
+cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
 
 // ---- token sampling (k_sample.cu)
 struct SampleCall {

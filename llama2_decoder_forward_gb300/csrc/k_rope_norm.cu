@@ -90,16 +90,17 @@ __global__ void __launch_bounds__(RN_THREADS) rope_norm_append_kernel(RopeNormAr
     load4(src + (size_t)head0 * d + e0, nx);
     load4(src + (size_t)head0 * d + e1, nx + 4);
   }
-  // the row's sequence and position
-  int b = r, pos;
+  // the row's sequence, its place in the cache, and the position that it rotates by
+  int b = r, place;
   if (a.cu_rows) {
     b = sequence_of(a.cu_rows, a.n_seq, r, threadIdx.x & 31);
     if (b < 0) return;  // a row of no sequence
-    pos = a.start_pos[b] + (r - a.cu_rows[b]);
+    place = a.start_pos[b] + (r - a.cu_rows[b]);
   } else {
-    pos = a.start_pos[b];
+    place = a.start_pos[b];
   }
-  const bool pos_ok = pos >= 0 && (a.rotary == 0 || pos < a.n_pos);
+  const int pos = a.positions ? a.positions[r] : place;
+  const bool pos_ok = place >= 0 && (a.rotary == 0 || (pos >= 0 && pos < a.n_pos));
   if (!pos_ok && chunk0 == 0 && threadIdx.x == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
   // its cache slot, of K/V head 0 (the heads lie slot_step slots apart); -1: not cached
   long long slot0 = -1;
@@ -107,16 +108,16 @@ __global__ void __launch_bounds__(RN_THREADS) rope_norm_append_kernel(RopeNormAr
   if (pos_ok && head_end > a.n_q) {
     uint32_t bad = 0;
     if (a.page_size == 0) {
-      if (pos < a.capacity && b < a.batch_cap)
-        slot0 = ((long long)a.layer * a.batch_cap + b) * a.n_kv * a.capacity + pos;
+      if (place < a.capacity && b < a.batch_cap)
+        slot0 = ((long long)a.layer * a.batch_cap + b) * a.n_kv * a.capacity + place;
       else
         bad = LLAMA_FLAG_POS_RANGE;
     } else {
-      const int pi = pos / a.page_size;
+      const int pi = place / a.page_size;
       if (pi < a.max_pages) {
         const int page = a.page_table[(size_t)b * a.max_pages + pi];
         if (page >= 0 && page < a.n_pages)
-          slot0 = ((long long)a.layer * a.n_pages + page) * a.n_kv * a.page_size + (pos - pi * a.page_size);
+          slot0 = ((long long)a.layer * a.n_pages + page) * a.n_kv * a.page_size + (place - pi * a.page_size);
         else
           bad = LLAMA_FLAG_PAGE_RANGE;
       } else {

@@ -1,0 +1,325 @@
+"""The operators on caches whose slots are not one token after the other against
+plain fp64 forms: rows moved after a tree is accepted, eviction by accumulated
+weight, rows appended with positions of their own.
+
+Moves and selections are exact. Appended rows: as in the tests of
+llama_op_rope_norm_append, one rounding (2^-8 relative in bf16, 2^-24 in fp32) of
+an fp32 value whose own error is some 2^-24 of the head's largest value.
+"""
+import math
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from _common import f64, need_gpu, to_dev
+from llama2_decoder_forward_gb300 import binding, synth
+from oracle import attention_forms as A
+from oracle import cache_ops as C
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _model(nq, nkv, d=128, dtype="bf16", max_batch=8, max_seq=4096, n_layers=1):
+    need_gpu()
+    shape = synth.Shape(n_layers, 256, nq, nkv, d, 256, 256, dtype=dtype)
+    w = {"layers": [synth.layer_weights(shape, 3, l) for l in range(n_layers)]}
+    return binding.Model(shape, to_dev(w), max_batch=max_batch, max_tokens=0, max_seq=max_seq,
+                         has_embed_head=False), shape
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _within(got, ref, bound, what):
+    got = f64(got)
+    err = np.abs(got - ref)
+    bad = ~(err <= bound)
+    if bad.any():
+        i = np.unravel_index(np.argmax(np.where(np.isfinite(err), err - bound, np.inf)), err.shape)
+        raise AssertionError("%s: %d of %d out of tolerance; worst at %s: got %r ref %r bound %r"
+                             % (what, bad.sum(), bad.size, i, got[i], ref[i], np.broadcast_to(bound, err.shape)[i]))
+
+
+def _cache(shape, B, slots, page, e4m3=False, seed=1, spare=3):
+    """A cache for B sequences of `slots` slots, filled with numbers that tell the slots apart, and its page table."""
+    kw = dict(e4m3=(0.5, 0.25)) if e4m3 else {}
+    if page:
+        n = -(-slots // page)
+        order = torch.randperm(B * n + spare, generator=_gen(seed))[:B * n].view(B, n).to(torch.int32)
+        kv = binding.KVCache(shape, n_pages=B * n + spare, page_size=page, page_table=order.cuda(), **kw)
+    else:
+        kv = binding.KVCache(shape, batch=B + 1, capacity=slots + 5, **kw)
+    for i, t in enumerate((kv.k, kv.v)):
+        x = torch.randint(0, 1 << 30, t.shape, generator=_gen(seed + 7 + i), dtype=torch.int32)
+        # bit patterns: a move copies them, whatever they stand for
+        if e4m3:
+            t.copy_(x.to(torch.uint8))
+        elif t.dtype == torch.bfloat16:
+            t.view(torch.int16).copy_(x.to(torch.int16))
+        else:
+            t.view(torch.int32).copy_(x)
+    return kv
+
+
+def _bits(t):
+    return t.view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()]).cpu().numpy()
+
+
+def _at(kv, b, slot):
+    """Index of a slot's heads in one layer's bits."""
+    if kv.page_size == 0:
+        return (b, slice(None), slot)
+    return (int(kv.page_table[b, slot // kv.page_size]), slice(None), slot % kv.page_size)
+
+
+TYPES = [("bf16", False, 128), ("bf16", True, 128), ("f32", False, 64), ("f32", False, 40), ("f32", False, 256),
+         ("f32", False, 8)]
+
+
+# --------------------------------------------------------------------------- commit
+def _commit_case(dtype, e4m3, d, page, starts, paths, nkv=3, layers=3, layer=None, width=None, pad=-7, seed=3):
+    m, shape = _model(nkv, nkv, d, dtype, max_batch=len(starts), n_layers=layers)
+    kv = _cache(shape, len(starts), 12 + max(s + max(p, default=0) for s, p in zip(starts, paths)), page, e4m3, seed)
+    want = [_bits(t).copy() for t in (kv.k, kv.v)]
+    for w in want:
+        old = w.copy()
+        for b, (s, p) in enumerate(zip(starts, paths)):
+            for i, x in enumerate(p):
+                for l in range(layers) if layer is None else [layer]:
+                    w[l][_at(kv, b, s + i)] = old[l][_at(kv, b, s + x)]
+    width = width or max(1, max(map(len, paths)))
+    path = [p + [pad] * (width - len(p)) for p in paths]
+    m.op_cache_commit(kv, _i32(starts), _i32(path), _i32([len(p) for p in paths]), layer=layer)
+    m.sync()
+    for t, w in zip((kv.k, kv.v), want):
+        assert np.array_equal(_bits(t), w)
+
+
+@pytest.mark.parametrize("dtype,e4m3,d", TYPES)
+@pytest.mark.parametrize("page", [0, 16, 48])
+def test_commit(dtype, e4m3, d, page):
+    _commit_case(dtype, e4m3, d, page, [0, 30, 17, 5], [[0, 1, 2], [0, 3, 4, 11, 25], [], [7]])
+
+
+@pytest.mark.parametrize("n", [1, 2, 31, 33, 64, 130, 700])
+def test_commit_lengths(n):
+    r = np.random.RandomState(n)
+    _commit_case("bf16", False, 128, 16, [3, 40], [sorted(r.choice(2 * n, n, replace=False).tolist()), list(range(n))])
+
+
+def test_commit_one_layer():
+    _commit_case("bf16", False, 128, 16, [9, 0], [[0, 2], [1, 3, 4]], layer=1)
+
+
+def test_commit_long_paths_of_wide_rows():
+    r = np.random.RandomState(1)
+    _commit_case("f32", False, 256, 16, [0], [sorted(r.choice(900, 500, replace=False).tolist())], nkv=1, layers=1)
+
+
+def test_commit_bad_paths_are_flagged_and_skipped():
+    m, shape = _model(2, 2, max_batch=6)
+    kv = _cache(shape, 6, 64, 16, spare=0)
+    kv.page_table[5, 1] = 99
+    starts = [8, 60, -1, 0, 0, 14]
+    paths = [[2, 1, 4], [1, 70, 71], [1, 2, 3], [0, 1, 2], [1, 2, 3], [1, 2, 3]]
+    # 0: the 1 does not ascend, the 4 does again; 1 leaves the cache; 2 starts before it;
+    # 3 and 4 have lengths out of range (4's is cut); 5 reaches a page that is not there
+    want = [_bits(t).copy() for t in (kv.k, kv.v)]
+    for w in want:
+        old = w.copy()
+        w[0][_at(kv, 0, 8)], w[0][_at(kv, 0, 10)] = old[0][_at(kv, 0, 10)], old[0][_at(kv, 0, 12)]
+        w[0][_at(kv, 1, 60)] = old[0][_at(kv, 1, 61)]
+        w[0][_at(kv, 4, 0)], w[0][_at(kv, 4, 1)], w[0][_at(kv, 4, 2)] = (old[0][_at(kv, 4, i)] for i in (1, 2, 3))
+        w[0][_at(kv, 5, 14)] = old[0][_at(kv, 5, 15)]  # the others lie on page 99
+    m.op_cache_commit(kv, _i32(starts), _i32(paths), _i32([3, 3, 3, -2, 9, 3]))
+    rc, flags = m.sync_status()
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE | binding.FLAG_PAGE_RANGE
+    for t, w in zip((kv.k, kv.v), want):
+        assert np.array_equal(_bits(t), w)
+
+
+# --------------------------------------------------------------------------- evict
+def _evict_case(dtype, e4m3, d, page, lens, keep, first, recent, nkv=2, layers=2, layer=None, weights=None, ld=None,
+                alias=False, seed=5):
+    B, top = len(lens), max(max(lens), 1)
+    m, shape = _model(nkv, nkv, d, dtype, max_batch=B, n_layers=layers)
+    kv = _cache(shape, B, top, page, e4m3, seed)
+    ld = ld or top
+    n_l = layers if layer is None else 1
+    if weights is None:
+        weights = torch.rand(n_l, B, nkv, ld, generator=_gen(seed)).log().neg()
+    w0 = weights.numpy().copy()
+    want = [_bits(t).copy() for t in (kv.k, kv.v)]
+    old = [w.copy() for w in want]
+    kept = np.full((n_l, B, nkv, keep), -1, np.int32)
+    wout = np.zeros_like(w0)
+    for l in range(n_l):
+        for b, n in enumerate(lens):
+            for g in range(nkv):
+                k = C.evict(w0[l, b, g, :n], keep, first, recent)
+                kept[l, b, g, :len(k)] = k
+                wout[l, b, g, :len(k)] = w0[l, b, g, k]
+                for w, o in zip(want, old):
+                    for i, x in enumerate(k):
+                        li = l if layer is None else layer
+                        to, fro = _at(kv, b, i), _at(kv, b, x)
+                        w[li][to[0], g, to[2]] = o[li][fro[0], g, fro[2]]
+    wd = weights.cuda()
+    kd = torch.full(kept.shape, 77, dtype=torch.int32, device="cuda")
+    od = wd if alias else torch.full_like(wd, 9.0)
+    m.op_cache_evict(kv, _i32(lens), keep, wd, kd, layer=layer, first=first, recent=recent,
+                     weights_out=None if alias else od)
+    m.sync()
+    assert np.array_equal(kd.cpu().numpy(), kept)
+    assert np.array_equal(od.cpu().numpy(), wout, equal_nan=True)
+    if not alias:
+        assert np.array_equal(wd.cpu().numpy(), w0, equal_nan=True)
+    for t, w in zip((kv.k, kv.v), want):
+        assert np.array_equal(_bits(t), w)
+
+
+@pytest.mark.parametrize("dtype,e4m3,d", TYPES)
+@pytest.mark.parametrize("page", [0, 16, 48])
+def test_evict(dtype, e4m3, d, page):
+    _evict_case(dtype, e4m3, d, page, [90, 0, 41, 40, 1], 40, 3, 11)
+
+
+@pytest.mark.parametrize("alias", [False, True])
+@pytest.mark.parametrize("lens,keep,first,recent", [
+    ([1500, 700], 600, 4, 100), ([513, 512], 511, 0, 0), ([600], 1, 0, 0), ([600], 1, 1, 0), ([600], 1, 0, 1),
+    ([700, 699], 20, 20, 0), ([700], 300, 0, 300), ([700], 300, 100, 200), ([2], 1, 0, 0), ([1025], 1024, 1000, 23),
+    ([5000], 2100, 4, 64)])
+def test_evict_sizes(lens, keep, first, recent, alias):
+    _evict_case("bf16", False, 128, 16, lens, keep, first, recent, alias=alias, layers=1)
+
+
+def test_evict_one_layer():
+    _evict_case("bf16", False, 128, 16, [100, 50], 30, 2, 5, layers=3, layer=1)
+
+
+def test_evict_room_behind():
+    # weights with room for more slots than are filled: zeros there, nothing read
+    w = torch.full((1, 2, 2, 400), float("nan"))
+    w[..., :300] = torch.rand(1, 2, 2, 300, generator=_gen(8))
+    _evict_case("bf16", False, 128, 0, [300, 200], 128, 4, 32, layers=1, weights=w, ld=400)
+
+
+def test_evict_keep_above_everything():
+    _evict_case("bf16", False, 128, 16, [30, 12], 64, 4, 32, layers=1)
+
+
+@pytest.mark.parametrize("kind", ["zeros", "ties", "signs", "nan", "inf", "tiny", "steps"])
+def test_evict_weights(kind):
+    n = 900
+    w = torch.rand(1, 2, 2, n, generator=_gen(11))
+    if kind == "zeros":
+        w.zero_()
+    elif kind == "ties":
+        w = (w * 5).floor()
+    elif kind == "signs":
+        w = (w - 0.5) * 3
+        w[..., ::7] = -0.0
+        w[..., 3::7] = 0.0
+    elif kind == "nan":
+        w[..., ::2] = float("nan")  # more than are dropped: some NaN stay
+    elif kind == "inf":
+        w[..., ::5] = float("inf")
+        w[..., 1::5] = -float("inf")
+    elif kind == "tiny":
+        w = w * 1e-41  # below the normal numbers
+    else:
+        w = 1.0 + torch.randint(0, 40, w.shape, generator=_gen(12)) * 2.0 ** -23  # the last bits decide
+    _evict_case("bf16", False, 128, 16, [n, n - 1], 600, 3, 50, layers=1, weights=w.float())
+
+
+def test_evict_many_heads():
+    # more (layer, sequence, head) items than the slices of one would fill
+    _evict_case("bf16", False, 128, 16, [70, 64, 33, 71] * 5, 32, 1, 8, nkv=8, layers=4)
+
+
+def test_evict_bad_lengths_and_pages_are_flagged():
+    m, shape = _model(2, 2, max_batch=4)
+    kv = _cache(shape, 4, 64, 16)
+    kv.page_table[3, 2] = -5
+    w = torch.rand(1, 4, 2, 64, generator=_gen(13)).cuda()
+    old = [_bits(t).copy() for t in (kv.k, kv.v)]
+    table = kv.page_table.cpu()
+    kept = torch.zeros(1, 4, 2, 20, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(w)
+    m.op_cache_evict(kv, _i32([-3, 70, 20, 64]), 20, w, kept, weights_out=out)
+    rc, flags = m.sync_status()
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE | binding.FLAG_PAGE_RANGE
+    assert torch.all(kept[0, 0] == -1) and torch.all(out[0, 0] == 0)
+    wh = w.cpu().numpy()
+    for b, n in ((1, 64), (2, 20), (3, 64)):  # 70 is cut to the cache's 64 slots
+        for g in range(2):
+            k = C.evict(wh[0, b, g, :n], 20, 0, 0)
+            assert kept[0, b, g].tolist() == k
+            for t, o in zip((kv.k, kv.v), old):
+                got = _bits(t)[0]
+                for i, x in enumerate(k):
+                    a, f = (int(table[b, s // 16]) for s in (i, x))
+                    from_bad = b == 3 and x // 16 == 2
+                    src = o[0][f, g, x % 16] if not from_bad else o[0][a, g, i % 16]
+                    assert np.array_equal(got[a, g, i % 16], src)
+
+
+# --------------------------------------------------------------------------- rows with positions of their own
+@pytest.mark.parametrize("dtype,d,rotary,half", [("bf16", 128, 128, True), ("bf16", 128, 64, False), ("f32", 64, 64, True)])
+@pytest.mark.parametrize("token", [False, True])
+def test_append_positions(dtype, d, rotary, half, token):
+    nq, nkv, lens, starts = 4, 2, ([1, 1, 1] if token else [5, 0, 3]), [30, 4, 0]
+    m, shape = _model(nq, nkv, d, dtype)
+    n, dt = sum(lens), shape.torch_dtype
+    pos = torch.randint(0, 90, (n,), generator=_gen(2)).tolist()
+    x = torch.randn(n, shape.qkv_rows, generator=_gen(4))
+    table = A.rotation_table(90, rotary).astype(np.float32)
+    kv = binding.KVCache(shape, batch=3, capacity=40)
+    q = torch.empty(n, nq * d, dtype=dt, device="cuda")
+    cu = np.concatenate(([0], np.cumsum(lens))).tolist()
+    rope = binding.Rope(torch.from_numpy(table).cuda(), binding.ROPE_HALF if half else binding.ROPE_ADJACENT)
+    m.op_rope_norm_append(x.cuda(), _i32(starts), 0, kv, q, rope=rope, cu_rows=None if token else _i32(cu),
+                          positions=_i32(pos))
+    m.sync()
+    xf, (K, V) = f64(x).reshape(n, nq + 2 * nkv, d), (f64(t)[0].copy() for t in (kv.k, kv.v))
+    eps = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+
+    def close(got, ref, what):
+        _within(got, ref, eps * np.abs(ref) + (2.0 ** -18 if dtype == "bf16" else 2.0 ** -19) * np.abs(ref).max(), what)
+
+    for b in range(3):
+        for i in range(lens[b]):
+            r, s = cu[b] + i, starts[b] + i
+            cs = table[pos[r]].astype(np.float64)
+            close(q[r].view(nq, d), A.rotate(xf[r, :nq], cs, half), "q")
+            close(K[b, :, s], A.rotate(xf[r, nq:nq + nkv], cs, half), "k")
+            close(V[b, :, s], xf[r, nq + nkv:], "v")
+            K[b, :, s] = V[b, :, s] = 0
+    assert not K.any() and not V.any()
+
+
+def test_append_positions_out_of_range():
+    m, shape = _model(4, 2)
+    x = torch.randn(4, shape.qkv_rows, generator=_gen(6)).cuda()
+    kv = binding.KVCache(shape, batch=4, capacity=16)
+    q = torch.full((4, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    rope = binding.Rope(binding.rope_table(10, 128))
+    # past the table; before it; a slot past the cache with a good position; all good
+    m.op_rope_norm_append(x, _i32([1, 2, 16, 3]), 0, kv, q, rope=rope, positions=_i32([10, -1, 9, 0]))
+    rc, flags = m.sync_status()
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE
+    assert torch.all(q[:2] == 0) and torch.all(q[2:].abs().sum(-1) > 0)
+    assert (kv.k != 0).any(-1).nonzero().tolist() == [[0, 3, 0, 3], [0, 3, 1, 3]]
+    # without rotation positions do not count
+    m.op_rope_norm_append(x, _i32([1, 2, 5, 3]), 0, kv, q, positions=_i32([-1, 1 << 30, 0, 0]))
+    m.sync()
+    assert torch.all(q.abs().sum(-1) > 0)
