@@ -40,7 +40,9 @@ __device__ __forceinline__ int move_row(const CacheMoveArgs& a, int b, int g, in
 __global__ void cache_move_kernel(CacheMoveArgs a, int slices, int rows_chunk) {
   grid_dep_wait();
   grid_dep_launch();
-  extern __shared__ int2 moves[];  // [2][rows_chunk] (from, to) rows of a chunk; from < 0: no move
+  // (from, to) rows of a chunk, from < 0: no move; [3][rows_chunk], because beside a
+  // thread that still stores a chunk another one may look up the chunk after the next
+  extern __shared__ int2 moves[];
   const int T = blockDim.x;
   long long item = blockIdx.x;
   const int slice = (int)(item % slices);
@@ -101,16 +103,17 @@ __global__ void cache_move_kernel(CacheMoveArgs a, int slices, int rows_chunk) {
   const int ld = a.row_bytes / 16;
   look_up(first, moves);
   __syncthreads();
-  int half = 0;
-  for (int i0 = first; i0 < n; i0 += rows_chunk, half ^= 1) {
-    const int2* mv = moves + half * rows_chunk;
+  int part = 0;
+  for (int i0 = first; i0 < n; i0 += rows_chunk) {
+    const int2* mv = moves + part * rows_chunk;
+    part = part == 2 ? 0 : part + 1;
     uint4 x[UNITS];
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
       const int u = threadIdx.x + k * T, r = u / upr;
       if (r < rows_chunk && mv[r].x >= 0) x[k] = cache[(size_t)mv[r].x * ld + (u - r * upr)];
     }
-    if (i0 + rows_chunk < n) look_up(i0 + rows_chunk, moves + (half ^ 1) * rows_chunk);
+    if (i0 + rows_chunk < n) look_up(i0 + rows_chunk, moves + part * rows_chunk);
     __syncthreads();  // the chunk is read: its slots may be written
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
@@ -245,7 +248,7 @@ cudaError_t launch_cache_move(const CacheMoveArgs& a, cudaStream_t st) {
     while (upr / slices % 2 == 0 && upr / slices > 2 && items * slices < 4 * a.sm_count) slices *= 2;
   }
   const int rows = std::min(MAX_ROWS, std::max(1, T * UNITS / (upr / slices)));
-  return launch_k(cache_move_kernel, dim3((unsigned)(items * slices)), dim3(T), 2 * rows * sizeof(int2), st, 0, a,
+  return launch_k(cache_move_kernel, dim3((unsigned)(items * slices)), dim3(T), 3 * rows * sizeof(int2), st, 0, a,
                   slices, rows);
 }
 

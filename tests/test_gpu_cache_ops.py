@@ -246,6 +246,35 @@ def test_evict_many_heads():
     _evict_case("bf16", False, 128, 16, [70, 64, 33, 71] * 5, 32, 1, 8, nkv=8, layers=4)
 
 
+@pytest.mark.parametrize("layers,nkv,page,n,keep,dtype,d", [
+    (8, 32, 16, 4000, 1500, "bf16", 128), (32, 32, 0, 2000, 1900, "bf16", 128), (1, 1, 16, 20000, 15000, "bf16", 128),
+    (4, 8, 64, 3000, 2000, "f32", 256), (2, 3, 0, 6000, 5999, "f32", 40)])
+def test_evict_long_lists(layers, nkv, page, n, keep, dtype, d):
+    # chunks follow one another in every CTA, and none may pass another one's rows by
+    m, shape = _model(nkv, nkv, d, dtype, max_batch=1, max_seq=8, n_layers=layers)
+    kv = _cache(shape, 1, n, page)
+    for i in range(3):
+        w = torch.rand(layers, 1, nkv, n, generator=_gen(i)).cuda()
+        order = torch.sort(w, dim=-1, descending=True, stable=True)[1][..., :keep]
+        kept = torch.sort(order, dim=-1)[0]
+        got = torch.empty(layers, 1, nkv, keep, dtype=torch.int32, device="cuda")
+
+        def rows(t, slot):  # [layers, nkv, slots, d]
+            l, g = torch.arange(layers, device="cuda")[:, None, None], torch.arange(nkv, device="cuda")[None, :, None]
+            if page:
+                return t[l, kv.page_table[0].long()[slot // page], g, slot % page]
+            return t[l, 0, g, slot]
+        ints = {2: torch.int16, 4: torch.int32}[kv.k.element_size()]
+        views = [t.view(ints) for t in (kv.k, kv.v)]
+        want = [rows(t, kept[:, 0]) for t in views]
+        m.op_cache_evict(kv, _i32([n]), keep, w, got, weights_out=torch.empty_like(w))
+        m.sync()
+        assert torch.equal(got.long(), kept)
+        at = torch.arange(keep, device="cuda").expand(layers, nkv, keep)
+        for t, x in zip(views, want):
+            assert torch.equal(rows(t, at), x)
+
+
 def test_evict_bad_lengths_and_pages_are_flagged():
     m, shape = _model(2, 2, max_batch=4)
     kv = _cache(shape, 4, 64, 16)
