@@ -608,6 +608,23 @@ int llama_op_rope_norm_append_at(llama_ctx* ctx, const void* qkv, int32_t qkv_dt
 int llama_op_cache_commit(llama_ctx* ctx, const llama_kv* kv, int32_t layer, const int32_t* start_pos,
                           int32_t B, const int32_t* path, int32_t path_ld, const int32_t* path_len);
 
+/* Decode attention that adds up how much every key weighs: computes
+ * llama_op_attention_decode_shared without a shared prefix (same arguments, types
+ * and flags) and, for each key j <= positions[b] and K/V head g,
+ *   weights[b][g][j] += the softmax weights of the group's query heads on key j,
+ * summed in the order of the heads.
+ *   weights : DEVICE fp32 [B][n_kv][weights_ld]; keys from positions[b] + 1 on are
+ *             left as they are
+ *   scratch : DEVICE, 16-byte aligned, room for fp32 [B][n_q][weights_ld]; holds anything
+ *             before and after, one will do for all layers
+ * A position of weights_ld or more counts as one past the cache (flagged, the keys in
+ * range are attended and weighed). A sequence without keys changes no weight. A NaN score
+ * makes the weights of all keys of its K/V head NaN. Up to 4096 query heads per K/V head.
+ * Two launches. */
+int llama_op_attention_decode_weights(llama_ctx* ctx, const void* q, const int32_t* positions, int32_t B,
+                                      int32_t layer, const llama_kv* kv, const llama_scores* scores,
+                                      float* weights, int64_t weights_ld, void* scratch, void* out);
+
 /* Evicts from every sequence with more than `keep` filled slots: of its slots 0 ..
  * lens[b]-1 (DEVICE int32 [B]) the `first` first, the `recent` last and, of those
  * between, the keep - first - recent of largest weight stay (equal weights: the lower slot; NaN

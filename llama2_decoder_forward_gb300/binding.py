@@ -149,6 +149,9 @@ _SIGS = {
                                                ctypes.POINTER(_Rope), c_void_p, c_void_p,
                                                ctypes.c_float, c_int32, ctypes.POINTER(KV), c_void_p,
                                                c_void_p, c_void_p]),
+    "llama_op_attention_decode_weights": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                                    ctypes.POINTER(KV), ctypes.POINTER(_Scores),
+                                                    c_void_p, ctypes.c_int64, c_void_p, c_void_p]),
     "llama_op_cache_commit": (c_int32, [c_void_p, ctypes.POINTER(KV), c_int32, c_void_p, c_int32,
                                         c_void_p, c_int32, c_void_p]),
     "llama_op_cache_evict": (c_int32, [c_void_p, ctypes.POINTER(KV), c_int32, c_void_p, c_int32, c_int32,
@@ -448,7 +451,7 @@ class Model:
         import torch
         l = lib()
         self._append, self._docs = l.llama_op_rope_norm_append, l.llama_op_attention_docs
-        self._append_at = l.llama_op_rope_norm_append_at
+        self._append_at, self._weights = l.llama_op_rope_norm_append_at, l.llama_op_attention_decode_weights
         self._shared = l.llama_op_attention_decode_shared
         self._dt, self._qkv_rows = shape.torch_dtype, shape.qkv_rows
         self._i32, self._f32 = torch.int32, torch.float32
@@ -646,6 +649,24 @@ class Model:
             _need("out", out, dt, qn, dev))
         if rc:
             raise LlamaError(rc, "llama_op_attention_decode_shared")
+
+    def op_attention_decode_weights(self, q, positions, layer, kv: KVCache, out, weights, scratch, *,
+                                    scores=None):
+        """Decode attention that adds every key's softmax weight, summed over the query heads
+        of its K/V head, to weights fp32 [B, n_kv, ld] (llama_op_attention_decode_weights).
+        scratch: fp32 [B, n_q, ld] or more, its contents free."""
+        s, dt, f32, dev = self.shape, self._dt, self._f32, self._dev
+        B, ld = positions.numel(), weights.shape[-1]
+        qn = B * s.n_q_heads * s.head_dim
+        if scratch.numel() < B * s.n_q_heads * ld:
+            raise ValueError("scratch: want %d values, got %d" % (B * s.n_q_heads * ld, scratch.numel()))
+        rc = self._weights(
+            self.ctx, _need("q", q, dt, qn, dev), _need("positions", positions, self._i32, B, dev), B, layer,
+            kv._now(s, dt, B, dev), None if scores is None else scores._now(f32, s.n_q_heads, dev),
+            _need("weights", weights, f32, B * s.n_kv_heads * ld, dev), ld,
+            _need("scratch", scratch, f32, scratch.numel(), dev), _need("out", out, dt, qn, dev))
+        if rc:
+            raise LlamaError(rc, "llama_op_attention_decode_weights")
 
     def op_cache_commit(self, kv: KVCache, start_pos, path, path_len, *, layer=None):
         """Moves the accepted rows of a drafted tree together (llama_op_cache_commit): path

@@ -142,10 +142,11 @@ Layout make_layout(const llama_config* c, int sm_count) {
   L.apart = take(std::max<size_t>(L.apart_bytes, 16));
   // fused RMSNorm: per-(128-feature tile, row) sums of squares of the residual stream
   L.ssq = take((H + 127) / 128 * (size_t)R * 4);
-  // partial results of decode attention over a shared prefix (bf16)
+  // partial results of decode attention over a shared prefix (bf16); rows' maxima and sums
+  // of decode attention with key weights (fp32)
   L.spart = take(c->dtype == LLAMA_BF16 ? shared_partial_bytes(c->max_batch, (int)nq, (int)nkv,
                                                                c->max_seq, sm_count)
-                                        : 16);
+                                        : (size_t)c->max_batch * nq * 8);
   L.total = off;
   return L;
 }
@@ -1384,75 +1385,121 @@ int llama_op_attention_docs(llama_ctx* c, const void* q, const void* k, const vo
                                         : launch_docs_simt(a, c->stream));
 }
 
+namespace {
+// Decode attention's arguments from a cache and its checks, but for the prefix.
+int decode_args(llama_ctx* c, const void* q, const int32_t* positions, int32_t B, int32_t layer,
+                const llama_kv* kv, const llama_scores* scores, void* out, SharedArgs* a) {
+  const llama_config& cf = c->cfg;
+  if (!q || !positions || !out || B < 1 || layer < 0 || layer >= cf.n_layers) return LLAMA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return LLAMA_ERR_INVALID_ARG;
+  if (B > cf.max_batch || B > 65535) return LLAMA_ERR_OUT_OF_RANGE;
+  TRY(check_kv(c, kv, B));
+  if (kv->kv_dtype != LLAMA_KV_MODEL) return LLAMA_ERR_UNSUPPORTED;
+  TRY(score_args(c, scores, &a->sc));
+  TRY(check_device(c));
+  const int64_t slots = kv->page_size ? (int64_t)kv->max_pages_per_seq * kv->page_size : kv->capacity;
+  a->q = q;
+  a->out = out;
+  a->positions = positions;
+  a->k_cache = kv->k;
+  a->v_cache = kv->v;
+  a->page_table = kv->page_table;
+  a->B = B;
+  a->n_q = cf.n_q_heads;
+  a->n_kv = cf.n_kv_heads;
+  a->head_dim = cf.head_dim;
+  a->layer = layer;
+  a->page_size = kv->page_size;
+  a->capacity = kv->capacity;
+  a->batch_cap = kv->batch_capacity;
+  a->n_pages = kv->n_pages;
+  a->max_pages = kv->max_pages_per_seq;
+  a->key_limit = (int)std::min<int64_t>(slots, cf.max_seq);
+  a->status = c->status;
+  a->sm_count = c->sm_count;
+  return LLAMA_OK;
+}
+// The cache's views of the tensor-core forms, and q as boxes of G heads and rows_box rows.
+int decode_maps(llama_ctx* c, const llama_kv* kv, int64_t q_rows, int rows_box, SharedArgs* a) {
+  const llama_config& cf = c->cfg;
+  trim_maps(c);
+  const uint64_t d = cf.head_dim, nkv = cf.n_kv_heads;
+  const uint64_t rows = kv->page_size ? (uint64_t)kv->n_pages * nkv * kv->page_size
+                                      : (uint64_t)kv->batch_capacity * nkv * kv->capacity;
+  a->box_rows = attn_decode_box_rows(kv->page_size);
+  a->map_q = map3d(c, a->q, d, cf.n_q_heads, q_rows, cf.n_q_heads / cf.n_kv_heads, rows_box);
+  a->map_k = map3d(c, kv->k, d, rows, cf.n_layers, a->box_rows, 1);
+  a->map_v = map3d(c, kv->v, d, rows, cf.n_layers, a->box_rows, 1);
+  a->map_k16 = map3d(c, kv->k, d, rows, cf.n_layers, 16, 1);
+  a->map_v16 = map3d(c, kv->v, d, rows, cf.n_layers, 16, 1);
+  return a->map_q && a->map_k && a->map_v && a->map_k16 && a->map_v16 ? LLAMA_OK : LLAMA_ERR_CUDA;
+}
+}  // namespace
+
 int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t* positions,
                                      int32_t B, int32_t layer, const llama_kv* kv,
                                      int32_t shared_len, int32_t shared_seq,
                                      const llama_scores* scores, void* out) {
   TRY(check_ctx(c));
   const llama_config& cf = c->cfg;
-  if (!q || !positions || !out || B < 1 || layer < 0 || layer >= cf.n_layers || shared_len < 0 ||
-      shared_seq < 0)
-    return LLAMA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(out)) return LLAMA_ERR_INVALID_ARG;
-  if (B > cf.max_batch || B > 65535) return LLAMA_ERR_OUT_OF_RANGE;
-  TRY(check_kv(c, kv, B));
-  if (kv->kv_dtype != LLAMA_KV_MODEL) return LLAMA_ERR_UNSUPPORTED;
-  if (shared_seq >= (kv->page_size ? B : kv->batch_capacity)) return LLAMA_ERR_INVALID_ARG;
-  const int64_t slots = kv->page_size ? (int64_t)kv->max_pages_per_seq * kv->page_size : kv->capacity;
-  const int limit = (int)std::min<int64_t>(slots, cf.max_seq);
-  if (shared_len > limit) return LLAMA_ERR_OUT_OF_RANGE;
+  if (shared_len < 0 || shared_seq < 0) return LLAMA_ERR_INVALID_ARG;
   SharedArgs a{};
-  TRY(score_args(c, scores, &a.sc));
-  TRY(check_device(c));
-  a.q = q;
-  a.out = out;
-  a.positions = positions;
-  a.k_cache = kv->k;
-  a.v_cache = kv->v;
-  a.page_table = kv->page_table;
-  a.B = B;
-  a.n_q = cf.n_q_heads;
-  a.n_kv = cf.n_kv_heads;
-  a.head_dim = cf.head_dim;
-  a.layer = layer;
-  a.page_size = kv->page_size;
-  a.capacity = kv->capacity;
-  a.batch_cap = kv->batch_capacity;
-  a.n_pages = kv->n_pages;
-  a.max_pages = kv->max_pages_per_seq;
-  a.key_limit = limit;
+  TRY(decode_args(c, q, positions, B, layer, kv, scores, out, &a));
+  if (shared_seq >= (kv->page_size ? B : kv->batch_capacity)) return LLAMA_ERR_INVALID_ARG;
+  if (shared_len > a.key_limit) return LLAMA_ERR_OUT_OF_RANGE;
   // a batch of one that is its own prefix has nothing to share
   a.shared_len = B == 1 && shared_seq == 0 ? 0 : shared_len;
   a.shared_seq = shared_seq;
-  a.status = c->status;
-  a.sm_count = c->sm_count;
   if (cf.dtype != LLAMA_BF16) {
     Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
     c->launches++;
     return cuda_rc(launch_shared_simt(a, c->stream));
   }
   const SharedPlan plan =
-      shared_plan(B, cf.n_q_heads, cf.n_kv_heads, limit, a.shared_len, c->sm_count);
+      shared_plan(B, cf.n_q_heads, cf.n_kv_heads, a.key_limit, a.shared_len, c->sm_count);
   if (plan.partials * (128 + 2) * sizeof(float) + 16 >
       shared_partial_bytes(cf.max_batch, cf.n_q_heads, cf.n_kv_heads, cf.max_seq, c->sm_count))
     return LLAMA_ERR_WORKSPACE;
-  trim_maps(c);
-  const uint64_t d = cf.head_dim, nkv = cf.n_kv_heads;
-  const uint64_t rows = kv->page_size ? (uint64_t)kv->n_pages * nkv * kv->page_size
-                                      : (uint64_t)kv->batch_capacity * nkv * kv->capacity;
-  const uint32_t G = cf.n_q_heads / cf.n_kv_heads;
-  a.box_rows = attn_decode_box_rows(kv->page_size);
-  a.map_q = map3d(c, q, d, cf.n_q_heads, B, G, plan.rows_seq);
-  a.map_k = map3d(c, kv->k, d, rows, cf.n_layers, a.box_rows, 1);
-  a.map_v = map3d(c, kv->v, d, rows, cf.n_layers, a.box_rows, 1);
-  a.map_k16 = map3d(c, kv->k, d, rows, cf.n_layers, 16, 1);
-  a.map_v16 = map3d(c, kv->v, d, rows, cf.n_layers, 16, 1);
-  if (!a.map_q || !a.map_k || !a.map_v || !a.map_k16 || !a.map_v16) return LLAMA_ERR_CUDA;
+  TRY(decode_maps(c, kv, B, plan.rows_seq, &a));
   a.partial = c->at<float>(c->L.spart);
   Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
   c->launches += (plan.prefix_parts ? 1 : 0) + (plan.join ? 2 : 1);
   if (plan.prefix_parts) TRY(cuda_rc(launch_shared_prefix(a, plan, c->stream)));
   return cuda_rc(launch_shared_own(a, plan, c->stream));
+}
+
+int llama_op_attention_decode_weights(llama_ctx* c, const void* q, const int32_t* positions, int32_t B,
+                                      int32_t layer, const llama_kv* kv, const llama_scores* scores,
+                                      float* weights, int64_t weights_ld, void* scratch, void* out) {
+  TRY(check_ctx(c));
+  const llama_config& cf = c->cfg;
+  if (!weights || !scratch || weights_ld < 1 || !aligned16(scratch) ||
+      (reinterpret_cast<uintptr_t>(weights) & 3u) != 0)
+    return LLAMA_ERR_INVALID_ARG;
+  if (cf.n_q_heads / cf.n_kv_heads > 4096) return LLAMA_ERR_UNSUPPORTED;
+  SharedArgs a{};
+  TRY(decode_args(c, q, positions, B, layer, kv, scores, out, &a));
+  a.key_limit = (int)std::min<int64_t>(a.key_limit, weights_ld);
+  WeightsArgs w{};
+  w.scores = reinterpret_cast<float*>(scratch);
+  w.weights = weights;
+  w.ld = weights_ld;
+  if (cf.dtype != LLAMA_BF16) {
+    w.stats = c->at<float>(c->L.spart);
+    Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
+    c->launches += 2;
+    TRY(cuda_rc(launch_shared_simt(a, c->stream, &w)));
+    return cuda_rc(launch_add_weights_f32(a, w, c->stream));
+  }
+  const SharedPlan plan = weights_plan(B, cf.n_q_heads, cf.n_kv_heads, a.key_limit, c->sm_count);
+  if (plan.partials * (128 + 2) * sizeof(float) + 16 >
+      shared_partial_bytes(cf.max_batch, cf.n_q_heads, cf.n_kv_heads, cf.max_seq, c->sm_count))
+    return LLAMA_ERR_WORKSPACE;
+  TRY(decode_maps(c, kv, B, plan.rows_seq, &a));
+  a.partial = c->at<float>(c->L.spart);
+  Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
+  c->launches += 2;
+  return cuda_rc(launch_decode_weights(a, plan, w, c->stream));
 }
 
 namespace {

@@ -317,10 +317,22 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
 // own keys of a decode batch and the merge with its prefix (k_attn_own.cu)
 cudaError_t attn_own_prepare();
 cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStream_t st);
+// Decode attention that adds up its keys' weights: the own keys of a batch without a
+// prefix, their scores kept, then the joining kernel.
+struct WeightsArgs {
+  float* scores;         // [B][n_kv][ld][G]
+  float* weights;        // [B][n_kv][ld]
+  int64_t ld;
+  float* stats;          // fp32 models: [B n_q][2], maximum and sum of a row
+};
+SharedPlan weights_plan(int B, int n_q, int n_kv, int key_limit, int sm_count);
+cudaError_t launch_decode_weights(const SharedArgs& a, const SharedPlan& s, const WeightsArgs& w, cudaStream_t st);
+cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cudaStream_t st);
 // fp32 on the CUDA cores, any head_dim (k_attn_simt.cu)
 cudaError_t attn_simt_prepare();
 cudaError_t launch_docs_simt(const DocsArgs& a, cudaStream_t st);
-cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st);
+// w: also its scores and every row's maximum and sum
+cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st, const WeightsArgs* w = nullptr);
 
 // ---- rows moved together in the cache (k_cache_move.cu)
 struct CacheMoveArgs {

@@ -79,6 +79,10 @@ struct OwnParams {
   size_t rows, own_room;       // B n_q; partials behind the prefix's
   float scale, cap;
   const float* slopes;
+  // key weights: every score (log2 units), [B][n_kv][ld][G], for the joining kernel
+  float* scores;
+  float* weights;              // [B][n_kv][ld]
+  int64_t ld;
 };
 
 __device__ __forceinline__ void consumers_bar() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
@@ -142,6 +146,7 @@ __device__ __forceinline__ void clean_v(uint8_t* v, int lead, int valid, int lan
 
 // Groups of up to 8 heads: keys on the MMA rows. Lane l tracks heads 2(l%4)
 // and 2(l%4) + 1. Leaves (max, sum, O) of this warp in shared memory.
+template <bool WEIGH>
 __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, uint64_t* full,
                                              uint64_t* empty, volatile uint32_t* stop, int b, int g,
                                              int kbeg, int kend, int pos, int warp, int lane) {
@@ -197,6 +202,8 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
         float x = score(sc, s0[i] + s1[i]);
         if (p.slopes) x = fmaf(-sl[i & 1], (float)(pos - k0 - key), x);
         sv[i] = key >= lead && key < valid ? x : -INFINITY;
+        if (WEIGH && key < valid && hc + (i & 1) < G)
+          p.scores[(((size_t)b * p.n_kv + g) * p.ld + k0 + key) * G + hc + (i & 1)] = x;
       }
       float corr[2];
 #pragma unroll
@@ -270,6 +277,7 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
 }
 
 // Groups of 9 to 16 heads: heads on the MMA rows (zero-padded to 16).
+template <bool WEIGH>
 __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem, uint64_t* full,
                                               uint64_t* empty, volatile uint32_t* stop, int b, int g,
                                               int kbeg, int kend, int pos, int warp, int lane) {
@@ -331,6 +339,8 @@ __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem,
           float x = score(sc, sv[nb][i]);
           if (p.slopes) x = fmaf(-sl[i >> 1], (float)(pos - k0 - key), x);
           sv[nb][i] = key >= lead && key < valid ? x : -INFINITY;
+          if (WEIGH && key < valid && r0 + 8 * (i >> 1) < G)
+            p.scores[(((size_t)b * p.n_kv + g) * p.ld + k0 + key) * G + r0 + 8 * (i >> 1)] = x;
           mx[i >> 1] = fmaxf(mx[i >> 1], sv[nb][i]);
         }
 #pragma unroll
@@ -487,7 +497,7 @@ __device__ __forceinline__ void store_row(bf16* dst, int lane, const RowSum& r) 
       make_uint2(pack_bf16(r.o.x * i, r.o.y * i), pack_bf16(r.o.z * i, r.o.w * i));
 }
 
-template <bool KEYS>
+template <bool KEYS, bool WEIGH>
 __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     attn_own_kernel(const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapV,
@@ -610,9 +620,9 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
       return;
     }
     if (KEYS)
-      consume_keys(p, smem, full, empty, stop, b, g, kbeg, kend, pos, warp, lane);
+      consume_keys<WEIGH>(p, smem, full, empty, stop, b, g, kbeg, kend, pos, warp, lane);
     else
-      consume_heads(p, smem, full, empty, stop, b, g, kbeg, kend, pos, warp, lane);
+      consume_heads<WEIGH>(p, smem, full, empty, stop, b, g, kbeg, kend, pos, warp, lane);
     consumers_bar();
     if (*stop && !p.cluster) return;
   } else if (warp == 4) {  // (a cluster's barriers do not count threads that left)
@@ -721,15 +731,71 @@ __global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int 
   store_row(p.out + (size_t)bh * HD, lane, x);
 }
 
+// Key weights: joins a row's splits, and adds to the weight of every key of a
+// (sequence, K/V head) what the group's heads gave it,
+//   weights[key] += sum over heads of 2^(score - max) / sum,
+// each key by one thread and its heads in order. NAT: scores in natural units,
+// one part per row, whose output is there already (fp32 models).
+constexpr int WEIGH_THREADS = 256;
+template <bool NAT>
+__global__ void __launch_bounds__(WEIGH_THREADS) attn_weights_kernel(OwnParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  extern __shared__ float2 stat[];  // maximum and reciprocal sum of the group's G heads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.G;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const int n = key_position(p.positions[b], p.key_limit) + 1;
+  int used = n > 0;  // splits that have keys
+  if (used && p.splits > 1) {
+    const int share = own_share(p, n);
+    used = (n + share - 1) / share;
+  }
+  if (!bc_ok(used <= p.splits && n <= p.ld, p.status)) return;
+  const size_t row0 = (size_t)b * p.n_q + (size_t)g * G;
+  float* w = p.weights + ((size_t)b * p.n_kv + g) * p.ld;
+  const float* sc = p.scores + ((size_t)b * p.n_kv + g) * p.ld * G;
+  for (int r = warp; r < G; r += WEIGH_THREADS / 32) {
+    const float2* ml = reinterpret_cast<const float2*>(p.own_ml) + (row0 + r) * p.splits;
+    float m = -INFINITY, l = 0.f;
+    for (int s = lane; s < used; s += 32) m = fmaxf(m, ml[s].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int s = lane; s < used; s += 32) {
+      const float2 x = ml[s];
+      if (x.x != -INFINITY) l = fmaf(x.y, NAT ? expf(x.x - m) : exp2f(x.x - m), l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) stat[r] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f || l != l ? 1.f / l : 0.f);
+    if (!NAT && r % gridDim.x == blockIdx.x) {  // the output rows are shared out over the chunks
+      Parts<8> own;
+      RowSum x;
+      own.load(p.own_o, p.own_ml, (row0 + r) * p.splits, p.splits, lane);
+      own.fold(used, lane, x);
+      store_row(p.out + (row0 + r) * HD, lane, x);
+    }
+  }
+  __syncthreads();
+  for (int i = blockIdx.x * WEIGH_THREADS + threadIdx.x; i < n; i += gridDim.x * WEIGH_THREADS) {
+    float sum = 0.f;
+    for (int r = 0; r < G; ++r) {
+      const float x = sc[(size_t)i * G + r] - stat[r].x;
+      sum = fmaf(NAT ? expf(x) : ex2(x), stat[r].y, sum);
+    }
+    w[i] += sum;
+  }
+}
+
 }  // namespace
 
 cudaError_t attn_own_prepare() {
-  cudaError_t e = cudaFuncSetAttribute(attn_own_kernel<true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)OWN_SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_own_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)OWN_SMEM);
-  return e;
+  const void* const all[] = {(const void*)attn_own_kernel<true, false>, (const void*)attn_own_kernel<false, false>,
+                             (const void*)attn_own_kernel<true, true>, (const void*)attn_own_kernel<false, true>};
+  for (const void* f : all) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)OWN_SMEM);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, int sm_count) {
@@ -779,7 +845,13 @@ size_t shared_partial_bytes(int max_batch, int n_q, int n_kv, int max_seq, int s
   return (prefix + own) * (HD + 2) * sizeof(float) + 16;
 }
 
-cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStream_t st) {
+// Chunks of a (sequence, K/V head)'s keys that the weights' kernel takes at a time:
+// four CTAs per SM, and a key per thread at least.
+static int weight_chunks(int keys, int pairs, int sm_count) {
+  return std::max(1, std::min((keys + WEIGH_THREADS - 1) / WEIGH_THREADS, 4 * sm_count / pairs));
+}
+
+static OwnParams own_params(const SharedArgs& a, const SharedPlan& s) {
   OwnParams p{};
   p.q = (const bf16*)a.q;
   p.out = (bf16*)a.out;
@@ -823,16 +895,65 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
   p.scale = a.sc.scale;
   p.cap = a.sc.cap;
   p.slopes = a.sc.slopes;
+  return p;
+}
+
+cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStream_t st) {
+  const OwnParams p = own_params(a, s);
+  const size_t rows = p.rows;
   const dim3 grid(s.own_splits, a.n_kv, a.B), block(OWN_THREADS);
   const dim3 cluster(s.cluster ? s.own_splits : 0, 1, 1);
   const cudaError_t e =
-      p.G <= 8 ? launch_kc(attn_own_kernel<true>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
+      p.G <= 8 ? launch_kc(attn_own_kernel<true, false>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
                            *a.map_v, *a.map_k16, *a.map_v16, p)
-               : launch_kc(attn_own_kernel<false>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
+               : launch_kc(attn_own_kernel<false, false>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
                            *a.map_v, *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess || !s.join) return e;
   return launch_k(attn_own_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 0, p,
                   (int)rows);
+}
+
+SharedPlan weights_plan(int B, int n_q, int n_kv, int key_limit, int sm_count) {
+  SharedPlan s = shared_plan(B, n_q, n_kv, key_limit, 0, sm_count);
+  s.cluster = 0;  // the weights need a row's maximum and sum over all splits first
+  s.join = 1;
+  s.partials = (size_t)B * n_q * s.own_splits;
+  return s;
+}
+
+cudaError_t launch_decode_weights(const SharedArgs& a, const SharedPlan& s, const WeightsArgs& w, cudaStream_t st) {
+  OwnParams p = own_params(a, s);
+  p.scores = w.scores;
+  p.weights = w.weights;
+  p.ld = w.ld;
+  const dim3 grid(s.own_splits, a.n_kv, a.B), block(OWN_THREADS);
+  const cudaError_t e =
+      p.G <= 8 ? launch_k(attn_own_kernel<true, true>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
+                          *a.map_k16, *a.map_v16, p)
+               : launch_k(attn_own_kernel<false, true>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
+                          *a.map_k16, *a.map_v16, p);
+  if (e != cudaSuccess) return e;
+  const int chunks = weight_chunks(a.key_limit, a.B * a.n_kv, a.sm_count);
+  return launch_k(attn_weights_kernel<false>, dim3(chunks, a.n_kv, a.B), dim3(WEIGH_THREADS),
+                  p.G * sizeof(float2), st, 0, p);
+}
+
+cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cudaStream_t st) {
+  OwnParams p{};
+  p.positions = a.positions;
+  p.status = a.status;
+  p.n_q = a.n_q;
+  p.n_kv = a.n_kv;
+  p.G = a.n_q / a.n_kv;
+  p.key_limit = a.key_limit;
+  p.splits = 1;
+  p.own_ml = w.stats;
+  p.scores = w.scores;
+  p.weights = w.weights;
+  p.ld = w.ld;
+  const int chunks = weight_chunks(a.key_limit, a.B * a.n_kv, a.sm_count);
+  return launch_k(attn_weights_kernel<true>, dim3(chunks, a.n_kv, a.B), dim3(WEIGH_THREADS),
+                  p.G * sizeof(float2), st, 0, p);
 }
 
 }  // namespace llgb

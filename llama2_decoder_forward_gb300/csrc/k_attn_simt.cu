@@ -55,6 +55,9 @@ struct SimtParams {
   int n_seq;
   int row_chunks;  // chunks of 16 heads per K/V head
   int splits;      // CTAs (a cluster) that share an item's key tiles
+  // key weights: the scores [n_seq][n_kv][ld][G] and every row's maximum and sum, or null
+  float *scores, *stats;
+  int64_t ld;
 };
 
 // Work item -> (document, tile of `rows` query rows, first row, row count), for a
@@ -257,6 +260,8 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
         if (p.sc.cap > 0.f) v = p.sc.cap * tanhf(v * icap);
         if (p.sc.slopes) v -= slope[i] * fabsf((float)(qi - key));
         const bool keep = key < n_keys && (!DOCS || key <= qi || key < pre);
+        if (!DOCS && p.scores && keep && r0 + i < rows)
+          p.scores[(((size_t)b * p.n_kv + g) * p.ld + key) * p.G + (h0 - g * p.G) + r0 + i] = v;
         s[i][j] = keep ? v : -INFINITY;
       }
       float mx = fmaxf(s[i][0], s[i][1]);
@@ -336,6 +341,7 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
           }
         }
       }
+      m[i] = M;
       l[i] = L;
     }
     cluster_sync_all();  // nobody leaves while its rows are read
@@ -348,6 +354,8 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
 #pragma unroll
     for (int x = 0; x < DL; ++x) w[x] = n_keys > 0 ? o[i][x] / l[i] : 0.f;
     store_dims<DL>(p.out + row_off(r), lane, d, w);
+    if (!DOCS && p.stats && lane == 0)
+      *reinterpret_cast<float2*>(p.stats + 2 * ((size_t)b * p.n_q + h0 + r)) = make_float2(merge_max(m[i], l[i]), l[i]);
   }
 }
 
@@ -412,8 +420,13 @@ cudaError_t launch_docs_simt(const DocsArgs& a, cudaStream_t st) {
   return run<4, true>(p, tiles * a.n_q, st);
 }
 
-cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st) {
+cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st, const WeightsArgs* w) {
   SimtParams p{};
+  if (w) {
+    p.scores = w->scores;
+    p.stats = w->stats;
+    p.ld = w->ld;
+  }
   p.q = (const float*)a.q;
   p.k = (const float*)a.k_cache;
   p.v = (const float*)a.v_cache;

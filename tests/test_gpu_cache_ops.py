@@ -352,3 +352,194 @@ def test_append_positions_out_of_range():
     m.op_rope_norm_append(x, _i32([1, 2, 5, 3]), 0, kv, q, positions=_i32([-1, 1 << 30, 0, 0]))
     m.sync()
     assert torch.all(q.abs().sum(-1) > 0)
+
+
+# --------------------------------------------------------------------------- key weights
+def _slopes(nq):
+    return torch.exp2(-8.0 * torch.arange(1, nq + 1).float() / nq)
+
+
+def _randn(shape, dtype, seed, std=1.0):
+    return (torch.randn(*shape, generator=_gen(seed)) * std).to(dtype)
+
+
+def _filled(shape, B, slots, page, dtype, seed, std=1.5, read=None):
+    """A random cache of layer 0 .. n_layers - 1; slots that `read` [B] does not cover hold NaN and infinities."""
+    L, nkv, d = shape.n_layers, shape.n_kv_heads, shape.head_dim
+    if page:
+        n = -(-slots // page)
+        pt = torch.randperm(B * n + 2, generator=_gen(seed))[:B * n].view(B, n).to(torch.int32)
+        size = (L, B * n + 2, nkv, page, d)
+    else:
+        pt, size = None, (L, B, nkv, slots, d)
+    k, v = _randn(size, dtype, seed + 1, std), _randn(size, dtype, seed + 2)
+    if read is not None:
+        used = torch.zeros(size[1], size[3], dtype=torch.bool)
+        for b, n in enumerate(read):
+            j = torch.arange(n)
+            if page:
+                used[pt[b].long()[j // page], j % page] = True
+            else:
+                used[b, :n] = True
+        k.transpose(2, 3)[:, ~used] = float("nan")
+        v.transpose(2, 3)[:, ~used] = torch.tensor(float("inf"))
+    kw = dict(n_pages=size[1], page_size=page, page_table=pt.cuda()) if page else dict(batch=B, capacity=slots)
+    kv = binding.KVCache(shape, k=k.cuda(), v=v.cuda(), **kw)
+    return kv, k, v, pt
+
+
+def _keys_of(t, pt, page, layer, b, n):
+    """Rows 0 .. n - 1 of a sequence in fp64, [n_kv, n, d]."""
+    j = torch.arange(n)
+    if page:
+        return f64(t[layer][pt[b].long()[j // page], :, j % page]).transpose(1, 0, 2)
+    return f64(t[layer, b, :, :n])
+
+
+def _score_error(q, K, scale, cap, bias_n):
+    """What a score may be off by: fp32 sums of d products, each addition of which may cut
+    (2^-23), and a few roundings of the scaled, capped and biased value."""
+    d = q.shape[-1]
+    S = float((np.abs(q) @ np.abs(K).T).max()) * scale
+    return (d + 8) * 2.0 ** -23 * S + 16 * 2.0 ** -24 * (min(S, cap) if cap else S) + 16 * 2.0 ** -24 * (cap + bias_n)
+
+
+def _out_bound(ref, mass, dtype, err, n):
+    """An output's rounding, the weights' (bf16: one rounding to bf16 at most), the scores' on both
+    a weight and the sum, and the sums' own."""
+    eps = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    return eps * np.abs(ref) + mass * ((2.0 ** -8 if dtype == "bf16" else 0.0) + 2 * err + (n / 8 + 64) * 2.0 ** -24) + 1e-30
+
+
+def _weights_case(nq, nkv, d, dtype, positions, *, page=16, cap=0.0, bias=False, scale=0.0, slots=None, ld=None, seed=31,
+                  layers=1, layer=0, max_seq=None, calls=1, heads=None):
+    B, top = len(positions), max(max(positions) + 1, 1)
+    slots = slots or top
+    ld = ld or top
+    m, shape = _model(nq, nkv, d, dtype, max_batch=B, max_seq=max_seq or slots, n_layers=layers)
+    dt = shape.torch_dtype
+    kv, k, v, pt = _filled(shape, B, slots, page, dt, seed, read=[p + 1 for p in positions])
+    q = _randn((B, nq, d), dt, seed + 5, 1.5)
+    w0 = torch.rand(B, nkv, ld, generator=_gen(seed + 6))
+    w, scratch = w0.cuda(), torch.full((B, nq, ld), float("nan"), device="cuda")
+    out = torch.full((B, nq * d), 3.0, dtype=dt, device="cuda")
+    sl = _slopes(nq) if bias else None
+    sc = binding.Scores(scale, cap, None if sl is None else sl.cuda())
+    for _ in range(calls):
+        m.op_attention_decode_weights(q.cuda(), _i32(positions), layer, kv, out, w, scratch, scores=sc)
+    m.sync()
+    qf, got_w = f64(q), f64(w)
+    sc = scale or 1 / math.sqrt(d)
+    for b, p in enumerate(positions):
+        n = p + 1
+        K, V = _keys_of(k, pt, page, layer, b, n), _keys_of(v, pt, page, layer, b, n)
+        where, all_keys = np.arange(n), np.ones(n, bool)
+        for g in range(nkv):
+            G = nq // nkv
+            if heads is not None and g not in heads:
+                continue
+            add, tol = np.zeros(n), np.zeros(n)
+            for h in range(g * G, g * G + G):
+                e = _score_error(qf[b, h], K[g], sc, cap, n if bias else 0)
+                pr = C.weigh(qf[b, h], K[g], p, where, all_keys, sc, cap, 0.0 if sl is None else float(sl[h]))
+                add, tol = add + pr, tol + pr * (2 * e + (n / 8 + 64) * 2.0 ** -24)
+                _within(out[b].view(nq, d)[h], pr @ V[g], _out_bound(pr @ V[g], pr @ np.abs(V[g]), dtype, e, n),
+                        "out b=%d h=%d n=%d" % (b, h, n))
+            want = f64(w0)[b, g].copy()
+            want[:n] += calls * add
+            bound = (G + calls) * 2.0 ** -24 * np.abs(want)
+            bound[:n] += calls * tol + 1e-37
+            bound[n:] = 0.0
+            _within(got_w[b, g], want, bound, "weights b=%d g=%d n=%d" % (b, g, n))
+
+
+OPTS = [dict(), dict(cap=30.0), dict(bias=True), dict(cap=20.0, bias=True, scale=0.11)]
+
+
+@pytest.mark.parametrize("nq,nkv", [(4, 4), (8, 1), (6, 2), (16, 1), (12, 1), (5, 5)])
+@pytest.mark.parametrize("opt", OPTS)
+def test_weights_bf16(nq, nkv, opt):
+    _weights_case(nq, nkv, 128, "bf16", [0, 14, 15, 16, 62, 63, 64, 300], **opt)
+
+
+@pytest.mark.parametrize("page", [0, 16, 64, 80])
+@pytest.mark.parametrize("slots,ld", [(700, 700), (5000, 5000), (700, 1000), (4000, 690)])
+def test_weights_rooms(page, slots, ld):
+    _weights_case(8, 2, 128, "bf16", [689, 3, 130], page=page, slots=slots, ld=ld)
+
+
+@pytest.mark.parametrize("B,nq,nkv", [(1, 32, 32), (1, 8, 1), (40, 8, 1), (130, 2, 2)])
+def test_weights_batches(B, nq, nkv):
+    _weights_case(nq, nkv, 128, "bf16", [(37 * i + 5) % 290 for i in range(B)], heads=[0, nkv - 1])
+
+
+def test_weights_long_splits():
+    _weights_case(8, 1, 128, "bf16", [19999], page=64, cap=50.0)
+    _weights_case(16, 1, 128, "bf16", [9000, 1], page=16, slots=30000)
+
+
+def test_weights_add_up_over_calls_and_layers():
+    _weights_case(4, 2, 128, "bf16", [70, 20], calls=3, layers=2, layer=1)
+
+
+@pytest.mark.parametrize("nq,nkv,d", [(4, 2, 64), (2, 2, 40), (20, 1, 128), (40, 1, 64), (1, 1, 256), (3, 1, 8)])
+@pytest.mark.parametrize("page", [0, 16, 5])
+@pytest.mark.parametrize("opt", OPTS)
+def test_weights_fp32(nq, nkv, d, page, opt):
+    _weights_case(nq, nkv, d, "f32", [0, 15, 64, 300], page=page, **opt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weights_bad_positions_and_pages(dtype):
+    m, shape = _model(4, 2, 128, dtype, max_batch=4, max_seq=64)
+    kv, k, v, pt = _filled(shape, 4, 64, 16, shape.torch_dtype, 3)
+    q = _randn((4, 4, 128), shape.torch_dtype, 4, 1.5).cuda()
+    scratch = torch.empty(4, 4, 50, device="cuda")
+
+    def call(positions):
+        w, out = torch.ones(4, 2, 50, device="cuda"), torch.full((4, 512), 3.0, dtype=shape.torch_dtype, device="cuda")
+        m.op_attention_decode_weights(q, _i32(positions), 0, kv, out, w, scratch)
+        return m.sync_status(), w, out
+    # no keys; past the weights' room; far past; in range
+    (rc, flags), w, out = call([-1, 50, 2 ** 31 - 1, 49])
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE
+    assert torch.all(out[0] == 0) and torch.all(w[0] == 1)
+    (rc, _), w2, out2 = call([49, 49, 49, 49])
+    assert rc == 0 and torch.equal(w[1:], w2[1:]) and torch.equal(out[1:], out2[1:])
+    total = (w2 - 1).double().sum(-1)
+    assert torch.all((total - 2).abs() < 1e-4)  # each of the two heads' weights add up to one
+    kv.page_table[2, 1] = 77
+    (rc, flags), w3, _ = call([49, 49, 49, 49])
+    assert rc == 5 and flags == binding.FLAG_PAGE_RANGE and torch.isfinite(w3).all()
+    kv.page_table = pt.cuda()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("slots", [100, 4000])
+def test_weights_nan_stays_in_its_heads(dtype, slots):
+    m, shape = _model(4, 2, 128, dtype, max_batch=2, max_seq=slots)
+    kv, k, v, pt = _filled(shape, 2, slots, 16, shape.torch_dtype, 5)
+    kv.k[0, int(pt[0, 4]), 1, 3] = float("nan")  # key 67 of sequence 0, K/V head 1
+    q = _randn((2, 4, 128), shape.torch_dtype, 6, 1.5).cuda()
+    q[1, 0, 5] = float("nan")  # head 0 of sequence 1: K/V head 0
+    w, out = torch.zeros(2, 2, slots, device="cuda"), torch.empty(2, 512, dtype=shape.torch_dtype, device="cuda")
+    m.op_attention_decode_weights(q, _i32([90, 80]), 0, kv, out, w, torch.empty(2, 4, slots, device="cuda"))
+    m.sync()
+    bad = torch.isnan(w)
+    assert bad[0, 1, :91].all() and not bad[0, 1, 91:].any() and not bad[0, 0].any()
+    assert bad[1, 0, :81].all() and not bad[1, 0, 81:].any() and not bad[1, 1].any()
+    bad = torch.isnan(out.view(2, 4, 128))
+    assert bad[0, 2:].all() and not bad[0, :2].any() and bad[1, 0].all() and not bad[1, 1:].any()
+
+
+def test_weights_give_the_plain_decode_output():
+    m, shape = _model(8, 2, max_batch=3, max_seq=700)
+    kv, *_ = _filled(shape, 3, 700, 16, torch.bfloat16, 7)
+    q, pos = _randn((3, 8, 128), torch.bfloat16, 8, 1.5).cuda(), _i32([699, 5, 320])
+    outs = [torch.empty(3, 1024, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    m.op_attention_decode_shared(q, pos, 0, kv, outs[0])
+    m.op_attention_decode_weights(q, pos, 0, kv, outs[1], torch.zeros(3, 2, 700, device="cuda"),
+                                  torch.empty(3, 8, 700, device="cuda"))
+    m.sync()
+    # the same sums merged in another order: a rounding apart
+    assert torch.all((outs[0].float() - outs[1].float()).abs() <= 2.0 ** -7 * outs[0].float().abs() + 2.0 ** -18)
