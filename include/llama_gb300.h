@@ -591,6 +591,28 @@ int llama_op_rope_norm_append_at(llama_ctx* ctx, const void* qkv, int32_t qkv_dt
                                  const void* q_gain, const void* k_gain, float norm_eps, int32_t layer,
                                  const llama_kv* kv, void* q_out, void* k_out, void* v_out);
 
+/* Attention of drafted rows over a cache. q T [n_rows, n_q, d] (rotated, 16-byte
+ * aligned); sequence b owns rows cu_rows[b] .. cu_rows[b+1] - 1 (DEVICE int32 [B+1],
+ * non-decreasing; a sequence may have none), whose K and V are in its cache slots
+ * start_pos[b], start_pos[b] + 1, .. (DEVICE int32 [B]). Row i of a sequence attends slots
+ * 0 .. start_pos[b]-1 and the slot of row j of the same sequence where bit j % 32 of
+ * mask[row][j / 32] is set (DEVICE uint32 [n_rows][mask_words]; its ancestors and itself,
+ * say; bits past the sequence's rows count for nothing, and what the words do not reach is hidden).
+ * mask NULL: rows 0 .. i (a chain). A row that sees no key gives zeros. positions
+ * (DEVICE int32 [n_rows], 0 .. 2^30, others are cut there; NULL: the slots) are read for the
+ * distance bias of scores alone, which goes by |position - position|; a cached key's is its slot.
+ * out T [n_rows, n_q d]; rows of no sequence are left as they were.
+ * V must be finite in a sequence's rows (a hidden one may take part with weight 0) and
+ * |V| as in llama_op_attention_docs. cu_rows outside [0, n_rows] or decreasing, a
+ * negative start (its rows give zeros) and slots past the cache (not attended) set
+ * LLAMA_FLAG_POS_RANGE, a page id outside the pool LLAMA_FLAG_PAGE_RANGE (its keys read
+ * as zeros). Any number of rows, n_rows * n_q < 2^30; B as the cache allows. The cache has
+ * the context's dtype (an E4M3 cache is UNSUPPORTED). One launch, bf16 two. */
+int llama_op_attention_tree(llama_ctx* ctx, const void* q, int32_t n_rows, const int32_t* cu_rows,
+                            const int32_t* start_pos, int32_t B, const uint32_t* mask,
+                            int32_t mask_words, const int32_t* positions, int32_t layer,
+                            const llama_kv* kv, const llama_scores* scores, void* out);
+
 /* Of a cache's layers, all. */
 #define LLAMA_ALL_LAYERS (-1)
 

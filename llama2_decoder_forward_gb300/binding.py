@@ -152,6 +152,9 @@ _SIGS = {
     "llama_op_attention_decode_weights": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32,
                                                     ctypes.POINTER(KV), ctypes.POINTER(_Scores),
                                                     c_void_p, ctypes.c_int64, c_void_p, c_void_p]),
+    "llama_op_attention_tree": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
+                                          c_void_p, c_int32, c_void_p, c_int32, ctypes.POINTER(KV),
+                                          ctypes.POINTER(_Scores), c_void_p]),
     "llama_op_cache_commit": (c_int32, [c_void_p, ctypes.POINTER(KV), c_int32, c_void_p, c_int32,
                                         c_void_p, c_int32, c_void_p]),
     "llama_op_cache_evict": (c_int32, [c_void_p, ctypes.POINTER(KV), c_int32, c_void_p, c_int32, c_int32,
@@ -451,6 +454,7 @@ class Model:
         import torch
         l = lib()
         self._append, self._docs = l.llama_op_rope_norm_append, l.llama_op_attention_docs
+        self._tree = l.llama_op_attention_tree
         self._append_at, self._weights = l.llama_op_rope_norm_append_at, l.llama_op_attention_decode_weights
         self._shared = l.llama_op_attention_decode_shared
         self._dt, self._qkv_rows = shape.torch_dtype, shape.qkv_rows
@@ -649,6 +653,29 @@ class Model:
             _need("out", out, dt, qn, dev))
         if rc:
             raise LlamaError(rc, "llama_op_attention_decode_shared")
+
+    def op_attention_tree(self, q, cu_rows, start_pos, layer, kv: KVCache, out, *, mask=None, positions=None,
+                          scores=None):
+        """Attention of drafted rows over a cache (llama_op_attention_tree): q [n_rows, n_q, d]
+        packed by cu_rows int32 [B + 1], row i of sequence b in slot start_pos[b] + i; mask
+        int32 [n_rows, words], bit j % 32 of word j // 32 for row j of the same
+        sequence, or None for chains; positions int32 [n_rows], for a distance bias."""
+        s, dt, i32, dev = self.shape, self._dt, self._i32, self._dev
+        n, B = q.shape[0], start_pos.numel()
+        qn, words = n * s.n_q_heads * s.head_dim, 0
+        if mask is not None:
+            if mask.dim() != 2:
+                raise ValueError("mask: want [n_rows, words], got %s" % (tuple(mask.shape),))
+            words = mask.shape[1]
+        rc = self._tree(
+            self.ctx, _need("q", q, dt, qn, dev), n, _need("cu_rows", cu_rows, i32, B + 1, dev),
+            _need("start_pos", start_pos, i32, B, dev), B,
+            None if mask is None else _need("mask", mask, i32, n * words, dev), words,
+            None if positions is None else _need("positions", positions, i32, n, dev), layer,
+            kv._now(s, dt, B, dev), None if scores is None else scores._now(self._f32, s.n_q_heads, dev),
+            _need("out", out, dt, qn, dev))
+        if rc:
+            raise LlamaError(rc, "llama_op_attention_tree")
 
     def op_attention_decode_weights(self, q, positions, layer, kv: KVCache, out, weights, scratch, *,
                                     scores=None):

@@ -142,11 +142,12 @@ Layout make_layout(const llama_config* c, int sm_count) {
   L.apart = take(std::max<size_t>(L.apart_bytes, 16));
   // fused RMSNorm: per-(128-feature tile, row) sums of squares of the residual stream
   L.ssq = take((H + 127) / 128 * (size_t)R * 4);
-  // partial results of decode attention over a shared prefix (bf16); rows' maxima and sums
+  // partial results of decode attention over a shared prefix and of trees (bf16); rows' maxima and sums
   // of decode attention with key weights (fp32)
-  L.spart = take(c->dtype == LLAMA_BF16 ? shared_partial_bytes(c->max_batch, (int)nq, (int)nkv,
-                                                               c->max_seq, sm_count)
-                                        : (size_t)c->max_batch * nq * 8);
+  L.spart = take(c->dtype == LLAMA_BF16
+                     ? std::max(shared_partial_bytes(c->max_batch, (int)nq, (int)nkv, c->max_seq, sm_count),
+                                tree_partial_bytes(sm_count))
+                     : (size_t)c->max_batch * nq * 8);
   L.total = off;
   return L;
 }
@@ -1420,7 +1421,8 @@ int decode_args(llama_ctx* c, const void* q, const int32_t* positions, int32_t B
   return LLAMA_OK;
 }
 // The cache's views of the tensor-core forms, and q as boxes of G heads and rows_box rows.
-int decode_maps(llama_ctx* c, const llama_kv* kv, int64_t q_rows, int rows_box, SharedArgs* a) {
+extern "C++" template <typename Args>
+int decode_maps(llama_ctx* c, const llama_kv* kv, int64_t q_rows, int rows_box, Args* a) {
   const llama_config& cf = c->cfg;
   trim_maps(c);
   const uint64_t d = cf.head_dim, nkv = cf.n_kv_heads;
@@ -1500,6 +1502,59 @@ int llama_op_attention_decode_weights(llama_ctx* c, const void* q, const int32_t
   Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
   c->launches += 2;
   return cuda_rc(launch_decode_weights(a, plan, w, c->stream));
+}
+
+int llama_op_attention_tree(llama_ctx* c, const void* q, int32_t n_rows, const int32_t* cu_rows,
+                            const int32_t* start_pos, int32_t B, const uint32_t* mask, int32_t mask_words,
+                            const int32_t* positions, int32_t layer, const llama_kv* kv,
+                            const llama_scores* scores, void* out) {
+  TRY(check_ctx(c));
+  const llama_config& cf = c->cfg;
+  if (!q || !cu_rows || !start_pos || !out || n_rows < 1 || B < 1 || layer < 0 || layer >= cf.n_layers ||
+      (mask && mask_words < 1))
+    return LLAMA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return LLAMA_ERR_INVALID_ARG;
+  if ((int64_t)n_rows * cf.n_q_heads >= (1ll << 30)) return LLAMA_ERR_OUT_OF_RANGE;
+  TRY(check_kv(c, kv, B));
+  if (kv->kv_dtype != LLAMA_KV_MODEL) return LLAMA_ERR_UNSUPPORTED;
+  TreeArgs a{};
+  TRY(score_args(c, scores, &a.sc));
+  TRY(check_device(c));
+  a.q = q;
+  a.out = out;
+  a.n_rows = n_rows;
+  a.B = B;
+  a.n_q = cf.n_q_heads;
+  a.n_kv = cf.n_kv_heads;
+  a.head_dim = cf.head_dim;
+  a.layer = layer;
+  a.cu_rows = cu_rows;
+  a.start_pos = start_pos;
+  a.mask = mask;
+  a.mask_words = mask ? mask_words : 0;
+  a.row_pos = positions;
+  a.k_cache = kv->k;
+  a.v_cache = kv->v;
+  a.page_table = kv->page_table;
+  a.page_size = kv->page_size;
+  a.capacity = kv->capacity;
+  a.batch_cap = kv->batch_capacity;
+  a.n_pages = kv->n_pages;
+  a.max_pages = kv->max_pages_per_seq;
+  const int64_t slots = kv->page_size ? (int64_t)kv->max_pages_per_seq * kv->page_size : kv->capacity;
+  a.key_limit = (int)std::min<int64_t>(slots, 0x7fffff00);
+  a.status = c->status;
+  a.sm_count = c->sm_count;
+  if (cf.dtype != LLAMA_BF16) {
+    Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
+    c->launches++;
+    return cuda_rc(launch_tree_simt(a, c->stream));
+  }
+  TRY(decode_maps(c, kv, n_rows, 128 / (cf.n_q_heads / cf.n_kv_heads), &a));
+  a.partial = c->at<float>(c->L.spart);
+  Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
+  c->launches += 2;
+  return cuda_rc(launch_tree_tc(a, c->stream));
 }
 
 namespace {

@@ -24,6 +24,9 @@ __device__ __forceinline__ int key_position(int pos, int key_limit) {
   return max(min(pos, key_limit - 1), -1);
 }
 
+// Positions of drafted rows are cut to 0 .. kMaxPos, so that distances stay in an int.
+constexpr int kMaxPos = 1 << 30;
+
 // The maximum that a partial result of sum l is merged with: a maximum passes over
 // NaN scores, and without a finite one beside them the part would count as
 // empty, so a NaN sum takes part as +inf, which the merge turns into NaN.

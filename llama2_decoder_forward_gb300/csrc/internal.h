@@ -295,6 +295,28 @@ struct SharedArgs {
   int box_rows = 16, sm_count = 152;
   float* partial = nullptr;    // workspace, SharedPlan::partials x (128 + 2) floats
 };
+// Trees of drafted rows over a cache.
+struct TreeArgs {
+  const void* q;               // [n_rows, n_q, d]
+  void* out;
+  int n_rows, B, n_q, n_kv, head_dim, layer;
+  const int32_t *cu_rows, *start_pos;  // [B + 1], [B]
+  const uint32_t* mask;        // [n_rows][mask_words] or null (causal)
+  int mask_words;
+  const int32_t* row_pos;      // [n_rows] or null (the slots)
+  const void *k_cache, *v_cache;
+  const int32_t* page_table;
+  int page_size, capacity, batch_cap, n_pages, max_pages, key_limit;
+  ScoreArgs sc;
+  uint32_t* status;
+  const CUtensorMap *map_q = nullptr, *map_k = nullptr, *map_v = nullptr, *map_k16 = nullptr,
+                    *map_v16 = nullptr;
+  int box_rows = 16, sm_count = 152;
+  float* partial = nullptr;    // workspace, tree_partial_bytes
+};
+size_t tree_partial_bytes(int sm_count);
+cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st);    // k_attn_forms_tc.cu
+cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t st);  // k_attn_simt.cu
 // How a decode batch over a shared prefix is cut: the prefix kernel's grid
 // (prefix_splits, row_blocks, n_kv) and the own keys' splits.
 struct SharedPlan {

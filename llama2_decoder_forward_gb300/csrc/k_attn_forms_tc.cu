@@ -67,8 +67,8 @@ constexpr uint32_t OFF_BAR = SLOTS * TILE;
 // what the two threads of a row exchange: fp32 [2 row tiles][2 halves][128], the
 // tile's maxima, at the end the sums. One buffer is enough: a tile's maxima are
 // read before its P is announced, and the next tile's scores come after that.
-constexpr uint32_t OFF_WORK = OFF_BAR + 256;  // documents: two published work items, 32 bytes each
-constexpr uint32_t OFF_X = OFF_WORK + 64;
+constexpr uint32_t OFF_WORK = OFF_BAR + 256;  // documents, trees: two published work items, up to 48 bytes each
+constexpr uint32_t OFF_X = OFF_WORK + 128;
 constexpr size_t FORMS_SMEM = OFF_X + 2 * 2 * 128 * 4;
 constexpr int FORMS_THREADS = 640;
 constexpr int MAXK = 4, MAXV = 2;           // ring sizes at most
@@ -99,8 +99,15 @@ struct FormsParams {
   int sm_count;
   int waiting;                              // the own keys' CTAs wait for this kernel
   float own_items;                          // how many those are
+  // trees: out, cu_rows, n_rows, n_docs as documents; the cache as a prefix
+  const int32_t *start_pos, *row_pos;
+  const uint32_t* mask;
+  int mask_words, least_tiles;
   float poly[13];                           // KCapFixed: kTanh times powers of scale / cap
 };
+
+// What a launch works on.
+enum { MPrefix, MDocs, MTree };
 
 // What the scores need. A cap bounds them, so up to kFixedCap (log2 units) the
 // weights are 2^s with no maximum subtracted: 2^+-72 times a sum stays inside fp32
@@ -164,6 +171,12 @@ struct Ring {
       phase ^= 1;
     }
   }
+  __device__ __forceinline__ void back() {
+    if (--slot < 0) {
+      slot += n;
+      phase ^= 1;
+    }
+  }
 };
 
 // Cache row of the keys starting at k0 of sequence b, K/V head g; a page
@@ -183,9 +196,9 @@ __device__ __forceinline__ int forms_kv_row(const FormsParams& p, int b, int g, 
 // j + lane / 8, step lane % 8): looked up once per four tiles and ahead of the
 // wait for a free slot (a lookup per box in front of its copy held every tile
 // back by some 2000 cycles).
-__device__ __forceinline__ int tile_rows(const FormsParams& p, int g, int tile, int kmax, int lane) {
+__device__ __forceinline__ int tile_rows(const FormsParams& p, int b, int g, int tile, int kmax, int lane) {
   const int k0 = (tile + (lane >> 3)) * TN + (lane & 7) * 16;
-  return k0 < kmax ? forms_kv_row(p, p.shared_seq, g, k0) : 0;
+  return k0 < kmax ? forms_kv_row(p, b, g, k0) : 0;
 }
 
 // K or V tile of keys k0 .. k0 + nvalid - 1 by a whole warp, completing on bar.
@@ -283,6 +296,12 @@ __device__ __forceinline__ void add_pair(float& a, float& b, uint32_t x) {
       : "r"(x));
 }
 
+// Scores of keys whose bit is 0 replaced.
+__device__ __forceinline__ void hide_bits(float* x, uint32_t bits, float with) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = bits >> i & 1u ? x[i] : with;
+}
+
 // 32 aligned bytes: a thread owns a row, so a smaller store would write half a sector
 __device__ __forceinline__ void store_sector(void* dst, const uint32_t* x) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]),
@@ -360,8 +379,9 @@ struct FormsWork {
   int t0, n_tiles;      // first key tile and how many
   int kmax;             // keys below this exist for some row
   int nt0, nt1;         // key tiles that row tile 0 / 1 visits
-  int split, seq0;      // prefix: key split, first sequence
+  int split, seq0;      // prefix: key split, first sequence; trees: partial (-1: none), sequence
   int last_rows;        // keys of the last tile; over TN: all
+  int start;            // trees: cached keys in front of the tree
 };
 // Documents: what follows from an item's document, first row and head.
 __device__ __forceinline__ void doc_work(const FormsParams& p, int lo, int n, int q0, int pre, int h0, int g,
@@ -446,13 +466,197 @@ __device__ __forceinline__ int prefix_share(const FormsParams& p, int lane) {
   return __reduce_min_sync(0xffffffffu, __float_as_uint(best) == top ? share : INT_MAX);
 }
 
-template <bool DOCS, int KIND>
+// Trees. An item is a block of a sequence's rows (one or two row tiles) and a K/V
+// head; it has T key tiles. All items' tiles, in one line (sequence, head, block, tile),
+// are cut into equal chunks, one per CTA, so that every SM gets the same number of
+// tiles whatever the lengths. A CTA's first and last item may be shared with its
+// neighbours: those leave partial results (CTA c: 2c for its first item, 2c + 1 for its
+// last), which the joining kernel merges; items within a chunk are stored at once.
+struct TreeSeq {   // a sequence's rows, its keys, and the tiles of all its items
+  int lo, n, start, keys, T, blocks;
+  long long tiles;
+};
+__device__ __forceinline__ TreeSeq tree_seq(const FormsParams& p, int b, uint32_t* status) {
+  TreeSeq s;
+  doc_rows(p.cu_rows, b, p.n_rows, status, s.lo, s.n);
+  const int start = p.start_pos[b];
+  const long long end = (long long)start + s.n;
+  if (s.n > 0 && (start < 0 || end > p.key_limit)) flag(status, LLAMA_FLAG_POS_RANGE);
+  s.keys = start < 0 ? 0 : (int)(end < p.key_limit ? end : p.key_limit);
+  s.start = start < 0 ? 0 : min(start, s.keys);
+  const int rows = p.alternate ? p.rows_seq : 2 * p.rows_seq;
+  s.T = max(1, (s.keys + TN - 1) / TN);  // one, to store the rows of a sequence without keys
+  s.blocks = (s.n + rows - 1) / rows;
+  s.tiles = (long long)s.blocks * p.n_kv * s.T;
+  return s;
+}
+// Sum of x over the lanes up to each one.
+__device__ __forceinline__ long long sum_upto(long long x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+// Tiles of a chunk, for a whole warp; *total: of all items.
+__device__ __forceinline__ long long tree_chunk(const FormsParams& p, int ctas, int lane, uint32_t* status,
+                                                long long* total) {
+  long long all = 0;
+  for (int b = lane; b < p.n_docs; b += 32) all += tree_seq(p, b, status).tiles;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  *total = all;
+  return max((long long)p.least_tiles, (all + ctas - 1) / ctas);
+}
+// The item that tile u belongs to, for a whole warp whose questions ascend.
+struct TreeCursor {
+  int b0 = 0;
+  long long before = 0;  // tiles of the sequences before b0
+};
+struct TreeItem {
+  int b, g, block, lo, n, start, keys, T;
+  long long first;       // its first tile
+};
+__device__ __forceinline__ bool tree_item(const FormsParams& p, long long u, TreeCursor& c, int lane, TreeItem& it) {
+  for (; c.b0 < p.n_docs; c.b0 += 32) {
+    TreeSeq s{};
+    if (c.b0 + lane < p.n_docs) s = tree_seq(p, c.b0 + lane, nullptr);
+    const long long upto = c.before + sum_upto(s.tiles, lane);
+    const uint32_t m = __ballot_sync(0xffffffffu, u < upto);
+    if (m) {
+      const int w = __ffs(m) - 1;
+      it.b = c.b0 + w;
+      it.lo = __shfl_sync(0xffffffffu, s.lo, w);
+      it.n = __shfl_sync(0xffffffffu, s.n, w);
+      it.start = __shfl_sync(0xffffffffu, s.start, w);
+      it.keys = __shfl_sync(0xffffffffu, s.keys, w);
+      it.T = __shfl_sync(0xffffffffu, s.T, w);
+      const int blocks = __shfl_sync(0xffffffffu, s.blocks, w);
+      const long long base = __shfl_sync(0xffffffffu, upto - s.tiles, w);
+      const int item = (int)((u - base) / it.T);
+      it.first = base + (long long)item * it.T;
+      it.g = item / blocks;
+      it.block = item - it.g * blocks;
+      return true;
+    }
+    c.before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+// What follows from an item's published part.
+__device__ __forceinline__ void tree_work(const FormsParams& p, FormsWork& w) {
+  w.pre = w.h0 = 0;
+  w.nt0 = p.alternate ? (w.n_tiles + 1) / 2 : w.n_tiles;
+  w.nt1 = p.alternate ? w.n_tiles / 2 : w.q0 + p.rows_seq < w.n ? w.n_tiles : 0;
+  w.last_rows = w.kmax - (w.t0 + w.n_tiles - 1) * TN;
+}
+// Which of the 32 keys from the x-th row of its tree on (x may be negative: cached
+// keys, all visible) row i of the tree attends; `there` rows of the tree are in the cache.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t tree_word(const FormsParams& p, size_t row, int i, int there, int j) {
+  uint32_t m = low_bits(min(there, p.mask ? INT_MAX : i + 1) - 32 * j);
+  if (p.mask && m) m &= j < p.mask_words ? p.mask[row * p.mask_words + j] : 0u;
+  return m;
+}
+__device__ __forceinline__ uint32_t tree_bits(const FormsParams& p, size_t row, int i, int there, int x) {
+  if (x <= -32) return ~0u;
+  if (x < 0) return low_bits(-x) | tree_word(p, row, i, there, 0) << -x;
+  const int j = x >> 5, s = x & 31;
+  const uint32_t a = tree_word(p, row, i, there, j);
+  return s ? __funnelshift_r(a, tree_word(p, row, i, there, j + 1), s) : a;
+}
+
+__device__ __forceinline__ void softmax_bar() {  // the 16 softmax warps
+  asm volatile("bar.sync 9, 512;" ::: "memory");
+}
+
+// 32 outputs of a row, times inv, as bf16
+__device__ __forceinline__ void store_out(const FormsParams& p, bf16* dst, const float* u, float inv) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 16) {
+    uint32_t x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = pack_bf16(u[i + 2 * k] * inv, u[i + 2 * k + 1] * inv);
+    if (p.out32) {
+      store_sector(dst + i, x);
+    } else {
+      *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+  }
+}
+
+// A tree item's rows, from tensor memory to the output or to a partial result. Two row
+// tiles with the same rows (alternate) are merged first: thread (t, grp) of a row takes
+// 32 of its 128 dims from both. Every softmax thread calls this.
+__device__ __forceinline__ void tree_store(const FormsParams& p, const FormsWork& w, bool alt, int t, int grp, int r,
+                                           uint32_t tl, bool row_ok, size_t row, int head, float m, float l,
+                                           int count, float* x, volatile uint32_t* stop) {
+  m = count == 0 || l == 0.f ? -INFINITY : merge_max(m, l);
+  float f0 = 1.f, f1 = 0.f;
+  if (alt) {
+    x[t * 256 + 128 * grp + r] = grp ? l : m;
+    softmax_bar();  // (and both tiles' last MMAs are done)
+    const float m0 = x[r], l0 = x[128 + r], m1 = x[256 + r], l1 = x[384 + r];
+    m = fmaxf(m0, m1);
+    f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
+    f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+    l = (m0 == -INFINITY ? 0.f : l0 * f0) + (m1 == -INFINITY ? 0.f : l1 * f1);
+  }
+  tc_fence_after();
+  const bool go = !__any_sync(0xffffffffu, *stop);
+  const size_t at = (size_t)max(w.split, 0) * (alt ? TM : 2 * TM) + (alt ? 0 : t * TM) + r;
+  const bool store = go && row_ok &&
+                     bc_ok(row < (size_t)p.n_rows && (w.split < 0 || at < p.partials), p.status);
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  // non-alternate: 64 dims of this row tile; alternate: 32 of both
+  const int d0 = 64 * grp + (alt ? 32 * t : 0);
+  if (alt || w.nt1 > 0 || t == 0) {
+#pragma unroll 1
+    for (int q = 0; q < (alt ? 32 : 64); q += 32) {
+      float u[32];
+      const uint32_t oc = tl + O_COL + (uint32_t)((alt ? 0 : t * 128) + d0 + q);
+      tmem_ld32(oc, reinterpret_cast<uint32_t*>(u));
+      tmem_ld_wait();
+      if (alt) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i] = f0 != 0.f ? u[i] * f0 : 0.f;
+        if (w.nt1 > 0) {
+#pragma unroll
+          for (int h = 0; h < 32; h += 16) {
+            uint32_t v[16];
+            tmem_ld16(oc + 128 + h, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[h + i] = f1 != 0.f ? fmaf(__uint_as_float(v[i]), f1, u[h + i]) : u[h + i];
+          }
+        }
+      }
+      if (store && w.split < 0) {
+        store_out(p, p.out + (row * p.n_q + head) * 128 + d0 + q, u, inv);
+      } else if (store) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          store_sector(p.part_o + at * 128 + d0 + q + i, reinterpret_cast<const uint32_t*>(u + i));
+      }
+    }
+    if (store && w.split >= 0 && grp == 0 && (!alt || t == 0)) {
+      p.part_ml[2 * at] = m;
+      p.part_ml[2 * at + 1] = l;
+    }
+  }
+  if (alt) softmax_bar();  // the exchange and the other tile's O have been read
+}
+
+template <int MODE, int KIND>
 __global__ void __launch_bounds__(FORMS_THREADS, 1)
     attn_forms_kernel(const __grid_constant__ CUtensorMap mapQ,
                       const __grid_constant__ CUtensorMap mapK,
                       const __grid_constant__ CUtensorMap mapV,
                       const __grid_constant__ CUtensorMap mapK16,
                       const __grid_constant__ CUtensorMap mapV16, FormsParams p) {
+  constexpr bool DOCS = MODE == MDocs, TREE = MODE == MTree, PREFIX = MODE == MPrefix;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint64_t* qempty = qfull + 1;
@@ -512,7 +716,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     fence_mbar_init();
   }
   if (warp == 18) tmem_alloc(const_cast<uint32_t*>(ctl), 512);
-  if (!DOCS && warp == 17) {
+  if (PREFIX && warp == 17) {
     const int n = prefix_share<KIND>(p, lane);
     if (lane == 0) {
       ctl[4] = n;
@@ -525,14 +729,33 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl[0], 0);
-  const int share = DOCS ? 0 : __shfl_sync(0xffffffffu, ctl[4], 0);
+  const int share = PREFIX ? __shfl_sync(0xffffffffu, ctl[4], 0) : 0;
 
   // launched with 640 x 96 registers: 512 x 104 + 128 x 64
   // The it-th work item, as the Q and K producer published it: the walk to it
   // costs some 3000 cycles, which in every warp delayed each item's start.
   auto work = [&](int it, FormsWork& w) -> bool {
-    if (!DOCS) return it == 0 && prefix_work(p, share, w);
+    if (PREFIX) return it == 0 && prefix_work(p, share, w);
     const int s = it & 1;
+    if (TREE) {
+      const bool ok = __all_sync(0xffffffffu, wait_bar(&wfull[s], (it >> 1) & 1, stop, p.status));
+      const volatile int4* from = box + 3 * s;
+      w.lo = from->x;
+      w.n = from->y;
+      w.q0 = from->z;
+      w.g = from->w;
+      w.t0 = from[1].x;
+      w.n_tiles = from[1].y;
+      w.split = from[1].z;
+      w.seq0 = from[1].w;
+      w.start = from[2].x;
+      w.kmax = from[2].y;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&wempty[s]);
+      if (!ok || w.n == 0) return false;
+      tree_work(p, w);
+      return true;
+    }
     const bool ok = __all_sync(0xffffffffu, wait_bar(&wfull[s], (it >> 1) & 1, stop, p.status));
     const int lo = box[2 * s].x, n = box[2 * s].y, q0 = box[2 * s].z, pre = box[2 * s].w;
     const int h0 = box[2 * s + 1].x, g = box[2 * s + 1].y;
@@ -554,8 +777,52 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       int issued = 0, loaded_q = 0, rows = 0;
       bool ok = true;
       DocCursor cursor;
+      TreeCursor where;
+      long long u = 0, u_end = 0;  // trees: what is left of this CTA's chunk
+      if (TREE) {
+        long long total;
+        const long long chunk = tree_chunk(p, gridDim.x, lane, blockIdx.x == 0 ? p.status : nullptr, &total);
+        u = min(total, chunk * blockIdx.x);
+        u_end = min(total, u + chunk);
+      }
       for (int it = 0; ok; ++it) {
-        if (DOCS) {
+        if (TREE) {
+          TreeItem item{};
+          bool more = u < u_end && tree_item(p, u, where, lane, item);
+          if (more) {
+            w.lo = item.lo;
+            w.n = item.n;
+            w.q0 = item.block * (p.alternate ? p.rows_seq : 2 * p.rows_seq);
+            w.g = item.g;
+            w.t0 = (int)(u - item.first);
+            w.n_tiles = (int)min((long long)(item.T - w.t0), u_end - u);
+            w.split = w.n_tiles == item.T ? -1 : 2 * (int)blockIdx.x + (it > 0);
+            w.seq0 = item.b;
+            w.start = item.start;
+            w.kmax = item.keys;
+            tree_work(p, w);
+            u += w.n_tiles;
+          }
+          ok = __all_sync(0xffffffffu, wait_bar(&wempty[it & 1], ((it >> 1) & 1) ^ 1, stop, p.status));
+          if (!ok) break;
+          if (lane == 0) {
+            volatile int4* to = box + 3 * (it & 1);
+            to->x = w.lo;
+            to->y = more ? w.n : 0;  // an item has rows
+            to->z = w.q0;
+            to->w = w.g;
+            to[1].x = w.t0;
+            to[1].y = w.n_tiles;
+            to[1].z = w.split;
+            to[1].w = w.seq0;
+            to[2].x = w.start;
+            to[2].y = w.kmax;
+            mbar_arrive(&wfull[it & 1]);
+          }
+          __syncwarp();
+          if (!more) break;
+          rows = tile_rows(p, w.seq0, w.g, w.t0, w.kmax, lane);
+        } else if (DOCS) {
           const bool more = next_doc(p, it, cursor, w);
           ok = __all_sync(0xffffffffu, wait_bar(&wempty[it & 1], ((it >> 1) & 1) ^ 1, stop, p.status));
           if (!ok) break;
@@ -573,7 +840,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           if (!more) break;
         } else {
           if (it > 0 || !prefix_work(p, share, w)) break;
-          rows = tile_rows(p, w.g, w.t0, w.kmax, lane);
+          rows = tile_rows(p, p.shared_seq, w.g, w.t0, w.kmax, lane);
         }
         ok = __all_sync(0xffffffffu, wait_bar(qempty, (it & 1) ^ 1, stop, p.status));
         if (!ok) break;
@@ -589,11 +856,13 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
                 tma_load_3d(d, &mapQ, qfull, 64 * half, p.head_pairs ? w.h0 + t : w.h0,
                             w.lo + w.q0 + (p.head_pairs ? 0 : t * TM));
               else
-                tma_load_3d(d, &mapQ, qfull, 64 * half, w.g * p.G, w.seq0 + t * p.rows_seq);
+                tma_load_3d(d, &mapQ, qfull, 64 * half, w.g * p.G,
+                            (TREE ? w.lo + w.q0 : w.seq0) + t * p.rows_seq);
             }
         }
         for (int j = 0; j < w.n_tiles; ++j) {
-          if (!DOCS && j > 0 && (j & 3) == 0) rows = tile_rows(p, w.g, w.t0 + j, w.kmax, lane);
+          if (!DOCS && j > 0 && (j & 3) == 0)
+            rows = tile_rows(p, TREE ? w.seq0 : p.shared_seq, w.g, w.t0 + j, w.kmax, lane);
           ok = __all_sync(0xffffffffu, wait_bar(&kempty[r.slot], r.phase ^ 1, stop, p.status));
           if (!ok) break;
           load_tile<DOCS>(p, &mapK, &mapK16, kslots + r.slot * TILE, &kfull[r.slot], w.g, w.lo,
@@ -615,7 +884,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       bool ok = true;
       for (int it = 0; ok && work(it, w); ++it) {
         for (int j = 0; ok && j < w.n_tiles; ++j) {
-          if (!DOCS && (j & 3) == 0) rows = tile_rows(p, w.g, w.t0 + j, w.kmax, lane);
+          if (!DOCS && (j & 3) == 0)
+            rows = tile_rows(p, TREE ? w.seq0 : p.shared_seq, w.g, w.t0 + j, w.kmax, lane);
           ok = __all_sync(0xffffffffu, wait_bar(&vempty[r.slot], r.phase ^ 1, stop, p.status));
           if (!ok) break;
           const bool ragged = j + 1 == w.n_tiles && w.last_rows < TN;
@@ -760,6 +1030,15 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
             kr.step();
             vr.step();
           }
+        if (TREE && alt && (w.n_tiles & 1)) {  // the next item's tiles start at the next slot
+          if (t) {
+            kr.step();
+            vr.step();
+          } else {
+            kr.back();
+            vr.back();
+          }
+        }
         theirs += others;
       }
       if (elect_one()) tc_commit(&drained[t]);
@@ -791,7 +1070,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     if (DOCS && count == 0) continue;
     // this row: its position, its visible keys, where it goes
     bool row_ok;
-    int pos, lim, head;
+    int pos, lim, head, tree_i = 0;
     size_t row;  // documents: packed row; prefix: sequence
     const int pre = w.pre;
     if (DOCS) {
@@ -801,6 +1080,14 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       lim = min(max(i + 1, pre), w.n);
       head = p.head_pairs ? w.h0 + t : w.h0;
       row = (size_t)w.lo + i;
+    } else if (TREE) {
+      const int i = w.q0 + (p.alternate ? 0 : t * p.rows_seq) + r / p.G;
+      row_ok = r < p.rows_seq * p.G && i < w.n;
+      row = (size_t)w.lo + i;
+      tree_i = i;
+      pos = BIAS && row_ok ? p.row_pos ? min(max(p.row_pos[row], 0), kMaxPos) : w.start + i : 0;
+      lim = w.start;
+      head = w.g * p.G + r % p.G;
     } else {
       const int s = w.seq0 + (p.alternate ? 0 : t * p.rows_seq) + r / p.G;
       row_ok = r < p.rows_seq * p.G && s < p.B;
@@ -817,9 +1104,23 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       tc_fence_after();
       const int k0 = (w.t0 + (alt ? 2 * j + t : j)) * TN + NK * grp;  // this thread's first key
       const int left = lim - k0;                                    // visible keys (over NK: all)
-      const bool part = !__all_sync(0xffffffffu, left >= NK);
+      const bool part = TREE ? left < NK : !__all_sync(0xffffffffu, left >= NK);
+      uint32_t sees[2] = {~0u, ~0u};  // trees: the visible ones of this thread's keys
+      if (TREE && part) {
+        const int there = w.kmax - w.start;
+        sees[0] = row_ok ? tree_bits(p, row, tree_i, there, -left) : 0u;
+        sees[1] = row_ok ? tree_bits(p, row, tree_i, there, 32 - left) : 0u;
+      }
       // a warp that sees none of the tile's keys (above the diagonal): its weights are 0
-      const bool none = !__any_sync(0xffffffffu, left > 0);
+      const bool none = !__any_sync(0xffffffffu, TREE ? (sees[0] | sees[1]) != 0 : left > 0);
+      auto hide_keys = [&](float* x, float with) {  // the hidden ones of all NK keys
+        if (TREE) {
+          hide_bits(x, sees[0], with);
+          hide_bits(x + 32, sees[1], with);
+        } else {
+          hide<NK>(x, left, with);
+        }
+      };
       float x[KIND == KCapFixed ? 1 : NK];
       if (KIND != KCapFixed) {
         tmem_ld32(sc, reinterpret_cast<uint32_t*>(x));
@@ -829,7 +1130,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       if (KIND == KCap && !none) {
         // hidden keys and rows must not choose the path: they may hold anything,
         // and the paths differ in the last bits
-        if (part) hide<NK>(x, left, 0.f);
+        if (part) hide_keys(x, 0.f);
         const int level = cap_level<NK>(x, row_ok ? yk : 0.f);  // tanh; times cl with the bias below
         if (level == 0) {
 #pragma unroll
@@ -852,11 +1153,14 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       float cb = ct, sb = sl, base = BIAS ? sl * (float)(k0 - pos) : 0.f;
       if (BIAS && !none) {
         const int d0 = k0 - pos;
-        const bool ahead = DOCS && __any_sync(0xffffffffu, pre > pos && d0 + NK - 1 > 0);
+        const bool ahead = TREE ? __any_sync(0xffffffffu, part || (row_ok && d0 + NK - 1 > 0))
+                                : DOCS && __any_sync(0xffffffffu, pre > pos && d0 + NK - 1 > 0);
         if (ahead || __any_sync(0xffffffffu, fabsf(sl) > 2.f)) {
 #pragma unroll
           for (int i = 0; i < NK; ++i) {
-            const float dist = (float)(d0 + i);
+            float dist = (float)(d0 + i);
+            if (TREE && part && p.row_pos && i >= left && k0 + i < w.kmax)  // a row of the tree
+              dist = (float)(min(max(p.row_pos[w.lo + (i - left)], 0), kMaxPos) - pos);
             x[i] = fmaf(sl, ahead ? -fabsf(dist) : dist, x[i] * ct);
           }
           cb = 1.f;
@@ -865,7 +1169,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       }
       float mu = 0.f;
       if (KIND != KCapFixed) {
-        if (part && !none) hide<NK>(x, left, -INFINITY);
+        if (part && !none) hide_keys(x, -INFINITY);
         // ---- the row's maximum, and O rescaled when it grew
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if (none) {
@@ -948,7 +1252,12 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           tmem_ld_wait();
           // hidden keys and rows must not choose the path: they may hold
           // anything, and the paths differ in the last bits
-          if (part) hide<32>(y, left - q, 0.f);
+          if (part) {
+            if (TREE)
+              hide_bits(y, sees[q / 32], 0.f);
+            else
+              hide<32>(y, left - q, 0.f);
+          }
           const int level = cap_level<32>(y, row_ok ? yk : 0.f);
           if (level == 0) {  // the coefficients hold scale, cap and log2e
 #pragma unroll
@@ -964,7 +1273,12 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = cap_any(y[i], zc, cl);
           }
-          if (part) hide<32>(y, left - q, -INFINITY);
+          if (part) {
+            if (TREE)
+              hide_bits(y, sees[q / 32], -INFINITY);
+            else
+              hide<32>(y, left - q, -INFINITY);
+          }
           weigh(y, q);
         }
       } else {
@@ -982,7 +1296,9 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     half_bar(bar_id);
     l = xch[0] + xch[128];
     half_bar(bar_id);  // both have read: the next item may write
-    if (!__any_sync(0xffffffffu, *stop)) {
+    if (TREE) {
+      tree_store(p, w, alt, t, grp, r, tl, row_ok, row, head, m, l, count, reinterpret_cast<float*>(smem + OFF_X), stop);
+    } else if (!__any_sync(0xffffffffu, *stop)) {
       tc_fence_after();
       if (DOCS) {
         if (count > 0) {
@@ -1046,13 +1362,69 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
 using FormsKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
                              const CUtensorMap, const CUtensorMap, FormsParams);
 
-template <bool DOCS>
+template <int MODE>
 FormsKernel forms_kernel(int kind) {
   switch (kind) {
-    case KPlain: return attn_forms_kernel<DOCS, KPlain>;
-    case KBias: return attn_forms_kernel<DOCS, KBias>;
-    case KCapFixed: return attn_forms_kernel<DOCS, KCapFixed>;
-    default: return attn_forms_kernel<DOCS, KCap>;
+    case KPlain: return attn_forms_kernel<MODE, KPlain>;
+    case KBias: return attn_forms_kernel<MODE, KBias>;
+    case KCapFixed: return attn_forms_kernel<MODE, KCapFixed>;
+    default: return attn_forms_kernel<MODE, KCap>;
+  }
+}
+
+// Merges the partial results of tree items that several chunks share. Block (c, y): the
+// item that chunk c + 1 starts within, if that is the item's first such chunk; its
+// rows 16 y .. 16 y + 15, a warp for every four.
+__global__ void __launch_bounds__(128) attn_tree_join_kernel(FormsParams p, int ctas) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long total;
+  const long long chunk = tree_chunk(p, ctas, lane, nullptr, &total), u = chunk * (blockIdx.x + 1);
+  if (u >= total) return;
+  TreeCursor where;
+  TreeItem it;
+  if (!tree_item(p, u, where, lane, it) || it.first == u || u - it.first > chunk) return;
+  const int c0 = blockIdx.x;  // the chunk that the item starts in
+  const int parts = (int)((it.first + it.T - 1) / chunk) - c0 + 1;
+  const int rows_tile = p.rows_seq * p.G, rows_slot = p.alternate ? TM : 2 * TM;
+  const int q0 = it.block * (p.alternate ? p.rows_seq : 2 * p.rows_seq);
+  const bool first = it.first == chunk * c0;
+  for (int k = 0; k < 4; ++k) {
+    const int r = blockIdx.y * 16 + warp * 4 + k, tile = r / TM, rt = r - tile * TM;
+    const int i = q0 + tile * p.rows_seq + rt / p.G;
+    if (r >= rows_slot || rt >= rows_tile || i >= it.n) continue;
+    auto at = [&](int s) {  // partial s of the row
+      return (size_t)(2 * (c0 + s) + (s == 0 && !first)) * rows_slot + r;
+    };
+    if (!bc_ok(at(parts - 1) < p.partials, p.status)) return;
+    float m = -INFINITY, l = 0.f;
+    for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_ml[2 * at(s)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < parts && m != -INFINITY; s0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (s0 + lane < parts) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at(s0 + lane));
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+      if (f != 0.f) l = fmaf(ml.y, f, l);
+#pragma unroll 4
+      for (int s = 0; s < min(32, parts - s0); ++s) {
+        const float fs = __shfl_sync(0xffffffffu, f, s);
+        const float4 x = *reinterpret_cast<const float4*>(p.part_o + at(s0 + s) * 128 + 4 * lane);
+        if (fs != 0.f) {
+          v.x = fmaf(x.x, fs, v.x);
+          v.y = fmaf(x.y, fs, v.y);
+          v.z = fmaf(x.z, fs, v.z);
+          v.w = fmaf(x.w, fs, v.w);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    bf16* dst = p.out + (((size_t)it.lo + i) * p.n_q + it.g * p.G + rt % p.G) * 128;
+    reinterpret_cast<uint2*>(dst)[lane] = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
   }
 }
 
@@ -1073,11 +1445,11 @@ int score_kind(const ScoreArgs& s, FormsParams* p) {
   return KCapFixed;
 }
 
-template <bool DOCS>
+template <int MODE>
 cudaError_t prep() {
   for (int i = 0; i < 4; ++i) {
     const cudaError_t e = cudaFuncSetAttribute(
-        forms_kernel<DOCS>(i), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FORMS_SMEM);
+        forms_kernel<MODE>(i), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FORMS_SMEM);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -1086,8 +1458,9 @@ cudaError_t prep() {
 }  // namespace
 
 cudaError_t attn_forms_prepare() {
-  const cudaError_t e = prep<true>();
-  return e == cudaSuccess ? prep<false>() : e;
+  cudaError_t e = prep<MDocs>();
+  if (e == cudaSuccess) e = prep<MPrefix>();
+  return e == cudaSuccess ? prep<MTree>() : e;
 }
 
 cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st) {
@@ -1108,7 +1481,7 @@ cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st) {
   const int rows = p.head_pairs ? TM : 2 * TM, per = p.head_pairs ? a.n_q / 2 : a.n_q;
   const long long tiles = a.n_rows / rows + (long long)std::min(a.n_docs, a.n_rows);  // an upper bound
   const unsigned grid = (unsigned)std::min<long long>(tiles * per, a.sm_count);
-  return launch_k(forms_kernel<true>(kind), dim3(grid), dim3(FORMS_THREADS), FORMS_SMEM, st, 0,
+  return launch_k(forms_kernel<MDocs>(kind), dim3(grid), dim3(FORMS_THREADS), FORMS_SMEM, st, 0,
                   *a.map_q, *a.map_k, *a.map_v, *a.map_k, *a.map_v, p);
 }
 
@@ -1142,9 +1515,53 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
   p.sm_count = a.sm_count;
   p.waiting = !s.join;
   p.own_items = (float)((double)a.B * a.n_kv * s.own_splits);
-  return launch_k(forms_kernel<false>(kind), dim3(s.prefix_splits, s.row_blocks, a.n_kv),
+  return launch_k(forms_kernel<MPrefix>(kind), dim3(s.prefix_splits, s.row_blocks, a.n_kv),
                   dim3(FORMS_THREADS), FORMS_SMEM, st, 0, *a.map_q, *a.map_k, *a.map_v, *a.map_k16,
                   *a.map_v16, p);
+}
+
+size_t tree_partial_bytes(int sm_count) {
+  return (size_t)2 * sm_count * 2 * TM * (128 + 2) * sizeof(float);
+}
+
+cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
+  if (a.head_dim != 128) return cudaErrorInvalidValue;
+  FormsParams p{};
+  p.n_q = a.n_q;
+  p.n_kv = a.n_kv;
+  p.G = a.n_q / a.n_kv;
+  const int kind = score_kind(a.sc, &p);
+  p.status = a.status;
+  p.out = (bf16*)a.out;
+  p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+  p.cu_rows = a.cu_rows;
+  p.n_rows = a.n_rows;
+  p.n_docs = a.B;
+  p.start_pos = a.start_pos;
+  p.row_pos = a.row_pos;
+  p.mask = a.mask;
+  p.mask_words = a.mask_words;
+  p.page_table = a.page_table;
+  p.layer = a.layer;
+  p.page_size = a.page_size;
+  p.capacity = a.capacity;
+  p.n_pages = a.n_pages;
+  p.max_pages = a.max_pages;
+  p.box_rows = a.box_rows;
+  p.key_limit = a.key_limit;
+  p.rows_seq = TM / p.G;
+  // both row tiles on the same rows where a sequence's fit into one, by the mean
+  p.alternate = (long long)a.n_rows <= (long long)a.B * p.rows_seq;
+  p.least_tiles = 1;
+  p.partials = (size_t)2 * a.sm_count * (p.alternate ? TM : 2 * TM);
+  p.part_o = a.partial;
+  p.part_ml = a.partial + p.partials * 128;
+  const int ctas = a.sm_count;
+  const cudaError_t e = launch_k(forms_kernel<MTree>(kind), dim3(ctas), dim3(FORMS_THREADS), FORMS_SMEM, st, 0,
+                                 *a.map_q, *a.map_k, *a.map_v, *a.map_k16, *a.map_v16, p);
+  if (e != cudaSuccess || ctas < 2) return e;
+  return launch_k(attn_tree_join_kernel, dim3(ctas - 1, (p.alternate ? TM : 2 * TM) / 16), dim3(128), 0, st, 0, p,
+                  ctas);
 }
 
 }  // namespace llgb

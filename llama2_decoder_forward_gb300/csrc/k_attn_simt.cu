@@ -58,7 +58,14 @@ struct SimtParams {
   // key weights: the scores [n_seq][n_kv][ld][G] and every row's maximum and sum, or null
   float *scores, *stats;
   int64_t ld;
+  // trees: out, cu_rows, n_rows, n_docs as documents, the cache as in decode
+  const int32_t *start_pos, *row_pos;
+  const uint32_t* mask;
+  int mask_words;
 };
+
+// What a launch works on: decode rows, documents, trees of drafted rows over a cache.
+enum { SDecode, SDocs, STree };
 
 // Work item -> (document, tile of `rows` query rows, first row, row count), for a
 // whole warp: 32 documents per step, their tile counts summed by a warp scan.
@@ -153,8 +160,9 @@ __device__ __forceinline__ void store_dims(float* row, int lane, int d, const fl
   }
 }
 
-template <int RW, int DM, bool DOCS>
+template <int RW, int DM, int MODE>
 __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
+  constexpr bool TREE = MODE == STree, DOCS = MODE == SDocs || TREE;  // DOCS: packed rows of one head
   grid_dep_wait();
   grid_dep_launch();
   using Tile = SimtTile<RW, DM>;
@@ -169,7 +177,7 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
   const int d = p.d;
   const int item = blockIdx.x / p.splits, part = blockIdx.x - item * p.splits;
   // which rows
-  int b, g, h0, lo = 0, n = 0, q0 = 0, rows, n_keys, pre = 0, pos = 0;
+  int b, g, h0, lo = 0, n = 0, q0 = 0, rows, n_keys, pre = 0, pos = 0, start = 0;
   if (DOCS) {
     const int h = item % p.n_q;
     int tile;
@@ -180,8 +188,16 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     q0 = tile * RT;
     rows = min(RT, n - q0);
     if (!bc_ok(lo + q0 + rows <= p.n_rows && h0 < p.n_q, p.status)) return;
-    pre = p.prefix_len ? min(max(p.prefix_len[b], 0), n) : 0;
-    n_keys = max(q0 + rows, pre);
+    if (TREE) {
+      start = p.start_pos[b];
+      const long long end = (long long)start + n;
+      if ((start < 0 || end > p.key_limit) && q0 == 0 && part == 0 && threadIdx.x == 0)
+        flag(p.status, LLAMA_FLAG_POS_RANGE);
+      n_keys = start < 0 ? 0 : (int)(end < p.key_limit ? end : p.key_limit);
+    } else {
+      pre = p.prefix_len ? min(max(p.prefix_len[b], 0), n) : 0;
+      n_keys = max(q0 + rows, pre);
+    }
   } else {
     const int c = item % p.row_chunks;
     g = (item / p.row_chunks) % p.n_kv;
@@ -205,7 +221,7 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
       const int j = i / (DM / 4), x = 4 * (i % (DM / 4));
       long long off = -1;
       if (k0 + j < n_keys && x < d)
-        off = DOCS ? ((long long)(lo + k0 + j) * p.n_kv + g) * d : key_offset(p, b, g, k0 + j);
+        off = MODE == SDocs ? ((long long)(lo + k0 + j) * p.n_kv + g) * d : key_offset(p, b, g, k0 + j);
       copy16(sk + j * LD + x, off < 0 ? p.k : p.k + off + x, off >= 0);
       copy16(sv + j * LD + x, off < 0 ? p.v : p.v + off + x, off >= 0);
     }
@@ -252,14 +268,28 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     }
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-      const int qi = DOCS ? q0 + r0 + i : pos;
+      // the row's index, and (trees: for the bias alone) its position
+      const int ri = q0 + r0 + i;
+      int qi = DOCS ? ri : pos;
+      if (TREE && p.sc.slopes && r0 + i < rows)
+        qi = p.row_pos ? min(max(p.row_pos[lo + ri], 0), kMaxPos) : start + ri;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int key = k0 + lane + 32 * j;
         float v = s[i][j] * p.sc.scale;
         if (p.sc.cap > 0.f) v = p.sc.cap * tanhf(v * icap);
-        if (p.sc.slopes) v -= slope[i] * fabsf((float)(qi - key));
-        const bool keep = key < n_keys && (!DOCS || key <= qi || key < pre);
+        const int x = key - start;  // trees: the key's row
+        if (p.sc.slopes) {
+          int at = key;
+          if (TREE && p.row_pos && x >= 0 && key < n_keys) at = min(max(p.row_pos[lo + x], 0), kMaxPos);
+          v -= slope[i] * fabsf((float)(qi - at));
+        }
+        bool keep = key < n_keys;
+        if (MODE == SDocs) keep = keep && (key <= qi || key < pre);
+        if (TREE && keep && x >= 0)
+          keep = r0 + i < rows && (p.mask ? x < 32 * p.mask_words &&
+                                                (p.mask[(size_t)(lo + ri) * p.mask_words + (x >> 5)] >> (x & 31) & 1u)
+                                          : x <= ri);
         if (!DOCS && p.scores && keep && r0 + i < rows)
           p.scores[(((size_t)b * p.n_kv + g) * p.ld + key) * p.G + (h0 - g * p.G) + r0 + i] = v;
         s[i][j] = keep ? v : -INFINITY;
@@ -352,29 +382,29 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
     if (r >= rows || (p.splits > 1 && r % p.splits != part)) continue;
     float w[DL];
 #pragma unroll
-    for (int x = 0; x < DL; ++x) w[x] = n_keys > 0 ? o[i][x] / l[i] : 0.f;
+    for (int x = 0; x < DL; ++x) w[x] = n_keys > 0 && (!TREE || l[i] != 0.f) ? o[i][x] / l[i] : 0.f;
     store_dims<DL>(p.out + row_off(r), lane, d, w);
     if (!DOCS && p.stats && lane == 0)
       *reinterpret_cast<float2*>(p.stats + 2 * ((size_t)b * p.n_q + h0 + r)) = make_float2(merge_max(m[i], l[i]), l[i]);
   }
 }
 
-template <int RW, int DM, bool DOCS>
+template <int RW, int DM, int MODE>
 cudaError_t prep() {
-  return cudaFuncSetAttribute(attn_simt_kernel<RW, DM, DOCS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(attn_simt_kernel<RW, DM, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)SimtTile<RW, DM>::bytes);
 }
 
-template <int RW, bool DOCS>
+template <int RW, int MODE>
 cudaError_t run(const SimtParams& p, long long items, cudaStream_t st) {
   const dim3 grid((unsigned)(items * p.splits)), cluster(p.splits > 1 ? p.splits : 0, 1, 1);
   if (p.d <= 64)
-    return launch_kc(attn_simt_kernel<RW, 64, DOCS>, grid, dim3(S_THREADS), SimtTile<RW, 64>::bytes,
+    return launch_kc(attn_simt_kernel<RW, 64, MODE>, grid, dim3(S_THREADS), SimtTile<RW, 64>::bytes,
                      st, cluster, p);
   if (p.d <= 128)
-    return launch_kc(attn_simt_kernel<RW, 128, DOCS>, grid, dim3(S_THREADS), SimtTile<RW, 128>::bytes,
+    return launch_kc(attn_simt_kernel<RW, 128, MODE>, grid, dim3(S_THREADS), SimtTile<RW, 128>::bytes,
                      st, cluster, p);
-  return launch_kc(attn_simt_kernel<RW, 256, DOCS>, grid, dim3(S_THREADS), SimtTile<RW, 256>::bytes,
+  return launch_kc(attn_simt_kernel<RW, 256, MODE>, grid, dim3(S_THREADS), SimtTile<RW, 256>::bytes,
                    st, cluster, p);
 }
 
@@ -390,8 +420,9 @@ int simt_splits(long long items, int keys, int sm_count) {
 }  // namespace
 
 cudaError_t attn_simt_prepare() {
-  cudaError_t (*const all[])() = {prep<4, 64, true>,  prep<4, 128, true>,  prep<4, 256, true>,
-                                  prep<2, 64, false>, prep<2, 128, false>, prep<2, 256, false>};
+  cudaError_t (*const all[])() = {prep<4, 64, SDocs>,   prep<4, 128, SDocs>,   prep<4, 256, SDocs>,
+                                  prep<2, 64, SDecode>, prep<2, 128, SDecode>, prep<2, 256, SDecode>,
+                                  prep<4, 64, STree>,   prep<4, 128, STree>,   prep<4, 256, STree>};
   for (auto f : all) {
     const cudaError_t e = f();
     if (e != cudaSuccess) return e;
@@ -417,7 +448,7 @@ cudaError_t launch_docs_simt(const DocsArgs& a, cudaStream_t st) {
   p.n_docs = a.n_docs;
   const long long tiles = a.n_rows / 32 + std::min(a.n_docs, a.n_rows);  // an upper bound
   p.splits = simt_splits(tiles * a.n_q, a.n_rows, a.sm_count);
-  return run<4, true>(p, tiles * a.n_q, st);
+  return run<4, SDocs>(p, tiles * a.n_q, st);
 }
 
 cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st, const WeightsArgs* w) {
@@ -452,7 +483,39 @@ cudaError_t launch_shared_simt(const SharedArgs& a, cudaStream_t st, const Weigh
   p.row_chunks = (p.G + 15) / 16;
   const long long items = (long long)a.B * a.n_kv * p.row_chunks;
   p.splits = simt_splits(items, a.key_limit, a.sm_count);
-  return run<2, false>(p, items, st);
+  return run<2, SDecode>(p, items, st);
+}
+
+cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t st) {
+  SimtParams p{};
+  p.q = (const float*)a.q;
+  p.k = (const float*)a.k_cache;
+  p.v = (const float*)a.v_cache;
+  p.out = (float*)a.out;
+  p.n_q = a.n_q;
+  p.n_kv = a.n_kv;
+  p.G = a.n_q / a.n_kv;
+  p.d = a.head_dim;
+  p.sc = a.sc;
+  p.status = a.status;
+  p.cu_rows = a.cu_rows;
+  p.n_rows = a.n_rows;
+  p.n_docs = a.B;
+  p.start_pos = a.start_pos;
+  p.row_pos = a.row_pos;
+  p.mask = a.mask;
+  p.mask_words = a.mask_words;
+  p.page_table = a.page_table;
+  p.layer = a.layer;
+  p.page_size = a.page_size;
+  p.capacity = a.capacity;
+  p.batch_cap = a.batch_cap;
+  p.n_pages = a.n_pages;
+  p.max_pages = a.max_pages;
+  p.key_limit = a.key_limit;
+  const long long tiles = a.n_rows / 32 + std::min(a.B, a.n_rows);  // an upper bound
+  p.splits = simt_splits(tiles * a.n_q, a.key_limit, a.sm_count);
+  return run<4, STree>(p, tiles * a.n_q, st);
 }
 
 }  // namespace llgb

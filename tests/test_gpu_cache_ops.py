@@ -543,3 +543,224 @@ def test_weights_give_the_plain_decode_output():
     m.sync()
     # the same sums merged in another order: a rounding apart
     assert torch.all((outs[0].float() - outs[1].float()).abs() <= 2.0 ** -7 * outs[0].float().abs() + 2.0 ** -18)
+
+
+# --------------------------------------------------------------------------- trees
+def _random_tree(n, seed):
+    r = np.random.RandomState(seed)
+    return [-1] + [int(r.randint(max(0, i - 6), i)) for i in range(1, n)]
+
+
+def _tree_case(nq, nkv, d, dtype, starts, rows, *, page=16, cap=0.0, bias=False, scale=0.0, slopes=None, mask="tree",
+               words=None, lead=0, tail=0, layers=1, layer=0, seed=51, std=1.5, heads=None, slots=None, positions=True,
+               check=None):
+    """mask: "tree" (random parents), "chain" (none given), or "any" (random bits, some rows without any)."""
+    B, n = len(starts), lead + sum(rows) + tail
+    top = max(1, max(s + r for s, r in zip(starts, rows)))
+    slots = slots or top
+    m, shape = _model(nq, nkv, d, dtype, max_batch=B, max_seq=16, n_layers=layers)
+    dt = shape.torch_dtype
+    kv, k, v, pt = _filled(shape, B, slots, page, dt, seed, std, read=[s + r for s, r in zip(starts, rows)])
+    q = _randn((n, nq, d), dt, seed + 5, std)
+    cu = [lead]
+    for r in rows:
+        cu.append(cu[-1] + r)
+    words = words or max(1, -(-max(rows) // 32))
+    bits = np.full((n, words), -1, np.int32)  # rows of nobody: every bit
+    sees, at = [], torch.randint(0, 9, (n,), generator=_gen(seed + 7)).tolist()
+    r = np.random.RandomState(seed)
+    for b, (s, c) in enumerate(zip(starts, rows)):
+        if mask == "any":
+            see = r.rand(c, c) < 0.4
+            see[r.rand(c) < 0.3] = False
+        else:
+            parents = _random_tree(c, seed + b) if mask == "tree" else list(range(-1, c - 1))
+            see = C.tree_visible(parents)
+            for i in range(c):
+                at[cu[b] + i] = at[cu[b] + parents[i]] + 1 if parents[i] >= 0 else s
+        if c and mask != "chain":
+            wide = np.concatenate((see, r.rand(c, max(0, 32 * words - c)) < 0.5), 1)  # bits past the rows: anything
+            bits[cu[b]:cu[b] + c] = C.mask_words(wide, words)
+            see[:, 32 * words:] = False
+        sees.append(see)
+    sl = torch.tensor(slopes) if slopes is not None else _slopes(nq) if bias else None
+    out = torch.full((n, nq * d), 3.0, dtype=dt, device="cuda")
+    m.op_attention_tree(q.cuda(), _i32(cu), _i32(starts), layer, kv, out,
+                        mask=None if mask == "chain" else torch.from_numpy(bits).cuda(),
+                        positions=_i32(at) if positions else None,
+                        scores=binding.Scores(scale, cap, None if sl is None else sl.cuda()))
+    m.sync()
+    qf, got = f64(q), f64(out).reshape(n, nq, d)
+    sc = scale or 1 / math.sqrt(d)
+    for b, (s, c) in enumerate(zip(starts, rows)):
+        K, V = _keys_of(k, pt, page, layer, b, s + c), _keys_of(v, pt, page, layer, b, s + c)
+        lo = cu[b]
+        pos = np.array(at[lo:lo + c]) if positions else s + np.arange(c)
+        where = np.concatenate((np.arange(s), pos))
+        for i in range(c) if check is None else [x for x in check if x < c]:
+            keep = np.concatenate((np.ones(s, bool), sees[b][i]))
+            for h in range(nq) if heads is None else heads:
+                g, slope = h // (nq // nkv), 0.0 if sl is None else float(sl[h])
+                far = float(np.abs(slope) * np.abs(pos[i] - where).max()) if sl is not None else 0.0
+                e = _score_error(qf[lo + i, h], K[g], sc, cap, far)
+                ref, mass = C.attend(qf[lo + i, h], K[g], V[g], pos[i], where, keep, sc, cap, slope)
+                _within(got[lo + i, h], ref, _out_bound(ref, mass, dtype, e, s + c),
+                        "tree b=%d row=%d head=%d start=%d rows=%d" % (b, i, h, s, c))
+    outside = list(range(lead)) + list(range(cu[-1], n))
+    assert np.all(got[outside] == 3.0)
+    return got
+
+
+@pytest.mark.parametrize("nq,nkv", [(4, 4), (8, 1), (6, 2), (5, 5), (16, 1), (12, 1)])
+@pytest.mark.parametrize("opt", OPTS)
+@pytest.mark.parametrize("mask", ["tree", "any"])
+def test_tree_bf16(nq, nkv, opt, mask):
+    _tree_case(nq, nkv, 128, "bf16", [130, 0, 0, 57, 255], [9, 5, 0, 1, 12], mask=mask, lead=2, tail=3, **opt)
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 31, 32, 33, 63, 64, 65, 127, 128, 129, 130, 200, 300])
+@pytest.mark.parametrize("start", [0, 1, 100, 128, 250])
+def test_tree_rows_and_starts(n, start):
+    _tree_case(2, 1, 128, "bf16", [start], [n], mask="any", check=[0, 1, 14, 31, 32, 62, 64, 100, 127, 128, 199, 257, 299])
+
+
+@pytest.mark.parametrize("nq,nkv", [(2, 1), (8, 1)])
+@pytest.mark.parametrize("mask", ["tree", "chain"])
+def test_tree_mixed_batches(nq, nkv, mask):
+    # some sequences fill several blocks of rows, some one row; both row-tile forms
+    rows = [1, 130, 3, 0, 64, 17, 40]
+    _tree_case(nq, nkv, 128, "bf16", [200, 5, 0, 90, 300, 128, 127], rows, mask=mask, check=[0, 2, 16, 39, 63, 64, 129])
+    _tree_case(nq, nkv, 128, "bf16", [200, 5, 0, 90, 300, 128, 127], [1, 13, 3, 0, 6, 17, 4], mask=mask)
+
+
+@pytest.mark.parametrize("page", [0, 16, 64, 80])
+@pytest.mark.parametrize("slots", [None, 2000])
+def test_tree_caches(page, slots):
+    _tree_case(4, 2, 128, "bf16", [70, 500], [10, 7], page=page, slots=slots, layers=2, layer=1)
+
+
+@pytest.mark.parametrize("nq,nkv,starts,rows", [
+    (8, 1, [9000], [20]), (8, 8, [5000], [40]), (2, 2, [20000], [129]), (64, 8, [3000], [64]), (32, 32, [1000, 4000], [9, 5])])
+def test_tree_shared_chunks(nq, nkv, starts, rows):
+    # few items: their keys are cut over many CTAs and joined
+    _tree_case(nq, nkv, 128, "bf16", starts, rows, page=64, check=[0, 4, 8, 19, 63, 128], heads=[0, nq // 2, nq - 1])
+
+
+@pytest.mark.parametrize("B", [33, 90, 200])
+def test_tree_many_sequences(B):
+    r = np.random.RandomState(B)
+    _tree_case(2, 1, 128, "bf16", r.randint(0, 400, B).tolist(), r.randint(0, 8, B).tolist(), check=[0, 5])
+
+
+def test_tree_many_items_per_cta():
+    # more items than SMs, of odd tile counts: chunks begin and end anywhere
+    r = np.random.RandomState(3)
+    _tree_case(16, 16, 128, "bf16", r.randint(0, 700, 30).tolist(), [6] * 30, check=[0, 5], heads=[0, 7, 15])
+    _tree_case(16, 16, 128, "bf16", r.randint(0, 700, 20).tolist(), [150] * 20, check=[0, 149], heads=[0, 7, 15])
+
+
+@pytest.mark.parametrize("words", [1, 2, 7])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tree_mask_widths(words, dtype):
+    # words that do not reach all rows hide them; words past the rows count for nothing
+    _tree_case(2, 1, 128, dtype, [60, 3], [70, 20], mask="any", words=words)
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("slopes", [[4.0, 0.01], [-0.5, 3.0], [0.0, 100.0]])
+@pytest.mark.parametrize("positions", [True, False])
+def test_tree_slopes(cap, slopes, positions):
+    _tree_case(2, 1, 128, "bf16", [300, 40], [20, 9], cap=cap, slopes=slopes, positions=positions)
+
+
+@pytest.mark.parametrize("cap,scale", [(50.0, 0.0), (50.3, 0.0), (2.0, 0.5), (0.05, 1.0), (2000.0, 0.0), (300.0, 4.0)])
+def test_tree_caps(cap, scale):
+    _tree_case(4, 2, 128, "bf16", [200], [30], cap=cap, scale=scale, check=[0, 13, 29])
+
+
+def test_tree_large_scores():
+    _tree_case(2, 1, 128, "bf16", [260], [30], std=12.0, check=[0, 11, 29])
+
+
+@pytest.mark.parametrize("nq,nkv,d", [(4, 2, 64), (2, 2, 40), (20, 1, 128), (1, 1, 256), (3, 1, 8)])
+@pytest.mark.parametrize("opt", OPTS)
+@pytest.mark.parametrize("mask", ["tree", "any", "chain"])
+def test_tree_fp32(nq, nkv, d, opt, mask):
+    _tree_case(nq, nkv, d, "f32", [130, 0, 7, 64], [9, 40, 0, 1], mask=mask, page=5, lead=1, tail=2, **opt)
+
+
+def test_tree_fp32_shared_keys():
+    _tree_case(2, 1, 64, "f32", [3000], [40], page=0, check=[0, 39])
+
+
+def test_tree_output_aligned_to_16_bytes_only():
+    m, shape = _model(4, 2, max_batch=1)
+    kv, *_ = _filled(shape, 1, 300, 16, torch.bfloat16, 9)
+    q = _randn((9, 4, 128), torch.bfloat16, 10).cuda()
+    outs = [torch.empty(9 * 512 + 8, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for o, off in zip(outs, (0, 8)):
+        m.op_attention_tree(q, _i32([0, 9]), _i32([250]), 0, kv, o[off:off + 9 * 512])
+    m.sync()
+    assert torch.equal(outs[0][:9 * 512], outs[1][8:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("opt", OPTS)
+@pytest.mark.parametrize("slots", [1000, 200])
+def test_tree_nan_reaches_the_rows_that_see_it(dtype, opt, slots):
+    start = slots - 20
+    m, shape = _model(4, 2, 128, dtype, max_batch=2)
+    kv, k, v, pt = _filled(shape, 2, slots, 16, shape.torch_dtype, 12)
+    parents = _random_tree(20, 4)
+    see = C.tree_visible(parents)
+
+    def poison(t, b, slot, g):
+        t[0, int(pt[b, slot // 16]), g, slot % 16] = float("nan")
+    poison(kv.k, 0, start + 7, 1)    # a tree row's K: the rows that see it, heads of K/V head 1
+    poison(kv.k, 1, start // 2, 0)   # a cached key: every row of sequence 1, heads of K/V head 0
+    q = _randn((40, 4, 128), shape.torch_dtype, 13).cuda()
+    q[3, 0, 1] = float("nan")        # one query row and head
+    out = torch.empty(40, 512, dtype=shape.torch_dtype, device="cuda")
+    sl = _slopes(4).cuda() if opt.get("bias") else None
+    bits = torch.from_numpy(np.concatenate((C.mask_words(see), C.mask_words(see)))).cuda()
+    m.op_attention_tree(q, _i32([0, 20, 40]), _i32([start, start]), 0, kv, out, mask=bits,
+                        scores=binding.Scores(opt.get("scale", 0.0), opt.get("cap", 0.0), sl))
+    m.sync()
+    bad = torch.isnan(out.view(40, 4, 128)).cpu().numpy()
+    want = np.zeros((40, 4), bool)
+    want[:20, 2:] = see[:, 7:8]
+    want[20:, :2] = True
+    want[3, 0] = True
+    assert np.array_equal(bad.all(-1), want) and np.array_equal(bad.any(-1), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tree_bad_bounds_are_flagged(dtype):
+    m, shape = _model(4, 2, 128, dtype, max_batch=4)
+    dt = shape.torch_dtype
+    kv, k, v, pt = _filled(shape, 4, 64, 16, dt, 21)
+    q = _randn((12, 4, 128), dt, 22).cuda()
+
+    def call(cu, starts):
+        out = torch.full((12, 512), 3.0, dtype=dt, device="cuda")
+        m.op_attention_tree(q, _i32(cu), _i32(starts), 0, kv, out)
+        return m.sync_status(), out
+    (rc, flags), base = call([0, 3, 6, 9, 12], [10, 20, 30, 40])
+    assert rc == 0
+    # a negative start: zeros; past the cache: what is in it is attended; far past
+    (rc, flags), out = call([0, 3, 6, 9, 12], [-1, 62, 2 ** 31 - 2, 40])
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE
+    assert torch.all(out[:3] == 0) and torch.equal(out[9:], base[9:])
+    (_, _), all64 = call([0, 3, 6, 9, 12], [61, 61, 61, 61])
+    assert torch.isfinite(out.float()).all()
+    # sequence 2's rows, whose own slots are past the cache, attend all 64 cached slots: as row 8, the last, does there
+    assert torch.allclose(out[8].float(), all64[8].float(), rtol=2.0 ** -6, atol=1e-3)
+    # rows out of range, and decreasing
+    (rc, flags), out = call([0, 3, 6, 9, 40], [10, 20, 30, 40])
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE and torch.equal(out, base)
+    (rc, flags), out = call([0, 3, 2, 9, 12], [10, 20, 30, 40])  # (row 2 is sequence 0's and 2's)
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE and torch.equal(out[:2], base[:2]) and torch.equal(out[9:], base[9:])
+    kv.page_table[1, 0] = 99
+    (rc, flags), out = call([0, 3, 6, 9, 12], [10, 20, 30, 40])
+    assert rc == 5 and flags == binding.FLAG_PAGE_RANGE
+    assert torch.equal(out[:3], base[:3]) and torch.equal(out[6:], base[6:]) and torch.isfinite(out.float()).all()
