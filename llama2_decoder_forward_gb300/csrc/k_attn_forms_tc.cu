@@ -67,7 +67,7 @@ constexpr uint32_t OFF_BAR = SLOTS * TILE;
 // what the two threads of a row exchange: fp32 [2 row tiles][2 halves][128], the
 // tile's maxima, at the end the sums. One buffer is enough: a tile's maxima are
 // read before its P is announced, and the next tile's scores come after that.
-constexpr uint32_t OFF_WORK = OFF_BAR + 256;  // documents, trees: two published work items, up to 48 bytes each
+constexpr uint32_t OFF_WORK = OFF_BAR + 256;  // documents, trees: two published work items, up to 48 bytes each; a barrier
 constexpr uint32_t OFF_X = OFF_WORK + 128;
 constexpr size_t FORMS_SMEM = OFF_X + 2 * 2 * 128 * 4;
 constexpr int FORMS_THREADS = 640;
@@ -168,12 +168,6 @@ struct Ring {
     slot += k;
     if (slot >= n) {
       slot -= n;
-      phase ^= 1;
-    }
-  }
-  __device__ __forceinline__ void back() {
-    if (--slot < 0) {
-      slot += n;
       phase ^= 1;
     }
   }
@@ -567,10 +561,6 @@ __device__ __forceinline__ uint32_t tree_bits(const FormsParams& p, size_t row, 
   return s ? __funnelshift_r(a, tree_word(p, row, i, there, j + 1), s) : a;
 }
 
-__device__ __forceinline__ void softmax_bar() {  // the 16 softmax warps
-  asm volatile("bar.sync 9, 512;" ::: "memory");
-}
-
 // 32 outputs of a row, times inv, as bf16
 __device__ __forceinline__ void store_out(const FormsParams& p, bf16* dst, const float* u, float inv) {
 #pragma unroll
@@ -592,7 +582,17 @@ __device__ __forceinline__ void store_out(const FormsParams& p, bf16* dst, const
 // 32 of its 128 dims from both. Every softmax thread calls this.
 __device__ __forceinline__ void tree_store(const FormsParams& p, const FormsWork& w, bool alt, int t, int grp, int r,
                                            uint32_t tl, bool row_ok, size_t row, int head, float m, float l,
-                                           int count, float* x, volatile uint32_t* stop) {
+                                           int count, float* x, uint64_t* meet, uint32_t& ph_meet,
+                                           volatile uint32_t* stop) {
+  // all 16 warps, by a wait that ends
+  auto softmax_bar = [&] {
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(meet);
+    wait_bar(meet, ph_meet, stop, p.status);
+    ph_meet ^= 1;
+    __syncwarp();
+  };
   m = count == 0 || l == 0.f ? -INFINITY : merge_max(m, l);
   float f0 = 1.f, f1 = 0.f;
   if (alt) {
@@ -677,6 +677,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   volatile uint32_t* stop = ctl + 1;
   static_assert((2 + 2 * MAXK + 2 * MAXV + 1 + 10 + 4) * 8 + 20 <= 256, "barrier block");
   volatile int4* box = reinterpret_cast<volatile int4*>(smem + OFF_WORK);
+  uint64_t* meet = reinterpret_cast<uint64_t*>(smem + OFF_WORK + 96);  // trees: the softmax warps
   grid_dep_wait();
   grid_dep_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -703,6 +704,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       mbar_init(&vempty[s], readers);
     }
     mbar_init(vland, 1);
+    mbar_init(meet, 16);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
       mbar_init(&pready[2 * t], 8);
@@ -764,6 +766,17 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     if (!ok || n == 0) return false;
     doc_work(p, lo, n, q0, pre, h0, g, w);
     return true;
+  };
+  // Trees with alternate row tiles: an item of an odd number of tiles gets an empty one,
+  // so that a slot's tiles are always the same row tile's. (Otherwise an issuer could
+  // wait for a slot's next phase before the other one's was over, and take the phase
+  // before, which has the same parity, for it.)
+  auto even_out = [&](Ring& r, uint64_t* empty, uint64_t* full, int& issued, bool& ok) {
+    ok = __all_sync(0xffffffffu, wait_bar(&empty[r.slot], r.phase ^ 1, stop, p.status));
+    if (!ok) return;
+    if (lane == 0) mbar_arrive(&full[r.slot]);
+    ++issued;
+    r.step();
   };
   if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -870,6 +883,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           ++issued;
           r.step();
         }
+        if (TREE && ok && alt && (w.n_tiles & 1)) even_out(r, kempty, kfull, issued, ok);
       }
       // no copy in flight when the CTA exits
       if (loaded_q) mbar_wait(qfull, (loaded_q - 1) & 1, p.status);
@@ -910,6 +924,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           if (ok) ++issued;
           r.step();
         }
+        if (TREE && ok && alt && (w.n_tiles & 1)) even_out(r, vempty, vfull, issued, ok);
       }
       for (int j = max(0, issued - VR); j < issued; ++j)
         mbar_wait(&vfull[j % VR], (j / VR) & 1, p.status);
@@ -1030,14 +1045,16 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
             kr.step();
             vr.step();
           }
-        if (TREE && alt && (w.n_tiles & 1)) {  // the next item's tiles start at the next slot
-          if (t) {
-            kr.step();
-            vr.step();
-          } else {
-            kr.back();
-            vr.back();
+        if (TREE && alt && t && (w.n_tiles & 1)) {  // the empty tile that evens an odd item out
+          wait_bar(&kfull[kr.slot], kr.phase, stop, p.status);
+          wait_bar(&vfull[vr.slot], vr.phase, stop, p.status);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&kempty[kr.slot]);
+            mbar_arrive(&vempty[vr.slot]);
           }
+          kr.step(stride);
+          vr.step(stride);
         }
         theirs += others;
       }
@@ -1063,7 +1080,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     const float cl = p.cap * kLog2e, yk = CAP ? p.scale / p.cap : 0.f;
     const float ct = KIND == KCap ? cl : c;  // log2 units of a raw score (of tanh)
     FormsWork w{};
-    uint32_t ph_s = 0, ph_fin = 0;  // phases of sfull, fin
+    uint32_t ph_s = 0, ph_fin = 0, ph_meet = 0;  // phases of sfull, fin, meet
 #pragma unroll 1
     for (int it = 0; work(it, w); ++it) {
     const int count = t ? w.nt1 : w.nt0;
@@ -1297,7 +1314,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     l = xch[0] + xch[128];
     half_bar(bar_id);  // both have read: the next item may write
     if (TREE) {
-      tree_store(p, w, alt, t, grp, r, tl, row_ok, row, head, m, l, count, reinterpret_cast<float*>(smem + OFF_X), stop);
+      tree_store(p, w, alt, t, grp, r, tl, row_ok, row, head, m, l, count,
+                 reinterpret_cast<float*>(smem + OFF_X), meet, ph_meet, stop);
     } else if (!__any_sync(0xffffffffu, *stop)) {
       tc_fence_after();
       if (DOCS) {

@@ -553,7 +553,7 @@ def _random_tree(n, seed):
 
 def _tree_case(nq, nkv, d, dtype, starts, rows, *, page=16, cap=0.0, bias=False, scale=0.0, slopes=None, mask="tree",
                words=None, lead=0, tail=0, layers=1, layer=0, seed=51, std=1.5, heads=None, slots=None, positions=True,
-               check=None):
+               check=None, calls=1):
     """mask: "tree" (random parents), "chain" (none given), or "any" (random bits, some rows without any)."""
     B, n = len(starts), lead + sum(rows) + tail
     top = max(1, max(s + r for s, r in zip(starts, rows)))
@@ -585,10 +585,11 @@ def _tree_case(nq, nkv, d, dtype, starts, rows, *, page=16, cap=0.0, bias=False,
         sees.append(see)
     sl = torch.tensor(slopes) if slopes is not None else _slopes(nq) if bias else None
     out = torch.full((n, nq * d), 3.0, dtype=dt, device="cuda")
-    m.op_attention_tree(q.cuda(), _i32(cu), _i32(starts), layer, kv, out,
-                        mask=None if mask == "chain" else torch.from_numpy(bits).cuda(),
-                        positions=_i32(at) if positions else None,
-                        scores=binding.Scores(scale, cap, None if sl is None else sl.cuda()))
+    args = (q.cuda(), _i32(cu), _i32(starts), layer, kv, out)
+    kw = dict(mask=None if mask == "chain" else torch.from_numpy(bits).cuda(), positions=_i32(at) if positions else None,
+              scores=binding.Scores(scale, cap, None if sl is None else sl.cuda()))
+    for _ in range(calls):
+        m.op_attention_tree(*args, **kw)
     m.sync()
     qf, got = f64(q), f64(out).reshape(n, nq, d)
     sc = scale or 1 / math.sqrt(d)
@@ -657,6 +658,14 @@ def test_tree_many_items_per_cta():
     r = np.random.RandomState(3)
     _tree_case(16, 16, 128, "bf16", r.randint(0, 700, 30).tolist(), [6] * 30, check=[0, 5], heads=[0, 7, 15])
     _tree_case(16, 16, 128, "bf16", r.randint(0, 700, 20).tolist(), [150] * 20, check=[0, 149], heads=[0, 7, 15])
+
+
+@pytest.mark.parametrize("rows", [9, 140])
+def test_tree_long_items_per_cta(rows):
+    # a CTA walks several items of many tiles, odd and even counts, and calls follow at once
+    r = np.random.RandomState(rows)
+    _tree_case(32, 32, 128, "bf16", r.randint(1, 4000, 12).tolist(), r.randint(1, rows + 1, 12).tolist(), check=[0, 5, 131],
+               heads=[0, 13, 31], calls=6)
 
 
 @pytest.mark.parametrize("words", [1, 2, 7])
