@@ -1600,10 +1600,10 @@ int llama_op_cache_commit(llama_ctx* c, const llama_kv* kv, int32_t layer, const
   a.path = path;
   a.start = start_pos;
   a.count = path_len;
-  if (!move_fits(a)) return LLAMA_ERR_OUT_OF_RANGE;
+  if (B > 65535 || a.layers > 65535) return LLAMA_ERR_OUT_OF_RANGE;
   Prof pf(c, LLAMA_KERNEL_ROPE_APPEND);
   c->launches++;
-  return cuda_rc(launch_cache_move(a, c->stream));
+  return cuda_rc(launch_cache_commit(a, c->stream));
 }
 
 int llama_op_cache_evict(llama_ctx* c, const llama_kv* kv, int32_t layer, const int32_t* lens, int32_t B,
@@ -1636,10 +1636,11 @@ int llama_op_cache_evict(llama_ctx* c, const llama_kv* kv, int32_t layer, const 
   e.recent = recent;
   e.limit = a.limit;
   e.status = c->status;
+  e.sm_count = c->sm_count;
   Prof pf(c, LLAMA_KERNEL_ROPE_APPEND);
   c->launches += 2;
   TRY(cuda_rc(launch_evict_select(e, c->stream)));
-  return cuda_rc(launch_cache_move(a, c->stream));
+  return cuda_rc(launch_cache_evict(a, c->stream));
 }
 
 int llama_op_argmax(llama_ctx* c, const float* logits, int32_t B, int32_t V, int32_t* ids) {

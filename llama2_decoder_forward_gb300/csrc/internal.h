@@ -342,7 +342,7 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
 // Decode attention that adds up its keys' weights: the own keys of a batch without a
 // prefix, their scores kept, then the joining kernel.
 struct WeightsArgs {
-  float* scores;         // [B][n_kv][ld][G]
+  float* scores;         // [B][n_q][ld]
   float* weights;        // [B][n_kv][ld]
   int64_t ld;
   float* stats;          // fp32 models: [B n_q][2], maximum and sum of a row
@@ -372,7 +372,8 @@ struct CacheMoveArgs {
   // evict: slot kept[layer][b][g][i] to i, where lens[b] is above list_ld
   const int32_t *kept = nullptr, *lens = nullptr;
 };
-cudaError_t launch_cache_move(const CacheMoveArgs& a, cudaStream_t st);
+cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t st);
+cudaError_t launch_cache_evict(const CacheMoveArgs& a, cudaStream_t st);
 struct EvictArgs {
   const float* weights;        // [layers][B][n_kv][ld]
   float* weights_out;
@@ -381,6 +382,7 @@ struct EvictArgs {
   int64_t ld;
   int layers, B, n_kv, keep, first, recent, limit;
   uint32_t* status;
+  int sm_count;
 };
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
 

@@ -76,6 +76,12 @@ constexpr uint32_t O_COL = 256;             // S tiles at columns 0 and 128, O t
 constexpr float kLazy = 8.f;
 static_assert(FORMS_SMEM <= 232448, "227 KB of shared memory per CTA");
 
+// A tree item that several CTAs share: its block of rows, and the number of its first
+// partial result (the others are those of the next CTAs).
+struct TreeShared {
+  int lo, n, q0, g, first;
+};
+
 struct FormsParams {
   int n_q, n_kv, G;
   float scale, cap;
@@ -103,6 +109,8 @@ struct FormsParams {
   const int32_t *start_pos, *row_pos;
   const uint32_t* mask;
   int mask_words, least_tiles;
+  struct TreeShared* shared;                // [CTAs] the item that each CTA begins and does not end,
+  int* shared_parts;                        // and how many partial results it has (0: no such item)
   float poly[13];                           // KCapFixed: kTanh times powers of scale / cap
 };
 
@@ -461,12 +469,15 @@ __device__ __forceinline__ int prefix_share(const FormsParams& p, int lane) {
 }
 
 // Trees. An item is a block of a sequence's rows (one or two row tiles) and a K/V
-// head; it has T key tiles. All items' tiles, in one line (sequence, head, block, tile),
+// head; it has T key tiles. All items' tiles, in one line (block, sequence, head, tile),
 // are cut into equal chunks, one per CTA, so that every SM gets the same number of
-// tiles whatever the lengths. A CTA's first and last item may be shared with its
-// neighbours: those leave partial results (CTA c: 2c for its first item, 2c + 1 for its
-// last), which the joining kernel merges; items within a chunk are stored at once.
-struct TreeSeq {   // a sequence's rows, its keys, and the tiles of all its items
+// tiles whatever the lengths. The blocks come first so that those of the same keys are
+// worked on at the same time, by CTAs far apart in the line, and read the keys from L2
+// but once (32 sequences of up to 8192 keys, two blocks of 256 rows each: XXX).
+// A CTA's first and last item may be shared with its neighbours: those leave partial
+// results (CTA c: 2c for its first item, 2c + 1 for its last), which the joining kernel
+// merges; items within a chunk are stored at once.
+struct TreeSeq {   // a sequence's rows, its keys, and the tiles of a block's items
   int lo, n, start, keys, T, blocks;
   long long tiles;
 };
@@ -481,7 +492,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const FormsParams& p, int b, uint32_
   const int rows = p.alternate ? p.rows_seq : 2 * p.rows_seq;
   s.T = max(1, (s.keys + TN - 1) / TN);  // one, to store the rows of a sequence without keys
   s.blocks = (s.n + rows - 1) / rows;
-  s.tiles = (long long)s.blocks * p.n_kv * s.T;
+  s.tiles = (long long)p.n_kv * s.T;
   return s;
 }
 // Sum of x over the lanes up to each one.
@@ -497,7 +508,10 @@ __device__ __forceinline__ long long sum_upto(long long x, int lane) {
 __device__ __forceinline__ long long tree_chunk(const FormsParams& p, int ctas, int lane, uint32_t* status,
                                                 long long* total) {
   long long all = 0;
-  for (int b = lane; b < p.n_docs; b += 32) all += tree_seq(p, b, status).tiles;
+  for (int b = lane; b < p.n_docs; b += 32) {
+    const TreeSeq s = tree_seq(p, b, status);
+    all += s.blocks * s.tiles;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   *total = all;
@@ -505,38 +519,41 @@ __device__ __forceinline__ long long tree_chunk(const FormsParams& p, int ctas, 
 }
 // The item that tile u belongs to, for a whole warp whose questions ascend.
 struct TreeCursor {
-  int b0 = 0;
-  long long before = 0;  // tiles of the sequences before b0
+  int block = 0, b0 = 0;
+  long long before = 0, start = 0;  // tiles in front of b0, of the block
 };
 struct TreeItem {
   int b, g, block, lo, n, start, keys, T;
   long long first;       // its first tile
 };
 __device__ __forceinline__ bool tree_item(const FormsParams& p, long long u, TreeCursor& c, int lane, TreeItem& it) {
-  for (; c.b0 < p.n_docs; c.b0 += 32) {
-    TreeSeq s{};
-    if (c.b0 + lane < p.n_docs) s = tree_seq(p, c.b0 + lane, nullptr);
-    const long long upto = c.before + sum_upto(s.tiles, lane);
-    const uint32_t m = __ballot_sync(0xffffffffu, u < upto);
-    if (m) {
-      const int w = __ffs(m) - 1;
-      it.b = c.b0 + w;
-      it.lo = __shfl_sync(0xffffffffu, s.lo, w);
-      it.n = __shfl_sync(0xffffffffu, s.n, w);
-      it.start = __shfl_sync(0xffffffffu, s.start, w);
-      it.keys = __shfl_sync(0xffffffffu, s.keys, w);
-      it.T = __shfl_sync(0xffffffffu, s.T, w);
-      const int blocks = __shfl_sync(0xffffffffu, s.blocks, w);
-      const long long base = __shfl_sync(0xffffffffu, upto - s.tiles, w);
-      const int item = (int)((u - base) / it.T);
-      it.first = base + (long long)item * it.T;
-      it.g = item / blocks;
-      it.block = item - it.g * blocks;
-      return true;
+  for (;;) {
+    for (; c.b0 < p.n_docs; c.b0 += 32) {
+      TreeSeq s{};
+      if (c.b0 + lane < p.n_docs) s = tree_seq(p, c.b0 + lane, nullptr);
+      const long long mine = s.blocks > c.block ? s.tiles : 0, upto = c.before + sum_upto(mine, lane);
+      const uint32_t m = __ballot_sync(0xffffffffu, u < upto);
+      if (m) {
+        const int w = __ffs(m) - 1;
+        it.b = c.b0 + w;
+        it.block = c.block;
+        it.lo = __shfl_sync(0xffffffffu, s.lo, w);
+        it.n = __shfl_sync(0xffffffffu, s.n, w);
+        it.start = __shfl_sync(0xffffffffu, s.start, w);
+        it.keys = __shfl_sync(0xffffffffu, s.keys, w);
+        it.T = __shfl_sync(0xffffffffu, s.T, w);
+        const long long base = __shfl_sync(0xffffffffu, upto - mine, w);
+        it.g = (int)((u - base) / it.T);
+        it.first = base + (long long)it.g * it.T;
+        return true;
+      }
+      c.before = __shfl_sync(0xffffffffu, upto, 31);
     }
-    c.before = __shfl_sync(0xffffffffu, upto, 31);
+    if (c.before == c.start) return false;  // no sequence has so many blocks
+    c.start = c.before;
+    ++c.block;
+    c.b0 = 0;
   }
-  return false;
 }
 // What follows from an item's published part.
 __device__ __forceinline__ void tree_work(const FormsParams& p, FormsWork& w) {
@@ -681,6 +698,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   grid_dep_wait();
   grid_dep_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (TREE && threadIdx.x == 0) p.shared_parts[blockIdx.x] = 0;
   if ((smem_u32(smem) & 1023u) != 0 ||  // the swizzled tiles need 1024-byte alignment
       !bc_smem(smem, FORMS_SMEM, 1024, threadIdx.x == 0 ? p.status : nullptr)) {
     if (threadIdx.x == 0) flag(p.status, LLAMA_FLAG_INDEX);
@@ -727,6 +745,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         *p.used = used;
     }
   }
+  long long chunk = 0, total = 0;  // trees: tiles of a CTA, of all
+  if (TREE && warp == 16) chunk = tree_chunk(p, gridDim.x, lane, blockIdx.x == 0 ? p.status : nullptr, &total);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -791,13 +811,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       bool ok = true;
       DocCursor cursor;
       TreeCursor where;
-      long long u = 0, u_end = 0;  // trees: what is left of this CTA's chunk
-      if (TREE) {
-        long long total;
-        const long long chunk = tree_chunk(p, gridDim.x, lane, blockIdx.x == 0 ? p.status : nullptr, &total);
-        u = min(total, chunk * blockIdx.x);
-        u_end = min(total, u + chunk);
-      }
+      long long u = min(total, chunk * blockIdx.x);  // trees: what is left of this CTA's chunk
+      const long long u_end = min(total, u + chunk);
       for (int it = 0; ok; ++it) {
         if (TREE) {
           TreeItem item{};
@@ -815,6 +830,11 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
             w.kmax = item.keys;
             tree_work(p, w);
             u += w.n_tiles;
+            if (w.split >= 0 && w.t0 == 0 && lane == 0) {
+              const int last = (int)((item.first + item.T - 1) / chunk);
+              p.shared[blockIdx.x] = TreeShared{w.lo, w.n, w.q0, w.g, w.split};
+              p.shared_parts[blockIdx.x] = last - (int)blockIdx.x + 1;
+            }
           }
           ok = __all_sync(0xffffffffu, wait_bar(&wempty[it & 1], ((it >> 1) & 1) ^ 1, stop, p.status));
           if (!ok) break;
@@ -1115,9 +1135,19 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     }
     const float sl = BIAS && p.slopes && row_ok ? p.slopes[head] * kLog2e : 0.f;
     float m = KIND == KCapFixed ? 0.f : -INFINITY, l = 0.f;
+    const bool idle = TREE && !__any_sync(0xffffffffu, row_ok);  // rows that nobody has: P may be anything
     for (int j = 0; j < count; ++j) {
       wait_bar(&sfull[t], ph_s, stop, p.status);
       ph_s ^= 1;
+      if (idle) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&pready[2 * t]);
+          mbar_arrive(&pready[2 * t + 1]);
+        }
+        continue;
+      }
       tc_fence_after();
       const int k0 = (w.t0 + (alt ? 2 * j + t : j)) * TN + NK * grp;  // this thread's first key
       const int left = lim - k0;                                    // visible keys (over NK: all)
@@ -1390,58 +1420,80 @@ FormsKernel forms_kernel(int kind) {
   }
 }
 
-// Merges the partial results of tree items that several chunks share. Block (c, y): the
-// item that chunk c + 1 starts within, if that is the item's first such chunk; its
-// rows 16 y .. 16 y + 15, a warp for every four.
-__global__ void __launch_bounds__(128) attn_tree_join_kernel(FormsParams p, int ctas) {
+// Merges the partial results of the tree items that several CTAs share: a warp per row at
+// a time. Every block makes the list of those items, so that no block is without work.
+constexpr int JOIN_WARPS = 8, JOIN_AHEAD = 8;
+__global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(FormsParams p, int ctas) {
   grid_dep_wait();
   grid_dep_launch();
+  extern __shared__ int2 items[];  // [ctas] CTA that begins the item, its partial results
+  __shared__ int n_items;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long total;
-  const long long chunk = tree_chunk(p, ctas, lane, nullptr, &total), u = chunk * (blockIdx.x + 1);
-  if (u >= total) return;
-  TreeCursor where;
-  TreeItem it;
-  if (!tree_item(p, u, where, lane, it) || it.first == u || u - it.first > chunk) return;
-  const int c0 = blockIdx.x;  // the chunk that the item starts in
-  const int parts = (int)((it.first + it.T - 1) / chunk) - c0 + 1;
+  if (warp == 0) {
+    int n = 0;
+    for (int c0 = 0; c0 < ctas; c0 += 32) {
+      const int parts = c0 + lane < ctas ? p.shared_parts[c0 + lane] : 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, parts > 0);
+      if (parts > 0) items[n + __popc(m & ((1u << lane) - 1u))] = make_int2(c0 + lane, parts);
+      n += __popc(m);
+    }
+    if (lane == 0) n_items = n;
+  }
+  __syncthreads();
   const int rows_tile = p.rows_seq * p.G, rows_slot = p.alternate ? TM : 2 * TM;
-  const int q0 = it.block * (p.alternate ? p.rows_seq : 2 * p.rows_seq);
-  const bool first = it.first == chunk * c0;
-  for (int k = 0; k < 4; ++k) {
-    const int r = blockIdx.y * 16 + warp * 4 + k, tile = r / TM, rt = r - tile * TM;
-    const int i = q0 + tile * p.rows_seq + rt / p.G;
-    if (r >= rows_slot || rt >= rows_tile || i >= it.n) continue;
-    auto at = [&](int s) {  // partial s of the row
-      return (size_t)(2 * (c0 + s) + (s == 0 && !first)) * rows_slot + r;
-    };
-    if (!bc_ok(at(parts - 1) < p.partials, p.status)) return;
+  for (int task = blockIdx.x * JOIN_WARPS + warp; task < n_items * rows_slot; task += gridDim.x * JOIN_WARPS) {
+    const int2 which = items[task / rows_slot];
+    const int r = task % rows_slot, tile = r / TM, rt = r - tile * TM, parts = which.y;
+    const TreeShared it = p.shared[which.x];
+    const int index = it.q0 + tile * p.rows_seq + rt / p.G;  // the row of the tree
+    if (rt >= rows_tile || index >= it.n ||
+        !bc_ok((size_t)2 * (which.x + parts) * rows_slot <= p.partials && it.lo + index < p.n_rows, p.status))
+      continue;
+    // partial s of the item
+    auto at = [&](int s) { return (size_t)(s == 0 ? it.first : 2 * (which.x + s)) * rows_slot + r; };
     float m = -INFINITY, l = 0.f;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_ml[2 * at(s)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < parts && m != -INFINITY; s0 += 32) {
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+      const int n = min(32, parts - s0);
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (s0 + lane < parts) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at(s0 + lane));
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-      if (f != 0.f) l = fmaf(ml.y, f, l);
-#pragma unroll 4
-      for (int s = 0; s < min(32, parts - s0); ++s) {
-        const float fs = __shfl_sync(0xffffffffu, f, s);
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + at(s0 + s) * 128 + 4 * lane);
-        if (fs != 0.f) {
-          v.x = fmaf(x.x, fs, v.x);
-          v.y = fmaf(x.y, fs, v.y);
-          v.z = fmaf(x.z, fs, v.z);
-          v.w = fmaf(x.w, fs, v.w);
+      if (lane < n) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at(s0 + lane));
+      float4 x[JOIN_AHEAD];
+      auto load = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < JOIN_AHEAD; ++i)
+          if (s + i < n) x[i] = *reinterpret_cast<const float4*>(p.part_o + at(s0 + s + i) * 128 + 4 * lane);
+      };
+      load(0);
+      float top = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mx = fmaxf(m, top), old = m == -INFINITY ? 0.f : exp2f(m - mx);
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mx);
+      float sum = f != 0.f ? ml.y * f : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l = (m == -INFINITY ? 0.f : l * old) + sum;
+      v.x *= old;
+      v.y *= old;
+      v.z *= old;
+      v.w *= old;
+      m = mx;
+      for (int s = 0; s < n; s += JOIN_AHEAD) {
+        if (s > 0) load(s);
+#pragma unroll
+        for (int i = 0; i < JOIN_AHEAD; ++i) {
+          const float fs = __shfl_sync(0xffffffffu, f, (s + i) & 31);
+          if (s + i < n && fs != 0.f) {  // a part without visible keys may hold anything
+            v.x = fmaf(x[i].x, fs, v.x);
+            v.y = fmaf(x[i].y, fs, v.y);
+            v.z = fmaf(x[i].z, fs, v.z);
+            v.w = fmaf(x[i].w, fs, v.w);
+          }
         }
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    bf16* dst = p.out + (((size_t)it.lo + i) * p.n_q + it.g * p.G + rt % p.G) * 128;
+    bf16* dst = p.out + (((size_t)it.lo + index) * p.n_q + it.g * p.G + rt % p.G) * 128;
     reinterpret_cast<uint2*>(dst)[lane] = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
   }
 }
@@ -1539,7 +1591,7 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
 }
 
 size_t tree_partial_bytes(int sm_count) {
-  return (size_t)2 * sm_count * 2 * TM * (128 + 2) * sizeof(float);
+  return (size_t)2 * sm_count * 2 * TM * (128 + 2) * sizeof(float) + sm_count * (sizeof(TreeShared) + sizeof(int));
 }
 
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
@@ -1574,12 +1626,13 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
   p.partials = (size_t)2 * a.sm_count * (p.alternate ? TM : 2 * TM);
   p.part_o = a.partial;
   p.part_ml = a.partial + p.partials * 128;
+  p.shared = reinterpret_cast<TreeShared*>(a.partial + p.partials * 130);
+  p.shared_parts = reinterpret_cast<int*>(p.shared + a.sm_count);
   const int ctas = a.sm_count;
   const cudaError_t e = launch_k(forms_kernel<MTree>(kind), dim3(ctas), dim3(FORMS_THREADS), FORMS_SMEM, st, 0,
                                  *a.map_q, *a.map_k, *a.map_v, *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess || ctas < 2) return e;
-  return launch_k(attn_tree_join_kernel, dim3(ctas - 1, (p.alternate ? TM : 2 * TM) / 16), dim3(128), 0, st, 0, p,
-                  ctas);
+  return launch_k(attn_tree_join_kernel, dim3(4 * ctas), dim3(32 * JOIN_WARPS), ctas * sizeof(int2), st, 0, p, ctas);
 }
 
 }  // namespace llgb

@@ -79,7 +79,7 @@ struct OwnParams {
   size_t rows, own_room;       // B n_q; partials behind the prefix's
   float scale, cap;
   const float* slopes;
-  // key weights: every score (log2 units), [B][n_kv][ld][G], for the joining kernel
+  // key weights: every score (log2 units), [B][n_q][ld], for the joining kernel
   float* scores;
   float* weights;              // [B][n_kv][ld]
   int64_t ld;
@@ -203,7 +203,7 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
         if (p.slopes) x = fmaf(-sl[i & 1], (float)(pos - k0 - key), x);
         sv[i] = key >= lead && key < valid ? x : -INFINITY;
         if (WEIGH && key < valid && hc + (i & 1) < G)
-          p.scores[(((size_t)b * p.n_kv + g) * p.ld + k0 + key) * G + hc + (i & 1)] = x;
+          p.scores[((size_t)b * p.n_q + g * G + hc + (i & 1)) * p.ld + k0 + key] = x;
       }
       float corr[2];
 #pragma unroll
@@ -340,7 +340,7 @@ __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem,
           if (p.slopes) x = fmaf(-sl[i >> 1], (float)(pos - k0 - key), x);
           sv[nb][i] = key >= lead && key < valid ? x : -INFINITY;
           if (WEIGH && key < valid && r0 + 8 * (i >> 1) < G)
-            p.scores[(((size_t)b * p.n_kv + g) * p.ld + k0 + key) * G + r0 + 8 * (i >> 1)] = x;
+            p.scores[((size_t)b * p.n_q + g * G + r0 + 8 * (i >> 1)) * p.ld + k0 + key] = x;
           mx[i >> 1] = fmaxf(mx[i >> 1], sv[nb][i]);
         }
 #pragma unroll
@@ -735,8 +735,10 @@ __global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int 
 // (sequence, K/V head) what the group's heads gave it,
 //   weights[key] += sum over heads of 2^(score - max) / sum,
 // each key by one thread and its heads in order. NAT: scores in natural units,
-// one part per row, whose output is there already (fp32 models).
-constexpr int WEIGH_THREADS = 256;
+// one part per row, whose output is there already (fp32 models). A thread takes 4
+// keys at a time, a block's width apart (rows of any stride are read whole lines at a
+// time), and 4 heads; the first ones are loaded before the maxima and sums.
+constexpr int WEIGH_THREADS = 256, WEIGH_KEYS = 4, WEIGH_HEADS = 4;
 template <bool NAT>
 __global__ void __launch_bounds__(WEIGH_THREADS) attn_weights_kernel(OwnParams p) {
   grid_dep_wait();
@@ -753,7 +755,23 @@ __global__ void __launch_bounds__(WEIGH_THREADS) attn_weights_kernel(OwnParams p
   if (!bc_ok(used <= p.splits && n <= p.ld, p.status)) return;
   const size_t row0 = (size_t)b * p.n_q + (size_t)g * G;
   float* w = p.weights + ((size_t)b * p.n_kv + g) * p.ld;
-  const float* sc = p.scores + ((size_t)b * p.n_kv + g) * p.ld * G;
+  const float* sc = p.scores + row0 * p.ld;
+  int i = blockIdx.x * (WEIGH_THREADS * WEIGH_KEYS) + threadIdx.x;
+  float old[WEIGH_KEYS], x[WEIGH_HEADS][WEIGH_KEYS];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int k = 0; k < WEIGH_HEADS; ++k)
+#pragma unroll
+      for (int q = 0; q < WEIGH_KEYS; ++q)
+        if (r0 + k < G && i + q * WEIGH_THREADS < n) x[k][q] = sc[(size_t)(r0 + k) * p.ld + i + q * WEIGH_THREADS];
+  };
+  auto load_old = [&] {
+#pragma unroll
+    for (int q = 0; q < WEIGH_KEYS; ++q)
+      if (i + q * WEIGH_THREADS < n) old[q] = w[i + q * WEIGH_THREADS];
+  };
+  load_old();
+  load(0);
   for (int r = warp; r < G; r += WEIGH_THREADS / 32) {
     const float2* ml = reinterpret_cast<const float2*>(p.own_ml) + (row0 + r) * p.splits;
     float m = -INFINITY, l = 0.f;
@@ -761,28 +779,45 @@ __global__ void __launch_bounds__(WEIGH_THREADS) attn_weights_kernel(OwnParams p
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     for (int s = lane; s < used; s += 32) {
-      const float2 x = ml[s];
-      if (x.x != -INFINITY) l = fmaf(x.y, NAT ? expf(x.x - m) : exp2f(x.x - m), l);
+      const float2 y = ml[s];
+      if (y.x != -INFINITY) l = fmaf(y.y, NAT ? expf(y.x - m) : exp2f(y.x - m), l);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) stat[r] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f || l != l ? 1.f / l : 0.f);
-    if (!NAT && r % gridDim.x == blockIdx.x) {  // the output rows are shared out over the chunks
-      Parts<8> own;
-      RowSum x;
-      own.load(p.own_o, p.own_ml, (row0 + r) * p.splits, p.splits, lane);
-      own.fold(used, lane, x);
-      store_row(p.out + (row0 + r) * HD, lane, x);
-    }
   }
   __syncthreads();
-  for (int i = blockIdx.x * WEIGH_THREADS + threadIdx.x; i < n; i += gridDim.x * WEIGH_THREADS) {
-    float sum = 0.f;
-    for (int r = 0; r < G; ++r) {
-      const float x = sc[(size_t)i * G + r] - stat[r].x;
-      sum = fmaf(NAT ? expf(x) : ex2(x), stat[r].y, sum);
+  for (bool first = true; i < n; i += gridDim.x * (WEIGH_THREADS * WEIGH_KEYS), first = false) {
+    if (!first) {
+      load_old();
+      load(0);
     }
-    w[i] += sum;
+    float sum[WEIGH_KEYS] = {};
+    for (int r0 = 0; r0 < G; r0 += WEIGH_HEADS) {
+      if (r0 > 0) load(r0);
+#pragma unroll
+      for (int k = 0; k < WEIGH_HEADS; ++k) {
+        if (r0 + k >= G) break;
+        const float2 st = stat[r0 + k];
+#pragma unroll
+        for (int q = 0; q < WEIGH_KEYS; ++q) {
+          const float y = x[k][q] - st.x;
+          sum[q] = fmaf(NAT ? expf(y) : ex2(y), st.y, sum[q]);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < WEIGH_KEYS; ++q)
+      if (i + q * WEIGH_THREADS < n) w[i + q * WEIGH_THREADS] = old[q] + sum[q];
+  }
+  if (NAT) return;
+  for (int r = warp; r < G; r += WEIGH_THREADS / 32) {
+    if (r % gridDim.x != blockIdx.x) continue;  // the output rows are shared out over the chunks
+    Parts<8> own;
+    RowSum row;
+    own.load(p.own_o, p.own_ml, (row0 + r) * p.splits, p.splits, lane);
+    own.fold(used, lane, row);
+    store_row(p.out + (row0 + r) * HD, lane, row);
   }
 }
 
@@ -843,12 +878,6 @@ size_t shared_partial_bytes(int max_batch, int n_q, int n_kv, int max_seq, int s
   const size_t prefix = std::max(2 * rows, std::min<size_t>(256 * (size_t)sm_count, rows * 2 * tiles));
   const size_t own = std::max(rows, std::min<size_t>(4 * (size_t)sm_count * G, rows * 128));
   return (prefix + own) * (HD + 2) * sizeof(float) + 16;
-}
-
-// Chunks of a (sequence, K/V head)'s keys that the weights' kernel takes at a time:
-// four CTAs per SM, and a key per thread at least.
-static int weight_chunks(int keys, int pairs, int sm_count) {
-  return std::max(1, std::min((keys + WEIGH_THREADS - 1) / WEIGH_THREADS, 4 * sm_count / pairs));
 }
 
 static OwnParams own_params(const SharedArgs& a, const SharedPlan& s) {
@@ -921,6 +950,15 @@ SharedPlan weights_plan(int B, int n_q, int n_kv, int key_limit, int sm_count) {
   return s;
 }
 
+// 8 CTAs per SM share the keys of all (sequence, K/V head) pairs, a pass of the threads each at least.
+template <bool NAT>
+static cudaError_t launch_weights(const OwnParams& p, const SharedArgs& a, cudaStream_t st) {
+  const int per = WEIGH_THREADS * WEIGH_KEYS;
+  const int chunks = std::max(1, std::min((a.key_limit + per - 1) / per, 8 * a.sm_count / (a.B * a.n_kv)));
+  return launch_k(attn_weights_kernel<NAT>, dim3(chunks, a.n_kv, a.B), dim3(WEIGH_THREADS), p.G * sizeof(float2), st,
+                  0, p);
+}
+
 cudaError_t launch_decode_weights(const SharedArgs& a, const SharedPlan& s, const WeightsArgs& w, cudaStream_t st) {
   OwnParams p = own_params(a, s);
   p.scores = w.scores;
@@ -933,9 +971,7 @@ cudaError_t launch_decode_weights(const SharedArgs& a, const SharedPlan& s, cons
                : launch_k(attn_own_kernel<false, true>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
                           *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess) return e;
-  const int chunks = weight_chunks(a.key_limit, a.B * a.n_kv, a.sm_count);
-  return launch_k(attn_weights_kernel<false>, dim3(chunks, a.n_kv, a.B), dim3(WEIGH_THREADS),
-                  p.G * sizeof(float2), st, 0, p);
+  return launch_weights<false>(p, a, st);
 }
 
 cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cudaStream_t st) {
@@ -951,9 +987,7 @@ cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cu
   p.scores = w.scores;
   p.weights = w.weights;
   p.ld = w.ld;
-  const int chunks = weight_chunks(a.key_limit, a.B * a.n_kv, a.sm_count);
-  return launch_k(attn_weights_kernel<true>, dim3(chunks, a.n_kv, a.B), dim3(WEIGH_THREADS),
-                  p.G * sizeof(float2), st, 0, p);
+  return launch_weights<true>(p, a, st);
 }
 
 }  // namespace llgb

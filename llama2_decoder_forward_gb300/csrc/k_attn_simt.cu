@@ -55,7 +55,7 @@ struct SimtParams {
   int n_seq;
   int row_chunks;  // chunks of 16 heads per K/V head
   int splits;      // CTAs (a cluster) that share an item's key tiles
-  // key weights: the scores [n_seq][n_kv][ld][G] and every row's maximum and sum, or null
+  // key weights: the scores [n_seq][n_q][ld] and every row's maximum and sum, or null
   float *scores, *stats;
   int64_t ld;
   // trees: out, cu_rows, n_rows, n_docs as documents, the cache as in decode
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
                                                 (p.mask[(size_t)(lo + ri) * p.mask_words + (x >> 5)] >> (x & 31) & 1u)
                                           : x <= ri);
         if (!DOCS && p.scores && keep && r0 + i < rows)
-          p.scores[(((size_t)b * p.n_kv + g) * p.ld + key) * p.G + (h0 - g * p.G) + r0 + i] = v;
+          p.scores[((size_t)b * p.n_q + h0 + r0 + i) * p.ld + key] = v;
         s[i][j] = keep ? v : -INFINITY;
       }
       float mx = fmaxf(s[i][0], s[i][1]);

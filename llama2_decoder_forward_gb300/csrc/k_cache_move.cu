@@ -9,9 +9,9 @@
 // Both lists ascend, so list[i] >= i, and a cache is compacted in place without a
 // second one: chunk c of the list writes slots that only chunks 0 .. c read, so a
 // CTA that has loaded a chunk may store it (after a barrier), and the next chunk's
-// loads need not wait for those stores. CTAs share nothing: each owns a slice of
-// the columns of K or of V of one (layer, sequence, K/V head), down to 32 bytes (a
-// sector) where there are few heads.
+// loads need not wait for those stores. CTAs share no row they move.
+//
+// Bound by the bytes of the rows, read and written once each.
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,86 +21,143 @@ namespace llgb {
 
 namespace {
 
+constexpr int MOVE_THREADS = 256;
 constexpr int UNITS = 8;            // 16-byte units that a thread has in flight
 constexpr int MAX_ROWS = 1024;      // rows of a chunk (256 threads x 8 units, slices of 2 units)
 
-// Row of a slot within its layer; -1 (flagged) for a page outside the pool.
-__device__ __forceinline__ int move_row(const CacheMoveArgs& a, int b, int g, int slot) {
-  if (a.page_size == 0) return (b * a.n_kv + g) * a.capacity + slot;
+// Row, within its layer, of a slot's K/V head 0 (the heads are slot_step rows apart); -1
+// (flagged) for a page outside the pool.
+__device__ __forceinline__ int move_row(const CacheMoveArgs& a, int b, int slot) {
+  if (a.page_size == 0) return b * a.n_kv * a.capacity + slot;
   const int pi = slot / a.page_size;
   const int page = pi < a.max_pages ? a.page_table[(size_t)b * a.max_pages + pi] : -1;
   if (page < 0 || page >= a.n_pages) {
     flag(a.status, LLAMA_FLAG_PAGE_RANGE);
     return -1;
   }
-  return (page * a.n_kv + g) * a.page_size + (slot - pi * a.page_size);
+  return page * a.n_kv * a.page_size + (slot - pi * a.page_size);
 }
 
-// Grid: slices, then K / V, K/V head, sequence, layer.
-__global__ void cache_move_kernel(CacheMoveArgs a, int slices, int rows_chunk) {
+// Commit. Grid: groups of `heads` K/V heads, sequences, layers. A sequence's path and
+// pages are the same for all heads of K and V, so a block looks them up once for as
+// many heads as fill its threads; a path is mostly one chunk.
+__global__ void __launch_bounds__(MOVE_THREADS) cache_commit_kernel(CacheMoveArgs a, int heads, int rows_chunk) {
+  grid_dep_wait();
+  grid_dep_launch();
+  extern __shared__ int2 moves[];  // [rows_chunk] (from, to) rows of K/V head 0; from < 0: no move
+  const int b = blockIdx.y, l = blockIdx.z, g0 = blockIdx.x * heads, n_heads = min(heads, a.n_kv - g0);
+  const int upr = a.row_bytes / 16, step = a.page_size == 0 ? a.capacity : a.page_size;
+  const bool report = blockIdx.x == 0 && l == 0;
+  const int base = a.start[b], len = a.count[b];
+  if ((base < 0 || len < 0 || len > a.list_ld) && report && threadIdx.x == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
+  const int n = base < 0 ? 0 : min(max(len, 0), a.list_ld);
+  const int32_t* path = a.path + (size_t)b * a.list_ld;
+  const size_t layer0 = (size_t)(a.layer + l) * a.layer_rows;
+  for (int i0 = 0; i0 < n; i0 += rows_chunk) {
+    const int rows = min(rows_chunk, n - i0), per_head = rows * upr;
+    if (i0 > 0) __syncthreads();
+    for (int r = threadIdx.x; r < rows; r += MOVE_THREADS) {
+      const int i = i0 + r, s = path[i];
+      int2 m = make_int2(-1, -1);
+      if (s < i || (i > 0 && s <= path[i - 1]) || s >= a.limit - base) {
+        if (report) flag(a.status, LLAMA_FLAG_POS_RANGE);
+      } else if (s != i) {
+        m = make_int2(move_row(a, b, base + s), move_row(a, b, base + i));
+        if (m.y < 0) m.x = -1;
+      }
+      moves[r] = m;
+    }
+    __syncthreads();
+    // unit u = (K / V, head, row, 16 bytes): a thread's units are MOVE_THREADS apart, so one
+    // division finds the first and additions the others
+    const int step_hk = MOVE_THREADS / per_head, step_r = (MOVE_THREADS - step_hk * per_head) / upr,
+              step_c = MOVE_THREADS - step_hk * per_head - step_r * upr;
+    const int hk0 = threadIdx.x / per_head, r0 = (threadIdx.x - hk0 * per_head) / upr;
+    const int c0 = threadIdx.x - hk0 * per_head - r0 * upr;
+    auto walk = [&](auto&& f) {
+      int hk = hk0, r = r0, c = c0;
+#pragma unroll
+      for (int k = 0; k < UNITS; ++k) {
+        if (hk < 2 * n_heads) {
+          const int2 m = moves[r];
+          const int v = hk >= n_heads;
+          uint4* at = reinterpret_cast<uint4*>(v ? a.v : a.k) +
+                      (layer0 + (size_t)(g0 + hk - (v ? n_heads : 0)) * step) * upr + c;
+          if (m.x >= 0 && bc_ok(g0 + hk - (v ? n_heads : 0) < a.n_kv, a.status)) f(k, at, m);
+        }
+        c += step_c;
+        r += step_r;
+        hk += step_hk;
+        if (c >= upr) {
+          c -= upr;
+          ++r;
+        }
+        if (r >= rows) {
+          r -= rows;
+          ++hk;
+        }
+      }
+    };
+    uint4 x[UNITS];
+    walk([&](int k, const uint4* at, int2 m) { x[k] = at[(size_t)m.x * upr]; });
+    __syncthreads();  // the chunk is read: its slots may be written
+    walk([&](int k, uint4* at, int2 m) { at[(size_t)m.y * upr] = x[k]; });
+  }
+}
+
+// Evict: what stays, moved. Grid: slices, then K / V, K/V head, sequence, layer. Each CTA
+// owns a slice of the columns of K or V of one head, down to 32 bytes (a sector) where
+// there are few heads.
+__global__ void __launch_bounds__(MOVE_THREADS) cache_evict_kernel(CacheMoveArgs a, int slices, int rows_chunk) {
   grid_dep_wait();
   grid_dep_launch();
   // (from, to) rows of a chunk, from < 0: no move; [3][rows_chunk], because beside a
   // thread that still stores a chunk another one may look up the chunk after the next
   extern __shared__ int2 moves[];
-  const int T = blockDim.x;
   long long item = blockIdx.x;
   const int slice = (int)(item % slices);
   item /= slices;
   const int is_v = (int)(item & 1);
   item >>= 1;
   const int g = (int)(item % a.n_kv);
-  item /= a.n_kv;
-  const int b = (int)(item % a.B), l = (int)(item / a.B);
-  const int upr = a.row_bytes / 16 / slices;  // units of a row of the slice
-  // the list, and how much of it there is
-  const int32_t* list;
-  int n, base = 0, first = 0;
-  if (a.path) {
-    list = a.path + (size_t)b * a.list_ld;
-    base = a.start[b];
-    n = a.count[b];
-    const bool ok = base >= 0 && n >= 0 && n <= a.list_ld;
-    if (!ok && threadIdx.x == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
-    n = base < 0 ? 0 : min(max(n, 0), a.list_ld);
-  } else {
-    list = a.kept + (((size_t)l * a.B + b) * a.n_kv + g) * a.list_ld;
-    const int len = min(max(a.lens[b], 0), a.limit);
-    n = len <= a.list_ld ? 0 : a.list_ld;  // nothing was dropped: nothing moves
-    // the first slot that moves: list[i] == i up to there
-    for (int step = (n + T - 1) / T, end = n; end > first && step > 0;) {
-      const int i = first + threadIdx.x * step;
-      const int same = __syncthreads_count(i < end && list[i] == i);
-      if (same == 0) break;
-      if (step == 1) {
-        first += same;
-        break;
-      }
-      first += (same - 1) * step;
-      end = min(end, first + step);
-      step = (end - first + T - 1) / T;
+  const int b = (int)(item / a.n_kv % a.B), l = (int)(item / a.n_kv / a.B);
+  const int len = min(max(a.lens[b], 0), a.limit);
+  if (len <= a.list_ld) return;  // nothing was dropped: nothing moves
+  const int n = a.list_ld, upr = a.row_bytes / 16 / slices, ld = a.row_bytes / 16;  // units of a row's slice, of a row
+  const int32_t* list = a.kept + (size_t)item * n;
+  // the first slot that moves: list[i] == i up to there
+  int first = 0;
+  for (int step = (n + MOVE_THREADS - 1) / MOVE_THREADS, end = n; end > first;) {
+    const int i = first + threadIdx.x * step;
+    const int same = __syncthreads_count(i < end && list[i] == i);
+    if (same == 0) break;
+    if (step == 1) {
+      first += same;
+      break;
     }
+    first += (same - 1) * step;
+    end = min(end, first + step);
+    step = (end - first + MOVE_THREADS - 1) / MOVE_THREADS;
   }
-  // rows of the chunk at i0, into its half of `moves`
+  const int head = g * (a.page_size == 0 ? a.capacity : a.page_size);
+  // rows of the chunk at i0, into its part of `moves`
   auto look_up = [&](int i0, int2* to) {
-    for (int r = threadIdx.x; r < rows_chunk; r += T) {
+    for (int r = threadIdx.x; r < rows_chunk; r += MOVE_THREADS) {
       const int i = i0 + r;
       int2 m = make_int2(-1, -1);
       if (i < n) {
         const int s = list[i];
-        if (a.path && (s < i || (i > 0 && s <= list[i - 1]) || s >= a.limit - base)) {
-          if (is_v == 0 && slice == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
-        } else if (s != i && bc_ok(s > i && base + s < a.limit, a.status)) {
-          m = make_int2(move_row(a, b, g, base + s), move_row(a, b, g, base + i));
-          if (m.y < 0) m.x = -1;
+        if (s != i && bc_ok(s > i && s < len, a.status)) {
+          m = make_int2(move_row(a, b, s), move_row(a, b, i));
+          m = m.x < 0 || m.y < 0 ? make_int2(-1, -1) : make_int2(m.x + head, m.y + head);
+          if (!bc_ok((size_t)max(m.x, m.y) < a.layer_rows || m.x < 0, a.status)) m.x = -1;
         }
       }
       to[r] = m;
     }
   };
-  uint4* cache = reinterpret_cast<uint4*>(is_v ? a.v : a.k) +
-                 (size_t)(a.layer + l) * a.layer_rows * (a.row_bytes / 16) + (size_t)slice * upr;
-  const int ld = a.row_bytes / 16;
+  uint4* cache = reinterpret_cast<uint4*>(is_v ? a.v : a.k) + (size_t)(a.layer + l) * a.layer_rows * ld +
+                 (size_t)slice * upr;
   look_up(first, moves);
   __syncthreads();
   int part = 0;
@@ -110,21 +167,21 @@ __global__ void cache_move_kernel(CacheMoveArgs a, int slices, int rows_chunk) {
     uint4 x[UNITS];
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
-      const int u = threadIdx.x + k * T, r = u / upr;
+      const int u = threadIdx.x + k * MOVE_THREADS, r = u / upr;
       if (r < rows_chunk && mv[r].x >= 0) x[k] = cache[(size_t)mv[r].x * ld + (u - r * upr)];
     }
     if (i0 + rows_chunk < n) look_up(i0 + rows_chunk, moves + part * rows_chunk);
     __syncthreads();  // the chunk is read: its slots may be written
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
-      const int u = threadIdx.x + k * T, r = u / upr;
+      const int u = threadIdx.x + k * MOVE_THREADS, r = u / upr;
       if (r < rows_chunk && mv[r].x >= 0) cache[(size_t)mv[r].y * ld + (u - r * upr)] = x[k];
     }
   }
 }
 
 // ---------------------------------------------------------------- which keys stay
-constexpr int SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32;
+constexpr int SPAN = 8192;                    // weights that a CTA holds
 constexpr int BINS = 2048;
 
 // Weights in ascending order as unsigned numbers: -0 as 0, NaN below everything.
@@ -133,16 +190,24 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return w != w ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// One CTA per (layer, sequence, K/V head): the m-th largest of the weights between
-// the first and the recent slots by three counting passes of 11, 11 and 10 bits,
-// then one ordered pass that lists what stays and moves its weights.
-__global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(EvictArgs a) {
+// One CTA of T threads per (layer, sequence, K/V head): the m-th largest of the weights
+// between the first and the recent slots by three counting passes of 11, 11 and 10
+// bits, then one ordered pass that lists what stays and moves its weights. A warp owns
+// consecutive slots, 32 at a time, so ranks within it are bit counts and the warps
+// exchange one pair of counts. Up to 8192 weights are read once and stay in shared
+// memory (in order_of's form; the list tells where the others lie), longer lists are
+// read again for every pass, 8192 at a time.
+template <int T>
+__global__ void __launch_bounds__(T) evict_select_kernel(EvictArgs a) {
   grid_dep_wait();
   grid_dep_launch();
+  constexpr int WARPS = T / 32, PER = BINS / T;
+  extern __shared__ float held[];  // [min(SPAN, most slots)]
   __shared__ uint32_t bins[BINS];
-  __shared__ int part[2][SEL_WARPS];
+  __shared__ int2 part[WARPS];
   __shared__ uint32_t found[2];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t below = (1u << lane) - 1u;
   const int b = (int)(blockIdx.x / a.n_kv % a.B);
   const float* w = a.weights + (size_t)blockIdx.x * a.ld;
   float* out = a.weights_out + (size_t)blockIdx.x * a.ld;
@@ -151,35 +216,69 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(EvictArgs a) 
   if (len != n && t == 0 && blockIdx.x % a.n_kv == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
   const bool all = n <= a.keep;
   const int lo = a.first, hi = n - a.recent;  // candidates
+  auto load = [&](int s0) {
+#pragma unroll 4
+    for (int i = t; i < min(SPAN, n - s0); i += T) held[i] = w[s0 + i];
+    __syncthreads();
+  };
+  // sums over the warps in front of this one, and over all
+  auto across = [&](int2 mine, int2& all) {
+    if (lane == 0) part[warp] = mine;
+    __syncthreads();
+    const int2 c = lane < WARPS ? part[lane] : make_int2(0, 0);
+    int2 up = c;
+#pragma unroll
+    for (int o = 1; o < WARPS; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, up.x, o), y = __shfl_up_sync(0xffffffffu, up.y, o);
+      if (lane >= o) {
+        up.x += x;
+        up.y += y;
+      }
+    }
+    all = make_int2(__shfl_sync(0xffffffffu, up.x, WARPS - 1), __shfl_sync(0xffffffffu, up.y, WARPS - 1));
+    return make_int2(__shfl_sync(0xffffffffu, up.x - c.x, warp), __shfl_sync(0xffffffffu, up.y - c.y, warp));
+  };
+  for (int i = t; i < BINS; i += T) bins[i] = 0;
+  load(0);
   uint32_t least = 0, ties = 0;               // the smallest weight that stays, and how many equal to it
   int want = a.keep - a.first - a.recent;
   if (!all && want > 0) {
     int shift = 21;
     uint32_t prefix = 0, mask = 0;
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int width = pass == 2 ? 10 : 11;
-      for (int i = t; i < BINS; i += SEL_THREADS) bins[i] = 0;
-      __syncthreads();
-      for (int i = lo + t; i < hi; i += SEL_THREADS) {
-        const uint32_t u = order_of(w[i]);
-        if ((u & mask) == prefix) atomicAdd(&bins[(u >> shift) & ((1u << width) - 1u)], 1u);
+#pragma unroll 1
+      for (int s0 = 0; s0 < n; s0 += SPAN) {
+        if (n > SPAN && (s0 > 0 || pass > 0)) {
+          __syncthreads();
+          load(s0);
+        }
+        const int from = max(0, lo - s0), to = min(SPAN, hi - s0);
+#pragma unroll 4
+        for (int i = from + t; i < to; i += T) {
+          const uint32_t u = order_of(held[i]);
+          if ((u & mask) == prefix) atomicAdd(&bins[(u >> shift) & ((1u << width) - 1u)], 1u);
+        }
       }
       __syncthreads();
-      // suffix sums from the largest bin on: thread t has bins BINS - 1 - 4 t and the three below
-      const int top = BINS - 1 - 4 * t;
-      uint32_t c[4], sum = 0;
+      // suffix sums from the largest bin on: thread t has the PER bins below BINS - PER t
+      const int top = BINS - 1 - PER * t;
+      uint32_t c[PER], sum = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum += c[k] = bins[top - k];
+      for (int k = 0; k < PER; ++k) {
+        sum += c[k] = bins[top - k];
+        bins[top - k] = 0;  // for the next pass
+      }
       uint32_t upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
       }
-      if (lane == 31) part[0][warp] = (int)upto;
-      __syncthreads();
-      uint32_t before = upto - sum;
-      for (int k = 0; k < warp; ++k) before += (uint32_t)part[0][k];
+      int2 total;
+      const int2 mine = make_int2((int)__shfl_sync(0xffffffffu, upto, 31), 0);
+      uint32_t before = upto - sum + (uint32_t)across(mine, total).x;
       if (before < (uint32_t)want && before + sum >= (uint32_t)want) {
         int k = 0;
         while (before + c[k] < (uint32_t)want) before += c[k++];
@@ -191,70 +290,90 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(EvictArgs a) 
       mask |= ((1u << width) - 1u) << shift;
       want -= (int)found[1];
       shift = pass == 0 ? 10 : 0;
-      __syncthreads();
     }
     least = prefix;
     ties = (uint32_t)want;
   }
-  // what stays, in order; a slot's weight moves to a slot that was read before or with it
+  // What stays, in order: the spans one after the other, the warps of a span in parallel.
+  // A weight moves to a slot that its span or an earlier one holds, and those were read.
   const bool none = a.keep - a.first - a.recent == 0;
   int done = 0, tied = 0;  // listed so far, equal to `least` so far
-  for (int i0 = 0; i0 < n; i0 += SEL_THREADS) {
-    const int i = i0 + t;
-    const float x = i < n ? w[i] : 0.f;
-    bool stays = i < n && (all || i < lo || i >= hi), tie = false;
-    if (i < n && !stays && !none) {
-      const uint32_t u = order_of(x);
-      stays = u > least;
-      tie = u == least;
+#pragma unroll 1
+  for (int s0 = 0; s0 < n; s0 += SPAN) {
+    if (n > SPAN) {
+      __syncthreads();
+      load(s0);
     }
-    const uint32_t mt = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) part[0][warp] = __popc(mt);
-    __syncthreads();  // (also: every weight of these slots is read)
-    int rank = tied + __popc(mt & ((1u << lane) - 1u));
-    for (int k = 0; k < SEL_WARPS; ++k) {
-      if (k < warp) rank += part[0][k];
-      tied += part[0][k];
+    const int m = min(SPAN, n - s0), own = (m + T - 1) / T;  // 32-slot steps of a warp
+    const int at0 = warp * 32 * own + lane;
+    // whether slot at0 + 32 k stays whatever the ties (1), or is one (2)
+    auto kind = [&](int i) {
+      if (i >= m) return 0;
+      if (all || s0 + i < lo || s0 + i >= hi) return 1;
+      const uint32_t u = order_of(held[i]);
+      return none ? 0 : u > least ? 1 : u == least ? 2 : 0;
+    };
+    int2 count = make_int2(0, 0);
+    for (int k = 0; k < own; ++k) {
+      const int x = kind(at0 + 32 * k);
+      count.x += __popc(__ballot_sync(0xffffffffu, x == 1));
+      count.y += __popc(__ballot_sync(0xffffffffu, x == 2));
     }
-    stays |= tie && rank < (int)ties;
-    const uint32_t ms = __ballot_sync(0xffffffffu, stays);
-    if (lane == 0) part[1][warp] = __popc(ms);
-    __syncthreads();
-    int at = done + __popc(ms & ((1u << lane) - 1u));
-    for (int k = 0; k < SEL_WARPS; ++k) {
-      if (k < warp) at += part[1][k];
-      done += part[1][k];
+    int2 sums;
+    const int2 front = across(count, sums);
+    // the ties that stay are the first ones: `ties` of them in all
+    int rank = tied + front.y, at = done + front.x + max(0, min(front.y, (int)ties - tied));
+    for (int k = 0; k < own; ++k) {
+      const int i = at0 + 32 * k, x = kind(i);
+      const uint32_t me = __ballot_sync(0xffffffffu, x == 2);
+      const bool s = x == 1 || (x == 2 && rank + __popc(me & below) < (int)ties);
+      const uint32_t ms = __ballot_sync(0xffffffffu, s);
+      const int to = at + __popc(ms & below);
+      if (s && bc_ok(to < a.keep && to <= s0 + i, a.status)) {
+        kept[to] = s0 + i;
+        out[to] = held[i];
+      }
+      at += __popc(ms);
+      rank += __popc(me);
     }
-    if (stays && bc_ok(at < a.keep && at <= i, a.status)) {
-      kept[at] = i;
-      out[at] = x;
-    }
+    done += sums.x + max(0, min(sums.y, (int)ties - tied));
+    tied += sums.y;
+    __syncthreads();  // `part` and `held` have been read
   }
-  __syncthreads();
-  for (int i = done + t; i < a.keep; i += SEL_THREADS) kept[i] = -1;
-  for (long long i = done + t; i < a.ld; i += SEL_THREADS) out[i] = 0.f;
+  for (int i = done + t; i < a.keep; i += T) kept[i] = -1;
+  for (long long i = done + t; i < a.ld; i += T) out[i] = 0.f;
 }
 
 }  // namespace
 
-cudaError_t launch_cache_move(const CacheMoveArgs& a, cudaStream_t st) {
+cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t st) {
+  const int upr = a.row_bytes / 16, room = MOVE_THREADS * UNITS / (2 * upr);  // rows of one head's K and V
+  // as many heads as a block has room for, but blocks for every SM
+  const long long pairs = (long long)a.layers * a.B;
+  const int heads = (int)std::max<long long>(
+      1, std::min<long long>({room / a.list_ld, a.n_kv, a.n_kv * pairs / (2 * a.sm_count)}));
+  const int rows = std::min(a.list_ld, room / heads);
+  return launch_k(cache_commit_kernel, dim3((a.n_kv + heads - 1) / heads, a.B, a.layers), dim3(MOVE_THREADS),
+                  rows * sizeof(int2), st, 0, a, heads, rows);
+}
+
+cudaError_t launch_cache_evict(const CacheMoveArgs& a, cudaStream_t st) {
   const int upr = a.row_bytes / 16;
   const long long items = (long long)a.layers * a.B * a.n_kv * 2;
-  int slices = 1, T = 256;
-  if (a.path) {
-    // a few rows: as many threads as the longest path needs
-    while (T > 32 && (long long)T / 2 * UNITS >= (long long)a.list_ld * upr) T /= 2;
-  } else {
-    while (upr / slices % 2 == 0 && upr / slices > 2 && items * slices < 4 * a.sm_count) slices *= 2;
-  }
-  const int rows = std::min(MAX_ROWS, std::max(1, T * UNITS / (upr / slices)));
-  return launch_k(cache_move_kernel, dim3((unsigned)(items * slices)), dim3(T), 3 * rows * sizeof(int2), st, 0, a,
-                  slices, rows);
+  int slices = 1;
+  while (upr / slices % 2 == 0 && upr / slices > 2 && items * slices < 4 * a.sm_count) slices *= 2;
+  const int rows = std::min(MAX_ROWS, MOVE_THREADS * UNITS / (upr / slices));
+  return launch_k(cache_evict_kernel, dim3((unsigned)(items * slices)), dim3(MOVE_THREADS), 3 * rows * sizeof(int2),
+                  st, 0, a, slices, rows);
 }
 
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st) {
-  return launch_k(evict_select_kernel, dim3((unsigned)((long long)a.layers * a.B * a.n_kv)), dim3(SEL_THREADS), 0, st,
-                  0, a);
+  const long long items = (long long)a.layers * a.B * a.n_kv;
+  const size_t sm = (size_t)std::min(SPAN, a.limit) * sizeof(float);
+  // few items: the time of one counts; many: how many run at a time
+  return items <= 2 * a.sm_count
+             ? launch_k(evict_select_kernel<1024>, dim3((unsigned)items), dim3(1024), sm, st, 0, a)
+             : launch_k(evict_select_kernel<256>, dim3((unsigned)items), dim3(256), sm, st, 0, a);
 }
 
 }  // namespace llgb
