@@ -875,8 +875,12 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           if (it > 0 || !prefix_work(p, share, w)) break;
           rows = tile_rows(p, p.shared_seq, w.g, w.t0, w.kmax, lane);
         }
+        // trees: the first two K tiles come before Q, whose slot is free only after the last
+        // item's last scores (their own slots are free sooner, and wait for no Q of this item)
+        const int q_at = TREE ? min(w.n_tiles, 2) : 0;
+        auto load_q = [&] {
         ok = __all_sync(0xffffffffu, wait_bar(qempty, (it & 1) ^ 1, stop, p.status));
-        if (!ok) break;
+        if (!ok) return;
         ++loaded_q;
         if (lane == 0) {
           const int q_tiles = alt || w.nt1 == 0 ? 1 : 2;
@@ -893,7 +897,11 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
                             (TREE ? w.lo + w.q0 : w.seq0) + t * p.rows_seq);
             }
         }
-        for (int j = 0; j < w.n_tiles; ++j) {
+        };
+        if (q_at == 0) load_q();
+        for (int j = 0; ok && j < w.n_tiles; ++j) {
+          if (TREE && j > 0 && j == q_at) load_q();
+          if (!ok) break;
           if (!DOCS && j > 0 && (j & 3) == 0)
             rows = tile_rows(p, TREE ? w.seq0 : p.shared_seq, w.g, w.t0 + j, w.kmax, lane);
           ok = __all_sync(0xffffffffu, wait_bar(&kempty[r.slot], r.phase ^ 1, stop, p.status));
@@ -903,6 +911,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           ++issued;
           r.step();
         }
+        if (TREE && ok && q_at == w.n_tiles) load_q();
         if (TREE && ok && alt && (w.n_tiles & 1)) even_out(r, kempty, kfull, issued, ok);
       }
       // no copy in flight when the CTA exits
@@ -1420,9 +1429,9 @@ FormsKernel forms_kernel(int kind) {
   }
 }
 
-// Merges the partial results of the tree items that several CTAs share: a warp per row at
-// a time. Every block makes the list of those items, so that no block is without work.
-constexpr int JOIN_WARPS = 8, JOIN_AHEAD = 8;
+// Merges the partial results of the tree items that several CTAs share: a warp takes 2
+// rows and 4 partial results at a time, whose loads hide each other's latency. Every block makes the list of those items, so that no block is without work.
+constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2, JOIN_AHEAD = 4, JOIN_PARTS = 32 / JOIN_ROWS;
 __global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(FormsParams p, int ctas) {
   grid_dep_wait();
   grid_dep_launch();
@@ -1441,60 +1450,79 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(Form
   }
   __syncthreads();
   const int rows_tile = p.rows_seq * p.G, rows_slot = p.alternate ? TM : 2 * TM;
-  for (int task = blockIdx.x * JOIN_WARPS + warp; task < n_items * rows_slot; task += gridDim.x * JOIN_WARPS) {
-    const int2 which = items[task / rows_slot];
-    const int r = task % rows_slot, tile = r / TM, rt = r - tile * TM, parts = which.y;
+  const int row_l = lane / JOIN_PARTS, part_l = lane % JOIN_PARTS;  // of this lane's maximum and sum
+  for (int task = blockIdx.x * JOIN_WARPS + warp; task < n_items * (rows_slot / JOIN_ROWS); task += gridDim.x * JOIN_WARPS) {
+    const int2 which = items[task / (rows_slot / JOIN_ROWS)];
+    const int r0 = task % (rows_slot / JOIN_ROWS) * JOIN_ROWS, tile = r0 / TM, rt0 = r0 - tile * TM, parts = which.y;
     const TreeShared it = p.shared[which.x];
-    const int index = it.q0 + tile * p.rows_seq + rt / p.G;  // the row of the tree
-    if (rt >= rows_tile || index >= it.n ||
-        !bc_ok((size_t)2 * (which.x + parts) * rows_slot <= p.partials && it.lo + index < p.n_rows, p.status))
+    const int q0 = it.q0 + tile * p.rows_seq;
+    // rows of nobody lie behind the others
+    if (rt0 >= rows_tile || q0 + rt0 / p.G >= it.n ||
+        !bc_ok((size_t)2 * (which.x + parts) * rows_slot <= p.partials, p.status))
       continue;
-    // partial s of the item
-    auto at = [&](int s) { return (size_t)(s == 0 ? it.first : 2 * (which.x + s)) * rows_slot + r; };
-    float m = -INFINITY, l = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-      const int n = min(32, parts - s0);
+    // partial s of row r0
+    auto at = [&](int s) { return (size_t)(s == 0 ? it.first : 2 * (which.x + s)) * rows_slot + r0; };
+    float m = -INFINITY, l = 0.f;  // of row row_l
+    float4 v[JOIN_ROWS];
+#pragma unroll
+    for (int k = 0; k < JOIN_ROWS; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < parts; s0 += JOIN_PARTS) {
+      const int n = min(JOIN_PARTS, parts - s0);
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < n) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at(s0 + lane));
-      float4 x[JOIN_AHEAD];
+      if (part_l < n) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at(s0 + part_l) + row_l));
+      float4 x[JOIN_AHEAD][JOIN_ROWS];
       auto load = [&](int s) {
 #pragma unroll
         for (int i = 0; i < JOIN_AHEAD; ++i)
-          if (s + i < n) x[i] = *reinterpret_cast<const float4*>(p.part_o + at(s0 + s + i) * 128 + 4 * lane);
+#pragma unroll
+          for (int k = 0; k < JOIN_ROWS; ++k)
+            if (s + i < n) x[i][k] = *reinterpret_cast<const float4*>(p.part_o + (at(s0 + s + i) + k) * 128 + 4 * lane);
       };
       load(0);
       float top = ml.x;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = JOIN_PARTS / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const float mx = fmaxf(m, top), old = m == -INFINITY ? 0.f : exp2f(m - mx);
       const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mx);
       float sum = f != 0.f ? ml.y * f : 0.f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int o = JOIN_PARTS / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       l = (m == -INFINITY ? 0.f : l * old) + sum;
-      v.x *= old;
-      v.y *= old;
-      v.z *= old;
-      v.w *= old;
       m = mx;
+#pragma unroll
+      for (int k = 0; k < JOIN_ROWS; ++k) {
+        const float fo = __shfl_sync(0xffffffffu, old, JOIN_PARTS * k);
+        v[k].x *= fo;
+        v[k].y *= fo;
+        v[k].z *= fo;
+        v[k].w *= fo;
+      }
       for (int s = 0; s < n; s += JOIN_AHEAD) {
         if (s > 0) load(s);
 #pragma unroll
-        for (int i = 0; i < JOIN_AHEAD; ++i) {
-          const float fs = __shfl_sync(0xffffffffu, f, (s + i) & 31);
-          if (s + i < n && fs != 0.f) {  // a part without visible keys may hold anything
-            v.x = fmaf(x[i].x, fs, v.x);
-            v.y = fmaf(x[i].y, fs, v.y);
-            v.z = fmaf(x[i].z, fs, v.z);
-            v.w = fmaf(x[i].w, fs, v.w);
+        for (int i = 0; i < JOIN_AHEAD; ++i)
+#pragma unroll
+          for (int k = 0; k < JOIN_ROWS; ++k) {
+            const float fs = __shfl_sync(0xffffffffu, f, JOIN_PARTS * k + (s + i) % JOIN_PARTS);
+            if (s + i < n && fs != 0.f) {  // a part without visible keys may hold anything
+              v[k].x = fmaf(x[i][k].x, fs, v[k].x);
+              v[k].y = fmaf(x[i][k].y, fs, v[k].y);
+              v[k].z = fmaf(x[i][k].z, fs, v[k].z);
+              v[k].w = fmaf(x[i][k].w, fs, v[k].w);
+            }
           }
-        }
       }
     }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    bf16* dst = p.out + (((size_t)it.lo + index) * p.n_q + it.g * p.G + rt % p.G) * 128;
-    reinterpret_cast<uint2*>(dst)[lane] = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+    const float inv_l = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+    for (int k = 0; k < JOIN_ROWS; ++k) {
+      const float inv = __shfl_sync(0xffffffffu, inv_l, JOIN_PARTS * k);
+      const int rt = rt0 + k, index = q0 + rt / p.G;  // the row of the tree
+      if (rt >= rows_tile || index >= it.n || !bc_ok(it.lo + index < p.n_rows, p.status)) continue;
+      bf16* dst = p.out + (((size_t)it.lo + index) * p.n_q + it.g * p.G + rt % p.G) * 128;
+      reinterpret_cast<uint2*>(dst)[lane] =
+          make_uint2(pack_bf16(v[k].x * inv, v[k].y * inv), pack_bf16(v[k].z * inv, v[k].w * inv));
+    }
   }
 }
 

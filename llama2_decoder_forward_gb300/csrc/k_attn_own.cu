@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int 
 // time), and 4 heads; the first ones are loaded before the maxima and sums.
 constexpr int WEIGH_THREADS = 256, WEIGH_KEYS = 4, WEIGH_HEADS = 4;
 template <bool NAT>
-__global__ void __launch_bounds__(WEIGH_THREADS) attn_weights_kernel(OwnParams p) {
+__global__ void __launch_bounds__(WEIGH_THREADS, 4) attn_weights_kernel(OwnParams p) {
   grid_dep_wait();
   grid_dep_launch();
   extern __shared__ float2 stat[];  // maximum and reciprocal sum of the group's G heads
@@ -756,6 +756,18 @@ __global__ void __launch_bounds__(WEIGH_THREADS) attn_weights_kernel(OwnParams p
   const size_t row0 = (size_t)b * p.n_q + (size_t)g * G;
   float* w = p.weights + ((size_t)b * p.n_kv + g) * p.ld;
   const float* sc = p.scores + row0 * p.ld;
+  const int key_blocks = NAT ? gridDim.x : gridDim.x - 1;
+  if (!NAT && blockIdx.x == key_blocks) {  // one block joins the output rows
+    for (int r = warp; r < G; r += WEIGH_THREADS / 32) {
+      Parts<8> own;
+      RowSum row;
+      own.load(p.own_o, p.own_ml, (row0 + r) * p.splits, p.splits, lane);
+      own.fold(used, lane, row);
+      store_row(p.out + (row0 + r) * HD, lane, row);
+    }
+    return;
+  }
+  if (blockIdx.x * (WEIGH_THREADS * WEIGH_KEYS) >= n) return;
   int i = blockIdx.x * (WEIGH_THREADS * WEIGH_KEYS) + threadIdx.x;
   float old[WEIGH_KEYS], x[WEIGH_HEADS][WEIGH_KEYS];
   auto load = [&](int r0) {
@@ -787,7 +799,7 @@ __global__ void __launch_bounds__(WEIGH_THREADS) attn_weights_kernel(OwnParams p
     if (lane == 0) stat[r] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f || l != l ? 1.f / l : 0.f);
   }
   __syncthreads();
-  for (bool first = true; i < n; i += gridDim.x * (WEIGH_THREADS * WEIGH_KEYS), first = false) {
+  for (bool first = true; i < n; i += key_blocks * (WEIGH_THREADS * WEIGH_KEYS), first = false) {
     if (!first) {
       load_old();
       load(0);
@@ -809,15 +821,6 @@ __global__ void __launch_bounds__(WEIGH_THREADS) attn_weights_kernel(OwnParams p
 #pragma unroll
     for (int q = 0; q < WEIGH_KEYS; ++q)
       if (i + q * WEIGH_THREADS < n) w[i + q * WEIGH_THREADS] = old[q] + sum[q];
-  }
-  if (NAT) return;
-  for (int r = warp; r < G; r += WEIGH_THREADS / 32) {
-    if (r % gridDim.x != blockIdx.x) continue;  // the output rows are shared out over the chunks
-    Parts<8> own;
-    RowSum row;
-    own.load(p.own_o, p.own_ml, (row0 + r) * p.splits, p.splits, lane);
-    own.fold(used, lane, row);
-    store_row(p.out + (row0 + r) * HD, lane, row);
   }
 }
 
@@ -955,7 +958,7 @@ template <bool NAT>
 static cudaError_t launch_weights(const OwnParams& p, const SharedArgs& a, cudaStream_t st) {
   const int per = WEIGH_THREADS * WEIGH_KEYS;
   const int chunks = std::max(1, std::min((a.key_limit + per - 1) / per, 8 * a.sm_count / (a.B * a.n_kv)));
-  return launch_k(attn_weights_kernel<NAT>, dim3(chunks, a.n_kv, a.B), dim3(WEIGH_THREADS), p.G * sizeof(float2), st,
+  return launch_k(attn_weights_kernel<NAT>, dim3(chunks + !NAT, a.n_kv, a.B), dim3(WEIGH_THREADS), p.G * sizeof(float2), st,
                   0, p);
 }
 

@@ -38,28 +38,33 @@ __device__ __forceinline__ int move_row(const CacheMoveArgs& a, int b, int slot)
   return page * a.n_kv * a.page_size + (slot - pi * a.page_size);
 }
 
-// Commit. Grid: groups of `heads` K/V heads, sequences, layers. A sequence's path and
-// pages are the same for all heads of K and V, so a block looks them up once for as
-// many heads as fill its threads; a path is mostly one chunk.
-__global__ void __launch_bounds__(MOVE_THREADS) cache_commit_kernel(CacheMoveArgs a, int heads, int rows_chunk) {
+// Commit. Grid: groups of `heads` K/V heads, sequences, runs of layers. A sequence's path
+// and pages are the same for all layers and heads, K and V, so a block looks them up once
+// for as many heads as fill its threads and walks its layers: while it waits for
+// one layer's rows to store them, the next one's are on their way. A path is mostly one
+// chunk.
+constexpr int COMMIT_UNITS = 4;
+__global__ void __launch_bounds__(MOVE_THREADS, 3) cache_commit_kernel(CacheMoveArgs a, int heads, int rows_chunk,
+                                                                       int run) {
   grid_dep_wait();
   grid_dep_launch();
   extern __shared__ int2 moves[];  // [rows_chunk] (from, to) rows of K/V head 0; from < 0: no move
-  const int b = blockIdx.y, l = blockIdx.z, g0 = blockIdx.x * heads, n_heads = min(heads, a.n_kv - g0);
+  const int b = blockIdx.y, l0 = blockIdx.z * run, l1 = min(a.layers, l0 + run);
+  const int g0 = blockIdx.x * heads, n_heads = min(heads, a.n_kv - g0);
   const int upr = a.row_bytes / 16, step = a.page_size == 0 ? a.capacity : a.page_size;
-  const bool report = blockIdx.x == 0 && l == 0;
+  const bool report = blockIdx.x == 0 && l0 == 0;
   const int base = a.start[b], len = a.count[b];
   if ((base < 0 || len < 0 || len > a.list_ld) && report && threadIdx.x == 0) flag(a.status, LLAMA_FLAG_POS_RANGE);
   const int n = base < 0 ? 0 : min(max(len, 0), a.list_ld);
   const int32_t* path = a.path + (size_t)b * a.list_ld;
-  const size_t layer0 = (size_t)(a.layer + l) * a.layer_rows;
+  const size_t layer_units = a.layer_rows * upr;
   for (int i0 = 0; i0 < n; i0 += rows_chunk) {
     const int rows = min(rows_chunk, n - i0), per_head = rows * upr;
     if (i0 > 0) __syncthreads();
     for (int r = threadIdx.x; r < rows; r += MOVE_THREADS) {
-      const int i = i0 + r, s = path[i];
+      const int i = i0 + r, s = path[i], before = i > 0 ? path[i - 1] : -1;
       int2 m = make_int2(-1, -1);
-      if (s < i || (i > 0 && s <= path[i - 1]) || s >= a.limit - base) {
+      if (s < i || s <= before || s >= a.limit - base) {
         if (report) flag(a.status, LLAMA_FLAG_POS_RANGE);
       } else if (s != i) {
         m = make_int2(move_row(a, b, base + s), move_row(a, b, base + i));
@@ -68,40 +73,59 @@ __global__ void __launch_bounds__(MOVE_THREADS) cache_commit_kernel(CacheMoveArg
       moves[r] = m;
     }
     __syncthreads();
-    // unit u = (K / V, head, row, 16 bytes): a thread's units are MOVE_THREADS apart, so one
-    // division finds the first and additions the others
+    // Unit u = (K / V, head, row, 16 bytes): a thread's units are MOVE_THREADS apart, so one
+    // division finds the first and additions the others. Its places in the first layer:
     const int step_hk = MOVE_THREADS / per_head, step_r = (MOVE_THREADS - step_hk * per_head) / upr,
               step_c = MOVE_THREADS - step_hk * per_head - step_r * upr;
-    const int hk0 = threadIdx.x / per_head, r0 = (threadIdx.x - hk0 * per_head) / upr;
-    const int c0 = threadIdx.x - hk0 * per_head - r0 * upr;
-    auto walk = [&](auto&& f) {
-      int hk = hk0, r = r0, c = c0;
+    int hk = threadIdx.x / per_head, r = (threadIdx.x - hk * per_head) / upr;
+    int c = threadIdx.x - hk * per_head - r * upr;
+    const uint4* from[COMMIT_UNITS];
+    int to[COMMIT_UNITS];  // rows further down; 0: no move
 #pragma unroll
-      for (int k = 0; k < UNITS; ++k) {
-        if (hk < 2 * n_heads) {
-          const int2 m = moves[r];
-          const int v = hk >= n_heads;
-          uint4* at = reinterpret_cast<uint4*>(v ? a.v : a.k) +
-                      (layer0 + (size_t)(g0 + hk - (v ? n_heads : 0)) * step) * upr + c;
-          if (m.x >= 0 && bc_ok(g0 + hk - (v ? n_heads : 0) < a.n_kv, a.status)) f(k, at, m);
-        }
-        c += step_c;
-        r += step_r;
-        hk += step_hk;
-        if (c >= upr) {
-          c -= upr;
-          ++r;
-        }
-        if (r >= rows) {
-          r -= rows;
-          ++hk;
+    for (int k = 0; k < COMMIT_UNITS; ++k) {
+      from[k] = nullptr;
+      to[k] = 0;
+      if (hk < 2 * n_heads && moves[r].x >= 0) {
+        const int2 m = moves[r];
+        const int v = hk >= n_heads, g = g0 + hk - (v ? n_heads : 0);
+        const size_t row = (size_t)m.x + (size_t)g * step;
+        if (bc_ok(row < a.layer_rows && (size_t)m.y + (size_t)g * step < a.layer_rows, a.status)) {
+          from[k] = reinterpret_cast<const uint4*>(v ? a.v : a.k) + (a.layer + l0) * layer_units + row * upr + c;
+          to[k] = m.y - m.x;
         }
       }
+      c += step_c;
+      r += step_r;
+      hk += step_hk;
+      if (c >= upr) {
+        c -= upr;
+        ++r;
+      }
+      if (r >= rows) {
+        r -= rows;
+        ++hk;
+      }
+    }
+    uint4 x[2][COMMIT_UNITS];
+    auto load = [&](int l, uint4* y) {
+#pragma unroll
+      for (int k = 0; k < COMMIT_UNITS; ++k)
+        if (from[k]) y[k] = from[k][(l - l0) * layer_units];
     };
-    uint4 x[UNITS];
-    walk([&](int k, const uint4* at, int2 m) { x[k] = at[(size_t)m.x * upr]; });
-    __syncthreads();  // the chunk is read: its slots may be written
-    walk([&](int k, uint4* at, int2 m) { at[(size_t)m.y * upr] = x[k]; });
+    auto store = [&](int l, const uint4* y) {
+      __syncthreads();  // every thread has read its rows of this layer: they may be written
+#pragma unroll
+      for (int k = 0; k < COMMIT_UNITS; ++k)
+        if (from[k]) const_cast<uint4*>(from[k])[(l - l0) * layer_units + (long long)to[k] * upr] = y[k];
+    };
+    load(l0, x[0]);
+    for (int l = l0; l < l1; l += 2) {
+      if (l + 1 < l1) load(l + 1, x[1]);
+      store(l, x[0]);
+      if (l + 1 == l1) break;
+      if (l + 2 < l1) load(l + 2, x[0]);
+      store(l + 1, x[1]);
+    }
   }
 }
 
@@ -187,25 +211,32 @@ constexpr int BINS = 2048;
 // Weights in ascending order as unsigned numbers: -0 as 0, NaN below everything.
 __device__ __forceinline__ uint32_t order_of(float w) {
   const uint32_t u = __float_as_uint(w + 0.f);
-  return w != w ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return w != w ? 0u : u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
 // One CTA of T threads per (layer, sequence, K/V head): the m-th largest of the weights
-// between the first and the recent slots by three counting passes of 11, 11 and 10
-// bits, then one ordered pass that lists what stays and moves its weights. A warp owns
-// consecutive slots, 32 at a time, so ranks within it are bit counts and the warps
-// exchange one pair of counts. Up to 8192 weights are read once and stay in shared
-// memory (in order_of's form; the list tells where the others lie), longer lists are
-// read again for every pass, 8192 at a time.
+// between the first and the recent slots, by counting how many have each value of
+// their upper 11 bits, then of the next 11 and the last 10 among those that share the
+// found ones; then one ordered pass that lists what stays and moves its weights. A
+// warp owns consecutive slots, 32 at a time, so ranks within it are bit counts and
+// the warps exchange one pair of counts. Up to 8192 weights are read once and stay in
+// shared memory; longer lists are read again for every pass, 8192 at a time. Bound by
+// the instructions per weight, so the second and third counts look only at the weights
+// that share the first 11 bits, which are few: listed while they fit into LISTED.
+constexpr int LISTED = 1024;  // with a span's weights and the bins just below 48 KB
 template <int T>
 __global__ void __launch_bounds__(T) evict_select_kernel(EvictArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   constexpr int WARPS = T / 32, PER = BINS / T;
+  static_assert((SPAN + BINS + BINS / 8 + LISTED + 2 * WARPS + 4) * 4 <= 48 * 1024, "without an opt-in");
+  static_assert(SPAN / T <= 32, "a thread's slots of a span are the bits of a word");
   extern __shared__ float held[];  // [min(SPAN, most slots)]
-  __shared__ uint32_t bins[BINS];
+  __shared__ uint32_t bins[BINS + BINS / 8];  // bin i at i + i / 8: a thread's bins lie in a row, and conflict-free
+  auto bin = [&](uint32_t i) -> uint32_t& { return bins[i + (i >> 3)]; };
+  __shared__ uint32_t listed[LISTED];
   __shared__ int2 part[WARPS];
-  __shared__ uint32_t found[2];
+  __shared__ uint32_t found[2], n_listed;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint32_t below = (1u << lane) - 1u;
   const int b = (int)(blockIdx.x / a.n_kv % a.B);
@@ -217,9 +248,22 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictArgs a) {
   const bool all = n <= a.keep;
   const int lo = a.first, hi = n - a.recent;  // candidates
   auto load = [&](int s0) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = t; i < min(SPAN, n - s0); i += T) held[i] = w[s0 + i];
     __syncthreads();
+  };
+  // f for every candidate's order, a span at a time
+  auto candidates = [&](bool again, auto&& f) {
+#pragma unroll 1
+    for (int s0 = 0; s0 < n; s0 += SPAN) {
+      if (n > SPAN && (s0 > 0 || again)) {
+        __syncthreads();
+        load(s0);
+      }
+      const int to = min(SPAN, hi - s0);
+#pragma unroll 4
+      for (int i = max(0, lo - s0) + t; i < to; i += T) f(order_of(held[i]));
+    }
   };
   // sums over the warps in front of this one, and over all
   auto across = [&](int2 mine, int2& all) {
@@ -238,60 +282,60 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictArgs a) {
     all = make_int2(__shfl_sync(0xffffffffu, up.x, WARPS - 1), __shfl_sync(0xffffffffu, up.y, WARPS - 1));
     return make_int2(__shfl_sync(0xffffffffu, up.x - c.x, warp), __shfl_sync(0xffffffffu, up.y - c.y, warp));
   };
-  for (int i = t; i < BINS; i += T) bins[i] = 0;
-  load(0);
-  uint32_t least = 0, ties = 0;               // the smallest weight that stays, and how many equal to it
   int want = a.keep - a.first - a.recent;
-  if (!all && want > 0) {
-    int shift = 21;
-    uint32_t prefix = 0, mask = 0;
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int width = pass == 2 ? 10 : 11;
-#pragma unroll 1
-      for (int s0 = 0; s0 < n; s0 += SPAN) {
-        if (n > SPAN && (s0 > 0 || pass > 0)) {
-          __syncthreads();
-          load(s0);
-        }
-        const int from = max(0, lo - s0), to = min(SPAN, hi - s0);
-#pragma unroll 4
-        for (int i = from + t; i < to; i += T) {
-          const uint32_t u = order_of(held[i]);
-          if ((u & mask) == prefix) atomicAdd(&bins[(u >> shift) & ((1u << width) - 1u)], 1u);
-        }
-      }
-      __syncthreads();
-      // suffix sums from the largest bin on: thread t has the PER bins below BINS - PER t
-      const int top = BINS - 1 - PER * t;
-      uint32_t c[PER], sum = 0;
+  // the bin that the want-th largest is in; want becomes its rank there; the bins are 0 again
+  auto find = [&] {
+    __syncthreads();
+    // suffix sums from the largest bin on: thread t has the PER bins below BINS - PER t
+    const int top = BINS - 1 - PER * t;
+    uint32_t c[PER], sum = 0;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        sum += c[k] = bins[top - k];
-        bins[top - k] = 0;  // for the next pass
-      }
-      uint32_t upto = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      int2 total;
-      const int2 mine = make_int2((int)__shfl_sync(0xffffffffu, upto, 31), 0);
-      uint32_t before = upto - sum + (uint32_t)across(mine, total).x;
-      if (before < (uint32_t)want && before + sum >= (uint32_t)want) {
-        int k = 0;
-        while (before + c[k] < (uint32_t)want) before += c[k++];
-        found[0] = (uint32_t)(top - k);
-        found[1] = before;
-      }
-      __syncthreads();
-      prefix |= found[0] << shift;
-      mask |= ((1u << width) - 1u) << shift;
-      want -= (int)found[1];
-      shift = pass == 0 ? 10 : 0;
+    for (int k = 0; k < PER; ++k) {
+      sum += c[k] = bin(top - k);
+      bin(top - k) = 0;
     }
-    least = prefix;
+    uint32_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    int2 total;
+    const int2 mine = make_int2((int)__shfl_sync(0xffffffffu, upto, 31), 0);
+    uint32_t before = upto - sum + (uint32_t)across(mine, total).x;
+    if (before < (uint32_t)want && before + sum >= (uint32_t)want) {
+      int k = 0;
+      while (before + c[k] < (uint32_t)want) before += c[k++];
+      found[0] = (uint32_t)(top - k);
+      found[1] = before;
+    }
+    __syncthreads();
+    want -= (int)found[1];
+    return found[0];
+  };
+  for (int i = t; i < BINS + BINS / 8; i += T) bins[i] = 0;
+  if (t == 0) n_listed = 0;
+  load(0);
+  uint32_t least = 0, ties = 0;  // the smallest weight that stays, and how many equal to it
+  if (!all && want > 0) {
+    candidates(false, [&](uint32_t u) { atomicAdd(&bin(u >> 21), 1u); });
+    const uint32_t upper = find();
+    candidates(true, [&](uint32_t u) {
+      if (u >> 21 != upper) return;
+      atomicAdd(&bin((u >> 10) & 2047u), 1u);
+      const uint32_t at = atomicAdd(&n_listed, 1u);
+      if (at < LISTED) listed[at] = u;
+    });
+    const uint32_t middle = upper << 11 | find();
+    auto last = [&](uint32_t u) {
+      if (u >> 10 == middle) atomicAdd(&bin(u & 1023u), 1u);
+    };
+    if (n_listed <= LISTED) {
+      for (int i = t; i < (int)n_listed; i += T) last(listed[i]);
+    } else {
+      candidates(true, last);
+    }
+    least = middle << 10 | find();
     ties = (uint32_t)want;
   }
   // What stays, in order: the spans one after the other, the warps of a span in parallel.
@@ -306,35 +350,36 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictArgs a) {
     }
     const int m = min(SPAN, n - s0), own = (m + T - 1) / T;  // 32-slot steps of a warp
     const int at0 = warp * 32 * own + lane;
-    // whether slot at0 + 32 k stays whatever the ties (1), or is one (2)
-    auto kind = [&](int i) {
-      if (i >= m) return 0;
-      if (all || s0 + i < lo || s0 + i >= hi) return 1;
-      const uint32_t u = order_of(held[i]);
-      return none ? 0 : u > least ? 1 : u == least ? 2 : 0;
-    };
-    int2 count = make_int2(0, 0);
+    uint32_t sure = 0, tie = 0;  // bit k: slot at0 + 32 k stays whatever the ties, is one
+#pragma unroll 4
     for (int k = 0; k < own; ++k) {
-      const int x = kind(at0 + 32 * k);
-      count.x += __popc(__ballot_sync(0xffffffffu, x == 1));
-      count.y += __popc(__ballot_sync(0xffffffffu, x == 2));
+      const int i = at0 + 32 * k;
+      if (i >= m) break;
+      const bool always = all || s0 + i < lo || s0 + i >= hi;
+      const uint32_t u = order_of(held[i]);
+      sure |= (uint32_t)(always || (!none && u > least)) << k;
+      tie |= (uint32_t)(!always && !none && u == least) << k;
     }
     int2 sums;
-    const int2 front = across(count, sums);
+    const int2 front = across(make_int2(__reduce_add_sync(0xffffffffu, __popc(sure)),
+                                        __reduce_add_sync(0xffffffffu, __popc(tie))), sums);
     // the ties that stay are the first ones: `ties` of them in all
     int rank = tied + front.y, at = done + front.x + max(0, min(front.y, (int)ties - tied));
+#pragma unroll 4
     for (int k = 0; k < own; ++k) {
-      const int i = at0 + 32 * k, x = kind(i);
-      const uint32_t me = __ballot_sync(0xffffffffu, x == 2);
-      const bool s = x == 1 || (x == 2 && rank + __popc(me & below) < (int)ties);
+      bool s = sure >> k & 1u;
+      const uint32_t me = __ballot_sync(0xffffffffu, tie >> k & 1u);
+      if (me) {
+        s = s || ((tie >> k & 1u) && rank + __popc(me & below) < (int)ties);
+        rank += __popc(me);
+      }
       const uint32_t ms = __ballot_sync(0xffffffffu, s);
-      const int to = at + __popc(ms & below);
+      const int i = at0 + 32 * k, to = at + __popc(ms & below);
       if (s && bc_ok(to < a.keep && to <= s0 + i, a.status)) {
         kept[to] = s0 + i;
         out[to] = held[i];
       }
       at += __popc(ms);
-      rank += __popc(me);
     }
     done += sums.x + max(0, min(sums.y, (int)ties - tied));
     tied += sums.y;
@@ -347,14 +392,15 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictArgs a) {
 }  // namespace
 
 cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t st) {
-  const int upr = a.row_bytes / 16, room = MOVE_THREADS * UNITS / (2 * upr);  // rows of one head's K and V
-  // as many heads as a block has room for, but blocks for every SM
-  const long long pairs = (long long)a.layers * a.B;
-  const int heads = (int)std::max<long long>(
-      1, std::min<long long>({room / a.list_ld, a.n_kv, a.n_kv * pairs / (2 * a.sm_count)}));
-  const int rows = std::min(a.list_ld, room / heads);
-  return launch_k(cache_commit_kernel, dim3((a.n_kv + heads - 1) / heads, a.B, a.layers), dim3(MOVE_THREADS),
-                  rows * sizeof(int2), st, 0, a, heads, rows);
+  const int upr = a.row_bytes / 16, room = MOVE_THREADS * COMMIT_UNITS / (2 * upr);  // rows of one head's K and V
+  const int heads = std::max(1, std::min(room / a.list_ld, a.n_kv)), rows = std::min(a.list_ld, room / heads);
+  const int groups = (a.n_kv + heads - 1) / heads;
+  // runs of layers that give every SM its 3 blocks
+  const long long pairs = (long long)groups * a.B;
+  const int runs = (int)std::min<long long>(a.layers, (3 * a.sm_count + pairs - 1) / pairs);
+  const int run = (a.layers + runs - 1) / runs;
+  return launch_k(cache_commit_kernel, dim3(groups, a.B, (a.layers + run - 1) / run), dim3(MOVE_THREADS),
+                  rows * sizeof(int2), st, 0, a, heads, rows, run);
 }
 
 cudaError_t launch_cache_evict(const CacheMoveArgs& a, cudaStream_t st) {
