@@ -1553,6 +1553,10 @@ int llama_op_attention_tree(llama_ctx* c, const void* q, int32_t n_rows, const i
   TRY(decode_maps(c, kv, n_rows, 128 / (cf.n_q_heads / cf.n_kv_heads), &a));
   a.partial = c->at<float>(c->L.spart);
   Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
+  if (tree_own_applies(a)) {
+    c->launches++;
+    return cuda_rc(launch_tree_own(a, c->stream));
+  }
   c->launches += 2;
   return cuda_rc(launch_tree_tc(a, c->stream));
 }

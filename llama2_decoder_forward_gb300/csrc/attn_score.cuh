@@ -1,5 +1,6 @@
 // Pieces shared by the attention kernels with capped or biased scores: a
-// document's rows, a decode row's last key, the cap, how partial results are merged.
+// document's rows, a decode row's last key, what a tree's row sees, the cap, how
+// partial results are merged.
 #pragma once
 
 #include "common.cuh"
@@ -26,6 +27,27 @@ __device__ __forceinline__ int key_position(int pos, int key_limit) {
 
 // Positions of drafted rows are cut to 0 .. kMaxPos, so that distances stay in an int.
 constexpr int kMaxPos = 1 << 30;
+
+// What rows of drafted trees see of each other.
+struct TreeMask {
+  const uint32_t* bits;  // [rows][words], or null: a row sees the rows up to itself
+  int words;
+};
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// Rows 32 j .. of a tree that its row i (`row` of all) sees; `there` rows of the tree are in the cache.
+__device__ __forceinline__ uint32_t tree_word(const TreeMask& t, size_t row, int i, int there, int j) {
+  uint32_t m = low_bits(min(there, t.bits ? 0x7fffffff : i + 1) - 32 * j);
+  if (t.bits && m) m &= j < t.words ? t.bits[row * t.words + j] : 0u;
+  return m;
+}
+// Which of the 32 keys from the tree's x-th row on it sees; x may be negative: cached keys, all visible.
+__device__ __forceinline__ uint32_t tree_bits(const TreeMask& t, size_t row, int i, int there, int x) {
+  if (x <= -32) return ~0u;
+  if (x < 0) return low_bits(-x) | tree_word(t, row, i, there, 0) << -x;
+  const int j = x >> 5, s = x & 31;
+  const uint32_t a = tree_word(t, row, i, there, j);
+  return s ? __funnelshift_r(a, tree_word(t, row, i, there, j + 1), s) : a;
+}
 
 // The maximum that a partial result of sum l is merged with: a maximum passes over
 // NaN scores, and without a finite one beside them the part would count as

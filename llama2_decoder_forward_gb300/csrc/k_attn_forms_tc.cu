@@ -107,8 +107,8 @@ struct FormsParams {
   float own_items;                          // how many those are
   // trees: out, cu_rows, n_rows, n_docs as documents; the cache as a prefix
   const int32_t *start_pos, *row_pos;
-  const uint32_t* mask;
-  int mask_words, least_tiles;
+  TreeMask tree;
+  int least_tiles;
   struct TreeShared* shared;                // [CTAs] the item that each CTA begins and does not end,
   int* shared_parts;                        // and how many partial results it has (0: no such item)
   float poly[13];                           // KCapFixed: kTanh times powers of scale / cap
@@ -562,22 +562,6 @@ __device__ __forceinline__ void tree_work(const FormsParams& p, FormsWork& w) {
   w.nt1 = p.alternate ? w.n_tiles / 2 : w.q0 + p.rows_seq < w.n ? w.n_tiles : 0;
   w.last_rows = w.kmax - (w.t0 + w.n_tiles - 1) * TN;
 }
-// Which of the 32 keys from the x-th row of its tree on (x may be negative: cached
-// keys, all visible) row i of the tree attends; `there` rows of the tree are in the cache.
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-__device__ __forceinline__ uint32_t tree_word(const FormsParams& p, size_t row, int i, int there, int j) {
-  uint32_t m = low_bits(min(there, p.mask ? INT_MAX : i + 1) - 32 * j);
-  if (p.mask && m) m &= j < p.mask_words ? p.mask[row * p.mask_words + j] : 0u;
-  return m;
-}
-__device__ __forceinline__ uint32_t tree_bits(const FormsParams& p, size_t row, int i, int there, int x) {
-  if (x <= -32) return ~0u;
-  if (x < 0) return low_bits(-x) | tree_word(p, row, i, there, 0) << -x;
-  const int j = x >> 5, s = x & 31;
-  const uint32_t a = tree_word(p, row, i, there, j);
-  return s ? __funnelshift_r(a, tree_word(p, row, i, there, j + 1), s) : a;
-}
-
 // 32 outputs of a row, times inv, as bf16
 __device__ __forceinline__ void store_out(const FormsParams& p, bf16* dst, const float* u, float inv) {
 #pragma unroll
@@ -1164,8 +1148,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       uint32_t sees[2] = {~0u, ~0u};  // trees: the visible ones of this thread's keys
       if (TREE && part) {
         const int there = w.kmax - w.start;
-        sees[0] = row_ok ? tree_bits(p, row, tree_i, there, -left) : 0u;
-        sees[1] = row_ok ? tree_bits(p, row, tree_i, there, 32 - left) : 0u;
+        sees[0] = row_ok ? tree_bits(p.tree, row, tree_i, there, -left) : 0u;
+        sees[1] = row_ok ? tree_bits(p.tree, row, tree_i, there, 32 - left) : 0u;
       }
       // a warp that sees none of the tile's keys (above the diagonal): its weights are 0
       const bool none = !__any_sync(0xffffffffu, TREE ? (sees[0] | sees[1]) != 0 : left > 0);
@@ -1431,11 +1415,15 @@ FormsKernel forms_kernel(int kind) {
 
 // Merges the partial results of the tree items that several CTAs share: a warp takes 2
 // rows and 4 partial results at a time, whose loads hide each other's latency. Every block makes the list of those items, so that no block is without work.
+struct JoinItem {
+  int cta, parts;  // the CTA that begins it
+  TreeShared of;
+};
 constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2, JOIN_AHEAD = 4, JOIN_PARTS = 32 / JOIN_ROWS;
 __global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(FormsParams p, int ctas) {
   grid_dep_wait();
   grid_dep_launch();
-  extern __shared__ int2 items[];  // [ctas] CTA that begins the item, its partial results
+  extern __shared__ JoinItem items[];  // [ctas]
   __shared__ int n_items;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (warp == 0) {
@@ -1443,7 +1431,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(Form
     for (int c0 = 0; c0 < ctas; c0 += 32) {
       const int parts = c0 + lane < ctas ? p.shared_parts[c0 + lane] : 0;
       const uint32_t m = __ballot_sync(0xffffffffu, parts > 0);
-      if (parts > 0) items[n + __popc(m & ((1u << lane) - 1u))] = make_int2(c0 + lane, parts);
+      if (parts > 0) items[n + __popc(m & ((1u << lane) - 1u))] = JoinItem{c0 + lane, parts, p.shared[c0 + lane]};
       n += __popc(m);
     }
     if (lane == 0) n_items = n;
@@ -1452,16 +1440,16 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(Form
   const int rows_tile = p.rows_seq * p.G, rows_slot = p.alternate ? TM : 2 * TM;
   const int row_l = lane / JOIN_PARTS, part_l = lane % JOIN_PARTS;  // of this lane's maximum and sum
   for (int task = blockIdx.x * JOIN_WARPS + warp; task < n_items * (rows_slot / JOIN_ROWS); task += gridDim.x * JOIN_WARPS) {
-    const int2 which = items[task / (rows_slot / JOIN_ROWS)];
-    const int r0 = task % (rows_slot / JOIN_ROWS) * JOIN_ROWS, tile = r0 / TM, rt0 = r0 - tile * TM, parts = which.y;
-    const TreeShared it = p.shared[which.x];
+    const JoinItem& item = items[task / (rows_slot / JOIN_ROWS)];
+    const TreeShared& it = item.of;
+    const int r0 = task % (rows_slot / JOIN_ROWS) * JOIN_ROWS, tile = r0 / TM, rt0 = r0 - tile * TM, parts = item.parts;
     const int q0 = it.q0 + tile * p.rows_seq;
     // rows of nobody lie behind the others
     if (rt0 >= rows_tile || q0 + rt0 / p.G >= it.n ||
-        !bc_ok((size_t)2 * (which.x + parts) * rows_slot <= p.partials, p.status))
+        !bc_ok((size_t)2 * (item.cta + parts) * rows_slot <= p.partials, p.status))
       continue;
     // partial s of row r0
-    auto at = [&](int s) { return (size_t)(s == 0 ? it.first : 2 * (which.x + s)) * rows_slot + r0; };
+    auto at = [&](int s) { return (size_t)(s == 0 ? it.first : 2 * (item.cta + s)) * rows_slot + r0; };
     float m = -INFINITY, l = 0.f;  // of row row_l
     float4 v[JOIN_ROWS];
 #pragma unroll
@@ -1637,8 +1625,7 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
   p.n_docs = a.B;
   p.start_pos = a.start_pos;
   p.row_pos = a.row_pos;
-  p.mask = a.mask;
-  p.mask_words = a.mask_words;
+  p.tree = TreeMask{a.mask, a.mask_words};
   p.page_table = a.page_table;
   p.layer = a.layer;
   p.page_size = a.page_size;
@@ -1660,7 +1647,8 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
   const cudaError_t e = launch_k(forms_kernel<MTree>(kind), dim3(ctas), dim3(FORMS_THREADS), FORMS_SMEM, st, 0,
                                  *a.map_q, *a.map_k, *a.map_v, *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess || ctas < 2) return e;
-  return launch_k(attn_tree_join_kernel, dim3(4 * ctas), dim3(32 * JOIN_WARPS), ctas * sizeof(int2), st, 0, p, ctas);
+  return launch_k(attn_tree_join_kernel, dim3(4 * ctas), dim3(32 * JOIN_WARPS), ctas * sizeof(JoinItem),
+                  st, 0, p, ctas);
 }
 
 }  // namespace llgb

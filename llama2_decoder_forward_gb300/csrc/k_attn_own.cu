@@ -83,7 +83,45 @@ struct OwnParams {
   float* scores;
   float* weights;              // [B][n_kv][ld]
   int64_t ld;
+  // small trees: every sequence's rows in blocks of tree_rows
+  const int32_t *cu_rows, *start_pos, *row_pos;
+  TreeMask tree;
+  int n_rows, n_seq, tree_rows;
 };
+
+// What a launch works on: a decode row per sequence; the same with its scores kept; the
+// rows of small trees.
+enum { ODecode, OWeigh, OTree };
+
+// The rows of a CTA: the query heads of one K/V head, of one decode row or of several
+// tree rows (row r: head r % G of tree row i0 + r / G).
+struct OwnRows {
+  int b, g, count;             // sequence, K/V head, rows
+  int pos;                     // decode: the row's position
+  int lo, i0, start, there;    // trees: the sequence's first row, the block's, cached keys, tree rows in the cache
+};
+// Which (row, query head) of q and the output row r is.
+template <int MODE>
+__device__ __forceinline__ size_t row_head(const OwnParams& p, const OwnRows& R, int r) {
+  if (MODE != OTree) return (size_t)R.b * p.n_q + (size_t)R.g * p.G + r;
+  const int i = r / p.G;
+  return (size_t)(R.lo + R.i0 + i) * p.n_q + (size_t)R.g * p.G + (r - i * p.G);
+}
+template <int MODE>
+__device__ __forceinline__ float row_slope(const OwnParams& p, const OwnRows& R, int r) {
+  return r < R.count ? __ldcg(p.slopes + R.g * p.G + (MODE == OTree ? r % p.G : r)) * 1.4426950408889634f : 0.f;
+}
+// Trees: the position of row r, of key k (n keys in all), and the visible ones of 32 keys from k on.
+__device__ __forceinline__ int tree_pos(const OwnParams& p, const OwnRows& R, int x) {
+  return p.row_pos ? min(max(__ldcg(p.row_pos + R.lo + x), 0), kMaxPos) : R.start + x;
+}
+__device__ __forceinline__ int tree_key_pos(const OwnParams& p, const OwnRows& R, int k) {
+  return k < R.start || k - R.start >= R.there ? k : tree_pos(p, R, k - R.start);
+}
+__device__ __forceinline__ uint32_t row_sees(const OwnParams& p, const OwnRows& R, int r, int k) {
+  const int i = R.i0 + r / p.G;
+  return r < R.count ? tree_bits(p.tree, (size_t)R.lo + i, i, R.there, k - R.start) : 0u;
+}
 
 __device__ __forceinline__ void consumers_bar() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
@@ -144,27 +182,30 @@ __device__ __forceinline__ void clean_v(uint8_t* v, int lead, int valid, int lan
   __syncwarp();
 }
 
-// Groups of up to 8 heads: keys on the MMA rows. Lane l tracks heads 2(l%4)
-// and 2(l%4) + 1. Leaves (max, sum, O) of this warp in shared memory.
-template <bool WEIGH>
+// Up to 8 rows: keys on the MMA rows. Lane l tracks rows 2(l%4) and 2(l%4) + 1. Leaves (max, sum, O) of this warp in shared memory.
+template <int MODE>
 __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, uint64_t* full,
-                                             uint64_t* empty, volatile uint32_t* stop, int b, int g,
-                                             int kbeg, int kend, int pos, int warp, int lane) {
-  const int G = p.G, hq = lane >> 2, hc = 2 * (lane & 3);
+                                             uint64_t* empty, volatile uint32_t* stop, const OwnRows& R,
+                                             int kbeg, int kend, int warp, int lane) {
+  const int G = R.count, hq = lane >> 2, hc = 2 * (lane & 3);
   uint32_t qf[8][2];  // Q^T fragments: head lane/4
-  const bf16* qb = p.q + ((size_t)b * p.n_q + (size_t)g * G + hq) * HD;
+  const bf16* qb = p.q + row_head<MODE>(p, R, hq) * HD;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
     const int col = kk * 16 + 2 * (lane & 3);
     qf[kk][0] = hq < G ? __ldcg(reinterpret_cast<const unsigned*>(qb + col)) : 0u;
     qf[kk][1] = hq < G ? __ldcg(reinterpret_cast<const unsigned*>(qb + col + 8)) : 0u;
   }
-  constexpr float kLog2e = 1.4426950408889634f;
   const ScoreConst sc(p.scale, p.cap);
   float sl[2] = {0.f, 0.f};
   if (p.slopes) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) sl[j] = hc + j < G ? __ldcg(p.slopes + g * G + hc + j) * kLog2e : 0.f;
+    for (int j = 0; j < 2; ++j) sl[j] = row_slope<MODE>(p, R, hc + j);
+  }
+  int pos[2] = {0, 0};  // trees: the two rows' positions, for the bias
+  if (MODE == OTree && p.slopes) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) pos[j] = hc + j < G ? tree_pos(p, R, R.i0 + (hc + j) / p.G) : 0;
   }
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[8][4];
 #pragma unroll
@@ -195,15 +236,22 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
         ldsm_x4(kbase + (kk >> 2) * HALF + swz128(row, chunk), a[0], a[1], a[2], a[3]);
         mma_bf16_16816((kk & 1) ? s1 : s0, a, qf[kk][0], qf[kk][1]);
       }
+      uint32_t sees[2] = {~0u, ~0u};  // trees: the keys that the two rows see
+      if (MODE == OTree && k0 + SUB > R.start) {
+        sees[0] = row_sees(p, R, hc, k0);
+        sees[1] = row_sees(p, R, hc + 1, k0);
+      }
       float sv[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = (lane >> 2) + (i >= 2 ? 8 : 0);
         float x = score(sc, s0[i] + s1[i]);
-        if (p.slopes) x = fmaf(-sl[i & 1], (float)(pos - k0 - key), x);
-        sv[i] = key >= lead && key < valid ? x : -INFINITY;
-        if (WEIGH && key < valid && hc + (i & 1) < G)
-          p.scores[((size_t)b * p.n_q + g * G + hc + (i & 1)) * p.ld + k0 + key] = x;
+        if (p.slopes)
+          x = fmaf(-sl[i & 1], MODE == OTree ? fabsf((float)(pos[i & 1] - tree_key_pos(p, R, k0 + key)))
+                                             : (float)(R.pos - k0 - key), x);
+        sv[i] = key >= lead && key < valid && (MODE != OTree || (sees[i & 1] >> key & 1u)) ? x : -INFINITY;
+        if (MODE == OWeigh && key < valid && hc + (i & 1) < G)
+          p.scores[row_head<MODE>(p, R, hc + (i & 1)) * p.ld + k0 + key] = x;
       }
       float corr[2];
 #pragma unroll
@@ -277,13 +325,13 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
 }
 
 // Groups of 9 to 16 heads: heads on the MMA rows (zero-padded to 16).
-template <bool WEIGH>
+template <int MODE>
 __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem, uint64_t* full,
-                                              uint64_t* empty, volatile uint32_t* stop, int b, int g,
-                                              int kbeg, int kend, int pos, int warp, int lane) {
-  const int G = p.G, r0 = lane >> 2;
+                                              uint64_t* empty, volatile uint32_t* stop, const OwnRows& R,
+                                              int kbeg, int kend, int warp, int lane) {
+  const int G = R.count, r0 = lane >> 2;
   uint32_t qa[8][4];
-  const bf16* qb = p.q + ((size_t)b * p.n_q + (size_t)g * G) * HD;
+  const bf16* qb = p.q + row_head<MODE>(p, R, 0) * HD;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
@@ -291,12 +339,11 @@ __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem,
       const int row = r0 + 8 * (i & 1), col = kk * 16 + 2 * (lane & 3) + 8 * (i >> 1);
       qa[kk][i] = row < G ? __ldcg(reinterpret_cast<const unsigned*>(qb + row * HD + col)) : 0u;
     }
-  constexpr float kLog2e = 1.4426950408889634f;
   const ScoreConst sc(p.scale, p.cap);
   float sl[2] = {0.f, 0.f};
   if (p.slopes) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) sl[j] = r0 + 8 * j < G ? __ldcg(p.slopes + g * G + r0 + 8 * j) * kLog2e : 0.f;
+    for (int j = 0; j < 2; ++j) sl[j] = row_slope<MODE>(p, R, r0 + 8 * j);
   }
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[16][4];
 #pragma unroll
@@ -337,10 +384,10 @@ __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem,
         for (int i = 0; i < 4; ++i) {
           const int key = nb * 8 + 2 * (lane & 3) + (i & 1);
           float x = score(sc, sv[nb][i]);
-          if (p.slopes) x = fmaf(-sl[i >> 1], (float)(pos - k0 - key), x);
+          if (p.slopes) x = fmaf(-sl[i >> 1], (float)(R.pos - k0 - key), x);
           sv[nb][i] = key >= lead && key < valid ? x : -INFINITY;
-          if (WEIGH && key < valid && r0 + 8 * (i >> 1) < G)
-            p.scores[((size_t)b * p.n_q + g * G + r0 + 8 * (i >> 1)) * p.ld + k0 + key] = x;
+          if (MODE == OWeigh && key < valid && r0 + 8 * (i >> 1) < G)
+            p.scores[row_head<MODE>(p, R, r0 + 8 * (i >> 1)) * p.ld + k0 + key] = x;
           mx[i >> 1] = fmaxf(mx[i >> 1], sv[nb][i]);
         }
 #pragma unroll
@@ -497,7 +544,33 @@ __device__ __forceinline__ void store_row(bf16* dst, int lane, const RowSum& r) 
       make_uint2(pack_bf16(r.o.x * i, r.o.y * i), pack_bf16(r.o.z * i, r.o.w * i));
 }
 
-template <bool KEYS, bool WEIGH>
+// Small trees: the z-th block of tree_rows rows, for a whole warp; false: there are fewer.
+__device__ __forceinline__ bool tree_block(const OwnParams& p, int z, int lane, int& b, int& i0, int& lo, int& n) {
+  for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+    int my_lo = 0, my_n = 0;
+    if (b0 + lane < p.n_seq) doc_rows(p.cu_rows, b0 + lane, p.n_rows, nullptr, my_lo, my_n);
+    const int blocks = (my_n + p.tree_rows - 1) / p.tree_rows;
+    int upto = blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, z < upto);
+    if (m) {
+      const int w = __ffs(m) - 1;
+      b = b0 + w;
+      i0 = (z - __shfl_sync(0xffffffffu, upto - blocks, w)) * p.tree_rows;
+      lo = __shfl_sync(0xffffffffu, my_lo, w);
+      n = __shfl_sync(0xffffffffu, my_n, w);
+      return true;
+    }
+    z -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+
+template <bool KEYS, int MODE>
 __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     attn_own_kernel(const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapV,
@@ -511,6 +584,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   volatile uint32_t* stop = reinterpret_cast<volatile uint32_t*>(empty + STAGES);
   const int split = blockIdx.x, g = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  OwnRows R{};
   // With a prefix kernel before this one, what this one reads is complete: that
   // kernel waited for it. One CTA's producer waits for the prefix kernel itself,
   // so that whoever waits for this kernel has waited for both.
@@ -537,7 +611,19 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     tma_prefetch_desc(&mapV16);
   }
   int b = blockIdx.z, pos;
-  if (p.sorted) {
+  if (MODE == OTree) {
+    int n;
+    if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0 && warp == 0)  // bad bounds are flagged once
+      for (int i = lane, x, y; i < p.n_seq; i += 32) doc_rows(p.cu_rows, i, p.n_rows, p.status, x, y);
+    if (!tree_block(p, blockIdx.z, lane, b, R.i0, R.lo, n)) return;  // a cluster's CTAs all do
+    const int start = p.start_pos[b];
+    const long long end = (long long)start + n;
+    if ((start < 0 || end > p.key_limit) && split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
+    pos = (start < 0 ? 0 : (int)(end < p.key_limit ? end : p.key_limit)) - 1;  // the last key
+    R.start = start < 0 ? 0 : min(start, pos + 1);
+    R.there = pos + 1 - R.start;
+    R.count = min(p.tree_rows, n - R.i0) * p.G;
+  } else if (p.sorted) {
     // the blockIdx.z-th longest sequence, so that the longest start first: one key
     // of 32 bits per sequence, its length and (ties) its number
     int* key = reinterpret_cast<int*>(smem + OFF_SORT);
@@ -567,8 +653,14 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   // the producer's first page ids, without splits loaded beside the position
   int page = warp == 4 && p.splits == 1 ? own_page(p, b, p.base + lane * SUB) : 0;
   if (!p.sorted) __syncthreads();
-  if ((pos < 0 || pos >= p.key_limit) && split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
-  pos = key_position(pos, p.key_limit);
+  if (MODE != OTree) {
+    if ((pos < 0 || pos >= p.key_limit) && split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
+    pos = key_position(pos, p.key_limit);
+    R.count = p.G;
+  }
+  R.b = b;
+  R.g = g;
+  R.pos = pos;
   const int n = pos + 1;
   const int share = own_share(p, n), kbeg = p.base + split * share;
   const int kend = min(n, kbeg + share);
@@ -620,9 +712,9 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
       return;
     }
     if (KEYS)
-      consume_keys<WEIGH>(p, smem, full, empty, stop, b, g, kbeg, kend, pos, warp, lane);
+      consume_keys<MODE>(p, smem, full, empty, stop, R, kbeg, kend, warp, lane);
     else
-      consume_heads<WEIGH>(p, smem, full, empty, stop, b, g, kbeg, kend, pos, warp, lane);
+      consume_heads<MODE>(p, smem, full, empty, stop, R, kbeg, kend, warp, lane);
     consumers_bar();
     if (*stop && !p.cluster) return;
   } else if (warp == 4) {  // (a cluster's barriers do not count threads that left)
@@ -641,7 +733,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   // a cluster's rows: [16][128] outputs, then maximum and sum [16][2]
   float* mine = reinterpret_cast<float*>(smem) + 4 * 16 * HD + 128;
   static_assert((4 * 16 * HD + 128 + 16 * (HD + 2)) * 4 <= STAGES * STAGE, "the cluster's rows fit the ring");
-  for (int r = warp; r < p.G; r += 4) {  // a warp per row
+  for (int r = warp; r < R.count; r += 4) {  // a warp per row
     RowSum x;
     if (any && !*stop) {
       float mx = -INFINITY;
@@ -658,7 +750,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
         }
       }
     }
-    const size_t bh = (size_t)b * p.n_q + (size_t)g * p.G + r;
+    const size_t bh = row_head<MODE>(p, R, r);
     if (!bc_ok(bh < p.rows && (!p.join || bh * p.splits + split < p.own_room), p.status)) continue;
     if (p.cluster) {
       reinterpret_cast<float4*>(mine + r * HD)[lane] = x.o;
@@ -677,7 +769,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   if (!p.cluster) return;
   cluster_sync_all();
   // row r is folded by CTA r % splits of the cluster, in the order of the splits
-  for (int i = warp; i * p.splits + split < p.G; i += 4) {
+  for (int i = warp; i * p.splits + split < R.count; i += 4) {
     const int r = i * p.splits + split;
     const uint32_t ro = smem_u32(mine + r * HD) + 16 * lane, rm = smem_u32(mine + 16 * HD + 2 * r);
     float2 ml = make_float2(-INFINITY, 0.f);
@@ -697,7 +789,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
         x.add(fq, dsmem_ld4(dsmem_addr(ro, q)));
       }
     }
-    const size_t bh = (size_t)b * p.n_q + (size_t)g * p.G + r;
+    const size_t bh = row_head<MODE>(p, R, r);
     Parts<8> pre;
     pre.load(p.part_o, p.part_ml, bh * p.prefix_parts, parts, lane);
     pre.fold(parts, lane, x);
@@ -827,8 +919,9 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 4) attn_weights_kernel(OwnParam
 }  // namespace
 
 cudaError_t attn_own_prepare() {
-  const void* const all[] = {(const void*)attn_own_kernel<true, false>, (const void*)attn_own_kernel<false, false>,
-                             (const void*)attn_own_kernel<true, true>, (const void*)attn_own_kernel<false, true>};
+  const void* const all[] = {(const void*)attn_own_kernel<true, ODecode>, (const void*)attn_own_kernel<false, ODecode>,
+                             (const void*)attn_own_kernel<true, OWeigh>, (const void*)attn_own_kernel<false, OWeigh>,
+                             (const void*)attn_own_kernel<true, OTree>};
   for (const void* f : all) {
     const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)OWN_SMEM);
     if (e != cudaSuccess) return e;
@@ -936,9 +1029,9 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
   const dim3 grid(s.own_splits, a.n_kv, a.B), block(OWN_THREADS);
   const dim3 cluster(s.cluster ? s.own_splits : 0, 1, 1);
   const cudaError_t e =
-      p.G <= 8 ? launch_kc(attn_own_kernel<true, false>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
+      p.G <= 8 ? launch_kc(attn_own_kernel<true, ODecode>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
                            *a.map_v, *a.map_k16, *a.map_v16, p)
-               : launch_kc(attn_own_kernel<false, false>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
+               : launch_kc(attn_own_kernel<false, ODecode>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
                            *a.map_v, *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess || !s.join) return e;
   return launch_k(attn_own_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 0, p,
@@ -969,9 +1062,9 @@ cudaError_t launch_decode_weights(const SharedArgs& a, const SharedPlan& s, cons
   p.ld = w.ld;
   const dim3 grid(s.own_splits, a.n_kv, a.B), block(OWN_THREADS);
   const cudaError_t e =
-      p.G <= 8 ? launch_k(attn_own_kernel<true, true>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
+      p.G <= 8 ? launch_k(attn_own_kernel<true, OWeigh>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
                           *a.map_k16, *a.map_v16, p)
-               : launch_k(attn_own_kernel<false, true>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
+               : launch_k(attn_own_kernel<false, OWeigh>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
                           *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess) return e;
   return launch_weights<false>(p, a, st);
@@ -991,6 +1084,62 @@ cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cu
   p.weights = w.weights;
   p.ld = w.ld;
   return launch_weights<true>(p, a, st);
+}
+
+// Trees of few rows: blocks of 8 (row, head) pairs of a K/V head on this kernel, or 128
+// and 256 on the tensor-core kernel. In a cache with room for 4096 positions, this kernel and
+// that one: 16 sequences of 8 rows, 32 heads 104 and 122 us, 64 of one row, 32 / 8 heads
+// 104 and 112; two blocks (a second pass over the keys, mostly from L2) 8 sequences of 13
+// rows, 40 heads, up to 500 keys 19 and 32, up to 8000 138 and 108, up to 2000 capped 48
+// and 73 (the softmax of the other kernel works on all 128 rows); three 91 and 60. Where 8
+// CTAs for each (sequence, K/V head) are few and the context may be long, the other
+// kernel's equal shares count: one row, 8 K/V heads, 30000 keys 43 and 31 us.
+bool tree_own_applies(const TreeArgs& a) {
+  const int G = a.n_q / a.n_kv;
+  if (a.head_dim != HD || G > 8 || (long long)a.n_rows + a.B > 65535) return false;
+  const long long pairs = (long long)a.B * a.n_kv, rows = (a.n_rows + a.B - 1) / a.B;  // the mean
+  const long long blocks = (rows + 8 / G - 1) / (8 / G);
+  if (8 * pairs < 2 * a.sm_count && a.key_limit > 8192) return false;
+  return blocks == 1 || (blocks == 2 && (a.sc.cap > 0.f || a.sc.slopes || a.key_limit <= 2048));
+}
+
+cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st) {
+  OwnParams p{};
+  p.q = (const bf16*)a.q;
+  p.out = (bf16*)a.out;
+  p.page_table = a.page_table;
+  p.status = a.status;
+  p.n_q = a.n_q;
+  p.n_kv = a.n_kv;
+  p.G = a.n_q / a.n_kv;
+  p.layer = a.layer;
+  p.page_size = a.page_size;
+  p.capacity = a.capacity;
+  p.n_pages = a.n_pages;
+  p.max_pages = a.max_pages;
+  p.box_rows = a.box_rows;
+  p.key_limit = a.key_limit;
+  p.rows = (size_t)a.n_rows * a.n_q;
+  p.scale = a.sc.scale;
+  p.cap = a.sc.cap;
+  p.slopes = a.sc.slopes;
+  p.cu_rows = a.cu_rows;
+  p.start_pos = a.start_pos;
+  p.row_pos = a.row_pos;
+  p.tree = TreeMask{a.mask, a.mask_words};
+  p.n_rows = a.n_rows;
+  p.n_seq = a.B;
+  p.tree_rows = 8 / p.G;
+  const int blocks = a.n_rows / p.tree_rows + std::min(a.B, a.n_rows);  // an upper bound
+  const int pairs = std::max(a.B, a.n_rows / p.tree_rows) * a.n_kv;
+  int k = 1;
+  while (pairs * k < 2 * a.sm_count && k < 8 && a.key_limit / (2 * k) >= 64) k *= 2;
+  p.splits = k;
+  p.min_share = 64;
+  p.cluster = k > 1;
+  const dim3 grid(k, a.n_kv, blocks), cluster(k > 1 ? k : 0, 1, 1);
+  return launch_kc(attn_own_kernel<true, OTree>, grid, dim3(OWN_THREADS), OWN_SMEM, st, cluster, *a.map_k, *a.map_v,
+                   *a.map_k16, *a.map_v16, p);
 }
 
 }  // namespace llgb

@@ -668,6 +668,24 @@ def test_tree_long_items_per_cta(rows):
                heads=[0, 13, 31], calls=6)
 
 
+@pytest.mark.parametrize("nq,nkv", [(8, 1), (4, 4), (6, 2), (5, 1), (5, 5)])
+@pytest.mark.parametrize("slots", [600, 3000, 20000])
+@pytest.mark.parametrize("opt", OPTS)
+def test_tree_few_rows(nq, nkv, slots, opt):
+    # blocks of 8 (row, head) pairs, one, two and more per sequence; with room, and without keys
+    _tree_case(nq, nkv, 128, "bf16", [300, 0, 17, 511, 130], [1, 2, 0, 3, 1], mask="any", slots=slots, lead=1, tail=1, **opt)
+
+
+@pytest.mark.parametrize("B,rows", [(1, 1), (1, 8), (40, 2), (100, 8), (3, 13)])
+@pytest.mark.parametrize("page", [0, 16, 64])
+def test_tree_few_rows_batches(B, rows, page):
+    r = np.random.RandomState(B + rows)
+    _tree_case(2, 2, 128, "bf16", r.randint(0, 900, B).tolist(), r.randint(1, rows + 1, B).tolist(), page=page,
+               check=[0, 1, 7, 12], calls=3)
+    _tree_case(4, 1, 128, "bf16", r.randint(0, 900, B).tolist(), r.randint(0, rows + 1, B).tolist(), page=page, cap=20.0,
+               bias=True, check=[0, 1, 7, 12])
+
+
 @pytest.mark.parametrize("words", [1, 2, 7])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tree_mask_widths(words, dtype):
@@ -705,19 +723,20 @@ def test_tree_fp32_shared_keys():
 def test_tree_output_aligned_to_16_bytes_only():
     m, shape = _model(4, 2, max_batch=1)
     kv, *_ = _filled(shape, 1, 300, 16, torch.bfloat16, 9)
-    q = _randn((9, 4, 128), torch.bfloat16, 10).cuda()
-    outs = [torch.empty(9 * 512 + 8, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
-    for o, off in zip(outs, (0, 8)):
-        m.op_attention_tree(q, _i32([0, 9]), _i32([250]), 0, kv, o[off:off + 9 * 512])
-    m.sync()
-    assert torch.equal(outs[0][:9 * 512], outs[1][8:])
+    for n in (2, 40):
+        q = _randn((n, 4, 128), torch.bfloat16, 10).cuda()
+        outs = [torch.empty(n * 512 + 8, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        for o, off in zip(outs, (0, 8)):
+            m.op_attention_tree(q, _i32([0, n]), _i32([250]), 0, kv, o[off:off + n * 512])
+        m.sync()
+        assert torch.equal(outs[0][:n * 512], outs[1][8:])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("opt", OPTS)
-@pytest.mark.parametrize("slots", [1000, 200])
+@pytest.mark.parametrize("slots", [1000, 200, 9000])
 def test_tree_nan_reaches_the_rows_that_see_it(dtype, opt, slots):
-    start = slots - 20
+    start = min(slots - 20, 980)
     m, shape = _model(4, 2, 128, dtype, max_batch=2)
     kv, k, v, pt = _filled(shape, 2, slots, 16, shape.torch_dtype, 12)
     parents = _random_tree(20, 4)
