@@ -1640,11 +1640,9 @@ int llama_op_cache_evict(llama_ctx* c, const llama_kv* kv, int32_t layer, const 
   e.recent = recent;
   e.limit = a.limit;
   e.status = c->status;
-  e.sm_count = c->sm_count;
   Prof pf(c, LLAMA_KERNEL_ROPE_APPEND);
-  c->launches += 2;
-  TRY(cuda_rc(launch_evict_select(e, c->stream)));
-  return cuda_rc(launch_cache_evict(a, c->stream));
+  c->launches += evict_launches(a.layers, B, a.n_kv, c->sm_count);
+  return cuda_rc(launch_evict(e, a, c->stream));
 }
 
 int llama_op_argmax(llama_ctx* c, const float* logits, int32_t B, int32_t V, int32_t* ids) {

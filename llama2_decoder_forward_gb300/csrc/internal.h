@@ -375,7 +375,6 @@ struct CacheMoveArgs {
   const int32_t *kept = nullptr, *lens = nullptr;
 };
 cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t st);
-cudaError_t launch_cache_evict(const CacheMoveArgs& a, cudaStream_t st);
 struct EvictArgs {
   const float* weights;        // [layers][B][n_kv][ld]
   float* weights_out;
@@ -384,9 +383,9 @@ struct EvictArgs {
   int64_t ld;
   int layers, B, n_kv, keep, first, recent, limit;
   uint32_t* status;
-  int sm_count;
 };
-cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t st);
+cudaError_t launch_evict(const EvictArgs& e, const CacheMoveArgs& a, cudaStream_t st);
+int evict_launches(int layers, int B, int n_kv, int sm_count);
 
 // ---- token sampling (k_sample.cu)
 struct SampleCall {

@@ -108,7 +108,6 @@ struct FormsParams {
   // trees: out, cu_rows, n_rows, n_docs as documents; the cache as a prefix
   const int32_t *start_pos, *row_pos;
   TreeMask tree;
-  int least_tiles;
   struct TreeShared* shared;                // [CTAs] the item that each CTA begins and does not end,
   int* shared_parts;                        // and how many partial results it has (0: no such item)
   float poly[13];                           // KCapFixed: kTanh times powers of scale / cap
@@ -515,7 +514,7 @@ __device__ __forceinline__ long long tree_chunk(const FormsParams& p, int ctas, 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   *total = all;
-  return max((long long)p.least_tiles, (all + ctas - 1) / ctas);
+  return max(1ll, (all + ctas - 1) / ctas);
 }
 // The item that tile u belongs to, for a whole warp whose questions ascend.
 struct TreeCursor {
@@ -1637,7 +1636,6 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
   p.rows_seq = TM / p.G;
   // both row tiles on the same rows where a sequence's fit into one, by the mean
   p.alternate = (long long)a.n_rows <= (long long)a.B * p.rows_seq;
-  p.least_tiles = 1;
   p.partials = (size_t)2 * a.sm_count * (p.alternate ? TM : 2 * TM);
   p.part_o = a.partial;
   p.part_ml = a.partial + p.partials * 128;
