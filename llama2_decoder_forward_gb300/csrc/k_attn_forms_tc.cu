@@ -516,44 +516,85 @@ __device__ __forceinline__ long long tree_chunk(const FormsParams& p, int ctas, 
   *total = all;
   return max(1ll, (all + ctas - 1) / ctas);
 }
-// The item that tile u belongs to, for a whole warp whose questions ascend.
-struct TreeCursor {
-  int block = 0, b0 = 0;
-  long long before = 0, start = 0;  // tiles in front of b0, of the block
-};
+// A walk over the items for a whole warp: to the one that a tile belongs to, then from
+// one to the next. Each lane holds a sequence; 32 of them are looked at together.
 struct TreeItem {
   int b, g, block, lo, n, start, keys, T;
   long long first;       // its first tile
 };
-__device__ __forceinline__ bool tree_item(const FormsParams& p, long long u, TreeCursor& c, int lane, TreeItem& it) {
-  for (;;) {
-    for (; c.b0 < p.n_docs; c.b0 += 32) {
-      TreeSeq s{};
-      if (c.b0 + lane < p.n_docs) s = tree_seq(p, c.b0 + lane, nullptr);
-      const long long mine = s.blocks > c.block ? s.tiles : 0, upto = c.before + sum_upto(mine, lane);
+struct TreeWalk {
+  const FormsParams& p;
+  int lane, block = 0, b0 = 0;
+  uint32_t have = 0;     // the lanes whose sequence has such a block
+  TreeSeq s;
+  long long upto;        // tiles up to the lane's sequence's end
+  TreeItem it;
+  __device__ __forceinline__ TreeWalk(const FormsParams& p_, int lane_) : p(p_), lane(lane_) {}
+  __device__ __forceinline__ void load(long long before) {
+    s = TreeSeq{};
+    if (b0 + lane < p.n_docs) s = tree_seq(p, b0 + lane, nullptr);
+    const bool mine = s.blocks > block;
+    upto = before + sum_upto(mine ? s.tiles : 0, lane);
+    have = __ballot_sync(0xffffffffu, mine);
+  }
+  // the next 32 sequences, or the next block of the first 32; false: no sequence has one
+  __device__ __forceinline__ bool more() {
+    const long long before = __shfl_sync(0xffffffffu, upto, 31);
+    b0 += 32;
+    if (b0 < p.n_docs) {
+      load(before);
+      return true;
+    }
+    if (before == block_start) return false;
+    block_start = before;
+    ++block;
+    b0 = 0;
+    load(before);
+    return true;
+  }
+  __device__ __forceinline__ void take(int w, long long base) {  // lane w's sequence, its first item
+    it.b = b0 + w;
+    it.block = block;
+    it.lo = __shfl_sync(0xffffffffu, s.lo, w);
+    it.n = __shfl_sync(0xffffffffu, s.n, w);
+    it.start = __shfl_sync(0xffffffffu, s.start, w);
+    it.keys = __shfl_sync(0xffffffffu, s.keys, w);
+    it.T = __shfl_sync(0xffffffffu, s.T, w);
+    it.g = 0;
+    it.first = base;
+  }
+  // the item of tile u
+  __device__ __forceinline__ bool seek(long long u) {
+    load(0);
+    for (;;) {
       const uint32_t m = __ballot_sync(0xffffffffu, u < upto);
       if (m) {
         const int w = __ffs(m) - 1;
-        it.b = c.b0 + w;
-        it.block = c.block;
-        it.lo = __shfl_sync(0xffffffffu, s.lo, w);
-        it.n = __shfl_sync(0xffffffffu, s.n, w);
-        it.start = __shfl_sync(0xffffffffu, s.start, w);
-        it.keys = __shfl_sync(0xffffffffu, s.keys, w);
-        it.T = __shfl_sync(0xffffffffu, s.T, w);
-        const long long base = __shfl_sync(0xffffffffu, upto - mine, w);
-        it.g = (int)((u - base) / it.T);
-        it.first = base + (long long)it.g * it.T;
+        take(w, __shfl_sync(0xffffffffu, upto - (s.blocks > block ? s.tiles : 0), w));
+        it.g = (int)((u - it.first) / it.T);
+        it.first += (long long)it.g * it.T;
         return true;
       }
-      c.before = __shfl_sync(0xffffffffu, upto, 31);
+      if (!more()) return false;
     }
-    if (c.before == c.start) return false;  // no sequence has so many blocks
-    c.start = c.before;
-    ++c.block;
-    c.b0 = 0;
   }
-}
+  __device__ __forceinline__ bool next() {
+    const long long first = it.first + it.T;
+    if (it.g + 1 < p.n_kv) {
+      ++it.g;
+      it.first = first;
+      return true;
+    }
+    uint32_t m = have & ~((2u << (it.b - b0)) - 1u);  // (2 << 31 is 0: no lane behind the last)
+    while (!m) {
+      if (!more()) return false;
+      m = have;
+    }
+    take(__ffs(m) - 1, first);
+    return true;
+  }
+  long long block_start = 0;  // tiles in front of the block
+};
 // What follows from an item's published part.
 __device__ __forceinline__ void tree_work(const FormsParams& p, FormsWork& w) {
   w.pre = w.h0 = 0;
@@ -584,20 +625,17 @@ __device__ __forceinline__ void tree_store(const FormsParams& p, const FormsWork
                                            uint32_t tl, bool row_ok, size_t row, int head, float m, float l,
                                            int count, float* x, uint64_t* meet, uint32_t& ph_meet,
                                            volatile uint32_t* stop) {
-  // all 16 warps, by a wait that ends
-  auto softmax_bar = [&] {
+  m = count == 0 || l == 0.f ? -INFINITY : merge_max(m, l);
+  float f0 = 1.f, f1 = 0.f;
+  if (alt) {
+    x[t * 256 + 128 * grp + r] = grp ? l : m;
+    // all 16 warps, by a wait that ends (and both tiles' last MMAs are done)
     tc_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(meet);
     wait_bar(meet, ph_meet, stop, p.status);
     ph_meet ^= 1;
     __syncwarp();
-  };
-  m = count == 0 || l == 0.f ? -INFINITY : merge_max(m, l);
-  float f0 = 1.f, f1 = 0.f;
-  if (alt) {
-    x[t * 256 + 128 * grp + r] = grp ? l : m;
-    softmax_bar();  // (and both tiles' last MMAs are done)
     const float m0 = x[r], l0 = x[128 + r], m1 = x[256 + r], l1 = x[384 + r];
     m = fmaxf(m0, m1);
     f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
@@ -646,7 +684,11 @@ __device__ __forceinline__ void tree_store(const FormsParams& p, const FormsWork
       p.part_ml[2 * at + 1] = l;
     }
   }
-  if (alt) softmax_bar();  // the exchange and the other tile's O have been read
+  if (alt) {  // the exchange and the other tile's O have been read: the next item waits for that
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(meet + 1);
+  }
 }
 
 template <int MODE, int KIND>
@@ -677,7 +719,8 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
   volatile uint32_t* stop = ctl + 1;
   static_assert((2 + 2 * MAXK + 2 * MAXV + 1 + 10 + 4) * 8 + 20 <= 256, "barrier block");
   volatile int4* box = reinterpret_cast<volatile int4*>(smem + OFF_WORK);
-  uint64_t* meet = reinterpret_cast<uint64_t*>(smem + OFF_WORK + 96);  // trees: the softmax warps
+  // trees: the softmax warps have left their rows' maxima and sums; they have read them and O
+  uint64_t* meet = reinterpret_cast<uint64_t*>(smem + OFF_WORK + 96);
   grid_dep_wait();
   grid_dep_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -706,6 +749,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     }
     mbar_init(vland, 1);
     mbar_init(meet, 16);
+    mbar_init(meet + 1, 16);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
       mbar_init(&pready[2 * t], 8);
@@ -793,13 +837,13 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       int issued = 0, loaded_q = 0, rows = 0;
       bool ok = true;
       DocCursor cursor;
-      TreeCursor where;
+      TreeWalk walk(p, lane);
       long long u = min(total, chunk * blockIdx.x);  // trees: what is left of this CTA's chunk
       const long long u_end = min(total, u + chunk);
       for (int it = 0; ok; ++it) {
         if (TREE) {
-          TreeItem item{};
-          bool more = u < u_end && tree_item(p, u, where, lane, item);
+          const bool more = u < u_end && (it == 0 ? walk.seek(u) : walk.next());
+          const TreeItem& item = walk.it;
           if (more) {
             w.lo = item.lo;
             w.n = item.n;
@@ -837,7 +881,6 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           }
           __syncwarp();
           if (!more) break;
-          rows = tile_rows(p, w.seq0, w.g, w.t0, w.kmax, lane);
         } else if (DOCS) {
           const bool more = next_doc(p, it, cursor, w);
           ok = __all_sync(0xffffffffu, wait_bar(&wempty[it & 1], ((it >> 1) & 1) ^ 1, stop, p.status));
@@ -860,7 +903,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         }
         // trees: the first two K tiles come before Q, whose slot is free only after the last
         // item's last scores (their own slots are free sooner, and wait for no Q of this item)
-        const int q_at = TREE ? min(w.n_tiles, 2) : 0;
+        const int q_at = TREE && it > 0 ? min(w.n_tiles, 2) : 0;
         auto load_q = [&] {
         ok = __all_sync(0xffffffffu, wait_bar(qempty, (it & 1) ^ 1, stop, p.status));
         if (!ok) return;
@@ -882,8 +925,9 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         }
         };
         if (q_at == 0) load_q();
+        if (TREE) rows = tile_rows(p, w.seq0, w.g, w.t0, w.kmax, lane);
         for (int j = 0; ok && j < w.n_tiles; ++j) {
-          if (TREE && j > 0 && j == q_at) load_q();
+          if (TREE && q_at > 0 && j == q_at) load_q();
           if (!ok) break;
           if (!DOCS && j > 0 && (j & 3) == 0)
             rows = tile_rows(p, TREE ? w.seq0 : p.shared_seq, w.g, w.t0 + j, w.kmax, lane);
@@ -894,7 +938,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
           ++issued;
           r.step();
         }
-        if (TREE && ok && q_at == w.n_tiles) load_q();
+        if (TREE && ok && q_at > 0 && q_at == w.n_tiles) load_q();
         if (TREE && ok && alt && (w.n_tiles & 1)) even_out(r, kempty, kfull, issued, ok);
       }
       // no copy in flight when the CTA exits
@@ -1093,6 +1137,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     const float ct = KIND == KCap ? cl : c;  // log2 units of a raw score (of tanh)
     FormsWork w{};
     uint32_t ph_s = 0, ph_fin = 0, ph_meet = 0;  // phases of sfull, fin, meet
+    const int row_i = r / p.G, row_h = r - row_i * p.G;  // trees: the row's index in its block, its head
 #pragma unroll 1
     for (int it = 0; work(it, w); ++it) {
     const int count = t ? w.nt1 : w.nt0;
@@ -1110,13 +1155,13 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       head = p.head_pairs ? w.h0 + t : w.h0;
       row = (size_t)w.lo + i;
     } else if (TREE) {
-      const int i = w.q0 + (p.alternate ? 0 : t * p.rows_seq) + r / p.G;
+      const int i = w.q0 + (p.alternate ? 0 : t * p.rows_seq) + row_i;
       row_ok = r < p.rows_seq * p.G && i < w.n;
       row = (size_t)w.lo + i;
       tree_i = i;
       pos = BIAS && row_ok ? p.row_pos ? min(max(p.row_pos[row], 0), kMaxPos) : w.start + i : 0;
       lim = w.start;
-      head = w.g * p.G + r % p.G;
+      head = w.g * p.G + row_h;
     } else {
       const int s = w.seq0 + (p.alternate ? 0 : t * p.rows_seq) + r / p.G;
       row_ok = r < p.rows_seq * p.G && s < p.B;
@@ -1128,6 +1173,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
     const float sl = BIAS && p.slopes && row_ok ? p.slopes[head] * kLog2e : 0.f;
     float m = KIND == KCapFixed ? 0.f : -INFINITY, l = 0.f;
     const bool idle = TREE && !__any_sync(0xffffffffu, row_ok);  // rows that nobody has: P may be anything
+    if (TREE && alt && it > 0) wait_bar(meet + 1, (it - 1) & 1, stop, p.status);  // as in tree_store
     for (int j = 0; j < count; ++j) {
       wait_bar(&sfull[t], ph_s, stop, p.status);
       ph_s ^= 1;
