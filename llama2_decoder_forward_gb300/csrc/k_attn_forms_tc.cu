@@ -1469,19 +1469,24 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(Form
   grid_dep_wait();
   grid_dep_launch();
   extern __shared__ JoinItem items[];  // [ctas]
-  __shared__ int n_items;
+  __shared__ int counts[JOIN_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp == 0) {
-    int n = 0;
-    for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const int parts = c0 + lane < ctas ? p.shared_parts[c0 + lane] : 0;
-      const uint32_t m = __ballot_sync(0xffffffffu, parts > 0);
-      if (parts > 0) items[n + __popc(m & ((1u << lane) - 1u))] = JoinItem{c0 + lane, parts, p.shared[c0 + lane]};
-      n += __popc(m);
+  int n_items = 0;
+  for (int c0 = 0; c0 < ctas; c0 += 32 * JOIN_WARPS) {  // a thread per CTA: its item beside whether it has one
+    const int c = c0 + threadIdx.x;
+    JoinItem it{};
+    if (c < ctas) it = JoinItem{c, p.shared_parts[c], p.shared[c]};
+    const uint32_t m = __ballot_sync(0xffffffffu, it.parts > 0);
+    if (lane == 0) counts[warp] = __popc(m);
+    __syncthreads();
+    int at = n_items + __popc(m & ((1u << lane) - 1u));
+    for (int w = 0; w < JOIN_WARPS; ++w) {
+      if (w < warp) at += counts[w];
+      n_items += counts[w];
     }
-    if (lane == 0) n_items = n;
+    if (it.parts > 0) items[at] = it;
+    __syncthreads();
   }
-  __syncthreads();
   const int rows_tile = p.rows_seq * p.G, rows_slot = p.alternate ? TM : 2 * TM;
   const int row_l = lane / JOIN_PARTS, part_l = lane % JOIN_PARTS;  // of this lane's maximum and sum
   for (int task = blockIdx.x * JOIN_WARPS + warp; task < n_items * (rows_slot / JOIN_ROWS); task += gridDim.x * JOIN_WARPS) {
