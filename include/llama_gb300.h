@@ -663,7 +663,7 @@ int llama_op_attention_decode_weights(llama_ctx* ctx, const void* q, const int32
  * first + recent <= keep. A length outside [0, limit], limit the cache's slots and
  * weights_ld, sets LLAMA_FLAG_POS_RANGE and is cut; a page id outside the pool sets
  * LLAMA_FLAG_PAGE_RANGE and its rows are not moved. A sequence's pages must be its
- * own. Any cache type. Asynchronous; one or two launches. */
+ * own. Any cache type. Asynchronous; one launch. */
 int llama_op_cache_evict(llama_ctx* ctx, const llama_kv* kv, int32_t layer, const int32_t* lens, int32_t B,
                          int32_t keep, int32_t first, int32_t recent, const float* weights,
                          int64_t weights_ld, float* weights_out, int32_t* kept);

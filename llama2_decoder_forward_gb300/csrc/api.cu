@@ -1641,7 +1641,7 @@ int llama_op_cache_evict(llama_ctx* c, const llama_kv* kv, int32_t layer, const 
   e.limit = a.limit;
   e.status = c->status;
   Prof pf(c, LLAMA_KERNEL_ROPE_APPEND);
-  c->launches += evict_launches(a.layers, B, a.n_kv, c->sm_count);
+  c->launches++;
   return cuda_rc(launch_evict(e, a, c->stream));
 }
 

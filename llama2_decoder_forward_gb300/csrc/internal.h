@@ -385,7 +385,6 @@ struct EvictArgs {
   uint32_t* status;
 };
 cudaError_t launch_evict(const EvictArgs& e, const CacheMoveArgs& a, cudaStream_t st);
-int evict_launches(int layers, int B, int n_kv, int sm_count);
 
 // ---- token sampling (k_sample.cu)
 struct SampleCall {

@@ -22,9 +22,6 @@ namespace llgb {
 namespace {
 
 constexpr int MOVE_THREADS = 256;
-constexpr int UNITS = 8;            // 16-byte units that a thread has in flight
-constexpr int FUSED_UNITS = 5;      // the same in the kernel that selects and moves, four of which share an SM
-constexpr int MAX_ROWS = 1024;      // rows of a chunk (256 threads x 8 units, slices of 2 units)
 
 // Row, within its layer, of a slot's K/V head 0 (the heads are slot_step rows apart); -1
 // (flagged) for a page outside the pool.
@@ -130,16 +127,20 @@ __global__ void __launch_bounds__(MOVE_THREADS, 3) cache_commit_kernel(CacheMove
   }
 }
 
-// Evict: the kept rows of one K/V head, moved by a CTA: of each row `cols` units from
-// unit col0 on, of K's row and, behind it, V's. Slots look up their rows a chunk ahead,
-// and the list is read two chunks ahead, so that a chunk waits for one latency.
-template <int MINE, int UNITS>  // rows of a chunk that a thread looks up, at most; units that it moves
+// Evict: the kept rows of one K/V head, moved by a CTA of T threads, U units each at a
+// time: of each row `cols` units from unit col0 on, of K's row and, behind it, V's. Slots
+// look up their rows a chunk ahead, and the list is read two chunks ahead, so that a
+// chunk waits for one latency. moves: [3][rows_chunk], because beside a thread that still
+// stores a chunk another one may look up the chunk after the next.
+template <int T, int U>
 __device__ __forceinline__ void move_kept(const CacheMoveArgs& a, int2* moves, const int32_t* list, int l, int b, int g,
-                                          int col0, int cols, int rows_chunk) {
+                                          int col0, int cols) {
+  const int rows_chunk = T / cols * U;
+  constexpr int MINE = (T / 2 * U + T - 1) / T;  // rows of a chunk that a thread looks up, with 2 columns
   const int n = a.list_ld, ld = a.row_bytes / 16;
   // the first slot that moves: list[i] == i up to there
   int first = 0;
-  for (int step = (n + MOVE_THREADS - 1) / MOVE_THREADS, end = n; end > first;) {
+  for (int step = (n + T - 1) / T, end = n; end > first;) {
     const int i = first + threadIdx.x * step;
     const int same = __syncthreads_count(i < end && list[i] == i);
     if (same == 0) break;
@@ -149,14 +150,14 @@ __device__ __forceinline__ void move_kept(const CacheMoveArgs& a, int2* moves, c
     }
     first += (same - 1) * step;
     end = min(end, first + step);
-    step = (end - first + MOVE_THREADS - 1) / MOVE_THREADS;
+    step = (end - first + T - 1) / T;
   }
   const int head = g * (a.page_size == 0 ? a.capacity : a.page_size);
   int slot[MINE];
   auto read_list = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < MINE; ++k) {
-      const int r = threadIdx.x + k * MOVE_THREADS;
+      const int r = threadIdx.x + k * T;
       slot[k] = r < rows_chunk && i0 + r < n ? list[i0 + r] : -1;
     }
   };
@@ -164,7 +165,7 @@ __device__ __forceinline__ void move_kept(const CacheMoveArgs& a, int2* moves, c
   auto look_up = [&](int i0, int2* to) {
 #pragma unroll
     for (int k = 0; k < MINE; ++k) {
-      const int r = threadIdx.x + k * MOVE_THREADS, i = i0 + r, s = slot[k];
+      const int r = threadIdx.x + k * T, i = i0 + r, s = slot[k];
       if (r >= rows_chunk) break;
       int2 m = make_int2(-1, -1);
       if (s > i && bc_ok(s < a.limit, a.status)) {
@@ -176,7 +177,7 @@ __device__ __forceinline__ void move_kept(const CacheMoveArgs& a, int2* moves, c
     }
   };
   // a thread's units: one column of the rows r0, r0 + step_r, ..
-  const int step_r = MOVE_THREADS / cols, r0 = threadIdx.x / cols, col = col0 + (int)threadIdx.x - r0 * cols;
+  const int step_r = T / cols, r0 = threadIdx.x / cols, col = col0 + (int)threadIdx.x - r0 * cols;
   uint4* at = reinterpret_cast<uint4*>(col < ld ? a.k : a.v) + (size_t)(a.layer + l) * a.layer_rows * ld +
               (col < ld ? col : col - ld);
   read_list(first);
@@ -187,36 +188,20 @@ __device__ __forceinline__ void move_kept(const CacheMoveArgs& a, int2* moves, c
   for (int i0 = first; i0 < n; i0 += rows_chunk) {
     const int2* mv = moves + part * rows_chunk;
     part = part == 2 ? 0 : part + 1;
-    int2 m[UNITS];
-    uint4 x[UNITS];
+    int2 m[U];
+    uint4 x[U];
 #pragma unroll
-    for (int k = 0; k < UNITS; ++k) m[k] = r0 < step_r ? mv[r0 + k * step_r] : make_int2(-1, -1);
+    for (int k = 0; k < U; ++k) m[k] = r0 < step_r ? mv[r0 + k * step_r] : make_int2(-1, -1);
 #pragma unroll
-    for (int k = 0; k < UNITS; ++k)
+    for (int k = 0; k < U; ++k)
       if (m[k].x >= 0) x[k] = at[(size_t)m[k].x * ld];
     look_up(i0 + rows_chunk, moves + part * rows_chunk);
     read_list(i0 + 2 * rows_chunk);
     __syncthreads();  // the chunk is read: its slots may be written
 #pragma unroll
-    for (int k = 0; k < UNITS; ++k)
+    for (int k = 0; k < U; ++k)
       if (m[k].x >= 0) at[(size_t)m[k].y * ld] = x[k];
   }
-}
-
-// Few heads: the moves alone, a CTA per slice of the columns of K or V of one head, down
-// to 32 bytes (a sector). Grid: slices, then K / V, K/V head, sequence, layer.
-__global__ void __launch_bounds__(MOVE_THREADS, 2) cache_evict_kernel(CacheMoveArgs a, int slices, int rows_chunk) {
-  grid_dep_wait();
-  grid_dep_launch();
-  // [3][rows_chunk], because beside a thread that still stores a chunk another one may
-  // look up the chunk after the next
-  extern __shared__ int2 moves[];
-  long long item = blockIdx.x;
-  const int cols = a.row_bytes / 16 / slices, col0 = (int)(item % (2 * slices)) * cols;
-  item /= 2 * slices;
-  const int g = (int)(item % a.n_kv), b = (int)(item / a.n_kv % a.B), l = (int)(item / a.n_kv / a.B);
-  if (min(max(a.lens[b], 0), a.limit) <= a.list_ld) return;  // nothing was dropped: nothing moves
-  move_kept<MAX_ROWS / MOVE_THREADS, UNITS>(a, moves, a.kept + (size_t)item * a.list_ld, l, b, g, col0, cols, rows_chunk);
 }
 
 // ---------------------------------------------------------------- which keys stay
@@ -237,11 +222,10 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 // the warps exchange one pair of counts. Up to 8192 weights are read once and stay in
 // shared memory; longer lists are read again for every pass, 8192 at a time. Bound by
 // the instructions per weight, so the second and third counts look only at the weights
-// that share the first 11 bits, which are few: listed while they fit into LISTED. Returns
-// how many slots there were.
+// that share the first 11 bits, which are few: listed while they fit into LISTED.
 constexpr int LISTED = 1024;  // with a span's weights and the bins just below 48 KB
 template <int T>
-__device__ __forceinline__ int select_kept(const EvictArgs& a, float* held, int item) {
+__device__ __forceinline__ void select_kept(const EvictArgs& a, float* held, int item) {
   constexpr int WARPS = T / 32, PER = BINS / T;
   static_assert((SPAN + BINS + BINS / 8 + LISTED + 2 * WARPS + 4) * 4 <= 48 * 1024, "without an opt-in");
   static_assert(SPAN / T <= 32, "a thread's slots of a span are the bits of a word");
@@ -400,28 +384,26 @@ __device__ __forceinline__ int select_kept(const EvictArgs& a, float* held, int 
   }
   for (int i = done + t; i < a.keep; i += T) kept[i] = -1;
   for (long long i = done + t; i < a.ld; i += T) out[i] = 0.f;
-  return n;
 }
 
-template <int T>
-__global__ void __launch_bounds__(T) evict_select_kernel(EvictArgs a) {
-  grid_dep_wait();
-  grid_dep_launch();
-  extern __shared__ float held[];  // [min(SPAN, most slots)]
-  select_kept<T>(a, held, blockIdx.x);
-}
-
-// Many heads: a CTA selects a head's keys and moves them, so that one CTA's counting and
-// the others' moves share an SM.
-__global__ void __launch_bounds__(MOVE_THREADS, 4) evict_kernel(EvictArgs e, CacheMoveArgs a, int rows_chunk) {
+// A head's keys selected and moved by a CTA, so that one CTA's counting and the others'
+// moves share an SM; or, where heads are few, by a cluster of `ctas`: its first CTA selects,
+// and each moves a slice of the columns, down to 32 bytes (a sector).
+template <int T, int U>
+__global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs e, CacheMoveArgs a, int ctas) {
   grid_dep_wait();
   grid_dep_launch();
   extern __shared__ float held[];  // [min(SPAN, most slots)]; then the moves
-  const int item = blockIdx.x;
-  if (select_kept<MOVE_THREADS>(e, held, item) <= a.list_ld) return;
-  __syncthreads();  // the list is written, and `held` free
-  move_kept<2, FUSED_UNITS>(a, reinterpret_cast<int2*>(held), a.kept + (size_t)item * a.list_ld, item / a.n_kv / a.B,
-            item / a.n_kv % a.B, item % a.n_kv, 0, a.row_bytes / 8, rows_chunk);
+  const int item = blockIdx.x / ctas, rank = blockIdx.x - item * ctas, b = item / a.n_kv % a.B;
+  if (rank == 0) select_kept<T>(e, held, item);
+  if (ctas > 1)
+    cluster_sync_all();  // the list is written
+  else
+    __syncthreads();     // and `held` free
+  if (min(max(a.lens[b], 0), a.limit) <= a.list_ld) return;  // nothing was dropped: nothing moves
+  const int cols = a.row_bytes / 8 / ctas;
+  move_kept<T, U>(a, reinterpret_cast<int2*>(held), a.kept + (size_t)item * a.list_ld, item / a.n_kv / a.B, b,
+                  item % a.n_kv, rank * cols, cols);
 }
 
 }  // namespace
@@ -439,27 +421,24 @@ cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t st) {
                   rows * sizeof(int2), st, 0, a, heads, rows, run);
 }
 
-cudaError_t launch_evict(const EvictArgs& e, const CacheMoveArgs& a, cudaStream_t st) {
-  const int upr = a.row_bytes / 16;
-  const long long items = (long long)a.layers * a.B * a.n_kv;
-  const size_t sm = (size_t)std::min(SPAN, e.limit) * sizeof(float);
-  if (items > 2 * a.sm_count) {
-    const int rows = std::min(MAX_ROWS, MOVE_THREADS / (2 * upr) * FUSED_UNITS);
-    return launch_k(evict_kernel, dim3((unsigned)items), dim3(MOVE_THREADS),
-                    std::max<size_t>(sm, 3 * rows * sizeof(int2)), st, 0, e, a, rows);
-  }
-  const cudaError_t err = launch_k(evict_select_kernel<1024>, dim3((unsigned)items), dim3(1024), sm, st, 0, e);
-  if (err != cudaSuccess) return err;
-  int slices = 1;
-  while (upr / slices % 2 == 0 && upr / slices > 2 && items * 2 * slices < 4 * a.sm_count) slices *= 2;
-  const int rows = std::min(MAX_ROWS, MOVE_THREADS / (upr / slices) * UNITS);
-  return launch_k(cache_evict_kernel, dim3((unsigned)(items * 2 * slices)), dim3(MOVE_THREADS),
-                  3 * rows * sizeof(int2), st, 0, a, slices, rows);
+template <int T, int U>
+static cudaError_t run_evict(const EvictArgs& e, const CacheMoveArgs& a, int items, int ctas, cudaStream_t st) {
+  const int rows = T / (a.row_bytes / 8 / ctas) * U;
+  const size_t sm = std::max(std::min(SPAN, e.limit) * sizeof(float), 3 * rows * sizeof(int2));
+  return launch_kc(evict_kernel<T, U>, dim3((unsigned)(items * ctas)), dim3(T), sm, st,
+                   ctas > 1 ? dim3(ctas, 1, 1) : dim3(0, 0, 0), e, a, ctas);
 }
 
-// Launches of an eviction: one where there are heads enough.
-int evict_launches(int layers, int B, int n_kv, int sm_count) {
-  return (long long)layers * B * n_kv > 2 * sm_count ? 1 : 2;
+cudaError_t launch_evict(const EvictArgs& e, const CacheMoveArgs& a, cudaStream_t st) {
+  const int items = a.layers * a.B * a.n_kv;
+  // 1024 heads of 4096 slots, 1500 kept: 272 us with four CTAs per SM and 5 units a thread,
+  // 299 with three and 8, 319 with four and 4; select and move as two kernels 290
+  if (items > 2 * a.sm_count) return run_evict<256, 5>(e, a, items, 1, st);
+  int ctas = 1;
+  while (ctas < 8 && items * ctas < 2 * a.sm_count && a.row_bytes / 8 / (2 * ctas) >= 2 &&
+         a.row_bytes / 8 % (2 * ctas) == 0)
+    ctas *= 2;
+  return run_evict<1024, 2>(e, a, items, ctas, st);
 }
 
 }  // namespace llgb
