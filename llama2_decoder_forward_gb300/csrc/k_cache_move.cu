@@ -138,9 +138,10 @@ __device__ __forceinline__ void move_kept(const CacheMoveArgs& a, int2* moves, c
   const int rows_chunk = T / cols * U;
   constexpr int MINE = (T / 2 * U + T - 1) / T;  // rows of a chunk that a thread looks up, with 2 columns
   const int n = a.list_ld, ld = a.row_bytes / 16;
-  // the first slot that moves: list[i] == i up to there
+  // the first slot that moves: list[i] == i up to there (two loads in a row; a few
+  // chunks in which nothing moves are done sooner)
   int first = 0;
-  for (int step = (n + T - 1) / T, end = n; end > first;) {
+  if (n > 4 * rows_chunk) for (int step = (n + T - 1) / T, end = n; end > first;) {
     const int i = first + threadIdx.x * step;
     const int same = __syncthreads_count(i < end && list[i] == i);
     if (same == 0) break;
@@ -216,14 +217,14 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 
 // What stays of one (layer, sequence, K/V head), by a CTA of T threads: the m-th largest of the weights
 // between the first and the recent slots, by counting how many have each value of
-// their upper 11 bits, then of the next 11 and the last 10 among those that share the
-// found ones; then one ordered pass that lists what stays and moves its weights. A
+// their upper 11 bits; those that share the found ones, if few, are compared with each
+// other, else counted by the next 11 and the last 10 bits; then one ordered pass that
+// lists what stays and moves its weights. A
 // warp owns consecutive slots, 32 at a time, so ranks within it are bit counts and
 // the warps exchange one pair of counts. Up to 8192 weights are read once and stay in
 // shared memory; longer lists are read again for every pass, 8192 at a time. Bound by
-// the instructions per weight, so the second and third counts look only at the weights
-// that share the first 11 bits, which are few: listed while they fit into LISTED.
-constexpr int LISTED = 1024;  // with a span's weights and the bins just below 48 KB
+// the instructions per weight and, where there are few heads, by the barriers.
+constexpr int LISTED = 256;
 template <int T>
 __device__ __forceinline__ void select_kept(const EvictArgs& a, float* held, int item) {
   constexpr int WARPS = T / 32, PER = BINS / T;
@@ -319,20 +320,37 @@ __device__ __forceinline__ void select_kept(const EvictArgs& a, float* held, int
     const uint32_t upper = find();
     candidates(true, [&](uint32_t u) {
       if (u >> 21 != upper) return;
-      atomicAdd(&bin((u >> 10) & 2047u), 1u);
       const uint32_t at = atomicAdd(&n_listed, 1u);
       if (at < LISTED) listed[at] = u;
     });
-    const uint32_t middle = upper << 11 | find();
-    auto last = [&](uint32_t u) {
-      if (u >> 10 == middle) atomicAdd(&bin(u & 1023u), 1u);
-    };
-    if (n_listed <= LISTED) {
-      for (int i = t; i < (int)n_listed; i += T) last(listed[i]);
+    __syncthreads();
+    if (n_listed <= LISTED) {  // each against all: whose rank is want?
+      const int m = (int)n_listed;
+      if (t < m) {
+        const uint32_t u = listed[t];
+        int above = 0, equal = 0;
+        for (int i = 0; i < m; ++i) {
+          above += listed[i] > u;
+          equal += listed[i] == u;
+        }
+        if (above < want && want <= above + equal) {  // the same from every thread that has this weight
+          found[0] = u;
+          found[1] = (uint32_t)above;
+        }
+      }
+      __syncthreads();
+      least = found[0];
+      want -= (int)found[1];
     } else {
-      candidates(true, last);
+      candidates(true, [&](uint32_t u) {
+        if (u >> 21 == upper) atomicAdd(&bin((u >> 10) & 2047u), 1u);
+      });
+      const uint32_t middle = upper << 11 | find();
+      candidates(true, [&](uint32_t u) {
+        if (u >> 10 == middle) atomicAdd(&bin(u & 1023u), 1u);
+      });
+      least = middle << 10 | find();
     }
-    least = middle << 10 | find();
     ties = (uint32_t)want;
   }
   // What stays, in order: the spans one after the other, the warps of a span in parallel.
@@ -438,7 +456,7 @@ cudaError_t launch_evict(const EvictArgs& e, const CacheMoveArgs& a, cudaStream_
   while (ctas < 8 && items * ctas < 2 * a.sm_count && a.row_bytes / 8 / (2 * ctas) >= 2 &&
          a.row_bytes / 8 % (2 * ctas) == 0)
     ctas *= 2;
-  return run_evict<1024, 2>(e, a, items, ctas, st);
+  return run_evict<512, 4>(e, a, items, ctas, st);
 }
 
 }  // namespace llgb
