@@ -642,7 +642,7 @@ int llama_op_cache_commit(llama_ctx* ctx, const llama_kv* kv, int32_t layer, con
  * A position of weights_ld or more counts as one past the cache (flagged, the keys in
  * range are attended and weighed). A sequence without keys changes no weight. A NaN score
  * makes the weights of all keys of its K/V head NaN. Up to 4096 query heads per K/V head.
- * Two launches. */
+ * One or two launches. */
 int llama_op_attention_decode_weights(llama_ctx* ctx, const void* q, const int32_t* positions, int32_t B,
                                       int32_t layer, const llama_kv* kv, const llama_scores* scores,
                                       float* weights, int64_t weights_ld, void* scratch, void* out);

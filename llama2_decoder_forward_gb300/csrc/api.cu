@@ -1500,7 +1500,7 @@ int llama_op_attention_decode_weights(llama_ctx* c, const void* q, const int32_t
   TRY(decode_maps(c, kv, B, plan.rows_seq, &a));
   a.partial = c->at<float>(c->L.spart);
   Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
-  c->launches += 2;
+  c->launches += plan.keep ? 1 : 2;
   return cuda_rc(launch_decode_weights(a, plan, w, c->stream));
 }
 

@@ -331,6 +331,7 @@ struct SharedPlan {
   int cluster;          // the own splits of a row form a thread-block cluster
   int join;             // own splits leave partials, which a joining kernel merges
   size_t partials;      // partial rows in all
+  int keep;             // key weights: scores of a row that a CTA keeps (0: they go to the joining kernel)
 };
 SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, int sm_count);
 size_t shared_partial_bytes(int max_batch, int n_q, int n_kv, int max_seq, int sm_count);

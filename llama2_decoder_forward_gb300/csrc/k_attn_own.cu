@@ -57,7 +57,9 @@ constexpr uint32_t HALF = TILE_K * 128;         // 64 keys x 64 dims: 8 KB
 constexpr uint32_t STAGE = 4 * HALF;            // K and V, two dim halves each
 constexpr int SORT_MAX = 256;                   // sequences that a CTA sorts
 constexpr uint32_t OFF_SORT = STAGES * STAGE + 256;
-constexpr size_t OWN_SMEM = OFF_SORT + (2 * SORT_MAX + 4) * 4 + 1024;
+constexpr uint32_t OFF_KEEP = OFF_SORT + (2 * SORT_MAX + 4) * 4;  // key weights: scores, in the kernel that adds them up
+constexpr size_t OWN_SMEM = OFF_KEEP + 1024;
+constexpr size_t OWN_SMEM_MOST = 113 * 1024;    // two CTAs per SM
 static_assert((4 * 16 * HD + 128) * 4 <= STAGES * STAGE, "the merge area aliases the ring");
 
 struct OwnParams {
@@ -83,6 +85,7 @@ struct OwnParams {
   float* scores;
   float* weights;              // [B][n_kv][ld]
   int64_t ld;
+  int keep;                    // room for so many of a row's scores in shared memory, the weights added here; 0: above
   // small trees: every sequence's rows in blocks of tree_rows
   const int32_t *cu_rows, *start_pos, *row_pos;
   TreeMask tree;
@@ -99,6 +102,12 @@ struct OwnRows {
   int b, g, count;             // sequence, K/V head, rows
   int pos;                     // decode: the row's position
   int lo, i0, start, there;    // trees: the sequence's first row, the block's, cached keys, tree rows in the cache
+};
+// Where the scores are kept: row r's of key k at at[r ld + k - first].
+struct OwnKeep {
+  float* at;
+  int64_t ld;
+  int first;
 };
 // Which (row, query head) of q and the output row r is.
 template <int MODE>
@@ -185,7 +194,7 @@ __device__ __forceinline__ void clean_v(uint8_t* v, int lead, int valid, int lan
 // Up to 8 rows: keys on the MMA rows. Lane l tracks rows 2(l%4) and 2(l%4) + 1. Leaves (max, sum, O) of this warp in shared memory.
 template <int MODE>
 __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, uint64_t* full,
-                                             uint64_t* empty, volatile uint32_t* stop, const OwnRows& R,
+                                             uint64_t* empty, volatile uint32_t* stop, const OwnRows& R, const OwnKeep& keep,
                                              int kbeg, int kend, int warp, int lane) {
   const int G = R.count, hq = lane >> 2, hc = 2 * (lane & 3);
   uint32_t qf[8][2];  // Q^T fragments: head lane/4
@@ -251,7 +260,7 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
                                              : (float)(R.pos - k0 - key), x);
         sv[i] = key >= lead && key < valid && (MODE != OTree || (sees[i & 1] >> key & 1u)) ? x : -INFINITY;
         if (MODE == OWeigh && key < valid && hc + (i & 1) < G)
-          p.scores[row_head<MODE>(p, R, hc + (i & 1)) * p.ld + k0 + key] = x;
+          keep.at[(hc + (i & 1)) * keep.ld + (k0 + key - keep.first)] = x;
       }
       float corr[2];
 #pragma unroll
@@ -327,7 +336,7 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
 // Groups of 9 to 16 heads: heads on the MMA rows (zero-padded to 16).
 template <int MODE>
 __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem, uint64_t* full,
-                                              uint64_t* empty, volatile uint32_t* stop, const OwnRows& R,
+                                              uint64_t* empty, volatile uint32_t* stop, const OwnRows& R, const OwnKeep& keep,
                                               int kbeg, int kend, int warp, int lane) {
   const int G = R.count, r0 = lane >> 2;
   uint32_t qa[8][4];
@@ -387,7 +396,7 @@ __device__ __forceinline__ void consume_heads(const OwnParams& p, uint8_t* smem,
           if (p.slopes) x = fmaf(-sl[i >> 1], (float)(R.pos - k0 - key), x);
           sv[nb][i] = key >= lead && key < valid ? x : -INFINITY;
           if (MODE == OWeigh && key < valid && r0 + 8 * (i >> 1) < G)
-            p.scores[row_head<MODE>(p, R, r0 + 8 * (i >> 1)) * p.ld + k0 + key] = x;
+            keep.at[(r0 + 8 * (i >> 1)) * keep.ld + (k0 + key - keep.first)] = x;
           mx[i >> 1] = fmaxf(mx[i >> 1], sv[nb][i]);
         }
 #pragma unroll
@@ -570,6 +579,28 @@ __device__ __forceinline__ bool tree_block(const OwnParams& p, int z, int lane, 
   return false;
 }
 
+// The sequence of a packed row, for a whole warp, or -1.
+__device__ __forceinline__ int tree_sequence(const OwnParams& p, int row, int lane) {
+  for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+    int lo = 0, n = 0;
+    if (b0 + lane < p.n_seq) doc_rows(p.cu_rows, b0 + lane, p.n_rows, nullptr, lo, n);
+    const uint32_t m = __ballot_sync(0xffffffffu, row >= lo && row < lo + n);
+    if (m) return b0 + __ffs(m) - 1;
+  }
+  return -1;
+}
+// Keys of sequence b, and what its rows need of them.
+__device__ __forceinline__ int tree_keys(const OwnParams& p, int b, OwnRows& R) {
+  int lo, n;
+  doc_rows(p.cu_rows, b, p.n_rows, nullptr, lo, n);
+  const int start = p.start_pos[b];
+  const long long end = (long long)start + n;
+  const int keys = start < 0 ? 0 : (int)(end < p.key_limit ? end : p.key_limit);
+  R.start = start < 0 ? 0 : min(start, keys);
+  R.there = keys - R.start;
+  return keys;
+}
+
 template <bool KEYS, int MODE>
 __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     attn_own_kernel(const __grid_constant__ CUtensorMap mapK,
@@ -616,12 +647,8 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0 && warp == 0)  // bad bounds are flagged once
       for (int i = lane, x, y; i < p.n_seq; i += 32) doc_rows(p.cu_rows, i, p.n_rows, p.status, x, y);
     if (!tree_block(p, blockIdx.z, lane, b, R.i0, R.lo, n)) return;  // a cluster's CTAs all do
-    const int start = p.start_pos[b];
-    const long long end = (long long)start + n;
-    if ((start < 0 || end > p.key_limit) && split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
-    pos = (start < 0 ? 0 : (int)(end < p.key_limit ? end : p.key_limit)) - 1;  // the last key
-    R.start = start < 0 ? 0 : min(start, pos + 1);
-    R.there = pos + 1 - R.start;
+    pos = tree_keys(p, b, R) - 1;  // the last key
+    if ((p.start_pos[b] < 0 || R.there < n) && split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
     R.count = min(p.tree_rows, n - R.i0) * p.G;
   } else if (p.sorted) {
     // the blockIdx.z-th longest sequence, so that the longest start first: one key
@@ -665,6 +692,14 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   const int share = own_share(p, n), kbeg = p.base + split * share;
   const int kend = min(n, kbeg + share);
   const bool any = kend > max(kbeg, p.first);
+  OwnKeep keep{};
+  if (MODE == OWeigh) {
+    if (p.keep)
+      keep = OwnKeep{reinterpret_cast<float*>(smem + OFF_KEEP), p.keep, kbeg};
+    else
+      keep = OwnKeep{p.scores + row_head<MODE>(p, R, 0) * p.ld, p.ld, 0};
+    if (!bc_ok(!any || kend - keep.first <= keep.ld, p.status)) return;
+  }
   if (any) {
     const int n_tiles = (kend - kbeg + TILE_K - 1) / TILE_K;
     if (warp == 4) {  // ------------------------------------------------ producer
@@ -712,9 +747,9 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
       return;
     }
     if (KEYS)
-      consume_keys<MODE>(p, smem, full, empty, stop, R, kbeg, kend, warp, lane);
+      consume_keys<MODE>(p, smem, full, empty, stop, R, keep, kbeg, kend, warp, lane);
     else
-      consume_heads<MODE>(p, smem, full, empty, stop, R, kbeg, kend, warp, lane);
+      consume_heads<MODE>(p, smem, full, empty, stop, R, keep, kbeg, kend, warp, lane);
     consumers_bar();
     if (*stop && !p.cluster) return;
   } else if (warp == 4) {  // (a cluster's barriers do not count threads that left)
@@ -732,7 +767,16 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   const float* sm = so + 4 * 16 * HD;
   // a cluster's rows: [16][128] outputs, then maximum and sum [16][2]
   float* mine = reinterpret_cast<float*>(smem) + 4 * 16 * HD + 128;
-  static_assert((4 * 16 * HD + 128 + 16 * (HD + 2)) * 4 <= STAGES * STAGE, "the cluster's rows fit the ring");
+  // key weights added here: the rows' maxima and reciprocal sums, and the first keys' old weights
+  float2* stat = reinterpret_cast<float2*>(smem + OFF_SORT);
+  constexpr int OLD = 4;
+  float old[OLD];
+  float* w = MODE == OWeigh ? p.weights + ((size_t)b * p.n_kv + g) * p.ld : nullptr;
+  if (MODE == OWeigh && p.keep) {
+#pragma unroll
+    for (int q = 0; q < OLD; ++q)
+      if (kbeg + (int)threadIdx.x + 128 * q < kend) old[q] = w[kbeg + threadIdx.x + 128 * q];
+  }
   for (int r = warp; r < R.count; r += 4) {  // a warp per row
     RowSum x;
     if (any && !*stop) {
@@ -752,6 +796,8 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     }
     const size_t bh = row_head<MODE>(p, R, r);
     if (!bc_ok(bh < p.rows && (!p.join || bh * p.splits + split < p.own_room), p.status)) continue;
+    if (MODE == OWeigh && p.keep && lane == 0)
+      stat[r] = make_float2(x.m == -INFINITY ? 0.f : x.m, x.l > 0.f || x.l != x.l ? 1.f / x.l : 0.f);
     if (p.cluster) {
       reinterpret_cast<float4*>(mine + r * HD)[lane] = x.o;
       if (lane == 0) *reinterpret_cast<float2*>(mine + 16 * HD + 2 * r) = make_float2(x.m, x.l);
@@ -764,6 +810,16 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
       const size_t at = bh * p.splits + split;
       reinterpret_cast<float4*>(p.own_o + at * HD)[lane] = x.o;
       if (lane == 0) *reinterpret_cast<float2*>(p.own_ml + 2 * at) = make_float2(x.m, x.l);
+    }
+  }
+  if (MODE == OWeigh && p.keep) {
+    consumers_bar();  // `stat`
+    if (*stop) return;
+    for (int q = 0; kbeg + (int)threadIdx.x + 128 * q < kend; ++q) {
+      const int i = kbeg + threadIdx.x + 128 * q;
+      float sum = 0.f;
+      for (int r = 0; r < R.count; ++r) sum = fmaf(ex2(keep.at[r * keep.ld + (i - kbeg)] - stat[r].x), stat[r].y, sum);
+      w[i] = (q == 0 ? old[0] : q == 1 ? old[1] : q == 2 ? old[2] : q == 3 ? old[3] : w[i]) + sum;
     }
   }
   if (!p.cluster) return;
@@ -799,6 +855,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
 }
 
 // Joins a row's prefix partials and own splits, one warp per (sequence, head).
+template <int MODE>
 __global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int rows) {
   grid_dep_wait();
   grid_dep_launch();
@@ -810,7 +867,15 @@ __global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int 
   own.load(p.own_o, p.own_ml, (size_t)bh * p.splits, p.splits, lane);
   int parts = p.prefix_parts ? __ldcg(p.used) : 0;
   if (!bc_ok(parts <= p.prefix_parts && (size_t)rows * p.splits <= p.own_room, p.status)) return;
-  const int n = key_position(__ldcg(p.positions + bh / p.n_q), p.key_limit) + 1;
+  int n;  // keys of the row
+  if (MODE == OTree) {
+    const int b = tree_sequence(p, bh / p.n_q, lane);
+    if (b < 0) return;  // a row of no sequence
+    OwnRows R{};
+    n = tree_keys(p, b, R);
+  } else {
+    n = key_position(__ldcg(p.positions + bh / p.n_q), p.key_limit) + 1;
+  }
   int used = n > p.first;  // own splits that have keys
   if (used && p.splits > 1) {
     const int share = own_share(p, n);
@@ -923,7 +988,7 @@ cudaError_t attn_own_prepare() {
                              (const void*)attn_own_kernel<true, OWeigh>, (const void*)attn_own_kernel<false, OWeigh>,
                              (const void*)attn_own_kernel<true, OTree>};
   for (const void* f : all) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)OWN_SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)OWN_SMEM_MOST);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -1034,12 +1099,27 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
                : launch_kc(attn_own_kernel<false, ODecode>, grid, block, OWN_SMEM, st, cluster, *a.map_k,
                            *a.map_v, *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess || !s.join) return e;
-  return launch_k(attn_own_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 0, p,
+  return launch_k(attn_own_join_kernel<ODecode>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 0, p,
                   (int)rows);
+}
+
+// Scores of a row that the kernel itself can keep, so that it adds up the weights and the
+// joining kernel falls away: where one CTA has all keys of a row, and shared memory for
+// them costs no CTA that would be resident otherwise. 0: none. (64 sequences of up to 60
+// keys, 8 K/V heads 9.5 us, with the joining kernel 12.0, 32 of up to 200, 32 heads 19.6 and 22.2; the
+// splits of a cluster likewise measured slower, 4 sequences of up to 1000 keys 18.7 and 13.4.)
+static int weights_keep(const SharedPlan& s, int B, int n_q, int n_kv, int sm_count) {
+  const int G = n_q / n_kv, most = G <= 8 ? 3 : 2;
+  const long long bytes = (long long)OWN_SMEM + 4ll * G * s.keys;
+  if (s.own_splits > 1 || bytes > (long long)OWN_SMEM_MOST) return 0;
+  const long long resident = std::min<long long>(most, 227 * 1024 / (bytes + 1024));
+  return resident == most || resident * sm_count >= (long long)B * n_kv ? s.keys : 0;
 }
 
 SharedPlan weights_plan(int B, int n_q, int n_kv, int key_limit, int sm_count) {
   SharedPlan s = shared_plan(B, n_q, n_kv, key_limit, 0, sm_count);
+  s.keep = weights_keep(s, B, n_q, n_kv, sm_count);
+  if (s.keep) return s;
   s.cluster = 0;  // the weights need a row's maximum and sum over all splits first
   s.join = 1;
   s.partials = (size_t)B * n_q * s.own_splits;
@@ -1051,8 +1131,8 @@ template <bool NAT>
 static cudaError_t launch_weights(const OwnParams& p, const SharedArgs& a, cudaStream_t st) {
   const int per = WEIGH_THREADS * WEIGH_KEYS;
   const int chunks = std::max(1, std::min((a.key_limit + per - 1) / per, 8 * a.sm_count / (a.B * a.n_kv)));
-  return launch_k(attn_weights_kernel<NAT>, dim3(chunks + !NAT, a.n_kv, a.B), dim3(WEIGH_THREADS), p.G * sizeof(float2), st,
-                  0, p);
+  return launch_k(attn_weights_kernel<NAT>, dim3(chunks + !NAT, a.n_kv, a.B), dim3(WEIGH_THREADS),
+                  p.G * sizeof(float2), st, 0, p);
 }
 
 cudaError_t launch_decode_weights(const SharedArgs& a, const SharedPlan& s, const WeightsArgs& w, cudaStream_t st) {
@@ -1060,13 +1140,15 @@ cudaError_t launch_decode_weights(const SharedArgs& a, const SharedPlan& s, cons
   p.scores = w.scores;
   p.weights = w.weights;
   p.ld = w.ld;
+  p.keep = s.keep;
   const dim3 grid(s.own_splits, a.n_kv, a.B), block(OWN_THREADS);
+  const size_t sm = OWN_SMEM + (size_t)4 * p.G * s.keep;
   const cudaError_t e =
-      p.G <= 8 ? launch_k(attn_own_kernel<true, OWeigh>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
+      p.G <= 8 ? launch_k(attn_own_kernel<true, OWeigh>, grid, block, sm, st, 0, *a.map_k, *a.map_v,
                           *a.map_k16, *a.map_v16, p)
-               : launch_k(attn_own_kernel<false, OWeigh>, grid, block, OWN_SMEM, st, 0, *a.map_k, *a.map_v,
-                          *a.map_k16, *a.map_v16, p);
-  if (e != cudaSuccess) return e;
+               : launch_k(attn_own_kernel<false, OWeigh>, grid, block, sm, st, 0, *a.map_k, *a.map_v,
+                           *a.map_k16, *a.map_v16, p);
+  if (e != cudaSuccess || s.keep) return e;
   return launch_weights<false>(p, a, st);
 }
 
@@ -1093,7 +1175,7 @@ cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cu
 // rows, 40 heads, up to 500 keys 19 and 32, up to 8000 138 and 108, up to 2000 capped 48
 // and 73 (the softmax of the other kernel works on all 128 rows); three 91 and 60. Where 8
 // CTAs for each (sequence, K/V head) are few and the context may be long, the other
-// kernel's equal shares count: one row, 8 K/V heads, 30000 keys 43 and 31 us.
+// kernel's equal shares count: one row, 8 K/V heads, 30000 keys 34 (57 CTAs each) and 30 us.
 bool tree_own_applies(const TreeArgs& a) {
   const int G = a.n_q / a.n_kv;
   if (a.head_dim != HD || G > 8 || (long long)a.n_rows + a.B > 65535) return false;
@@ -1131,15 +1213,27 @@ cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st) {
   p.n_seq = a.B;
   p.tree_rows = 8 / p.G;
   const int blocks = a.n_rows / p.tree_rows + std::min(a.B, a.n_rows);  // an upper bound
+  // splits as in shared_plan; clusters where all are resident at once (4 sequences of 2 rows,
+  // 32 / 8 heads, up to 1000 keys 9.7 us, with the joining kernel 11.0; 8 sequences of one
+  // row, 64 / 8 heads, up to 4096 keys, 512 CTAs 24.5 and 21.9)
   const int pairs = std::max(a.B, a.n_rows / p.tree_rows) * a.n_kv;
   int k = 1;
   while (pairs * k < 2 * a.sm_count && k < 8 && a.key_limit / (2 * k) >= 64) k *= 2;
+  while (k > 1 && p.rows * k * (HD + 2) * sizeof(float) > tree_partial_bytes(a.sm_count)) k /= 2;
   p.splits = k;
   p.min_share = 64;
-  p.cluster = k > 1;
-  const dim3 grid(k, a.n_kv, blocks), cluster(k > 1 ? k : 0, 1, 1);
-  return launch_kc(attn_own_kernel<true, OTree>, grid, dim3(OWN_THREADS), OWN_SMEM, st, cluster, *a.map_k, *a.map_v,
-                   *a.map_k16, *a.map_v16, p);
+  p.cluster = k > 1 && pairs * k <= 3 * a.sm_count;
+  p.join = k > 1 && !p.cluster;
+  p.own_room = p.rows * k;
+  p.own_o = a.partial;
+  p.own_ml = a.partial + p.own_room * HD;
+  p.part_o = p.own_o;  // no prefix: no parts of it
+  p.part_ml = p.own_ml;
+  const cudaError_t e = launch_kc(attn_own_kernel<true, OTree>, dim3(k, a.n_kv, blocks), dim3(OWN_THREADS), OWN_SMEM,
+                                  st, dim3(p.cluster ? k : 0, 1, 1), *a.map_k, *a.map_v, *a.map_k16, *a.map_v16, p);
+  if (e != cudaSuccess || !p.join) return e;
+  return launch_k(attn_own_join_kernel<OTree>, dim3((unsigned)((p.rows + 3) / 4)), dim3(128), 0, st, 0, p,
+                  (int)p.rows);
 }
 
 }  // namespace llgb
