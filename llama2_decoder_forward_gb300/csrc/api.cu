@@ -1514,7 +1514,8 @@ int llama_op_attention_tree(llama_ctx* c, const void* q, int32_t n_rows, const i
       (mask && mask_words < 1))
     return LLAMA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return LLAMA_ERR_INVALID_ARG;
-  if ((int64_t)n_rows * cf.n_q_heads >= (1ll << 30)) return LLAMA_ERR_OUT_OF_RANGE;
+  if ((int64_t)n_rows * cf.n_q_heads >= (1ll << 30) || (mask && mask_words > (1 << 25)))
+    return LLAMA_ERR_OUT_OF_RANGE;
   TRY(check_kv(c, kv, B));
   if (kv->kv_dtype != LLAMA_KV_MODEL) return LLAMA_ERR_UNSUPPORTED;
   TreeArgs a{};
@@ -1553,10 +1554,7 @@ int llama_op_attention_tree(llama_ctx* c, const void* q, int32_t n_rows, const i
   TRY(decode_maps(c, kv, n_rows, 128 / (cf.n_q_heads / cf.n_kv_heads), &a));
   a.partial = c->at<float>(c->L.spart);
   Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
-  if (tree_own_applies(a)) {
-    c->launches++;
-    return cuda_rc(launch_tree_own(a, c->stream));
-  }
+  if (tree_own_applies(a)) return cuda_rc(launch_tree_own(a, c->stream, &c->launches));
   c->launches += 2;
   return cuda_rc(launch_tree_tc(a, c->stream));
 }

@@ -317,7 +317,7 @@ struct TreeArgs {
 size_t tree_partial_bytes(int sm_count);
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st);    // k_attn_forms_tc.cu
 bool tree_own_applies(const TreeArgs& a);  // trees of few rows: k_attn_own.cu
-cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st);
+cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launches);
 cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t st);  // k_attn_simt.cu
 // How a decode batch over a shared prefix is cut: the prefix kernel's grid
 // (prefix_splits, row_blocks, n_kv) and the own keys' splits.

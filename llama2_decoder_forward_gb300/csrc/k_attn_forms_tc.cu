@@ -1,6 +1,6 @@
 // Attention with capped or biased scores on the 5th-generation tensor cores
 // (tcgen05), head_dim 128, bf16: packed documents (causal, with a two-way
-// prefix), and the shared prefix of a decode batch.
+// prefix), the shared prefix of a decode batch, and drafted trees over a cache.
 //
 //   x = scale q.k;  s = (cap tanh(x / cap) or x) - slope |i - j|;  p = softmax(s);  o = sum p v
 //
@@ -25,10 +25,11 @@
 //   documents, else            : rows q0 .. q0+127 and q0+128 .. q0+255;
 //   prefix, over 128 rows      : two blocks of (sequence, head of the group) rows;
 //   prefix, up to 128 rows     : the same rows; tile t takes every second key tile
-//                                (two key splits; each K/V tile has one reader).
+//                                (two key splits; each K/V tile has one reader);
+//   trees                      : as a prefix, row blocks of (tree row, head of the group).
 // so K and V are loaded once for both. Every mask here is "keys below a row's
 // limit": max(position + 1, prefix) for documents, the sequence's keys for the
-// prefix. O is rescaled lazily, when a row's maximum grows by more than 2^8.
+// prefix; trees add their rows' own bits in the key tiles that hold drafted rows. O is rescaled lazily, when a row's maximum grows by more than 2^8.
 //
 // Documents run as one CTA per SM that takes its share of the work items: the
 // producers load the next item's Q, K and V while the softmax and the store of
@@ -472,7 +473,8 @@ __device__ __forceinline__ int prefix_share(const FormsParams& p, int lane) {
 // are cut into equal chunks, one per CTA, so that every SM gets the same number of
 // tiles whatever the lengths. The blocks come first so that those of the same keys are
 // worked on at the same time, by CTAs far apart in the line, and read the keys from L2
-// but once (32 sequences of up to 8192 keys, two blocks of 256 rows each: XXX).
+// but once (32 sequences of up to 8192 keys, two blocks of 256 rows each: 254 -> 236 us
+// before the joining kernel).
 // A CTA's first and last item may be shared with its neighbours: those leave partial
 // results (CTA c: 2c for its first item, 2c + 1 for its last), which the joining kernel
 // merges; items within a chunk are stored at once.
@@ -503,14 +505,28 @@ __device__ __forceinline__ long long sum_upto(long long x, int lane) {
   }
   return x;
 }
-// Tiles of a chunk, for a whole warp; *total: of all items.
-__device__ __forceinline__ long long tree_chunk(const FormsParams& p, int ctas, int lane, uint32_t* status,
-                                                long long* total) {
-  long long all = 0;
-  for (int b = lane; b < p.n_docs; b += 32) {
-    const TreeSeq s = tree_seq(p, b, status);
-    all += s.blocks * s.tiles;
+// Each lane looks at this many sequences in a row.
+__device__ __forceinline__ int tree_per_lane(const FormsParams& p) { return (p.n_docs + 31) / 32; }
+// Tiles of the lane's sequences: of all their items (all), of those of one block.
+__device__ __forceinline__ long long tree_tiles(const FormsParams& p, int block, int lane, uint32_t* status,
+                                                long long* all) {
+  const int per = tree_per_lane(p);
+  long long mine = 0;
+  *all = 0;
+#pragma unroll 4
+  for (int i = 0; i < per; ++i) {
+    if (lane * per + i >= p.n_docs) break;
+    const TreeSeq s = tree_seq(p, lane * per + i, status);
+    *all += s.blocks * s.tiles;
+    mine += s.blocks > block ? s.tiles : 0;
   }
+  return mine;
+}
+// Tiles of a chunk, for a whole warp; *total: of all items; *mine: the lane's of the first blocks.
+__device__ __forceinline__ long long tree_chunk(const FormsParams& p, int ctas, int lane, uint32_t* status,
+                                                long long* total, long long* mine) {
+  long long all;
+  *mine = tree_tiles(p, 0, lane, status, &all);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   *total = all;
@@ -563,9 +579,23 @@ struct TreeWalk {
     it.g = 0;
     it.first = base;
   }
-  // the item of tile u
-  __device__ __forceinline__ bool seek(long long u) {
-    load(0);
+  // the item of tile u; mine: the tiles of the lane's sequences' first blocks
+  __device__ __forceinline__ bool seek(long long u, long long mine) {
+    for (;; ++block) {
+      long long all;
+      if (block > 0) mine = tree_tiles(p, block, lane, nullptr, &all);
+      const long long end = block_start + sum_upto(mine, lane);
+      const uint32_t m = __ballot_sync(0xffffffffu, u < end);
+      if (m) {
+        const int w = __ffs(m) - 1;
+        b0 = w * tree_per_lane(p);
+        load(__shfl_sync(0xffffffffu, end - mine, w));
+        break;
+      }
+      const long long last = __shfl_sync(0xffffffffu, end, 31);
+      if (last == block_start) return false;
+      block_start = last;
+    }
     for (;;) {
       const uint32_t m = __ballot_sync(0xffffffffu, u < upto);
       if (m) {
@@ -772,8 +802,9 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
         *p.used = used;
     }
   }
-  long long chunk = 0, total = 0;  // trees: tiles of a CTA, of all
-  if (TREE && warp == 16) chunk = tree_chunk(p, gridDim.x, lane, blockIdx.x == 0 ? p.status : nullptr, &total);
+  long long chunk = 0, total = 0, first_blocks = 0;  // trees: tiles of a CTA, of all, of the lane's first blocks
+  if (TREE && warp == 16)
+    chunk = tree_chunk(p, gridDim.x, lane, blockIdx.x == 0 ? p.status : nullptr, &total, &first_blocks);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -842,7 +873,7 @@ __global__ void __launch_bounds__(FORMS_THREADS, 1)
       const long long u_end = min(total, u + chunk);
       for (int it = 0; ok; ++it) {
         if (TREE) {
-          const bool more = u < u_end && (it == 0 ? walk.seek(u) : walk.next());
+          const bool more = u < u_end && (it == 0 ? walk.seek(u, first_blocks) : walk.next());
           const TreeItem& item = walk.it;
           if (more) {
             w.lo = item.lo;

@@ -1,6 +1,7 @@
 // Decode attention with capped or biased scores: the keys a sequence owns
 // (from the shared prefix's end to its position), bf16, head_dim 128, and the
-// merge with the prefix's partial results (k_attn_forms_tc.cu).
+// merge with the prefix's partial results (k_attn_forms_tc.cu). The same kernel adds up
+// how much each key weighs, and takes trees of few rows.
 //
 //   x = scale q.k;  s = (cap tanh(x / cap) or x) - slope (i - j);  softmax;  sum p v
 //
@@ -56,6 +57,7 @@ constexpr uint32_t SUB_HALF = SUB * 128;        // 16 keys x 64 dims
 constexpr uint32_t HALF = TILE_K * 128;         // 64 keys x 64 dims: 8 KB
 constexpr uint32_t STAGE = 4 * HALF;            // K and V, two dim halves each
 constexpr int SORT_MAX = 256;                   // sequences that a CTA sorts
+constexpr int TREE_COUNTED = 128;               // sequences whose blocks of tree rows a CTA counts
 constexpr uint32_t OFF_SORT = STAGES * STAGE + 256;
 constexpr uint32_t OFF_KEEP = OFF_SORT + (2 * SORT_MAX + 4) * 4;  // key weights: scores, in the kernel that adds them up
 constexpr size_t OWN_SMEM = OFF_KEEP + 1024;
@@ -86,10 +88,10 @@ struct OwnParams {
   float* weights;              // [B][n_kv][ld]
   int64_t ld;
   int keep;                    // room for so many of a row's scores in shared memory, the weights added here; 0: above
-  // small trees: every sequence's rows in blocks of tree_rows
+  // small trees: a sequence's rows in blocks of 2^tree_shift
   const int32_t *cu_rows, *start_pos, *row_pos;
   TreeMask tree;
-  int n_rows, n_seq, tree_rows;
+  int n_rows, n_seq, tree_shift;
 };
 
 // What a launch works on: a decode row per sequence; the same with its scores kept; the
@@ -553,12 +555,31 @@ __device__ __forceinline__ void store_row(bf16* dst, int lane, const RowSum& r) 
       make_uint2(pack_bf16(r.o.x * i, r.o.y * i), pack_bf16(r.o.z * i, r.o.w * i));
 }
 
-// Small trees: the z-th block of tree_rows rows, for a whole warp; false: there are fewer.
+// Small trees: which block of 2^tree_shift rows CTA z has, for a whole warp; false: none. Few
+// sequences' blocks are counted, so that CTAs to spare come last (64 sequences of 13 rows, 32
+// heads, 1000 keys 141 us, searched 148). Among many sequence b's begin with CTA
+// cu_rows[b] / 2^tree_shift + b, which leaves room for each and one CTA or none to spare, and
+// a lookup goes 32 ways (256 sequences of a row, 32 heads, 512 keys: counted 192 us, searched 179;
+// 512 sequences, 64 / 8 heads, 256 keys 145 and 92).
 __device__ __forceinline__ bool tree_block(const OwnParams& p, int z, int lane, int& b, int& i0, int& lo, int& n) {
+  if (p.n_seq > TREE_COUNTED) {
+    auto begin = [&](int i) { return (min(max(p.cu_rows[i], 0), p.n_rows) >> p.tree_shift) + i; };
+    b = 0;
+    for (int len = p.n_seq; len > 1;) {
+      const int step = (len + 31) / 32, i = lane * step;
+      const uint32_t m = __ballot_sync(0xffffffffu, i < len && begin(b + i) <= z);
+      const int w = m ? 31 - __clz(m) : 0;
+      b += w * step;
+      len = min(step, len - w * step);
+    }
+    doc_rows(p.cu_rows, b, p.n_rows, nullptr, lo, n);
+    i0 = (z - begin(b)) << p.tree_shift;
+    return i0 >= 0 && i0 < n;
+  }
   for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
     int my_lo = 0, my_n = 0;
     if (b0 + lane < p.n_seq) doc_rows(p.cu_rows, b0 + lane, p.n_rows, nullptr, my_lo, my_n);
-    const int blocks = (my_n + p.tree_rows - 1) / p.tree_rows;
+    const int blocks = (my_n + (1 << p.tree_shift) - 1) >> p.tree_shift;
     int upto = blocks;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -569,7 +590,7 @@ __device__ __forceinline__ bool tree_block(const OwnParams& p, int z, int lane, 
     if (m) {
       const int w = __ffs(m) - 1;
       b = b0 + w;
-      i0 = (z - __shfl_sync(0xffffffffu, upto - blocks, w)) * p.tree_rows;
+      i0 = (z - __shfl_sync(0xffffffffu, upto - blocks, w)) << p.tree_shift;
       lo = __shfl_sync(0xffffffffu, my_lo, w);
       n = __shfl_sync(0xffffffffu, my_n, w);
       return true;
@@ -649,7 +670,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     if (!tree_block(p, blockIdx.z, lane, b, R.i0, R.lo, n)) return;  // a cluster's CTAs all do
     pos = tree_keys(p, b, R) - 1;  // the last key
     if ((p.start_pos[b] < 0 || R.there < n) && split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
-    R.count = min(p.tree_rows, n - R.i0) * p.G;
+    R.count = min(1 << p.tree_shift, n - R.i0) * p.G;
   } else if (p.sorted) {
     // the blockIdx.z-th longest sequence, so that the longest start first: one key
     // of 32 bits per sequence, its length and (ties) its number
@@ -1178,14 +1199,14 @@ cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cu
 // kernel's equal shares count: one row, 8 K/V heads, 30000 keys 34 (57 CTAs each) and 30 us.
 bool tree_own_applies(const TreeArgs& a) {
   const int G = a.n_q / a.n_kv;
-  if (a.head_dim != HD || G > 8 || (long long)a.n_rows + a.B > 65535) return false;
+  if (a.head_dim != HD || G > 8 || (long long)a.B + a.n_rows > 65535) return false;  // the launch's grid
   const long long pairs = (long long)a.B * a.n_kv, rows = (a.n_rows + a.B - 1) / a.B;  // the mean
   const long long blocks = (rows + 8 / G - 1) / (8 / G);
   if (8 * pairs < 2 * a.sm_count && a.key_limit > 8192) return false;
   return blocks == 1 || (blocks == 2 && (a.sc.cap > 0.f || a.sc.slopes || a.key_limit <= 2048));
 }
 
-cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st) {
+cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launches) {
   OwnParams p{};
   p.q = (const bf16*)a.q;
   p.out = (bf16*)a.out;
@@ -1211,12 +1232,12 @@ cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st) {
   p.tree = TreeMask{a.mask, a.mask_words};
   p.n_rows = a.n_rows;
   p.n_seq = a.B;
-  p.tree_rows = 8 / p.G;
-  const int blocks = a.n_rows / p.tree_rows + std::min(a.B, a.n_rows);  // an upper bound
+  while (2 * p.G << p.tree_shift <= 8) ++p.tree_shift;
+  const int blocks = (a.n_rows >> p.tree_shift) + a.B;
   // splits as in shared_plan; clusters where all are resident at once (4 sequences of 2 rows,
   // 32 / 8 heads, up to 1000 keys 9.7 us, with the joining kernel 11.0; 8 sequences of one
   // row, 64 / 8 heads, up to 4096 keys, 512 CTAs 24.5 and 21.9)
-  const int pairs = std::max(a.B, a.n_rows / p.tree_rows) * a.n_kv;
+  const int pairs = std::max(a.B, a.n_rows >> p.tree_shift) * a.n_kv;
   int k = 1;
   while (pairs * k < 2 * a.sm_count && k < 8 && a.key_limit / (2 * k) >= 64) k *= 2;
   while (k > 1 && p.rows * k * (HD + 2) * sizeof(float) > tree_partial_bytes(a.sm_count)) k /= 2;
@@ -1224,6 +1245,7 @@ cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st) {
   p.min_share = 64;
   p.cluster = k > 1 && pairs * k <= 3 * a.sm_count;
   p.join = k > 1 && !p.cluster;
+  *launches += p.join ? 2 : 1;
   p.own_room = p.rows * k;
   p.own_o = a.partial;
   p.own_ml = a.partial + p.own_room * HD;
