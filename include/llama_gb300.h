@@ -606,8 +606,8 @@ int llama_op_rope_norm_append_at(llama_ctx* ctx, const void* qkv, int32_t qkv_dt
  * |V| as in llama_op_attention_docs. cu_rows outside [0, n_rows] or decreasing, a
  * negative start (its rows give zeros) and slots past the cache (not attended) set
  * LLAMA_FLAG_POS_RANGE, a page id outside the pool LLAMA_FLAG_PAGE_RANGE (its keys read
- * as zeros). Any number of rows, n_rows * n_q < 2^30; B as the cache allows. The cache has
- * the context's dtype (an E4M3 cache is UNSUPPORTED). One launch, bf16 two. */
+ * as zeros). Any number of rows, n_rows * n_q < 2^30; mask_words to 2^25; B as the cache
+ * allows. The cache has the context's dtype (an E4M3 cache is UNSUPPORTED). One or two launches. */
 int llama_op_attention_tree(llama_ctx* ctx, const void* q, int32_t n_rows, const int32_t* cu_rows,
                             const int32_t* start_pos, int32_t B, const uint32_t* mask,
                             int32_t mask_words, const int32_t* positions, int32_t layer,

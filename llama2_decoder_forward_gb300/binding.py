@@ -664,7 +664,7 @@ class Model:
         n, B = q.shape[0], start_pos.numel()
         qn, words = n * s.n_q_heads * s.head_dim, 0
         if mask is not None:
-            if mask.dim() != 2:
+            if mask.dim() != 2 or mask.shape[1] < 1:
                 raise ValueError("mask: want [n_rows, words], got %s" % (tuple(mask.shape),))
             words = mask.shape[1]
         rc = self._tree(

@@ -792,3 +792,500 @@ def test_tree_bad_bounds_are_flagged(dtype):
     (rc, flags), out = call([0, 3, 6, 9, 12], [10, 20, 30, 40])
     assert rc == 5 and flags == binding.FLAG_PAGE_RANGE
     assert torch.equal(out[:3], base[:3]) and torch.equal(out[6:], base[6:]) and torch.isfinite(out.float()).all()
+
+
+# --------------------------------------------------------------------------- together, as they are used
+def _place(kv, pt, layer, b, rows, values):
+    """Puts values [n, n_kv, d] at slots `rows` of sequence b, for K and V."""
+    for t, x in zip((kv.k, kv.v), values):
+        if pt is None:
+            t[layer, b, :, rows] = x.transpose(0, 1)
+        else:
+            t[layer, pt[b].long()[rows // kv.page_size].cuda(), :, (rows % kv.page_size).cuda()] = x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_verified_drafts_run(dtype):
+    """Two sequences, two layers: prompts are cached, then three times a tree is drafted, appended
+    at its depths' positions, attended, and its accepted path kept. The cache then is the one
+    that plain appends of the accepted tokens give, to the bit, and each accepted row's output
+    is its attention over that cache."""
+    nq, nkv, d, layers, page = 4, 2, 128, 2, 16
+    m, shape = _model(nq, nkv, d, dtype, max_batch=2, max_seq=256, n_layers=layers)
+    dt = shape.torch_dtype
+    pt = torch.randperm(20, generator=_gen(1)).view(2, 10).to(torch.int32)
+    kv, plain = (binding.KVCache(shape, n_pages=20, page_size=page, page_table=pt.cuda()) for _ in range(2))
+    rope = binding.Rope(None, binding.ROPE_HALF, d)
+    kw = dict(rope=rope, k_gain=(1 + 0.1 * torch.randn(d, generator=_gen(2))).to(dt).cuda())
+    slopes = _slopes(nq)
+    scores = binding.Scores(cap=25.0, slopes=slopes.cuda())
+    lens = [19, 33]
+    cu = _i32([0, lens[0], sum(lens)])
+    q = torch.empty(sum(lens), nq * d, dtype=dt, device="cuda")
+    for l in range(layers):
+        x = _randn((sum(lens), shape.qkv_rows), torch.float32, 300 + l).cuda()
+        for c in (kv, plain):
+            m.op_rope_norm_append(x, _i32([0, 0]), l, c, q, cu_rows=cu, **kw)
+    for step in range(3):
+        rows = [12, 7 + step]
+        n = sum(rows)
+        parents = [_random_tree(r, 60 + 2 * step + b) for b, r in enumerate(rows)]
+        see = [C.tree_visible(p) for p in parents]
+        pos, paths = [], []
+        for b in range(2):
+            pos += [lens[b] + int(see[b][i].sum()) - 1 for i in range(rows[b])]
+            leaf = rows[b] - 1 - step * b
+            paths.append([j for j in range(rows[b]) if see[b][leaf, j]])
+        mask = torch.from_numpy(np.concatenate([C.mask_words(s) for s in see])).cuda()
+        cu, start, at = _i32([0, rows[0], n]), _i32(lens), _i32(pos)
+        outs, qs = [], []
+        for l in range(layers):
+            x = _randn((n, shape.qkv_rows), torch.float32, 320 + 2 * step + l).cuda()
+            q, o = (torch.empty(n, nq * d, dtype=dt, device="cuda") for _ in range(2))
+            m.op_rope_norm_append(x, start, l, kv, q, cu_rows=cu, positions=at, **kw)
+            m.op_attention_tree(q, cu, start, l, kv, o, mask=mask, positions=at, scores=scores)
+            outs.append(o)
+            qs.append(q)
+            keep = [p for p in paths[0]] + [rows[0] + p for p in paths[1]]
+            q2 = torch.empty(len(keep), nq * d, dtype=dt, device="cuda")
+            m.op_rope_norm_append(x[keep].contiguous(), start, l, plain, q2,
+                                  cu_rows=_i32([0, len(paths[0]), len(keep)]), **kw)
+            m.sync()
+            assert torch.equal(q[keep], q2)
+        width = max(map(len, paths))
+        m.op_cache_commit(kv, start, _i32([p + [0] * (width - len(p)) for p in paths]), _i32([len(p) for p in paths]))
+        m.sync()
+        for b in range(2):
+            lens[b] += len(paths[b])
+            for l in range(layers):
+                K, V = (_keys_of(t.cpu(), pt, page, l, b, lens[b]) for t in (plain.k, plain.v))
+                for got, want in zip((kv.k, kv.v), (K, V)):
+                    assert np.array_equal(_keys_of(got.cpu(), pt, page, l, b, lens[b]), want)
+                for i, row in enumerate(paths[b]):
+                    seen = lens[b] - len(paths[b]) + i + 1
+                    r = row + (rows[0] if b else 0)
+                    for h in range(nq):
+                        g, qf = h // 2, f64(qs[l])[r].reshape(nq, d)[h]
+                        ref, mass = C.attend(qf, K[g][:seen], V[g][:seen], seen - 1, np.arange(seen), np.ones(seen, bool),
+                                             1 / math.sqrt(d), 25.0, float(slopes[h]))
+                        e = _score_error(qf, K[g], 1 / math.sqrt(d), 25.0, seen)
+                        _within(outs[l][r].view(nq, d)[h], ref, _out_bound(ref, mass, dtype, e, seen),
+                                "step %d layer %d sequence %d row %d head %d" % (step, l, b, row, h))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bounded_cache_run(dtype):
+    """Two sequences, two layers: tokens are appended behind the kept keys at their own positions,
+    weigh the keys they attend, and whenever a cache is full its lightest keys are dropped.
+    Every head's keys, their weights and the outputs are those of lists kept in fp64."""
+    nq, nkv, d, layers, page, top, keep, first, recent = 4, 2, 128, 2, 16, 44, 24, 3, 6
+    m, shape = _model(nq, nkv, d, dtype, max_batch=2, max_seq=256, n_layers=layers)
+    dt = shape.torch_dtype
+    pt = torch.randperm(6, generator=_gen(4)).view(2, 3).to(torch.int32)
+    kv = binding.KVCache(shape, n_pages=6, page_size=page, page_table=pt.cuda())
+    rope = binding.Rope(None, binding.ROPE_ADJACENT, d)
+    w = torch.zeros(layers, 2, nkv, 48, device="cuda")
+    scratch = torch.empty(2, nq, 48, device="cuda")
+    kept = torch.empty(layers, 2, nkv, keep, dtype=torch.int32, device="cuda")
+    # what is in the cache: [layer][sequence][head] of keys, values, weights and what those may be off by
+    have = [[[dict(k=[], v=[], w=[], e=[]) for _ in range(nkv)] for _ in range(2)] for _ in range(layers)]
+    token, lens, evictions = [0, 7], [0, 0], 0
+    q, o = (torch.empty(2, nq * d, dtype=dt, device="cuda") for _ in range(2))
+    k, v = (torch.empty(2, nkv * d, dtype=dt, device="cuda") for _ in range(2))
+    for step in range(top + 2 * (top - keep) + 3):
+        for l in range(layers):
+            x = _randn((2, shape.qkv_rows), torch.float32, 400 + 2 * step + l, 1.3).cuda()
+            m.op_rope_norm_append(x, _i32(lens), l, kv, q, rope=rope, positions=_i32(token), k_out=k, v_out=v)
+            m.op_attention_decode_weights(q, _i32(lens), l, kv, o, w[l], scratch)
+            m.sync()
+            for b in range(2):
+                for g in range(nkv):
+                    H = have[l][b][g]
+                    H["k"].append(f64(k)[b].reshape(nkv, d)[g])
+                    H["v"].append(f64(v)[b].reshape(nkv, d)[g])
+                    H["w"].append(0.0)
+                    H["e"].append(0.0)
+                    K, V, n = np.stack(H["k"]), np.stack(H["v"]), len(H["k"])
+                    for h in (2 * g, 2 * g + 1):
+                        qf = f64(q)[b].reshape(nq, d)[h]
+                        p = C.weigh(qf, K, 0, np.arange(n), np.ones(n, bool), 1 / math.sqrt(d))
+                        e = _score_error(qf, K, 1 / math.sqrt(d), 0.0, 0)
+                        _within(o[b].view(nq, d)[h], p @ V, _out_bound(p @ V, p @ np.abs(V), dtype, e, n),
+                                "step %d layer %d sequence %d head %d" % (step, l, b, h))
+                        for j in range(n):
+                            H["w"][j] += p[j]
+                            # its error and, of the sum so far, a rounding
+                            H["e"][j] += p[j] * (2 * e + (n / 8 + 64) * 2.0 ** -24) + 2 * 2.0 ** -24 * H["w"][j]
+        lens = [n + 1 for n in lens]
+        token = [t + 1 for t in token]
+        got = f64(w)
+        for l in range(layers):
+            for b in range(2):
+                for g in range(nkv):
+                    H = have[l][b][g]
+                    _within(got[l, b, g, :lens[b]], np.array(H["w"]), np.array(H["e"]) + 1e-37, "weights")
+                    assert np.all(got[l, b, g, lens[b]:] == 0)
+        if lens[0] == top:
+            evictions += 1
+            m.op_cache_evict(kv, _i32(lens), keep, w, kept, first=first, recent=recent)
+            m.sync()
+            for l in range(layers):
+                for b in range(2):
+                    for g in range(nkv):
+                        stay = C.evict(got[l, b, g, :top], keep, first, recent)
+                        assert kept[l, b, g].tolist() == stay
+                        H = have[l][b][g]
+                        for name in H:
+                            H[name] = [H[name][i] for i in stay]
+            lens = [keep] * 2
+    assert evictions == 3
+
+
+# --------------------------------------------------------------------------- streams, graphs, sizes
+class _Step:
+    """All five calls on buffers of their own; tree rows enough for the tensor-core kernel, and few."""
+
+    def __init__(self, nq=8, nkv=2, seed=0, stream=None, B=2):
+        self.m, shape = _model(nq, nkv, max_batch=B, max_seq=1024)
+        self.kv, *_ = _filled(shape, B, 1024, 16, torch.bfloat16, 500 + seed)
+        self.first = [self.kv.k.clone(), self.kv.v.clone()]
+        self.rows = [40, 23]
+        n = sum(self.rows)
+        self.x = torch.empty(n, shape.qkv_rows, device="cuda")
+        self.cu, self.start = _i32([0, 40, 63]), _i32([700, 300])
+        self.one, self.few = _i32([0, 1, 3]), _randn((3, nq, 128), torch.bfloat16, 520 + seed).cuda()
+        self.at = _i32([0] * n)
+        self.mask = torch.empty(n, 2, dtype=torch.int32, device="cuda")
+        self.path, self.path_len = _i32([[0] * 8] * 2), _i32([0, 0])
+        self.lens = _i32([0, 0])
+        self.w = torch.zeros(1, B, nkv, 1024, device="cuda")
+        self.scratch = torch.empty(B, nq, 1024, device="cuda")
+        self.rope = binding.Rope(None, binding.ROPE_HALF, 128)
+        self.seed = seed
+        bf = dict(dtype=torch.bfloat16, device="cuda")
+        self.q, self.o, self.o2 = torch.empty(n, nq * 128, **bf), torch.empty(n, nq * 128, **bf), torch.empty(3, nq * 128, **bf)
+        self.o3, self.kept = torch.empty(B, nq * 128, **bf), torch.empty(1, B, nkv, 200, dtype=torch.int32, device="cuda")
+        if stream is not None:
+            torch.cuda.synchronize()
+            self.m.set_stream(stream)
+
+    def inputs(self, i):
+        r = np.random.RandomState(31 * i + self.seed)
+        self.kv.k.copy_(self.first[0])
+        self.kv.v.copy_(self.first[1])
+        self.x.copy_(_randn(self.x.shape, torch.float32, 540 + i + self.seed))
+        self.start.copy_(_i32(r.randint(250, 900, 2).tolist()))
+        self.at.copy_(_i32(r.randint(0, 500, 63).tolist()))
+        self.mask.copy_(torch.from_numpy(np.concatenate([C.mask_words(C.tree_visible(_random_tree(n, i)), 2) for n in self.rows])))
+        paths = [sorted(r.choice(n, 8, replace=False).tolist()) for n in self.rows]
+        self.path.copy_(_i32(paths))
+        self.path_len.copy_(_i32([int(r.randint(0, 9)), 8]))
+        self.lens.copy_(self.start + self.path_len)
+        self.w.copy_(torch.rand(self.w.shape, generator=_gen(i)))
+
+    def run(self):
+        m, kv = self.m, self.kv
+        m.op_rope_norm_append(self.x, self.start, 0, kv, self.q, cu_rows=self.cu, positions=self.at, rope=self.rope)
+        m.op_attention_tree(self.q, self.cu, self.start, 0, kv, self.o, mask=self.mask, scores=binding.Scores(cap=30.0))
+        m.op_attention_tree(self.few, self.one, self.start, 0, kv, self.o2)
+        m.op_cache_commit(kv, self.start, self.path, self.path_len)
+        m.op_attention_decode_weights(self.q[:2], self.start, 0, kv, self.o3, self.w, self.scratch)
+        m.op_cache_evict(kv, self.lens, 200, self.w, self.kept, first=4, recent=20)
+
+    def results(self):
+        # (slots behind the kept ones hold anything: all of them are compared here, since the moves are the same)
+        return [t.clone() for t in (self.q, self.o, self.o2, self.o3, self.w, self.kept, self.kv.k.view(torch.int16),
+                                    self.kv.v.view(torch.int16))]
+
+
+def test_captured_replays_follow_their_buffers():
+    s = torch.cuda.Stream()
+    steps = [_Step(stream=s), _Step(nq=16, nkv=16, seed=1, stream=s)]
+    graphs = []
+    for st in steps:
+        st.inputs(9)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            st.run()
+        graphs.append(g)
+    # and a second graph of the first context: both use its one workspace, in turn
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        steps[0].run()
+    for st, pair in ((steps[0], (graphs[0], g)), (steps[1], (graphs[1],))):
+        for i in range(4):
+            st.inputs(i)
+            torch.cuda.synchronize()
+            st.run()
+            st.m.sync()
+            want = st.results()
+            for graph in pair:
+                st.inputs(i)
+                torch.cuda.synchronize()
+                with torch.cuda.stream(s):
+                    graph.replay()
+                torch.cuda.synchronize()
+                for a, b in zip(st.results(), want):
+                    assert torch.equal(a.nan_to_num() if a.is_floating_point() else a,
+                                       b.nan_to_num() if b.is_floating_point() else b)
+        st.m.sync()
+
+
+def test_two_contexts_on_two_streams_at_once():
+    steps = [_Step(seed=i, nq=nq, nkv=nkv, stream=torch.cuda.Stream()) for i, (nq, nkv) in enumerate(((8, 2), (4, 4)))]
+    alone = []
+    for st in steps:
+        st.inputs(3)
+        torch.cuda.synchronize()
+        st.run()
+        st.m.sync()
+        alone.append(st.results())
+    for _ in range(10):
+        for st in steps:
+            st.inputs(3)
+        torch.cuda.synchronize()
+        for st in steps:
+            st.run()
+        for st in steps:
+            st.m.sync()
+        for st, want in zip(steps, alone):
+            for a, b in zip(st.results(), want):
+                assert torch.equal(a.nan_to_num() if a.is_floating_point() else a,
+                                   b.nan_to_num() if b.is_floating_point() else b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [0, 64])
+def test_cache_offsets_past_32_bits(dtype, page):
+    # the last slots of a cache of more than 2^31 values
+    nq, nkv, d, cap, n, rows = 4, 2, 128, 1 << 17, 150, 9
+    B = 2 if page else 66
+    m, shape = _model(nq, nkv, d, dtype, max_batch=B, max_seq=256)
+    dt = shape.torch_dtype
+    if page:
+        total = 66 * cap // page
+        pt = torch.full((2, 4), -1, dtype=torch.int32)
+        pt[1, :3] = torch.tensor([total - 3, total - 1, total - 2])
+        kv = binding.KVCache(shape, n_pages=total, page_size=page, page_table=pt.cuda())
+    else:
+        pt, kv = None, binding.KVCache(shape, batch=B, capacity=cap)
+    assert kv.k.numel() > 1 << 31
+    last = B - 1
+    K, V = (_randn((n, nkv, d), dt, 600 + i, 1.5) for i in range(2))
+
+    def fill():
+        _place(kv, pt, 0, last, torch.arange(n), (K.cuda(), V.cuda()))
+
+    def there():
+        j = torch.arange(n)
+        if page:
+            return [t[0, pt[last].long()[j // page].cuda(), :, (j % page).cuda()].cpu() for t in (kv.k, kv.v)]
+        return [t[0, last, :, :n].transpose(0, 1).cpu() for t in (kv.k, kv.v)]
+    fill()
+    kf, vf = f64(K).transpose(1, 0, 2), f64(V).transpose(1, 0, 2)
+    # a chain of rows, few and more
+    for r in (1, rows, 60):
+        q = _randn((r, nq, d), dt, 610, 1.5)
+        out = torch.empty(r, nq * d, dtype=dt, device="cuda")
+        m.op_attention_tree(q.cuda(), _i32([0] * B + [r]), _i32([0] * last + [n - r]), 0, kv, out)
+        m.sync()
+        for i in range(r):
+            for h in range(nq):
+                qf, c = f64(q)[i, h], n - r + i + 1
+                ref, mass = C.attend(qf, kf[h // 2, :c], vf[h // 2, :c], 0, np.arange(c), np.ones(c, bool), 1 / math.sqrt(d))
+                e = _score_error(qf, kf[h // 2], 1 / math.sqrt(d), 0, 0)
+                _within(out[i].view(nq, d)[h], ref, _out_bound(ref, mass, dtype, e, n), "tree")
+    q = torch.zeros(B, nq, d, dtype=dt)
+    q[last] = _randn((nq, d), dt, 611, 1.5)
+    w, scratch = torch.zeros(B, nkv, 160, device="cuda"), torch.empty(B, nq, 160, device="cuda")
+    out = torch.empty(B, nq * d, dtype=dt, device="cuda")
+    m.op_attention_decode_weights(q.cuda(), _i32([-1] * last + [n - 1]), 0, kv, out, w, scratch)
+    rc, flags = m.sync_status()
+    assert rc == 5 and flags == binding.FLAG_POS_RANGE and torch.all(w[:last] == 0)
+    for g in range(nkv):
+        want, tol = np.zeros(n), np.zeros(n)
+        for h in (2 * g, 2 * g + 1):
+            p = C.weigh(f64(q)[last, h], kf[g], 0, np.arange(n), np.ones(n, bool), 1 / math.sqrt(d))
+            e = _score_error(f64(q)[last, h], kf[g], 1 / math.sqrt(d), 0, 0)
+            want, tol = want + p, tol + p * (2 * e + (n / 8 + 64) * 2.0 ** -24)
+            _within(out[last].view(nq, d)[h], p @ vf[g], _out_bound(p @ vf[g], p @ np.abs(vf[g]), dtype, e, n), "weights")
+        _within(w[last, g, :n], want, tol + 4 * 2.0 ** -24 * want + 1e-37, "weights")
+    path = sorted(np.random.RandomState(5).choice(100, 30, replace=False).tolist())
+    m.op_cache_commit(kv, _i32([0] * last + [40]), _i32([[0] * 30] * last + [path]), _i32([0] * last + [30]))
+    m.sync()
+    for got, was in zip(there(), (K, V)):
+        want = was.clone()
+        want[40:70] = was[[40 + p for p in path]]
+        assert torch.equal(got, want)
+    fill()
+    kept = torch.empty(1, B, nkv, 50, dtype=torch.int32, device="cuda")
+    was_w = f64(w)
+    m.op_cache_evict(kv, _i32([0] * last + [n]), 50, w.view(1, B, nkv, 160), kept, first=2, recent=10)
+    m.sync()
+    for g in range(nkv):
+        stay = C.evict(was_w[last, g, :n], 50, 2, 10)
+        assert kept[0, last, g].tolist() == stay
+        for got, was in zip(there(), (K, V)):
+            assert torch.equal(got[:50, g], was[stay, g])
+    # a row appended at a far slot, at a position of its own
+    x = torch.zeros(B, shape.qkv_rows, device="cuda")
+    x[last] = _randn((shape.qkv_rows,), torch.float32, 612).cuda()
+    rope = binding.Rope(None, binding.ROPE_HALF, d)
+    outs = [torch.empty(B, nq * d, dtype=dt, device="cuda") for _ in range(2)]
+    got = []
+    for o, slot, at in zip(outs, (n - 1, 30), (_i32([0] * last + [30]), None)):
+        m.op_rope_norm_append(x, _i32([-1] * last + [slot]), 0, kv, o, rope=rope, positions=at)
+        assert m.sync_status() == (5, binding.FLAG_POS_RANGE)
+        got.append([t[slot] for t in there()])
+    assert torch.equal(outs[0], outs[1]) and all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_weight_offsets_past_32_bits():
+    # the last head's weights lie more than 2^31 values from the first's
+    m, shape = _model(2, 2, max_batch=2, max_seq=256)
+    kv, k, v, pt = _filled(shape, 2, 150, 16, torch.bfloat16, 620)
+    ld = (1 << 31) // 3 + 8
+    q = _randn((2, 2, 128), torch.bfloat16, 621, 1.5).cuda()
+    w, scratch = (torch.empty(2, 2, ld, device="cuda") for _ in range(2))
+    small, out, ref = torch.zeros(2, 2, 150, device="cuda"), *(torch.empty(2, 256, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w[:, :, :200] = 0
+    pos = _i32([149, 140])
+    m.op_attention_decode_weights(q, pos, 0, kv, out, w, scratch)
+    m.op_attention_decode_weights(q, pos, 0, kv, ref, small, torch.empty(2, 2, 150, device="cuda"))
+    m.sync()
+    assert torch.equal(out, ref) and torch.equal(w[:, :, :150], small) and torch.all(w[:, :, 150:200] == 0)
+    kept = torch.empty(1, 2, 2, 50, dtype=torch.int32, device="cuda")
+    m.op_cache_evict(kv, pos + 1, 50, w.unsqueeze(0), kept, recent=10)
+    m.sync()
+    for b in range(2):
+        for g in range(2):
+            stay = C.evict(f64(small)[b, g, :150 - 9 * b], 50, 0, 10)
+            assert kept[0, b, g].tolist() == stay
+            assert torch.equal(w[b, g, :50], small[b, g, stay]) and not w[b, g, 50:].any()
+
+
+def test_tree_searched_blocks():
+    # so many sequences that a CTA looks its own up, some without rows
+    r = np.random.RandomState(7)
+    for nq, nkv, B in ((2, 2, 129), (8, 1, 300), (4, 2, 1100)):
+        rows = r.randint(0, 8 if nq == 2 else 3, B).tolist()
+        rows[-1], rows[0] = 2, 0
+        _tree_case(nq, nkv, 128, "bf16", r.randint(0, 60, B).tolist(), rows, check=[0, 6], heads=[0, nq - 1], lead=3, tail=2)
+    _tree_case(2, 2, 128, "bf16", [5] * 200, [0] * 150 + [70] + [0] * 49, check=[0, 8, 69])
+
+
+# --------------------------------------------------------------------------- refusals
+def test_refusals():
+    m, shape = _model(4, 2, max_batch=2, max_seq=64)
+    m32, s32 = _model(2, 1, 40, "f32", max_batch=2, max_seq=64)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    kv = binding.KVCache(shape, batch=2, capacity=64)
+    fp8 = binding.KVCache(shape, batch=2, capacity=64, e4m3=(1.0, 1.0))
+    q, out, cu, start = torch.zeros(2, 512, **bf), torch.zeros(2, 512, **bf), _i32([0, 1, 2]), _i32([3, 4])
+    w, scratch = torch.zeros(1, 2, 2, 64, device="cuda"), torch.zeros(2, 4, 64, device="cuda")
+    path, n = _i32([[0, 1]] * 2), _i32([1, 1])
+    kept = torch.zeros(1, 2, 2, 8, dtype=torch.int32, device="cuda")
+    good = {
+        "tree": (m.op_attention_tree, dict(q=q, cu_rows=cu, start_pos=start, layer=0, kv=kv, out=out)),
+        "weights": (m.op_attention_decode_weights, dict(q=q, positions=start, layer=0, kv=kv, out=out, weights=w[0], scratch=scratch)),
+        "commit": (m.op_cache_commit, dict(kv=kv, start_pos=start, path=path, path_len=n)),
+        "evict": (m.op_cache_evict, dict(kv=kv, lens=start, keep=8, weights=w, kept=kept)),
+    }
+
+    def refused(rc, name, **kw):
+        fn, base = good[name]
+        if rc is None:
+            with pytest.raises(ValueError):
+                fn(**dict(base, **kw))
+            return
+        with pytest.raises(binding.LlamaError) as e:
+            fn(**dict(base, **kw))
+        assert e.value.rc == rc, (name, kw, e.value.rc)
+    for fn, kw in good.values():
+        fn(**kw)
+    m.sync()
+    three = _i32([0, 0, 0])
+    kv3 = binding.KVCache(shape, batch=3, capacity=64)
+    skew = torch.zeros(2 * 512 + 4, **bf)[4:].view(2, 512)  # 8 bytes past a 16-byte boundary
+    for name in ("tree", "weights"):
+        for layer in (-1, 1):
+            refused(1, name, layer=layer)
+        refused(2, name, kv=fp8)
+        refused(1, name, q=skew)
+        refused(1, name, out=skew)
+        for sc in (binding.Scores(cap=-1.0), binding.Scores(scale=float("nan")), binding.Scores(cap=1e-35)):
+            refused(1, name, scores=sc)
+        refused(None, name, scores=binding.Scores(slopes=torch.ones(3, device="cuda")))
+        for key in ("q", "out"):
+            refused(None, name, **{key: torch.zeros(2, 512, device="cuda")})
+            refused(None, name, **{key: torch.zeros(2, 511, **bf)})
+            refused(None, name, **{key: torch.zeros(2, 512, dtype=torch.bfloat16)})
+            refused(None, name, **{key: torch.zeros(512, 2, **bf).t()})
+    for layer in (-2, 1):
+        refused(1, "commit", layer=layer)
+        refused(1, "evict", layer=layer)
+    for name, key in (("tree", "cu_rows"), ("tree", "start_pos"), ("weights", "positions"), ("commit", "start_pos"),
+                      ("commit", "path"), ("commit", "path_len"), ("evict", "lens"), ("evict", "kept")):
+        t = good[name][1][key]
+        refused(None, name, **{key: t.cpu()})
+        refused(None, name, **{key: t.long()})
+        if key != "kept":
+            refused(None, name, **{key: torch.stack((t, t), -1)[..., 0]})  # with a stride
+    # lengths that do not fit each other
+    refused(None, "tree", cu_rows=_i32([0, 2]))
+    refused(None, "tree", mask=torch.zeros(1, 1, dtype=torch.int32, device="cuda"))
+    refused(None, "tree", mask=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    refused(None, "tree", mask=torch.zeros(2, 1, dtype=torch.int64, device="cuda"))
+    refused(None, "tree", positions=_i32([0]))
+    refused(None, "tree", mask=torch.zeros(2, 0, dtype=torch.int32, device="cuda"))
+    refused(None, "weights", scratch=torch.zeros(2, 4, 63, device="cuda"))
+    refused(None, "weights", weights=torch.zeros(2, 1, 64, device="cuda"))
+    refused(None, "weights", weights=torch.zeros(2, 2, 64, **bf))
+    refused(1, "weights", scratch=torch.zeros(2 * 4 * 64 + 1, device="cuda")[1:])
+    refused(None, "commit", path_len=_i32([1]))
+    refused(1, "commit", path=torch.zeros(2, 0, dtype=torch.int32, device="cuda"))
+    for kw in (dict(keep=0, kept=kept[..., :0].contiguous()), dict(first=-1), dict(recent=-1), dict(first=5, recent=4), dict(first=2 ** 31 - 1, recent=2 ** 31 - 1)):
+        refused(1, "evict", **kw)
+    refused(None, "evict", keep=9)
+    refused(None, "evict", weights=torch.zeros(1, 2, 1, 64, device="cuda"))
+    refused(None, "evict", weights_out=torch.zeros(1, 2, 2, 32, device="cuda"))
+    refused(None, "evict", weights_out=torch.zeros(1, 2, 2, 64))
+    # more sequences than the context or the cache has
+    many = {"tree": dict(cu_rows=_i32([0, 1, 2, 2]), start_pos=three),
+            "weights": dict(q=torch.zeros(3, 512, **bf), out=torch.zeros(3, 512, **bf), positions=three,
+                            weights=torch.zeros(3, 2, 64, device="cuda"), scratch=torch.zeros(3, 4, 64, device="cuda"))}
+    refused(1, "tree", **many["tree"])
+    refused(3, "weights", **many["weights"])
+    refused(3, "weights", kv=kv3, **many["weights"])
+    refused(1, "commit", start_pos=three, path=_i32([[0]] * 3), path_len=three)
+    # fp32 contexts: caches of another type, or none that fits the heads
+    with pytest.raises(ValueError):
+        m32.op_cache_commit(kv, start, path, n)
+    with pytest.raises(ValueError):
+        m32.op_attention_tree(torch.zeros(2, 80, device="cuda"), cu, start, 0, kv, torch.zeros(2, 80, device="cuda"))
+    # another device
+    m._dev += 1
+    try:
+        for fn, kw in good.values():
+            with pytest.raises(ValueError):
+                fn(**kw)
+    finally:
+        m._dev -= 1
+    m.sync()
+    m32.sync()
+
+
+# --------------------------------------------------------------------------- checked build
+def test_suite_passes_on_the_bounds_check_build():
+    # every kernel checks its shared-memory layout and index invariants there
+    need_gpu()
+    if os.environ.get("LLAMA_GB300_BOUNDS_CHECK") == "1":
+        pytest.skip("this is that run")
+    from llama2_decoder_forward_gb300 import build
+    build.build_library(checked=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", os.path.abspath(__file__)],
+                       cwd=root, env=dict(os.environ, LLAMA_GB300_BOUNDS_CHECK="1"), capture_output=True, text=True,
+                       timeout=1200)
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
