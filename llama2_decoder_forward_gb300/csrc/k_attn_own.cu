@@ -1240,9 +1240,16 @@ cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launche
   const int pairs = std::max(a.B, a.n_rows >> p.tree_shift) * a.n_kv;
   int k = 1;
   while (pairs * k < 2 * a.sm_count && k < 8 && a.key_limit / (2 * k) >= 64) k *= 2;
+  p.min_share = 64;
+  // enough CTAs, but one each: a long sequence among short ones is cut in two (5 sequences of 13
+  // rows, 40 heads, 2000 keys the longest 36.8 -> 33.7 us, 8 of 8 rows 37.9 -> 33.4; shares
+  // of 64 keys and more, and four of them, up to 3 us more; twice as many pairs 43 -> 46 so)
+  if (k == 1 && pairs < 4 * a.sm_count && a.key_limit >= 1024) {
+    k = 2;
+    p.min_share = 512;
+  }
   while (k > 1 && p.rows * k * (HD + 2) * sizeof(float) > tree_partial_bytes(a.sm_count)) k /= 2;
   p.splits = k;
-  p.min_share = 64;
   p.cluster = k > 1 && pairs * k <= 3 * a.sm_count;
   p.join = k > 1 && !p.cluster;
   *launches += p.join ? 2 : 1;

@@ -686,6 +686,13 @@ def test_tree_few_rows_batches(B, rows, page):
                bias=True, check=[0, 1, 7, 12])
 
 
+@pytest.mark.parametrize("opt", OPTS)
+def test_tree_few_rows_cut_in_two(opt):
+    # enough CTAs already, with keys for two each in some sequences
+    _tree_case(40, 40, 128, "bf16", [1980, 0, 499, 505, 1020], [13, 13, 13, 8, 0], slots=2000, page=0, mask="any",
+               check=[0, 7, 8, 12], heads=[0, 17, 39], calls=2, **opt)
+
+
 @pytest.mark.parametrize("words", [1, 2, 7])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tree_mask_widths(words, dtype):
