@@ -1141,6 +1141,13 @@ SharedPlan weights_plan(int B, int n_q, int n_kv, int key_limit, int sm_count) {
   SharedPlan s = shared_plan(B, n_q, n_kv, key_limit, 0, sm_count);
   s.keep = weights_keep(s, B, n_q, n_kv, sm_count);
   if (s.keep) return s;
+  // The splits are joined by the second kernel in any case, so that more of them, of long
+  // rows, cost little and leave SMs less idle at the end: 5 CTAs per SM with 1024 keys (64
+  // sequences of up to 16384 keys, 8 K/V heads, one CTA each 412 us, two 371; 32 of up to 4096,
+  // two 64.2, three 62.5, four 65.5; 64 of up to 1500 keys, one 52.5, two 56.2).
+  const int pairs = B * n_kv, once = s.own_splits;
+  while (pairs * s.own_splits < 5 * sm_count && s.own_splits < 8 && s.keys / (s.own_splits + 1) >= 1024) ++s.own_splits;
+  if (once == 1 && s.own_splits > 1) s.min_share = 512;
   s.cluster = 0;  // the weights need a row's maximum and sum over all splits first
   s.join = 1;
   s.partials = (size_t)B * n_q * s.own_splits;

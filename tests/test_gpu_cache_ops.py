@@ -478,6 +478,12 @@ def test_weights_long_splits():
     _weights_case(16, 1, 128, "bf16", [9000, 1], page=16, slots=30000)
 
 
+def test_weights_more_splits_of_long_rows():
+    # 320 pairs and 160: two to five splits each, of some rows one
+    _weights_case(40, 40, 128, "bf16", [2999, 0, 511, 512, 1025, 2100, 64, -1 + 1024], slots=3000, heads=[0, 39])
+    _weights_case(40, 40, 128, "bf16", [5999, 300, 4100, 65], page=64, cap=30.0, bias=True, heads=[0, 39])
+
+
 def test_weights_add_up_over_calls_and_layers():
     _weights_case(4, 2, 128, "bf16", [70, 20], calls=3, layers=2, layer=1)
 
