@@ -578,7 +578,8 @@ int llama_op_attention_decode_shared(llama_ctx* ctx, const void* q, const int32_
  * that were accepted (llama_op_cache_commit). A cache held to a number of keys adds up
  * what each key weighs (llama_op_attention_decode_weights), drops the lightest
  * (llama_op_cache_evict), and appends at slots behind the kept ones with the tokens'
- * own positions. Streams, devices, graphs and overlaps as above. ---- */
+ * own positions. Streams, devices, graphs and overlaps as above; a sequence's slots from
+ * 2^31 - 65536 on count as past the cache. ---- */
 
 /* llama_op_rope_norm_append with positions of their own: row r goes to the slot that
  * cu_rows and start_pos say, and rotates by positions[r] (DEVICE int32 [n_rows]; NULL: by

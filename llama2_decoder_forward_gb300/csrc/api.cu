@@ -1504,6 +1504,9 @@ int llama_op_attention_decode_weights(llama_ctx* c, const void* q, const int32_t
   return cuda_rc(launch_decode_weights(a, plan, w, c->stream));
 }
 
+// Slots of a sequence that trees, commit and eviction reach: loops step past them by less than 65536.
+static constexpr int64_t kMostSlots = 0x7fffffff - 65535;
+
 int llama_op_attention_tree(llama_ctx* c, const void* q, int32_t n_rows, const int32_t* cu_rows,
                             const int32_t* start_pos, int32_t B, const uint32_t* mask, int32_t mask_words,
                             const int32_t* positions, int32_t layer, const llama_kv* kv,
@@ -1543,7 +1546,7 @@ int llama_op_attention_tree(llama_ctx* c, const void* q, int32_t n_rows, const i
   a.n_pages = kv->n_pages;
   a.max_pages = kv->max_pages_per_seq;
   const int64_t slots = kv->page_size ? (int64_t)kv->max_pages_per_seq * kv->page_size : kv->capacity;
-  a.key_limit = (int)std::min<int64_t>(slots, 0x7fffff00);
+  a.key_limit = (int)std::min<int64_t>(slots, kMostSlots);
   a.status = c->status;
   a.sm_count = c->sm_count;
   if (cf.dtype != LLAMA_BF16) {
@@ -1578,7 +1581,7 @@ void move_args(const llama_ctx* c, const llama_kv* kv, int32_t layer, int32_t B,
   a->max_pages = kv->max_pages_per_seq;
   a->page_table = kv->page_table;
   a->limit = (int)std::min<int64_t>(
-      kv->page_size ? (int64_t)kv->max_pages_per_seq * kv->page_size : kv->capacity, 0x7fffffff);
+      kv->page_size ? (int64_t)kv->max_pages_per_seq * kv->page_size : kv->capacity, kMostSlots);
   a->status = c->status;
   a->sm_count = c->sm_count;
 }

@@ -400,7 +400,7 @@ __device__ __forceinline__ void select_kept(const EvictArgs& a, float* held, int
     tied += sums.y;
     __syncthreads();  // `part` and `held` have been read
   }
-  for (int i = done + t; i < a.keep; i += T) kept[i] = -1;
+  for (long long i = done + t; i < a.keep; i += T) kept[i] = -1;
   for (long long i = done + t; i < a.ld; i += T) out[i] = 0.f;
 }
 
