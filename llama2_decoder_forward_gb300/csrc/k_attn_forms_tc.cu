@@ -1490,13 +1490,18 @@ FormsKernel forms_kernel(int kind) {
 }
 
 // Merges the partial results of the tree items that several CTAs share: a warp takes 2
-// rows and 4 partial results at a time, whose loads hide each other's latency. Every block makes the list of those items, so that no block is without work.
+// rows and AHEAD partial results at a time, whose loads hide each other's latency. Every
+// block makes the list of those items, so that no block is without work. Few items have many
+// parts each: four ahead, three blocks per SM (one sequence of 26 rows 16.2 us, two ahead 17.5).
+// Many have two or so, and what counts is how many rows are worked on: two ahead, four
+// blocks (32 sequences of 64 rows, 8192 keys 253.7 us, four ahead 259.0; 64 of 32 rows 101.9, 106.5).
 struct JoinItem {
   int cta, parts;  // the CTA that begins it
   TreeShared of;
 };
-constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2, JOIN_AHEAD = 4, JOIN_PARTS = 32 / JOIN_ROWS;
-__global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(FormsParams p, int ctas) {
+constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2, JOIN_PARTS = 32 / JOIN_ROWS;
+template <int AHEAD>
+__global__ void __launch_bounds__(32 * JOIN_WARPS, AHEAD == 4 ? 3 : 4) attn_tree_join_kernel(FormsParams p, int ctas) {
   grid_dep_wait();
   grid_dep_launch();
   extern __shared__ JoinItem items[];  // [ctas]
@@ -1539,10 +1544,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(Form
       const int n = min(JOIN_PARTS, parts - s0);
       float2 ml = make_float2(-INFINITY, 0.f);
       if (part_l < n) ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at(s0 + part_l) + row_l));
-      float4 x[JOIN_AHEAD][JOIN_ROWS];
+      float4 x[AHEAD][JOIN_ROWS];
       auto load = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < JOIN_AHEAD; ++i)
+        for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
           for (int k = 0; k < JOIN_ROWS; ++k)
             if (s + i < n) x[i][k] = *reinterpret_cast<const float4*>(p.part_o + (at(s0 + s + i) + k) * 128 + 4 * lane);
@@ -1566,10 +1571,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS, 3) attn_tree_join_kernel(Form
         v[k].z *= fo;
         v[k].w *= fo;
       }
-      for (int s = 0; s < n; s += JOIN_AHEAD) {
+      for (int s = 0; s < n; s += AHEAD) {
         if (s > 0) load(s);
 #pragma unroll
-        for (int i = 0; i < JOIN_AHEAD; ++i)
+        for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
           for (int k = 0; k < JOIN_ROWS; ++k) {
             const float fs = __shfl_sync(0xffffffffu, f, JOIN_PARTS * k + (s + i) % JOIN_PARTS);
@@ -1716,8 +1721,13 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
   p.box_rows = a.box_rows;
   p.key_limit = a.key_limit;
   p.rows_seq = TM / p.G;
-  // both row tiles on the same rows where a sequence's fit into one, by the mean
-  p.alternate = (long long)a.n_rows <= (long long)a.B * p.rows_seq;
+  // both row tiles on the same rows where a sequence's fit into one, by the mean; and, of few items,
+  // where they fit into two: twice the CTAs have a part then, of half the size (26 rows, 64 / 8
+  // heads, 1000, 2000 and 4000 keys 16.7, 18.3 and 19.7 us, so 16.1, 15.9 and 17.6; two
+  // sequences of 4000 24.6 and 22.4; five of 500 18.4 and 19.3)
+  const long long tiles = ((long long)a.n_rows + (long long)a.B * p.rows_seq - 1) / ((long long)a.B * p.rows_seq);
+  p.alternate = tiles <= 1 || (tiles == 2 && 9ll * a.B * a.n_kv <= a.sm_count);
+  const long long items = (p.alternate ? tiles : (tiles + 1) / 2) * a.B * a.n_kv;  // about
   p.partials = (size_t)2 * a.sm_count * (p.alternate ? TM : 2 * TM);
   p.part_o = a.partial;
   p.part_ml = a.partial + p.partials * 128;
@@ -1727,8 +1737,10 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
   const cudaError_t e = launch_k(forms_kernel<MTree>(kind), dim3(ctas), dim3(FORMS_THREADS), FORMS_SMEM, st, 0,
                                  *a.map_q, *a.map_k, *a.map_v, *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess || ctas < 2) return e;
-  return launch_k(attn_tree_join_kernel, dim3(4 * ctas), dim3(32 * JOIN_WARPS), ctas * sizeof(JoinItem),
-                  st, 0, p, ctas);
+  const dim3 block(32 * JOIN_WARPS);
+  const size_t list = ctas * sizeof(JoinItem);
+  return 2 * items >= ctas ? launch_k(attn_tree_join_kernel<2>, dim3(8 * ctas), block, list, st, 0, p, ctas)
+                           : launch_k(attn_tree_join_kernel<4>, dim3(4 * ctas), block, list, st, 0, p, ctas);
 }
 
 }  // namespace llgb
