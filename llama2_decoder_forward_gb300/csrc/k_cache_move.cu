@@ -40,9 +40,11 @@ __device__ __forceinline__ int move_row(const CacheMoveArgs& a, int b, int slot)
 // and pages are the same for all layers and heads, K and V, so a block looks them up once
 // for as many heads as fill its threads and walks its layers: while it waits for
 // one layer's rows to store them, the next one's are on their way. A path is mostly one
-// chunk.
-constexpr int COMMIT_UNITS = 4;
-__global__ void __launch_bounds__(MOVE_THREADS, 3) cache_commit_kernel(CacheMoveArgs a, int heads, int rows_chunk,
+// chunk. Bound by the latency of look-ups and rows, so by how many blocks are resident: 64
+// sequences, 32 layers of 32 E4M3 heads (66 MB read and written), 8 blocks per SM with 2 units a
+// thread 28.1 us, 4 with 4 32.1, 3 with 4 35.7, 8 with 1 38.
+constexpr int COMMIT_UNITS = 2;
+__global__ void __launch_bounds__(MOVE_THREADS, 8) cache_commit_kernel(CacheMoveArgs a, int heads, int rows_chunk,
                                                                        int run) {
   grid_dep_wait();
   grid_dep_launch();
@@ -430,10 +432,10 @@ cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t st) {
   const int upr = a.row_bytes / 16, room = MOVE_THREADS * COMMIT_UNITS / (2 * upr);  // rows of one head's K and V
   const int heads = std::max(1, std::min(room / a.list_ld, a.n_kv)), rows = std::min(a.list_ld, room / heads);
   const int groups = (a.n_kv + heads - 1) / heads;
-  // runs of layers that give every SM three times its 3 blocks (once: 39.3 instead of 35.6 us
-  // for 64 sequences, 32 layers of 32 E4M3 heads; six times: 37.5)
+  // runs of layers that give every SM twice its 8 blocks (once 30.1 instead of 28.1 us in the
+  // same case; four times 28.7, but 11.8 instead of 10.0 with 8 heads)
   const long long pairs = (long long)groups * a.B;
-  const int runs = (int)std::min<long long>(a.layers, (9 * a.sm_count + pairs - 1) / pairs);
+  const int runs = (int)std::min<long long>(a.layers, (16 * a.sm_count + pairs - 1) / pairs);
   const int run = (a.layers + runs - 1) / runs;
   return launch_k(cache_commit_kernel, dim3(groups, a.B, (a.layers + run - 1) / run), dim3(MOVE_THREADS),
                   rows * sizeof(int2), st, 0, a, heads, rows, run);
