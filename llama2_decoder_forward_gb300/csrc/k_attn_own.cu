@@ -1156,11 +1156,12 @@ SharedPlan weights_plan(int B, int n_q, int n_kv, int key_limit, int sm_count) {
   return s;
 }
 
-// 8 CTAs per SM share the keys of all (sequence, K/V head) pairs, a pass of the threads each at least.
+// 16 CTAs per SM share the keys of all (sequence, K/V head) pairs, a pass of the threads each at
+// least (64 sequences of up to 16384 keys 367 us, eight 371; short ones the same).
 template <bool NAT>
 static cudaError_t launch_weights(const OwnParams& p, const SharedArgs& a, cudaStream_t st) {
   const int per = WEIGH_THREADS * WEIGH_KEYS;
-  const int chunks = std::max(1, std::min((a.key_limit + per - 1) / per, 8 * a.sm_count / (a.B * a.n_kv)));
+  const int chunks = std::max(1, std::min((a.key_limit + per - 1) / per, 16 * a.sm_count / (a.B * a.n_kv)));
   return launch_k(attn_weights_kernel<NAT>, dim3(chunks + !NAT, a.n_kv, a.B), dim3(WEIGH_THREADS),
                   p.G * sizeof(float2), st, 0, p);
 }
@@ -1206,13 +1207,23 @@ cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cu
 // and 73 (the softmax of the other kernel works on all 128 rows); three 91 and 60. Where 8
 // CTAs for each (sequence, K/V head) are few and the context may be long, the other
 // kernel's equal shares count: one row, 8 K/V heads, 30000 keys 34 (57 CTAs each) and 30 us.
+// Several blocks of few short sequences: all of their CTAs are resident, and the other
+// kernel takes 10 us and more whatever they hold (one sequence, 64 / 8 heads, 750 and 1500
+// keys: 4 rows 9.9 and 11.0 us, the other 13.0 and 14.7; 26 rows 14.1 and 20.2, the other 15.4 and
+// 16.2; 4 sequences of 8 rows, 300 and 750 keys 12.1 and 17.8, the other 13.7 and 14.4).
+static long long tree_pairs(const TreeArgs& a) {  // CTAs without splits, by the mean rows
+  const int G = a.n_q / a.n_kv, rows = (a.n_rows + a.B - 1) / a.B;
+  int shift = 0;
+  while (2 * G << shift <= 8) ++shift;
+  return (long long)a.B * a.n_kv * ((rows + (1 << shift) - 1) >> shift);
+}
 bool tree_own_applies(const TreeArgs& a) {
   const int G = a.n_q / a.n_kv;
   if (a.head_dim != HD || G > 8 || (long long)a.B + a.n_rows > 65535) return false;  // the launch's grid
-  const long long pairs = (long long)a.B * a.n_kv, rows = (a.n_rows + a.B - 1) / a.B;  // the mean
-  const long long blocks = (rows + 8 / G - 1) / (8 / G);
-  if (8 * pairs < 2 * a.sm_count && a.key_limit > 8192) return false;
-  return blocks == 1 || (blocks == 2 && (a.sc.cap > 0.f || a.sc.slopes || a.key_limit <= 2048));
+  const long long heads = (long long)a.B * a.n_kv, pairs = tree_pairs(a);
+  if (8 * heads < 2 * a.sm_count && a.key_limit > 8192) return false;
+  if (pairs == heads || (pairs == 2 * heads && (a.sc.cap > 0.f || a.sc.slopes || a.key_limit <= 2048))) return true;
+  return pairs <= 3 * a.sm_count && pairs * a.key_limit <= 1100ll * a.sm_count;
 }
 
 cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launches) {
@@ -1243,12 +1254,14 @@ cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launche
   p.n_seq = a.B;
   while (2 * p.G << p.tree_shift <= 8) ++p.tree_shift;
   const int blocks = (a.n_rows >> p.tree_shift) + a.B;
-  // splits as in shared_plan; clusters where all are resident at once (4 sequences of 2 rows,
-  // 32 / 8 heads, up to 1000 keys 9.7 us, with the joining kernel 11.0; 8 sequences of one
-  // row, 64 / 8 heads, up to 4096 keys, 512 CTAs 24.5 and 21.9)
-  const int pairs = std::max(a.B, a.n_rows >> p.tree_shift) * a.n_kv;
+  // As many splits as are resident at once, three CTAs per SM, in clusters; of the odd sizes
+  // that of 3 pays (128 pairs of up to 1500 keys 16.0 us, clusters of 2 19.7, more than are resident
+  // with a joining kernel 23.8; 64 pairs of 750 in clusters of 4 11.1, of 7 18.3). Long sequences
+  // take the joining kernel (64 pairs of up to 6700 keys, 4 splits 44.7, 8 with it 40.0).
+  const int pairs = (int)std::min(tree_pairs(a), 65535ll);
   int k = 1;
-  while (pairs * k < 2 * a.sm_count && k < 8 && a.key_limit / (2 * k) >= 64) k *= 2;
+  for (const int x : {8, 4, 3, 2})
+    if (k == 1 && pairs * x <= (x == 8 && a.key_limit > 4096 ? 4 : 3) * a.sm_count && a.key_limit / x >= 64) k = x;
   p.min_share = 64;
   // enough CTAs, but one each: a long sequence among short ones is cut in two (5 sequences of 13
   // rows, 40 heads, 2000 keys the longest 36.8 -> 33.7 us, 8 of 8 rows 37.9 -> 33.4; shares

@@ -692,6 +692,16 @@ def test_tree_few_rows_batches(B, rows, page):
                bias=True, check=[0, 1, 7, 12])
 
 
+@pytest.mark.parametrize("nq,nkv,starts,rows", [
+    (64, 8, [700], [16]), (64, 8, [30, 0, 200, 61], [8, 3, 10, 9]), (16, 16, [800], [26]), (32, 8, [70, 150], [26, 31]),
+    (8, 1, [500], [40]), (10, 5, [333, 2, 400], [30, 1, 12]), (64, 8, [5000, 3, 4100, 64, 900, 1, 0, 2500], [1] * 8)])
+@pytest.mark.parametrize("opt", [OPTS[0], OPTS[3]])
+def test_tree_several_blocks(nq, nkv, starts, rows, opt):
+    # blocks of 8 (row, head) pairs enough to be resident at once, in clusters of up to 8 CTAs
+    _tree_case(nq, nkv, 128, "bf16", starts, rows, mask="any", check=[0, 1, 7, 8, 15, 25, 39], heads=[0, nq // 2 - 1, nq - 1],
+               lead=1, tail=1, **opt)
+
+
 @pytest.mark.parametrize("opt", OPTS)
 def test_tree_few_rows_cut_in_two(opt):
     # enough CTAs already, with keys for two each in some sequences
