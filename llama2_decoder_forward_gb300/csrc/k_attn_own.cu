@@ -1210,7 +1210,9 @@ cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cu
 // Several blocks of few short sequences: all of their CTAs are resident, and the other
 // kernel takes 10 us and more whatever they hold (one sequence, 64 / 8 heads, 750 and 1500
 // keys: 4 rows 9.9 and 11.0 us, the other 13.0 and 14.7; 26 rows 14.1 and 20.2, the other 15.4 and
-// 16.2; 4 sequences of 8 rows, 300 and 750 keys 12.1 and 17.8, the other 13.7 and 14.4).
+// 16.2; 4 sequences of 8 rows, 300 and 750 keys 12.1 and 17.8, the other 13.7 and 14.4). And where
+// the other kernel has several items per SM, of a tile or so (6 sequences of 17 rows, 32 heads,
+// 20 and 120 keys 11.5 and 13.8, the other 22.3 and 15.9; 40 of 30 rows, 8 heads, 130 keys 22.6, 20.5).
 static long long tree_pairs(const TreeArgs& a) {  // CTAs without splits, by the mean rows
   const int G = a.n_q / a.n_kv, rows = (a.n_rows + a.B - 1) / a.B;
   int shift = 0;
@@ -1220,10 +1222,12 @@ static long long tree_pairs(const TreeArgs& a) {  // CTAs without splits, by the
 bool tree_own_applies(const TreeArgs& a) {
   const int G = a.n_q / a.n_kv;
   if (a.head_dim != HD || G > 8 || (long long)a.B + a.n_rows > 65535) return false;  // the launch's grid
-  const long long heads = (long long)a.B * a.n_kv, pairs = tree_pairs(a);
+  const long long heads = (long long)a.B * a.n_kv, pairs = tree_pairs(a), rows = (a.n_rows + a.B - 1) / a.B;
   if (8 * heads < 2 * a.sm_count && a.key_limit > 8192) return false;
   if (pairs == heads || (pairs == 2 * heads && (a.sc.cap > 0.f || a.sc.slopes || a.key_limit <= 2048))) return true;
-  return pairs <= 3 * a.sm_count && pairs * a.key_limit <= 1100ll * a.sm_count;
+  const long long items = heads * ((rows * G + 127) / 128);  // about, the other kernel's
+  return (pairs <= 3 * a.sm_count && pairs * a.key_limit <= 1100ll * a.sm_count) ||
+         (items > a.sm_count && pairs <= 4 * items && pairs * a.key_limit <= 450ll * a.sm_count);
 }
 
 cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launches) {

@@ -454,6 +454,9 @@ cudaError_t launch_evict(const EvictArgs& e, const CacheMoveArgs& a, cudaStream_
   // 1024 heads of 4096 slots, 1500 kept: 272 us with four CTAs per SM and 5 units a thread,
   // 299 with three and 8, 319 with four and 4; select and move as two kernels 290
   if (items > 2 * a.sm_count) return run_evict<256, 5>(e, a, items, 1, st);
+  // more heads than SMs: two CTAs of half the size each (160 heads of 1088 slots 44.7 us, one of
+  // 512 threads 51.9; but of 200 slots 10.1 and 9.4)
+  if (items > a.sm_count && e.limit >= 512) return run_evict<256, 5>(e, a, items, 2, st);
   // up to two CTAs per SM, which are resident at once (48 heads of 62 slots 7.7 us, twice as many
   // CTAs 13.6; 144 of 4000, 1500 kept, 56 and 70)
   int ctas = 1;

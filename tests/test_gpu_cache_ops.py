@@ -248,7 +248,8 @@ def test_evict_many_heads():
 
 @pytest.mark.parametrize("layers,nkv,page,n,keep,dtype,d", [
     (8, 32, 16, 4000, 1500, "bf16", 128), (32, 32, 0, 2000, 1900, "bf16", 128), (1, 1, 16, 20000, 15000, "bf16", 128),
-    (4, 8, 64, 3000, 2000, "f32", 256), (2, 3, 0, 6000, 5999, "f32", 40)])
+    (4, 8, 64, 3000, 2000, "f32", 256), (2, 3, 0, 6000, 5999, "f32", 40),
+    (5, 32, 16, 3000, 1000, "bf16", 128), (40, 5, 0, 700, 300, "f32", 8), (9, 30, 64, 1500, 1490, "f32", 40)])
 def test_evict_long_lists(layers, nkv, page, n, keep, dtype, d):
     # chunks follow one another in every CTA, and none may pass another one's rows by
     m, shape = _model(nkv, nkv, d, dtype, max_batch=1, max_seq=8, n_layers=layers)
@@ -694,7 +695,7 @@ def test_tree_few_rows_batches(B, rows, page):
 
 @pytest.mark.parametrize("nq,nkv,starts,rows", [
     (64, 8, [700], [16]), (64, 8, [30, 0, 200, 61], [8, 3, 10, 9]), (16, 16, [800], [26]), (32, 8, [70, 150], [26, 31]),
-    (8, 1, [500], [40]), (10, 5, [333, 2, 400], [30, 1, 12]), (64, 8, [5000, 3, 4100, 64, 900, 1, 0, 2500], [1] * 8)])
+    (32, 32, [3, 0, 20, 7, 11, 2], [17, 20, 3, 24, 17, 17]), (8, 1, [500], [40]), (10, 5, [333, 2, 400], [30, 1, 12]), (64, 8, [5000, 3, 4100, 64, 900, 1, 0, 2500], [1] * 8)])
 @pytest.mark.parametrize("opt", [OPTS[0], OPTS[3]])
 def test_tree_several_blocks(nq, nkv, starts, rows, opt):
     # blocks of 8 (row, head) pairs enough to be resident at once, in clusters of up to 8 CTAs
