@@ -91,7 +91,7 @@ struct OwnParams {
   // small trees: a sequence's rows in blocks of 2^tree_shift
   const int32_t *cu_rows, *start_pos, *row_pos;
   TreeMask tree;
-  int n_rows, n_seq, tree_shift;
+  int n_rows, n_seq, tree_shift, slices, per;  // a group's heads in slices of `per`
 };
 
 // What a launch works on: a decode row per sequence; the same with its scores kept; the
@@ -99,11 +99,12 @@ struct OwnParams {
 enum { ODecode, OWeigh, OTree };
 
 // The rows of a CTA: the query heads of one K/V head, of one decode row or of several
-// tree rows (row r: head r % G of tree row i0 + r / G).
+// tree rows (row r: head r % per of the slice, of tree row i0 + r / per).
 struct OwnRows {
   int b, g, count;             // sequence, K/V head, rows
   int pos;                     // decode: the row's position
   int lo, i0, start, there;    // trees: the sequence's first row, the block's, cached keys, tree rows in the cache
+  int head;                    // and the first query head
 };
 // Where the scores are kept: row r's of key k at at[r ld + k - first].
 struct OwnKeep {
@@ -115,12 +116,12 @@ struct OwnKeep {
 template <int MODE>
 __device__ __forceinline__ size_t row_head(const OwnParams& p, const OwnRows& R, int r) {
   if (MODE != OTree) return (size_t)R.b * p.n_q + (size_t)R.g * p.G + r;
-  const int i = r / p.G;
-  return (size_t)(R.lo + R.i0 + i) * p.n_q + (size_t)R.g * p.G + (r - i * p.G);
+  const int i = r / p.per;
+  return (size_t)(R.lo + R.i0 + i) * p.n_q + R.head + (r - i * p.per);
 }
 template <int MODE>
 __device__ __forceinline__ float row_slope(const OwnParams& p, const OwnRows& R, int r) {
-  return r < R.count ? __ldcg(p.slopes + R.g * p.G + (MODE == OTree ? r % p.G : r)) * 1.4426950408889634f : 0.f;
+  return r < R.count ? __ldcg(p.slopes + (MODE == OTree ? R.head + r % p.per : R.g * p.G + r)) * 1.4426950408889634f : 0.f;
 }
 // Trees: the position of row r, of key k (n keys in all), and the visible ones of 32 keys from k on.
 __device__ __forceinline__ int tree_pos(const OwnParams& p, const OwnRows& R, int x) {
@@ -130,7 +131,7 @@ __device__ __forceinline__ int tree_key_pos(const OwnParams& p, const OwnRows& R
   return k < R.start || k - R.start >= R.there ? k : tree_pos(p, R, k - R.start);
 }
 __device__ __forceinline__ uint32_t row_sees(const OwnParams& p, const OwnRows& R, int r, int k) {
-  const int i = R.i0 + r / p.G;
+  const int i = R.i0 + r / p.per;
   return r < R.count ? tree_bits(p.tree, (size_t)R.lo + i, i, R.there, k - R.start) : 0u;
 }
 
@@ -216,7 +217,7 @@ __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, 
   int pos[2] = {0, 0};  // trees: the two rows' positions, for the bias
   if (MODE == OTree && p.slopes) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) pos[j] = hc + j < G ? tree_pos(p, R, R.i0 + (hc + j) / p.G) : 0;
+    for (int j = 0; j < 2; ++j) pos[j] = hc + j < G ? tree_pos(p, R, R.i0 + (hc + j) / p.per) : 0;
   }
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[8][4];
 #pragma unroll
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
   uint64_t* empty = full + STAGES;
   volatile uint32_t* stop = reinterpret_cast<volatile uint32_t*>(empty + STAGES);
-  const int split = blockIdx.x, g = blockIdx.y;
+  const int split = blockIdx.x, g = MODE == OTree ? blockIdx.y / p.slices : blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   OwnRows R{};
   // With a prefix kernel before this one, what this one reads is complete: that
@@ -670,7 +671,9 @@ __global__ void __launch_bounds__(OWN_THREADS, KEYS ? 3 : 2)
     if (!tree_block(p, blockIdx.z, lane, b, R.i0, R.lo, n)) return;  // a cluster's CTAs all do
     pos = tree_keys(p, b, R) - 1;  // the last key
     if ((p.start_pos[b] < 0 || R.there < n) && split == 0 && threadIdx.x == 0) flag(p.status, LLAMA_FLAG_POS_RANGE);
-    R.count = min(1 << p.tree_shift, n - R.i0) * p.G;
+    const int h = (blockIdx.y - g * p.slices) * p.per;
+    R.head = g * p.G + h;
+    R.count = min(1 << p.tree_shift, n - R.i0) * min(p.per, p.G - h);
   } else if (p.sorted) {
     // the blockIdx.z-th longest sequence, so that the longest start first: one key
     // of 32 bits per sequence, its length and (ties) its number
@@ -1213,15 +1216,22 @@ cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cu
 // 16.2; 4 sequences of 8 rows, 300 and 750 keys 12.1 and 17.8, the other 13.7 and 14.4). And where
 // the other kernel has several items per SM, of a tile or so (6 sequences of 17 rows, 32 heads,
 // 20 and 120 keys 11.5 and 13.8, the other 22.3 and 15.9; 40 of 30 rows, 8 heads, 130 keys 22.6, 20.5).
+// Groups of more than 8 heads: in slices, each with a pass over the keys (one sequence of 4 rows, 16 / 1
+// heads, 300 and 1100 keys 8.6 and 8.8 us, the other kernel 11.5 and 14.0).
+static void tree_slices(int G, int* slices, int* per) {
+  *slices = (G + 7) / 8;
+  *per = (G + *slices - 1) / *slices;
+}
 static long long tree_pairs(const TreeArgs& a) {  // CTAs without splits, by the mean rows
-  const int G = a.n_q / a.n_kv, rows = (a.n_rows + a.B - 1) / a.B;
-  int shift = 0;
-  while (2 * G << shift <= 8) ++shift;
-  return (long long)a.B * a.n_kv * ((rows + (1 << shift) - 1) >> shift);
+  const int rows = (a.n_rows + a.B - 1) / a.B;
+  int shift = 0, slices, per;
+  tree_slices(a.n_q / a.n_kv, &slices, &per);
+  while (2 * per << shift <= 8) ++shift;
+  return (long long)a.B * a.n_kv * slices * ((rows + (1 << shift) - 1) >> shift);
 }
 bool tree_own_applies(const TreeArgs& a) {
   const int G = a.n_q / a.n_kv;
-  if (a.head_dim != HD || G > 8 || (long long)a.B + a.n_rows > 65535) return false;  // the launch's grid
+  if (a.head_dim != HD || (long long)a.B + a.n_rows > 65535 || a.n_kv > 32767) return false;  // the launch's grid
   const long long heads = (long long)a.B * a.n_kv, pairs = tree_pairs(a), rows = (a.n_rows + a.B - 1) / a.B;
   if (8 * heads < 2 * a.sm_count && a.key_limit > 8192) return false;
   if (pairs == heads || (pairs == 2 * heads && (a.sc.cap > 0.f || a.sc.slopes || a.key_limit <= 2048))) return true;
@@ -1256,7 +1266,8 @@ cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launche
   p.tree = TreeMask{a.mask, a.mask_words};
   p.n_rows = a.n_rows;
   p.n_seq = a.B;
-  while (2 * p.G << p.tree_shift <= 8) ++p.tree_shift;
+  tree_slices(p.G, &p.slices, &p.per);
+  while (2 * p.per << p.tree_shift <= 8) ++p.tree_shift;
   const int blocks = (a.n_rows >> p.tree_shift) + a.B;
   // As many splits as are resident at once, three CTAs per SM, in clusters; of the odd sizes
   // that of 3 pays (128 pairs of up to 1500 keys 16.0 us, clusters of 2 19.7, more than are resident
@@ -1284,7 +1295,7 @@ cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launche
   p.own_ml = a.partial + p.own_room * HD;
   p.part_o = p.own_o;  // no prefix: no parts of it
   p.part_ml = p.own_ml;
-  const cudaError_t e = launch_kc(attn_own_kernel<true, OTree>, dim3(k, a.n_kv, blocks), dim3(OWN_THREADS), OWN_SMEM,
+  const cudaError_t e = launch_kc(attn_own_kernel<true, OTree>, dim3(k, a.n_kv * p.slices, blocks), dim3(OWN_THREADS), OWN_SMEM,
                                   st, dim3(p.cluster ? k : 0, 1, 1), *a.map_k, *a.map_v, *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess || !p.join) return e;
   return launch_k(attn_own_join_kernel<OTree>, dim3((unsigned)((p.rows + 3) / 4)), dim3(128), 0, st, 0, p,

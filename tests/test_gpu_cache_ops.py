@@ -695,7 +695,8 @@ def test_tree_few_rows_batches(B, rows, page):
 
 @pytest.mark.parametrize("nq,nkv,starts,rows", [
     (64, 8, [700], [16]), (64, 8, [30, 0, 200, 61], [8, 3, 10, 9]), (16, 16, [800], [26]), (32, 8, [70, 150], [26, 31]),
-    (32, 32, [3, 0, 20, 7, 11, 2], [17, 20, 3, 24, 17, 17]), (8, 1, [500], [40]), (10, 5, [333, 2, 400], [30, 1, 12]), (64, 8, [5000, 3, 4100, 64, 900, 1, 0, 2500], [1] * 8)])
+    (16, 1, [700, 20, 0], [5, 9, 1]), (12, 1, [60, 0, 333], [1, 2, 1]), (18, 2, [100, 0, 33, 90], [2, 1, 3, 0]),
+    (32, 2, [260, 1500], [1, 1]), (16, 1, [90] * 140, [1] * 140), (32, 32, [3, 0, 20, 7, 11, 2], [17, 20, 3, 24, 17, 17]), (8, 1, [500], [40]), (10, 5, [333, 2, 400], [30, 1, 12]), (64, 8, [5000, 3, 4100, 64, 900, 1, 0, 2500], [1] * 8)])
 @pytest.mark.parametrize("opt", [OPTS[0], OPTS[3]])
 def test_tree_several_blocks(nq, nkv, starts, rows, opt):
     # blocks of 8 (row, head) pairs enough to be resident at once, in clusters of up to 8 CTAs
