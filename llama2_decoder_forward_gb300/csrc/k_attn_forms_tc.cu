@@ -29,7 +29,8 @@
 //   trees                      : as a prefix, row blocks of (tree row, head of the group).
 // so K and V are loaded once for both. Every mask here is "keys below a row's
 // limit": max(position + 1, prefix) for documents, the sequence's keys for the
-// prefix; trees add their rows' own bits in the key tiles that hold drafted rows. O is rescaled lazily, when a row's maximum grows by more than 2^8.
+// prefix; trees add their rows' own bits in the key tiles that hold drafted rows. O is
+// rescaled lazily, when a row's maximum grows by more than 2^8.
 //
 // Documents run as one CTA per SM that takes its share of the work items: the
 // producers load the next item's Q, K and V while the softmax and the store of

@@ -194,7 +194,8 @@ __device__ __forceinline__ void clean_v(uint8_t* v, int lead, int valid, int lan
   __syncwarp();
 }
 
-// Up to 8 rows: keys on the MMA rows. Lane l tracks rows 2(l%4) and 2(l%4) + 1. Leaves (max, sum, O) of this warp in shared memory.
+// Up to 8 rows: keys on the MMA rows. Lane l tracks rows 2(l%4) and 2(l%4) + 1. Leaves
+// (max, sum, O) of this warp in shared memory.
 template <int MODE>
 __device__ __forceinline__ void consume_keys(const OwnParams& p, uint8_t* smem, uint64_t* full,
                                              uint64_t* empty, volatile uint32_t* stop, const OwnRows& R, const OwnKeep& keep,
@@ -1295,8 +1296,9 @@ cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launche
   p.own_ml = a.partial + p.own_room * HD;
   p.part_o = p.own_o;  // no prefix: no parts of it
   p.part_ml = p.own_ml;
-  const cudaError_t e = launch_kc(attn_own_kernel<true, OTree>, dim3(k, a.n_kv * p.slices, blocks), dim3(OWN_THREADS), OWN_SMEM,
-                                  st, dim3(p.cluster ? k : 0, 1, 1), *a.map_k, *a.map_v, *a.map_k16, *a.map_v16, p);
+  const cudaError_t e = launch_kc(attn_own_kernel<true, OTree>, dim3(k, a.n_kv * p.slices, blocks),
+                                  dim3(OWN_THREADS), OWN_SMEM, st, dim3(p.cluster ? k : 0, 1, 1), *a.map_k,
+                                  *a.map_v, *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess || !p.join) return e;
   return launch_k(attn_own_join_kernel<OTree>, dim3((unsigned)((p.rows + 3) / 4)), dim3(128), 0, st, 0, p,
                   (int)p.rows);

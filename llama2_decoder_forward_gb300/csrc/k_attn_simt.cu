@@ -1,6 +1,8 @@
 // Attention with capped or biased scores on the CUDA cores, for fp32 models
-// with any head_dim up to 256: packed documents (two-way prefix, causal rest)
-// and decode over a cache with a shared prefix.
+// with any head_dim up to 256: packed documents (two-way prefix, causal rest),
+// decode over a cache with a shared prefix (if asked, its scores and each row's maximum
+// and sum are kept for the key weights), and drafted trees, whose rows are taken as a
+// document's and whose keys come from the cache.
 //
 //   x = scale q.k;  s = (cap tanh(x / cap) or x) - slope |i - j|;  softmax;  sum p v
 //
