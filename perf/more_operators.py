@@ -197,7 +197,7 @@ def work(c):
     if c["op"] == "tree":
         keys = sum(a + b for a, b in zip(lens, rows))
         seen = sum(n * len(t) + sum(bin(x).count("1") for x in _ancestors(t)[0]) for n, t in zip(lens, _trees(c)))
-        words = 0 if c["chain"] else -(-c["rows"] // 32)
+        words = 0 if c["chain"] else -(-max(rows) // 32)
         return {"bytes": 2 * keys * nkv * d * es + sum(rows) * (2 * c["n_q"] * d * es + 4 * words),
                 "flops": 4 * d * c["n_q"] * seen}
     if c["op"] == "commit":  # rows that are where they belong do not move
@@ -267,7 +267,7 @@ def prepare(c, seed):
         cu = [0]
         for x in rows:
             cu.append(cu[-1] + x)
-        words = -(-c["rows"] // 32)
+        words = -(-max(rows) // 32)
         bits, at = [], []
         for start, t in zip(lens, _trees(c)):
             b, depth = _ancestors(t)
