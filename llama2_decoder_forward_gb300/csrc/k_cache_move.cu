@@ -413,15 +413,17 @@ template <int T, int U>
 __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs e, CacheMoveArgs a, int ctas) {
   grid_dep_wait();
   grid_dep_launch();
-  extern __shared__ float held[];  // [min(SPAN, most slots)]; then the moves
+  extern __shared__ __align__(16) float held[];  // [min(SPAN, most slots)]; then the moves, int2 [3][rows of a chunk]
   const int item = blockIdx.x / ctas, rank = blockIdx.x - item * ctas, b = item / a.n_kv % a.B;
+  const int cols = a.row_bytes / 8 / ctas;
+  if (!bc_smem(held, max(min(SPAN, e.limit) * 4, 3 * (T / cols * U) * 8), 16, threadIdx.x == 0 ? a.status : nullptr))
+    return;  // a cluster's CTAs all do
   if (rank == 0) select_kept<T>(e, held, item);
   if (ctas > 1)
     cluster_sync_all();  // the list is written
   else
     __syncthreads();     // and `held` free
   if (min(max(a.lens[b], 0), a.limit) <= a.list_ld) return;  // nothing was dropped: nothing moves
-  const int cols = a.row_bytes / 8 / ctas;
   move_kept<T, U>(a, reinterpret_cast<int2*>(held), a.kept + (size_t)item * a.list_ld, item / a.n_kv / a.B, b,
                   item % a.n_kv, rank * cols, cols);
 }
