@@ -1318,7 +1318,7 @@ int llama_op_rope_norm_append_at(llama_ctx* c, const void* qkv, int32_t qkv_dtyp
   a.n_seq = B;
   a.cu_rows = cu_rows;
   a.start_pos = start_pos;
-  a.positions = positions;
+  a.positions = a.rotary > 0 ? positions : nullptr;  // read by the rotation alone
   a.q_gain = q_gain;
   a.k_gain = k_gain;
   a.eps = norm_eps;
