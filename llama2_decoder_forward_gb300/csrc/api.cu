@@ -142,11 +142,12 @@ Layout make_layout(const llama_config* c, int sm_count) {
   L.apart = take(std::max<size_t>(L.apart_bytes, 16));
   // fused RMSNorm: per-(128-feature tile, row) sums of squares of the residual stream
   L.ssq = take((H + 127) / 128 * (size_t)R * 4);
-  // partial results of decode attention over a shared prefix and of trees (bf16); rows' maxima and sums
-  // of decode attention with key weights (fp32)
+  // partial results of decode attention over a shared prefix, of key weights and of trees (bf16); rows'
+  // maxima and sums of decode attention with key weights (fp32)
   L.spart = take(c->dtype == LLAMA_BF16
-                     ? std::max(shared_partial_bytes(c->max_batch, (int)nq, (int)nkv, c->max_seq, sm_count),
-                                tree_partial_bytes(sm_count))
+                     ? std::max({shared_partial_bytes(c->max_batch, (int)nq, (int)nkv, c->max_seq, sm_count),
+                                 weights_partial_bytes(c->max_batch, (int)nq, (int)nkv, c->max_seq, sm_count),
+                                 tree_partial_bytes(sm_count)})
                      : (size_t)c->max_batch * nq * 8);
   L.total = off;
   return L;
@@ -1459,7 +1460,7 @@ int llama_op_attention_decode_shared(llama_ctx* c, const void* q, const int32_t*
   }
   const SharedPlan plan =
       shared_plan(B, cf.n_q_heads, cf.n_kv_heads, a.key_limit, a.shared_len, c->sm_count);
-  if (plan.partials * (128 + 2) * sizeof(float) + 16 >
+  if (plan.partials * kPartial + 16 >
       shared_partial_bytes(cf.max_batch, cf.n_q_heads, cf.n_kv_heads, cf.max_seq, c->sm_count))
     return LLAMA_ERR_WORKSPACE;
   TRY(decode_maps(c, kv, B, plan.rows_seq, &a));
@@ -1494,8 +1495,8 @@ int llama_op_attention_decode_weights(llama_ctx* c, const void* q, const int32_t
     return cuda_rc(launch_add_weights_f32(a, w, c->stream));
   }
   const SharedPlan plan = weights_plan(B, cf.n_q_heads, cf.n_kv_heads, a.key_limit, c->sm_count);
-  if (plan.partials * (128 + 2) * sizeof(float) + 16 >
-      shared_partial_bytes(cf.max_batch, cf.n_q_heads, cf.n_kv_heads, cf.max_seq, c->sm_count))
+  if (plan.partials * kPartial + 16 >
+      weights_partial_bytes(cf.max_batch, cf.n_q_heads, cf.n_kv_heads, cf.max_seq, c->sm_count))
     return LLAMA_ERR_WORKSPACE;
   TRY(decode_maps(c, kv, B, plan.rows_seq, &a));
   a.partial = c->at<float>(c->L.spart);
@@ -1557,7 +1558,9 @@ int llama_op_attention_tree(llama_ctx* c, const void* q, int32_t n_rows, const i
   TRY(decode_maps(c, kv, n_rows, 128 / (cf.n_q_heads / cf.n_kv_heads), &a));
   a.partial = c->at<float>(c->L.spart);
   Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
-  if (tree_own_applies(a)) return cuda_rc(launch_tree_own(a, c->stream, &c->launches));
+  const TreePlan plan = tree_plan(n_rows, B, a.n_q, a.n_kv, a.key_limit, a.sc.cap > 0.f || a.sc.slopes, a.sm_count,
+                                  tree_partial_bytes(a.sm_count));
+  if (plan.own) return cuda_rc(launch_tree_own(a, plan, c->stream, &c->launches));
   c->launches += 2;
   return cuda_rc(launch_tree_tc(a, c->stream));
 }

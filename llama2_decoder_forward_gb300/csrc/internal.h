@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "../../include/llama_gb300.h"
+#include "attn_plan.h"
 
 namespace llgb {
 
@@ -316,25 +317,8 @@ struct TreeArgs {
 };
 size_t tree_partial_bytes(int sm_count);
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st);    // k_attn_forms_tc.cu
-bool tree_own_applies(const TreeArgs& a);  // trees of few rows: k_attn_own.cu
-cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launches);
+cudaError_t launch_tree_own(const TreeArgs& a, const TreePlan& t, cudaStream_t st, int64_t* launches);  // k_attn_own.cu
 cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t st);  // k_attn_simt.cu
-// How a decode batch over a shared prefix is cut: the prefix kernel's grid
-// (prefix_splits, row_blocks, n_kv) and the own keys' splits.
-struct SharedPlan {
-  int rows_seq;         // sequences of a 128-row tile
-  int alternate;        // one row tile: the two halves of a CTA share its keys
-  int row_blocks, tiles_per_split, prefix_splits;
-  int prefix_parts;     // partials per row of the prefix kernel (0: no prefix)
-  int base, keys;       // own keys start in the tile at base, and are `keys` at most
-  int own_splits, min_share;  // key splits, and the keys that a split has at least
-  int cluster;          // the own splits of a row form a thread-block cluster
-  int join;             // own splits leave partials, which a joining kernel merges
-  size_t partials;      // partial rows in all
-  int keep;             // key weights: scores of a row that a CTA keeps (0: they go to the joining kernel)
-};
-SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, int sm_count);
-size_t shared_partial_bytes(int max_batch, int n_q, int n_kv, int max_seq, int sm_count);
 // bf16, head_dim 128 on tcgen05 (k_attn_forms_tc.cu)
 cudaError_t attn_forms_prepare();
 cudaError_t launch_docs_tc(const DocsArgs& a, cudaStream_t st);
@@ -350,7 +334,6 @@ struct WeightsArgs {
   int64_t ld;
   float* stats;          // fp32 models: [B n_q][2], maximum and sum of a row
 };
-SharedPlan weights_plan(int B, int n_q, int n_kv, int key_limit, int sm_count);
 cudaError_t launch_decode_weights(const SharedArgs& a, const SharedPlan& s, const WeightsArgs& w, cudaStream_t st);
 cudaError_t launch_add_weights_f32(const SharedArgs& a, const WeightsArgs& w, cudaStream_t st);
 // fp32 on the CUDA cores, any head_dim (k_attn_simt.cu)

@@ -61,7 +61,8 @@ constexpr int TREE_COUNTED = 128;               // sequences whose blocks of tre
 constexpr uint32_t OFF_SORT = STAGES * STAGE + 256;
 constexpr uint32_t OFF_KEEP = OFF_SORT + (2 * SORT_MAX + 4) * 4;  // key weights: scores, in the kernel that adds them up
 constexpr size_t OWN_SMEM = OFF_KEEP + 1024;
-constexpr size_t OWN_SMEM_MOST = 113 * 1024;    // two CTAs per SM
+constexpr size_t OWN_SMEM_MOST = kOwnSmemMost;
+static_assert(OWN_SMEM == kOwnSmem && HD == kPlanHeadDim, "what the plans count on");
 static_assert((4 * 16 * HD + 128) * 4 <= STAGES * STAGE, "the merge area aliases the ring");
 
 struct OwnParams {
@@ -1021,53 +1022,6 @@ cudaError_t attn_own_prepare() {
   return cudaSuccess;
 }
 
-SharedPlan shared_plan(int B, int n_q, int n_kv, int key_limit, int shared_len, int sm_count) {
-  SharedPlan s{};
-  const int G = n_q / n_kv;
-  // prefix: one CTA per SM, each with its share of the key tiles
-  s.rows_seq = 128 / G;
-  s.alternate = B <= s.rows_seq;
-  s.row_blocks = s.alternate ? 1 : (B + 2 * s.rows_seq - 1) / (2 * s.rows_seq);
-  const int tiles = (shared_len + 127) / 128;
-  if (tiles > 0) {
-    const int want = std::max(1, sm_count / (n_kv * s.row_blocks));
-    s.tiles_per_split = (tiles + want - 1) / want;
-    s.prefix_splits = (tiles + s.tiles_per_split - 1) / s.tiles_per_split;
-    s.prefix_parts = s.prefix_splits * (s.alternate ? 2 : 1);
-  }
-  // own keys: split while two CTAs per SM are not reached and a split keeps 64
-  // keys (one tile); where a cluster's 8 CTAs do not reach them, as many as are
-  // resident, with 256 keys (their partials are read again)
-  s.base = shared_len / 64 * 64;
-  const int keys = std::max(1, key_limit - s.base), pairs = B * n_kv;
-  int k = 1;
-  while (pairs * k < 2 * sm_count && k < 8 && keys / (2 * k) >= 64) k *= 2;
-  if (k == 8 && pairs * k < 2 * sm_count) k = std::max(k, std::min({128, 3 * sm_count / pairs, keys / 256}));
-  s.keys = keys;
-  s.own_splits = k;
-  s.min_share = k > 8 ? 256 : 64;
-  // A long prefix: own CTAs that started beside it leave partials for a joining
-  // kernel, so that others can follow on their SMs. A short one (4 turns): they
-  // wait for it and merge.
-  const int turns = s.alternate ? (s.tiles_per_split + 1) / 2 : s.tiles_per_split;
-  s.join = k > 8 || turns > 4;
-  s.cluster = k > 1 && !s.join;
-  const size_t rows = (size_t)B * n_q;
-  s.partials = rows * s.prefix_parts + (s.join ? rows * s.own_splits : 0);
-  return s;
-}
-
-size_t shared_partial_bytes(int max_batch, int n_q, int n_kv, int max_seq, int sm_count) {
-  // shared_plan's partials over every batch up to max_batch and every prefix:
-  // prefix parts are at most 256 rows a CTA at one CTA per SM, or two per row;
-  // own splits stay below 4 CTAs per SM
-  const size_t rows = (size_t)max_batch * n_q, G = n_q / n_kv;
-  const size_t tiles = (size_t)(max_seq + 127) / 128;
-  const size_t prefix = std::max(2 * rows, std::min<size_t>(256 * (size_t)sm_count, rows * 2 * tiles));
-  const size_t own = std::max(rows, std::min<size_t>(4 * (size_t)sm_count * G, rows * 128));
-  return (prefix + own) * (HD + 2) * sizeof(float) + 16;
-}
-
 static OwnParams own_params(const SharedArgs& a, const SharedPlan& s) {
   OwnParams p{};
   p.q = (const bf16*)a.q;
@@ -1128,36 +1082,6 @@ cudaError_t launch_shared_own(const SharedArgs& a, const SharedPlan& s, cudaStre
   if (e != cudaSuccess || !s.join) return e;
   return launch_k(attn_own_join_kernel<ODecode>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 0, p,
                   (int)rows);
-}
-
-// Scores of a row that the kernel itself can keep, so that it adds up the weights and the
-// joining kernel falls away: where one CTA has all keys of a row, and shared memory for
-// them costs no CTA that would be resident otherwise. 0: none. (64 sequences of up to 60
-// keys, 8 K/V heads 9.5 us, with the joining kernel 12.0, 32 of up to 200, 32 heads 19.6 and 22.2; the
-// splits of a cluster likewise measured slower, 4 sequences of up to 1000 keys 18.7 and 13.4.)
-static int weights_keep(const SharedPlan& s, int B, int n_q, int n_kv, int sm_count) {
-  const int G = n_q / n_kv, most = G <= 8 ? 3 : 2;
-  const long long bytes = (long long)OWN_SMEM + 4ll * G * s.keys;
-  if (s.own_splits > 1 || bytes > (long long)OWN_SMEM_MOST) return 0;
-  const long long resident = std::min<long long>(most, 227 * 1024 / (bytes + 1024));
-  return resident == most || resident * sm_count >= (long long)B * n_kv ? s.keys : 0;
-}
-
-SharedPlan weights_plan(int B, int n_q, int n_kv, int key_limit, int sm_count) {
-  SharedPlan s = shared_plan(B, n_q, n_kv, key_limit, 0, sm_count);
-  s.keep = weights_keep(s, B, n_q, n_kv, sm_count);
-  if (s.keep) return s;
-  // The splits are joined by the second kernel in any case, so that more of them, of long
-  // rows, cost little and leave SMs less idle at the end: 5 CTAs per SM with 1024 keys (64
-  // sequences of up to 16384 keys, 8 K/V heads, one CTA each 412 us, two 371; 32 of up to 4096,
-  // two 64.2, three 62.5, four 65.5; 64 of up to 1500 keys, one 52.5, two 56.2).
-  const int pairs = B * n_kv, once = s.own_splits;
-  while (pairs * s.own_splits < 5 * sm_count && s.own_splits < 8 && s.keys / (s.own_splits + 1) >= 1024) ++s.own_splits;
-  if (once == 1 && s.own_splits > 1) s.min_share = 512;
-  s.cluster = 0;  // the weights need a row's maximum and sum over all splits first
-  s.join = 1;
-  s.partials = (size_t)B * n_q * s.own_splits;
-  return s;
 }
 
 // 16 CTAs per SM share the keys of all (sequence, K/V head) pairs, a pass of the threads each at
@@ -1241,7 +1165,7 @@ bool tree_own_applies(const TreeArgs& a) {
          (items > a.sm_count && pairs <= 4 * items && pairs * a.key_limit <= 450ll * a.sm_count);
 }
 
-cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launches) {
+cudaError_t launch_tree_own(const TreeArgs& a, const TreePlan& t, cudaStream_t st, int64_t* launches) {
   OwnParams p{};
   p.q = (const bf16*)a.q;
   p.out = (bf16*)a.out;
@@ -1267,29 +1191,14 @@ cudaError_t launch_tree_own(const TreeArgs& a, cudaStream_t st, int64_t* launche
   p.tree = TreeMask{a.mask, a.mask_words};
   p.n_rows = a.n_rows;
   p.n_seq = a.B;
-  tree_slices(p.G, &p.slices, &p.per);
-  while (2 * p.per << p.tree_shift <= 8) ++p.tree_shift;
-  const int blocks = (a.n_rows >> p.tree_shift) + a.B;
-  // As many splits as are resident at once, three CTAs per SM, in clusters; of the odd sizes
-  // that of 3 pays (128 pairs of up to 1500 keys 16.0 us, clusters of 2 19.7, more than are resident
-  // with a joining kernel 23.8; 64 pairs of 750 in clusters of 4 11.1, of 7 18.3). Long sequences
-  // take the joining kernel (64 pairs of up to 6700 keys, 4 splits 44.7, 8 with it 40.0).
-  const int pairs = (int)std::min(tree_pairs(a), 65535ll);
-  int k = 1;
-  for (const int x : {8, 4, 3, 2})
-    if (k == 1 && pairs * x <= (x == 8 && a.key_limit > 4096 ? 4 : 3) * a.sm_count && a.key_limit / x >= 64) k = x;
-  p.min_share = 64;
-  // enough CTAs, but one each: a long sequence among short ones is cut in two (5 sequences of 13
-  // rows, 40 heads, 2000 keys the longest 36.8 -> 33.7 us, 8 of 8 rows 37.9 -> 33.4; shares
-  // of 64 keys and more, and four of them, up to 3 us more; twice as many pairs 43 -> 46 so)
-  if (k == 1 && pairs < 4 * a.sm_count && a.key_limit >= 1024) {
-    k = 2;
-    p.min_share = 512;
-  }
-  while (k > 1 && p.rows * k * (HD + 2) * sizeof(float) > tree_partial_bytes(a.sm_count)) k /= 2;
-  p.splits = k;
-  p.cluster = k > 1 && pairs * k <= 3 * a.sm_count;
-  p.join = k > 1 && !p.cluster;
+  p.tree_shift = t.shift;
+  p.slices = t.slices;
+  p.per = t.per;
+  p.splits = t.splits;
+  p.min_share = t.min_share;
+  p.cluster = t.cluster;
+  p.join = t.join;
+  const int blocks = (a.n_rows >> t.shift) + a.B, k = t.splits;
   *launches += p.join ? 2 : 1;
   p.own_room = p.rows * k;
   p.own_o = a.partial;
