@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(S_THREADS) attn_simt_kernel(SimtParams p) {
       if ((start < 0 || end > p.key_limit) && q0 == 0 && part == 0 && threadIdx.x == 0)
         flag(p.status, LLAMA_FLAG_POS_RANGE);
       n_keys = start < 0 ? 0 : (int)(end < p.key_limit ? end : p.key_limit);
+      // rows past the cache lie behind all keys, as far as the bias's softmax can tell, and start + row stays an int
+      start = min(max(start, 0), n_keys);
     } else {
       pre = p.prefix_len ? min(max(p.prefix_len[b], 0), n) : 0;
       n_keys = max(q0 + rows, pre);
