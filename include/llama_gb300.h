@@ -170,11 +170,18 @@ typedef struct llama_kv {
 
 typedef struct llama_ctx llama_ctx;
 
-/* Bytes of device workspace llama_init needs for cfg (256-byte aligned). */
+/* Bytes of device workspace for cfg with which every operation runs on all SMs (256-byte
+ * aligned). */
 int llama_workspace_bytes(const llama_config* cfg, size_t* bytes);
 
+/* The least that llama_init takes. The rest (bf16: up to 41 MB, where other partial results
+ * need less room) is for partial results of llama_op_attention_tree alone: with less, that
+ * call splits its work over as many SMs as there is room for, one at least, and everything
+ * else runs as it does with all of it. */
+int llama_workspace_least_bytes(const llama_config* cfg, size_t* bytes);
+
 /* Build a context. workspace: device buffer of at least
- * llama_workspace_bytes bytes, 256-byte aligned, owned by the caller and
+ * llama_workspace_least_bytes bytes, 256-byte aligned, owned by the caller and
  * untouched by anyone else while the context lives. stream: a cudaStream_t
  * (NULL = legacy default stream). Enqueues the RoPE table fill on stream.
  * On success *out receives the context (free with llama_free). */

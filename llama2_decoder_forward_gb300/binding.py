@@ -91,6 +91,8 @@ class KV(ctypes.Structure):
 
 _SIGS = {
     "llama_workspace_bytes": (c_int32, [ctypes.POINTER(LlamaConfig), ctypes.POINTER(ctypes.c_size_t)]),
+    "llama_workspace_least_bytes": (c_int32, [ctypes.POINTER(LlamaConfig),
+                                              ctypes.POINTER(ctypes.c_size_t)]),
     "llama_init": (c_int32, [ctypes.POINTER(LlamaConfig), ctypes.POINTER(Weights), c_void_p,
                              ctypes.c_size_t, c_void_p, ctypes.POINTER(c_void_p)]),
     "llama_set_stream": (c_int32, [c_void_p, c_void_p]),
@@ -244,6 +246,14 @@ def workspace_bytes(cfg: LlamaConfig) -> int:
     rc = lib().llama_workspace_bytes(ctypes.byref(cfg), ctypes.byref(n))
     if rc:
         raise LlamaError(rc, "llama_workspace_bytes")
+    return n.value
+
+
+def workspace_least_bytes(cfg: LlamaConfig) -> int:
+    n = ctypes.c_size_t(0)
+    rc = lib().llama_workspace_least_bytes(ctypes.byref(cfg), ctypes.byref(n))
+    if rc:
+        raise LlamaError(rc, "llama_workspace_least_bytes")
     return n.value
 
 
@@ -417,11 +427,12 @@ class Model:
     on the GPU ({"embed", "final_norm", "lm_head", "layers": [...]}); a
     layer-only model passes {"layers": [...]} and has_embed_head=False.
     Layers made by quantize_layer_e4m3 (E4M3 projections with row scales)
-    select weight_dtype LLAMA_W_E4M3.
+    select weight_dtype LLAMA_W_E4M3. tree_room=False leaves out the part of the workspace
+    that op_attention_tree alone needs to run on every SM (llama_workspace_least_bytes).
     """
 
     def __init__(self, shape, weights, *, max_batch, max_tokens, max_seq, has_embed_head=True,
-                 stream=None):
+                 stream=None, tree_room=True):
         import torch
         self.shape = shape
         self.weights = weights  # keep the tensors alive
@@ -433,7 +444,7 @@ class Model:
         w8 = "wqkv_scale" in layers[0]
         self.cfg = make_config(shape, max_batch, max_tokens, max_seq, has_embed_head,
                                W_E4M3 if w8 else W_MODEL)
-        nbytes = workspace_bytes(self.cfg)
+        nbytes = workspace_bytes(self.cfg) if tree_room else workspace_least_bytes(self.cfg)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
         arr = (LayerWeights * len(layers))()
         for i, lw in enumerate(layers):

@@ -70,7 +70,7 @@ int sm_count_or_default() {
 // Workspace layout (byte offsets from the workspace base).
 struct Layout {
   size_t status, rope, x, u, qkv, q, kside, vside, o, a, u_last, logits, ids, tok, pos, apart,
-      ssq, spart, total;
+      ssq, spart, least, total;
   size_t apart_bytes;
   int R;
 };
@@ -142,14 +142,15 @@ Layout make_layout(const llama_config* c, int sm_count) {
   L.apart = take(std::max<size_t>(L.apart_bytes, 16));
   // fused RMSNorm: per-(128-feature tile, row) sums of squares of the residual stream
   L.ssq = take((H + 127) / 128 * (size_t)R * 4);
-  // partial results of decode attention over a shared prefix, of key weights and of trees (bf16); rows'
-  // maxima and sums of decode attention with key weights (fp32)
-  L.spart = take(c->dtype == LLAMA_BF16
-                     ? std::max({shared_partial_bytes(c->max_batch, (int)nq, (int)nkv, c->max_seq, sm_count),
-                                 weights_partial_bytes(c->max_batch, (int)nq, (int)nkv, c->max_seq, sm_count),
-                                 tree_partial_bytes(sm_count)})
-                     : (size_t)c->max_batch * nq * 8);
-  L.total = off;
+  // last, partial results of decode attention over a shared prefix, of key weights and (as many as
+  // there is room for) of trees, bf16
+  L.spart = off;
+  take(c->dtype == LLAMA_BF16
+           ? std::max(shared_partial_bytes(c->max_batch, (int)nq, (int)nkv, c->max_seq, sm_count),
+                      weights_partial_bytes(c->max_batch, (int)nq, (int)nkv, c->max_seq, sm_count))
+           : 16);
+  L.least = off;
+  L.total = c->dtype == LLAMA_BF16 ? std::max(off, L.spart + align_up(tree_partial_bytes(sm_count))) : off;
   return L;
 }
 
@@ -171,6 +172,7 @@ struct llama_ctx {
   std::vector<llama_layer_weights> layers;
   char* ws = nullptr;
   Layout L;
+  size_t spart_bytes = 0;  // of the workspace from L.spart on
   uint32_t* status = nullptr;
   float2* rope = nullptr;
   std::map<Key2, CUtensorMap> maps;
@@ -750,6 +752,13 @@ int llama_workspace_bytes(const llama_config* cfg, size_t* bytes) {
   return LLAMA_OK;
 }
 
+int llama_workspace_least_bytes(const llama_config* cfg, size_t* bytes) {
+  if (!bytes) return LLAMA_ERR_INVALID_ARG;
+  TRY(check_config(cfg));
+  *bytes = make_layout(cfg, sm_count_or_default()).least;
+  return LLAMA_OK;
+}
+
 int llama_init(const llama_config* cfg, const llama_weights* w, void* workspace,
                size_t workspace_bytes, void* stream, llama_ctx** out) {
   if (!out || !w) return LLAMA_ERR_INVALID_ARG;
@@ -788,7 +797,7 @@ int llama_init(const llama_config* cfg, const llama_weights* w, void* workspace,
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return LLAMA_ERR_CUDA;
   Layout L = make_layout(cfg, sms);
-  if (workspace_bytes < L.total) return LLAMA_ERR_WORKSPACE;
+  if (workspace_bytes < L.least) return LLAMA_ERR_WORKSPACE;
   llama_ctx* c = new (std::nothrow) llama_ctx();
   if (!c) return LLAMA_ERR_INVALID_ARG;
   c->cfg = *cfg;
@@ -802,6 +811,7 @@ int llama_init(const llama_config* cfg, const llama_weights* w, void* workspace,
   c->layers.assign(w->layers, w->layers + cfg->n_layers);
   c->ws = reinterpret_cast<char*>(workspace);
   c->L = L;
+  c->spart_bytes = std::min(workspace_bytes, L.total) - L.spart;
   c->status = c->at<uint32_t>(L.status);
   c->rope = c->at<float2>(L.rope);
   int rc = LLAMA_OK;
@@ -1488,7 +1498,7 @@ int llama_op_attention_decode_weights(llama_ctx* c, const void* q, const int32_t
   w.weights = weights;
   w.ld = weights_ld;
   if (cf.dtype != LLAMA_BF16) {
-    w.stats = c->at<float>(c->L.spart);
+    w.stats = c->at<float>(c->L.o);  // [B n_q][2]; free between steps, and head_dim is 8 at least
     Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
     c->launches += 2;
     TRY(cuda_rc(launch_shared_simt(a, c->stream, &w)));
@@ -1557,9 +1567,10 @@ int llama_op_attention_tree(llama_ctx* c, const void* q, int32_t n_rows, const i
   }
   TRY(decode_maps(c, kv, n_rows, 128 / (cf.n_q_heads / cf.n_kv_heads), &a));
   a.partial = c->at<float>(c->L.spart);
+  a.partial_bytes = c->spart_bytes;
   Prof pf(c, LLAMA_KERNEL_ATTN_DECODE);
   const TreePlan plan = tree_plan(n_rows, B, a.n_q, a.n_kv, a.key_limit, a.sc.cap > 0.f || a.sc.slopes, a.sm_count,
-                                  tree_partial_bytes(a.sm_count));
+                                  c->spart_bytes);
   if (plan.own) return cuda_rc(launch_tree_own(a, plan, c->stream, &c->launches));
   c->launches += 2;
   return cuda_rc(launch_tree_tc(a, c->stream));

@@ -313,9 +313,10 @@ struct TreeArgs {
   const CUtensorMap *map_q = nullptr, *map_k = nullptr, *map_v = nullptr, *map_k16 = nullptr,
                     *map_v16 = nullptr;
   int box_rows = 16, sm_count = 152;
-  float* partial = nullptr;    // workspace, tree_partial_bytes
+  float* partial = nullptr;    // workspace, up to tree_partial_bytes of use
+  size_t partial_bytes = 0;
 };
-size_t tree_partial_bytes(int sm_count);
+size_t tree_partial_bytes(int sm_count);  // with which the tensor-core kernel has a CTA on every SM
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st);    // k_attn_forms_tc.cu
 cudaError_t launch_tree_own(const TreeArgs& a, const TreePlan& t, cudaStream_t st, int64_t* launches);  // k_attn_own.cu
 cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t st);  // k_attn_simt.cu

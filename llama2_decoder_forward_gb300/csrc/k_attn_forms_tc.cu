@@ -1696,9 +1696,9 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const SharedPlan& s, cudaS
                   *a.map_v16, p);
 }
 
-size_t tree_partial_bytes(int sm_count) {
-  return (size_t)2 * sm_count * 2 * TM * (128 + 2) * sizeof(float) + sm_count * (sizeof(TreeShared) + sizeof(int));
-}
+// Of a CTA: the partial results of its first and its last item, and what the join needs to know.
+static size_t tree_cta_bytes(int rows_slot) { return 2 * rows_slot * kPartial + sizeof(TreeShared) + sizeof(int); }
+size_t tree_partial_bytes(int sm_count) { return sm_count * tree_cta_bytes(2 * TM); }
 
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
   if (a.head_dim != 128) return cudaErrorInvalidValue;
@@ -1732,12 +1732,14 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t st) {
   const long long tiles = ((long long)a.n_rows + (long long)a.B * p.rows_seq - 1) / ((long long)a.B * p.rows_seq);
   p.alternate = tiles <= 1 || (tiles == 2 && 9ll * a.B * a.n_kv <= a.sm_count);
   const long long items = (p.alternate ? tiles : (tiles + 1) / 2) * a.B * a.n_kv;  // about
-  p.partials = (size_t)2 * a.sm_count * (p.alternate ? TM : 2 * TM);
+  // a CTA per SM, or as many as there is room for; one alone has all items whole, and no partial results
+  const int rows_slot = p.alternate ? TM : 2 * TM;
+  const int ctas = (int)std::min<size_t>(a.sm_count, std::max<size_t>(1, a.partial_bytes / tree_cta_bytes(rows_slot)));
+  p.partials = ctas > 1 ? (size_t)2 * ctas * rows_slot : 0;
   p.part_o = a.partial;
   p.part_ml = a.partial + p.partials * 128;
   p.shared = reinterpret_cast<TreeShared*>(a.partial + p.partials * 130);
-  p.shared_parts = reinterpret_cast<int*>(p.shared + a.sm_count);
-  const int ctas = a.sm_count;
+  p.shared_parts = reinterpret_cast<int*>(p.shared + ctas);
   const cudaError_t e = launch_k(forms_kernel<MTree>(kind), dim3(ctas), dim3(FORMS_THREADS), FORMS_SMEM, st, 0,
                                  *a.map_q, *a.map_k, *a.map_v, *a.map_k16, *a.map_v16, p);
   if (e != cudaSuccess || ctas < 2) return e;
