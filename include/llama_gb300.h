@@ -611,7 +611,11 @@ int llama_op_rope_norm_append_at(llama_ctx* ctx, const void* qkv, int32_t qkv_dt
  * distance bias of scores alone, which goes by |position - position|; a cached key's is its slot.
  * out T [n_rows, n_q d]; rows of no sequence are left as they were.
  * V must be finite in a sequence's rows (a hidden one may take part with weight 0) and
- * |V| as in llama_op_attention_docs. cu_rows outside [0, n_rows] or decreasing, a
+ * |V| as in llama_op_attention_docs. bf16: softmax weights are rounded once to bf16, as in
+ * llama_op_attention_docs, on the tensor-core kernel (error against 64 bits 0.0021 of the
+ * outputs' root mean square, of which rounding the output is 0.0017), and kept to twice
+ * the digits on the one for few rows (0.0017); which one a call takes follows from n_rows / B,
+ * the heads and the cache's room. cu_rows outside [0, n_rows] or decreasing, a
  * negative start (its rows give zeros) and slots past the cache (not attended) set
  * LLAMA_FLAG_POS_RANGE, a page id outside the pool LLAMA_FLAG_PAGE_RANGE (its keys read
  * as zeros). Any number of rows, n_rows * n_q < 2^30; mask_words to 2^25; B as the cache

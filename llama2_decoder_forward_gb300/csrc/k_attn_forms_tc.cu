@@ -475,13 +475,18 @@ __device__ __forceinline__ int prefix_share(const FormsParams& p, int lane) {
 // tiles whatever the lengths. The blocks come first so that those of the same keys are
 // worked on at the same time, by CTAs far apart in the line, and read the keys from L2
 // but once (32 sequences of up to 8192 keys, two blocks of 256 rows each: 254 -> 236 us
-// before the joining kernel).
+// before the joining kernel, in short bursts).
 // A CTA's first and last item may be shared with its neighbours: those leave partial
 // results (CTA c: 2c for its first item, 2c + 1 for its last), which the joining kernel
 // merges; items within a chunk are stored at once. Bound by the softmax beside the MMAs
 // (tensor pipe active 59 % of the time): 32 sequences of 64 rows over up to 8192 keys,
-// 64 / 8 heads, 254 us with the join, 1.22 PFLOP/s; of few items by the latency of one
-// tile and the join: one sequence of 26 rows over 1000 keys 16 us.
+// 64 / 8 heads, 279 us with the join, 1.11 PFLOP/s (254 us in short bursts, before the clock
+// falls); of few items by the latency of one tile and the join: one sequence of 26 rows over
+// 1000 keys 16 us. P as a high and a low bf16 part, two MMAs each, takes the error of trees
+// to that of the output's rounding (0.00214 -> 0.00166, one sequence 0.00175 -> 0.00166), and
+// these cases 279 -> 358 and 16.5 -> 17.0 us: not done, as for documents. These instances
+// spill 92 to 128 bytes of a thread's registers, 56 to 104 of them read again (TreeWalk in
+// the producer, the bits and positions in the softmax).
 struct TreeSeq {   // a sequence's rows, its keys, and the tiles of a block's items
   int lo, n, start, keys, T, blocks;
   long long tiles;
@@ -1498,7 +1503,8 @@ FormsKernel forms_kernel(int kind) {
 // block makes the list of those items, so that no block is without work. Few items have many
 // parts each: four ahead, three blocks per SM (one sequence of 26 rows 16.2 us, two ahead 17.5).
 // Many have two or so, and what counts is how many rows are worked on: two ahead, four
-// blocks (32 sequences of 64 rows, 8192 keys 253.7 us, four ahead 259.0; 64 of 32 rows 101.9, 106.5).
+// blocks (in short bursts 32 sequences of 64 rows, 8192 keys 253.7 us, four ahead 259.0; 64 of
+// 32 rows 101.9, 106.5).
 struct JoinItem {
   int cta, parts;  // the CTA that begins it
   TreeShared of;
