@@ -480,13 +480,12 @@ __device__ __forceinline__ int prefix_share(const FormsParams& p, int lane) {
 // results (CTA c: 2c for its first item, 2c + 1 for its last), which the joining kernel
 // merges; items within a chunk are stored at once. Bound by the softmax beside the MMAs
 // (tensor pipe active 59 % of the time): 32 sequences of 64 rows over up to 8192 keys,
-// 64 / 8 heads, 279 us with the join, 1.11 PFLOP/s (254 us in short bursts, before the clock
-// falls); of few items by the latency of one tile and the join: one sequence of 26 rows over
-// 1000 keys 16 us. P as a high and a low bf16 part, two MMAs each, takes the error of trees
-// to that of the output's rounding (0.00214 -> 0.00166, one sequence 0.00175 -> 0.00166), and
-// these cases 279 -> 358 and 16.5 -> 17.0 us: not done, as for documents. These instances
-// spill 92 to 128 bytes of a thread's registers, 56 to 104 of them read again (TreeWalk in
-// the producer, the bits and positions in the softmax).
+// 64 / 8 heads, 279 us with the join, 1.11 PFLOP/s (254 us in short bursts); of few items by
+// the latency of one tile and the join: one sequence of 26 rows over 1000 keys 16 us.
+// P as a high and a low bf16 part, two MMAs each, takes the error of trees to that of the
+// output's rounding (0.00214 -> 0.00166, one sequence 0.00175 -> 0.00166), and these cases
+// 279 -> 358 and 16.5 -> 17.0 us: not done, as for documents. These instances store 92 to
+// 128 bytes of spilled registers per thread and load 56 to 104.
 struct TreeSeq {   // a sequence's rows, its keys, and the tiles of a block's items
   int lo, n, start, keys, T, blocks;
   long long tiles;
